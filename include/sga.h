@@ -298,6 +298,92 @@ sga_status sga_relabel_csr(const int32_t *indptr, const int32_t *indices, int64_
 sga_status sga_permute_rows(const void *src, int64_t N, int64_t row_bytes, const int32_t *perm,
                             int inverse, void *dst, void *stream);
 
+/* ---- attention over packed sequences ---------------------------------------
+ *
+ * Global attention beside the edge attention: every row attends to the rows of
+ * its own graph (or token sequence) in a packed batch.  Sequence b is rows
+ * seq_ptr[b] .. seq_ptr[b+1] of the node tensors (it may be empty); row i sees
+ * the keys j of its own sequence, with causal = 1 those with j <= i only:
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),
+ *   out_i = sum_j exp(s_ij - lse_i) v_j.
+ * Grouped heads: Q, out [T, H, D]; K, V [T, Hkv, D] with H a multiple of Hkv;
+ * query head h reads key head h / (H / Hkv).  lse [T, H] float32.
+ * T >= seq_ptr[B]: rows behind the last sequence are neither read nor written.
+ * D in {32, 64, 128}; H*D <= 16384; dtype as for the other layers.
+ * What a row does not see does not reach it: an infinity or NaN in another
+ * sequence, or in a later row under causal, leaves its results unchanged.
+ *
+ * A plan holds the tile lists of one batch's lengths and head layout and
+ * serves every layer's forward and backward pass on it.  The plan is only
+ * read by the calls (the error word aside): calls on one plan may overlap,
+ * on different streams or in different captured graphs; only a workspace may
+ * not be shared by calls that overlap. */
+typedef struct sga_seq_plan sga_seq_plan;
+
+/* seq_ptr: [B+1] int32, device; seq_ptr[0] = 0, non-decreasing (SGA_EINVAL
+ * otherwise).  Read during this call only, which synchronises `stream` and
+ * allocates the plan's device memory on the current device. */
+sga_status sga_seq_plan_create(const int32_t *seq_ptr, int64_t B, int H, int Hkv, int D, sga_dtype dt, int causal,
+                               void *stream, sga_seq_plan **out);
+void sga_seq_plan_destroy(sga_seq_plan *plan);
+
+/* seq_ptr[B]: the rows that sequences cover. */
+int64_t sga_seq_plan_rows(const sga_seq_plan *plan);
+
+/* Device workspace of seq_attn_bwd (256-byte aligned). */
+size_t sga_seq_bwd_workspace_bytes(const sga_seq_plan *plan);
+
+/* As sga_read_device_error, for a sequence plan. */
+sga_status sga_seq_read_device_error(const sga_seq_plan *plan, void *stream, int32_t *code);
+
+/* scale: positive and finite.  The current device must be the plan's. */
+sga_status seq_attn_fwd(const sga_seq_plan *plan, const void *Q, const void *K, const void *V, int64_t T, float scale,
+                        void *out, float *lse, void *stream);
+
+/* dQ [T, H, D], dK and dV [T, Hkv, D] (summed over the heads of a group) from
+ * the forward's out and lse.  No atomics: bitwise reproducible. */
+sga_status seq_attn_bwd(const sga_seq_plan *plan, const void *Q, const void *K, const void *V, const void *out,
+                        const float *lse, const void *dOut, int64_t T, float scale, void *dQ, void *dK, void *dV,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- layer norm -------------------------------------------------------------
+ *
+ * Over the rows of X [N, C] in dt: mean and rstd = 1 / sqrt(var + eps)
+ * (float32 [N], kept for the backward pass), out = (X - mean) rstd weight +
+ * bias.  weight, bias: [C] in wdt (float32, or dt), NULL for none (a bias
+ * needs a weight).  1 <= C <= 2^20.  Pointers need the alignment of their
+ * element; 16-byte aligned rows (C * element a multiple of 16) are moved 16
+ * bytes at a time.  The backward returns dX in dt and, unless dweight is NULL,
+ * dweight and (unless NULL) dbias in wdt, summed over the rows in a fixed
+ * order: bitwise reproducible.  Its workspace (16-byte aligned) is needed for
+ * dweight only. */
+sga_status layer_norm_fwd(const void *X, const void *weight, const void *bias, int64_t N, int64_t C, float eps,
+                          sga_dtype dt, sga_dtype wdt, void *out, float *mean, float *rstd, void *stream);
+size_t sga_norm_bwd_workspace_bytes(int64_t N, int64_t C);
+sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, const float *rstd, const void *dOut,
+                          int64_t N, int64_t C, sga_dtype dt, sga_dtype wdt, void *dX, void *dweight, void *dbias,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- embedding --------------------------------------------------------------
+ *
+ * out[t] = scale table[ids[t]] for ids [N] (int32 or int64: id_bytes 4 or 8)
+ * and table [V, C] in dt; N, V < 2^31 - 1, C <= 2^20.  An id outside [0, V)
+ * reads as a row of zeros, adds to no gradient and sets a bit in the device's
+ * error word.  The backward writes all of dTable [V, C] = scale times the sum
+ * of dOut over each row's tokens (zero for a row without one, and for
+ * padding_idx >= 0), summed by tokens sorted by id in a fixed order: bitwise
+ * reproducible.  Its workspace is 256-byte aligned. */
+sga_status embed_fwd(const void *ids, int id_bytes, const void *table, int64_t N, int64_t V, int64_t C, float scale,
+                     sga_dtype dt, void *out, void *stream);
+size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t C);
+sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N, int64_t V, int64_t C, float scale,
+                     int64_t padding_idx, sga_dtype dt, void *dTable, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/* Read and clear the current device's error word of the embedding calls.
+ * Synchronises `stream`; SGA_EDEVICE_CHECK if it was non-zero. */
+sga_status sga_embed_read_device_error(void *stream, int32_t *code);
+
 const char *sga_status_string(sga_status s);
 
 /* Last CUDA error code seen by a call that returned SGA_ECUDA (0 if none). */
@@ -418,7 +504,11 @@ typedef enum {
     SGA_KERN_AGG_FWD = 19, SGA_KERN_AGG_FWD_MERGE = 20, SGA_KERN_AGG_BWD = 21,
     SGA_KERN_AGG_BWD_MERGE = 22,
     SGA_KERN_GAT_FWD = 23, SGA_KERN_GAT_BWD_DST = 24, SGA_KERN_GAT_BWD_SRC = 25,
-    SGA_KERN_COUNT = 26
+    SGA_KERN_SEQ_FWD = 26, SGA_KERN_SEQ_BWD_ROWS = 27, SGA_KERN_SEQ_BWD_DQ = 28,
+    SGA_KERN_SEQ_BWD_DKDV = 29, SGA_KERN_NORM_FWD = 30, SGA_KERN_NORM_BWD = 31,
+    SGA_KERN_NORM_REDUCE = 32, SGA_KERN_EMBED_FWD = 33, SGA_KERN_EMBED_SORT = 34,
+    SGA_KERN_EMBED_SUM = 35, SGA_KERN_EMBED_JOIN = 36,
+    SGA_KERN_COUNT = 37
 } sga_kernel_id;
 /* (Planned GATv2 passes merge their split rows inside the edge kernels --
  * the last chunk of a row to finish merges it -- so SGA_KERN_GATV2_FWD_MERGE

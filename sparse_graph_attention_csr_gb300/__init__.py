@@ -1,4 +1,6 @@
-"""Fused CSR edge attention (Graph Transformer, GATv2) on sm_103a.
+"""Fused CSR edge attention (Graph Transformer, GATv2) on sm_103a, and the
+dense operators around it: attention over packed sequences, layer norm and
+embedding lookup.
 
 A thin ctypes binding over the C ABI of ``libsga.so`` (declared in
 ``include/sga.h``).  This module only marshals arguments: every step of the
@@ -11,10 +13,13 @@ sources), int32, on the GPU.  Node tensors are [N, H, D], float32 or bfloat16.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsga.so")
@@ -28,7 +33,9 @@ KERNELS = {
     "gatv2_bwd_src": 10, "gatv2_bwd_merge": 11, "gatv2_bwd_dx": 12, "gatv2_bwd_dw": 13,
     "gatv2_bwd_reduce": 14, "bsr_fwd": 15, "bsr_bwd_delta": 16, "bsr_bwd_dq": 17,
     "bsr_bwd_dkdv": 18, "agg_fwd": 19, "agg_fwd_merge": 20, "agg_bwd": 21, "agg_bwd_merge": 22,
-    "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25,
+    "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25, "seq_fwd": 26, "seq_bwd_rows": 27,
+    "seq_bwd_dq": 28, "seq_bwd_dkdv": 29, "norm_fwd": 30, "norm_bwd": 31, "norm_reduce": 32,
+    "embed_fwd": 33, "embed_sort": 34, "embed_sum": 35, "embed_join": 36,
 }
 
 SGA_LAYER_ATTENTION, SGA_LAYER_MINMAX, SGA_LAYER_GAT = 0, 1, 2
@@ -113,6 +120,23 @@ _SIGNATURES = {
     "sga_reorder": ([_vp, _vp, _i64, _i64, _int, _vp, _vp], _int),
     "sga_relabel_csr": ([_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp], _int),
     "sga_permute_rows": ([_vp, _i64, _i64, _vp, _int, _vp, _vp], _int),
+    "sga_seq_plan_create": ([_vp, _i64, _int, _int, _int, _int, _int, _vp, ctypes.POINTER(_vp)], _int),
+    "sga_seq_plan_destroy": ([_vp], None),
+    "sga_seq_plan_rows": ([_vp], _i64),
+    "sga_seq_bwd_workspace_bytes": ([_vp], ctypes.c_size_t),
+    "sga_seq_read_device_error": ([_vp, _vp, ctypes.POINTER(ctypes.c_int32)], _int),
+    "seq_attn_fwd": ([_vp, _vp, _vp, _vp, _i64, _f32, _vp, _vp, _vp], _int),
+    "seq_attn_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _f32, _vp, _vp, _vp, _vp,
+                      ctypes.c_size_t, _vp], _int),
+    "layer_norm_fwd": ([_vp, _vp, _vp, _i64, _i64, _f32, _int, _int, _vp, _vp, _vp, _vp], _int),
+    "sga_norm_bwd_workspace_bytes": ([_i64, _i64], ctypes.c_size_t),
+    "layer_norm_bwd": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp,
+                        ctypes.c_size_t, _vp], _int),
+    "embed_fwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _int, _vp, _vp], _int),
+    "sga_embed_bwd_workspace_bytes": ([_i64, _i64], ctypes.c_size_t),
+    "embed_bwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _i64, _int, _vp, _vp, ctypes.c_size_t,
+                   _vp], _int),
+    "sga_embed_read_device_error": ([_vp, ctypes.POINTER(ctypes.c_int32)], _int),
     "sga_profile_start": ([_int], _int),
     "sga_profile_stop": ([ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i64)], _int),
 }
@@ -598,6 +622,380 @@ def agg_minmax_bwd(plan: Plan, mask, dOut, dX=None, stream=None):
     return dX
 
 
+# ------------------------------------------- attention over packed sequences
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _place(device, stream):
+    """(context, raw stream) of a call on tensors of ``device``: on ``stream``,
+    or the device's current stream.  Inside the context that device and stream
+    are current, so results and workspaces are allocated on the stream that
+    writes them."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return _NO_CONTEXT, torch.cuda.current_stream().cuda_stream
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _tensor(t, name, device, dtype, shape):
+    """A contiguous CUDA tensor of exactly this device, dtype and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _distinct(ins, outs):
+    """Outputs must not share memory with inputs or one another."""
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), n, True) for n, t in outs]
+    spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), n, False) for n, t in ins]
+    for i, (b, e, n, _) in enumerate(spans[:len(outs)]):
+        for b2, e2, n2, _ in spans[i + 1:]:
+            if b < e2 and b2 < e:
+                raise ValueError(f"{n} shares memory with {n2}")
+
+
+class SeqPlan:
+    """A plan for attention over packed sequences: sequence b is rows
+    seq_ptr[b] .. seq_ptr[b + 1] of the node tensors ([B + 1] int32, from 0,
+    non-decreasing; a sequence may be empty).  One plan serves the forward and
+    backward pass of every layer on the batch.  ``seq_ptr`` is read here only.
+
+    ``H`` query heads of ``D`` elements (32, 64 or 128) share ``kv_heads`` key
+    and value heads (default H); ``causal``: row i sees rows j <= i of its
+    sequence, otherwise all of them.  Calls on one plan may overlap (other
+    streams, captured graphs); the plan must outlive them.
+    """
+
+    def __init__(self, seq_ptr: torch.Tensor, H: int, D: int, dtype=torch.bfloat16,
+                 kv_heads: int | None = None, causal: bool = True, stream=None):
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"the layers compute in torch.float32 or torch.bfloat16, not {dtype}")
+        _need(seq_ptr, "seq_ptr", torch.int32)
+        if seq_ptr.dim() != 1 or seq_ptr.numel() < 1:
+            raise ValueError("seq_ptr must be 1-D with B + 1 entries")
+        self.B = seq_ptr.numel() - 1
+        self.H, self.D = int(H), int(D)
+        self.kv_heads = self.H if kv_heads is None else int(kv_heads)
+        self.causal, self.dtype, self.device = bool(causal), dtype, seq_ptr.device
+        self._h = None
+        handle = ctypes.c_void_p()
+        ctx, raw = _place(self.device, stream)
+        with ctx:
+            _check(_lib().sga_seq_plan_create(
+                _ptr(seq_ptr), self.B, self.H, self.kv_heads, self.D,
+                SGA_F32 if dtype == torch.float32 else SGA_BF16, 1 if causal else 0, raw,
+                ctypes.byref(handle)), "sga_seq_plan_create")
+        self._h = handle
+        self.rows = int(_lib().sga_seq_plan_rows(handle))
+        self._ws_bytes = int(_lib().sga_seq_bwd_workspace_bytes(handle))
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _LIB is not None:
+            _LIB.sga_seq_plan_destroy(h)
+            self._h = None
+
+    @property
+    def handle(self):
+        return self._h
+
+    def device_error(self, stream=None) -> int:
+        """Read and clear the device error word (0 = no failed check)."""
+        code = ctypes.c_int32()
+        ctx, raw = _place(self.device, stream)
+        with ctx:
+            st = _lib().sga_seq_read_device_error(self._h, raw, ctypes.byref(code))
+        if st not in (SGA_OK, SGA_EDEVICE_CHECK):
+            _check(st, "sga_seq_read_device_error")
+        return int(code.value)
+
+
+def _seq_inputs(plan, Q, K, V):
+    T = Q.shape[0] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else plan.rows
+    if T < plan.rows:
+        raise ValueError(f"Q has {T} rows, the plan's sequences cover {plan.rows}")
+    _tensor(Q, "Q", plan.device, plan.dtype, (T, plan.H, plan.D))
+    _tensor(K, "K", plan.device, plan.dtype, (T, plan.kv_heads, plan.D))
+    _tensor(V, "V", plan.device, plan.dtype, (T, plan.kv_heads, plan.D))
+    return T
+
+
+def _seq_scale(plan, scale):
+    scale = 1.0 / math.sqrt(plan.D) if scale is None else float(scale)
+    if not 0.0 < scale < math.inf:
+        raise ValueError(f"scale must be positive and finite, got {scale}")
+    return scale
+
+
+def _seq_result(plan, like, given, name, fill=0.0):
+    """The given result tensor, or a new one: rows behind the last sequence,
+    which the kernels leave as they are, are filled in a new one."""
+    if given is not None:
+        _tensor(given, name, plan.device, like.dtype, like.shape)
+        return given
+    t = torch.empty_like(like)
+    if t.shape[0] > plan.rows:
+        t[plan.rows:].fill_(fill)
+    return t
+
+
+def seq_attn_fwd(plan: SeqPlan, Q, K, V, scale: float | None = None, out=None, lse=None,
+                 stream=None):
+    """Attention of every row over the rows of its own sequence: (out [T, H, D],
+    lse [T, H] float32) of Q [T, H, D] and K, V [T, kv_heads, D]; ``scale``
+    defaults to 1 / sqrt(D).  T may exceed the plan's rows: rows behind the
+    last sequence are not read, and are zero (lse: -inf) in results allocated
+    here, left as they were in results passed in."""
+    T = _seq_inputs(plan, Q, K, V)
+    scale = _seq_scale(plan, scale)
+    ctx, raw = _place(plan.device, stream)
+    with ctx:
+        own = out is None and lse is None
+        out = _seq_result(plan, Q, out, "out")
+        if lse is None:
+            lse = torch.empty((T, plan.H), dtype=torch.float32, device=plan.device)
+            if T > plan.rows:
+                lse[plan.rows:].fill_(-math.inf)
+        else:
+            _tensor(lse, "lse", plan.device, torch.float32, (T, plan.H))
+        if not own:
+            _distinct((("Q", Q), ("K", K), ("V", V)), (("out", out), ("lse", lse)))
+        _check(_lib().seq_attn_fwd(plan.handle, Q.data_ptr(), K.data_ptr(), V.data_ptr(), T, scale,
+                                   out.data_ptr(), lse.data_ptr(), raw), "seq_attn_fwd")
+    return out, lse
+
+
+def seq_attn_bwd(plan: SeqPlan, Q, K, V, out, lse, dOut, scale: float | None = None, dQ=None,
+                 dK=None, dV=None, stream=None):
+    """(dQ [T, H, D], dK, dV [T, kv_heads, D]) from the forward's out and lse.
+    Rows behind the last sequence: as in seq_attn_fwd, zero in new results."""
+    T = _seq_inputs(plan, Q, K, V)
+    _tensor(out, "out", plan.device, plan.dtype, Q.shape)
+    _tensor(dOut, "dOut", plan.device, plan.dtype, Q.shape)
+    _tensor(lse, "lse", plan.device, torch.float32, (T, plan.H))
+    scale = _seq_scale(plan, scale)
+    ctx, raw = _place(plan.device, stream)
+    with ctx:
+        own = dQ is None and dK is None and dV is None
+        dQ = _seq_result(plan, Q, dQ, "dQ")
+        dK = _seq_result(plan, K, dK, "dK")
+        dV = _seq_result(plan, V, dV, "dV")
+        if not own:
+            _distinct((("Q", Q), ("K", K), ("V", V), ("out", out), ("lse", lse), ("dOut", dOut)),
+                      (("dQ", dQ), ("dK", dK), ("dV", dV)))
+        ws = torch.empty(plan._ws_bytes, dtype=torch.uint8, device=plan.device)
+        _check(_lib().seq_attn_bwd(plan.handle, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
+                                   out.data_ptr(), lse.data_ptr(), dOut.data_ptr(), T, scale,
+                                   dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(),
+                                   plan._ws_bytes, raw), "seq_attn_bwd")
+    return dQ, dK, dV
+
+
+# ------------------------------------------------------------------ layer norm
+
+def _norm_inputs(X, weight, bias=None):
+    if not isinstance(X, torch.Tensor) or not X.is_cuda:
+        raise ValueError("X must be a CUDA tensor")
+    if X.dim() < 1 or X.shape[-1] < 1:
+        raise ValueError(f"X must be [..., C] with C >= 1, got {tuple(X.shape)}")
+    dt = _dtype_code(X)
+    if not X.is_contiguous():
+        raise ValueError("X must be contiguous")
+    C = X.shape[-1]
+    if weight is None:
+        if bias is not None:
+            raise ValueError("a bias needs a weight")
+        return dt, dt, C
+    wdtype = weight.dtype if isinstance(weight, torch.Tensor) else None
+    if wdtype != torch.float32 and wdtype != X.dtype:
+        raise TypeError(f"weight must be {X.dtype} or torch.float32, got {wdtype}")
+    _tensor(weight, "weight", X.device, wdtype, (C,))
+    if bias is not None:
+        _tensor(bias, "bias", X.device, wdtype, (C,))
+    return dt, SGA_F32 if wdtype == torch.float32 else SGA_BF16, C
+
+
+def layer_norm_fwd(X, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None,
+                   stream=None):
+    """Layer norm over the last dimension of X [..., C]: (out, mean, rstd) with
+    mean and rstd = 1 / sqrt(var + eps) float32 of X's leading shape.  weight,
+    bias: [C], float32 or X's dtype, or None.  ``out`` may be X itself."""
+    dt, wdt, C = _norm_inputs(X, weight, bias)
+    eps = float(eps)
+    if not 0.0 <= eps < math.inf:
+        raise ValueError(f"eps must be finite and not negative, got {eps}")
+    lead = X.shape[:-1]
+    ctx, raw = _place(X.device, stream)
+    with ctx:
+        own = out is None and mean is None and rstd is None
+        out = torch.empty_like(X) if out is None else out
+        mean = torch.empty(lead, dtype=torch.float32, device=X.device) if mean is None else mean
+        rstd = torch.empty(lead, dtype=torch.float32, device=X.device) if rstd is None else rstd
+        if not own:
+            _tensor(out, "out", X.device, X.dtype, X.shape)
+            _tensor(mean, "mean", X.device, torch.float32, lead)
+            _tensor(rstd, "rstd", X.device, torch.float32, lead)
+            ins = [(n, t) for n, t in (("X", X), ("weight", weight), ("bias", bias)) if t is not None]
+            if out.data_ptr() == X.data_ptr():   # in place: a row is read before it is written
+                _distinct(ins, (("mean", mean), ("rstd", rstd)))
+                _distinct(ins[1:], (("out", out), ("mean", mean), ("rstd", rstd)))
+            else:
+                _distinct(ins, (("out", out), ("mean", mean), ("rstd", rstd)))
+        _check(_lib().layer_norm_fwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
+                                     None if bias is None else bias.data_ptr(), X.numel() // C, C,
+                                     eps, dt, wdt, out.data_ptr(), mean.data_ptr(),
+                                     rstd.data_ptr(), raw), "layer_norm_fwd")
+    return out, mean, rstd
+
+
+def layer_norm_bwd(X, weight, mean, rstd, dOut, bias: bool = True, dX=None, dweight=None,
+                   dbias=None, stream=None):
+    """(dX, dweight, dbias) from the forward's mean and rstd; dweight and dbias
+    in weight's dtype, None without a weight (dbias also with bias=False)."""
+    dt, wdt, C = _norm_inputs(X, weight)
+    _tensor(dOut, "dOut", X.device, X.dtype, X.shape)
+    lead = X.shape[:-1]
+    _tensor(mean, "mean", X.device, torch.float32, lead)
+    _tensor(rstd, "rstd", X.device, torch.float32, lead)
+    if weight is None and (dweight is not None or dbias is not None):
+        raise ValueError("dweight and dbias need a weight")
+    if not bias and dbias is not None:
+        raise ValueError("dbias given with bias=False")
+    N = X.numel() // C
+    ctx, raw = _place(X.device, stream)
+    with ctx:
+        own = dX is None and dweight is None and dbias is None
+        dX = torch.empty_like(X) if dX is None else dX
+        ws, nbytes = None, 0
+        if weight is not None:
+            dweight = torch.empty_like(weight) if dweight is None else dweight
+            if bias:
+                dbias = torch.empty_like(weight) if dbias is None else dbias
+            nbytes = int(_lib().sga_norm_bwd_workspace_bytes(N, C))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+        if not own:
+            outs = [("dX", dX)]
+            _tensor(dX, "dX", X.device, X.dtype, X.shape)
+            for n, t in (("dweight", dweight), ("dbias", dbias)):
+                if t is not None:
+                    _tensor(t, n, X.device, weight.dtype, weight.shape)
+                    outs.append((n, t))
+            ins = [("X", X), ("dOut", dOut), ("mean", mean), ("rstd", rstd)]
+            _distinct(ins + ([("weight", weight)] if weight is not None else []), outs)
+        _check(_lib().layer_norm_bwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
+                                     mean.data_ptr(), rstd.data_ptr(), dOut.data_ptr(), N, C, dt,
+                                     wdt, dX.data_ptr(),
+                                     None if dweight is None else dweight.data_ptr(),
+                                     None if dbias is None else dbias.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), nbytes, raw),
+               "layer_norm_bwd")
+    return dX, dweight, dbias
+
+
+# ------------------------------------------------------------------- embedding
+
+def _embed_ids(ids):
+    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
+        raise ValueError("ids must be a CUDA tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    return ids.element_size()
+
+
+def _embed_scale(scale):
+    scale = float(scale)
+    if not math.isfinite(scale):
+        raise ValueError(f"scale must be finite, got {scale}")
+    return scale
+
+
+def embed_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
+    """out [*ids.shape, C] = scale * table[ids] for a table [V, C].  An id
+    outside [0, V) gives a row of zeros and sets the device's error word
+    (embed_device_error)."""
+    id_bytes = _embed_ids(ids)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[1] < 1:
+        raise ValueError("table must be [V, C] with C >= 1")
+    dt = _dtype_code(table)
+    V, C = table.shape
+    _tensor(table, "table", ids.device, table.dtype, (V, C))
+    scale = _embed_scale(scale)
+    shape = (*ids.shape, C)
+    ctx, raw = _place(ids.device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(shape, dtype=table.dtype, device=ids.device)
+        else:
+            _tensor(out, "out", ids.device, table.dtype, shape)
+            _distinct((("ids", ids), ("table", table)), (("out", out),))
+        _check(_lib().embed_fwd(ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(), V, C, scale,
+                                dt, out.data_ptr(), raw), "embed_fwd")
+    return out
+
+
+def embed_bwd(ids, dOut, num_rows: int, scale: float = 1.0, padding_idx: int | None = None,
+              dTable=None, stream=None):
+    """dTable [num_rows, C] = scale * the sum of dOut [*ids.shape, C] over each
+    row's tokens, in a fixed order (bitwise reproducible); zero for rows
+    without a token and for padding_idx.  Ids outside the table add nothing
+    and set the device's error word."""
+    id_bytes = _embed_ids(ids)
+    if not isinstance(dOut, torch.Tensor) or dOut.dim() < 1 or dOut.shape[-1] < 1:
+        raise ValueError("dOut must be [*ids.shape, C] with C >= 1")
+    dt = _dtype_code(dOut)
+    C, V = dOut.shape[-1], int(num_rows)
+    _tensor(dOut, "dOut", ids.device, dOut.dtype, (*ids.shape, C))
+    if V < 0:
+        raise ValueError(f"num_rows must not be negative, got {V}")
+    if padding_idx is None:
+        padding_idx = -1
+    elif not 0 <= padding_idx < V:
+        raise ValueError(f"padding_idx must be in [0, {V}), got {padding_idx}")
+    scale = _embed_scale(scale)
+    N = ids.numel()
+    ctx, raw = _place(ids.device, stream)
+    with ctx:
+        if dTable is None:
+            dTable = torch.empty((V, C), dtype=dOut.dtype, device=ids.device)
+        else:
+            _tensor(dTable, "dTable", ids.device, dOut.dtype, (V, C))
+            _distinct((("ids", ids), ("dOut", dOut)), (("dTable", dTable),))
+        nbytes = int(_lib().sga_embed_bwd_workspace_bytes(N, C))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=ids.device)
+        _check(_lib().embed_bwd(ids.data_ptr(), id_bytes, dOut.data_ptr(), N, V, C, scale,
+                                padding_idx, dt, dTable.data_ptr(), ws.data_ptr(), nbytes, raw),
+               "embed_bwd")
+    return dTable
+
+
+def embed_device_error(device=None, stream=None) -> int:
+    """Read and clear the embedding calls' error word on ``device`` (default:
+    the current one); 0 = every id was inside its table."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    code = ctypes.c_int32()
+    ctx, raw = _place(device, stream)
+    with ctx:
+        st = _lib().sga_embed_read_device_error(raw, ctypes.byref(code))
+    if st not in (SGA_OK, SGA_EDEVICE_CHECK):
+        _check(st, "sga_embed_read_device_error")
+    return int(code.value)
+
+
 # -------------------------------------------------------------- autograd layers
 
 class GTAttention(torch.autograd.Function):
@@ -696,3 +1094,69 @@ class GATv2Attention(torch.autograd.Function):
         dX, dWl, dWr, da = gatv2_bwd(ctx.plan, X, W_l, W_r, a, FL, FR, out, lse,
                                      dOut.contiguous(), ctx.slope)
         return dX, dWl, dWr, da, None, None
+
+
+class SeqAttention(torch.autograd.Function):
+    """Attention over packed sequences as an autograd function:
+    ``out = SeqAttention.apply(Q, K, V, plan, scale)`` (scale None:
+    1 / sqrt(D)).  Rows behind the plan's last sequence get zeros, in the
+    output and in the gradients."""
+
+    @staticmethod
+    def forward(ctx, Q, K, V, plan, scale=None):
+        Q, K, V = Q.contiguous(), K.contiguous(), V.contiguous()
+        out, lse = seq_attn_fwd(plan, Q, K, V, scale)
+        ctx.plan, ctx.scale = plan, scale
+        ctx.save_for_backward(Q, K, V, out, lse)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dOut):
+        Q, K, V, out, lse = ctx.saved_tensors
+        dQ, dK, dV = seq_attn_bwd(ctx.plan, Q, K, V, out, lse, dOut.contiguous(), ctx.scale)
+        return dQ, dK, dV, None, None
+
+
+class LayerNorm(torch.autograd.Function):
+    """Layer norm over the last dimension as an autograd function:
+    ``out = LayerNorm.apply(X, weight, bias, eps)``; weight and bias [C] in
+    float32 or X's dtype, or None."""
+
+    @staticmethod
+    def forward(ctx, X, weight=None, bias=None, eps=1e-5):
+        X = X.contiguous()
+        weight = None if weight is None else weight.contiguous()
+        bias = None if bias is None else bias.contiguous()
+        out, mean, rstd = layer_norm_fwd(X, weight, bias, eps)
+        ctx.save_for_backward(X, weight, mean, rstd)
+        ctx.has_bias = bias is not None
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dOut):
+        X, weight, mean, rstd = ctx.saved_tensors
+        dX, dw, db = layer_norm_bwd(X, weight, mean, rstd, dOut.contiguous(), ctx.has_bias)
+        return dX, dw, db, None
+
+
+class Embedding(torch.autograd.Function):
+    """Embedding lookup with scaling as an autograd function:
+    ``out = Embedding.apply(ids, table, scale, padding_idx)``; the table's
+    gradient is dense [V, C]."""
+
+    @staticmethod
+    def forward(ctx, ids, table, scale=1.0, padding_idx=None):
+        ids = ids.contiguous()
+        out = embed_fwd(ids, table.contiguous(), scale)
+        ctx.rows, ctx.scale, ctx.padding_idx = table.shape[0], scale, padding_idx
+        ctx.save_for_backward(ids)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dOut):
+        (ids,) = ctx.saved_tensors
+        dTable = embed_bwd(ids, dOut.contiguous(), ctx.rows, ctx.scale, ctx.padding_idx)
+        return None, dTable, None, None

@@ -1,0 +1,505 @@
+// Layer norm over the rows of X [N, C], forward and backward.
+//   mean = sum x / C,  var = sum (x - mean)^2 / C,  rstd = 1 / sqrt(var + eps)
+//   xhat = (x - mean) rstd,  y = xhat w + b
+//   g = dy w,  dx = rstd (g - sum(g) / C - xhat sum(g xhat) / C)
+//   dw = sum over rows dy xhat,  db = sum over rows dy
+//
+// Bound by DRAM: the forward reads x and writes y, the backward reads x and dy
+// and writes dx, each once.  A row is held in the registers of a group of
+// threads (4 to 32 lanes, or a whole block), so the variance is taken about
+// the mean without a second read.  Groups walk the rows with a fixed stride and
+// keep the columns' weights, and in the backward their sums of dw and db, in
+// registers; a block's groups are then added in a fixed order through shared
+// memory, and a second kernel adds the blocks in order: no atomics, bitwise
+// reproducible.  Statistics and sums are fp32.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace sga {
+
+void set_cuda_error(cudaError_t e);   // (api.cu)
+
+namespace {
+
+inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+sga_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return SGA_OK;
+    set_cuda_error(e);
+    return SGA_ECUDA;
+}
+
+struct NormArgs {
+    const void *X, *w, *b, *dY;
+    void *Y, *dX;
+    float *mean, *rstd;
+    const float *mean_in, *rstd_in;
+    float *part;             // [blocks][2][C] sums of dw, db
+    int64_t N;
+    int C;
+    float eps;
+};
+
+// EL consecutive elements at p as fp32: 16-byte loads where EL covers 16 bytes.
+template <typename T, int EL> __device__ __forceinline__ void load_el(const T *p, float (&x)[EL]) {
+    constexpr int CH = Elt<T>::EL;
+    if constexpr (EL % CH == 0) {
+#pragma unroll
+        for (int c = 0; c < EL; c += CH) unpack<T>(*reinterpret_cast<const uint4 *>(p + c), x + c);
+    } else {
+        x[0] = to_f32<T>(*p);
+    }
+}
+template <typename T, int EL> __device__ __forceinline__ void store_el(T *p, const float (&x)[EL]) {
+    constexpr int CH = Elt<T>::EL;
+    if constexpr (EL % CH == 0) {
+#pragma unroll
+        for (int c = 0; c < EL; c += CH) *reinterpret_cast<uint4 *>(p + c) = pack<T>(x + c);
+    } else {
+        *p = from_f32<T>(x[0]);
+    }
+}
+
+// Sum over the TPR threads of a row.  TPR > 32: the whole block is one row;
+// `red` holds a slot per warp and is free to be reused after the next call.
+template <int TPR, int K> __device__ __forceinline__ void row_sum(float (&v)[K], float (*red)[32]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = group_sum<(TPR < 32 ? TPR : 32)>(v[k]);
+    if constexpr (TPR > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[k][threadIdx.x >> 5] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            v[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < TPR / 32; ++i) v[k] += red[k][i];
+        }
+    }
+}
+
+template <typename TX, typename TW, int EL, int TPR, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
+    __shared__ float red[1][32];
+    constexpr int GPB = THREADS / TPR;
+    const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const int nvec = a.C / EL;
+    const TX *X = static_cast<const TX *>(a.X);
+    const TW *w = static_cast<const TW *>(a.w), *b = static_cast<const TW *>(a.b);
+    const float inv = 1.f / (float)a.C;
+    float wr[NV][EL], br[NV][EL];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = v * TPR + sub;
+#pragma unroll
+        for (int i = 0; i < EL; ++i) {
+            wr[v][i] = 1.f;
+            br[v][i] = 0.f;
+        }
+        if (c < nvec && w) load_el<TW, EL>(w + c * EL, wr[v]);
+        if (c < nvec && b) load_el<TW, EL>(b + c * EL, br[v]);
+    }
+    // every group of a warp runs the same number of rounds: the sums are warp-wide calls
+    for (int64_t r0 = (int64_t)blockIdx.x * GPB; r0 < a.N; r0 += (int64_t)gridDim.x * GPB) {
+        const int64_t row = r0 + grp;
+        const bool in = row < a.N;
+        float x[NV][EL], s[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * TPR + sub;
+#pragma unroll
+            for (int i = 0; i < EL; ++i) x[v][i] = 0.f;
+            if (in && c < nvec) load_el<TX, EL>(X + row * a.C + c * EL, x[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < EL; ++i) s[0] += x[v][i];
+        row_sum<TPR, 1>(s, red);
+        const float mean = s[0] * inv;
+        s[0] = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (v * TPR + sub < nvec)
+#pragma unroll
+                for (int i = 0; i < EL; ++i) s[0] = fmaf(x[v][i] - mean, x[v][i] - mean, s[0]);
+        row_sum<TPR, 1>(s, red);
+        const float rstd = rsqrtf(s[0] * inv + a.eps);
+        if (!in) continue;
+        if (sub == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+        TX *Y = static_cast<TX *>(a.Y) + row * a.C;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * TPR + sub;
+            if (c >= nvec) continue;
+            float y[EL];
+#pragma unroll
+            for (int i = 0; i < EL; ++i) y[i] = fmaf((x[v][i] - mean) * rstd, wr[v][i], br[v][i]);
+            store_el<TX, EL>(Y + c * EL, y);
+        }
+    }
+}
+
+template <typename TX, typename TW, int EL, int TPR, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
+    __shared__ float red[2][32];
+    extern __shared__ float acc_sm[];   // [2][C] sums of the block's groups
+    constexpr int GPB = THREADS / TPR;
+    const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const int nvec = a.C / EL;
+    const TX *X = static_cast<const TX *>(a.X), *dY = static_cast<const TX *>(a.dY);
+    const TW *w = static_cast<const TW *>(a.w);
+    const float inv = 1.f / (float)a.C;
+    float wr[NV][EL], dw[NV][EL], db[NV][EL];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = v * TPR + sub;
+#pragma unroll
+        for (int i = 0; i < EL; ++i) {
+            wr[v][i] = 1.f;
+            dw[v][i] = db[v][i] = 0.f;
+        }
+        if (c < nvec && w) load_el<TW, EL>(w + c * EL, wr[v]);
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * GPB; r0 < a.N; r0 += (int64_t)gridDim.x * GPB) {
+        const int64_t row = r0 + grp;
+        const bool in = row < a.N;
+        float x[NV][EL], g[NV][EL], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * TPR + sub;
+#pragma unroll
+            for (int i = 0; i < EL; ++i) x[v][i] = g[v][i] = 0.f;
+            if (in && c < nvec) {
+                load_el<TX, EL>(X + row * a.C + c * EL, x[v]);
+                load_el<TX, EL>(dY + row * a.C + c * EL, g[v]);
+            }
+        }
+        const float mean = in ? a.mean_in[row] : 0.f, rstd = in ? a.rstd_in[row] : 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (v * TPR + sub < nvec)
+#pragma unroll
+                for (int i = 0; i < EL; ++i) {
+                    x[v][i] = (x[v][i] - mean) * rstd;   // xhat
+                    db[v][i] += g[v][i];
+                    dw[v][i] = fmaf(g[v][i], x[v][i], dw[v][i]);
+                    g[v][i] *= wr[v][i];
+                    s[0] += g[v][i];
+                    s[1] = fmaf(g[v][i], x[v][i], s[1]);
+                }
+        row_sum<TPR, 2>(s, red);
+        if (!in) continue;
+        const float c1 = s[0] * inv, c2 = s[1] * inv;
+        TX *dX = static_cast<TX *>(a.dX) + row * a.C;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * TPR + sub;
+            if (c >= nvec) continue;
+            float o[EL];
+#pragma unroll
+            for (int i = 0; i < EL; ++i) o[i] = rstd * (g[v][i] - c1 - x[v][i] * c2);
+            store_el<TX, EL>(dX + c * EL, o);
+        }
+    }
+    if (!a.part) return;
+    // the block's groups, one after the other
+    for (int q = 0; q < GPB; ++q) {
+        __syncthreads();
+        if (grp == q)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = v * TPR + sub;
+                if (c >= nvec) continue;
+#pragma unroll
+                for (int i = 0; i < EL; ++i) {
+                    float *p = acc_sm + c * EL + i, *z = p + a.C;
+                    *p = (q ? *p : 0.f) + dw[v][i];
+                    *z = (q ? *z : 0.f) + db[v][i];
+                }
+            }
+    }
+    __syncthreads();
+    float *out = a.part + (int64_t)blockIdx.x * 2 * a.C;
+    for (int i = threadIdx.x; i < 2 * a.C; i += THREADS) out[i] = acc_sm[i];
+}
+
+// Rows too wide for registers: a block per row, x read again (from L2) in each step.
+template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_fwd_wide_kernel(const NormArgs a) {
+    __shared__ float red[1][32];
+    const TX *X = static_cast<const TX *>(a.X);
+    const TW *w = static_cast<const TW *>(a.w), *b = static_cast<const TW *>(a.b);
+    const float inv = 1.f / (float)a.C;
+    for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+        const TX *x = X + row * a.C;
+        TX *y = static_cast<TX *>(a.Y) + row * a.C;
+        float s[1] = {0.f};
+        for (int c = threadIdx.x; c < a.C; c += 256) s[0] += to_f32<TX>(x[c]);
+        row_sum<256, 1>(s, red);
+        const float mean = s[0] * inv;
+        s[0] = 0.f;
+        for (int c = threadIdx.x; c < a.C; c += 256) {
+            const float d = to_f32<TX>(x[c]) - mean;
+            s[0] = fmaf(d, d, s[0]);
+        }
+        row_sum<256, 1>(s, red);
+        const float rstd = rsqrtf(s[0] * inv + a.eps);
+        for (int c = threadIdx.x; c < a.C; c += 256)
+            y[c] = from_f32<TX>(fmaf((to_f32<TX>(x[c]) - mean) * rstd, w ? to_f32<TW>(w[c]) : 1.f,
+                                     b ? to_f32<TW>(b[c]) : 0.f));
+        if (threadIdx.x == 0) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
+    }
+}
+
+template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_bwd_wide_kernel(const NormArgs a) {
+    __shared__ float red[2][32];
+    const TW *w = static_cast<const TW *>(a.w);
+    const float inv = 1.f / (float)a.C;
+    for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+        const TX *x = static_cast<const TX *>(a.X) + row * a.C, *dy = static_cast<const TX *>(a.dY) + row * a.C;
+        TX *dx = static_cast<TX *>(a.dX) + row * a.C;
+        const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+        float s[2] = {0.f, 0.f};
+        for (int c = threadIdx.x; c < a.C; c += 256) {
+            const float g = to_f32<TX>(dy[c]) * (w ? to_f32<TW>(w[c]) : 1.f);
+            s[0] += g;
+            s[1] = fmaf(g, (to_f32<TX>(x[c]) - mean) * rstd, s[1]);
+        }
+        row_sum<256, 2>(s, red);
+        for (int c = threadIdx.x; c < a.C; c += 256) {
+            const float g = to_f32<TX>(dy[c]) * (w ? to_f32<TW>(w[c]) : 1.f);
+            dx[c] = from_f32<TX>(rstd * (g - s[0] * inv - (to_f32<TX>(x[c]) - mean) * rstd * (s[1] * inv)));
+        }
+    }
+}
+
+// Column sums of wide rows: a thread per column over the rows of a slab.
+template <typename TX> __global__ void __launch_bounds__(256) norm_cols_wide_kernel(const NormArgs a, int64_t slab) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    const int64_t r0 = (int64_t)blockIdx.y * slab, r1 = min(a.N, r0 + slab);
+    if (c >= a.C) return;
+    float dw = 0.f, db = 0.f;
+    for (int64_t r = r0; r < r1; ++r) {
+        const float dy = to_f32<TX>(static_cast<const TX *>(a.dY)[r * a.C + c]);
+        const float xh = (to_f32<TX>(static_cast<const TX *>(a.X)[r * a.C + c]) - a.mean_in[r]) * a.rstd_in[r];
+        dw = fmaf(dy, xh, dw);
+        db += dy;
+    }
+    float *out = a.part + (int64_t)blockIdx.y * 2 * a.C;
+    out[c] = dw;
+    out[a.C + c] = db;
+}
+
+// dw, db from the blocks' sums: 32 columns a block, its eight warps take every
+// eighth partial and are added in order.
+template <typename TW> __global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restrict__ part, int blocks,
+                                                                                 int C, TW *dw, TW *db) {
+    __shared__ float sm[8][32];
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane;   // column of [dw | db]
+    float s = 0.f;
+    if (i < 2 * (int64_t)C)
+        for (int b = wp; b < blocks; b += 8) s += part[(int64_t)b * 2 * C + i];
+    sm[wp][lane] = s;
+    __syncthreads();
+    if (wp == 0 && i < 2 * (int64_t)C) {
+        s = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s += sm[q][lane];
+        if (i < C) dw[i] = from_f32<TW>(s);
+        else if (db) db[i - C] = from_f32<TW>(s);
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 1;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+// Blocks of the backward pass, each with a row of sums: four an SM.
+constexpr int kNormBlocksPerSm = 4;
+int64_t bwd_blocks(int sms) { return (int64_t)sms * kNormBlocksPerSm; }
+
+template <typename TX, typename TW, int EL, int TPR, int NV>
+cudaError_t launch_fwd(const NormArgs &a, cudaStream_t s) {
+    constexpr int TH = TPR > 128 ? TPR : 128;
+    constexpr int GPB = TH / TPR;
+    const int64_t need = (a.N + GPB - 1) / GPB;
+    const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)sm_count() * 16);
+    note_launch(SGA_KERN_NORM_FWD, s, false);
+    norm_fwd_kernel<TX, TW, EL, TPR, NV, TH><<<grid, TH, 0, s>>>(a);
+    note_launch(SGA_KERN_NORM_FWD, s, true);
+    return cudaGetLastError();
+}
+
+template <typename TX, typename TW, int EL, int TPR, int NV>
+cudaError_t launch_bwd(const NormArgs &a, int &blocks, cudaStream_t s) {
+    constexpr int TH = TPR > 128 ? TPR : 128;
+    constexpr int GPB = TH / TPR;
+    const int64_t need = (a.N + GPB - 1) / GPB;
+    blocks = (int)std::min<int64_t>(need, bwd_blocks(sm_count()));
+    const size_t smem = a.part ? sizeof(float) * 2 * a.C : 0;
+    if (cudaError_t e = allow_smem<norm_bwd_kernel<TX, TW, EL, TPR, NV, TH>>(smem); e != cudaSuccess) return e;
+    note_launch(SGA_KERN_NORM_BWD, s, false);
+    norm_bwd_kernel<TX, TW, EL, TPR, NV, TH><<<(unsigned)blocks, TH, smem, s>>>(a);
+    note_launch(SGA_KERN_NORM_BWD, s, true);
+    return cudaGetLastError();
+}
+
+// Threads of a row by its number of 16-byte vectors (or of elements, where the
+// width or an address is no multiple of 16 bytes).
+template <typename TX, typename TW> cudaError_t norm_fwd_t(const NormArgs &a, bool vec, cudaStream_t s) {
+    constexpr int EL = Elt<TX>::EL;
+    const int nv = a.C / EL;
+    if (vec && nv <= 16) return launch_fwd<TX, TW, EL, 4, 4>(a, s);
+    if (vec && nv <= 32) return launch_fwd<TX, TW, EL, 8, 4>(a, s);
+    if (vec && nv <= 64) return launch_fwd<TX, TW, EL, 16, 4>(a, s);
+    if (vec && nv <= 128) return launch_fwd<TX, TW, EL, 32, 4>(a, s);
+    if (vec && nv <= 1024) return launch_fwd<TX, TW, EL, 256, 4>(a, s);
+    if (a.C <= 64) return launch_fwd<TX, TW, 1, 16, 4>(a, s);
+    if (a.C <= 512) return launch_fwd<TX, TW, 1, 32, 16>(a, s);
+    if (a.C <= 4096) return launch_fwd<TX, TW, 1, 256, 16>(a, s);
+    const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)sm_count() * 8);
+    note_launch(SGA_KERN_NORM_FWD, s, false);
+    norm_fwd_wide_kernel<TX, TW><<<grid, 256, 0, s>>>(a);
+    note_launch(SGA_KERN_NORM_FWD, s, true);
+    return cudaGetLastError();
+}
+
+template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bool vec, TW *dw, TW *db, cudaStream_t s) {
+    constexpr int EL = Elt<TX>::EL;
+    const int nv = a.C / EL;
+    int blocks = 0;
+    cudaError_t e;
+    if (vec && nv <= 8) e = launch_bwd<TX, TW, EL, 4, 2>(a, blocks, s);
+    else if (vec && nv <= 16) e = launch_bwd<TX, TW, EL, 8, 2>(a, blocks, s);
+    else if (vec && nv <= 32) e = launch_bwd<TX, TW, EL, 16, 2>(a, blocks, s);
+    else if (vec && nv <= 64) e = launch_bwd<TX, TW, EL, 32, 2>(a, blocks, s);
+    else if (vec && nv <= 512) e = launch_bwd<TX, TW, EL, 256, 2>(a, blocks, s);
+    else if (a.C <= 64) e = launch_bwd<TX, TW, 1, 16, 4>(a, blocks, s);
+    else if (a.C <= 512) e = launch_bwd<TX, TW, 1, 32, 16>(a, blocks, s);
+    else if (a.C <= 4096) e = launch_bwd<TX, TW, 1, 256, 16>(a, blocks, s);
+    else {
+        const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)sm_count() * 8);
+        note_launch(SGA_KERN_NORM_BWD, s, false);
+        norm_bwd_wide_kernel<TX, TW><<<grid, 256, 0, s>>>(a);
+        note_launch(SGA_KERN_NORM_BWD, s, true);
+        if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
+        const int64_t want = std::min<int64_t>(bwd_blocks(sm_count()), (a.N + 15) / 16);
+        const int64_t slab = (a.N + want - 1) / want;
+        blocks = (int)((a.N + slab - 1) / slab);
+        note_launch(SGA_KERN_NORM_BWD, s, false);
+        norm_cols_wide_kernel<TX><<<dim3((unsigned)((a.C + 255) / 256), (unsigned)blocks), 256, 0, s>>>(a, slab);
+        note_launch(SGA_KERN_NORM_BWD, s, true);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || !a.part) return e;
+    note_launch(SGA_KERN_NORM_REDUCE, s, false);
+    norm_reduce_kernel<TW><<<(unsigned)((2 * (int64_t)a.C + 31) / 32), 256, 0, s>>>(a.part, blocks, a.C, dw, db);
+    note_launch(SGA_KERN_NORM_REDUCE, s, true);
+    return cudaGetLastError();
+}
+
+sga_status check_norm(int64_t N, int64_t C, sga_dtype dt, sga_dtype wdt) {
+    if (N < 0 || C < 1) return SGA_EINVAL;
+    if (dt != SGA_F32 && dt != SGA_BF16) return SGA_EUNSUPPORTED;
+    if (wdt != SGA_F32 && wdt != dt) return SGA_EUNSUPPORTED;
+    if (C > (1 << 20)) return SGA_EUNSUPPORTED;
+    return SGA_OK;
+}
+size_t size_of(sga_dtype dt) { return dt == SGA_F32 ? 4 : 2; }
+
+}  // namespace
+}  // namespace sga
+
+using namespace sga;
+
+extern "C" {
+
+sga_status layer_norm_fwd(const void *X, const void *weight, const void *bias, int64_t N, int64_t C, float eps,
+                          sga_dtype dt, sga_dtype wdt, void *out, float *mean, float *rstd, void *stream) {
+    sga_status st = check_norm(N, C, dt, wdt);
+    if (st != SGA_OK) return st;
+    if (!(eps >= 0.f) || !(eps < INFINITY) || (bias && !weight)) return SGA_EINVAL;
+    if (N == 0) return SGA_OK;
+    const size_t e = size_of(dt), we = size_of(wdt);
+    if (!X || !out || !mean || !rstd || !aligned(X, e) || !aligned(out, e) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+        !aligned(weight, we) || !aligned(bias, we))
+        return SGA_EINVAL;
+    NormArgs a{};
+    a.X = X;
+    a.w = weight;
+    a.b = bias;
+    a.Y = out;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.N = N;
+    a.C = (int)C;
+    a.eps = eps;
+    const bool vec = (C * e) % 16 == 0 && aligned(X, 16) && aligned(out, 16) && aligned(weight, 16) && aligned(bias, 16);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dt == SGA_F32) return status_of(norm_fwd_t<float, float>(a, vec, s));
+    if (wdt == SGA_F32) return status_of(norm_fwd_t<__nv_bfloat16, float>(a, vec, s));
+    return status_of(norm_fwd_t<__nv_bfloat16, __nv_bfloat16>(a, vec, s));
+}
+
+size_t sga_norm_bwd_workspace_bytes(int64_t N, int64_t C) {
+    if (N <= 0 || C <= 0) return 0;
+    return (size_t)std::min<int64_t>(bwd_blocks(sm_count()), N) * 2 * (size_t)C * sizeof(float);
+}
+
+sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, const float *rstd, const void *dOut,
+                          int64_t N, int64_t C, sga_dtype dt, sga_dtype wdt, void *dX, void *dweight, void *dbias,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+    sga_status st = check_norm(N, C, dt, wdt);
+    if (st != SGA_OK) return st;
+    if ((dweight || dbias) && !weight) return SGA_EINVAL;
+    if (dbias && !dweight) return SGA_EINVAL;
+    const size_t e = size_of(dt), we = size_of(wdt);
+    if (!aligned(weight, we) || !aligned(dweight, we) || !aligned(dbias, we)) return SGA_EINVAL;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) {   // an empty sum
+        cudaError_t ce = cudaSuccess;
+        if (dweight) ce = cudaMemsetAsync(dweight, 0, C * we, s);
+        if (ce == cudaSuccess && dbias) ce = cudaMemsetAsync(dbias, 0, C * we, s);
+        return status_of(ce);
+    }
+    if (!X || !dOut || !dX || !mean || !rstd || !aligned(X, e) || !aligned(dOut, e) || !aligned(dX, e) ||
+        !aligned(mean, 4) || !aligned(rstd, 4))
+        return SGA_EINVAL;
+    if (dweight) {
+        if (!workspace || !aligned(workspace, 16)) return SGA_EINVAL;
+        if (workspace_bytes < sga_norm_bwd_workspace_bytes(N, C)) return SGA_EWORKSPACE;
+    }
+    NormArgs a{};
+    a.X = X;
+    a.w = weight;
+    a.dY = dOut;
+    a.dX = dX;
+    a.mean_in = mean;
+    a.rstd_in = rstd;
+    a.part = dweight ? static_cast<float *>(workspace) : nullptr;
+    a.N = N;
+    a.C = (int)C;
+    const bool vec = (C * e) % 16 == 0 && aligned(X, 16) && aligned(dOut, 16) && aligned(dX, 16) && aligned(weight, 16);
+    if (dt == SGA_F32)
+        return status_of(norm_bwd_t<float, float>(a, vec, static_cast<float *>(dweight), static_cast<float *>(dbias), s));
+    if (wdt == SGA_F32)
+        return status_of(norm_bwd_t<__nv_bfloat16, float>(a, vec, static_cast<float *>(dweight),
+                                                          static_cast<float *>(dbias), s));
+    return status_of(norm_bwd_t<__nv_bfloat16, __nv_bfloat16>(a, vec, static_cast<__nv_bfloat16 *>(dweight),
+                                                              static_cast<__nv_bfloat16 *>(dbias), s));
+}
+
+}  // extern "C"

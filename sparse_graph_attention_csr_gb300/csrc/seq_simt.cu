@@ -1,0 +1,444 @@
+// Packed-sequence attention in fp32, on the FMA pipes, and the row terms of
+// the backward pass for both dtypes.
+//
+// The tensor cores have no fp32 product, and the tolerance of the fp32 layers
+// (1e-5) rules out tf32, so these kernels are bound by the FMA rate (two
+// products of the forward, three and four of the backward's two passes).
+// Blocks of 256 threads (16 x 16) take a 64-row tile of one side and walk the
+// 64-row tiles of the other through shared memory; each thread holds a 4 x 4
+// piece of the scores and a 4 x D/16 piece of the result.  Tiles are row-major
+// with rows of D + 4 floats: both products read them 16 bytes at a time along
+// a row without bank conflicts, so no tile is stored transposed.
+//   forward: S = Q K^T, online softmax (running maximum and sum per row),
+//     O = O alpha + P V;
+//   dQ pass (a tile of queries): S, dP = dOut V^T, dS = P (dP - Delta),
+//     dQ += dS K;
+//   dK/dV pass (a tile of keys, over the query heads of its group): S^T =
+//     K Q^T, dP^T = V dOut^T, dV += P^T dOut, dK += dS^T Q.
+// The scores are computed twice in the backward pass so that every output row
+// is owned by one block: no atomics, bitwise reproducible.
+// A pair outside a row's interval is left out of the sums, not multiplied by
+// zero: an infinity or NaN there does not reach the row.
+#include "seq.h"
+
+namespace sga {
+namespace {
+
+constexpr int kT = 64;         // rows of a tile
+constexpr int kThreads = 256;
+constexpr int kPP = kT + 4;    // pitch of a score tile
+
+template <int D> constexpr int kPitch = D + 4;
+template <int D> constexpr int kTileFloats = kT * (D + 4);
+constexpr int kScoreFloats = kT * kPP;
+
+// rows [r0, r0 + 64) of head h of a [T][heads][D] tensor; rows past `rows` read as zero
+template <int D, typename T>
+__device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t r0, int64_t rows, int heads, int h) {
+    constexpr int EL = Elt<T>::EL, CH = D / EL;
+    for (int i = threadIdx.x; i < kT * CH; i += kThreads) {
+        const int r = i / CH, c = i % CH;
+        const int64_t row = r0 + r;
+        float v[EL];
+#pragma unroll
+        for (int x = 0; x < EL; ++x) v[x] = 0.f;
+        if (row < rows) unpack<T>(ldg16(src + (row * heads + h) * D + EL * c), v);
+#pragma unroll
+        for (int x = 0; x < EL; x += 4)
+            *reinterpret_cast<float4 *>(dst + r * kPitch<D> + EL * c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+    }
+}
+
+// s[a][c] = row (ty + 16 a) of A . row (tx + 16 c) of B
+template <int D>
+__device__ __forceinline__ void dot_tiles(float (&s)[4][4], const float *A, const float *B, int ty, int tx) {
+    float2 acc[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[a][c] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4 *>(A + (ty + 16 * a) * kPitch<D> + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4 *>(B + (tx + 16 * c) * kPitch<D> + d);
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[a][c] = ffma2(make_float2(x[a].x, x[a].y), make_float2(y[c].x, y[c].y), acc[a][c]);
+                acc[a][c] = ffma2(make_float2(x[a].z, x[a].w), make_float2(y[c].z, y[c].w), acc[a][c]);
+            }
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[a][c] = acc[a][c].x + acc[a][c].y;
+}
+
+// Columns of the result that a thread holds: 4 tx .. + 3 (and + 64 for D =
+// 128); 2 tx, 2 tx + 1 for D = 32.
+template <int D> constexpr int kCols = D / 16;
+template <int D> __device__ __forceinline__ int col_of(int tx, int x) {
+    return D == 32 ? 2 * tx + x : 4 * tx + (x & 3) + 64 * (x >> 2);
+}
+
+template <int D> __device__ __forceinline__ void load_cols(float (&v)[kCols<D>], const float *row, int tx) {
+    if constexpr (D == 32) {
+        const float2 t = *reinterpret_cast<const float2 *>(row + 2 * tx);
+        v[0] = t.x;
+        v[1] = t.y;
+    } else {
+#pragma unroll
+        for (int x = 0; x < kCols<D>; x += 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(row + 4 * tx + 16 * x);
+            v[x] = t.x;
+            v[x + 1] = t.y;
+            v[x + 2] = t.z;
+            v[x + 3] = t.w;
+        }
+    }
+}
+
+// acc[a][x] += sum_j P[ty + 16 a][j] B[j][col x] over the 64 rows of B, with
+// MASKED over those in [lo[a], hi[a]) only
+template <int D, bool MASKED>
+__device__ __forceinline__ void add_product(float (&acc)[4][kCols<D>], const float *P, const float *B, int ty, int tx,
+                                            const int (&lo)[4], const int (&hi)[4]) {
+    constexpr int NC = kCols<D>;
+#pragma unroll 2
+    for (int j = 0; j < kT; j += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) p[a] = *reinterpret_cast<const float4 *>(P + (ty + 16 * a) * kPP + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float v[NC];
+            load_cols<D>(v, B + (j + u) * kPitch<D>, tx);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const float w = u == 0 ? p[a].x : u == 1 ? p[a].y : u == 2 ? p[a].z : p[a].w;
+                if (MASKED) {
+                    if (j + u >= lo[a] && j + u < hi[a])
+#pragma unroll
+                        for (int x = 0; x < NC; ++x) acc[a][x] = fmaf(w, v[x], acc[a][x]);
+                } else {
+                    axpy2<NC>(acc[a], w, v);
+                }
+            }
+        }
+    }
+}
+
+template <int D, typename T>
+__device__ __forceinline__ void store_rows(T *dst, const float (&acc)[4][kCols<D>], const float (&f)[4], int64_t r0,
+                                           int64_t rows, int heads, int h, int ty, int tx) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const int64_t row = r0 + ty + 16 * a;
+        if (row >= rows) continue;
+        T *o = dst + (row * heads + h) * D;
+#pragma unroll
+        for (int x = 0; x < kCols<D>; ++x) o[col_of<D>(tx, x)] = from_f32<T>(acc[a][x] * f[a]);
+    }
+}
+
+__device__ __forceinline__ float half_max(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(SGA_FULL_MASK, v, o));
+    return v;
+}
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(SGA_FULL_MASK, v, o);
+    return v;
+}
+
+// What each of a thread's four rows sees: queries of a key row, or keys of a
+// query row.  Rows past the last see nothing.
+__device__ __forceinline__ void intervals(const SeqArgs &a, bool keys, int64_t r0, int ty, int64_t (&lo)[4], int64_t (&hi)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = r0 + ty + 16 * i;
+        lo[i] = hi[i] = 0;
+        if (row < a.rows) {
+            const int2 se = __ldg(a.range + row);
+            lo[i] = keys && a.causal ? row : se.x;
+            hi[i] = !keys && a.causal ? row + 1 : se.y;
+        }
+    }
+}
+__device__ __forceinline__ void in_tile(const int64_t (&lo)[4], const int64_t (&hi)[4], int64_t t0, int (&l)[4], int (&h)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        l[i] = (int)max((int64_t)0, min((int64_t)kT, lo[i] - t0));
+        h[i] = (int)max((int64_t)0, min((int64_t)kT, hi[i] - t0));
+    }
+}
+
+// ---- forward ------------------------------------------------------------------
+
+template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_fwd_simt_kernel(const SeqArgs a) {
+    extern __shared__ float sm[];
+    float *sQ = sm, *sKV = sQ + kTileFloats<D>, *sP = sKV + kTileFloats<D>;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const SeqTile t = a.qtiles[blockIdx.x / a.H];
+    const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
+    const int64_t q0 = (int64_t)t.tile * kT;
+    const float scale2 = a.scale * kLog2e;
+    load_tile<D>(sQ, static_cast<const T *>(a.Q), q0, a.rows, a.H, h);
+    int64_t lo[4], hi[4];
+    intervals(a, false, q0, ty, lo, hi);
+    float m[4], l[4], acc[4][kCols<D>];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < kCols<D>; ++x) acc[i][x] = 0.f;
+    }
+    for (int kt = t.t0; kt < t.t1; ++kt) {
+        const int64_t k0 = (int64_t)kt * kT;
+        const bool full = kt >= t.f0 && kt < t.f1;
+        int kl[4], kh[4];
+        in_tile(lo, hi, k0, kl, kh);
+        __syncthreads();
+        load_tile<D>(sKV, static_cast<const T *>(a.K), k0, a.rows, a.Hkv, hk);
+        __syncthreads();
+        float s[4][4];
+        dot_tiles<D>(s, sQ, sKV, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = tx + 16 * c;
+                s[i][c] = full || (j >= kl[i] && j < kh[i]) ? s[i][c] * scale2 : -INFINITY;
+                mx = fmaxf(mx, s[i][c]);
+            }
+            const float mn = fmaxf(m[i], half_max(mx));
+            const float al = exp2_diff(m[i], mn);
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float p = exp2_diff(s[i][c], mn);
+                sP[(ty + 16 * i) * kPP + tx + 16 * c] = p;
+                sum += p;
+            }
+            l[i] = l[i] * al + half_sum(sum);
+            m[i] = mn;
+#pragma unroll
+            for (int x = 0; x < kCols<D>; ++x) acc[i][x] *= al;
+        }
+        __syncthreads();
+        load_tile<D>(sKV, static_cast<const T *>(a.V), k0, a.rows, a.Hkv, hk);
+        __syncthreads();
+        if (full) add_product<D, false>(acc, sP, sKV, ty, tx, kl, kh);
+        else add_product<D, true>(acc, sP, sKV, ty, tx, kl, kh);
+    }
+    float inv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        inv[i] = 1.f / l[i];
+        const int64_t row = q0 + ty + 16 * i;
+        if (tx == 0 && row < a.rows) a.lse_w[row * a.H + h] = (m[i] + log2f(l[i])) * kLn2;
+    }
+    store_rows<D>(static_cast<T *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+}
+
+// ---- backward -------------------------------------------------------------------
+
+template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd_dq_simt_kernel(const SeqArgs a) {
+    extern __shared__ float sm[];
+    float *sQ = sm, *sG = sQ + kTileFloats<D>, *sK = sG + kTileFloats<D>, *sV = sK + kTileFloats<D>,
+          *sP = sV + kTileFloats<D>;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const SeqTile t = a.qtiles[blockIdx.x / a.H];
+    const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
+    const int64_t q0 = (int64_t)t.tile * kT;
+    const float scale2 = a.scale * kLog2e;
+    load_tile<D>(sQ, static_cast<const T *>(a.Q), q0, a.rows, a.H, h);
+    load_tile<D>(sG, static_cast<const T *>(a.dOut), q0, a.rows, a.H, h);
+    int64_t lo[4], hi[4];
+    intervals(a, false, q0, ty, lo, hi);
+    float ls[4], dl[4], acc[4][kCols<D>];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = (int64_t)h * a.rows_pad + q0 + ty + 16 * i;
+        ls[i] = a.ws_lse[r];
+        dl[i] = a.ws_delta[r];
+#pragma unroll
+        for (int x = 0; x < kCols<D>; ++x) acc[i][x] = 0.f;
+    }
+    for (int kt = t.t0; kt < t.t1; ++kt) {
+        const int64_t k0 = (int64_t)kt * kT;
+        const bool full = kt >= t.f0 && kt < t.f1;
+        int kl[4], kh[4];
+        in_tile(lo, hi, k0, kl, kh);
+        __syncthreads();
+        load_tile<D>(sK, static_cast<const T *>(a.K), k0, a.rows, a.Hkv, hk);
+        load_tile<D>(sV, static_cast<const T *>(a.V), k0, a.rows, a.Hkv, hk);
+        __syncthreads();
+        float s[4][4], g[4][4];
+        dot_tiles<D>(s, sQ, sK, ty, tx);
+        dot_tiles<D>(g, sG, sV, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = tx + 16 * c;
+                const bool on = full || (j >= kl[i] && j < kh[i]);
+                sP[(ty + 16 * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, -ls[i])) * (g[i][c] - dl[i]) : 0.f;
+            }
+        __syncthreads();
+        if (full) add_product<D, false>(acc, sP, sK, ty, tx, kl, kh);
+        else add_product<D, true>(acc, sP, sK, ty, tx, kl, kh);
+    }
+    const float f[4] = {a.scale, a.scale, a.scale, a.scale};
+    store_rows<D>(static_cast<T *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
+}
+
+template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd_dkdv_simt_kernel(const SeqArgs a) {
+    extern __shared__ float sm[];
+    float *sK = sm, *sV = sK + kTileFloats<D>, *sQ = sV + kTileFloats<D>, *sG = sQ + kTileFloats<D>,
+          *sP = sG + kTileFloats<D>, *sS = sP + kScoreFloats;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const SeqTile t = a.ktiles[blockIdx.x / a.Hkv];
+    const int hk = blockIdx.x % a.Hkv, grp = a.H / a.Hkv;
+    const int64_t k0 = (int64_t)t.tile * kT;
+    const float scale2 = a.scale * kLog2e;
+    load_tile<D>(sK, static_cast<const T *>(a.K), k0, a.rows, a.Hkv, hk);
+    load_tile<D>(sV, static_cast<const T *>(a.V), k0, a.rows, a.Hkv, hk);
+    int64_t lo[4], hi[4];
+    intervals(a, true, k0, ty, lo, hi);
+    float dk[4][kCols<D>], dv[4][kCols<D>];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int x = 0; x < kCols<D>; ++x) dk[i][x] = dv[i][x] = 0.f;
+    for (int h = hk * grp; h < (hk + 1) * grp; ++h)
+        for (int qt = t.t0; qt < t.t1; ++qt) {
+            const int64_t q0 = (int64_t)qt * kT;
+            const bool full = qt >= t.f0 && qt < t.f1;
+            int ql[4], qh[4];
+            in_tile(lo, hi, q0, ql, qh);
+            __syncthreads();
+            load_tile<D>(sQ, static_cast<const T *>(a.Q), q0, a.rows, a.H, h);
+            load_tile<D>(sG, static_cast<const T *>(a.dOut), q0, a.rows, a.H, h);
+            __syncthreads();
+            float s[4][4], g[4][4], ls[4], dl[4];
+            dot_tiles<D>(s, sK, sQ, ty, tx);
+            dot_tiles<D>(g, sV, sG, ty, tx);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int64_t r = (int64_t)h * a.rows_pad + q0 + tx + 16 * c;
+                ls[c] = a.ws_lse[r];
+                dl[c] = a.ws_delta[r];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int j = tx + 16 * c;
+                    const bool on = full || (j >= ql[i] && j < qh[i]);
+                    const float p = on ? fast_exp2(fmaf(s[i][c], scale2, -ls[c])) : 0.f;
+                    sP[(ty + 16 * i) * kPP + j] = p;
+                    sS[(ty + 16 * i) * kPP + j] = on ? p * (g[i][c] - dl[c]) : 0.f;
+                }
+            __syncthreads();
+            if (full) {
+                add_product<D, false>(dv, sP, sG, ty, tx, ql, qh);
+                add_product<D, false>(dk, sS, sQ, ty, tx, ql, qh);
+            } else {
+                add_product<D, true>(dv, sP, sG, ty, tx, ql, qh);
+                add_product<D, true>(dk, sS, sQ, ty, tx, ql, qh);
+            }
+        }
+    const float one[4] = {1.f, 1.f, 1.f, 1.f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
+    store_rows<D>(static_cast<T *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
+    store_rows<D>(static_cast<T *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
+}
+
+// Row terms: D / EL lanes of 16 bytes a (row, head).  Rows behind the last
+// sequence (to the end of its tile) get lse = +inf, so that their weights are
+// zero, and Delta = 0.
+template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
+    constexpr int EL = Elt<T>::EL, L = D / EL;
+    const int64_t g = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+    const int sub = threadIdx.x % L;
+    const int64_t row = g / a.H;
+    const int h = (int)(g % a.H);
+    if (row >= a.rows_pad) return;   // whole warps: rows_pad * H * L is a multiple of 32
+    float d = 0.f;
+    const bool in = row < a.rows;
+    if (in) {
+        const int64_t off = (row * a.H + h) * D + sub * EL;
+        float x[EL], y[EL];
+        unpack<T>(ldg16(static_cast<const T *>(a.out) + off), x);
+        unpack<T>(ldg16(static_cast<const T *>(a.dOut) + off), y);
+#pragma unroll
+        for (int i = 0; i < EL; ++i) d = fmaf(x[i], y[i], d);
+    }
+    d = group_sum<L>(d);
+    if (sub == 0) {
+        const int64_t at = (int64_t)h * a.rows_pad + row;
+        a.ws_lse[at] = in ? a.lse[row * a.H + h] * kLog2e : INFINITY;
+        a.ws_delta[at] = in ? d : 0.f;
+    }
+}
+
+template <typename T, int D> cudaError_t launch_fwd(const SeqArgs &a, cudaStream_t s) {
+    const size_t smem = sizeof(float) * (2 * kTileFloats<D> + kScoreFloats);
+    if (cudaError_t e = allow_smem<seq_fwd_simt_kernel<T, D>>(smem); e != cudaSuccess) return e;
+    note_launch(SGA_KERN_SEQ_FWD, s, false);
+    seq_fwd_simt_kernel<T, D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, smem, s>>>(a);
+    note_launch(SGA_KERN_SEQ_FWD, s, true);
+    return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
+    const size_t smem_q = sizeof(float) * (4 * kTileFloats<D> + kScoreFloats);
+    const size_t smem_k = sizeof(float) * (4 * kTileFloats<D> + 2 * kScoreFloats);
+    cudaError_t e = allow_smem<seq_bwd_dq_simt_kernel<T, D>>(smem_q);
+    if (e == cudaSuccess) e = allow_smem<seq_bwd_dkdv_simt_kernel<T, D>>(smem_k);
+    if (e == cudaSuccess) e = seq_row_terms<T>(a, D, s);
+    if (e != cudaSuccess) return e;
+    note_launch(SGA_KERN_SEQ_BWD_DKDV, s, false);
+    seq_bwd_dkdv_simt_kernel<T, D><<<(unsigned)((int64_t)a.n_tiles * a.Hkv), kThreads, smem_k, s>>>(a);
+    note_launch(SGA_KERN_SEQ_BWD_DKDV, s, true);
+    note_launch(SGA_KERN_SEQ_BWD_DQ, s, false);
+    seq_bwd_dq_simt_kernel<T, D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, smem_q, s>>>(a);
+    note_launch(SGA_KERN_SEQ_BWD_DQ, s, true);
+    return cudaGetLastError();
+}
+
+template <typename T, int D> cudaError_t launch_terms(const SeqArgs &a, cudaStream_t s) {
+    const int64_t threads = a.rows_pad * a.H * (D / Elt<T>::EL);
+    note_launch(SGA_KERN_SEQ_BWD_ROWS, s, false);
+    seq_row_terms_kernel<T, D><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(a);
+    note_launch(SGA_KERN_SEQ_BWD_ROWS, s, true);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s) {
+    return D == 32 ? launch_terms<T, 32>(a, s) : D == 64 ? launch_terms<T, 64>(a, s) : launch_terms<T, 128>(a, s);
+}
+template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t);
+template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
+
+template <typename T> cudaError_t seq_fwd_simt(const SeqArgs &a, int D, cudaStream_t s) {
+    return D == 32 ? launch_fwd<T, 32>(a, s) : D == 64 ? launch_fwd<T, 64>(a, s) : launch_fwd<T, 128>(a, s);
+}
+template <typename T> cudaError_t seq_bwd_simt(const SeqArgs &a, int D, cudaStream_t s) {
+    return D == 32 ? launch_bwd<T, 32>(a, s) : D == 64 ? launch_bwd<T, 64>(a, s) : launch_bwd<T, 128>(a, s);
+}
+template cudaError_t seq_fwd_simt<float>(const SeqArgs &, int, cudaStream_t);
+template cudaError_t seq_bwd_simt<float>(const SeqArgs &, int, cudaStream_t);
+template cudaError_t seq_fwd_simt<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
+template cudaError_t seq_bwd_simt<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
+
+}  // namespace sga
