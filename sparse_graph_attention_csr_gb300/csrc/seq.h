@@ -33,6 +33,7 @@ struct sga_seq_plan {
     int2 *d_range = nullptr;          // [rows] (s, e)
     sga::SeqTile *d_qtiles = nullptr; // row tiles of queries, most key tiles first
     sga::SeqTile *d_ktiles = nullptr; // row tiles of keys, most query tiles first
+    sga::SeqTile *d_qpairs = nullptr; // neighbouring row tiles of queries by twos (bf16, odd head groups)
     int32_t *d_err = nullptr;
     int64_t device_bytes = 0;
 };
@@ -49,7 +50,7 @@ struct SeqArgs {
     void *dQ, *dK, *dV;       // backward outputs
     float *ws_lse, *ws_delta; // [H][rows_pad] lse * log2(e) (+inf behind the last row) and Delta
     const int2 *range;
-    const SeqTile *qtiles, *ktiles;
+    const SeqTile *qtiles, *ktiles, *qpairs;
     int64_t rows, rows_pad;
     int H, Hkv, causal, n_tiles, num_sms;
     float scale;
@@ -63,5 +64,8 @@ inline int64_t seq_rows_pad(int64_t rows) { return (rows + 127) / 128 * 128; }
 template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s);
 template <typename T> cudaError_t seq_fwd_simt(const SeqArgs &a, int D, cudaStream_t s);
 template <typename T> cudaError_t seq_bwd_simt(const SeqArgs &a, int D, cudaStream_t s);
+// (seq_fwd.cu, seq_bwd.cu)
+cudaError_t seq_fwd_bf16(const SeqArgs &a, int D, cudaStream_t s);
+cudaError_t seq_bwd_bf16(const SeqArgs &a, int D, cudaStream_t s);
 
 }  // namespace sga

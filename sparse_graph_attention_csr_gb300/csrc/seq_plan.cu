@@ -68,7 +68,33 @@ std::vector<SeqTile> tile_list(const std::vector<int32_t> &ptr, int64_t rows, in
     return all;
 }
 
+// Neighbouring tiles by twos, by the key tiles that a pair walks; a missing
+// second tile lies past the rows and sees nothing.
+std::vector<SeqTile> pair_list(std::vector<SeqTile> all) {
+    std::sort(all.begin(), all.end(), [](const SeqTile &a, const SeqTile &b) { return a.tile < b.tile; });
+    if (all.size() % 2) {
+        SeqTile t = all.back();
+        ++t.tile;
+        t.t1 = t.f0 = t.f1 = t.t0;
+        all.push_back(t);
+    }
+    std::vector<int32_t> order(all.size() / 2);
+    for (size_t i = 0; i < order.size(); ++i) order[i] = (int32_t)i;
+    auto cost = [&](int32_t i) {
+        return std::max(all[2 * i].t1, all[2 * i + 1].t1) - std::min(all[2 * i].t0, all[2 * i + 1].t0);
+    };
+    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return cost(a) > cost(b); });
+    std::vector<SeqTile> out;
+    out.reserve(all.size());
+    for (int32_t i : order) {
+        out.push_back(all[2 * i]);
+        out.push_back(all[2 * i + 1]);
+    }
+    return out;
+}
+
 void seq_free(sga_seq_plan *p) {
+    cudaFree(p->d_qpairs);
     cudaFree(p->d_range);
     cudaFree(p->d_qtiles);
     cudaFree(p->d_ktiles);
@@ -85,10 +111,13 @@ template <typename P> cudaError_t dev_alloc(sga_seq_plan *p, P **out, size_t cou
 cudaError_t seq_build(sga_seq_plan *p, const std::vector<int32_t> &ptr, const int32_t *d_ptr, cudaStream_t s) {
     const std::vector<SeqTile> q = tile_list(ptr, p->rows, p->tile_rows, p->causal, false);
     const std::vector<SeqTile> k = tile_list(ptr, p->rows, p->tile_rows, p->causal, true);
+    const bool pairs = p->dt == SGA_BF16 && p->H / p->Hkv % 2 != 0;
+    const std::vector<SeqTile> qp = pairs ? pair_list(q) : std::vector<SeqTile>();
     p->n_tiles = (int)q.size();
     cudaError_t e = dev_alloc(p, &p->d_range, (size_t)p->rows);
     if (e == cudaSuccess) e = dev_alloc(p, &p->d_qtiles, q.size());
     if (e == cudaSuccess) e = dev_alloc(p, &p->d_ktiles, k.size());
+    if (e == cudaSuccess && pairs) e = dev_alloc(p, &p->d_qpairs, qp.size());
     if (e == cudaSuccess) e = dev_alloc(p, &p->d_err, 1);
     if (e == cudaSuccess) e = cudaMemsetAsync(p->d_err, 0, sizeof(int32_t), s);
     if (e == cudaSuccess && p->rows > 0) {
@@ -96,6 +125,8 @@ cudaError_t seq_build(sga_seq_plan *p, const std::vector<int32_t> &ptr, const in
         e = cudaGetLastError();
         if (e == cudaSuccess)
             e = cudaMemcpyAsync(p->d_qtiles, q.data(), q.size() * sizeof(SeqTile), cudaMemcpyHostToDevice, s);
+        if (e == cudaSuccess && pairs)
+            e = cudaMemcpyAsync(p->d_qpairs, qp.data(), qp.size() * sizeof(SeqTile), cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess)
             e = cudaMemcpyAsync(p->d_ktiles, k.data(), k.size() * sizeof(SeqTile), cudaMemcpyHostToDevice, s);
     }
@@ -118,6 +149,7 @@ SeqArgs seq_args(const sga_seq_plan *p, float scale) {
     a.range = p->d_range;
     a.qtiles = p->d_qtiles;
     a.ktiles = p->d_ktiles;
+    a.qpairs = p->d_qpairs;
     a.rows = p->rows;
     a.rows_pad = seq_rows_pad(p->rows);
     a.H = p->H;
@@ -130,12 +162,15 @@ SeqArgs seq_args(const sga_seq_plan *p, float scale) {
     return a;
 }
 
-// the call's device must be the plan's (its memory and the tensors' live there)
+// The call's device must be the plan's (its memory and the tensors' live
+// there).  Setting it binds the device's context to a thread that has made no
+// runtime call yet (an autograd worker): the tensor-map encoder needs one.
 sga_status on_device(const sga_seq_plan *p) {
     int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return status_of(e);
-    return dev == p->device ? SGA_OK : SGA_EINVAL;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev != p->device) return SGA_EINVAL;
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    return status_of(e);
 }
 
 }  // namespace
@@ -172,7 +207,7 @@ sga_status sga_seq_plan_create(const int32_t *seq_ptr, int64_t B, int H, int Hkv
         p->D = D;
         p->dt = dt;
         p->causal = causal;
-        p->tile_rows = 64;
+        p->tile_rows = dt == SGA_BF16 ? 128 : 64;
         e = cudaGetDevice(&p->device);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
         if (e == cudaSuccess) e = seq_build(p, ptr, seq_ptr, s);
@@ -230,7 +265,7 @@ sga_status seq_attn_fwd(const sga_seq_plan *p, const void *Q, const void *K, con
     a.out_w = out;
     a.lse_w = lse;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(p->dt == SGA_F32 ? seq_fwd_simt<float>(a, p->D, s) : seq_fwd_simt<__nv_bfloat16>(a, p->D, s));
+    return status_of(p->dt == SGA_F32 ? seq_fwd_simt<float>(a, p->D, s) : seq_fwd_bf16(a, p->D, s));
 }
 
 sga_status seq_attn_bwd(const sga_seq_plan *p, const void *Q, const void *K, const void *V, const void *out,
@@ -255,7 +290,7 @@ sga_status seq_attn_bwd(const sga_seq_plan *p, const void *Q, const void *K, con
     a.ws_lse = static_cast<float *>(workspace);
     a.ws_delta = a.ws_lse + (size_t)p->H * a.rows_pad;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(p->dt == SGA_F32 ? seq_bwd_simt<float>(a, p->D, s) : seq_bwd_simt<__nv_bfloat16>(a, p->D, s));
+    return status_of(p->dt == SGA_F32 ? seq_bwd_simt<float>(a, p->D, s) : seq_bwd_bf16(a, p->D, s));
 }
 
 }  // extern "C"

@@ -438,7 +438,5 @@ template <typename T> cudaError_t seq_bwd_simt(const SeqArgs &a, int D, cudaStre
 }
 template cudaError_t seq_fwd_simt<float>(const SeqArgs &, int, cudaStream_t);
 template cudaError_t seq_bwd_simt<float>(const SeqArgs &, int, cudaStream_t);
-template cudaError_t seq_fwd_simt<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
-template cudaError_t seq_bwd_simt<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
 
 }  // namespace sga

@@ -312,6 +312,8 @@ __global__ void __launch_bounds__(kDwThreads, 1) tc_dw_kernel(const __grid_const
 
 namespace {
 
+}  // namespace
+
 // The driver's tensor-map encoder, looked up once through the runtime.
 cudaError_t tmap_encoder(PFN_cuTensorMapEncodeTiled_v12000 &out) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
@@ -326,8 +328,6 @@ cudaError_t tmap_encoder(PFN_cuTensorMapEncodeTiled_v12000 &out) {
     out = encode;
     return cudaSuccess;
 }
-
-}  // namespace
 
 cudaError_t bf16_tensor_map(CUtensorMap *m, const __nv_bfloat16 *base, int64_t rows, int64_t cols,
                             int64_t row_elems, uint32_t box_cols, uint32_t box_rows) {

@@ -10,6 +10,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
 
@@ -62,6 +63,9 @@ inline int dw_slab_rows(int64_t M, int num_sms) {
 }
 
 cudaError_t tc_dw(const TcDw &p, cudaStream_t s);
+
+// The driver's tensor-map encoder, looked up once through the runtime.
+cudaError_t tmap_encoder(PFN_cuTensorMapEncodeTiled_v12000 &out);
 
 // TMA descriptor of a row-major [rows][cols] bf16 matrix with rows of
 // row_elems elements, boxes of box_cols x box_rows, 128-byte swizzle (the
