@@ -506,9 +506,8 @@ typedef enum {
     SGA_KERN_GAT_FWD = 23, SGA_KERN_GAT_BWD_DST = 24, SGA_KERN_GAT_BWD_SRC = 25,
     SGA_KERN_SEQ_FWD = 26, SGA_KERN_SEQ_BWD_ROWS = 27, SGA_KERN_SEQ_BWD_DQ = 28,
     SGA_KERN_SEQ_BWD_DKDV = 29, SGA_KERN_NORM_FWD = 30, SGA_KERN_NORM_BWD = 31,
-    SGA_KERN_NORM_REDUCE = 32, SGA_KERN_EMBED_FWD = 33, SGA_KERN_EMBED_SORT = 34,
-    SGA_KERN_EMBED_SUM = 35, SGA_KERN_EMBED_JOIN = 36,
-    SGA_KERN_COUNT = 37
+    SGA_KERN_NORM_REDUCE = 32, SGA_KERN_EMBED_FWD = 33, SGA_KERN_EMBED_BWD = 34,
+    SGA_KERN_COUNT = 35
 } sga_kernel_id;
 /* (Planned GATv2 passes merge their split rows inside the edge kernels --
  * the last chunk of a row to finish merges it -- so SGA_KERN_GATV2_FWD_MERGE

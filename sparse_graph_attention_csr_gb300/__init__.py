@@ -35,7 +35,7 @@ KERNELS = {
     "bsr_bwd_dkdv": 18, "agg_fwd": 19, "agg_fwd_merge": 20, "agg_bwd": 21, "agg_bwd_merge": 22,
     "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25, "seq_fwd": 26, "seq_bwd_rows": 27,
     "seq_bwd_dq": 28, "seq_bwd_dkdv": 29, "norm_fwd": 30, "norm_bwd": 31, "norm_reduce": 32,
-    "embed_fwd": 33, "embed_sort": 34, "embed_sum": 35, "embed_join": 36,
+    "embed_fwd": 33, "embed_bwd": 34,
 }
 
 SGA_LAYER_ATTENTION, SGA_LAYER_MINMAX, SGA_LAYER_GAT = 0, 1, 2
@@ -627,6 +627,13 @@ def agg_minmax_bwd(plan: Plan, mask, dOut, dX=None, stream=None):
 _NO_CONTEXT = contextlib.nullcontext()
 
 
+def _current_raw_stream(index):
+    """The raw handle of a device's current stream (without a Stream object
+    where torch offers that: 0.1 us instead of 2.9 us a call)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _place(device, stream):
     """(context, raw stream) of a call on tensors of ``device``: on ``stream``,
     or the device's current stream.  Inside the context that device and stream
@@ -634,7 +641,7 @@ def _place(device, stream):
     writes them."""
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            return _NO_CONTEXT, torch.cuda.current_stream().cuda_stream
+            return _NO_CONTEXT, _current_raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
@@ -643,6 +650,9 @@ def _place(device, stream):
 
 def _tensor(t, name, device, dtype, shape):
     """A contiguous CUDA tensor of exactly this device, dtype and shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous() and t.is_cuda):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device != device:

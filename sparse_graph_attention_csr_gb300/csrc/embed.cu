@@ -12,8 +12,11 @@
 // order is fixed and results are bitwise reproducible.
 #include <algorithm>
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
-#include "plan.h"
+
+namespace cg = cooperative_groups;
 
 namespace sga {
 
@@ -93,159 +96,326 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void *__restrict__
 }
 
 // ---- backward -----------------------------------------------------------------
+//
+// One cooperative launch (a block per SM, grid barriers between the steps):
+//   sort: least significant digit first, digits of at most 8 bits.  A warp owns
+//     a run of consecutive tokens and counts their digits in shared memory; a
+//     block adds its warps' counts per digit, a warp per digit adds the blocks',
+//     and every warp then places its tokens in order (equal digits of 32
+//     tokens ranked by lane), so the sort is stable.  Counts are whole numbers:
+//     the order in which they are added does not matter.
+//   sums: groups of lanes over chunks of the sorted list, as described above;
+//   joins: a warp per chunk whose last row runs on; rows of more than kLongRow
+//     chunks by the whole block.
+// The table's rows without a token are zeroed in the first step, whose latency
+// hides the stores.
 
-// Sort key of a token: its id, or V (last, never summed) for the padding id
-// and for an id outside the table.
-__global__ void embed_keys_kernel(const void *__restrict__ ids, bool wide, int64_t N, int64_t V, int64_t padding,
-                                  int32_t *__restrict__ key, int32_t *__restrict__ val) {
-    for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < N; t += (int64_t)gridDim.x * blockDim.x) {
-        int64_t id = id_at(ids, t, wide);
-        if (id < 0 || id >= V) {
-            atomicOr(&g_embed_err, kErrIndexRange);
-            id = V;
-        }
-        if (id == padding) id = V;
-        key[t] = (int32_t)id;
-        val[t] = (int32_t)t;
-    }
-}
+constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kDigits = 256;
+constexpr int kLongRow = 8;
 
-struct SumArgs {
-    const int32_t *key, *tok;   // sorted
-    const void *dOut;
+struct GradArgs {
+    const void *ids, *dOut;
     void *dTable;
+    int32_t *key[2], *tok[2];   // ping-pong buffers of the sort
+    int32_t *hist, *total;      // [digit][block] counts, [digit] sums
     float *part;                // [chunks][2][C]: the row that runs on from the chunk before, the row that runs on
-    int64_t N, V, chunks;
-    int L, C;
+    int64_t N, V, chunks, padding;
+    int wide, L, C, bits, passes, gshift;
     float scale;
 };
 
-// A warp per (chunk of L sorted tokens, slab of 32 * U groups of columns).
-template <typename T, bool VEC, int U> __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a, int slabs) {
+// Sort key of a token: its id, or V (last, never summed) for the padding id
+// and for an id outside the table.
+__device__ __forceinline__ int32_t key_of(const GradArgs &a, int64_t t) {
+    int64_t id = id_at(a.ids, t, a.wide);
+    if (id < 0 || id >= a.V) {
+        atomicOr(&g_embed_err, kErrIndexRange);
+        id = a.V;
+    }
+    return (int32_t)(id == a.padding ? a.V : id);
+}
+
+__device__ void sort_tokens(const GradArgs &a, int32_t (*cnt)[kDigits], int32_t *scan) {
+    cg::grid_group grid = cg::this_grid();
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, B = gridDim.x;
+    const int64_t per = (a.N + B - 1) / B, per_w = (per + kSortWarps - 1) / kSortWarps;
+    const int64_t b0 = blockIdx.x * per, b1 = min(a.N, b0 + per);
+    const int64_t w0 = min(b1, b0 + wp * per_w), w1 = min(b1, w0 + per_w);
+    for (int p = 0; p < a.passes; ++p) {
+        const int shift = p * a.bits;
+        const int32_t mask = (1 << a.bits) - 1;
+        const int32_t *kin = a.key[p & 1], *vin = a.tok[p & 1];
+        int32_t *kout = a.key[(p + 1) & 1], *vout = a.tok[(p + 1) & 1];
+        for (int d = lane; d < kDigits; d += 32) cnt[wp][d] = 0;
+        __syncwarp();
+        for (int64_t e = w0 + lane; e < w1; e += 32)
+            atomicAdd(&cnt[wp][((p ? __ldcg(kin + e) : key_of(a, e)) >> shift) & mask], 1);
+        __syncthreads();
+        if (threadIdx.x < kDigits) {
+            int32_t run = 0;
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int32_t c = cnt[w][threadIdx.x];
+                cnt[w][threadIdx.x] = run;
+                run += c;
+            }
+            a.hist[(int64_t)threadIdx.x * B + blockIdx.x] = run;
+        }
+        grid.sync();
+        for (int d = blockIdx.x + B * wp; d < kDigits; d += B * kSortWarps) {   // exclusive sums over the blocks
+            int32_t run = 0;
+            for (int i = 0; i < B; i += 32) {
+                const int32_t c = i + lane < B ? __ldcg(a.hist + (int64_t)d * B + i + lane) : 0;
+                int32_t x = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t y = __shfl_up_sync(SGA_FULL_MASK, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (i + lane < B) a.hist[(int64_t)d * B + i + lane] = run + x - c;
+                run += __shfl_sync(SGA_FULL_MASK, x, 31);
+            }
+            if (lane == 0) a.total[d] = run;
+        }
+        grid.sync();
+        // first position of every digit: exclusive sums over the digits' totals
+        if (threadIdx.x < kDigits) {
+            const int32_t c = __ldcg(a.total + threadIdx.x);
+            int32_t x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t y = __shfl_up_sync(SGA_FULL_MASK, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane == 31) scan[wp] = x;
+            scan[kSortWarps + threadIdx.x] = x - c;
+        }
+        __syncthreads();
+        if (threadIdx.x < kDigits) {
+            int32_t base = scan[kSortWarps + threadIdx.x] + __ldcg(a.hist + (int64_t)threadIdx.x * B + blockIdx.x);
+            for (int w = 0; w < wp; ++w) base += scan[w];
+            scan[kSortWarps + kDigits + threadIdx.x] = base;
+        }
+        __syncthreads();
+        for (int d = lane; d < kDigits; d += 32) cnt[wp][d] += scan[kSortWarps + kDigits + d];
+        __syncwarp();
+        for (int64_t e0 = w0; e0 < w1; e0 += 32) {
+            const int64_t e = e0 + lane;
+            const bool valid = e < w1;
+            const int32_t k = valid ? (p ? __ldcg(kin + e) : key_of(a, e)) : 0;
+            const int32_t v = valid ? (p ? __ldcg(vin + e) : (int32_t)e) : 0;
+            const int d = valid ? (k >> shift) & mask : kDigits;
+            const unsigned peers = __match_any_sync(SGA_FULL_MASK, d);
+            const int rank = __popc(peers & ((1u << lane) - 1u));
+            int32_t pos = 0;
+            if (valid) pos = cnt[wp][d] + rank;
+            __syncwarp();
+            if (valid) {
+                kout[pos] = k;
+                vout[pos] = v;
+                if (rank == 0) cnt[wp][d] = pos + __popc(peers);
+            }
+            __syncwarp();
+        }
+        grid.sync();
+    }
+}
+
+// A group of 1 << gshift lanes per (chunk of L sorted tokens, slab of U groups
+// of columns a lane).
+template <typename T, bool VEC, int U> __device__ __forceinline__ void sum_chunks(const GradArgs &a) {
     constexpr int EL = kEl<T, VEC>;
-    const int64_t w = (((int64_t)blockIdx.x * 256) + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    const int64_t chunk = w / slabs;
-    if (chunk >= a.chunks) return;
-    const int g0 = (int)(w % slabs) * 32 * U + lane, n = a.C / EL;
+    const int32_t *key = a.key[a.passes & 1], *tok = a.tok[a.passes & 1];
+    const int lanes = 1 << a.gshift, sub = threadIdx.x & (lanes - 1), n = a.C / EL, step = lanes * U;
+    const int slabs = (n + step - 1) / step;
     const T *dOut = static_cast<const T *>(a.dOut);
     T *dTable = static_cast<T *>(a.dTable);
-    const int64_t k0 = chunk * a.L, k1 = min(a.N, k0 + a.L);
-    float acc[U][EL];
-    int32_t cur = __ldg(a.key + k0);
-    // the first run continues one of the chunk before
-    bool joined = k0 > 0 && __ldg(a.key + k0 - 1) == cur;
-    auto clear = [&] {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < EL; ++i) acc[u][i] = 0.f;
-    };
-    auto flush = [&](bool goes_on) {
-        if (cur >= a.V) return;
-        if (joined || goes_on) {
-            float *p = a.part + ((chunk * 2) + (joined ? 0 : 1)) * a.C;
+    const int64_t items = a.chunks * slabs, groups = ((int64_t)gridDim.x * kSortThreads) >> a.gshift;
+    // neighbouring chunks on different SMs: the hot rows' chunks, alike in cost, are spread
+    for (int64_t it = (((int64_t)threadIdx.x >> a.gshift) * gridDim.x) + blockIdx.x; it < items; it += groups) {
+        const int64_t chunk = it / slabs;
+        const int g0 = (int)(it % slabs) * step + sub;
+        const int64_t k0 = chunk * a.L, k1 = min(a.N, k0 + a.L);
+        float acc[U][EL];
+        int32_t cur = __ldcg(key + k0);
+        bool joined = k0 > 0 && __ldcg(key + k0 - 1) == cur;   // the first run continues one of the chunk before
+        auto clear = [&] {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (g0 + 32 * u < n)
 #pragma unroll
-                    for (int i = 0; i < EL; ++i) p[(g0 + 32 * u) * EL + i] = acc[u][i];
-        } else {
-            T *o = dTable + (int64_t)cur * a.C;
+                for (int i = 0; i < EL; ++i) acc[u][i] = 0.f;
+        };
+        auto flush = [&](bool goes_on) {
+            if (cur >= a.V) return;
+            if (joined || goes_on) {
+                float *p = a.part + ((chunk * 2) + (joined ? 0 : 1)) * a.C;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (g0 + 32 * u < n) {
+                for (int u = 0; u < U; ++u)
+                    if (g0 + lanes * u < n)
 #pragma unroll
-                    for (int i = 0; i < EL; ++i) acc[u][i] *= a.scale;
-                    store_g<T, VEC>(o + (int64_t)(g0 + 32 * u) * EL, acc[u]);
-                }
-        }
-    };
-    clear();
-    for (int64_t kb = k0; kb < k1; kb += 32) {
-        const int m = (int)min((int64_t)32, k1 - kb);
-        const int32_t key = lane < m ? __ldg(a.key + kb + lane) : 0, tok = lane < m ? __ldg(a.tok + kb + lane) : 0;
-        for (int q = 0; q < m; q += 4) {
-            float x[4][U][EL];
-            int32_t kk[4];
+                        for (int i = 0; i < EL; ++i) p[(g0 + lanes * u) * EL + i] = acc[u][i];
+            } else {
+                T *o = dTable + (int64_t)cur * a.C;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                kk[z] = __shfl_sync(SGA_FULL_MASK, key, (q + z) & 31);
-                const int64_t t = __shfl_sync(SGA_FULL_MASK, tok, (q + z) & 31);
-                const bool on = q + z < m && kk[z] < a.V;
+                for (int u = 0; u < U; ++u)
+                    if (g0 + lanes * u < n) {
+                        float y[EL];
+#pragma unroll
+                        for (int i = 0; i < EL; ++i) y[i] = acc[u][i] * a.scale;
+                        store_g<T, VEC>(o + (int64_t)(g0 + lanes * u) * EL, y);
+                    }
+            }
+        };
+        clear();
+        for (int64_t q = k0; q < k1; q += 4) {   // L is a multiple of four, the lists are padded to one
+            const int4 kk = __ldcg(reinterpret_cast<const int4 *>(key + q)), tt = __ldcg(reinterpret_cast<const int4 *>(tok + q));
+            const int32_t ks[4] = {kk.x, kk.y, kk.z, kk.w}, ts[4] = {tt.x, tt.y, tt.z, tt.w};
+            uint4 raw[4][U];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-#pragma unroll
-                    for (int i = 0; i < EL; ++i) x[z][u][i] = 0.f;
-                    if (on && g0 + 32 * u < n) load_g<T, VEC>(dOut + t * a.C + (int64_t)(g0 + 32 * u) * EL, x[z][u]);
+                    raw[z][u] = make_uint4(0, 0, 0, 0);
+                    if (q + z < k1 && ks[z] < a.V && g0 + lanes * u < n) {
+                        const T *p = dOut + (int64_t)ts[z] * a.C + (int64_t)(g0 + lanes * u) * EL;
+                        if constexpr (VEC) raw[z][u] = ldg16_stream(p);
+                        else raw[z][u].x = __float_as_uint(to_f32<T>(__ldg(p)));
+                    }
                 }
-            }
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-                if (q + z >= m) break;
-                if (kk[z] != cur) {
+                if (q + z >= k1) break;
+                if (ks[z] != cur) {
                     flush(false);
                     clear();
-                    cur = kk[z];
+                    cur = ks[z];
                     joined = false;
                 }
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u) {
+                    float x[EL];
+                    if constexpr (VEC) unpack<T>(raw[z][u], x);
+                    else x[0] = __uint_as_float(raw[z][u].x);
 #pragma unroll
-                    for (int i = 0; i < EL; ++i) acc[u][i] += x[z][u][i];
+                    for (int i = 0; i < EL; ++i) acc[u][i] += x[i];
+                }
             }
         }
+        flush(k1 < a.N && __ldcg(key + k1) == cur);
     }
-    flush(k1 < a.N && __ldg(a.key + k1) == cur);
 }
 
-// A block per chunk whose last row runs on into the next chunk, and 32 columns:
-// the row's partials in chunk order, eight warps over a contiguous eighth each.
-template <typename T> __global__ void __launch_bounds__(256) embed_join_kernel(const SumArgs a) {
-    __shared__ float sm[8][32];
-    const int64_t c0 = blockIdx.x;
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int64_t kl = (c0 + 1) * a.L - 1;   // the chunk's last token
-    if (kl + 1 >= a.N) return;
-    const int32_t cur = __ldg(a.key + kl);
-    if (cur >= a.V || __ldg(a.key + kl + 1) != cur) return;
-    if (c0 > 0 && __ldg(a.key + c0 * a.L - 1) == cur) return;   // the row began in an earlier chunk
-    // one past the row's last token
-    int64_t lo = kl + 1, hi = a.N;
+// Whether chunk c0's last row begins in it and runs on; its id and last chunk.
+__device__ __forceinline__ bool runs_on(const GradArgs &a, const int32_t *key, int64_t c0, int32_t &cur, int64_t &cl) {
+    const int64_t kl = (c0 + 1) * a.L - 1;
+    if (kl + 1 >= a.N) return false;
+    cur = __ldcg(key + kl);
+    if (cur >= a.V || __ldcg(key + kl + 1) != cur) return false;
+    if (c0 > 0 && __ldcg(key + c0 * a.L - 1) == cur) return false;   // the row began in an earlier chunk
+    int64_t lo = kl + 1, hi = a.N;   // one past the row's last token: doubling steps, then halving
+    for (int64_t s = a.L; lo + s < hi; s *= 2) {
+        if (__ldcg(key + lo + s) == cur) lo += s;
+        else hi = lo + s;
+    }
     while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(a.key + mid) == cur) lo = mid + 1;
+        if (__ldcg(key + mid) == cur) lo = mid + 1;
         else hi = mid;
     }
-    const int64_t cl = (lo - 1) / a.L;       // the row's last chunk
-    const int64_t n = cl - c0, per = (n + 7) / 8;
-    const int col = blockIdx.y * 32 + lane;
+    cl = (lo - 1) / a.L;
+    return true;
+}
+
+// Partials of a column over the chunks [b, e) (slot 0), M of them in flight.
+template <int M> __device__ __forceinline__ float column_of(const GradArgs &a, int64_t b, int64_t e, int col) {
     float s = 0.f;
-    if (col < a.C) {
-        const int64_t b = c0 + 1 + wp * per, e = min(cl + 1, b + per);
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (wp == 0) v[0] = a.part[(c0 * 2 + 1) * a.C + col];
-        int64_t c = b;
-        for (; c + 4 <= e; c += 4)
+    for (int64_t c = b; c < e; c += M) {
+        float v[M];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) v[z] += a.part[(c + z) * 2 * a.C + col];
-        for (; c < e; ++c) v[0] += a.part[c * 2 * a.C + col];
-        s = (v[0] + v[1]) + (v[2] + v[3]);
+        for (int z = 0; z < M; ++z) v[z] = c + z < e ? __ldcg(a.part + (c + z) * 2 * a.C + col) : 0.f;
+#pragma unroll
+        for (int z = 0; z < M; ++z) s += v[z];
     }
-    sm[wp][lane] = s;
-    __syncthreads();
-    if (wp == 0 && col < a.C) {
-        s = 0.f;
+    return s;
+}
+
+template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &a, float *sm, int64_t *who) {
+    const int32_t *key = a.key[a.passes & 1];
+    T *dTable = static_cast<T *>(a.dTable);
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    for (int64_t base = (int64_t)blockIdx.x * kSortWarps; base < a.chunks; base += (int64_t)gridDim.x * kSortWarps) {
+        const int64_t c0 = base + wp;
+        int32_t cur = 0;
+        int64_t cl = 0;
+        const bool on = c0 < a.chunks && runs_on(a, key, c0, cur, cl);
+        const bool lng = on && cl - c0 > kLongRow;
+        if (lane == 0) who[wp] = lng ? cl : -1;
+        if (on && !lng)
+            for (int c = lane; c < a.C; c += 128) {   // four columns of a lane at a time
+                float s[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) s += sm[q][lane];
-        static_cast<T *>(a.dTable)[(int64_t)cur * a.C + col] = from_f32<T>(s * a.scale);
+                for (int z = 0; z < 4; ++z)
+                    s[z] = c + 32 * z < a.C ? __ldcg(a.part + (c0 * 2 + 1) * a.C + c + 32 * z) : 0.f;
+                for (int64_t k = c0 + 1; k <= cl; ++k)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        s[z] += c + 32 * z < a.C ? __ldcg(a.part + k * 2 * a.C + c + 32 * z) : 0.f;
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    if (c + 32 * z < a.C) dTable[(int64_t)cur * a.C + c + 32 * z] = from_f32<T>(s[z] * a.scale);
+            }
+        __syncthreads();
+        // long rows by the whole block: a warp per 32 columns and share of the chunks
+        const int cols = min(kSortWarps, (a.C + 31) / 32), shares = kSortWarps / cols, slab = wp % cols, share = wp / cols;
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (who[w] < 0) continue;   // (the same for the whole block)
+            const int64_t f = base + w, l = who[w], per = (l - f + shares - 1) / shares;
+            const int32_t id = __ldcg(key + (f + 1) * a.L - 1);
+            for (int cb = 0; cb < a.C; cb += 32 * cols) {
+                const int col = cb + slab * 32 + lane;
+                float s = 0.f;
+                if (col < a.C && share < shares) {
+                    if (share == 0) s = __ldcg(a.part + (f * 2 + 1) * a.C + col);
+                    s += column_of<16>(a, min(l + 1, f + 1 + share * per), min(l + 1, f + 1 + (share + 1) * per), col);
+                }
+                sm[wp * 32 + lane] = s;
+                __syncthreads();
+                if (share == 0 && col < a.C) {
+                    s = 0.f;
+                    for (int q = 0; q < shares; ++q) s += sm[(q * cols + slab) * 32 + lane];
+                    dTable[(int64_t)id * a.C + col] = from_f32<T>(s * a.scale);
+                }
+                __syncthreads();
+            }
+        }
+        __syncthreads();
     }
 }
+
+template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_kernel(const GradArgs a) {
+    __shared__ int32_t cnt[kSortWarps][kDigits];
+    __shared__ int32_t scan[kSortWarps + 2 * kDigits];
+    __shared__ int64_t who[kSortWarps];
+    const int64_t t0 = (int64_t)blockIdx.x * kSortThreads + threadIdx.x, nt = (int64_t)gridDim.x * kSortThreads;
+    if constexpr (VEC) {
+        for (int64_t i = t0; i < a.V * a.C / Elt<T>::EL; i += nt)
+            reinterpret_cast<uint4 *>(a.dTable)[i] = make_uint4(0, 0, 0, 0);
+    } else {
+        for (int64_t i = t0; i < a.V * a.C; i += nt) static_cast<T *>(a.dTable)[i] = from_f32<T>(0.f);
+    }
+    sort_tokens(a, cnt, scan);
+    sum_chunks<T, VEC, VEC ? 1 : 4>(a);
+    cg::this_grid().sync();
+    join_rows<T>(a, reinterpret_cast<float *>(cnt), who);
+}
+
+// Blocks of the gradient's launch: one an SM, fewer where that leaves them under 256 tokens.
+int grad_blocks(int64_t N, int sms) { return (int)std::min<int64_t>(sms, std::max<int64_t>(1, (N + 255) / 256)); }
 
 // Sorted tokens of a chunk: an equal share of the resident warps, at least 16.
 int chunk_len(int64_t N, int sms) {
-    const int64_t per = (N + (int64_t)sms * 32 - 1) / ((int64_t)sms * 32);
-    return (int)std::max<int64_t>(16, (per + 15) / 16 * 16);
+    const int64_t per = (N + (int64_t)sms * kSortWarps - 1) / ((int64_t)sms * kSortWarps);
+    return (int)std::max<int64_t>(16, (per + 3) / 4 * 4);
 }
 
 int bits_of(int64_t v) {
@@ -255,7 +425,7 @@ int bits_of(int64_t v) {
 }
 
 struct Layout {
-    size_t key[2], val[2], hist, scan, part, total;
+    size_t key[2], tok[2], hist, total, part, bytes;
 };
 Layout layout(int64_t N, int64_t C, int sms) {
     Layout l{};
@@ -266,16 +436,27 @@ Layout layout(int64_t N, int64_t C, int sms) {
         return at;
     };
     for (int i = 0; i < 2; ++i) {
-        l.key[i] = take((size_t)N * 4);
-        l.val[i] = take((size_t)N * 4);
+        l.key[i] = take((size_t)N * 4 + 16);
+        l.tok[i] = take((size_t)N * 4 + 16);
     }
-    const int64_t h = radix_hist_elems(N);
-    l.hist = take((size_t)h * 4);
-    l.scan = take((size_t)scan_tmp_elems(h) * 4);
+    l.hist = take((size_t)kDigits * grad_blocks(N, sms) * 4);
+    l.total = take(kDigits * 4);
     const int L = chunk_len(N, sms);
     l.part = take((size_t)((N + L - 1) / L) * 2 * C * 4);
-    l.total = off;
+    l.bytes = off;
     return l;
+}
+
+template <typename T, bool VEC> cudaError_t grad_t(GradArgs a, int blocks, cudaStream_t s) {
+    const int n = a.C / kEl<T, VEC>;
+    a.gshift = 0;
+    while (a.gshift < 5 && (1 << a.gshift) < n) ++a.gshift;
+    void *args[] = {&a};
+    note_launch(SGA_KERN_EMBED_BWD, s, false);
+    const cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(embed_grad_kernel<T, VEC>), dim3(blocks),
+                                                      dim3(kSortThreads), args, 0, s);
+    note_launch(SGA_KERN_EMBED_BWD, s, true);
+    return e;
 }
 
 sga_status check_embed(int64_t N, int64_t V, int64_t C, sga_dtype dt, int id_bytes) {
@@ -298,23 +479,6 @@ cudaError_t fwd_t(const void *ids, bool wide, const void *table, int64_t N, int6
     embed_fwd_kernel<T, VEC><<<grid, 256, 0, s>>>(ids, wide, static_cast<const T *>(table), N, V, C, scale, sh,
                                                   static_cast<T *>(out));
     note_launch(SGA_KERN_EMBED_FWD, s, true);
-    return cudaGetLastError();
-}
-
-template <typename T, bool VEC> cudaError_t sum_t(const SumArgs &a, cudaStream_t s) {
-    const int n = a.C / kEl<T, VEC>;
-    const int U = n <= 32 ? 1 : 2;
-    const int slabs = (n + 32 * U - 1) / (32 * U);
-    const unsigned grid = (unsigned)((a.chunks * slabs + 7) / 8);
-    note_launch(SGA_KERN_EMBED_SUM, s, false);
-    if (U == 1) embed_sum_kernel<T, VEC, 1><<<grid, 256, 0, s>>>(a, slabs);
-    else embed_sum_kernel<T, VEC, 2><<<grid, 256, 0, s>>>(a, slabs);
-    note_launch(SGA_KERN_EMBED_SUM, s, true);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.chunks < 2) return e;
-    note_launch(SGA_KERN_EMBED_JOIN, s, false);
-    embed_join_kernel<T><<<dim3((unsigned)(a.chunks - 1), (unsigned)((a.C + 31) / 32)), 256, 0, s>>>(a);
-    note_launch(SGA_KERN_EMBED_JOIN, s, true);
     return cudaGetLastError();
 }
 
@@ -343,7 +507,7 @@ sga_status embed_fwd(const void *ids, int id_bytes, const void *table, int64_t N
 }
 
 size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t C) {
-    return N <= 0 || C <= 0 || N >= INT32_MAX ? 0 : layout(N, C, sm_count()).total;
+    return N <= 0 || C <= 0 || N >= INT32_MAX ? 0 : layout(N, C, sm_count()).bytes;
 }
 
 sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N, int64_t V, int64_t C, float scale,
@@ -355,39 +519,38 @@ sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N,
     if (V > 0 && (!dTable || !aligned(dTable, e))) return SGA_EINVAL;
     if (N > 0 && (!ids || !aligned(ids, id_bytes) || !dOut || !aligned(dOut, e))) return SGA_EINVAL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (N == 0) return status_of(V > 0 ? cudaMemsetAsync(dTable, 0, (size_t)V * C * e, s) : cudaSuccess);
     const int sms = sm_count();
-    const Layout l = layout(std::max<int64_t>(N, 1), C, sms);
-    if (N > 0) {
-        if (!workspace || !aligned(workspace, 256)) return SGA_EINVAL;
-        if (workspace_bytes < l.total) return SGA_EWORKSPACE;
-    }
-    // rows without a token
-    cudaError_t ce = V > 0 ? cudaMemsetAsync(dTable, 0, (size_t)V * C * e, s) : cudaSuccess;
-    if (ce != cudaSuccess || N == 0) return status_of(ce);
-    auto at = [&](size_t off) { return reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + off); };
-    int32_t *ka = at(l.key[0]), *kb = at(l.key[1]), *va = at(l.val[0]), *vb = at(l.val[1]);
-    note_launch(SGA_KERN_EMBED_SORT, s, false);
-    embed_keys_kernel<<<(unsigned)std::min<int64_t>((N + 255) / 256, sms * 8), 256, 0, s>>>(ids, id_bytes == 8, N, V,
-                                                                                          padding_idx, ka, va);
-    ce = cudaGetLastError();
-    if (ce == cudaSuccess) ce = radix_sort_pairs(&ka, &va, &kb, &vb, N, bits_of(V), at(l.hist), at(l.scan), s);
-    note_launch(SGA_KERN_EMBED_SORT, s, true);
-    if (ce != cudaSuccess || V == 0) return status_of(ce);
-    SumArgs a{};
-    a.key = ka;
-    a.tok = va;
+    const Layout l = layout(N, C, sms);
+    if (!workspace || !aligned(workspace, 256)) return SGA_EINVAL;
+    if (workspace_bytes < l.bytes) return SGA_EWORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    GradArgs a{};
+    a.ids = ids;
+    a.wide = id_bytes == 8;
     a.dOut = dOut;
     a.dTable = dTable;
-    a.part = reinterpret_cast<float *>(at(l.part));
+    for (int i = 0; i < 2; ++i) {
+        a.key[i] = reinterpret_cast<int32_t *>(ws + l.key[i]);
+        a.tok[i] = reinterpret_cast<int32_t *>(ws + l.tok[i]);
+    }
+    a.hist = reinterpret_cast<int32_t *>(ws + l.hist);
+    a.total = reinterpret_cast<int32_t *>(ws + l.total);
+    a.part = reinterpret_cast<float *>(ws + l.part);
     a.N = N;
     a.V = V;
     a.C = (int)C;
     a.L = chunk_len(N, sms);
     a.chunks = (N + a.L - 1) / a.L;
+    a.padding = padding_idx;
     a.scale = scale;
+    const int bits = bits_of(V);
+    a.passes = (bits + 7) / 8;
+    a.bits = (bits + a.passes - 1) / a.passes;
     const bool vec = (C * e) % 16 == 0 && aligned(dOut, 16) && aligned(dTable, 16);
-    if (dt == SGA_F32) return status_of(vec ? sum_t<float, true>(a, s) : sum_t<float, false>(a, s));
-    return status_of(vec ? sum_t<__nv_bfloat16, true>(a, s) : sum_t<__nv_bfloat16, false>(a, s));
+    const int blocks = grad_blocks(N, sms);
+    if (dt == SGA_F32) return status_of(vec ? grad_t<float, true>(a, blocks, s) : grad_t<float, false>(a, blocks, s));
+    return status_of(vec ? grad_t<__nv_bfloat16, true>(a, blocks, s) : grad_t<__nv_bfloat16, false>(a, blocks, s));
 }
 
 sga_status sga_embed_read_device_error(void *stream, int32_t *code) {
