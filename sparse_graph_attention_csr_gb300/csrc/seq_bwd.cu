@@ -67,7 +67,7 @@ struct BwdParams {
 __device__ __forceinline__ void mma_rows128(uint32_t d, uint32_t ta, uint32_t b, uint32_t idesc, bool first) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        tc::mma_bf16_ts(d, ta + (kk >> 2) * 64 + (kk & 3) * 8, tc::desc_sw128_mn(b + kk * 2048, 16384), idesc,
+        tc::mma_bf16_ts_w(d, ta + (kk >> 2) * 64 + (kk & 3) * 8, tc::desc_sw128_mn(b + kk * 2048, 16384), idesc,
                         (!first || kk > 0) ? 1u : 0u);
 }
 // 128 x 128 over the head width, both operands K-major tiles of 128 rows.
@@ -75,7 +75,7 @@ template <int DP> __device__ __forceinline__ void mma_over_d(uint32_t d, uint32_
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
         const uint32_t o = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
-        tc::mma_bf16_ss(d, tc::desc_sw128(a + o), tc::desc_sw128(b + o), idesc, kk > 0);
+        tc::mma_bf16_ss_w(d, tc::desc_sw128(a + o), tc::desc_sw128(b + o), idesc, kk > 0);
     }
 }
 
@@ -181,7 +181,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t kv_full, full[C::NST], empty[C::NST], s_full, dp_full, p_full, ds_full, acc_full;
     __shared__ uint32_t tmem_base;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem);
     const SeqTile t = a.ktiles[blockIdx.x / a.Hkv];
     const int hk = blockIdx.x % a.Hkv, grp = a.H / a.Hkv;
@@ -238,54 +238,54 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
             tc::mbar_wait(&kv_full, 0, tc::kWaitLimit);
             for (int i = e - 1; i >= 0 && i >= e - C::NST; --i)
                 tc::mbar_wait(&full[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
-        } else if (warp == 1 && lane == 0) {   // ---------------------------- MMA issuer
+        } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128), idesc_g = tc::idesc_bf16(128, C::DP) | tc::kMajorMnB;
             const uint32_t ka = sbase + C::R0, va = ka + C::TB;
             auto entry = [&](int e) { return sbase + C::ST0 + (e % C::NST) * C::TB; };
-            auto landed = [&](int e) { return tc::mbar_wait(&full[e % C::NST], (e / C::NST) & 1, tc::kWaitLimit); };
-            bool ok = tc::mbar_wait(&kv_full, 0, tc::kWaitLimit) && landed(0);
+            auto landed = [&](int e) { return tc::warp_wait(&full[e % C::NST], (e / C::NST) & 1, tc::kWaitLimit); };
+            bool ok = tc::warp_wait(&kv_full, 0, tc::kWaitLimit) && landed(0);
             if (ok) {
                 tc::fence_after_sync();
                 mma_over_d<C::DP>(tS, ka, entry(0), idesc_s);
-                tc::mma_commit(&s_full);
+                tc::mma_commit_w(&s_full);
                 ok = landed(1);
             }
             if (ok) {
                 tc::fence_after_sync();
                 mma_over_d<C::DP>(tP, va, entry(1), idesc_s);
-                tc::mma_commit(&dp_full);
+                tc::mma_commit_w(&dp_full);
             }
             for (int i = 0; i < n && ok; ++i) {
                 const int e = 2 * i;
-                if (!tc::mbar_wait(&p_full, i & 1, tc::kWaitLimit)) ok = false;
+                if (!tc::warp_wait(&p_full, i & 1, tc::kWaitLimit)) ok = false;
                 if (!ok) break;
                 tc::fence_after_sync();
                 mma_rows128(tV, tS, entry(e + 1), idesc_g, i == 0);   // dV += P^T dOut
-                tc::mma_commit(&empty[(e + 1) % C::NST]);
+                tc::mma_commit_w(&empty[(e + 1) % C::NST]);
                 if (i + 1 < n) {
                     if (!landed(e + 2)) ok = false;
                     if (!ok) break;
                     tc::fence_after_sync();
                     mma_over_d<C::DP>(tS, ka, entry(e + 2), idesc_s);
-                    tc::mma_commit(&s_full);
+                    tc::mma_commit_w(&s_full);
                 }
-                if (!tc::mbar_wait(&ds_full, i & 1, tc::kWaitLimit)) ok = false;
+                if (!tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) ok = false;
                 if (!ok) break;
                 tc::fence_after_sync();
                 mma_rows128(tK, tP, entry(e), idesc_g, i == 0);       // dK += dS^T Q
-                tc::mma_commit(&empty[e % C::NST]);
+                tc::mma_commit_w(&empty[e % C::NST]);
                 if (i + 1 < n) {
                     if (!landed(e + 3)) ok = false;
                     if (!ok) break;
                     tc::fence_after_sync();
                     mma_over_d<C::DP>(tP, va, entry(e + 3), idesc_s);
-                    tc::mma_commit(&dp_full);
+                    tc::mma_commit_w(&dp_full);
                 }
             }
-            if (!ok) atomicOr(a.d_err, tc::kErrMmaTimeout);
+            if (!ok && lane == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // every product issued is complete before TMEM is released
-            tc::mma_commit(&acc_full);
-            tc::mbar_wait(&acc_full, 0, tc::kWaitLimit);
+            tc::mma_commit_w(&acc_full);
+            tc::warp_wait(&acc_full, 0, tc::kWaitLimit);
         }
         __syncwarp();
     } else {   // ---------------------------------------------------- weights and epilogue
@@ -426,7 +426,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t q_full, full[C::NST], empty[C::NST], s_full[2], dp_full, ds_full, acc_full;
     __shared__ uint32_t tmem_base;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem);
     const SeqTile t = a.qtiles[blockIdx.x / a.H];
     const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
@@ -473,43 +473,43 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
             tc::mbar_wait(&q_full, 0, tc::kWaitLimit);
             for (int i = e - 1; i >= 0 && i >= e - C::NST; --i)
                 tc::mbar_wait(&full[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
-        } else if (warp == 1 && lane == 0) {   // ---------------------------- MMA issuer
+        } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128), idesc_g = tc::idesc_bf16(128, C::DP) | tc::kMajorMnB;
             const uint32_t qa = sbase + C::R0, ga = qa + C::TB;
             auto entry = [&](int e) { return sbase + C::ST0 + (e % C::NST) * C::TB; };
-            auto landed = [&](int e) { return tc::mbar_wait(&full[e % C::NST], (e / C::NST) & 1, tc::kWaitLimit); };
+            auto landed = [&](int e) { return tc::warp_wait(&full[e % C::NST], (e / C::NST) & 1, tc::kWaitLimit); };
             auto scores = [&](int i) -> bool {
                 if (!landed(2 * i)) return false;
                 tc::fence_after_sync();
                 mma_over_d<C::DP>(tS + (i & 1) * 128, qa, entry(2 * i), idesc_s);
-                tc::mma_commit(&s_full[i & 1]);
+                tc::mma_commit_w(&s_full[i & 1]);
                 return true;
             };
             auto dprod = [&](int i) -> bool {
                 if (!landed(2 * i + 1)) return false;
                 tc::fence_after_sync();
                 mma_over_d<C::DP>(tP, ga, entry(2 * i + 1), idesc_s);
-                tc::mma_commit(&dp_full);
-                tc::mma_commit(&empty[(2 * i + 1) % C::NST]);
+                tc::mma_commit_w(&dp_full);
+                tc::mma_commit_w(&empty[(2 * i + 1) % C::NST]);
                 return true;
             };
-            bool ok = tc::mbar_wait(&q_full, 0, tc::kWaitLimit) && scores(0) && dprod(0);
+            bool ok = tc::warp_wait(&q_full, 0, tc::kWaitLimit) && scores(0) && dprod(0);
             for (int i = 0; i < n && ok; ++i) {
                 // S(i + 1) overwrites S(i - 1), read before dS(i - 1) arrived
                 if (i + 1 < n && !scores(i + 1)) ok = false;
-                if (!ok || !tc::mbar_wait(&ds_full, i & 1, tc::kWaitLimit)) {
+                if (!ok || !tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
                 mma_rows128(tQ, tP, entry(2 * i), idesc_g, i == 0);   // dQ += dS K
-                tc::mma_commit(&empty[(2 * i) % C::NST]);
+                tc::mma_commit_w(&empty[(2 * i) % C::NST]);
                 if (i + 1 < n && !dprod(i + 1)) ok = false;
             }
-            if (!ok) atomicOr(a.d_err, tc::kErrMmaTimeout);
+            if (!ok && lane == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // every product issued is complete before TMEM is released
-            tc::mma_commit(&acc_full);
-            tc::mbar_wait(&acc_full, 0, tc::kWaitLimit);
+            tc::mma_commit_w(&acc_full);
+            tc::warp_wait(&acc_full, 0, tc::kWaitLimit);
         }
         __syncwarp();
     } else {   // ---------------------------------------------------- weights and epilogue

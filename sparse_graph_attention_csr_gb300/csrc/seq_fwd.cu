@@ -5,7 +5,7 @@
 // tiles they see.
 //   warp 0, one lane: TMA loads -- the query tiles, then K and V tiles of 128
 //     keys in turn into a ring;
-//   warp 1, one lane: the products, in the order P V (previous key tile), S =
+//   warp 1: the products, in the order P V (previous key tile), S =
 //     Q K^T of one query tile, then of the other: while the softmax warps of
 //     one tile work, the tensor core has the other tile's products;
 //   (warps 2, 3 idle: registers are split by groups of four warps)
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t q_full, kv_full[C::NST], kv_empty[C::NST], s_full[NS], p_full[NS], o_full[NS], mma_done;
     __shared__ uint32_t tmem_base;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem);
 
     // the unit: per stage a row tile (with its key tiles) and a head
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             tc::mbar_wait(&q_full, 0, tc::kWaitLimit);
             for (int i = e - 1; i >= 0 && i >= e - C::NST; --i)
                 tc::mbar_wait(&kv_full[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
-        } else if (warp == 1 && lane == 0) {   // ---------------------------- MMA issuer
+        } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128), idesc_o = tc::idesc_bf16(128, C::DP) | tc::kMajorMnB;
             int pend[NS], np[NS];   // key tile whose P V is due, and P V's issued, per stage
 #pragma unroll
@@ -169,24 +169,24 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             }
             auto issue_pv = [&](int s) -> bool {   // O(s) += P(s) V(pend[s])
                 const int e = 2 * pend[s] + 1, b = e % C::NST;
-                if (!tc::mbar_wait(&p_full[s], np[s] & 1, tc::kWaitLimit) ||
-                    !tc::mbar_wait(&kv_full[b], (e / C::NST) & 1, tc::kWaitLimit))
+                if (!tc::warp_wait(&p_full[s], np[s] & 1, tc::kWaitLimit) ||
+                    !tc::warp_wait(&kv_full[b], (e / C::NST) & 1, tc::kWaitLimit))
                     return false;
                 tc::fence_after_sync();
                 const uint32_t va = sbase + C::ST0 + b * C::TB;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_bf16_ts(tO + s * C::DP, tS + s * 128 + kk * 8, tc::desc_sw128_mn(va + kk * 2048, 16384),
+                    tc::mma_bf16_ts_w(tO + s * C::DP, tS + s * 128 + kk * 8, tc::desc_sw128_mn(va + kk * 2048, 16384),
                                     idesc_o, (np[s] > 0 || kk > 0) ? 1u : 0u);
                 ++np[s];
-                if (t0 + pend[s] == st[s].t1 - 1) tc::mma_commit(&o_full[s]);
+                if (t0 + pend[s] == st[s].t1 - 1) tc::mma_commit_w(&o_full[s]);
                 pend[s] = -1;
                 return true;
             };
-            bool ok = tc::mbar_wait(&q_full, 0, tc::kWaitLimit);
+            bool ok = tc::warp_wait(&q_full, 0, tc::kWaitLimit);
             for (int i = 0; i < n && ok; ++i) {
                 const int e = 2 * i, b = e % C::NST;
-                if (!tc::mbar_wait(&kv_full[b], (e / C::NST) & 1, tc::kWaitLimit)) {
+                if (!tc::warp_wait(&kv_full[b], (e / C::NST) & 1, tc::kWaitLimit)) {
                     ok = false;
                     break;
                 }
@@ -204,22 +204,22 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
 #pragma unroll
                     for (int kk = 0; kk < C::DP / 16; ++kk) {
                         const uint32_t o = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
-                        tc::mma_bf16_ss(tS + s * 128, tc::desc_sw128(qa + o), tc::desc_sw128(ka + o), idesc_s, kk > 0);
+                        tc::mma_bf16_ss_w(tS + s * 128, tc::desc_sw128(qa + o), tc::desc_sw128(ka + o), idesc_s, kk > 0);
                     }
-                    tc::mma_commit(&s_full[s]);
+                    tc::mma_commit_w(&s_full[s]);
                     pend[s] = i;
                 }
                 if (!ok) break;
-                tc::mma_commit(&kv_empty[b]);
-                if (i >= 1) tc::mma_commit(&kv_empty[(e - 1) % C::NST]);
+                tc::mma_commit_w(&kv_empty[b]);
+                if (i >= 1) tc::mma_commit_w(&kv_empty[(e - 1) % C::NST]);
             }
 #pragma unroll
             for (int s = 0; s < NS; ++s)
                 if (ok && pend[s] >= 0 && !issue_pv(s)) ok = false;
-            if (!ok) atomicOr(a.d_err, tc::kErrMmaTimeout);
+            if (!ok && lane == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // every product issued is complete before TMEM is released
-            tc::mma_commit(&mma_done);
-            tc::mbar_wait(&mma_done, 0, tc::kWaitLimit);
+            tc::mma_commit_w(&mma_done);
+            tc::warp_wait(&mma_done, 0, tc::kWaitLimit);
         }
         __syncwarp();
     } else {   // ---------------------------------------------------- softmax + epilogue
