@@ -48,7 +48,7 @@ struct SeqArgs {
     void *out_w;              // forward outputs
     float *lse_w;
     void *dQ, *dK, *dV;       // backward outputs
-    float *ws_lse, *ws_delta; // [H][rows_pad] lse * log2(e) (+inf behind the last row) and Delta
+    float *ws_nlse, *ws_ndelta; // [H][rows_pad] -lse * log2(e) (-inf behind the last row) and -Delta
     const int2 *range;
     const SeqTile *qtiles, *ktiles, *qpairs;
     int64_t rows, rows_pad;
@@ -60,7 +60,7 @@ struct SeqArgs {
 // rows of a head's slice of the backward's row terms: whole tiles, 512-byte aligned
 inline int64_t seq_rows_pad(int64_t rows) { return (rows + 127) / 128 * 128; }
 
-// lse * log2(e) and Delta of every row, head-major (seq_simt.cu)
+// -lse * log2(e) and -Delta of every row, head-major (seq_simt.cu)
 template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s);
 template <typename T> cudaError_t seq_fwd_simt(const SeqArgs &a, int D, cudaStream_t s);
 template <typename T> cudaError_t seq_bwd_simt(const SeqArgs &a, int D, cudaStream_t s);

@@ -13,9 +13,12 @@
 //     dK += dS^T Q.  The products are issued dV(i), S(i + 1), dK(i), dP(i + 1):
 //     while the weights of i + 1 are formed the tensor core has dK(i) and
 //     dP(i + 1), while its dS is formed it has dV(i + 1) and S(i + 2).
-//   dQ pass (unit: 128 queries x head, over the key tiles they see): S, two
-//     buffers, dP with queries in the lanes, dS in bf16 over dP, dQ += dS K,
-//     issued S(i + 1), dQ(i), dP(i + 1).
+//   dQ pass (unit: 128 queries x head, over the key tiles they see): S and dP
+//     with queries in the lanes, Q and dOut as A operands in TMEM (as shared
+//     memory operands they would take half of its bandwidth, and with the loads
+//     more than there is), dS in bf16 over dP, dQ += dS K; issued S(i + 1),
+//     dQ(i), dP(i + 1): the weights of i + 1 are formed while dQ(i) and
+//     dP(i + 1) are computed.
 // Roles as in the forward: one lane loads by TMA, one issues the products,
 // eight warps (two per TMEM lane quarter, each with half of a tile's columns)
 // turn scores into weights.  P and dS are rounded to bf16 once (half a step,
@@ -31,10 +34,14 @@
 namespace sga {
 namespace {
 
-constexpr int kThreads = 384;   // control warps (load, MMA, two idle), eight weight warps
-constexpr int kSoft = 8;        // arrivals per handoff
-constexpr int kRCtrl = 56, kRSoft = 224;   // registers a thread after the split; 168 at launch
-static_assert(kRCtrl + 2 * kRSoft == 3 * 168, "register split");
+// Control warps (load, MMA, two idle) and two weight warps a TMEM lane quarter,
+// each with 64 of a tile's columns (four with 32 each measured the same at D =
+// 128 and 2% slower at D = 64).  Registers a thread at launch and after the split.
+constexpr int kParts = 2, kCols = 128 / kParts;
+constexpr int kSoft = 4 * kParts;   // arrivals per handoff
+constexpr int kThreads = 128 + 128 * kParts;
+constexpr int kRLaunch = 168, kRCtrl = 56, kRSoft = 224;
+static_assert(kRCtrl + kParts * kRSoft <= (kParts + 1) * kRLaunch, "register split");
 
 template <int D> struct BwdCfg {
     static constexpr int DP = D < 64 ? 64 : D, DA = DP / 64;
@@ -42,32 +49,62 @@ template <int D> struct BwdCfg {
     static constexpr uint32_t R0 = 0;                 // two resident tiles
     static constexpr uint32_t ST0 = 2 * TB;           // ring of streamed tiles
 };
+// The streamed tiles have a ring each: of the two that a step takes, one is
+// held longer than the other (Q until dK, K until dQ), and a common ring would
+// make the next loads wait for it.
 template <int D> struct KvCfg : BwdCfg<D> {
     using B = BwdCfg<D>;
-    static constexpr int NST = B::DP == 64 ? 8 : 4;
-    static constexpr uint32_t ROW0 = B::ST0 + NST * B::TB;        // lse, Delta of the queries of ring entry 2j
-    static constexpr uint32_t BYTES = ROW0 + NST / 2 * 1024;
+    static constexpr int NQ = B::DP == 64 ? 4 : 3, NG = B::DP == 64 ? 4 : 2;   // Q, dOut tiles in flight
+    static constexpr uint32_t G0 = B::ST0 + NQ * B::TB;
+    static constexpr uint32_t ROW0 = G0 + NG * B::TB;                         // -lse, -Delta of a step's queries: two slots
+    static constexpr uint32_t BAR0 = ROW0 + 2 * 1024, BYTES = BAR0 + 256;     // barriers
     static constexpr uint32_t TS = 0, TP = 128, TK = 256, TV = 256 + B::DP;   // S^T, dP^T, dK, dV
 };
 template <int D> struct QCfg : BwdCfg<D> {
     using B = BwdCfg<D>;
-    static constexpr int NST = B::DP == 64 ? 8 : 5;
-    static constexpr uint32_t BYTES = B::ST0 + NST * B::TB;
-    static constexpr uint32_t TS = 0, TP = 256, TQ = 384;         // two S buffers, dP, dQ
+    static constexpr int NK = 4, NV = 3;                          // K, V tiles in flight
+    static constexpr uint32_t ST0 = 0, V0 = ST0 + NK * B::TB, BYTES = V0 + NV * B::TB;
+    static constexpr uint32_t TS = 0, TP = 128, TQ = 256, TA = 384, TG = 448;   // S, dP, dQ; Q and dOut as A operands
 };
-static_assert(KvCfg<128>::BYTES + 1024 <= 226 * 1024 && QCfg<128>::BYTES + 1024 <= 226 * 1024, "shared memory");
+constexpr uint32_t kMaxSmem = 227 * 1024;
+static_assert(KvCfg<128>::BYTES <= kMaxSmem && QCfg<128>::BYTES + 1024 <= 226 * 1024, "shared memory");
+
+// A ring of N tiles in shared memory from `base`.
+template <int N, uint32_t TB> struct Ring {
+    uint64_t *full, *empty;
+    uint32_t base;
+    __device__ __forceinline__ uint32_t at(int i) const { return base + (i % N) * TB; }
+    __device__ __forceinline__ uint64_t *filled(int i) const { return &full[i % N]; }
+    __device__ __forceinline__ uint64_t *freed(int i) const { return &empty[i % N]; }
+    __device__ __forceinline__ bool wait_filled(int i) const { return tc::warp_wait(&full[i % N], (i / N) & 1, tc::kWaitLimit); }
+    // (one lane) room for tile i
+    __device__ __forceinline__ bool wait_room(int i) const {
+        return i < N || tc::mbar_wait(&empty[i % N], (i / N - 1) & 1, tc::kWaitLimit);
+    }
+    // (one lane) the last loads, of `n` issued, have landed
+    __device__ __forceinline__ void drain(int n) const {
+        for (int i = n - 1; i >= 0 && i >= n - N; --i) tc::mbar_wait(&full[i % N], (i / N) & 1, tc::kWaitLimit);
+    }
+    __device__ __forceinline__ void init() const {
+        for (int i = 0; i < N; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+    }
+};
 
 struct BwdParams {
     CUtensorMap tq, tk, tv, tg;
     SeqArgs a;
 };
 
-// A 128-deep product with the A operand in TMEM (its halves 64 columns apart,
-// 32 columns of bf16 pairs each) and 128 rows of B as an MN-major operand.
+// A 128-deep product with the A operand in TMEM, written over scores by the
+// weight warps (their parts kCols columns apart, half as many columns of bf16
+// pairs each), and 128 rows of B as an MN-major operand.
 __device__ __forceinline__ void mma_rows128(uint32_t d, uint32_t ta, uint32_t b, uint32_t idesc, bool first) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        tc::mma_bf16_ts_w(d, ta + (kk >> 2) * 64 + (kk & 3) * 8, tc::desc_sw128_mn(b + kk * 2048, 16384), idesc,
+        tc::mma_bf16_ts_w(d, ta + kk * kParts / 8 * kCols + kk % (8 / kParts) * 8, tc::desc_sw128_mn(b + kk * 2048, 16384), idesc,
                         (!first || kk > 0) ? 1u : 0u);
 }
 // 128 x 128 over the head width, both operands K-major tiles of 128 rows.
@@ -77,6 +114,32 @@ template <int DP> __device__ __forceinline__ void mma_over_d(uint32_t d, uint32_
         const uint32_t o = (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32);
         tc::mma_bf16_ss_w(d, tc::desc_sw128(a + o), tc::desc_sw128(b + o), idesc, kk > 0);
     }
+}
+
+// The same with the A operand a head's row in TMEM (bf16 pairs in order).
+template <int DP> __device__ __forceinline__ void mma_over_d_ts(uint32_t d, uint32_t ta, uint32_t b, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk)
+        tc::mma_bf16_ts_w(d, ta + kk * 8, tc::desc_sw128(b + (uint32_t)((kk >> 2) * 16384 + (kk & 3) * 32)), idesc, kk > 0);
+}
+
+// This part's columns of scores of this thread's TMEM lane.
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t *v) {
+    constexpr int N = kCols;
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tc::tmem_ld32_async(taddr + c, v + c);
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tc::tmem_wait_ld(v + c);
+}
+// The weights as bf16 pairs over the first half of their scores' columns.
+__device__ __forceinline__ void store_weights(uint32_t taddr, const float *p) {
+    constexpr int N = kCols;
+    static_assert(N == 64, "one store of 32 columns");
+    uint32_t pk[N / 2];
+#pragma unroll
+    for (int c = 0; c < N; c += 2) pk[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
+    tc::tmem_st32_async(taddr, pk);
+    tc::tmem_wait_st();
 }
 
 template <int D> struct RowFrag {
@@ -103,9 +166,11 @@ template <int D> struct RowFrag {
     }
 };
 
-// dK (DK) or dV of one key row by its warp, over the queries [lo, hi) alone.
-template <int D, bool DK>
-__device__ __forceinline__ void key_row_alone(const SeqArgs &a, int64_t row, int hk, int64_t lo, int64_t hi) {
+// Columns [c0, c0 + 32) of dK (DK) or dV of one key row by its warp, over the
+// queries [lo, hi) alone.
+template <int D>
+__device__ __forceinline__ void key_row_alone(const SeqArgs &a, bool DK, int64_t row, int hk, int64_t lo, int64_t hi,
+                                              int c0) {
     RowFrag<D> k, v, acc;
     const int64_t at = (row * a.Hkv + hk) * D;
     k.load(a.K, at);
@@ -119,18 +184,17 @@ __device__ __forceinline__ void key_row_alone(const SeqArgs &a, int64_t row, int
             q.load(a.Q, (r * a.H + h) * D);
             g.load(a.dOut, (r * a.H + h) * D);
             const int64_t t = (int64_t)h * a.rows_pad + r;
-            const float p = fast_exp2(fmaf(q.dot(k), a.scale * kLog2e, -a.ws_lse[t]));
-            const float w = DK ? p * (g.dot(v) - a.ws_delta[t]) : p;
+            const float p = fast_exp2(fmaf(q.dot(k), a.scale * kLog2e, a.ws_nlse[t]));
+            const float w = DK ? p * (g.dot(v) + a.ws_ndelta[t]) : p;
 #pragma unroll
             for (int i = 0; i < RowFrag<D>::W; ++i) acc.x[i] = fmaf(w, DK ? q.x[i] : g.x[i], acc.x[i]);
         }
-    acc.store(DK ? a.dK : a.dV, at, DK ? a.scale : 1.f, 0, D);
+    acc.store(DK ? a.dK : a.dV, at, DK ? a.scale : 1.f, c0, c0 + 32);
 }
 
-// Columns [c0, c1) of dQ of one query row by its warp, over the keys [lo, hi) alone.
+// Columns [c0, c0 + 32) of dQ of one query row by its warp, over the keys [lo, hi) alone.
 template <int D>
-__device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, int h, int64_t lo, int64_t hi, int c0,
-                                                int c1) {
+__device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, int h, int64_t lo, int64_t hi, int c0) {
     RowFrag<D> q, g, acc;
     const int64_t at = (row * a.H + h) * D, t = (int64_t)h * a.rows_pad + row;
     const int hk = h / (a.H / a.Hkv);
@@ -142,33 +206,30 @@ __device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, i
         RowFrag<D> k, v;
         k.load(a.K, (j * a.Hkv + hk) * D);
         v.load(a.V, (j * a.Hkv + hk) * D);
-        const float p = fast_exp2(fmaf(q.dot(k), a.scale * kLog2e, -a.ws_lse[t]));
-        const float w = p * (g.dot(v) - a.ws_delta[t]);
+        const float p = fast_exp2(fmaf(q.dot(k), a.scale * kLog2e, a.ws_nlse[t]));
+        const float w = p * (g.dot(v) + a.ws_ndelta[t]);
 #pragma unroll
         for (int i = 0; i < RowFrag<D>::W; ++i) acc.x[i] = fmaf(w, k.x[i], acc.x[i]);
     }
-    acc.store(a.dQ, at, a.scale, c0, c1);
+    acc.store(a.dQ, at, a.scale, c0, c0 + 32);
 }
 
-// N columns of a row from TMEM, scaled, to bf16 at dst (if `in`); whether any was not finite.
-template <int N>
-__device__ __forceinline__ bool store_from_tmem(uint32_t taddr, __nv_bfloat16 *dst, float f, bool in) {
+// 32 columns of a row from TMEM, scaled, to bf16 at dst (if `in`); the lanes
+// whose row was not finite.
+__device__ __forceinline__ uint32_t store_from_tmem(uint32_t taddr, __nv_bfloat16 *dst, float f, bool in) {
     bool bad = false;
+    uint32_t o[32];
+    tc::tmem_ld32(taddr, o);   // warp-collective: every lane takes part
+    float x[32];
 #pragma unroll
-    for (int cb = 0; cb < N; cb += 32) {
-        uint32_t o[32];
-        tc::tmem_ld32(taddr + cb, o);   // warp-collective: every lane takes part
-        float x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            x[i] = __uint_as_float(o[i]) * f;
-            bad |= !(fabsf(x[i]) < INFINITY);
-        }
-        if (in)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(dst + cb + 8 * q) = pack<__nv_bfloat16>(x + 8 * q);
+    for (int i = 0; i < 32; ++i) {
+        x[i] = __uint_as_float(o[i]) * f;
+        bad |= !(fabsf(x[i]) < INFINITY);
     }
-    return bad && in;
+    if (in)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(dst + 8 * q) = pack<__nv_bfloat16>(x + 8 * q);
+    return __ballot_sync(SGA_FULL_MASK, bad && in);
 }
 
 // ---- dK, dV -----------------------------------------------------------------------
@@ -176,13 +237,24 @@ __device__ __forceinline__ bool store_from_tmem(uint32_t taddr, __nv_bfloat16 *d
 template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_kernel(const __grid_constant__ BwdParams prm) {
     using C = KvCfg<D>;
     const SeqArgs &a = prm.a;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem =
-        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t kv_full, full[C::NST], empty[C::NST], s_full, dp_full, p_full, ds_full, acc_full;
-    __shared__ uint32_t tmem_base;
+    // The tiles take all but a few hundred bytes of the SM's shared memory, so
+    // the barriers lie behind them and the block's memory has to begin on the
+    // tiles' alignment, as it does for a kernel without static shared memory.
+    extern __shared__ __align__(1024) unsigned char smem[];
+    if (tc::smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
+        return;
+    }
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::BAR0);
+    uint64_t &kv_full = bar[0], &s_full = bar[1], &dp_full = bar[2], &p_full = bar[3], &ds_full = bar[4], &acc_full = bar[5];
+    uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(bar + 6);
+    uint64_t *ring_full = bar + 7, *ring_empty = ring_full + C::NQ + C::NG + 2;
+    static_assert((7 + 2 * (C::NQ + C::NG + 2)) * 8 <= 256, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem);
+    const Ring<C::NQ, C::TB> rq{ring_full, ring_empty, sbase + C::ST0};
+    const Ring<C::NG, C::TB> rg{ring_full + C::NQ, ring_empty + C::NQ, sbase + C::G0};
+    const Ring<2, 1024> rr{ring_full + C::NQ + C::NG, ring_empty + C::NQ + C::NG, sbase + C::ROW0};
     const SeqTile t = a.ktiles[blockIdx.x / a.Hkv];
     const int hk = blockIdx.x % a.Hkv, grp = a.H / a.Hkv;
     const int nt = t.t1 - t.t0, n = nt * grp;   // steps: (head of the group, query tile)
@@ -190,10 +262,9 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
     if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
     if (tid == 32) {
         tc::mbar_init(&kv_full, 1);
-        for (int i = 0; i < C::NST; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
-        }
+        rq.init();
+        rg.init();
+        rr.init();
         tc::mbar_init(&s_full, 1);
         tc::mbar_init(&dp_full, 1);
         tc::mbar_init(&p_full, kSoft);
@@ -212,75 +283,65 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
             tc::mbar_expect_tx(&kv_full, 2 * C::TB);
             seq::load_tile<C::DA>(sbase + C::R0, &prm.tk, hk, t.tile * 128, &kv_full);
             seq::load_tile<C::DA>(sbase + C::R0 + C::TB, &prm.tv, hk, t.tile * 128, &kv_full);
-            int e = 0;   // entry 2 i: Q, lse and Delta of step i; 2 i + 1: dOut
-            for (; e < 2 * n; ++e) {
-                const int b = e % C::NST, r = e / C::NST;
-                if (r >= 1 && !tc::mbar_wait(&empty[b], (r - 1) & 1, tc::kWaitLimit)) {
-                    ok = false;
-                    break;
-                }
-                const int h = hk * grp + (e >> 1) / nt, qt = t.t0 + (e >> 1) % nt;
-                const uint32_t dst = sbase + C::ST0 + b * C::TB;
-                if (e & 1) {
-                    tc::mbar_expect_tx(&full[b], C::TB);
-                    seq::load_tile<C::DA>(dst, &prm.tg, h, qt * 128, &full[b]);
-                } else {
-                    tc::mbar_expect_tx(&full[b], C::TB + 1024);
-                    seq::load_tile<C::DA>(dst, &prm.tq, h, qt * 128, &full[b]);
-                    const int64_t r0 = (int64_t)h * a.rows_pad + (int64_t)qt * 128;
-                    const uint32_t rows = sbase + C::ROW0 + (b >> 1) * 1024;
-                    tc::bulk_load(rows, a.ws_lse + r0, 512, &full[b]);
-                    tc::bulk_load(rows + 512, a.ws_delta + r0, 512, &full[b]);
-                }
+            int nq = 0, ng = 0, nr = 0;   // loads issued
+            for (int i = 0; i < n; ++i) {
+                const int hd = hk * grp + i / nt, row = (t.t0 + i % nt) * 128;
+                if (!(ok = rq.wait_room(i))) break;
+                tc::mbar_expect_tx(rq.filled(i), C::TB);
+                seq::load_tile<C::DA>(rq.at(i), &prm.tq, hd, row, rq.filled(i));
+                ++nq;
+                if (!(ok = rg.wait_room(i))) break;
+                tc::mbar_expect_tx(rg.filled(i), C::TB);
+                seq::load_tile<C::DA>(rg.at(i), &prm.tg, hd, row, rg.filled(i));
+                ++ng;
+                if (!(ok = rr.wait_room(i))) break;
+                tc::mbar_expect_tx(rr.filled(i), 1024);
+                tc::bulk_load(rr.at(i), a.ws_nlse + (int64_t)hd * a.rows_pad + row, 512, rr.filled(i));
+                tc::bulk_load(rr.at(i) + 512, a.ws_ndelta + (int64_t)hd * a.rows_pad + row, 512, rr.filled(i));
+                ++nr;
             }
             if (!ok) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // loads that no product consumed (only after a timeout) land before the CTA ends
             tc::mbar_wait(&kv_full, 0, tc::kWaitLimit);
-            for (int i = e - 1; i >= 0 && i >= e - C::NST; --i)
-                tc::mbar_wait(&full[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
+            rq.drain(nq);
+            rg.drain(ng);
+            rr.drain(nr);
         } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128), idesc_g = tc::idesc_bf16(128, C::DP) | tc::kMajorMnB;
             const uint32_t ka = sbase + C::R0, va = ka + C::TB;
-            auto entry = [&](int e) { return sbase + C::ST0 + (e % C::NST) * C::TB; };
-            auto landed = [&](int e) { return tc::warp_wait(&full[e % C::NST], (e / C::NST) & 1, tc::kWaitLimit); };
-            bool ok = tc::warp_wait(&kv_full, 0, tc::kWaitLimit) && landed(0);
-            if (ok) {
+            auto scores = [&](int i) -> bool {   // S^T = K Q^T
+                if (!rq.wait_filled(i)) return false;
                 tc::fence_after_sync();
-                mma_over_d<C::DP>(tS, ka, entry(0), idesc_s);
+                mma_over_d<C::DP>(tS, ka, rq.at(i), idesc_s);
                 tc::mma_commit_w(&s_full);
-                ok = landed(1);
-            }
-            if (ok) {
+                return true;
+            };
+            auto dprod = [&](int i) -> bool {    // dP^T = V dOut^T
+                if (!rg.wait_filled(i)) return false;
                 tc::fence_after_sync();
-                mma_over_d<C::DP>(tP, va, entry(1), idesc_s);
+                mma_over_d<C::DP>(tP, va, rg.at(i), idesc_s);
                 tc::mma_commit_w(&dp_full);
-            }
+                return true;
+            };
+            bool ok = tc::warp_wait(&kv_full, 0, tc::kWaitLimit) && scores(0) && dprod(0);
             for (int i = 0; i < n && ok; ++i) {
-                const int e = 2 * i;
-                if (!tc::warp_wait(&p_full, i & 1, tc::kWaitLimit)) ok = false;
-                if (!ok) break;
-                tc::fence_after_sync();
-                mma_rows128(tV, tS, entry(e + 1), idesc_g, i == 0);   // dV += P^T dOut
-                tc::mma_commit_w(&empty[(e + 1) % C::NST]);
-                if (i + 1 < n) {
-                    if (!landed(e + 2)) ok = false;
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    mma_over_d<C::DP>(tS, ka, entry(e + 2), idesc_s);
-                    tc::mma_commit_w(&s_full);
+                if (!tc::warp_wait(&p_full, i & 1, tc::kWaitLimit)) {
+                    ok = false;
+                    break;
                 }
-                if (!tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) ok = false;
-                if (!ok) break;
                 tc::fence_after_sync();
-                mma_rows128(tK, tP, entry(e), idesc_g, i == 0);       // dK += dS^T Q
-                tc::mma_commit_w(&empty[e % C::NST]);
-                if (i + 1 < n) {
-                    if (!landed(e + 3)) ok = false;
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    mma_over_d<C::DP>(tP, va, entry(e + 3), idesc_s);
-                    tc::mma_commit_w(&dp_full);
+                mma_rows128(tV, tS, rg.at(i), idesc_g, i == 0);   // dV += P^T dOut
+                tc::mma_commit_w(rg.freed(i));
+                if (i + 1 < n && !scores(i + 1)) ok = false;
+                if (!ok || !tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) {
+                    ok = false;
+                    break;
                 }
+                tc::fence_after_sync();
+                mma_rows128(tK, tP, rq.at(i), idesc_g, i == 0);   // dK += dS^T Q
+                tc::mma_commit_w(rq.freed(i));
+                tc::mma_commit_w(rr.freed(i));   // (read before dS arrived)
+                if (i + 1 < n && !dprod(i + 1)) ok = false;
             }
             if (!ok && lane == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // every product issued is complete before TMEM is released
@@ -290,7 +351,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
         __syncwarp();
     } else {   // ---------------------------------------------------- weights and epilogue
         tc::reg_inc<kRSoft>();
-        const int quarter = warp & 3, hf = (warp - 4) >> 2;   // half hf: queries 64 hf .. of a tile
+        const int quarter = warp & 3, part = (warp - 4) >> 2;   // part: queries N part .. of a tile
         const uint32_t tl = (uint32_t)(quarter * 32) << 16;
         const int64_t row = (int64_t)t.tile * 128 + quarter * 32 + lane;
         const bool in = row < a.rows;
@@ -302,88 +363,69 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
         }
         const float scale2 = a.scale * kLog2e;
         const float2 k2 = make_float2(scale2, scale2);
+        constexpr int N = kCols;
+        const uint32_t ts = tS + part * N + tl, tp = tP + part * N + tl;
         bool ok = true;
         for (int i = 0; i < n; ++i) {
-            const int qt = t.t0 + i % nt, b = (2 * i) % C::NST;
-            if (!tc::warp_wait(&full[b], ((2 * i) / C::NST) & 1, tc::kWaitLimit) ||
-                !tc::warp_wait(&s_full, i & 1, tc::kWaitLimit)) {
+            const int qt = t.t0 + i % nt;
+            if (!rr.wait_filled(i)) {
+                ok = false;
+                break;
+            }
+            // the columns' -lse, read while the scores are computed
+            float p[N], r[N];
+#pragma unroll
+            for (int c = 0; c < N; c += 4) tc::lds128(rr.at(i) + 4 * (part * N + c), r + c);
+            if (!tc::warp_wait(&s_full, i & 1, tc::kWaitLimit)) {
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
-            const float4 *ls = reinterpret_cast<const float4 *>(smem + C::ROW0 + (b >> 1) * 1024) + hf * 16;
-            const float4 *dl = ls + 32;
-            uint32_t v[64], pk[32];
-            tc::tmem_ld32_async(tS + hf * 64 + tl, v);
-            tc::tmem_ld32_async(tS + hf * 64 + 32 + tl, v + 32);
-            tc::tmem_wait_ld(v);
-            tc::tmem_wait_ld(v + 32);
-            float p[64];
+            uint32_t v[N];
+            load_scores(ts, v);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 l4 = ls[c >> 2];
+            for (int c = 0; c < N; c += 2) {
                 const float2 x = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2,
-                                       make_float2(-l4.x, -l4.y));
-                const float2 y = ffma2(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), k2,
-                                       make_float2(-l4.z, -l4.w));
+                                       make_float2(r[c], r[c + 1]));
                 p[c] = fast_exp2(x.x);
                 p[c + 1] = fast_exp2(x.y);
-                p[c + 2] = fast_exp2(y.x);
-                p[c + 3] = fast_exp2(y.y);
             }
-            uint32_t bits[2] = {0xffffffffu, 0xffffffffu};
-            const bool part = qt < t.f0 || qt >= t.f1;
-            if (part) {
+            const bool masked = qt < t.f0 || qt >= t.f1;
+            uint32_t bits[N / 32];
+            if (masked) {
                 const int cl = seq::rel(lo, (int64_t)qt * 128), ch = seq::rel(hi, (int64_t)qt * 128);
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    bits[w] = seq::column_bits(cl, ch, 2 * hf + w);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((bits[w] >> c) & 1u)) p[32 * w + c] = 0.f;
+                for (int c = 0; c < N; ++c) {
+                    if (c % 32 == 0) bits[c / 32] = seq::column_bits(cl, ch, (part * N + c) / 32);
+                    if (!((bits[c / 32] >> (c & 31)) & 1u)) p[c] = 0.f;
                 }
             }
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) pk[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
-            tc::tmem_st32_async(tS + hf * 64 + tl, pk);
-            tc::tmem_wait_st();
+            store_weights(ts, p);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&p_full);
 
+#pragma unroll
+            for (int c = 0; c < N; c += 4) tc::lds128(rr.at(i) + 512 + 4 * (part * N + c), r + c);   // the columns' -Delta
             if (!tc::warp_wait(&dp_full, i & 1, tc::kWaitLimit)) {
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
-            tc::tmem_ld32_async(tP + hf * 64 + tl, v);
-            tc::tmem_ld32_async(tP + hf * 64 + 32 + tl, v + 32);
-            tc::tmem_wait_ld(v);
-            tc::tmem_wait_ld(v + 32);
+            load_scores(tp, v);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 d4 = dl[c >> 2];
+            for (int c = 0; c < N; c += 2) {
                 const float2 x = fmul2(make_float2(p[c], p[c + 1]),
                                        fadd2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
-                                             make_float2(-d4.x, -d4.y)));
-                const float2 y = fmul2(make_float2(p[c + 2], p[c + 3]),
-                                       fadd2(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
-                                             make_float2(-d4.z, -d4.w)));
+                                             make_float2(r[c], r[c + 1])));
                 p[c] = x.x;
                 p[c + 1] = x.y;
-                p[c + 2] = y.x;
-                p[c + 3] = y.y;
             }
-            if (part)   // (zero weights times an infinity)
+            if (masked)   // (zero weights times an infinity)
 #pragma unroll
-                for (int w = 0; w < 2; ++w)
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((bits[w] >> c) & 1u)) p[32 * w + c] = 0.f;
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) pk[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
-            tc::tmem_st32_async(tP + hf * 64 + tl, pk);
-            tc::tmem_wait_st();
+                for (int c = 0; c < N; ++c)
+                    if (!((bits[c / 32] >> (c & 31)) & 1u)) p[c] = 0.f;
+            store_weights(tp, p);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ds_full);
@@ -391,17 +433,17 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
         if (ok && !tc::warp_wait(&acc_full, 0, tc::kWaitLimit)) ok = false;
         if (ok) {
             tc::fence_after_sync();
-            // half 0 stores dV, half 1 dK
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(hf ? a.dK : a.dV) + ((in ? row : 0) * a.Hkv + hk) * D;
-            const bool bad = store_from_tmem<D>((hf ? tK : tV) + tl, dst, hf ? a.scale : 1.f, in);
-            uint32_t again = __ballot_sync(SGA_FULL_MASK, bad);
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                const int64_t r = __shfl_sync(SGA_FULL_MASK, row, src), l = __shfl_sync(SGA_FULL_MASK, lo, src),
-                              u = __shfl_sync(SGA_FULL_MASK, hi, src);
-                if (hf) key_row_alone<D, true>(a, r, hk, l, u);
-                else key_row_alone<D, false>(a, r, hk, l, u);
+            for (int c = part; c < D / 16; c += kParts) {   // 32 columns each: dV's, then dK's
+                const bool dk = c >= D / 32;
+                const int c0 = (dk ? c - D / 32 : c) * 32;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(dk ? a.dK : a.dV) + ((in ? row : 0) * a.Hkv + hk) * D + c0;
+                uint32_t again = store_from_tmem((dk ? tK : tV) + c0 + tl, dst, dk ? a.scale : 1.f, in);
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    key_row_alone<D>(a, dk, __shfl_sync(SGA_FULL_MASK, row, src), hk, __shfl_sync(SGA_FULL_MASK, lo, src),
+                                     __shfl_sync(SGA_FULL_MASK, hi, src), c0);
+                }
             }
         } else if (lane == 0) {
             atomicOr(a.d_err, tc::kErrMmaTimeout);
@@ -424,23 +466,23 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t q_full, full[C::NST], empty[C::NST], s_full[2], dp_full, ds_full, acc_full;
+    __shared__ uint64_t q_full, s_free, ring_full[C::NK + C::NV], ring_empty[C::NK + C::NV], s_full, dp_full, ds_full, acc_full;
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem);
+    const Ring<C::NK, C::TB> rk{ring_full, ring_empty, sbase + C::ST0};
+    const Ring<C::NV, C::TB> rv{ring_full + C::NK, ring_empty + C::NK, sbase + C::V0};
     const SeqTile t = a.qtiles[blockIdx.x / a.H];
     const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
     const int n = t.t1 - t.t0;
 
     if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
     if (tid == 32) {
-        tc::mbar_init(&q_full, 1);
-        for (int i = 0; i < C::NST; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
-        }
-        tc::mbar_init(&s_full[0], 1);
-        tc::mbar_init(&s_full[1], 1);
+        tc::mbar_init(&q_full, kSoft);
+        tc::mbar_init(&s_free, kSoft);
+        rk.init();
+        rv.init();
+        tc::mbar_init(&s_full, 1);
         tc::mbar_init(&dp_full, 1);
         tc::mbar_init(&ds_full, kSoft);
         tc::mbar_init(&acc_full, 1);
@@ -448,62 +490,61 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tS = tmem_base + C::TS, tP = tmem_base + C::TP, tQ = tmem_base + C::TQ;
+    const uint32_t tS = tmem_base + C::TS, tP = tmem_base + C::TP, tQ = tmem_base + C::TQ, tA = tmem_base + C::TA,
+                   tG = tmem_base + C::TG;
 
     if (warp < 4) {
         tc::reg_dec<kRCtrl>();
         if (warp == 0 && lane == 0) {   // ----------------------------------- TMA producer
             bool ok = true;
-            tc::mbar_expect_tx(&q_full, 2 * C::TB);
-            seq::load_tile<C::DA>(sbase + C::R0, &prm.tq, h, t.tile * 128, &q_full);
-            seq::load_tile<C::DA>(sbase + C::R0 + C::TB, &prm.tg, h, t.tile * 128, &q_full);
-            int e = 0;   // entry 2 i: K, 2 i + 1: V of key tile i
-            for (; e < 2 * n; ++e) {
-                const int b = e % C::NST, r = e / C::NST;
-                if (r >= 1 && !tc::mbar_wait(&empty[b], (r - 1) & 1, tc::kWaitLimit)) {
+            int i = 0, v = 0;   // tiles of K and V issued
+            for (; i < n; ++i) {
+                if (!rk.wait_room(i)) {
                     ok = false;
                     break;
                 }
-                tc::mbar_expect_tx(&full[b], C::TB);
-                seq::load_tile<C::DA>(sbase + C::ST0 + b * C::TB, (e & 1) ? &prm.tv : &prm.tk, hk, (t.t0 + (e >> 1)) * 128,
-                                      &full[b]);
+                tc::mbar_expect_tx(rk.filled(i), C::TB);
+                seq::load_tile<C::DA>(rk.at(i), &prm.tk, hk, (t.t0 + i) * 128, rk.filled(i));
+                if (!rv.wait_room(i)) {
+                    ok = false;
+                    ++i;
+                    break;
+                }
+                tc::mbar_expect_tx(rv.filled(i), C::TB);
+                seq::load_tile<C::DA>(rv.at(i), &prm.tv, hk, (t.t0 + i) * 128, rv.filled(i));
+                ++v;
             }
             if (!ok) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // loads that no product consumed (only after a timeout) land before the CTA ends
-            tc::mbar_wait(&q_full, 0, tc::kWaitLimit);
-            for (int i = e - 1; i >= 0 && i >= e - C::NST; --i)
-                tc::mbar_wait(&full[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
+            rk.drain(i);
+            rv.drain(v);
         } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128), idesc_g = tc::idesc_bf16(128, C::DP) | tc::kMajorMnB;
-            const uint32_t qa = sbase + C::R0, ga = qa + C::TB;
-            auto entry = [&](int e) { return sbase + C::ST0 + (e % C::NST) * C::TB; };
-            auto landed = [&](int e) { return tc::warp_wait(&full[e % C::NST], (e / C::NST) & 1, tc::kWaitLimit); };
             auto scores = [&](int i) -> bool {
-                if (!landed(2 * i)) return false;
+                if (!rk.wait_filled(i)) return false;
                 tc::fence_after_sync();
-                mma_over_d<C::DP>(tS + (i & 1) * 128, qa, entry(2 * i), idesc_s);
-                tc::mma_commit_w(&s_full[i & 1]);
+                mma_over_d_ts<C::DP>(tS, tA, rk.at(i), idesc_s);
+                tc::mma_commit_w(&s_full);
                 return true;
             };
             auto dprod = [&](int i) -> bool {
-                if (!landed(2 * i + 1)) return false;
+                if (!rv.wait_filled(i)) return false;
                 tc::fence_after_sync();
-                mma_over_d<C::DP>(tP, ga, entry(2 * i + 1), idesc_s);
+                mma_over_d_ts<C::DP>(tP, tG, rv.at(i), idesc_s);
                 tc::mma_commit_w(&dp_full);
-                tc::mma_commit_w(&empty[(2 * i + 1) % C::NST]);
+                tc::mma_commit_w(rv.freed(i));
                 return true;
             };
             bool ok = tc::warp_wait(&q_full, 0, tc::kWaitLimit) && scores(0) && dprod(0);
             for (int i = 0; i < n && ok; ++i) {
-                // S(i + 1) overwrites S(i - 1), read before dS(i - 1) arrived
-                if (i + 1 < n && !scores(i + 1)) ok = false;
+                if (i + 1 < n && (!tc::warp_wait(&s_free, i & 1, tc::kWaitLimit) || !scores(i + 1))) ok = false;
                 if (!ok || !tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
-                mma_rows128(tQ, tP, entry(2 * i), idesc_g, i == 0);   // dQ += dS K
-                tc::mma_commit_w(&empty[(2 * i) % C::NST]);
+                mma_rows128(tQ, tP, rk.at(i), idesc_g, i == 0);   // dQ += dS K
+                tc::mma_commit_w(rk.freed(i));
                 if (i + 1 < n && !dprod(i + 1)) ok = false;
             }
             if (!ok && lane == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
@@ -514,7 +555,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
         __syncwarp();
     } else {   // ---------------------------------------------------- weights and epilogue
         tc::reg_inc<kRSoft>();
-        const int quarter = warp & 3, hf = (warp - 4) >> 2;   // half hf: keys 64 hf .. of a tile
+        const int quarter = warp & 3, part = (warp - 4) >> 2;   // part: keys N part .. of a tile
         const uint32_t tl = (uint32_t)(quarter * 32) << 16;
         const int64_t row = (int64_t)t.tile * 128 + quarter * 32 + lane;
         const bool in = row < a.rows;
@@ -525,24 +566,52 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
             hi = a.causal ? row + 1 : se.y;
         }
         const float scale2 = a.scale * kLog2e;
-        const float lse = a.ws_lse[(int64_t)h * a.rows_pad + row], delta = a.ws_delta[(int64_t)h * a.rows_pad + row];
-        const float2 k2 = make_float2(scale2, scale2), l2 = make_float2(-lse, -lse), d2 = make_float2(-delta, -delta);
+        const float nlse = a.ws_nlse[(int64_t)h * a.rows_pad + row], nd = a.ws_ndelta[(int64_t)h * a.rows_pad + row];
+        const float2 k2 = make_float2(scale2, scale2), l2 = make_float2(nlse, nlse), d2 = make_float2(nd, nd);
+        constexpr int N = kCols;
+        // the row's share of Q and dOut into TMEM (rows past the last, and the
+        // columns past a head of 32, as zeros)
+        {
+            constexpr int CW = C::DP / 2 / kParts;   // columns (bf16 pairs) of a part
+            for (int x = 0; x < 2; ++x) {
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(x ? a.dOut : a.Q) + ((in ? row : 0) * a.H + h) * D;
+#pragma unroll
+                for (int c = 0; c < CW; c += 8) {
+                    const int e = 2 * (part * CW + c);    // first element
+                    uint32_t u[8];
+#pragma unroll
+                    for (int k = 0; k < 8; k += 4) {
+                        const uint4 q = in && e + 2 * k < D ? ldg16(src + e + 2 * k) : make_uint4(0, 0, 0, 0);
+                        u[k] = q.x;
+                        u[k + 1] = q.y;
+                        u[k + 2] = q.z;
+                        u[k + 3] = q.w;
+                    }
+                    tc::tmem_st8_async((x ? tG : tA) + part * CW + c + tl, u);
+                }
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&q_full);
+        }
+        const uint32_t ts = tS + part * N + tl, tp = tP + part * N + tl;
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int kt = t.t0 + i;
-            if (!tc::warp_wait(&s_full[i & 1], (i >> 1) & 1, tc::kWaitLimit)) {
+            if (!tc::warp_wait(&s_full, i & 1, tc::kWaitLimit)) {
                 ok = false;
                 break;
             }
             tc::fence_after_sync();
-            uint32_t v[64], pk[32];
-            tc::tmem_ld32_async(tS + (i & 1) * 128 + hf * 64 + tl, v);
-            tc::tmem_ld32_async(tS + (i & 1) * 128 + hf * 64 + 32 + tl, v + 32);
-            tc::tmem_wait_ld(v);
-            tc::tmem_wait_ld(v + 32);
-            float p[64];
+            uint32_t v[N];
+            load_scores(ts, v);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&s_free);
+            float p[N];
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
+            for (int c = 0; c < N; c += 2) {
                 const float2 x = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2, l2);
                 p[c] = fast_exp2(x.x);
                 p[c + 1] = fast_exp2(x.y);
@@ -552,12 +621,9 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
                 break;
             }
             tc::fence_after_sync();
-            tc::tmem_ld32_async(tP + hf * 64 + tl, v);
-            tc::tmem_ld32_async(tP + hf * 64 + 32 + tl, v + 32);
-            tc::tmem_wait_ld(v);
-            tc::tmem_wait_ld(v + 32);
+            load_scores(tp, v);
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
+            for (int c = 0; c < N; c += 2) {
                 const float2 x = fmul2(make_float2(p[c], p[c + 1]),
                                        fadd2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), d2));
                 p[c] = x.x;
@@ -565,18 +631,14 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
             }
             if (kt < t.f0 || kt >= t.f1) {
                 const int cl = seq::rel(lo, (int64_t)kt * 128), ch = seq::rel(hi, (int64_t)kt * 128);
+                uint32_t bits = 0;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const uint32_t bits = seq::column_bits(cl, ch, 2 * hf + w);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((bits >> c) & 1u)) p[32 * w + c] = 0.f;
+                for (int c = 0; c < N; ++c) {
+                    if (c % 32 == 0) bits = seq::column_bits(cl, ch, (part * N + c) / 32);
+                    if (!((bits >> (c & 31)) & 1u)) p[c] = 0.f;
                 }
             }
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) pk[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
-            tc::tmem_st32_async(tP + hf * 64 + tl, pk);
-            tc::tmem_wait_st();
+            store_weights(tp, p);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ds_full);
@@ -584,16 +646,14 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
         if (ok && !tc::warp_wait(&acc_full, 0, tc::kWaitLimit)) ok = false;
         if (ok) {
             tc::fence_after_sync();
-            constexpr int HC = D < 64 ? 32 : D / 2;   // columns a half stores
-            if (hf * HC < D) {
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dQ) + ((in ? row : 0) * a.H + h) * D + hf * HC;
-                const bool bad = store_from_tmem<HC>(tQ + hf * HC + tl, dst, a.scale, in);
-                uint32_t again = __ballot_sync(SGA_FULL_MASK, bad);
+            for (int c0 = part * 32; c0 < D; c0 += 32 * kParts) {
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dQ) + ((in ? row : 0) * a.H + h) * D + c0;
+                uint32_t again = store_from_tmem(tQ + c0 + tl, dst, a.scale, in);
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;
                     query_row_alone<D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, __shfl_sync(SGA_FULL_MASK, lo, src),
-                                       __shfl_sync(SGA_FULL_MASK, hi, src), hf * HC, hf * HC + HC);
+                                       __shfl_sync(SGA_FULL_MASK, hi, src), c0);
                 }
             }
         } else if (lane == 0) {
@@ -616,12 +676,12 @@ template <int D> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tg, a.dOut, a.rows, a.H, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tk, a.K, a.rows, a.Hkv, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tv, a.V, a.rows, a.Hkv, D);
-    if (e == cudaSuccess) e = allow_smem<seq_bwd_dkdv_kernel<D>>(KvCfg<D>::BYTES + 1024);
+    if (e == cudaSuccess) e = allow_smem<seq_bwd_dkdv_kernel<D>>(KvCfg<D>::BYTES);
     if (e == cudaSuccess) e = allow_smem<seq_bwd_dq_kernel<D>>(QCfg<D>::BYTES + 1024);
     if (e == cudaSuccess) e = seq_row_terms<__nv_bfloat16>(a, D, s);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD_DKDV, s, false);
-    seq_bwd_dkdv_kernel<D><<<(unsigned)((int64_t)a.n_tiles * a.Hkv), kThreads, KvCfg<D>::BYTES + 1024, s>>>(prm);
+    seq_bwd_dkdv_kernel<D><<<(unsigned)((int64_t)a.n_tiles * a.Hkv), kThreads, KvCfg<D>::BYTES, s>>>(prm);
     note_launch(SGA_KERN_SEQ_BWD_DKDV, s, true);
     note_launch(SGA_KERN_SEQ_BWD_DQ, s, false);
     seq_bwd_dq_kernel<D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, QCfg<D>::BYTES + 1024, s>>>(prm);

@@ -287,8 +287,8 @@ sga_status seq_attn_bwd(const sga_seq_plan *p, const void *Q, const void *K, con
     a.dQ = dQ;
     a.dK = dK;
     a.dV = dV;
-    a.ws_lse = static_cast<float *>(workspace);
-    a.ws_delta = a.ws_lse + (size_t)p->H * a.rows_pad;
+    a.ws_nlse = static_cast<float *>(workspace);
+    a.ws_ndelta = a.ws_nlse + (size_t)p->H * a.rows_pad;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return status_of(p->dt == SGA_F32 ? seq_bwd_simt<float>(a, p->D, s) : seq_bwd_bf16(a, p->D, s));
 }

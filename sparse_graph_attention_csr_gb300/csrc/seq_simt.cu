@@ -267,8 +267,8 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t r = (int64_t)h * a.rows_pad + q0 + ty + 16 * i;
-        ls[i] = a.ws_lse[r];
-        dl[i] = a.ws_delta[r];
+        ls[i] = a.ws_nlse[r];
+        dl[i] = a.ws_ndelta[r];
 #pragma unroll
         for (int x = 0; x < kCols<D>; ++x) acc[i][x] = 0.f;
     }
@@ -290,7 +290,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
             for (int c = 0; c < 4; ++c) {
                 const int j = tx + 16 * c;
                 const bool on = full || (j >= kl[i] && j < kh[i]);
-                sP[(ty + 16 * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, -ls[i])) * (g[i][c] - dl[i]) : 0.f;
+                sP[(ty + 16 * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, ls[i])) * (g[i][c] + dl[i]) : 0.f;
             }
         __syncthreads();
         if (full) add_product<D, false>(acc, sP, sK, ty, tx, kl, kh);
@@ -334,8 +334,8 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int64_t r = (int64_t)h * a.rows_pad + q0 + tx + 16 * c;
-                ls[c] = a.ws_lse[r];
-                dl[c] = a.ws_delta[r];
+                ls[c] = a.ws_nlse[r];
+                dl[c] = a.ws_ndelta[r];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -343,9 +343,9 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
                 for (int c = 0; c < 4; ++c) {
                     const int j = tx + 16 * c;
                     const bool on = full || (j >= ql[i] && j < qh[i]);
-                    const float p = on ? fast_exp2(fmaf(s[i][c], scale2, -ls[c])) : 0.f;
+                    const float p = on ? fast_exp2(fmaf(s[i][c], scale2, ls[c])) : 0.f;
                     sP[(ty + 16 * i) * kPP + j] = p;
-                    sS[(ty + 16 * i) * kPP + j] = on ? p * (g[i][c] - dl[c]) : 0.f;
+                    sS[(ty + 16 * i) * kPP + j] = on ? p * (g[i][c] + dl[c]) : 0.f;
                 }
             __syncthreads();
             if (full) {
@@ -362,7 +362,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
 }
 
 // Row terms: D / EL lanes of 16 bytes a (row, head).  Rows behind the last
-// sequence (to the end of its tile) get lse = +inf, so that their weights are
+// sequence (to the end of its tile) get -lse = -inf, so that their weights are
 // zero, and Delta = 0.
 template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
     constexpr int EL = Elt<T>::EL, L = D / EL;
@@ -384,8 +384,8 @@ template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_term
     d = group_sum<L>(d);
     if (sub == 0) {
         const int64_t at = (int64_t)h * a.rows_pad + row;
-        a.ws_lse[at] = in ? a.lse[row * a.H + h] * kLog2e : INFINITY;
-        a.ws_delta[at] = in ? d : 0.f;
+        a.ws_nlse[at] = in ? -(a.lse[row * a.H + h] * kLog2e) : -INFINITY;
+        a.ws_ndelta[at] = in ? -d : 0.f;
     }
 }
 
