@@ -504,10 +504,10 @@ typedef enum {
     SGA_KERN_AGG_FWD = 19, SGA_KERN_AGG_FWD_MERGE = 20, SGA_KERN_AGG_BWD = 21,
     SGA_KERN_AGG_BWD_MERGE = 22,
     SGA_KERN_GAT_FWD = 23, SGA_KERN_GAT_BWD_DST = 24, SGA_KERN_GAT_BWD_SRC = 25,
-    SGA_KERN_SEQ_FWD = 26, SGA_KERN_SEQ_BWD_ROWS = 27, SGA_KERN_SEQ_BWD_DQ = 28,
-    SGA_KERN_SEQ_BWD_DKDV = 29, SGA_KERN_NORM_FWD = 30, SGA_KERN_NORM_BWD = 31,
-    SGA_KERN_NORM_REDUCE = 32, SGA_KERN_EMBED_FWD = 33, SGA_KERN_EMBED_BWD = 34,
-    SGA_KERN_COUNT = 35
+    SGA_KERN_SEQ_FWD = 26, SGA_KERN_SEQ_BWD_ROWS = 27, SGA_KERN_SEQ_BWD = 28,
+    SGA_KERN_NORM_FWD = 29, SGA_KERN_NORM_BWD = 30, SGA_KERN_NORM_REDUCE = 31,
+    SGA_KERN_EMBED_FWD = 32, SGA_KERN_EMBED_BWD = 33,
+    SGA_KERN_COUNT = 34
 } sga_kernel_id;
 /* (Planned GATv2 passes merge their split rows inside the edge kernels --
  * the last chunk of a row to finish merges it -- so SGA_KERN_GATV2_FWD_MERGE

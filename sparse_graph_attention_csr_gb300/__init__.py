@@ -34,8 +34,8 @@ KERNELS = {
     "gatv2_bwd_reduce": 14, "bsr_fwd": 15, "bsr_bwd_delta": 16, "bsr_bwd_dq": 17,
     "bsr_bwd_dkdv": 18, "agg_fwd": 19, "agg_fwd_merge": 20, "agg_bwd": 21, "agg_bwd_merge": 22,
     "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25, "seq_fwd": 26, "seq_bwd_rows": 27,
-    "seq_bwd_dq": 28, "seq_bwd_dkdv": 29, "norm_fwd": 30, "norm_bwd": 31, "norm_reduce": 32,
-    "embed_fwd": 33, "embed_bwd": 34,
+    "seq_bwd": 28, "norm_fwd": 29, "norm_bwd": 30, "norm_reduce": 31, "embed_fwd": 32,
+    "embed_bwd": 33,
 }
 
 SGA_LAYER_ATTENTION, SGA_LAYER_MINMAX, SGA_LAYER_GAT = 0, 1, 2
@@ -625,13 +625,10 @@ def agg_minmax_bwd(plan: Plan, mask, dOut, dX=None, stream=None):
 # ------------------------------------------- attention over packed sequences
 
 _NO_CONTEXT = contextlib.nullcontext()
-
-
-def _current_raw_stream(index):
-    """The raw handle of a device's current stream (without a Stream object
-    where torch offers that: 0.1 us instead of 2.9 us a call)."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+# The raw handle of a device's current stream, without a Stream object where
+# torch offers that (0.1 us instead of 2.9 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _place(device, stream):
@@ -640,8 +637,9 @@ def _place(device, stream):
     are current, so results and workspaces are allocated on the stream that
     writes them."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return _NO_CONTEXT, _current_raw_stream(device.index)
+        index = device.index
+        if torch.cuda.current_device() == index:
+            return _NO_CONTEXT, _raw_stream(index)
         stream = torch.cuda.current_stream(device)
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
@@ -650,8 +648,8 @@ def _place(device, stream):
 
 def _tensor(t, name, device, dtype, shape):
     """A contiguous CUDA tensor of exactly this device, dtype and shape."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous() and t.is_cuda):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device.index and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -661,8 +659,7 @@ def _tensor(t, name, device, dtype, shape):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _distinct(ins, outs):
@@ -735,9 +732,10 @@ def _seq_inputs(plan, Q, K, V):
     T = Q.shape[0] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else plan.rows
     if T < plan.rows:
         raise ValueError(f"Q has {T} rows, the plan's sequences cover {plan.rows}")
+    kv = (T, plan.kv_heads, plan.D)
     _tensor(Q, "Q", plan.device, plan.dtype, (T, plan.H, plan.D))
-    _tensor(K, "K", plan.device, plan.dtype, (T, plan.kv_heads, plan.D))
-    _tensor(V, "V", plan.device, plan.dtype, (T, plan.kv_heads, plan.D))
+    _tensor(K, "K", plan.device, plan.dtype, kv)
+    _tensor(V, "V", plan.device, plan.dtype, kv)
     return T
 
 
@@ -781,8 +779,10 @@ def seq_attn_fwd(plan: SeqPlan, Q, K, V, scale: float | None = None, out=None, l
             _tensor(lse, "lse", plan.device, torch.float32, (T, plan.H))
         if not own:
             _distinct((("Q", Q), ("K", K), ("V", V)), (("out", out), ("lse", lse)))
-        _check(_lib().seq_attn_fwd(plan.handle, Q.data_ptr(), K.data_ptr(), V.data_ptr(), T, scale,
-                                   out.data_ptr(), lse.data_ptr(), raw), "seq_attn_fwd")
+        st = _lib().seq_attn_fwd(plan._h, Q.data_ptr(), K.data_ptr(), V.data_ptr(), T, scale,
+                                 out.data_ptr(), lse.data_ptr(), raw)
+    if st:
+        raise SgaError(st, "seq_attn_fwd")
     return out, lse
 
 
@@ -805,35 +805,38 @@ def seq_attn_bwd(plan: SeqPlan, Q, K, V, out, lse, dOut, scale: float | None = N
             _distinct((("Q", Q), ("K", K), ("V", V), ("out", out), ("lse", lse), ("dOut", dOut)),
                       (("dQ", dQ), ("dK", dK), ("dV", dV)))
         ws = torch.empty(plan._ws_bytes, dtype=torch.uint8, device=plan.device)
-        _check(_lib().seq_attn_bwd(plan.handle, Q.data_ptr(), K.data_ptr(), V.data_ptr(),
-                                   out.data_ptr(), lse.data_ptr(), dOut.data_ptr(), T, scale,
-                                   dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), ws.data_ptr(),
-                                   plan._ws_bytes, raw), "seq_attn_bwd")
+        st = _lib().seq_attn_bwd(plan._h, Q.data_ptr(), K.data_ptr(), V.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), dOut.data_ptr(), T, scale, dQ.data_ptr(),
+                                 dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), plan._ws_bytes, raw)
+    if st:
+        raise SgaError(st, "seq_attn_bwd")
     return dQ, dK, dV
 
 
 # ------------------------------------------------------------------ layer norm
 
 def _norm_inputs(X, weight, bias=None):
+    """(device, shape, dtype code, weight's dtype code) of the checked inputs."""
     if not isinstance(X, torch.Tensor) or not X.is_cuda:
         raise ValueError("X must be a CUDA tensor")
-    if X.dim() < 1 or X.shape[-1] < 1:
-        raise ValueError(f"X must be [..., C] with C >= 1, got {tuple(X.shape)}")
-    dt = _dtype_code(X)
+    shape, dtype, device = X.shape, X.dtype, X.device
+    if not shape or shape[-1] < 1:
+        raise ValueError(f"X must be [..., C] with C >= 1, got {tuple(shape)}")
+    dt = SGA_BF16 if dtype is torch.bfloat16 else _dtype_code(X)
     if not X.is_contiguous():
         raise ValueError("X must be contiguous")
-    C = X.shape[-1]
     if weight is None:
         if bias is not None:
             raise ValueError("a bias needs a weight")
-        return dt, dt, C
+        return device, shape, dt, dt
     wdtype = weight.dtype if isinstance(weight, torch.Tensor) else None
-    if wdtype != torch.float32 and wdtype != X.dtype:
-        raise TypeError(f"weight must be {X.dtype} or torch.float32, got {wdtype}")
-    _tensor(weight, "weight", X.device, wdtype, (C,))
+    if wdtype is not torch.float32 and wdtype is not dtype:
+        raise TypeError(f"weight must be {dtype} or torch.float32, got {wdtype}")
+    row = shape[-1:]
+    _tensor(weight, "weight", device, wdtype, row)
     if bias is not None:
-        _tensor(bias, "bias", X.device, wdtype, (C,))
-    return dt, SGA_F32 if wdtype == torch.float32 else SGA_BF16, C
+        _tensor(bias, "bias", device, wdtype, row)
+    return device, shape, dt, SGA_F32 if wdtype is torch.float32 else SGA_BF16
 
 
 def layer_norm_fwd(X, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None,
@@ -841,31 +844,35 @@ def layer_norm_fwd(X, weight=None, bias=None, eps: float = 1e-5, out=None, mean=
     """Layer norm over the last dimension of X [..., C]: (out, mean, rstd) with
     mean and rstd = 1 / sqrt(var + eps) float32 of X's leading shape.  weight,
     bias: [C], float32 or X's dtype, or None.  ``out`` may be X itself."""
-    dt, wdt, C = _norm_inputs(X, weight, bias)
+    device, shape, dt, wdt = _norm_inputs(X, weight, bias)
     eps = float(eps)
     if not 0.0 <= eps < math.inf:
         raise ValueError(f"eps must be finite and not negative, got {eps}")
-    lead = X.shape[:-1]
-    ctx, raw = _place(X.device, stream)
+    lead, C = shape[:-1], shape[-1]
+    ctx, raw = _place(device, stream)
     with ctx:
         own = out is None and mean is None and rstd is None
-        out = torch.empty_like(X) if out is None else out
-        mean = torch.empty(lead, dtype=torch.float32, device=X.device) if mean is None else mean
-        rstd = torch.empty(lead, dtype=torch.float32, device=X.device) if rstd is None else rstd
+        if out is None:
+            out = torch.empty_like(X)
+        if mean is None:
+            mean = torch.empty(lead, dtype=torch.float32, device=device)
+        if rstd is None:
+            rstd = torch.empty_like(mean)
         if not own:
-            _tensor(out, "out", X.device, X.dtype, X.shape)
-            _tensor(mean, "mean", X.device, torch.float32, lead)
-            _tensor(rstd, "rstd", X.device, torch.float32, lead)
+            _tensor(out, "out", device, X.dtype, shape)
+            _tensor(mean, "mean", device, torch.float32, lead)
+            _tensor(rstd, "rstd", device, torch.float32, lead)
             ins = [(n, t) for n, t in (("X", X), ("weight", weight), ("bias", bias)) if t is not None]
             if out.data_ptr() == X.data_ptr():   # in place: a row is read before it is written
                 _distinct(ins, (("mean", mean), ("rstd", rstd)))
                 _distinct(ins[1:], (("out", out), ("mean", mean), ("rstd", rstd)))
             else:
                 _distinct(ins, (("out", out), ("mean", mean), ("rstd", rstd)))
-        _check(_lib().layer_norm_fwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
-                                     None if bias is None else bias.data_ptr(), X.numel() // C, C,
-                                     eps, dt, wdt, out.data_ptr(), mean.data_ptr(),
-                                     rstd.data_ptr(), raw), "layer_norm_fwd")
+        st = _lib().layer_norm_fwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
+                                   None if bias is None else bias.data_ptr(), X.numel() // C, C,
+                                   eps, dt, wdt, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), raw)
+    if st:
+        raise SgaError(st, "layer_norm_fwd")
     return out, mean, rstd
 
 
@@ -873,43 +880,46 @@ def layer_norm_bwd(X, weight, mean, rstd, dOut, bias: bool = True, dX=None, dwei
                    dbias=None, stream=None):
     """(dX, dweight, dbias) from the forward's mean and rstd; dweight and dbias
     in weight's dtype, None without a weight (dbias also with bias=False)."""
-    dt, wdt, C = _norm_inputs(X, weight)
-    _tensor(dOut, "dOut", X.device, X.dtype, X.shape)
-    lead = X.shape[:-1]
-    _tensor(mean, "mean", X.device, torch.float32, lead)
-    _tensor(rstd, "rstd", X.device, torch.float32, lead)
+    device, shape, dt, wdt = _norm_inputs(X, weight)
+    lead, C = shape[:-1], shape[-1]
+    _tensor(dOut, "dOut", device, X.dtype, shape)
+    _tensor(mean, "mean", device, torch.float32, lead)
+    _tensor(rstd, "rstd", device, torch.float32, lead)
     if weight is None and (dweight is not None or dbias is not None):
         raise ValueError("dweight and dbias need a weight")
     if not bias and dbias is not None:
         raise ValueError("dbias given with bias=False")
     N = X.numel() // C
-    ctx, raw = _place(X.device, stream)
+    ctx, raw = _place(device, stream)
+    lib = _lib()
     with ctx:
         own = dX is None and dweight is None and dbias is None
-        dX = torch.empty_like(X) if dX is None else dX
+        if dX is None:
+            dX = torch.empty_like(X)
         ws, nbytes = None, 0
         if weight is not None:
-            dweight = torch.empty_like(weight) if dweight is None else dweight
-            if bias:
-                dbias = torch.empty_like(weight) if dbias is None else dbias
-            nbytes = int(_lib().sga_norm_bwd_workspace_bytes(N, C))
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
+            if dweight is None:
+                dweight = torch.empty_like(weight)
+            if bias and dbias is None:
+                dbias = torch.empty_like(weight)
+            nbytes = lib.sga_norm_bwd_workspace_bytes(N, C)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         if not own:
             outs = [("dX", dX)]
-            _tensor(dX, "dX", X.device, X.dtype, X.shape)
+            _tensor(dX, "dX", device, X.dtype, shape)
             for n, t in (("dweight", dweight), ("dbias", dbias)):
                 if t is not None:
-                    _tensor(t, n, X.device, weight.dtype, weight.shape)
+                    _tensor(t, n, device, weight.dtype, weight.shape)
                     outs.append((n, t))
             ins = [("X", X), ("dOut", dOut), ("mean", mean), ("rstd", rstd)]
             _distinct(ins + ([("weight", weight)] if weight is not None else []), outs)
-        _check(_lib().layer_norm_bwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
-                                     mean.data_ptr(), rstd.data_ptr(), dOut.data_ptr(), N, C, dt,
-                                     wdt, dX.data_ptr(),
-                                     None if dweight is None else dweight.data_ptr(),
-                                     None if dbias is None else dbias.data_ptr(),
-                                     None if ws is None else ws.data_ptr(), nbytes, raw),
-               "layer_norm_bwd")
+        st = lib.layer_norm_bwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
+                                mean.data_ptr(), rstd.data_ptr(), dOut.data_ptr(), N, C, dt, wdt,
+                                dX.data_ptr(), None if dweight is None else dweight.data_ptr(),
+                                None if dbias is None else dbias.data_ptr(),
+                                None if ws is None else ws.data_ptr(), nbytes, raw)
+    if st:
+        raise SgaError(st, "layer_norm_bwd")
     return dX, dweight, dbias
 
 
@@ -939,20 +949,22 @@ def embed_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
     id_bytes = _embed_ids(ids)
     if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[1] < 1:
         raise ValueError("table must be [V, C] with C >= 1")
-    dt = _dtype_code(table)
-    V, C = table.shape
-    _tensor(table, "table", ids.device, table.dtype, (V, C))
+    dt, device, dtype = _dtype_code(table), ids.device, table.dtype
+    V, C = rows = table.shape
+    _tensor(table, "table", device, dtype, rows)
     scale = _embed_scale(scale)
     shape = (*ids.shape, C)
-    ctx, raw = _place(ids.device, stream)
+    ctx, raw = _place(device, stream)
     with ctx:
         if out is None:
-            out = torch.empty(shape, dtype=table.dtype, device=ids.device)
+            out = torch.empty(shape, dtype=dtype, device=device)
         else:
-            _tensor(out, "out", ids.device, table.dtype, shape)
+            _tensor(out, "out", device, dtype, shape)
             _distinct((("ids", ids), ("table", table)), (("out", out),))
-        _check(_lib().embed_fwd(ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(), V, C, scale,
-                                dt, out.data_ptr(), raw), "embed_fwd")
+        st = _lib().embed_fwd(ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(), V, C, scale,
+                              dt, out.data_ptr(), raw)
+    if st:
+        raise SgaError(st, "embed_fwd")
     return out
 
 
@@ -977,17 +989,19 @@ def embed_bwd(ids, dOut, num_rows: int, scale: float = 1.0, padding_idx: int | N
     scale = _embed_scale(scale)
     N = ids.numel()
     ctx, raw = _place(ids.device, stream)
+    lib = _lib()
     with ctx:
         if dTable is None:
             dTable = torch.empty((V, C), dtype=dOut.dtype, device=ids.device)
         else:
             _tensor(dTable, "dTable", ids.device, dOut.dtype, (V, C))
             _distinct((("ids", ids), ("dOut", dOut)), (("dTable", dTable),))
-        nbytes = int(_lib().sga_embed_bwd_workspace_bytes(N, C))
+        nbytes = lib.sga_embed_bwd_workspace_bytes(N, C)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=ids.device)
-        _check(_lib().embed_bwd(ids.data_ptr(), id_bytes, dOut.data_ptr(), N, V, C, scale,
-                                padding_idx, dt, dTable.data_ptr(), ws.data_ptr(), nbytes, raw),
-               "embed_bwd")
+        st = lib.embed_bwd(ids.data_ptr(), id_bytes, dOut.data_ptr(), N, V, C, scale, padding_idx,
+                           dt, dTable.data_ptr(), ws.data_ptr(), nbytes, raw)
+    if st:
+        raise SgaError(st, "embed_bwd")
     return dTable
 
 

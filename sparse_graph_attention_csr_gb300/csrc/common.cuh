@@ -175,6 +175,18 @@ constexpr int kErrIndexRange = 1;   // a gathered node id was outside [0, N)
 
 // ---- host-side launch bookkeeping (defined in api.cu) -----------------------
 namespace sga {
+// SMs of the current device (looked up once per device).
+inline int device_sms() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < kMaxDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    if (dev >= 0 && dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 void note_launch(sga_kernel_id which, cudaStream_t s, bool after);
 
 // Let Kernel launch with `smem` bytes of dynamic shared memory: raises the

@@ -36,13 +36,6 @@ sga_status status_of(cudaError_t e) {
 // Bit kErrIndexRange: an id outside [0, V) since the last read, per device.
 __device__ int32_t g_embed_err;
 
-int sm_count() {
-    int dev = 0, n = 1;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-}
-
 __device__ __forceinline__ int64_t id_at(const void *ids, int64_t t, bool wide) {
     return wide ? __ldg(static_cast<const long long *>(ids) + t) : (int64_t)__ldg(static_cast<const int *>(ids) + t);
 }
@@ -100,8 +93,8 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void *__restrict__
 // One cooperative launch (a block per SM, grid barriers between the steps):
 //   sort: least significant digit first, digits of at most 8 bits.  A warp owns
 //     a run of consecutive tokens and counts their digits in shared memory; a
-//     block adds its warps' counts per digit, a warp per digit adds the blocks',
-//     and every warp then places its tokens in order (equal digits of 32
+//     block adds its warps' counts per digit, then each block all blocks', and
+//     every warp places its tokens in order (equal digits of 32
 //     tokens ranked by lane), so the sort is stable.  Counts are whole numbers:
 //     the order in which they are added does not matter.
 //   sums: groups of lanes over chunks of the sorted list, as described above;
@@ -118,7 +111,7 @@ struct GradArgs {
     const void *ids, *dOut;
     void *dTable;
     int32_t *key[2], *tok[2];   // ping-pong buffers of the sort
-    int32_t *hist, *total;      // [digit][block] counts, [digit] sums
+    int32_t *hist;              // [digit][block] counts
     float *part;                // [chunks][2][C]: the row that runs on from the chunk before, the row that runs on
     int64_t N, V, chunks, padding;
     int wide, L, C, bits, passes, gshift;
@@ -162,25 +155,35 @@ __device__ void sort_tokens(const GradArgs &a, int32_t (*cnt)[kDigits], int32_t 
             a.hist[(int64_t)threadIdx.x * B + blockIdx.x] = run;
         }
         grid.sync();
-        for (int d = blockIdx.x + B * wp; d < kDigits; d += B * kSortWarps) {   // exclusive sums over the blocks
-            int32_t run = 0;
-            for (int i = 0; i < B; i += 32) {
-                const int32_t c = i + lane < B ? __ldcg(a.hist + (int64_t)d * B + i + lane) : 0;
-                int32_t x = c;
+        // every block adds the counts itself (40 loads a lane in flight at once, cheaper
+        // than a further step with its barrier): of a digit, all blocks' and the earlier blocks'
+        {
+            constexpr int DW = kDigits / kSortWarps;
+            int32_t all[DW], before[DW];
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int32_t y = __shfl_up_sync(SGA_FULL_MASK, x, o);
-                    if (lane >= o) x += y;
+            for (int k = 0; k < DW; ++k) {
+                const int32_t *h = a.hist + (int64_t)(wp * DW + k) * B;
+                all[k] = before[k] = 0;
+                for (int i = lane; i < B; i += 32) {
+                    const int32_t c = __ldcg(h + i);
+                    all[k] += c;
+                    before[k] += i < (int)blockIdx.x ? c : 0;
                 }
-                if (i + lane < B) a.hist[(int64_t)d * B + i + lane] = run + x - c;
-                run += __shfl_sync(SGA_FULL_MASK, x, 31);
             }
-            if (lane == 0) a.total[d] = run;
+#pragma unroll
+            for (int k = 0; k < DW; ++k) {
+                const int32_t t = __reduce_add_sync(SGA_FULL_MASK, all[k]), q = __reduce_add_sync(SGA_FULL_MASK, before[k]);
+                if (lane == 0) {
+                    scan[kSortWarps + wp * DW + k] = t;
+                    scan[kSortWarps + kDigits + wp * DW + k] = q;
+                }
+            }
         }
-        grid.sync();
+        __syncthreads();
         // first position of every digit: exclusive sums over the digits' totals
+        int32_t first = 0;
         if (threadIdx.x < kDigits) {
-            const int32_t c = __ldcg(a.total + threadIdx.x);
+            const int32_t c = scan[kSortWarps + threadIdx.x];
             int32_t x = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -188,13 +191,12 @@ __device__ void sort_tokens(const GradArgs &a, int32_t (*cnt)[kDigits], int32_t 
                 if (lane >= o) x += y;
             }
             if (lane == 31) scan[wp] = x;
-            scan[kSortWarps + threadIdx.x] = x - c;
+            first = x - c;
         }
         __syncthreads();
         if (threadIdx.x < kDigits) {
-            int32_t base = scan[kSortWarps + threadIdx.x] + __ldcg(a.hist + (int64_t)threadIdx.x * B + blockIdx.x);
-            for (int w = 0; w < wp; ++w) base += scan[w];
-            scan[kSortWarps + kDigits + threadIdx.x] = base;
+            for (int w = 0; w < wp; ++w) first += scan[w];
+            scan[kSortWarps + kDigits + threadIdx.x] += first;
         }
         __syncthreads();
         for (int d = lane; d < kDigits; d += 32) cnt[wp][d] += scan[kSortWarps + kDigits + d];
@@ -339,38 +341,50 @@ template <int M> __device__ __forceinline__ float column_of(const GradArgs &a, i
     return s;
 }
 
-template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &a, float *sm, int64_t *who) {
+template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &a, float *sm, int64_t (*who)[3]) {
     const int32_t *key = a.key[a.passes & 1];
     T *dTable = static_cast<T *>(a.dTable);
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    for (int64_t base = (int64_t)blockIdx.x * kSortWarps; base < a.chunks; base += (int64_t)gridDim.x * kSortWarps) {
-        const int64_t c0 = base + wp;
+    // a block's chunks are apart: the hot rows, which begin close together, go to different blocks
+    for (int64_t base = 0; base < a.chunks; base += (int64_t)gridDim.x * kSortWarps) {
+        const int64_t c0 = base + (int64_t)wp * gridDim.x + blockIdx.x;
         int32_t cur = 0;
         int64_t cl = 0;
         const bool on = c0 < a.chunks && runs_on(a, key, c0, cur, cl);
         const bool lng = on && cl - c0 > kLongRow;
-        if (lane == 0) who[wp] = lng ? cl : -1;
+        if (lane == 0) {
+            who[wp][0] = lng ? cl : -1;
+            who[wp][1] = c0;
+            who[wp][2] = cur;
+        }
+        const bool any = __syncthreads_or(lng);
         if (on && !lng)
             for (int c = lane; c < a.C; c += 128) {   // four columns of a lane at a time
                 float s[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
                     s[z] = c + 32 * z < a.C ? __ldcg(a.part + (c0 * 2 + 1) * a.C + c + 32 * z) : 0.f;
-                for (int64_t k = c0 + 1; k <= cl; ++k)
+                for (int64_t k = c0 + 1; k <= cl; k += 2) {
+                    float v[2][4];
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        s[z] += c + 32 * z < a.C ? __ldcg(a.part + k * 2 * a.C + c + 32 * z) : 0.f;
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            v[q][z] = k + q <= cl && c + 32 * z < a.C ? __ldcg(a.part + (k + q) * 2 * a.C + c + 32 * z) : 0.f;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) s[z] += v[0][z] + v[1][z];
+                }
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
                     if (c + 32 * z < a.C) dTable[(int64_t)cur * a.C + c + 32 * z] = from_f32<T>(s[z] * a.scale);
             }
-        __syncthreads();
+        if (!any) continue;
         // long rows by the whole block: a warp per 32 columns and share of the chunks
         const int cols = min(kSortWarps, (a.C + 31) / 32), shares = kSortWarps / cols, slab = wp % cols, share = wp / cols;
         for (int w = 0; w < kSortWarps; ++w) {
-            if (who[w] < 0) continue;   // (the same for the whole block)
-            const int64_t f = base + w, l = who[w], per = (l - f + shares - 1) / shares;
-            const int32_t id = __ldcg(key + (f + 1) * a.L - 1);
+            const int64_t l = who[w][0];
+            if (l < 0) continue;   // (the same for the whole block)
+            const int64_t f = who[w][1], id = who[w][2], per = (l - f + shares - 1) / shares;
             for (int cb = 0; cb < a.C; cb += 32 * cols) {
                 const int col = cb + slab * 32 + lane;
                 float s = 0.f;
@@ -383,7 +397,7 @@ template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &
                 if (share == 0 && col < a.C) {
                     s = 0.f;
                     for (int q = 0; q < shares; ++q) s += sm[(q * cols + slab) * 32 + lane];
-                    dTable[(int64_t)id * a.C + col] = from_f32<T>(s * a.scale);
+                    dTable[id * a.C + col] = from_f32<T>(s * a.scale);
                 }
                 __syncthreads();
             }
@@ -395,7 +409,7 @@ template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &
 template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_kernel(const GradArgs a) {
     __shared__ int32_t cnt[kSortWarps][kDigits];
     __shared__ int32_t scan[kSortWarps + 2 * kDigits];
-    __shared__ int64_t who[kSortWarps];
+    __shared__ int64_t who[kSortWarps][3];
     const int64_t t0 = (int64_t)blockIdx.x * kSortThreads + threadIdx.x, nt = (int64_t)gridDim.x * kSortThreads;
     if constexpr (VEC) {
         for (int64_t i = t0; i < a.V * a.C / Elt<T>::EL; i += nt)
@@ -425,7 +439,7 @@ int bits_of(int64_t v) {
 }
 
 struct Layout {
-    size_t key[2], tok[2], hist, total, part, bytes;
+    size_t key[2], tok[2], hist, part, bytes;
 };
 Layout layout(int64_t N, int64_t C, int sms) {
     Layout l{};
@@ -440,7 +454,6 @@ Layout layout(int64_t N, int64_t C, int sms) {
         l.tok[i] = take((size_t)N * 4 + 16);
     }
     l.hist = take((size_t)kDigits * grad_blocks(N, sms) * 4);
-    l.total = take(kDigits * 4);
     const int L = chunk_len(N, sms);
     l.part = take((size_t)((N + L - 1) / L) * 2 * C * 4);
     l.bytes = off;
@@ -474,7 +487,7 @@ cudaError_t fwd_t(const void *ids, bool wide, const void *table, int64_t N, int6
     int sh = 0;
     while (sh < 5 && (4 << sh) < n) ++sh;   // four groups a lane
     const int64_t blocks = ((N << sh) + 255) / 256;
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)sm_count() * 32);
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)device_sms() * 32);
     note_launch(SGA_KERN_EMBED_FWD, s, false);
     embed_fwd_kernel<T, VEC><<<grid, 256, 0, s>>>(ids, wide, static_cast<const T *>(table), N, V, C, scale, sh,
                                                   static_cast<T *>(out));
@@ -507,7 +520,7 @@ sga_status embed_fwd(const void *ids, int id_bytes, const void *table, int64_t N
 }
 
 size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t C) {
-    return N <= 0 || C <= 0 || N >= INT32_MAX ? 0 : layout(N, C, sm_count()).bytes;
+    return N <= 0 || C <= 0 || N >= INT32_MAX ? 0 : layout(N, C, device_sms()).bytes;
 }
 
 sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N, int64_t V, int64_t C, float scale,
@@ -520,7 +533,7 @@ sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N,
     if (N > 0 && (!ids || !aligned(ids, id_bytes) || !dOut || !aligned(dOut, e))) return SGA_EINVAL;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (N == 0) return status_of(V > 0 ? cudaMemsetAsync(dTable, 0, (size_t)V * C * e, s) : cudaSuccess);
-    const int sms = sm_count();
+    const int sms = device_sms();
     const Layout l = layout(N, C, sms);
     if (!workspace || !aligned(workspace, 256)) return SGA_EINVAL;
     if (workspace_bytes < l.bytes) return SGA_EWORKSPACE;
@@ -535,7 +548,6 @@ sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N,
         a.tok[i] = reinterpret_cast<int32_t *>(ws + l.tok[i]);
     }
     a.hist = reinterpret_cast<int32_t *>(ws + l.hist);
-    a.total = reinterpret_cast<int32_t *>(ws + l.total);
     a.part = reinterpret_cast<float *>(ws + l.part);
     a.N = N;
     a.V = V;

@@ -41,22 +41,51 @@ struct NormArgs {
     float eps;
 };
 
-// EL consecutive elements at p as fp32: 16-byte loads where EL covers 16 bytes.
-template <typename T, int EL> __device__ __forceinline__ void load_el(const T *p, float (&x)[EL]) {
-    constexpr int CH = Elt<T>::EL;
-    if constexpr (EL % CH == 0) {
+// EL consecutive elements as they lie in memory: 16-byte loads where EL covers
+// 16 bytes (or several), one load of EL elements otherwise.
+template <typename T, int EL> struct Raw {
+    static constexpr int B = EL * (int)sizeof(T);
+    static_assert(B % 16 == 0 || B == 8 || B == 4 || B == 2, "group");
+    uint32_t u[B >= 4 ? B / 4 : 1];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int c = 0; c < EL; c += CH) unpack<T>(*reinterpret_cast<const uint4 *>(p + c), x + c);
-    } else {
-        x[0] = to_f32<T>(*p);
+        for (int i = 0; i < (B >= 4 ? B / 4 : 1); ++i) u[i] = 0;
     }
-}
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (B % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < B / 16; ++i) {
+                const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
+                u[4 * i] = q.x;
+                u[4 * i + 1] = q.y;
+                u[4 * i + 2] = q.z;
+                u[4 * i + 3] = q.w;
+            }
+        } else if constexpr (B == 8) {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p);
+            u[0] = q.x;
+            u[1] = q.y;
+        } else if constexpr (B == 4) {
+            u[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            u[0] = *reinterpret_cast<const uint16_t *>(p);
+        }
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+        else return __uint_as_float((i & 1) ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);   // (bf16: the top half of fp32)
+    }
+};
+
 template <typename T, int EL> __device__ __forceinline__ void store_el(T *p, const float (&x)[EL]) {
     constexpr int CH = Elt<T>::EL;
     if constexpr (EL % CH == 0) {
 #pragma unroll
         for (int c = 0; c < EL; c += CH) *reinterpret_cast<uint4 *>(p + c) = pack<T>(x + c);
+    } else if constexpr (EL == 2 && sizeof(T) == 2) {
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(x[0], x[1]);
     } else {
+        static_assert(EL == 1, "group");
         *p = from_f32<T>(x[0]);
     }
 }
@@ -90,45 +119,51 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
     const TX *X = static_cast<const TX *>(a.X);
     const TW *w = static_cast<const TW *>(a.w), *b = static_cast<const TW *>(a.b);
     const float inv = 1.f / (float)a.C;
-    float wr[NV][EL], br[NV][EL];
+    Raw<TW, EL> wr[NV], br[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = v * TPR + sub;
-#pragma unroll
-        for (int i = 0; i < EL; ++i) {
-            wr[v][i] = 1.f;
-            br[v][i] = 0.f;
-        }
-        if (c < nvec && w) load_el<TW, EL>(w + c * EL, wr[v]);
-        if (c < nvec && b) load_el<TW, EL>(b + c * EL, br[v]);
+        wr[v].zero();
+        br[v].zero();
+        if (c < nvec && w) wr[v].load(w + c * EL);
+        if (c < nvec && b) br[v].load(b + c * EL);
     }
-    // every group of a warp runs the same number of rounds: the sums are warp-wide calls
-    for (int64_t r0 = (int64_t)blockIdx.x * GPB; r0 < a.N; r0 += (int64_t)gridDim.x * GPB) {
-        const int64_t row = r0 + grp;
-        const bool in = row < a.N;
-        float x[NV][EL], s[1] = {0.f};
+    const int64_t step = (int64_t)gridDim.x * GPB;
+    Raw<TX, EL> x[NV];   // a round ahead: the next row's loads are in flight while a row is summed
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = v * TPR + sub;
-#pragma unroll
-            for (int i = 0; i < EL; ++i) x[v][i] = 0.f;
-            if (in && c < nvec) load_el<TX, EL>(X + row * a.C + c * EL, x[v]);
+            x[v].zero();
+            if (row < a.N && c < nvec) x[v].load(X + row * a.C + c * EL);
         }
+    };
+    fetch((int64_t)blockIdx.x * GPB + grp);
+    // every group of a warp runs the same number of rounds: the sums are warp-wide calls
+    for (int64_t r0 = (int64_t)blockIdx.x * GPB; r0 < a.N; r0 += step) {
+        const int64_t row = r0 + grp;
+        float f[NV][EL], s[1] = {0.f};
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int i = 0; i < EL; ++i) s[0] += x[v][i];
+            for (int i = 0; i < EL; ++i) {
+                f[v][i] = x[v].at(i);
+                s[0] += f[v][i];
+            }
+        fetch(row + step);
         row_sum<TPR, 1>(s, red);
         const float mean = s[0] * inv;
         s[0] = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            if (v * TPR + sub < nvec)
 #pragma unroll
-                for (int i = 0; i < EL; ++i) s[0] = fmaf(x[v][i] - mean, x[v][i] - mean, s[0]);
+            for (int i = 0; i < EL; ++i) {
+                f[v][i] -= mean;
+                if (v * TPR + sub < nvec) s[0] = fmaf(f[v][i], f[v][i], s[0]);
+            }
         row_sum<TPR, 1>(s, red);
         const float rstd = rsqrtf(s[0] * inv + a.eps);
-        if (!in) continue;
+        if (row >= a.N) continue;
         if (sub == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
@@ -140,7 +175,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
             if (c >= nvec) continue;
             float y[EL];
 #pragma unroll
-            for (int i = 0; i < EL; ++i) y[i] = fmaf((x[v][i] - mean) * rstd, wr[v][i], br[v][i]);
+            for (int i = 0; i < EL; ++i) y[i] = w ? fmaf(f[v][i] * rstd, wr[v].at(i), br[v].at(i)) : f[v][i] * rstd;
             store_el<TX, EL>(Y + c * EL, y);
         }
     }
@@ -156,46 +191,57 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
     const TX *X = static_cast<const TX *>(a.X), *dY = static_cast<const TX *>(a.dY);
     const TW *w = static_cast<const TW *>(a.w);
     const float inv = 1.f / (float)a.C;
-    float wr[NV][EL], dw[NV][EL], db[NV][EL];
+    Raw<TW, EL> wr[NV];
+    float dw[NV][EL], db[NV][EL];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int c = v * TPR + sub;
+        wr[v].zero();
 #pragma unroll
-        for (int i = 0; i < EL; ++i) {
-            wr[v][i] = 1.f;
-            dw[v][i] = db[v][i] = 0.f;
-        }
-        if (c < nvec && w) load_el<TW, EL>(w + c * EL, wr[v]);
+        for (int i = 0; i < EL; ++i) dw[v][i] = db[v][i] = 0.f;
+        if (c < nvec && w) wr[v].load(w + c * EL);
     }
-    for (int64_t r0 = (int64_t)blockIdx.x * GPB; r0 < a.N; r0 += (int64_t)gridDim.x * GPB) {
-        const int64_t row = r0 + grp;
+    const int64_t step = (int64_t)gridDim.x * GPB;
+    Raw<TX, EL> xr[NV], gr[NV];   // a round ahead, as in the forward
+    float mean_r = 0.f, rstd_r = 0.f;
+    auto fetch = [&](int64_t row) {
         const bool in = row < a.N;
-        float x[NV][EL], g[NV][EL], s[2] = {0.f, 0.f};
+        mean_r = in ? a.mean_in[row] : 0.f;
+        rstd_r = in ? a.rstd_in[row] : 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = v * TPR + sub;
-#pragma unroll
-            for (int i = 0; i < EL; ++i) x[v][i] = g[v][i] = 0.f;
+            xr[v].zero();
+            gr[v].zero();
             if (in && c < nvec) {
-                load_el<TX, EL>(X + row * a.C + c * EL, x[v]);
-                load_el<TX, EL>(dY + row * a.C + c * EL, g[v]);
+                xr[v].load(X + row * a.C + c * EL);
+                gr[v].load(dY + row * a.C + c * EL);
             }
         }
-        const float mean = in ? a.mean_in[row] : 0.f, rstd = in ? a.rstd_in[row] : 0.f;
+    };
+    fetch((int64_t)blockIdx.x * GPB + grp);
+    for (int64_t r0 = (int64_t)blockIdx.x * GPB; r0 < a.N; r0 += step) {
+        const int64_t row = r0 + grp;
+        const float mean = mean_r, rstd = rstd_r;
+        float x[NV][EL], g[NV][EL], s[2] = {0.f, 0.f};
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (v * TPR + sub < nvec)
+        for (int v = 0; v < NV; ++v) {
+            const bool on = row < a.N && v * TPR + sub < nvec;
 #pragma unroll
-                for (int i = 0; i < EL; ++i) {
-                    x[v][i] = (x[v][i] - mean) * rstd;   // xhat
-                    db[v][i] += g[v][i];
-                    dw[v][i] = fmaf(g[v][i], x[v][i], dw[v][i]);
-                    g[v][i] *= wr[v][i];
-                    s[0] += g[v][i];
-                    s[1] = fmaf(g[v][i], x[v][i], s[1]);
-                }
+            for (int i = 0; i < EL; ++i) {
+                x[v][i] = (xr[v].at(i) - mean) * rstd;   // xhat
+                g[v][i] = gr[v].at(i);
+                if (!on) continue;
+                db[v][i] += g[v][i];
+                dw[v][i] = fmaf(g[v][i], x[v][i], dw[v][i]);
+                if (w) g[v][i] *= wr[v].at(i);
+                s[0] += g[v][i];
+                s[1] = fmaf(g[v][i], x[v][i], s[1]);
+            }
+        }
+        fetch(row + step);
         row_sum<TPR, 2>(s, red);
-        if (!in) continue;
+        if (row >= a.N) continue;
         const float c1 = s[0] * inv, c2 = s[1] * inv;
         TX *dX = static_cast<TX *>(a.dX) + row * a.C;
 #pragma unroll
@@ -299,32 +345,29 @@ template <typename TX> __global__ void __launch_bounds__(256) norm_cols_wide_ker
     out[a.C + c] = db;
 }
 
-// dw, db from the blocks' sums: 32 columns a block, its eight warps take every
-// eighth partial and are added in order.
-template <typename TW> __global__ void __launch_bounds__(256) norm_reduce_kernel(const float *__restrict__ part, int blocks,
-                                                                                 int C, TW *dw, TW *db) {
-    __shared__ float sm[8][32];
+// dw, db from the blocks' sums: 32 columns a block; its 32 warps take every
+// 32nd partial, four in flight, and are added in order.
+template <typename TW> __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ part, int blocks,
+                                                                                  int C, TW *dw, TW *db) {
+    __shared__ float sm[32][33];
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int64_t i = (int64_t)blockIdx.x * 32 + lane;   // column of [dw | db]
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane, n = 2 * (int64_t)C;   // column of [dw | db]
     float s = 0.f;
-    if (i < 2 * (int64_t)C)
-        for (int b = wp; b < blocks; b += 8) s += part[(int64_t)b * 2 * C + i];
+    if (i < n)
+        for (int b = wp; b < blocks; b += 128) {
+            float v[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[z] = b + 32 * z < blocks ? part[(b + 32 * z) * n + i] : 0.f;
+            s += (v[0] + v[1]) + (v[2] + v[3]);
+        }
     sm[wp][lane] = s;
     __syncthreads();
-    if (wp == 0 && i < 2 * (int64_t)C) {
-        s = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s += sm[q][lane];
-        if (i < C) dw[i] = from_f32<TW>(s);
-        else if (db) db[i - C] = from_f32<TW>(s);
+    s = group_sum<32>(sm[lane][wp]);   // warp wp: column wp of the block
+    const int64_t c = (int64_t)blockIdx.x * 32 + wp;
+    if (lane == 0 && c < n) {
+        if (c < C) dw[c] = from_f32<TW>(s);
+        else if (db) db[c - C] = from_f32<TW>(s);
     }
-}
-
-int sm_count() {
-    int dev = 0, n = 1;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
 }
 
 // Blocks of the backward pass, each with a row of sums: four an SM.
@@ -336,7 +379,7 @@ cudaError_t launch_fwd(const NormArgs &a, cudaStream_t s) {
     constexpr int TH = TPR > 128 ? TPR : 128;
     constexpr int GPB = TH / TPR;
     const int64_t need = (a.N + GPB - 1) / GPB;
-    const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)sm_count() * 16);
+    const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)device_sms() * 32);
     note_launch(SGA_KERN_NORM_FWD, s, false);
     norm_fwd_kernel<TX, TW, EL, TPR, NV, TH><<<grid, TH, 0, s>>>(a);
     note_launch(SGA_KERN_NORM_FWD, s, true);
@@ -348,7 +391,7 @@ cudaError_t launch_bwd(const NormArgs &a, int &blocks, cudaStream_t s) {
     constexpr int TH = TPR > 128 ? TPR : 128;
     constexpr int GPB = TH / TPR;
     const int64_t need = (a.N + GPB - 1) / GPB;
-    blocks = (int)std::min<int64_t>(need, bwd_blocks(sm_count()));
+    blocks = (int)std::min<int64_t>(need, bwd_blocks(device_sms()));
     const size_t smem = a.part ? sizeof(float) * 2 * a.C : 0;
     if (cudaError_t e = allow_smem<norm_bwd_kernel<TX, TW, EL, TPR, NV, TH>>(smem); e != cudaSuccess) return e;
     note_launch(SGA_KERN_NORM_BWD, s, false);
@@ -358,27 +401,36 @@ cudaError_t launch_bwd(const NormArgs &a, int &blocks, cudaStream_t s) {
 }
 
 // Threads of a row by its number of 16-byte vectors (or of elements, where the
-// width or an address is no multiple of 16 bytes).
-template <typename TX, typename TW> cudaError_t norm_fwd_t(const NormArgs &a, bool vec, cudaStream_t s) {
-    constexpr int EL = Elt<TX>::EL;
+// width or an address is no multiple of 16 bytes).  Two vectors a thread where
+// a warp can hold the row: of 1048576 x 256 bf16, 172 us (6.2 TB/s) with two,
+// 189 with four, 193 with one; blocks of 128 threads, 32 an SM (16 to 64 the
+// same, 8 15% slower).
+template <typename TX, typename TW> cudaError_t norm_fwd_t(const NormArgs &a, bool vec, bool pairs, cudaStream_t s) {
+    constexpr int EL = Elt<TX>::EL, P = sizeof(TX) == 2 ? 2 : 1;   // P: two bf16, one float
     const int nv = a.C / EL;
-    if (vec && nv <= 16) return launch_fwd<TX, TW, EL, 4, 4>(a, s);
-    if (vec && nv <= 32) return launch_fwd<TX, TW, EL, 8, 4>(a, s);
-    if (vec && nv <= 64) return launch_fwd<TX, TW, EL, 16, 4>(a, s);
+    if (vec && nv <= 8) return launch_fwd<TX, TW, EL, 4, 2>(a, s);
+    if (vec && nv <= 16) return launch_fwd<TX, TW, EL, 8, 2>(a, s);
+    if (vec && nv <= 32) return launch_fwd<TX, TW, EL, 16, 2>(a, s);
+    if (vec && nv <= 64) return launch_fwd<TX, TW, EL, 32, 2>(a, s);
     if (vec && nv <= 128) return launch_fwd<TX, TW, EL, 32, 4>(a, s);
     if (vec && nv <= 1024) return launch_fwd<TX, TW, EL, 256, 4>(a, s);
-    if (a.C <= 64) return launch_fwd<TX, TW, 1, 16, 4>(a, s);
-    if (a.C <= 512) return launch_fwd<TX, TW, 1, 32, 16>(a, s);
-    if (a.C <= 4096) return launch_fwd<TX, TW, 1, 256, 16>(a, s);
-    const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)sm_count() * 8);
+    if (pairs && a.C <= 64) return launch_fwd<TX, TW, P, 8, 8 / P>(a, s);
+    if (pairs && a.C <= 512) return launch_fwd<TX, TW, P, 32, 16 / P>(a, s);
+    if (pairs && a.C <= 4096) return launch_fwd<TX, TW, P, 256, 16 / P>(a, s);
+    if constexpr (P == 2) {   // an odd width, or bf16 rows off a 4-byte boundary
+        if (a.C <= 64) return launch_fwd<TX, TW, 1, 16, 4>(a, s);
+        if (a.C <= 512) return launch_fwd<TX, TW, 1, 32, 16>(a, s);
+        if (a.C <= 4096) return launch_fwd<TX, TW, 1, 256, 16>(a, s);
+    }
+    const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)device_sms() * 8);
     note_launch(SGA_KERN_NORM_FWD, s, false);
     norm_fwd_wide_kernel<TX, TW><<<grid, 256, 0, s>>>(a);
     note_launch(SGA_KERN_NORM_FWD, s, true);
     return cudaGetLastError();
 }
 
-template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bool vec, TW *dw, TW *db, cudaStream_t s) {
-    constexpr int EL = Elt<TX>::EL;
+template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bool vec, bool pairs, TW *dw, TW *db, cudaStream_t s) {
+    constexpr int EL = Elt<TX>::EL, P = sizeof(TX) == 2 ? 2 : 1;   // P: two bf16, one float
     const int nv = a.C / EL;
     int blocks = 0;
     cudaError_t e;
@@ -387,16 +439,19 @@ template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bo
     else if (vec && nv <= 32) e = launch_bwd<TX, TW, EL, 16, 2>(a, blocks, s);
     else if (vec && nv <= 64) e = launch_bwd<TX, TW, EL, 32, 2>(a, blocks, s);
     else if (vec && nv <= 512) e = launch_bwd<TX, TW, EL, 256, 2>(a, blocks, s);
+    else if (pairs && a.C <= 64) e = launch_bwd<TX, TW, P, 8, 8 / P>(a, blocks, s);
+    else if (pairs && a.C <= 512) e = launch_bwd<TX, TW, P, 32, 16 / P>(a, blocks, s);
+    else if (pairs && a.C <= 4096) e = launch_bwd<TX, TW, P, 256, 16 / P>(a, blocks, s);
     else if (a.C <= 64) e = launch_bwd<TX, TW, 1, 16, 4>(a, blocks, s);
     else if (a.C <= 512) e = launch_bwd<TX, TW, 1, 32, 16>(a, blocks, s);
     else if (a.C <= 4096) e = launch_bwd<TX, TW, 1, 256, 16>(a, blocks, s);
     else {
-        const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)sm_count() * 8);
+        const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)device_sms() * 8);
         note_launch(SGA_KERN_NORM_BWD, s, false);
         norm_bwd_wide_kernel<TX, TW><<<grid, 256, 0, s>>>(a);
         note_launch(SGA_KERN_NORM_BWD, s, true);
         if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
-        const int64_t want = std::min<int64_t>(bwd_blocks(sm_count()), (a.N + 15) / 16);
+        const int64_t want = std::min<int64_t>(bwd_blocks(device_sms()), (a.N + 15) / 16);
         const int64_t slab = (a.N + want - 1) / want;
         blocks = (int)((a.N + slab - 1) / slab);
         note_launch(SGA_KERN_NORM_BWD, s, false);
@@ -406,7 +461,7 @@ template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bo
     }
     if (e != cudaSuccess || !a.part) return e;
     note_launch(SGA_KERN_NORM_REDUCE, s, false);
-    norm_reduce_kernel<TW><<<(unsigned)((2 * (int64_t)a.C + 31) / 32), 256, 0, s>>>(a.part, blocks, a.C, dw, db);
+    norm_reduce_kernel<TW><<<(unsigned)((2 * (int64_t)a.C + 31) / 32), 1024, 0, s>>>(a.part, blocks, a.C, dw, db);
     note_launch(SGA_KERN_NORM_REDUCE, s, true);
     return cudaGetLastError();
 }
@@ -447,16 +502,20 @@ sga_status layer_norm_fwd(const void *X, const void *weight, const void *bias, i
     a.N = N;
     a.C = (int)C;
     a.eps = eps;
-    const bool vec = (C * e) % 16 == 0 && aligned(X, 16) && aligned(out, 16) && aligned(weight, 16) && aligned(bias, 16);
+    // rows on 16-byte boundaries are moved 16 bytes at a time, bf16 rows of an even width two elements at a time
+    auto fits = [&](size_t row, size_t w) {
+        return C * e % row == 0 && aligned(X, row) && aligned(out, row) && aligned(weight, w) && aligned(bias, w);
+    };
+    const bool vec = fits(16, 16), pairs = fits(4, dt == SGA_F32 ? 4 : 2 * we);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dt == SGA_F32) return status_of(norm_fwd_t<float, float>(a, vec, s));
-    if (wdt == SGA_F32) return status_of(norm_fwd_t<__nv_bfloat16, float>(a, vec, s));
-    return status_of(norm_fwd_t<__nv_bfloat16, __nv_bfloat16>(a, vec, s));
+    if (dt == SGA_F32) return status_of(norm_fwd_t<float, float>(a, vec, pairs, s));
+    if (wdt == SGA_F32) return status_of(norm_fwd_t<__nv_bfloat16, float>(a, vec, pairs, s));
+    return status_of(norm_fwd_t<__nv_bfloat16, __nv_bfloat16>(a, vec, pairs, s));
 }
 
 size_t sga_norm_bwd_workspace_bytes(int64_t N, int64_t C) {
     if (N <= 0 || C <= 0) return 0;
-    return (size_t)std::min<int64_t>(bwd_blocks(sm_count()), N) * 2 * (size_t)C * sizeof(float);
+    return (size_t)std::min<int64_t>(bwd_blocks(device_sms()), N) * 2 * (size_t)C * sizeof(float);
 }
 
 sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, const float *rstd, const void *dOut,
@@ -492,13 +551,16 @@ sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, 
     a.part = dweight ? static_cast<float *>(workspace) : nullptr;
     a.N = N;
     a.C = (int)C;
-    const bool vec = (C * e) % 16 == 0 && aligned(X, 16) && aligned(dOut, 16) && aligned(dX, 16) && aligned(weight, 16);
+    auto fits = [&](size_t row, size_t w) {
+        return C * e % row == 0 && aligned(X, row) && aligned(dOut, row) && aligned(dX, row) && aligned(weight, w);
+    };
+    const bool vec = fits(16, 16), pairs = fits(4, dt == SGA_F32 ? 4 : 2 * we);
     if (dt == SGA_F32)
-        return status_of(norm_bwd_t<float, float>(a, vec, static_cast<float *>(dweight), static_cast<float *>(dbias), s));
+        return status_of(norm_bwd_t<float, float>(a, vec, pairs, static_cast<float *>(dweight), static_cast<float *>(dbias), s));
     if (wdt == SGA_F32)
-        return status_of(norm_bwd_t<__nv_bfloat16, float>(a, vec, static_cast<float *>(dweight),
+        return status_of(norm_bwd_t<__nv_bfloat16, float>(a, vec, pairs, static_cast<float *>(dweight),
                                                           static_cast<float *>(dbias), s));
-    return status_of(norm_bwd_t<__nv_bfloat16, __nv_bfloat16>(a, vec, static_cast<__nv_bfloat16 *>(dweight),
+    return status_of(norm_bwd_t<__nv_bfloat16, __nv_bfloat16>(a, vec, pairs, static_cast<__nv_bfloat16 *>(dweight),
                                                               static_cast<__nv_bfloat16 *>(dbias), s));
 }
 

@@ -62,8 +62,8 @@ inline int64_t seq_rows_pad(int64_t rows) { return (rows + 127) / 128 * 128; }
 
 // -lse * log2(e) and -Delta of every row, head-major (seq_simt.cu)
 template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s);
-template <typename T> cudaError_t seq_fwd_simt(const SeqArgs &a, int D, cudaStream_t s);
-template <typename T> cudaError_t seq_bwd_simt(const SeqArgs &a, int D, cudaStream_t s);
+cudaError_t seq_fwd_f32(const SeqArgs &a, int D, cudaStream_t s);
+cudaError_t seq_bwd_f32(const SeqArgs &a, int D, cudaStream_t s);
 // (seq_fwd.cu, seq_bwd.cu)
 cudaError_t seq_fwd_bf16(const SeqArgs &a, int D, cudaStream_t s);
 cudaError_t seq_bwd_bf16(const SeqArgs &a, int D, cudaStream_t s);

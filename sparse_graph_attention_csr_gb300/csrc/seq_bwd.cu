@@ -3,7 +3,7 @@
 //   P = exp(S - lse), dP = dOut V^T, dS = P (dP - Delta),
 //   dV = P^T dOut, dK = scale dS^T Q, dQ = scale dS K
 //
-// Two passes, so that every output row is owned by one CTA: no atomics, no
+// Two passes (in one launch), so that every output row is owned by one CTA: no atomics, no
 // fp32 copy of dQ in memory, bitwise reproducible; S and dP are computed twice
 // (seven products a tile pair instead of five).
 //   dK/dV pass (unit: 128 keys x key head, over the query tiles that see them
@@ -63,11 +63,12 @@ template <int D> struct KvCfg : BwdCfg<D> {
 template <int D> struct QCfg : BwdCfg<D> {
     using B = BwdCfg<D>;
     static constexpr int NK = 4, NV = 3;                          // K, V tiles in flight
-    static constexpr uint32_t ST0 = 0, V0 = ST0 + NK * B::TB, BYTES = V0 + NV * B::TB;
+    static constexpr uint32_t ST0 = 0, V0 = ST0 + NK * B::TB;
+    static constexpr uint32_t BAR0 = V0 + NV * B::TB, BYTES = BAR0 + 256;   // barriers
     static constexpr uint32_t TS = 0, TP = 128, TQ = 256, TA = 384, TG = 448;   // S, dP, dQ; Q and dOut as A operands
 };
 constexpr uint32_t kMaxSmem = 227 * 1024;
-static_assert(KvCfg<128>::BYTES <= kMaxSmem && QCfg<128>::BYTES + 1024 <= 226 * 1024, "shared memory");
+static_assert(KvCfg<128>::BYTES <= kMaxSmem && QCfg<128>::BYTES <= kMaxSmem, "shared memory");
 
 // A ring of N tiles in shared memory from `base`.
 template <int N, uint32_t TB> struct Ring {
@@ -234,17 +235,9 @@ __device__ __forceinline__ uint32_t store_from_tmem(uint32_t taddr, __nv_bfloat1
 
 // ---- dK, dV -----------------------------------------------------------------------
 
-template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_kernel(const __grid_constant__ BwdParams prm) {
+template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm, unsigned char *smem, uint32_t unit) {
     using C = KvCfg<D>;
     const SeqArgs &a = prm.a;
-    // The tiles take all but a few hundred bytes of the SM's shared memory, so
-    // the barriers lie behind them and the block's memory has to begin on the
-    // tiles' alignment, as it does for a kernel without static shared memory.
-    extern __shared__ __align__(1024) unsigned char smem[];
-    if (tc::smem_u32(smem) & 1023) {
-        if (threadIdx.x == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
-        return;
-    }
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::BAR0);
     uint64_t &kv_full = bar[0], &s_full = bar[1], &dp_full = bar[2], &p_full = bar[3], &ds_full = bar[4], &acc_full = bar[5];
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(bar + 6);
@@ -255,8 +248,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
     const Ring<C::NQ, C::TB> rq{ring_full, ring_empty, sbase + C::ST0};
     const Ring<C::NG, C::TB> rg{ring_full + C::NQ, ring_empty + C::NQ, sbase + C::G0};
     const Ring<2, 1024> rr{ring_full + C::NQ + C::NG, ring_empty + C::NQ + C::NG, sbase + C::ROW0};
-    const SeqTile t = a.ktiles[blockIdx.x / a.Hkv];
-    const int hk = blockIdx.x % a.Hkv, grp = a.H / a.Hkv;
+    const SeqTile t = a.ktiles[unit / a.Hkv];
+    const int hk = unit % a.Hkv, grp = a.H / a.Hkv;
     const int nt = t.t1 - t.t0, n = nt * grp;   // steps: (head of the group, query tile)
 
     if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
@@ -460,20 +453,20 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dkdv_ker
 
 // ---- dQ ----------------------------------------------------------------------------
 
-template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kernel(const __grid_constant__ BwdParams prm) {
+template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, unsigned char *smem, uint32_t unit) {
     using C = QCfg<D>;
     const SeqArgs &a = prm.a;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem =
-        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t q_full, s_free, ring_full[C::NK + C::NV], ring_empty[C::NK + C::NV], s_full, dp_full, ds_full, acc_full;
-    __shared__ uint32_t tmem_base;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::BAR0);
+    uint64_t &q_full = bar[0], &s_full = bar[1], &s_free = bar[2], &dp_full = bar[3], &ds_full = bar[4], &acc_full = bar[5];
+    uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(bar + 6);
+    uint64_t *ring_full = bar + 7, *ring_empty = ring_full + C::NK + C::NV;
+    static_assert((7 + 2 * (C::NK + C::NV)) * 8 <= 256, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem);
     const Ring<C::NK, C::TB> rk{ring_full, ring_empty, sbase + C::ST0};
     const Ring<C::NV, C::TB> rv{ring_full + C::NK, ring_empty + C::NK, sbase + C::V0};
-    const SeqTile t = a.qtiles[blockIdx.x / a.H];
-    const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
+    const SeqTile t = a.qtiles[unit / a.H];
+    const int h = unit % a.H, hk = h / (a.H / a.Hkv);
     const int n = t.t1 - t.t0;
 
     if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
@@ -669,6 +662,22 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_dq_kerne
     }
 }
 
+// Both passes in one launch, the dK/dV units first: they are the longer ones,
+// and the dQ units fill the SMs that run out of them.  The tiles take all but a
+// few hundred bytes of an SM's shared memory, so the barriers lie behind them
+// and the block's memory has to begin on the tiles' alignment, as it does for a
+// kernel without static shared memory.
+template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_kernel(const __grid_constant__ BwdParams prm) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    if (tc::smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) atomicOr(prm.a.d_err, tc::kErrMmaTimeout);
+        return;
+    }
+    const uint32_t kv = (uint32_t)prm.a.n_tiles * prm.a.Hkv;
+    if (blockIdx.x < kv) dkdv_pass<D>(prm, smem, blockIdx.x);
+    else dq_pass<D>(prm, smem, blockIdx.x - kv);
+}
+
 template <int D> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
     BwdParams prm{};
     prm.a = a;
@@ -676,16 +685,13 @@ template <int D> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tg, a.dOut, a.rows, a.H, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tk, a.K, a.rows, a.Hkv, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tv, a.V, a.rows, a.Hkv, D);
-    if (e == cudaSuccess) e = allow_smem<seq_bwd_dkdv_kernel<D>>(KvCfg<D>::BYTES);
-    if (e == cudaSuccess) e = allow_smem<seq_bwd_dq_kernel<D>>(QCfg<D>::BYTES + 1024);
+    constexpr size_t smem = KvCfg<D>::BYTES > QCfg<D>::BYTES ? KvCfg<D>::BYTES : QCfg<D>::BYTES;
+    if (e == cudaSuccess) e = allow_smem<seq_bwd_kernel<D>>(smem);
     if (e == cudaSuccess) e = seq_row_terms<__nv_bfloat16>(a, D, s);
     if (e != cudaSuccess) return e;
-    note_launch(SGA_KERN_SEQ_BWD_DKDV, s, false);
-    seq_bwd_dkdv_kernel<D><<<(unsigned)((int64_t)a.n_tiles * a.Hkv), kThreads, KvCfg<D>::BYTES, s>>>(prm);
-    note_launch(SGA_KERN_SEQ_BWD_DKDV, s, true);
-    note_launch(SGA_KERN_SEQ_BWD_DQ, s, false);
-    seq_bwd_dq_kernel<D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, QCfg<D>::BYTES + 1024, s>>>(prm);
-    note_launch(SGA_KERN_SEQ_BWD_DQ, s, true);
+    note_launch(SGA_KERN_SEQ_BWD, s, false);
+    seq_bwd_kernel<D><<<(unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H)), kThreads, smem, s>>>(prm);
+    note_launch(SGA_KERN_SEQ_BWD, s, true);
     return cudaGetLastError();
 }
 

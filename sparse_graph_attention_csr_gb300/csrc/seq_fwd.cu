@@ -37,7 +37,7 @@ template <int D, int NS> struct FwdCfg {
     static constexpr int DP = D < 64 ? 64 : D;             // head width in shared memory and TMEM
     static constexpr int DA = DP / 64;
     static constexpr uint32_t TB = DA * 128 * 128;         // a tile of 128 rows
-    static constexpr int NST = NS == 2 ? (DP == 64 ? 8 : 5) : (DP == 64 ? 5 : 4);   // K and V tiles in flight
+    static constexpr int NST = NS == 2 ? (DP == 64 ? 8 : 5) : (DP == 64 ? 5 : 2);   // K and V tiles in flight
     static constexpr uint32_t Q0 = 0, ST0 = NS * TB;
     static constexpr uint32_t BYTES = ST0 + NST * TB;
     static constexpr int THREADS = 128 + 128 * NS;
@@ -378,7 +378,17 @@ cudaError_t seq_tensor_map(CUtensorMap *m, const void *base, int64_t rows, int h
 }
 
 cudaError_t seq_fwd_bf16(const SeqArgs &a, int D, cudaStream_t s) {
-    return D == 32 ? launch<32, 2>(a, s) : D == 64 ? launch<64, 2>(a, s) : launch<128, 2>(a, s);
+    // One row tile a CTA (two CTAs an SM) or two.  Two tiles share the key
+    // tiles' loads and give the tensor core work while one of them waits; one
+    // tile a CTA spreads few units over more SMs and ends more evenly.
+    // Measured, one : two tiles a CTA, D = 128, causal: 2048 rows, 8/2 heads
+    // (128 tiles) 31 : 35 us; 4096 (256) 54.5 : 55.7; 8192 (512) 117 : 103.
+    // D = 64: causal 4096 rows, 8 heads 43 : 48, 8192 80 : 84; full 4096 rows,
+    // 16 heads 92 : 88.
+    const bool one = (int64_t)a.n_tiles * a.H <= 2 * (int64_t)a.num_sms || (D <= 64 && a.causal);
+    if (D == 32) return one ? launch<32, 1>(a, s) : launch<32, 2>(a, s);
+    if (D == 64) return one ? launch<64, 1>(a, s) : launch<64, 2>(a, s);
+    return one ? launch<128, 1>(a, s) : launch<128, 2>(a, s);
 }
 
 }  // namespace sga

@@ -166,10 +166,11 @@ SeqArgs seq_args(const sga_seq_plan *p, float scale) {
 // there).  Setting it binds the device's context to a thread that has made no
 // runtime call yet (an autograd worker): the tensor-map encoder needs one.
 sga_status on_device(const sga_seq_plan *p) {
+    static thread_local int bound = -1;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && dev != p->device) return SGA_EINVAL;
-    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e == cudaSuccess && bound != dev && (e = cudaSetDevice(dev)) == cudaSuccess) bound = dev;
     return status_of(e);
 }
 
@@ -265,7 +266,7 @@ sga_status seq_attn_fwd(const sga_seq_plan *p, const void *Q, const void *K, con
     a.out_w = out;
     a.lse_w = lse;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(p->dt == SGA_F32 ? seq_fwd_simt<float>(a, p->D, s) : seq_fwd_bf16(a, p->D, s));
+    return status_of(p->dt == SGA_F32 ? seq_fwd_f32(a, p->D, s) : seq_fwd_bf16(a, p->D, s));
 }
 
 sga_status seq_attn_bwd(const sga_seq_plan *p, const void *Q, const void *K, const void *V, const void *out,
@@ -290,7 +291,7 @@ sga_status seq_attn_bwd(const sga_seq_plan *p, const void *Q, const void *K, con
     a.ws_nlse = static_cast<float *>(workspace);
     a.ws_ndelta = a.ws_nlse + (size_t)p->H * a.rows_pad;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(p->dt == SGA_F32 ? seq_bwd_simt<float>(a, p->D, s) : seq_bwd_bf16(a, p->D, s));
+    return status_of(p->dt == SGA_F32 ? seq_bwd_f32(a, p->D, s) : seq_bwd_bf16(a, p->D, s));
 }
 
 }  // extern "C"

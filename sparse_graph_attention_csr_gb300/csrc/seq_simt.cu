@@ -20,6 +20,7 @@
 // A pair outside a row's interval is left out of the sums, not multiplied by
 // zero: an infinity or NaN there does not reach the row.
 #include "seq.h"
+#include "tc.cuh"
 
 namespace sga {
 namespace {
@@ -32,20 +33,16 @@ template <int D> constexpr int kPitch = D + 4;
 template <int D> constexpr int kTileFloats = kT * (D + 4);
 constexpr int kScoreFloats = kT * kPP;
 
-// rows [r0, r0 + 64) of head h of a [T][heads][D] tensor; rows past `rows` read as zero
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(float *dst, const T *src, int64_t r0, int64_t rows, int heads, int h) {
-    constexpr int EL = Elt<T>::EL, CH = D / EL;
-    for (int i = threadIdx.x; i < kT * CH; i += kThreads) {
-        const int r = i / CH, c = i % CH;
-        const int64_t row = r0 + r;
-        float v[EL];
-#pragma unroll
-        for (int x = 0; x < EL; ++x) v[x] = 0.f;
-        if (row < rows) unpack<T>(ldg16(src + (row * heads + h) * D + EL * c), v);
-#pragma unroll
-        for (int x = 0; x < EL; x += 4)
-            *reinterpret_cast<float4 *>(dst + r * kPitch<D> + EL * c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+// rows [r0, r0 + 64) of head h of a [T][heads][D] tensor, asynchronously (rows
+// past `rows` as zeros)
+template <int D>
+__device__ __forceinline__ void load_tile(float *dst, const void *src, int64_t r0, int64_t rows, int heads, int h) {
+    constexpr int C4 = D / 4;
+    for (int i = threadIdx.x; i < kT * C4; i += kThreads) {
+        const int r = i / C4, c = i % C4;
+        const bool in = r0 + r < rows;
+        tc::cp16(tc::smem_u32(dst + r * kPitch<D> + 4 * c),
+                 static_cast<const float *>(src) + ((in ? r0 + r : 0) * heads + h) * D + 4 * c, in);
     }
 }
 
@@ -132,16 +129,16 @@ __device__ __forceinline__ void add_product(float (&acc)[4][kCols<D>], const flo
     }
 }
 
-template <int D, typename T>
-__device__ __forceinline__ void store_rows(T *dst, const float (&acc)[4][kCols<D>], const float (&f)[4], int64_t r0,
+template <int D>
+__device__ __forceinline__ void store_rows(float *dst, const float (&acc)[4][kCols<D>], const float (&f)[4], int64_t r0,
                                            int64_t rows, int heads, int h, int ty, int tx) {
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
         const int64_t row = r0 + ty + 16 * a;
         if (row >= rows) continue;
-        T *o = dst + (row * heads + h) * D;
+        float *o = dst + (row * heads + h) * D;
 #pragma unroll
-        for (int x = 0; x < kCols<D>; ++x) o[col_of<D>(tx, x)] = from_f32<T>(acc[a][x] * f[a]);
+        for (int x = 0; x < kCols<D>; ++x) o[col_of<D>(tx, x)] = acc[a][x] * f[a];
     }
 }
 
@@ -180,15 +177,19 @@ __device__ __forceinline__ void in_tile(const int64_t (&lo)[4], const int64_t (&
 
 // ---- forward ------------------------------------------------------------------
 
-template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_fwd_simt_kernel(const SeqArgs a) {
-    extern __shared__ float sm[];
-    float *sQ = sm, *sKV = sQ + kTileFloats<D>, *sP = sKV + kTileFloats<D>;
+template <int D> __global__ void __launch_bounds__(kThreads) seq_fwd_f32_kernel(const SeqArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    float *sQ = sm, *sK = sQ + kTileFloats<D>, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const SeqTile t = a.qtiles[blockIdx.x / a.H];
     const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
     const int64_t q0 = (int64_t)t.tile * kT;
     const float scale2 = a.scale * kLog2e;
-    load_tile<D>(sQ, static_cast<const T *>(a.Q), q0, a.rows, a.H, h);
+    load_tile<D>(sQ, a.Q, q0, a.rows, a.H, h);
+    load_tile<D>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    tc::cp_commit();
+    load_tile<D>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    tc::cp_commit();
     int64_t lo[4], hi[4];
     intervals(a, false, q0, ty, lo, hi);
     float m[4], l[4], acc[4][kCols<D>];
@@ -204,11 +205,13 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_fwd
         const bool full = kt >= t.f0 && kt < t.f1;
         int kl[4], kh[4];
         in_tile(lo, hi, k0, kl, kh);
-        __syncthreads();
-        load_tile<D>(sKV, static_cast<const T *>(a.K), k0, a.rows, a.Hkv, hk);
+        tc::cp_wait<1>();   // this K (V may be on its way)
         __syncthreads();
         float s[4][4];
-        dot_tiles<D>(s, sQ, sKV, ty, tx);
+        dot_tiles<D>(s, sQ, sK, ty, tx);
+        __syncthreads();
+        if (kt + 1 < t.t1) load_tile<D>(sK, a.K, k0 + kT, a.rows, a.Hkv, hk);   // beside the softmax and P V
+        tc::cp_commit();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float mx = -INFINITY;
@@ -232,11 +235,13 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_fwd
 #pragma unroll
             for (int x = 0; x < kCols<D>; ++x) acc[i][x] *= al;
         }
+        tc::cp_wait<1>();   // this V
         __syncthreads();
-        load_tile<D>(sKV, static_cast<const T *>(a.V), k0, a.rows, a.Hkv, hk);
+        if (full) add_product<D, false>(acc, sP, sV, ty, tx, kl, kh);
+        else add_product<D, true>(acc, sP, sV, ty, tx, kl, kh);
         __syncthreads();
-        if (full) add_product<D, false>(acc, sP, sKV, ty, tx, kl, kh);
-        else add_product<D, true>(acc, sP, sKV, ty, tx, kl, kh);
+        if (kt + 1 < t.t1) load_tile<D>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);   // beside the next scores
+        tc::cp_commit();
     }
     float inv[4];
 #pragma unroll
@@ -245,22 +250,24 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_fwd
         const int64_t row = q0 + ty + 16 * i;
         if (tx == 0 && row < a.rows) a.lse_w[row * a.H + h] = (m[i] + log2f(l[i])) * kLn2;
     }
-    store_rows<D>(static_cast<T *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+    store_rows<D>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
 }
 
 // ---- backward -------------------------------------------------------------------
 
-template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd_dq_simt_kernel(const SeqArgs a) {
-    extern __shared__ float sm[];
-    float *sQ = sm, *sG = sQ + kTileFloats<D>, *sK = sG + kTileFloats<D>, *sV = sK + kTileFloats<D>,
-          *sP = sV + kTileFloats<D>;
+template <int D> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float *sm, uint32_t unit) {
+    float *sQ = sm, *sG = sQ + kTileFloats<D>, *sV = sG + kTileFloats<D>, *sP = sV + kTileFloats<D>,
+          *sK = sP + kScoreFloats;   // two K tiles
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const SeqTile t = a.qtiles[blockIdx.x / a.H];
-    const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
+    const SeqTile t = a.qtiles[unit / a.H];
+    const int h = unit % a.H, hk = h / (a.H / a.Hkv);
     const int64_t q0 = (int64_t)t.tile * kT;
     const float scale2 = a.scale * kLog2e;
-    load_tile<D>(sQ, static_cast<const T *>(a.Q), q0, a.rows, a.H, h);
-    load_tile<D>(sG, static_cast<const T *>(a.dOut), q0, a.rows, a.H, h);
+    load_tile<D>(sQ, a.Q, q0, a.rows, a.H, h);
+    load_tile<D>(sG, a.dOut, q0, a.rows, a.H, h);
+    load_tile<D>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    load_tile<D>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    tc::cp_commit();
     int64_t lo[4], hi[4];
     intervals(a, false, q0, ty, lo, hi);
     float ls[4], dl[4], acc[4][kCols<D>];
@@ -275,15 +282,18 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
     for (int kt = t.t0; kt < t.t1; ++kt) {
         const int64_t k0 = (int64_t)kt * kT;
         const bool full = kt >= t.f0 && kt < t.f1;
+        float *sKi = sK + (kt - t.t0) % 2 * kTileFloats<D>, *sKn = sK + (kt - t.t0 + 1) % 2 * kTileFloats<D>;
         int kl[4], kh[4];
         in_tile(lo, hi, k0, kl, kh);
-        __syncthreads();
-        load_tile<D>(sK, static_cast<const T *>(a.K), k0, a.rows, a.Hkv, hk);
-        load_tile<D>(sV, static_cast<const T *>(a.V), k0, a.rows, a.Hkv, hk);
-        __syncthreads();
+        tc::cp_wait<0>();
+        __syncthreads();   // this K and V; the last dS K is done with the other K and with dS
+        if (kt + 1 < t.t1) load_tile<D>(sKn, a.K, k0 + kT, a.rows, a.Hkv, hk);
         float s[4][4], g[4][4];
-        dot_tiles<D>(s, sQ, sK, ty, tx);
         dot_tiles<D>(g, sG, sV, ty, tx);
+        __syncthreads();
+        if (kt + 1 < t.t1) load_tile<D>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);
+        tc::cp_commit();
+        dot_tiles<D>(s, sQ, sKi, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -293,24 +303,32 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
                 sP[(ty + 16 * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, ls[i])) * (g[i][c] + dl[i]) : 0.f;
             }
         __syncthreads();
-        if (full) add_product<D, false>(acc, sP, sK, ty, tx, kl, kh);
-        else add_product<D, true>(acc, sP, sK, ty, tx, kl, kh);
+        if (full) add_product<D, false>(acc, sP, sKi, ty, tx, kl, kh);
+        else add_product<D, true>(acc, sP, sKi, ty, tx, kl, kh);
     }
     const float f[4] = {a.scale, a.scale, a.scale, a.scale};
-    store_rows<D>(static_cast<T *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
+    store_rows<D>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
 }
 
-template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd_dkdv_simt_kernel(const SeqArgs a) {
-    extern __shared__ float sm[];
-    float *sK = sm, *sV = sK + kTileFloats<D>, *sQ = sV + kTileFloats<D>, *sG = sQ + kTileFloats<D>,
-          *sP = sG + kTileFloats<D>, *sS = sP + kScoreFloats;
+template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, float *sm, uint32_t unit) {
+    float *sK = sm, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>,
+          *sS = sP + kScoreFloats;   // two pairs of Q and dOut tiles
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const SeqTile t = a.ktiles[blockIdx.x / a.Hkv];
-    const int hk = blockIdx.x % a.Hkv, grp = a.H / a.Hkv;
+    const SeqTile t = a.ktiles[unit / a.Hkv];
+    const int hk = unit % a.Hkv, grp = a.H / a.Hkv;
     const int64_t k0 = (int64_t)t.tile * kT;
     const float scale2 = a.scale * kLog2e;
-    load_tile<D>(sK, static_cast<const T *>(a.K), k0, a.rows, a.Hkv, hk);
-    load_tile<D>(sV, static_cast<const T *>(a.V), k0, a.rows, a.Hkv, hk);
+    const int nt = t.t1 - t.t0, n = nt * grp;   // steps: (head of the group, query tile)
+    auto fetch = [&](int i) {
+        float *dst = sS + i % 2 * 2 * kTileFloats<D>;
+        const int64_t q0 = (int64_t)(t.t0 + i % nt) * kT;
+        load_tile<D>(dst, a.Q, q0, a.rows, a.H, hk * grp + i / nt);
+        load_tile<D>(dst + kTileFloats<D>, a.dOut, q0, a.rows, a.H, hk * grp + i / nt);
+    };
+    load_tile<D>(sK, a.K, k0, a.rows, a.Hkv, hk);
+    load_tile<D>(sV, a.V, k0, a.rows, a.Hkv, hk);
+    fetch(0);
+    tc::cp_commit();
     int64_t lo[4], hi[4];
     intervals(a, true, k0, ty, lo, hi);
     float dk[4][kCols<D>], dv[4][kCols<D>];
@@ -318,47 +336,60 @@ template <typename T, int D> __global__ void __launch_bounds__(kThreads) seq_bwd
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int x = 0; x < kCols<D>; ++x) dk[i][x] = dv[i][x] = 0.f;
-    for (int h = hk * grp; h < (hk + 1) * grp; ++h)
-        for (int qt = t.t0; qt < t.t1; ++qt) {
-            const int64_t q0 = (int64_t)qt * kT;
-            const bool full = qt >= t.f0 && qt < t.f1;
-            int ql[4], qh[4];
-            in_tile(lo, hi, q0, ql, qh);
-            __syncthreads();
-            load_tile<D>(sQ, static_cast<const T *>(a.Q), q0, a.rows, a.H, h);
-            load_tile<D>(sG, static_cast<const T *>(a.dOut), q0, a.rows, a.H, h);
-            __syncthreads();
-            float s[4][4], g[4][4], ls[4], dl[4];
-            dot_tiles<D>(s, sK, sQ, ty, tx);
-            dot_tiles<D>(g, sV, sG, ty, tx);
+    for (int step = 0; step < n; ++step) {
+        const float *sQ = sS + step % 2 * 2 * kTileFloats<D>, *sG = sQ + kTileFloats<D>;
+        const int qt = t.t0 + step % nt;
+        const int64_t q0 = (int64_t)qt * kT;
+        const bool full = qt >= t.f0 && qt < t.f1;
+        int ql[4], qh[4];
+        in_tile(lo, hi, q0, ql, qh);
+        float ls[4], dl[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int64_t r = (int64_t)(hk * grp + step / nt) * a.rows_pad + q0 + tx + 16 * c;
+            ls[c] = a.ws_nlse[r];
+            dl[c] = a.ws_ndelta[r];
+        }
+        tc::cp_wait<0>();
+        __syncthreads();   // these tiles; the last dS^T Q is done with the other ones and with dS
+        if (step + 1 < n) fetch(step + 1);
+        tc::cp_commit();
+        float s[4][4], g[4][4];
+        dot_tiles<D>(s, sK, sQ, ty, tx);
+        dot_tiles<D>(g, sV, sG, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int64_t r = (int64_t)h * a.rows_pad + q0 + tx + 16 * c;
-                ls[c] = a.ws_nlse[r];
-                dl[c] = a.ws_ndelta[r];
+                const int j = tx + 16 * c;
+                const bool on = full || (j >= ql[i] && j < qh[i]);
+                const float p = on ? fast_exp2(fmaf(s[i][c], scale2, ls[c])) : 0.f;
+                sP[(ty + 16 * i) * kPP + j] = p;
+                g[i][c] = on ? p * (g[i][c] + dl[c]) : 0.f;
             }
+        __syncthreads();
+        if (full) add_product<D, false>(dv, sP, sG, ty, tx, ql, qh);
+        else add_product<D, true>(dv, sP, sG, ty, tx, ql, qh);
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int j = tx + 16 * c;
-                    const bool on = full || (j >= ql[i] && j < qh[i]);
-                    const float p = on ? fast_exp2(fmaf(s[i][c], scale2, ls[c])) : 0.f;
-                    sP[(ty + 16 * i) * kPP + j] = p;
-                    sS[(ty + 16 * i) * kPP + j] = on ? p * (g[i][c] + dl[c]) : 0.f;
-                }
-            __syncthreads();
-            if (full) {
-                add_product<D, false>(dv, sP, sG, ty, tx, ql, qh);
-                add_product<D, false>(dk, sS, sQ, ty, tx, ql, qh);
-            } else {
-                add_product<D, true>(dv, sP, sG, ty, tx, ql, qh);
-                add_product<D, true>(dk, sS, sQ, ty, tx, ql, qh);
-            }
-        }
+            for (int c = 0; c < 4; ++c) sP[(ty + 16 * i) * kPP + tx + 16 * c] = g[i][c];   // dS^T over P^T
+        __syncthreads();
+        if (full) add_product<D, false>(dk, sP, sQ, ty, tx, ql, qh);
+        else add_product<D, true>(dk, sP, sQ, ty, tx, ql, qh);
+    }
     const float one[4] = {1.f, 1.f, 1.f, 1.f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
-    store_rows<D>(static_cast<T *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
-    store_rows<D>(static_cast<T *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
+    store_rows<D>(static_cast<float *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
+    store_rows<D>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
+}
+
+// Both passes in one launch, the dK/dV units (the longer ones) first.
+template <int D> __global__ void __launch_bounds__(kThreads) seq_bwd_f32_kernel(const SeqArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv;
+    if (blockIdx.x < kv) dkdv_pass<D>(a, sm, blockIdx.x);
+    else dq_pass<D>(a, sm, blockIdx.x - kv);
 }
 
 // Row terms: D / EL lanes of 16 bytes a (row, head).  Rows behind the last
@@ -389,28 +420,24 @@ template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_term
     }
 }
 
-template <typename T, int D> cudaError_t launch_fwd(const SeqArgs &a, cudaStream_t s) {
-    const size_t smem = sizeof(float) * (2 * kTileFloats<D> + kScoreFloats);
-    if (cudaError_t e = allow_smem<seq_fwd_simt_kernel<T, D>>(smem); e != cudaSuccess) return e;
+template <int D> cudaError_t launch_fwd(const SeqArgs &a, cudaStream_t s) {
+    constexpr size_t smem = sizeof(float) * (3 * kTileFloats<D> + kScoreFloats);
+    if (cudaError_t e = allow_smem<seq_fwd_f32_kernel<D>>(smem); e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_FWD, s, false);
-    seq_fwd_simt_kernel<T, D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, smem, s>>>(a);
+    seq_fwd_f32_kernel<D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, smem, s>>>(a);
     note_launch(SGA_KERN_SEQ_FWD, s, true);
     return cudaGetLastError();
 }
 
-template <typename T, int D> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
-    const size_t smem_q = sizeof(float) * (4 * kTileFloats<D> + kScoreFloats);
-    const size_t smem_k = sizeof(float) * (4 * kTileFloats<D> + 2 * kScoreFloats);
-    cudaError_t e = allow_smem<seq_bwd_dq_simt_kernel<T, D>>(smem_q);
-    if (e == cudaSuccess) e = allow_smem<seq_bwd_dkdv_simt_kernel<T, D>>(smem_k);
-    if (e == cudaSuccess) e = seq_row_terms<T>(a, D, s);
+template <int D> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
+    constexpr size_t smem = sizeof(float) * (6 * kTileFloats<D> + kScoreFloats);   // (dK/dV; dQ takes a tile less)
+    static_assert(smem <= 227 * 1024, "shared memory");
+    cudaError_t e = allow_smem<seq_bwd_f32_kernel<D>>(smem);
+    if (e == cudaSuccess) e = seq_row_terms<float>(a, D, s);
     if (e != cudaSuccess) return e;
-    note_launch(SGA_KERN_SEQ_BWD_DKDV, s, false);
-    seq_bwd_dkdv_simt_kernel<T, D><<<(unsigned)((int64_t)a.n_tiles * a.Hkv), kThreads, smem_k, s>>>(a);
-    note_launch(SGA_KERN_SEQ_BWD_DKDV, s, true);
-    note_launch(SGA_KERN_SEQ_BWD_DQ, s, false);
-    seq_bwd_dq_simt_kernel<T, D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, smem_q, s>>>(a);
-    note_launch(SGA_KERN_SEQ_BWD_DQ, s, true);
+    note_launch(SGA_KERN_SEQ_BWD, s, false);
+    seq_bwd_f32_kernel<D><<<(unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H)), kThreads, smem, s>>>(a);
+    note_launch(SGA_KERN_SEQ_BWD, s, true);
     return cudaGetLastError();
 }
 
@@ -430,13 +457,11 @@ template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStr
 template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t);
 template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
 
-template <typename T> cudaError_t seq_fwd_simt(const SeqArgs &a, int D, cudaStream_t s) {
-    return D == 32 ? launch_fwd<T, 32>(a, s) : D == 64 ? launch_fwd<T, 64>(a, s) : launch_fwd<T, 128>(a, s);
+cudaError_t seq_fwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
+    return D == 32 ? launch_fwd<32>(a, s) : D == 64 ? launch_fwd<64>(a, s) : launch_fwd<128>(a, s);
 }
-template <typename T> cudaError_t seq_bwd_simt(const SeqArgs &a, int D, cudaStream_t s) {
-    return D == 32 ? launch_bwd<T, 32>(a, s) : D == 64 ? launch_bwd<T, 64>(a, s) : launch_bwd<T, 128>(a, s);
+cudaError_t seq_bwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
+    return D == 32 ? launch_bwd<32>(a, s) : D == 64 ? launch_bwd<64>(a, s) : launch_bwd<128>(a, s);
 }
-template cudaError_t seq_fwd_simt<float>(const SeqArgs &, int, cudaStream_t);
-template cudaError_t seq_bwd_simt<float>(const SeqArgs &, int, cudaStream_t);
 
 }  // namespace sga
