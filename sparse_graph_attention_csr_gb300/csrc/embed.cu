@@ -142,8 +142,14 @@ __device__ void sort_tokens(const GradArgs &a, int32_t (*cnt)[kDigits], int32_t 
         int32_t *kout = a.key[(p + 1) & 1], *vout = a.tok[(p + 1) & 1];
         for (int d = lane; d < kDigits; d += 32) cnt[wp][d] = 0;
         __syncwarp();
-        for (int64_t e = w0 + lane; e < w1; e += 32)
-            atomicAdd(&cnt[wp][((p ? __ldcg(kin + e) : key_of(a, e)) >> shift) & mask], 1);
+        for (int64_t e = w0 + lane; e < w1; e += 128) {   // four keys of a lane in flight
+            int32_t k[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) k[z] = e + 32 * z < w1 ? (p ? __ldcg(kin + e + 32 * z) : key_of(a, e + 32 * z)) : -1;
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+                if (k[z] >= 0) atomicAdd(&cnt[wp][(k[z] >> shift) & mask], 1);
+        }
         __syncthreads();
         if (threadIdx.x < kDigits) {
             int32_t run = 0;
@@ -161,14 +167,24 @@ __device__ void sort_tokens(const GradArgs &a, int32_t (*cnt)[kDigits], int32_t 
             constexpr int DW = kDigits / kSortWarps;
             int32_t all[DW], before[DW];
 #pragma unroll
-            for (int k = 0; k < DW; ++k) {
-                const int32_t *h = a.hist + (int64_t)(wp * DW + k) * B;
-                all[k] = before[k] = 0;
-                for (int i = lane; i < B; i += 32) {
-                    const int32_t c = __ldcg(h + i);
-                    all[k] += c;
-                    before[k] += i < (int)blockIdx.x ? c : 0;
-                }
+            for (int k = 0; k < DW; ++k) all[k] = before[k] = 0;
+            const int32_t *h = a.hist + (int64_t)(wp * DW) * B;
+            for (int i0 = 0; i0 < B; i0 += 160) {
+                int32_t c[5][DW];
+#pragma unroll
+                for (int z = 0; z < 5; ++z)
+#pragma unroll
+                    for (int k = 0; k < DW; ++k) {
+                        const int i = i0 + 32 * z + lane;
+                        c[z][k] = i < B ? __ldcg(h + k * B + i) : 0;
+                    }
+#pragma unroll
+                for (int z = 0; z < 5; ++z)
+#pragma unroll
+                    for (int k = 0; k < DW; ++k) {
+                        all[k] += c[z][k];
+                        before[k] += i0 + 32 * z + lane < (int)blockIdx.x ? c[z][k] : 0;
+                    }
             }
 #pragma unroll
             for (int k = 0; k < DW; ++k) {
@@ -201,23 +217,31 @@ __device__ void sort_tokens(const GradArgs &a, int32_t (*cnt)[kDigits], int32_t 
         __syncthreads();
         for (int d = lane; d < kDigits; d += 32) cnt[wp][d] += scan[kSortWarps + kDigits + d];
         __syncwarp();
-        for (int64_t e0 = w0; e0 < w1; e0 += 32) {
-            const int64_t e = e0 + lane;
-            const bool valid = e < w1;
-            const int32_t k = valid ? (p ? __ldcg(kin + e) : key_of(a, e)) : 0;
-            const int32_t v = valid ? (p ? __ldcg(vin + e) : (int32_t)e) : 0;
-            const int d = valid ? (k >> shift) & mask : kDigits;
-            const unsigned peers = __match_any_sync(SGA_FULL_MASK, d);
-            const int rank = __popc(peers & ((1u << lane) - 1u));
-            int32_t pos = 0;
-            if (valid) pos = cnt[wp][d] + rank;
-            __syncwarp();
-            if (valid) {
-                kout[pos] = k;
-                vout[pos] = v;
-                if (rank == 0) cnt[wp][d] = pos + __popc(peers);
+        for (int64_t e0 = w0; e0 < w1; e0 += 128) {
+            int32_t k[4], v[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int64_t e = e0 + 32 * z + lane;
+                k[z] = e < w1 ? (p ? __ldcg(kin + e) : key_of(a, e)) : -1;
+                v[z] = e < w1 ? (p ? __ldcg(vin + e) : (int32_t)e) : 0;
             }
-            __syncwarp();
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                if (e0 + 32 * z >= w1) break;
+                const bool valid = k[z] >= 0;
+                const int d = valid ? (k[z] >> shift) & mask : kDigits;
+                const unsigned peers = __match_any_sync(SGA_FULL_MASK, d);
+                const int rank = __popc(peers & ((1u << lane) - 1u));
+                int32_t pos = 0;
+                if (valid) pos = cnt[wp][d] + rank;
+                __syncwarp();
+                if (valid) {
+                    kout[pos] = k[z];
+                    vout[pos] = v[z];
+                    if (rank == 0) cnt[wp][d] = pos + __popc(peers);
+                }
+                __syncwarp();
+            }
         }
         grid.sync();
     }
@@ -307,41 +331,78 @@ template <typename T, bool VEC, int U> __device__ __forceinline__ void sum_chunk
     }
 }
 
-// Whether chunk c0's last row begins in it and runs on; its id and last chunk.
+// Whether chunk c0's last row begins in it and runs on (the warp together): its
+// id and the last chunk that begins with it, found 32 chunks at a time.
 __device__ __forceinline__ bool runs_on(const GradArgs &a, const int32_t *key, int64_t c0, int32_t &cur, int64_t &cl) {
-    const int64_t kl = (c0 + 1) * a.L - 1;
-    if (kl + 1 >= a.N) return false;
-    cur = __ldcg(key + kl);
-    if (cur >= a.V || __ldcg(key + kl + 1) != cur) return false;
-    if (c0 > 0 && __ldcg(key + c0 * a.L - 1) == cur) return false;   // the row began in an earlier chunk
-    int64_t lo = kl + 1, hi = a.N;   // one past the row's last token: doubling steps, then halving
-    for (int64_t s = a.L; lo + s < hi; s *= 2) {
-        if (__ldcg(key + lo + s) == cur) lo += s;
-        else hi = lo + s;
+    const int lane = threadIdx.x & 31;
+    const int64_t kl = (c0 + 1) * a.L - 1;   // the chunk's last token
+    if (c0 >= a.chunks || kl + 1 >= a.N) return false;
+    const int64_t at = lane == 0 ? kl : lane == 1 ? kl + 1 : c0 > 0 ? c0 * a.L - 1 : kl;
+    const int32_t k = lane < 3 ? __ldcg(key + at) : 0;
+    cur = __shfl_sync(SGA_FULL_MASK, k, 0);
+    const int32_t next = __shfl_sync(SGA_FULL_MASK, k, 1), prev = __shfl_sync(SGA_FULL_MASK, k, 2);
+    if (cur >= a.V || next != cur || (c0 > 0 && prev == cur)) return false;   // (prev: the row began in an earlier chunk)
+    auto more = [&](int64_t stride) {   // chunks cl + stride, cl + 2 stride, .. that begin with the row: how many of 32
+        const int64_t c = cl + (lane + 1) * stride;
+        return __popc(__ballot_sync(SGA_FULL_MASK, c < a.chunks && __ldcg(key + (c < a.chunks ? c * a.L : 0)) == cur));
+    };
+    cl = c0 + 1;   // (it begins with token kl + 1)
+    int n = more(1);
+    cl += n;
+    if (n == 32) {
+        while ((n = more(32)) > 0) cl += 32 * (int64_t)n;
+        cl += more(1);
     }
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (__ldcg(key + mid) == cur) lo = mid + 1;
-        else hi = mid;
-    }
-    cl = (lo - 1) / a.L;
     return true;
 }
 
-// Partials of a column over the chunks [b, e) (slot 0), M of them in flight.
-template <int M> __device__ __forceinline__ float column_of(const GradArgs &a, int64_t b, int64_t e, int col) {
-    float s = 0.f;
+// W consecutive columns of the partials.
+template <int W> struct Cols {
+    float x[W];
+    __device__ __forceinline__ void load(const float *p) {
+        if constexpr (W == 4) {
+            const float4 q = __ldcg(reinterpret_cast<const float4 *>(p));
+            x[0] = q.x;
+            x[1] = q.y;
+            x[2] = q.z;
+            x[3] = q.w;
+        } else {
+            x[0] = __ldcg(p);
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = 0.f;
+    }
+    __device__ __forceinline__ void add(const Cols &o) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] += o.x[i];
+    }
+    template <typename T> __device__ __forceinline__ void store(T *o, float scale) const {
+#pragma unroll
+        for (int i = 0; i < W; ++i) o[i] = from_f32<T>(x[i] * scale);
+    }
+};
+
+// The partials of the chunks [b, e) (slot 0) at column `col`, M of them in flight.
+template <int W, int M> __device__ __forceinline__ Cols<W> columns_of(const GradArgs &a, int64_t b, int64_t e, int col) {
+    Cols<W> s;
+    s.zero();
     for (int64_t c = b; c < e; c += M) {
-        float v[M];
+        Cols<W> v[M];
 #pragma unroll
-        for (int z = 0; z < M; ++z) v[z] = c + z < e ? __ldcg(a.part + (c + z) * 2 * a.C + col) : 0.f;
+        for (int z = 0; z < M; ++z) {
+            v[z].zero();
+            if (c + z < e) v[z].load(a.part + (c + z) * 2 * a.C + col);
+        }
 #pragma unroll
-        for (int z = 0; z < M; ++z) s += v[z];
+        for (int z = 0; z < M; ++z) s.add(v[z]);
     }
     return s;
 }
 
-template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &a, float *sm, int64_t (*who)[3]) {
+// sm: kSortWarps * 32 * W floats.
+template <typename T, int W> __device__ __forceinline__ void join_rows(const GradArgs &a, float *sm, int64_t (*who)[3]) {
     const int32_t *key = a.key[a.passes & 1];
     T *dTable = static_cast<T *>(a.dTable);
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -350,7 +411,7 @@ template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &
         const int64_t c0 = base + (int64_t)wp * gridDim.x + blockIdx.x;
         int32_t cur = 0;
         int64_t cl = 0;
-        const bool on = c0 < a.chunks && runs_on(a, key, c0, cur, cl);
+        const bool on = runs_on(a, key, c0, cur, cl);
         const bool lng = on && cl - c0 > kLongRow;
         if (lane == 0) {
             who[wp][0] = lng ? cl : -1;
@@ -359,45 +420,40 @@ template <typename T> __device__ __forceinline__ void join_rows(const GradArgs &
         }
         const bool any = __syncthreads_or(lng);
         if (on && !lng)
-            for (int c = lane; c < a.C; c += 128) {   // four columns of a lane at a time
-                float s[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    s[z] = c + 32 * z < a.C ? __ldcg(a.part + (c0 * 2 + 1) * a.C + c + 32 * z) : 0.f;
-                for (int64_t k = c0 + 1; k <= cl; k += 2) {
-                    float v[2][4];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            v[q][z] = k + q <= cl && c + 32 * z < a.C ? __ldcg(a.part + (k + q) * 2 * a.C + c + 32 * z) : 0.f;
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) s[z] += v[0][z] + v[1][z];
-                }
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    if (c + 32 * z < a.C) dTable[(int64_t)cur * a.C + c + 32 * z] = from_f32<T>(s[z] * a.scale);
+            for (int col = lane * W; col < a.C; col += 32 * W) {
+                Cols<W> s;
+                s.load(a.part + (c0 * 2 + 1) * a.C + col);
+                s.add(columns_of<W, kLongRow / 2>(a, c0 + 1, cl + 1, col));
+                s.store(dTable + (int64_t)cur * a.C + col, a.scale);
             }
         if (!any) continue;
-        // long rows by the whole block: a warp per 32 columns and share of the chunks
-        const int cols = min(kSortWarps, (a.C + 31) / 32), shares = kSortWarps / cols, slab = wp % cols, share = wp / cols;
+        // long rows by the whole block: a warp per 32 W columns and share of the chunks
+        const int cols = min(kSortWarps, (a.C + 32 * W - 1) / (32 * W)), shares = kSortWarps / cols, slab = wp % cols,
+                  share = wp / cols;
         for (int w = 0; w < kSortWarps; ++w) {
             const int64_t l = who[w][0];
             if (l < 0) continue;   // (the same for the whole block)
             const int64_t f = who[w][1], id = who[w][2], per = (l - f + shares - 1) / shares;
-            for (int cb = 0; cb < a.C; cb += 32 * cols) {
-                const int col = cb + slab * 32 + lane;
-                float s = 0.f;
+            for (int cb = 0; cb < a.C; cb += 32 * W * cols) {
+                const int col = cb + (slab * 32 + lane) * W;
+                Cols<W> s;
+                s.zero();
                 if (col < a.C && share < shares) {
-                    if (share == 0) s = __ldcg(a.part + (f * 2 + 1) * a.C + col);
-                    s += column_of<16>(a, min(l + 1, f + 1 + share * per), min(l + 1, f + 1 + (share + 1) * per), col);
+                    s = columns_of<W, 8>(a, min(l + 1, f + 1 + share * per), min(l + 1, f + 1 + (share + 1) * per), col);
+                    if (share == 0) {
+                        Cols<W> v;
+                        v.load(a.part + (f * 2 + 1) * a.C + col);
+                        s.add(v);
+                    }
                 }
-                sm[wp * 32 + lane] = s;
+#pragma unroll
+                for (int i = 0; i < W; ++i) sm[(wp * 32 + lane) * W + i] = s.x[i];
                 __syncthreads();
                 if (share == 0 && col < a.C) {
-                    s = 0.f;
-                    for (int q = 0; q < shares; ++q) s += sm[(q * cols + slab) * 32 + lane];
-                    dTable[id * a.C + col] = from_f32<T>(s * a.scale);
+                    for (int q = 1; q < shares; ++q)
+#pragma unroll
+                        for (int i = 0; i < W; ++i) s.x[i] += sm[((q * cols + slab) * 32 + lane) * W + i];
+                    s.store(dTable + id * a.C + col, a.scale);
                 }
                 __syncthreads();
             }
@@ -420,7 +476,9 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
     sort_tokens(a, cnt, scan);
     sum_chunks<T, VEC, VEC ? 1 : 4>(a);
     cg::this_grid().sync();
-    join_rows<T>(a, reinterpret_cast<float *>(cnt), who);
+    static_assert(sizeof cnt >= kSortWarps * 32 * 4 * sizeof(float), "joins");
+    if (a.C % 4 == 0) join_rows<T, 4>(a, reinterpret_cast<float *>(cnt), who);
+    else join_rows<T, 1>(a, reinterpret_cast<float *>(cnt), who);
 }
 
 // Blocks of the gradient's launch: one an SM, fewer where that leaves them under 256 tokens.
