@@ -15,6 +15,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "tc.cuh"
 
 namespace sga {
 
@@ -181,6 +182,31 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
     }
 }
 
+// The sums of a block's groups, added one after the other in shared memory
+// (acc_sm: [2][C]), to the block's row of partials.
+template <int EL, int TPR, int NV, int THREADS>
+__device__ __forceinline__ void block_sums(const NormArgs &a, float *acc_sm, const float (&dw)[NV][EL], const float (&db)[NV][EL]) {
+    const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR, nvec = a.C / EL;
+    for (int q = 0; q < THREADS / TPR; ++q) {
+        __syncthreads();
+        if (grp == q)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = v * TPR + sub;
+                if (c >= nvec) continue;
+#pragma unroll
+                for (int i = 0; i < EL; ++i) {
+                    float *p = acc_sm + c * EL + i, *z = p + a.C;
+                    *p = (q ? *p : 0.f) + dw[v][i];
+                    *z = (q ? *z : 0.f) + db[v][i];
+                }
+            }
+    }
+    __syncthreads();
+    float *out = a.part + (int64_t)blockIdx.x * 2 * a.C;
+    for (int i = threadIdx.x; i < 2 * a.C; i += THREADS) out[i] = acc_sm[i];
+}
+
 template <typename TX, typename TW, int EL, int TPR, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
     __shared__ float red[2][32];
@@ -255,25 +281,100 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
         }
     }
     if (!a.part) return;
-    // the block's groups, one after the other
-    for (int q = 0; q < GPB; ++q) {
-        __syncthreads();
-        if (grp == q)
+    block_sums<EL, TPR, NV, THREADS>(a, acc_sm, dw, db);
+}
+
+// The backward pass for rows of whole 16-byte vectors that a warp can hold: the
+// same sums, but each thread copies its vectors of the next STAGES - 1 rows into
+// its own slots of shared memory (cp.async; nothing is shared, so there is no
+// barrier).  The loads in flight are then not bound by registers: 169343 x 512
+// bf16 takes 97 us with a row ahead in registers (128 threads, 16 warps an SM).
+constexpr int kRingThreads = 128, kRingStages = 6;
+
+template <typename TX, typename TW, int TPR, int NV>
+__global__ void __launch_bounds__(kRingThreads, 4) norm_bwd_ring_kernel(const NormArgs a) {
+    constexpr int EL = Elt<TX>::EL, GPB = kRingThreads / TPR;
+    extern __shared__ __align__(16) unsigned char ring_sm[];   // [stage][vector][x, dy][thread] 16 bytes; then [2][C] sums
+    const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+    const int nvec = a.C / EL;
+    const TX *X = static_cast<const TX *>(a.X), *dY = static_cast<const TX *>(a.dY);
+    const TW *w = static_cast<const TW *>(a.w);
+    const float inv = 1.f / (float)a.C;
+    Raw<TW, EL> wr[NV];
+    float dw[NV][EL], db[NV][EL];
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = v * TPR + sub;
-                if (c >= nvec) continue;
+    for (int v = 0; v < NV; ++v) {
+        const int c = v * TPR + sub;
+        wr[v].zero();
 #pragma unroll
-                for (int i = 0; i < EL; ++i) {
-                    float *p = acc_sm + c * EL + i, *z = p + a.C;
-                    *p = (q ? *p : 0.f) + dw[v][i];
-                    *z = (q ? *z : 0.f) + db[v][i];
-                }
-            }
+        for (int i = 0; i < EL; ++i) dw[v][i] = db[v][i] = 0.f;
+        if (c < nvec && w) wr[v].load(w + c * EL);
     }
-    __syncthreads();
-    float *out = a.part + (int64_t)blockIdx.x * 2 * a.C;
-    for (int i = threadIdx.x; i < 2 * a.C; i += THREADS) out[i] = acc_sm[i];
+    const int64_t step = (int64_t)gridDim.x * GPB, first = (int64_t)blockIdx.x * GPB + grp;
+    uint4 *slots = reinterpret_cast<uint4 *>(ring_sm) + threadIdx.x;
+    const uint32_t slot0 = tc::smem_u32(slots);
+    auto slot = [](int s, int v, int y) { return ((s * NV + v) * 2 + y) * kRingThreads; };
+    auto fetch = [&](int64_t row, int s) {
+        const bool in = row < a.N;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * TPR + sub;
+            const bool ok = in && c < nvec;
+            const int64_t at = ok ? row * a.C + c * EL : 0;
+            tc::cp16(slot0 + slot(s, v, 0) * 16, X + at, ok);
+            tc::cp16(slot0 + slot(s, v, 1) * 16, dY + at, ok);
+        }
+        tc::cp_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kRingStages - 1; ++s) fetch(first + s * step, s);
+    float mean_r = first < a.N ? a.mean_in[first] : 0.f, rstd_r = first < a.N ? a.rstd_in[first] : 0.f;
+    int s = 0;
+    // every group of a warp runs the same number of rounds: the sums are warp-wide calls
+    for (int64_t r0 = (int64_t)blockIdx.x * GPB; r0 < a.N; r0 += step) {
+        const int64_t row = r0 + grp, next = row + step;
+        const float mean = mean_r, rstd = rstd_r;
+        mean_r = next < a.N ? a.mean_in[next] : 0.f;
+        rstd_r = next < a.N ? a.rstd_in[next] : 0.f;
+        tc::cp_wait<kRingStages - 2>();
+        float x[NV][EL], g[NV][EL], sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            unpack<TX>(slots[slot(s, v, 0)], x[v]);
+            unpack<TX>(slots[slot(s, v, 1)], g[v]);
+            const bool on = row < a.N && v * TPR + sub < nvec;
+#pragma unroll
+            for (int i = 0; i < EL; ++i) {
+                x[v][i] = (x[v][i] - mean) * rstd;   // xhat
+                if (!on) continue;
+                db[v][i] += g[v][i];
+                dw[v][i] = fmaf(g[v][i], x[v][i], dw[v][i]);
+                if (w) g[v][i] *= wr[v].at(i);
+                sum[0] += g[v][i];
+                sum[1] = fmaf(g[v][i], x[v][i], sum[1]);
+            }
+        }
+        // the slot read a round ago
+        fetch(row + (kRingStages - 1) * step, s == 0 ? kRingStages - 1 : s - 1);
+        s = s + 1 == kRingStages ? 0 : s + 1;
+        row_sum<TPR, 2>(sum, nullptr);
+        if (row >= a.N) continue;
+        const float c1 = sum[0] * inv, c2 = sum[1] * inv;
+        TX *dX = static_cast<TX *>(a.dX) + row * a.C;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = v * TPR + sub;
+            if (c >= nvec) continue;
+            float o[EL];
+#pragma unroll
+            for (int i = 0; i < EL; ++i) o[i] = rstd * (g[v][i] - c1 - x[v][i] * c2);
+            store_el<TX, EL>(dX + c * EL, o);
+        }
+    }
+    tc::cp_wait<0>();
+    if (!a.part) return;
+    float *acc_sm = reinterpret_cast<float *>(ring_sm);   // (all slots are read)
+    block_sums<EL, TPR, NV, kRingThreads>(a, acc_sm, dw, db);
 }
 
 // Rows too wide for registers: a block per row, x read again (from L2) in each step.
@@ -400,6 +501,18 @@ cudaError_t launch_bwd(const NormArgs &a, int &blocks, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename TX, typename TW, int TPR, int NV> cudaError_t launch_bwd_ring(const NormArgs &a, int &blocks, cudaStream_t s) {
+    constexpr int GPB = kRingThreads / TPR;
+    blocks = (int)std::min<int64_t>((a.N + GPB - 1) / GPB, bwd_blocks(device_sms()));
+    const size_t ring = (size_t)kRingStages * NV * 2 * 16 * kRingThreads, sums = sizeof(float) * 2 * a.C;
+    const size_t smem = std::max(ring, sums);
+    if (cudaError_t e = allow_smem<norm_bwd_ring_kernel<TX, TW, TPR, NV>>(smem); e != cudaSuccess) return e;
+    note_launch(SGA_KERN_NORM_BWD, s, false);
+    norm_bwd_ring_kernel<TX, TW, TPR, NV><<<(unsigned)blocks, kRingThreads, smem, s>>>(a);
+    note_launch(SGA_KERN_NORM_BWD, s, true);
+    return cudaGetLastError();
+}
+
 // Threads of a row by its number of 16-byte vectors (or of elements, where the
 // width or an address is no multiple of 16 bytes).  Two vectors a thread where
 // a warp can hold the row: of 1048576 x 256 bf16, 172 us (6.2 TB/s) with two,
@@ -434,10 +547,10 @@ template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bo
     const int nv = a.C / EL;
     int blocks = 0;
     cudaError_t e;
-    if (vec && nv <= 8) e = launch_bwd<TX, TW, EL, 4, 2>(a, blocks, s);
-    else if (vec && nv <= 16) e = launch_bwd<TX, TW, EL, 8, 2>(a, blocks, s);
-    else if (vec && nv <= 32) e = launch_bwd<TX, TW, EL, 16, 2>(a, blocks, s);
-    else if (vec && nv <= 64) e = launch_bwd<TX, TW, EL, 32, 2>(a, blocks, s);
+    if (vec && nv <= 8) e = launch_bwd_ring<TX, TW, 4, 2>(a, blocks, s);
+    else if (vec && nv <= 16) e = launch_bwd_ring<TX, TW, 8, 2>(a, blocks, s);
+    else if (vec && nv <= 32) e = launch_bwd_ring<TX, TW, 16, 2>(a, blocks, s);
+    else if (vec && nv <= 64) e = launch_bwd_ring<TX, TW, 32, 2>(a, blocks, s);
     else if (vec && nv <= 512) e = launch_bwd<TX, TW, EL, 256, 2>(a, blocks, s);
     else if (pairs && a.C <= 64) e = launch_bwd<TX, TW, P, 8, 8 / P>(a, blocks, s);
     else if (pairs && a.C <= 512) e = launch_bwd<TX, TW, P, 32, 16 / P>(a, blocks, s);

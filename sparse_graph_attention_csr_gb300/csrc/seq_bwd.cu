@@ -29,6 +29,7 @@
 // Every wait is bounded; a timeout sets the plan's error word and ends the role.
 #include <algorithm>
 
+#include "seq_rows.cuh"
 #include "seq_tc.cuh"
 
 namespace sga {
@@ -141,78 +142,6 @@ __device__ __forceinline__ void store_weights(uint32_t taddr, const float *p) {
     for (int c = 0; c < N; c += 2) pk[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
     tc::tmem_st32_async(taddr, pk);
     tc::tmem_wait_st();
-}
-
-template <int D> struct RowFrag {
-    static constexpr int W = D / 32;
-    float x[W];
-    __device__ __forceinline__ void load(const void *base, int64_t off) {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(base) + off + (threadIdx.x & 31) * W;
-#pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = __bfloat162float(p[i]);
-    }
-    __device__ __forceinline__ float dot(const RowFrag &o) const {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) s = fmaf(x[i], o.x[i], s);
-        return group_sum<32>(s);
-    }
-    // store the columns [c0, c1)
-    __device__ __forceinline__ void store(void *base, int64_t off, float f, int c0, int c1) const {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const int c = (threadIdx.x & 31) * W + i;
-            if (c >= c0 && c < c1) static_cast<__nv_bfloat16 *>(base)[off + c] = __float2bfloat16_rn(x[i] * f);
-        }
-    }
-};
-
-// Columns [c0, c0 + 32) of dK (DK) or dV of one key row by its warp, over the
-// queries [lo, hi) alone.
-template <int D>
-__device__ __forceinline__ void key_row_alone(const SeqArgs &a, bool DK, int64_t row, int hk, int64_t lo, int64_t hi,
-                                              int c0) {
-    RowFrag<D> k, v, acc;
-    const int64_t at = (row * a.Hkv + hk) * D;
-    k.load(a.K, at);
-    v.load(a.V, at);
-#pragma unroll
-    for (int i = 0; i < RowFrag<D>::W; ++i) acc.x[i] = 0.f;
-    const int grp = a.H / a.Hkv;
-    for (int h = hk * grp; h < (hk + 1) * grp; ++h)
-        for (int64_t r = lo; r < hi; ++r) {
-            RowFrag<D> q, g;
-            q.load(a.Q, (r * a.H + h) * D);
-            g.load(a.dOut, (r * a.H + h) * D);
-            const int64_t t = (int64_t)h * a.rows_pad + r;
-            const float p = fast_exp2(fmaf(q.dot(k), a.scale * kLog2e, a.ws_nlse[t]));
-            const float w = DK ? p * (g.dot(v) + a.ws_ndelta[t]) : p;
-#pragma unroll
-            for (int i = 0; i < RowFrag<D>::W; ++i) acc.x[i] = fmaf(w, DK ? q.x[i] : g.x[i], acc.x[i]);
-        }
-    acc.store(DK ? a.dK : a.dV, at, DK ? a.scale : 1.f, c0, c0 + 32);
-}
-
-// Columns [c0, c0 + 32) of dQ of one query row by its warp, over the keys [lo, hi) alone.
-template <int D>
-__device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, int h, int64_t lo, int64_t hi, int c0) {
-    RowFrag<D> q, g, acc;
-    const int64_t at = (row * a.H + h) * D, t = (int64_t)h * a.rows_pad + row;
-    const int hk = h / (a.H / a.Hkv);
-    q.load(a.Q, at);
-    g.load(a.dOut, at);
-#pragma unroll
-    for (int i = 0; i < RowFrag<D>::W; ++i) acc.x[i] = 0.f;
-    for (int64_t j = lo; j < hi; ++j) {
-        RowFrag<D> k, v;
-        k.load(a.K, (j * a.Hkv + hk) * D);
-        v.load(a.V, (j * a.Hkv + hk) * D);
-        const float p = fast_exp2(fmaf(q.dot(k), a.scale * kLog2e, a.ws_nlse[t]));
-        const float w = p * (g.dot(v) + a.ws_ndelta[t]);
-#pragma unroll
-        for (int i = 0; i < RowFrag<D>::W; ++i) acc.x[i] = fmaf(w, k.x[i], acc.x[i]);
-    }
-    acc.store(a.dQ, at, a.scale, c0, c0 + 32);
 }
 
 // 32 columns of a row from TMEM, scaled, to bf16 at dst (if `in`); the lanes
@@ -434,8 +363,8 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;
-                    key_row_alone<D>(a, dk, __shfl_sync(SGA_FULL_MASK, row, src), hk, __shfl_sync(SGA_FULL_MASK, lo, src),
-                                     __shfl_sync(SGA_FULL_MASK, hi, src), c0);
+                    seq::key_row_alone<__nv_bfloat16, D>(a, dk, __shfl_sync(SGA_FULL_MASK, row, src), hk, __shfl_sync(SGA_FULL_MASK, lo, src),
+                                     __shfl_sync(SGA_FULL_MASK, hi, src), c0, 32);
                 }
             }
         } else if (lane == 0) {
@@ -645,8 +574,8 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;
-                    query_row_alone<D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, __shfl_sync(SGA_FULL_MASK, lo, src),
-                                       __shfl_sync(SGA_FULL_MASK, hi, src), c0);
+                    seq::query_row_alone<__nv_bfloat16, D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, __shfl_sync(SGA_FULL_MASK, lo, src),
+                                       __shfl_sync(SGA_FULL_MASK, hi, src), c0, 32);
                 }
             }
         } else if (lane == 0) {

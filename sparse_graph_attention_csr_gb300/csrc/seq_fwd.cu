@@ -27,6 +27,7 @@
 // Every wait is bounded; a timeout sets the plan's error word and ends the role.
 #include <algorithm>
 
+#include "seq_rows.cuh"
 #include "seq_tc.cuh"
 #include "tc_dx.cuh"
 
@@ -54,37 +55,6 @@ struct FwdParams {
     SeqArgs a;
     int pair_heads;   // NS = 2: the two tiles are two heads of one row tile
 };
-
-// One query row by its warp, over the keys [lo, hi) alone.
-template <int D>
-__device__ __forceinline__ void row_alone(const SeqArgs &a, int64_t row, int h, int hk, int64_t lo, int64_t hi) {
-    constexpr int W = D / 32;
-    const int lane = threadIdx.x & 31;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.Q) + (row * a.H + h) * D + lane * W;
-    float x[W], acc[W], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        x[i] = __bfloat162float(q[i]) * (a.scale * kLog2e);
-        acc[i] = 0.f;
-    }
-    for (int64_t j = lo; j < hi; ++j) {
-        const int64_t off = (j * a.Hkv + hk) * D + lane * W;
-        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.K) + off,
-                            *v = static_cast<const __nv_bfloat16 *>(a.V) + off;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) s = fmaf(x[i], __bfloat162float(k[i]), s);
-        s = group_sum<32>(s);
-        const float mn = fmaxf(m, s), al = exp2_diff(m, mn), p = exp2_diff(s, mn);
-        l = fmaf(l, al, p);
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] = fmaf(p, __bfloat162float(v[i]), acc[i] * al);
-    }
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out_w) + (row * a.H + h) * D + lane * W;
-#pragma unroll
-    for (int i = 0; i < W; ++i) o[i] = __float2bfloat16_rn(acc[i] / l);
-}
 
 template <int D, int NS>
 __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
@@ -326,7 +296,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
-                row_alone<D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, hk, __shfl_sync(SGA_FULL_MASK, lo, src),
+                seq::out_row_alone<__nv_bfloat16, D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, hk, __shfl_sync(SGA_FULL_MASK, lo, src),
                              __shfl_sync(SGA_FULL_MASK, hi, src));
             }
             tc::fence_before_sync();

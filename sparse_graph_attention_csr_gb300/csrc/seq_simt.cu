@@ -17,9 +17,10 @@
 //     K Q^T, dP^T = V dOut^T, dV += P^T dOut, dK += dS^T Q.
 // The scores are computed twice in the backward pass so that every output row
 // is owned by one block: no atomics, bitwise reproducible.
-// A pair outside a row's interval is left out of the sums, not multiplied by
-// zero: an infinity or NaN there does not reach the row.
-#include "seq.h"
+// A row whose result is not finite is computed again over its own interval alone
+// (seq_rows.cuh).  Leaving masked pairs out of every sum instead, with a test a
+// pair, took twice the time on tiles with a mask (512 rows, D = 32).
+#include "seq_rows.cuh"
 #include "tc.cuh"
 
 namespace sga {
@@ -99,11 +100,9 @@ template <int D> __device__ __forceinline__ void load_cols(float (&v)[kCols<D>],
     }
 }
 
-// acc[a][x] += sum_j P[ty + 16 a][j] B[j][col x] over the 64 rows of B, with
-// MASKED over those in [lo[a], hi[a]) only
-template <int D, bool MASKED>
-__device__ __forceinline__ void add_product(float (&acc)[4][kCols<D>], const float *P, const float *B, int ty, int tx,
-                                            const int (&lo)[4], const int (&hi)[4]) {
+// acc[a][x] += sum_j P[ty + 16 a][j] B[j][col x] over the 64 rows of B
+template <int D>
+__device__ __forceinline__ void add_product(float (&acc)[4][kCols<D>], const float *P, const float *B, int ty, int tx) {
     constexpr int NC = kCols<D>;
 #pragma unroll 2
     for (int j = 0; j < kT; j += 4) {
@@ -115,30 +114,42 @@ __device__ __forceinline__ void add_product(float (&acc)[4][kCols<D>], const flo
             float v[NC];
             load_cols<D>(v, B + (j + u) * kPitch<D>, tx);
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const float w = u == 0 ? p[a].x : u == 1 ? p[a].y : u == 2 ? p[a].z : p[a].w;
-                if (MASKED) {
-                    if (j + u >= lo[a] && j + u < hi[a])
-#pragma unroll
-                        for (int x = 0; x < NC; ++x) acc[a][x] = fmaf(w, v[x], acc[a][x]);
-                } else {
-                    axpy2<NC>(acc[a], w, v);
-                }
-            }
+            for (int a = 0; a < 4; ++a) axpy2<NC>(acc[a], u == 0 ? p[a].x : u == 1 ? p[a].y : u == 2 ? p[a].z : p[a].w, v);
         }
     }
 }
 
+// Stores the rows, scaled, and returns whether any element of this thread's row
+// a was not finite, as bit a.
 template <int D>
-__device__ __forceinline__ void store_rows(float *dst, const float (&acc)[4][kCols<D>], const float (&f)[4], int64_t r0,
-                                           int64_t rows, int heads, int h, int ty, int tx) {
+__device__ __forceinline__ uint32_t store_rows(float *dst, const float (&acc)[4][kCols<D>], const float (&f)[4], int64_t r0,
+                                               int64_t rows, int heads, int h, int ty, int tx) {
+    uint32_t bad = 0;
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
         const int64_t row = r0 + ty + 16 * a;
         if (row >= rows) continue;
         float *o = dst + (row * heads + h) * D;
 #pragma unroll
-        for (int x = 0; x < kCols<D>; ++x) o[col_of<D>(tx, x)] = acc[a][x] * f[a];
+        for (int x = 0; x < kCols<D>; ++x) {
+            const float y = acc[a][x] * f[a];
+            o[col_of<D>(tx, x)] = y;
+            if (!(fabsf(y) < INFINITY)) bad |= 1u << a;
+        }
+    }
+    return bad;
+}
+
+// Calls redo(a, half) for every row (ty + 16 a of the warp's half) of which a
+// thread found an element that is not finite; the warp together, after its stores.
+template <typename F> __device__ __forceinline__ void each_bad_row(uint32_t bad, F redo) {
+    if (!__any_sync(SGA_FULL_MASK, bad != 0)) return;
+    __syncwarp();
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const uint32_t who = __ballot_sync(SGA_FULL_MASK, (bad >> a) & 1u);
+        for (int half = 0; half < 2; ++half)
+            if ((who >> (16 * half)) & 0xffffu) redo(a, half);
     }
 }
 
@@ -237,8 +248,7 @@ template <int D> __global__ void __launch_bounds__(kThreads) seq_fwd_f32_kernel(
         }
         tc::cp_wait<1>();   // this V
         __syncthreads();
-        if (full) add_product<D, false>(acc, sP, sV, ty, tx, kl, kh);
-        else add_product<D, true>(acc, sP, sV, ty, tx, kl, kh);
+        add_product<D>(acc, sP, sV, ty, tx);
         __syncthreads();
         if (kt + 1 < t.t1) load_tile<D>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);   // beside the next scores
         tc::cp_commit();
@@ -250,7 +260,11 @@ template <int D> __global__ void __launch_bounds__(kThreads) seq_fwd_f32_kernel(
         const int64_t row = q0 + ty + 16 * i;
         if (tx == 0 && row < a.rows) a.lse_w[row * a.H + h] = (m[i] + log2f(l[i])) * kLn2;
     }
-    store_rows<D>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+    const uint32_t bad = store_rows<D>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+    each_bad_row(bad, [&](int i, int half) {
+        seq::out_row_alone<float, D>(a, q0 + (ty & ~1) + half + 16 * i, h, hk, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
+                                     __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half));
+    });
 }
 
 // ---- backward -------------------------------------------------------------------
@@ -303,11 +317,14 @@ template <int D> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float
                 sP[(ty + 16 * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, ls[i])) * (g[i][c] + dl[i]) : 0.f;
             }
         __syncthreads();
-        if (full) add_product<D, false>(acc, sP, sKi, ty, tx, kl, kh);
-        else add_product<D, true>(acc, sP, sKi, ty, tx, kl, kh);
+        add_product<D>(acc, sP, sKi, ty, tx);
     }
     const float f[4] = {a.scale, a.scale, a.scale, a.scale};
-    store_rows<D>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
+    const uint32_t bad = store_rows<D>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
+    each_bad_row(bad, [&](int i, int half) {
+        seq::query_row_alone<float, D>(a, q0 + (ty & ~1) + half + 16 * i, h, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
+                                       __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
+    });
 }
 
 template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, float *sm, uint32_t unit) {
@@ -368,20 +385,24 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, flo
                 g[i][c] = on ? p * (g[i][c] + dl[c]) : 0.f;
             }
         __syncthreads();
-        if (full) add_product<D, false>(dv, sP, sG, ty, tx, ql, qh);
-        else add_product<D, true>(dv, sP, sG, ty, tx, ql, qh);
+        add_product<D>(dv, sP, sG, ty, tx);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sP[(ty + 16 * i) * kPP + tx + 16 * c] = g[i][c];   // dS^T over P^T
         __syncthreads();
-        if (full) add_product<D, false>(dk, sP, sQ, ty, tx, ql, qh);
-        else add_product<D, true>(dk, sP, sQ, ty, tx, ql, qh);
+        add_product<D>(dk, sP, sQ, ty, tx);
     }
     const float one[4] = {1.f, 1.f, 1.f, 1.f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
-    store_rows<D>(static_cast<float *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
-    store_rows<D>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
+    const uint32_t bad_v = store_rows<D>(static_cast<float *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
+    const uint32_t bad_k = store_rows<D>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
+    for (int x = 0; x < 2; ++x)
+        each_bad_row(x ? bad_k : bad_v, [&](int i, int half) {
+            seq::key_row_alone<float, D>(a, x == 1, k0 + (ty & ~1) + half + 16 * i, hk,
+                                         __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
+                                         __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
+        });
 }
 
 // Both passes in one launch, the dK/dV units (the longer ones) first.
