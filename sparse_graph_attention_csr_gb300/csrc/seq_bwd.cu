@@ -231,31 +231,32 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
         } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128), idesc_g = tc::idesc_bf16(128, C::DP) | tc::kMajorMnB;
             const uint32_t ka = sbase + C::R0, va = ka + C::TB;
-            auto scores = [&](int i) -> bool {   // S^T = K Q^T
-                if (!rq.wait_filled(i)) return false;
-                tc::fence_after_sync();
+            auto scores = [&](int i) {   // S^T = K Q^T
                 mma_over_d<C::DP>(tS, ka, rq.at(i), idesc_s);
                 tc::mma_commit_w(&s_full);
-                return true;
             };
-            auto dprod = [&](int i) -> bool {    // dP^T = V dOut^T
-                if (!rg.wait_filled(i)) return false;
-                tc::fence_after_sync();
+            auto dprod = [&](int i) {    // dP^T = V dOut^T
                 mma_over_d<C::DP>(tP, va, rg.at(i), idesc_s);
                 tc::mma_commit_w(&dp_full);
-                return true;
             };
-            bool ok = tc::warp_wait(&kv_full, 0, tc::kWaitLimit) && scores(0) && dprod(0);
+            bool ok = tc::warp_wait(&kv_full, 0, tc::kWaitLimit) && rq.wait_filled(0) && rg.wait_filled(0);
+            if (ok) {
+                tc::fence_after_sync();
+                scores(0);
+                dprod(0);
+            }
             for (int i = 0; i < n && ok; ++i) {
-                if (!tc::warp_wait(&p_full, i & 1, tc::kWaitLimit)) {
+                // the next tiles have landed; their barriers are polled while the weights are formed
+                if ((i + 1 < n && !(rq.wait_filled(i + 1) && rg.wait_filled(i + 1))) ||
+                    !tc::warp_wait(&p_full, i & 1, tc::kWaitLimit)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after_sync();
                 mma_rows128(tV, tS, rg.at(i), idesc_g, i == 0);   // dV += P^T dOut
                 tc::mma_commit_w(rg.freed(i));
-                if (i + 1 < n && !scores(i + 1)) ok = false;
-                if (!ok || !tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) {
+                if (i + 1 < n) scores(i + 1);
+                if (!tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) {
                     ok = false;
                     break;
                 }
@@ -263,7 +264,7 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
                 mma_rows128(tK, tP, rq.at(i), idesc_g, i == 0);   // dK += dS^T Q
                 tc::mma_commit_w(rq.freed(i));
                 tc::mma_commit_w(rr.freed(i));   // (read before dS arrived)
-                if (i + 1 < n && !dprod(i + 1)) ok = false;
+                if (i + 1 < n) dprod(i + 1);
             }
             if (!ok && lane == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // every product issued is complete before TMEM is released
@@ -442,24 +443,31 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
             rv.drain(v);
         } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
             constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128), idesc_g = tc::idesc_bf16(128, C::DP) | tc::kMajorMnB;
-            auto scores = [&](int i) -> bool {
-                if (!rk.wait_filled(i)) return false;
-                tc::fence_after_sync();
+            auto scores = [&](int i) {
                 mma_over_d_ts<C::DP>(tS, tA, rk.at(i), idesc_s);
                 tc::mma_commit_w(&s_full);
-                return true;
             };
-            auto dprod = [&](int i) -> bool {
-                if (!rv.wait_filled(i)) return false;
-                tc::fence_after_sync();
+            auto dprod = [&](int i) {
                 mma_over_d_ts<C::DP>(tP, tG, rv.at(i), idesc_s);
                 tc::mma_commit_w(&dp_full);
                 tc::mma_commit_w(rv.freed(i));
-                return true;
             };
-            bool ok = tc::warp_wait(&q_full, 0, tc::kWaitLimit) && scores(0) && dprod(0);
+            bool ok = tc::warp_wait(&q_full, 0, tc::kWaitLimit) && rk.wait_filled(0) && rv.wait_filled(0);
+            if (ok) {
+                tc::fence_after_sync();
+                scores(0);
+                dprod(0);
+            }
             for (int i = 0; i < n && ok; ++i) {
-                if (i + 1 < n && (!tc::warp_wait(&s_free, i & 1, tc::kWaitLimit) || !scores(i + 1))) ok = false;
+                if (i + 1 < n) {   // (the next V has landed; its barrier is polled while dS is formed)
+                    if (!rk.wait_filled(i + 1) || !tc::warp_wait(&s_free, i & 1, tc::kWaitLimit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    scores(i + 1);
+                    ok = rv.wait_filled(i + 1);
+                }
                 if (!ok || !tc::warp_wait(&ds_full, i & 1, tc::kWaitLimit)) {
                     ok = false;
                     break;
@@ -467,7 +475,7 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
                 tc::fence_after_sync();
                 mma_rows128(tQ, tP, rk.at(i), idesc_g, i == 0);   // dQ += dS K
                 tc::mma_commit_w(rk.freed(i));
-                if (i + 1 < n && !dprod(i + 1)) ok = false;
+                if (i + 1 < n) dprod(i + 1);
             }
             if (!ok && lane == 0) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // every product issued is complete before TMEM is released

@@ -139,8 +139,9 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             }
             auto issue_pv = [&](int s) -> bool {   // O(s) += P(s) V(pend[s])
                 const int e = 2 * pend[s] + 1, b = e % C::NST;
-                if (!tc::warp_wait(&p_full[s], np[s] & 1, tc::kWaitLimit) ||
-                    !tc::warp_wait(&kv_full[b], (e / C::NST) & 1, tc::kWaitLimit))
+                // (V first: it has landed, and the poll is done while P is formed)
+                if (!tc::warp_wait(&kv_full[b], (e / C::NST) & 1, tc::kWaitLimit) ||
+                    !tc::warp_wait(&p_full[s], np[s] & 1, tc::kWaitLimit))
                     return false;
                 tc::fence_after_sync();
                 const uint32_t va = sbase + C::ST0 + b * C::TB;

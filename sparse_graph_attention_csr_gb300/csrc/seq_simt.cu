@@ -413,31 +413,39 @@ template <int D> __global__ void __launch_bounds__(kThreads) seq_bwd_f32_kernel(
     else dq_pass<D>(a, sm, blockIdx.x - kv);
 }
 
-// Row terms: D / EL lanes of 16 bytes a (row, head).  Rows behind the last
-// sequence (to the end of its tile) get -lse = -inf, so that their weights are
-// zero, and Delta = 0.
+// Row terms: D / EL lanes of 16 bytes a (row, head), four of them in flight.
+// Rows behind the last sequence (to the end of its tile) get -lse = -inf, so
+// that their weights are zero, and Delta = 0.
+constexpr int kTerms = 4;
 template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
-    constexpr int EL = Elt<T>::EL, L = D / EL;
-    const int64_t g = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+    constexpr int EL = Elt<T>::EL, L = D / EL, G = 256 / L;   // G items of a block at a time
     const int sub = threadIdx.x % L;
-    const int64_t row = g / a.H;
-    const int h = (int)(g % a.H);
-    if (row >= a.rows_pad) return;   // whole warps: rows_pad * H * L is a multiple of 32
-    float d = 0.f;
-    const bool in = row < a.rows;
-    if (in) {
-        const int64_t off = (row * a.H + h) * D + sub * EL;
-        float x[EL], y[EL];
-        unpack<T>(ldg16(static_cast<const T *>(a.out) + off), x);
-        unpack<T>(ldg16(static_cast<const T *>(a.dOut) + off), y);
+    const int64_t n = a.rows_pad * a.H, g0 = (int64_t)blockIdx.x * (G * kTerms) + threadIdx.x / L;
+    uint4 x[kTerms], y[kTerms];
 #pragma unroll
-        for (int i = 0; i < EL; ++i) d = fmaf(x[i], y[i], d);
+    for (int k = 0; k < kTerms; ++k) {
+        const int64_t g = g0 + k * G;
+        x[k] = y[k] = make_uint4(0, 0, 0, 0);
+        if (g < a.rows * a.H) {   // (an item's elements follow the one's before)
+            x[k] = ldg16(static_cast<const T *>(a.out) + g * D + sub * EL);
+            y[k] = ldg16(static_cast<const T *>(a.dOut) + g * D + sub * EL);
+        }
     }
-    d = group_sum<L>(d);
-    if (sub == 0) {
-        const int64_t at = (int64_t)h * a.rows_pad + row;
-        a.ws_nlse[at] = in ? -(a.lse[row * a.H + h] * kLog2e) : -INFINITY;
-        a.ws_ndelta[at] = in ? -d : 0.f;
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) {
+        const int64_t g = g0 + k * G;
+        float u[EL], v[EL], d = 0.f;
+        unpack<T>(x[k], u);
+        unpack<T>(y[k], v);
+#pragma unroll
+        for (int i = 0; i < EL; ++i) d = fmaf(u[i], v[i], d);
+        d = group_sum<L>(d);
+        if (sub == 0 && g < n) {
+            const int64_t row = g / a.H, at = (g % a.H) * a.rows_pad + row;
+            const bool in = row < a.rows;
+            a.ws_nlse[at] = in ? -(a.lse[g] * kLog2e) : -INFINITY;
+            a.ws_ndelta[at] = in ? -d : 0.f;
+        }
     }
 }
 
@@ -463,9 +471,9 @@ template <int D> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
 }
 
 template <typename T, int D> cudaError_t launch_terms(const SeqArgs &a, cudaStream_t s) {
-    const int64_t threads = a.rows_pad * a.H * (D / Elt<T>::EL);
+    constexpr int per = kTerms * 256 / (D / Elt<T>::EL);   // items of a block
     note_launch(SGA_KERN_SEQ_BWD_ROWS, s, false);
-    seq_row_terms_kernel<T, D><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(a);
+    seq_row_terms_kernel<T, D><<<(unsigned)((a.rows_pad * a.H + per - 1) / per), 256, 0, s>>>(a);
     note_launch(SGA_KERN_SEQ_BWD_ROWS, s, true);
     return cudaGetLastError();
 }

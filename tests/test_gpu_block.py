@@ -1,0 +1,107 @@
+"""The dense operators and the edge attention as a model uses them: token
+embedding -> norm -> (edge attention over the graph + attention over the whole
+graph) -> norm, with gradients to every parameter, against the same model in
+64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import sparse_graph_attention_csr_gb300 as sga
+
+pytestmark = pytest.mark.gpu
+
+LENS, V, H, HK, D = [37, 1, 70, 0, 130, 12], 23, 4, 2, 32
+C = H * D
+
+
+def batch(seed=0):
+    """Random graphs, one behind the other: node tokens, CSR over all nodes, sequence pointers."""
+    rng = np.random.default_rng(seed)
+    ptr = np.concatenate([[0], np.cumsum(LENS)])
+    rows = [np.sort(rng.integers(b, e, rng.integers(1, 6))) for b, e in zip(ptr[:-1], ptr[1:]) for _ in range(e - b)]
+    indptr = np.concatenate([[0], np.cumsum([len(r) for r in rows])]).astype(np.int32)
+    cu = lambda x, t=torch.int32: torch.as_tensor(np.asarray(x), dtype=t, device="cuda")
+    return cu(rng.integers(0, V, ptr[-1]), torch.int64), cu(indptr), cu(np.concatenate(rows)), cu(ptr)
+
+
+def parameters(dtype):
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)
+    p = {"table": r(V, C) * 0.3, "w1": 1 + 0.1 * r(C), "b1": 0.1 * r(C), "w2": 1 + 0.1 * r(C), "b2": 0.1 * r(C),
+         "Wq": r(C, C) / C ** 0.5, "Wk": r(C, HK * D) / C ** 0.5, "Wv": r(C, HK * D) / C ** 0.5,
+         "Wl": r(C, 3 * C) / C ** 0.5}
+    return {n: t.to("cuda", dtype).requires_grad_() for n, t in p.items()}
+
+
+def model(p, ids, seq_plan, plan):
+    x = sga.Embedding.apply(ids, p["table"], C ** 0.5)
+    y = sga.LayerNorm.apply(x, p["w1"], p["b1"])
+    T = ids.numel()
+    q, k, v = (y @ p[n] for n in ("Wq", "Wk", "Wv"))
+    whole = sga.SeqAttention.apply(q.view(T, H, D), k.view(T, HK, D), v.view(T, HK, D), seq_plan)
+    lq, lk, lv = (t.reshape(T, H, D) for t in (y @ p["Wl"]).split(C, 1))
+    local = sga.GTAttention.apply(lq, lk, lv, plan)
+    return sga.LayerNorm.apply(x + whole.reshape(T, C) + local.reshape(T, C), p["w2"], p["b2"])
+
+
+def model64(p, ids, indptr, indices, ptr):
+    x = p["table"][ids] * C ** 0.5
+    norm = lambda t, w, b: torch.nn.functional.layer_norm(t, (C,), w, b, 1e-5)
+    y = norm(x, p["w1"], p["b1"])
+    T = ids.numel()
+    seq = torch.searchsorted(ptr.long(), torch.arange(T, device="cuda"), right=True)
+    same = seq[:, None] == seq[None]
+    edges = torch.zeros(T, T, dtype=torch.float64, device="cuda")   # how often an edge is listed
+    dst = torch.repeat_interleave(torch.arange(T, device="cuda"), (indptr[1:] - indptr[:-1]).long())
+    edges.index_put_((dst, indices.long()), torch.ones(len(dst), dtype=torch.float64, device="cuda"), accumulate=True)
+
+    def attend(q, k, v, count):
+        k, v = (t.repeat_interleave(H // t.shape[1], 1) for t in (k, v))
+        e = torch.exp(torch.einsum("ihd,jhd->hij", q, k) / D ** 0.5) * count
+        return torch.einsum("hij,jhd->ihd", e / e.sum(-1, keepdim=True), v).reshape(T, C)
+
+    whole = attend((y @ p["Wq"]).view(T, H, D), (y @ p["Wk"]).view(T, HK, D), (y @ p["Wv"]).view(T, HK, D), same.double())
+    local = attend(*(t.reshape(T, H, D) for t in (y @ p["Wl"]).split(C, 1)), edges)
+    return norm(x + whole + local, p["w2"], p["b2"])
+
+
+def test_a_layer_and_its_gradients():
+    """fp32 throughout.  Each operator is within about (sum's length) 2^-24 of
+    its terms (their own tests); a few hundred terms and some ten stages, whose
+    errors enter the gradients twice, stay under 2 x 10 x 400 x 2^-24 = 5e-4 of
+    a tensor's norm, and the products in between add as much."""
+    ids, indptr, indices, ptr = batch()
+    tf32 = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = False
+    try:
+        p, p64 = parameters(torch.float32), parameters(torch.float64)
+        seq_plan = sga.SeqPlan(ptr, H, D, torch.float32, kv_heads=HK, causal=False)
+        plan = sga.Plan(indptr, indices, H, D, torch.float32)
+        G = torch.randn(ids.numel(), C, generator=torch.Generator().manual_seed(2), dtype=torch.float64).cuda()
+        out = model(p, ids, seq_plan, plan)
+        (out * G.float()).sum().backward()
+        ref = model64(p64, ids, indptr, indices, ptr)
+        (ref * G).sum().backward()
+    finally:
+        torch.backends.cuda.matmul.allow_tf32 = tf32
+    pairs = [("out", out, ref)] + [(n, p[n].grad, p64[n].grad) for n in p]
+    for name, a, b in pairs:
+        assert float((a.double() - b).norm()) <= 1e-3 * float(b.norm()), name
+    assert seq_plan.device_error() == 0 and plan.device_error() == 0 and sga.embed_device_error() == 0
+
+
+def test_a_captured_layer():
+    """The forward pass in bf16, captured and replayed on new tokens."""
+    ids, indptr, indices, ptr = batch(3)
+    p = {n: t.detach() for n, t in parameters(torch.bfloat16).items()}
+    seq_plan, plan = sga.SeqPlan(ptr, H, D, kv_heads=HK, causal=False), sga.Plan(indptr, indices, H, D)
+    with torch.no_grad():
+        model(p, ids, seq_plan, plan)   # (libraries initialised before the capture)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = model(p, ids, seq_plan, plan)
+        ids.copy_((ids * 7 + 5) % V)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, model(p, ids, seq_plan, plan))
