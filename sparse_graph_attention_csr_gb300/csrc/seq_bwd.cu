@@ -26,6 +26,12 @@
 //
 // As in the forward, a row whose result is not finite is computed again over
 // its own interval alone, so that nothing of a pair that is masked reaches it.
+// Measured: 8192 rows, 8/4 heads of 128, causal 302 us, full 561 us: 1.22
+// PFLOP/s of the five products that a backward pass needs, 1.71 of the seven
+// computed, the rate of the library's product under the power limit (1.70).
+// What is left to gain is the two repeated products, against an fp32 dQ in
+// memory that several CTAs add to.
+//
 // Every wait is bounded; a timeout sets the plan's error word and ends the role.
 #include <algorithm>
 

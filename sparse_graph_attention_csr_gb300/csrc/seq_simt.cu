@@ -2,13 +2,16 @@
 // the backward pass for both dtypes.
 //
 // The tensor cores have no fp32 product, and the tolerance of the fp32 layers
-// (1e-5) rules out tf32, so these kernels are bound by the FMA rate (two
+// (1e-5) rules out tf32, so these kernels are bound by the FMA pipes (two
 // products of the forward, three and four of the backward's two passes).
 // Blocks of 256 threads (16 x 16) take a 64-row tile of one side and walk the
-// 64-row tiles of the other through shared memory; each thread holds a 4 x 4
-// piece of the scores and a 4 x D/16 piece of the result.  Tiles are row-major
-// with rows of D + 4 floats: both products read them 16 bytes at a time along
-// a row without bank conflicts, so no tile is stored transposed.
+// 64-row tiles of the other through shared memory, the next tiles copied while
+// one is in use; each thread holds a 4 x 4 piece of the scores and a 4 x D/16
+// piece of the result.  Tiles are row-major with rows of D + 4 floats: both
+// products read them 16 bytes at a time along a row without bank conflicts, so
+// no tile is stored transposed.  Two blocks an SM where registers and shared
+// memory allow (forward, 2048 rows, 8 heads of 64, full: 366 -> 285 us, 30
+// TFLOP/s; backward with D = 32 593 -> 496 us; with D = 64 it spills and loses).
 //   forward: S = Q K^T, online softmax (running maximum and sum per row),
 //     O = O alpha + P V;
 //   dQ pass (a tile of queries): S, dP = dOut V^T, dS = P (dP - Delta),
@@ -19,7 +22,7 @@
 // is owned by one block: no atomics, bitwise reproducible.
 // A row whose result is not finite is computed again over its own interval alone
 // (seq_rows.cuh).  Leaving masked pairs out of every sum instead, with a test a
-// pair, took twice the time on tiles with a mask (512 rows, D = 32).
+// pair, took 78 instead of 66 us on five sequences of 1 to 512 rows, D = 32.
 #include "seq_rows.cuh"
 #include "tc.cuh"
 
@@ -188,7 +191,7 @@ __device__ __forceinline__ void in_tile(const int64_t (&lo)[4], const int64_t (&
 
 // ---- forward ------------------------------------------------------------------
 
-template <int D> __global__ void __launch_bounds__(kThreads) seq_fwd_f32_kernel(const SeqArgs a) {
+template <int D> __global__ void __launch_bounds__(kThreads, D < 128 ? 2 : 1) seq_fwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm, *sK = sQ + kTileFloats<D>, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -406,7 +409,7 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, flo
 }
 
 // Both passes in one launch, the dK/dV units (the longer ones) first.
-template <int D> __global__ void __launch_bounds__(kThreads) seq_bwd_f32_kernel(const SeqArgs a) {
+template <int D> __global__ void __launch_bounds__(kThreads, D == 32 ? 2 : 1) seq_bwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
     const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv;
     if (blockIdx.x < kv) dkdv_pass<D>(a, sm, blockIdx.x);
