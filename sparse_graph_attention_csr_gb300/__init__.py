@@ -2,11 +2,13 @@
 dense operators around it: attention over packed sequences, layer norm and
 embedding lookup.
 
-A thin ctypes binding over the C ABI of ``libsga.so`` (declared in
-``include/sga.h``).  This module only marshals arguments: every step of the
-forward and backward passes runs in the library's CUDA kernels.  PyTorch
-provides device memory and the current stream.  There is no CPU fallback: if
-the library is missing, every call raises.
+A thin binding over the C ABI of ``libsga.so`` (declared in
+``include/sga.h``): ctypes, and for the dense operators, whose smallest calls
+are shorter than an interpreter's checks, the native module ``_dense``.  This
+module only marshals arguments: every step of the forward and backward passes
+runs in the library's CUDA kernels.  PyTorch provides device memory and the
+current stream.  There is no CPU fallback: if a library is missing, every call
+raises.
 
 Graph convention: destination-sorted CSR (row i = destination, ``indices`` =
 sources), int32, on the GPU.  Node tensors are [N, H, D], float32 or bfloat16.
@@ -23,6 +25,7 @@ from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsga.so")
+DENSE_PATH = os.path.join(_HERE, "_dense.so")
 
 SGA_OK, SGA_EINVAL, SGA_EUNSUPPORTED, SGA_ECUDA, SGA_EWORKSPACE, SGA_EDEVICE_CHECK, SGA_ELIMIT = range(7)
 SGA_F32, SGA_BF16 = 0, 1
@@ -158,8 +161,26 @@ def _lib():
     return _LIB
 
 
+_EXT = None
+
+
+def _ext():
+    """The native entry of the dense operators (raises if it has not been built)."""
+    global _EXT
+    if _EXT is None:
+        _lib()
+        if not os.path.exists(DENSE_PATH):
+            raise ImportError(f"{DENSE_PATH} is missing: run sparse_graph_attention_csr_gb300.build "
+                              "(or __graft_entry__.build()) first; there is no CPU fallback")
+        from . import _dense
+        _dense.set_error(SgaError)
+        _EXT = _dense
+    return _EXT
+
+
 def load_library():
-    """Load the native library now; returns the ctypes handle."""
+    """Load the native libraries now; returns the ctypes handle."""
+    _ext()
     return _lib()
 
 
@@ -646,32 +667,6 @@ def _place(device, stream):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
-def _tensor(t, name, device, dtype, shape):
-    """A contiguous CUDA tensor of exactly this device, dtype and shape."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == device.index and t.is_contiguous()):
-        return
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _distinct(ins, outs):
-    """Outputs must not share memory with inputs or one another."""
-    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), n, True) for n, t in outs]
-    spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), n, False) for n, t in ins]
-    for i, (b, e, n, _) in enumerate(spans[:len(outs)]):
-        for b2, e2, n2, _ in spans[i + 1:]:
-            if b < e2 and b2 < e:
-                raise ValueError(f"{n} shares memory with {n2}")
-
-
 class SeqPlan:
     """A plan for attention over packed sequences: sequence b is rows
     seq_ptr[b] .. seq_ptr[b + 1] of the node tensors ([B + 1] int32, from 0,
@@ -705,7 +700,9 @@ class SeqPlan:
                 ctypes.byref(handle)), "sga_seq_plan_create")
         self._h = handle
         self.rows = int(_lib().sga_seq_plan_rows(handle))
-        self._ws_bytes = int(_lib().sga_seq_bwd_workspace_bytes(handle))
+        self._c = _ext().SeqPlan(handle.value, self.device.index, dtype == torch.float32, self.rows,
+                                 self.H, self.kv_heads, self.D,
+                                 int(_lib().sga_seq_bwd_workspace_bytes(handle)))
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -728,36 +725,6 @@ class SeqPlan:
         return int(code.value)
 
 
-def _seq_inputs(plan, Q, K, V):
-    T = Q.shape[0] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else plan.rows
-    if T < plan.rows:
-        raise ValueError(f"Q has {T} rows, the plan's sequences cover {plan.rows}")
-    kv = (T, plan.kv_heads, plan.D)
-    _tensor(Q, "Q", plan.device, plan.dtype, (T, plan.H, plan.D))
-    _tensor(K, "K", plan.device, plan.dtype, kv)
-    _tensor(V, "V", plan.device, plan.dtype, kv)
-    return T
-
-
-def _seq_scale(plan, scale):
-    scale = 1.0 / math.sqrt(plan.D) if scale is None else float(scale)
-    if not 0.0 < scale < math.inf:
-        raise ValueError(f"scale must be positive and finite, got {scale}")
-    return scale
-
-
-def _seq_result(plan, like, given, name, fill=0.0):
-    """The given result tensor, or a new one: rows behind the last sequence,
-    which the kernels leave as they are, are filled in a new one."""
-    if given is not None:
-        _tensor(given, name, plan.device, like.dtype, like.shape)
-        return given
-    t = torch.empty_like(like)
-    if t.shape[0] > plan.rows:
-        t[plan.rows:].fill_(fill)
-    return t
-
-
 def seq_attn_fwd(plan: SeqPlan, Q, K, V, scale: float | None = None, out=None, lse=None,
                  stream=None):
     """Attention of every row over the rows of its own sequence: (out [T, H, D],
@@ -765,207 +732,40 @@ def seq_attn_fwd(plan: SeqPlan, Q, K, V, scale: float | None = None, out=None, l
     defaults to 1 / sqrt(D).  T may exceed the plan's rows: rows behind the
     last sequence are not read, and are zero (lse: -inf) in results allocated
     here, left as they were in results passed in."""
-    T = _seq_inputs(plan, Q, K, V)
-    scale = _seq_scale(plan, scale)
-    ctx, raw = _place(plan.device, stream)
-    with ctx:
-        own = out is None and lse is None
-        out = _seq_result(plan, Q, out, "out")
-        if lse is None:
-            lse = torch.empty((T, plan.H), dtype=torch.float32, device=plan.device)
-            if T > plan.rows:
-                lse[plan.rows:].fill_(-math.inf)
-        else:
-            _tensor(lse, "lse", plan.device, torch.float32, (T, plan.H))
-        if not own:
-            _distinct((("Q", Q), ("K", K), ("V", V)), (("out", out), ("lse", lse)))
-        st = _lib().seq_attn_fwd(plan._h, Q.data_ptr(), K.data_ptr(), V.data_ptr(), T, scale,
-                                 out.data_ptr(), lse.data_ptr(), raw)
-    if st:
-        raise SgaError(st, "seq_attn_fwd")
-    return out, lse
+    return _ext().seq_attn_fwd(plan._c, Q, K, V, scale, out, lse, stream)
 
 
 def seq_attn_bwd(plan: SeqPlan, Q, K, V, out, lse, dOut, scale: float | None = None, dQ=None,
                  dK=None, dV=None, stream=None):
     """(dQ [T, H, D], dK, dV [T, kv_heads, D]) from the forward's out and lse.
     Rows behind the last sequence: as in seq_attn_fwd, zero in new results."""
-    T = _seq_inputs(plan, Q, K, V)
-    _tensor(out, "out", plan.device, plan.dtype, Q.shape)
-    _tensor(dOut, "dOut", plan.device, plan.dtype, Q.shape)
-    _tensor(lse, "lse", plan.device, torch.float32, (T, plan.H))
-    scale = _seq_scale(plan, scale)
-    ctx, raw = _place(plan.device, stream)
-    with ctx:
-        own = dQ is None and dK is None and dV is None
-        dQ = _seq_result(plan, Q, dQ, "dQ")
-        dK = _seq_result(plan, K, dK, "dK")
-        dV = _seq_result(plan, V, dV, "dV")
-        if not own:
-            _distinct((("Q", Q), ("K", K), ("V", V), ("out", out), ("lse", lse), ("dOut", dOut)),
-                      (("dQ", dQ), ("dK", dK), ("dV", dV)))
-        ws = torch.empty(plan._ws_bytes, dtype=torch.uint8, device=plan.device)
-        st = _lib().seq_attn_bwd(plan._h, Q.data_ptr(), K.data_ptr(), V.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), dOut.data_ptr(), T, scale, dQ.data_ptr(),
-                                 dK.data_ptr(), dV.data_ptr(), ws.data_ptr(), plan._ws_bytes, raw)
-    if st:
-        raise SgaError(st, "seq_attn_bwd")
-    return dQ, dK, dV
+    return _ext().seq_attn_bwd(plan._c, Q, K, V, out, lse, dOut, scale, dQ, dK, dV, stream)
 
 
 # ------------------------------------------------------------------ layer norm
-
-def _norm_inputs(X, weight, bias=None):
-    """(device, shape, dtype code, weight's dtype code) of the checked inputs."""
-    if not isinstance(X, torch.Tensor) or not X.is_cuda:
-        raise ValueError("X must be a CUDA tensor")
-    shape, dtype, device = X.shape, X.dtype, X.device
-    if not shape or shape[-1] < 1:
-        raise ValueError(f"X must be [..., C] with C >= 1, got {tuple(shape)}")
-    dt = SGA_BF16 if dtype is torch.bfloat16 else _dtype_code(X)
-    if not X.is_contiguous():
-        raise ValueError("X must be contiguous")
-    if weight is None:
-        if bias is not None:
-            raise ValueError("a bias needs a weight")
-        return device, shape, dt, dt
-    wdtype = weight.dtype if isinstance(weight, torch.Tensor) else None
-    if wdtype is not torch.float32 and wdtype is not dtype:
-        raise TypeError(f"weight must be {dtype} or torch.float32, got {wdtype}")
-    row = shape[-1:]
-    _tensor(weight, "weight", device, wdtype, row)
-    if bias is not None:
-        _tensor(bias, "bias", device, wdtype, row)
-    return device, shape, dt, SGA_F32 if wdtype is torch.float32 else SGA_BF16
-
 
 def layer_norm_fwd(X, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None,
                    stream=None):
     """Layer norm over the last dimension of X [..., C]: (out, mean, rstd) with
     mean and rstd = 1 / sqrt(var + eps) float32 of X's leading shape.  weight,
     bias: [C], float32 or X's dtype, or None.  ``out`` may be X itself."""
-    device, shape, dt, wdt = _norm_inputs(X, weight, bias)
-    eps = float(eps)
-    if not 0.0 <= eps < math.inf:
-        raise ValueError(f"eps must be finite and not negative, got {eps}")
-    lead, C = shape[:-1], shape[-1]
-    ctx, raw = _place(device, stream)
-    with ctx:
-        own = out is None and mean is None and rstd is None
-        if out is None:
-            out = torch.empty_like(X)
-        if mean is None:
-            mean = torch.empty(lead, dtype=torch.float32, device=device)
-        if rstd is None:
-            rstd = torch.empty_like(mean)
-        if not own:
-            _tensor(out, "out", device, X.dtype, shape)
-            _tensor(mean, "mean", device, torch.float32, lead)
-            _tensor(rstd, "rstd", device, torch.float32, lead)
-            ins = [(n, t) for n, t in (("X", X), ("weight", weight), ("bias", bias)) if t is not None]
-            if out.data_ptr() == X.data_ptr():   # in place: a row is read before it is written
-                _distinct(ins, (("mean", mean), ("rstd", rstd)))
-                _distinct(ins[1:], (("out", out), ("mean", mean), ("rstd", rstd)))
-            else:
-                _distinct(ins, (("out", out), ("mean", mean), ("rstd", rstd)))
-        st = _lib().layer_norm_fwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
-                                   None if bias is None else bias.data_ptr(), X.numel() // C, C,
-                                   eps, dt, wdt, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), raw)
-    if st:
-        raise SgaError(st, "layer_norm_fwd")
-    return out, mean, rstd
+    return _ext().layer_norm_fwd(X, weight, bias, eps, out, mean, rstd, stream)
 
 
 def layer_norm_bwd(X, weight, mean, rstd, dOut, bias: bool = True, dX=None, dweight=None,
                    dbias=None, stream=None):
     """(dX, dweight, dbias) from the forward's mean and rstd; dweight and dbias
     in weight's dtype, None without a weight (dbias also with bias=False)."""
-    device, shape, dt, wdt = _norm_inputs(X, weight)
-    lead, C = shape[:-1], shape[-1]
-    _tensor(dOut, "dOut", device, X.dtype, shape)
-    _tensor(mean, "mean", device, torch.float32, lead)
-    _tensor(rstd, "rstd", device, torch.float32, lead)
-    if weight is None and (dweight is not None or dbias is not None):
-        raise ValueError("dweight and dbias need a weight")
-    if not bias and dbias is not None:
-        raise ValueError("dbias given with bias=False")
-    N = X.numel() // C
-    ctx, raw = _place(device, stream)
-    lib = _lib()
-    with ctx:
-        own = dX is None and dweight is None and dbias is None
-        if dX is None:
-            dX = torch.empty_like(X)
-        ws, nbytes = None, 0
-        if weight is not None:
-            if dweight is None:
-                dweight = torch.empty_like(weight)
-            if bias and dbias is None:
-                dbias = torch.empty_like(weight)
-            nbytes = lib.sga_norm_bwd_workspace_bytes(N, C)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if not own:
-            outs = [("dX", dX)]
-            _tensor(dX, "dX", device, X.dtype, shape)
-            for n, t in (("dweight", dweight), ("dbias", dbias)):
-                if t is not None:
-                    _tensor(t, n, device, weight.dtype, weight.shape)
-                    outs.append((n, t))
-            ins = [("X", X), ("dOut", dOut), ("mean", mean), ("rstd", rstd)]
-            _distinct(ins + ([("weight", weight)] if weight is not None else []), outs)
-        st = lib.layer_norm_bwd(X.data_ptr(), None if weight is None else weight.data_ptr(),
-                                mean.data_ptr(), rstd.data_ptr(), dOut.data_ptr(), N, C, dt, wdt,
-                                dX.data_ptr(), None if dweight is None else dweight.data_ptr(),
-                                None if dbias is None else dbias.data_ptr(),
-                                None if ws is None else ws.data_ptr(), nbytes, raw)
-    if st:
-        raise SgaError(st, "layer_norm_bwd")
-    return dX, dweight, dbias
+    return _ext().layer_norm_bwd(X, weight, mean, rstd, dOut, bias, dX, dweight, dbias, stream)
 
 
 # ------------------------------------------------------------------- embedding
-
-def _embed_ids(ids):
-    if not isinstance(ids, torch.Tensor) or not ids.is_cuda:
-        raise ValueError("ids must be a CUDA tensor")
-    if ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"ids must be torch.int32 or torch.int64, got {ids.dtype}")
-    if not ids.is_contiguous():
-        raise ValueError("ids must be contiguous")
-    return ids.element_size()
-
-
-def _embed_scale(scale):
-    scale = float(scale)
-    if not math.isfinite(scale):
-        raise ValueError(f"scale must be finite, got {scale}")
-    return scale
-
 
 def embed_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
     """out [*ids.shape, C] = scale * table[ids] for a table [V, C].  An id
     outside [0, V) gives a row of zeros and sets the device's error word
     (embed_device_error)."""
-    id_bytes = _embed_ids(ids)
-    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[1] < 1:
-        raise ValueError("table must be [V, C] with C >= 1")
-    dt, device, dtype = _dtype_code(table), ids.device, table.dtype
-    V, C = rows = table.shape
-    _tensor(table, "table", device, dtype, rows)
-    scale = _embed_scale(scale)
-    shape = (*ids.shape, C)
-    ctx, raw = _place(device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=device)
-        else:
-            _tensor(out, "out", device, dtype, shape)
-            _distinct((("ids", ids), ("table", table)), (("out", out),))
-        st = _lib().embed_fwd(ids.data_ptr(), id_bytes, table.data_ptr(), ids.numel(), V, C, scale,
-                              dt, out.data_ptr(), raw)
-    if st:
-        raise SgaError(st, "embed_fwd")
-    return out
+    return _ext().embed_fwd(ids, table, scale, out, stream)
 
 
 def embed_bwd(ids, dOut, num_rows: int, scale: float = 1.0, padding_idx: int | None = None,
@@ -974,35 +774,7 @@ def embed_bwd(ids, dOut, num_rows: int, scale: float = 1.0, padding_idx: int | N
     row's tokens, in a fixed order (bitwise reproducible); zero for rows
     without a token and for padding_idx.  Ids outside the table add nothing
     and set the device's error word."""
-    id_bytes = _embed_ids(ids)
-    if not isinstance(dOut, torch.Tensor) or dOut.dim() < 1 or dOut.shape[-1] < 1:
-        raise ValueError("dOut must be [*ids.shape, C] with C >= 1")
-    dt = _dtype_code(dOut)
-    C, V = dOut.shape[-1], int(num_rows)
-    _tensor(dOut, "dOut", ids.device, dOut.dtype, (*ids.shape, C))
-    if V < 0:
-        raise ValueError(f"num_rows must not be negative, got {V}")
-    if padding_idx is None:
-        padding_idx = -1
-    elif not 0 <= padding_idx < V:
-        raise ValueError(f"padding_idx must be in [0, {V}), got {padding_idx}")
-    scale = _embed_scale(scale)
-    N = ids.numel()
-    ctx, raw = _place(ids.device, stream)
-    lib = _lib()
-    with ctx:
-        if dTable is None:
-            dTable = torch.empty((V, C), dtype=dOut.dtype, device=ids.device)
-        else:
-            _tensor(dTable, "dTable", ids.device, dOut.dtype, (V, C))
-            _distinct((("ids", ids), ("dOut", dOut)), (("dTable", dTable),))
-        nbytes = lib.sga_embed_bwd_workspace_bytes(N, C)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=ids.device)
-        st = lib.embed_bwd(ids.data_ptr(), id_bytes, dOut.data_ptr(), N, V, C, scale, padding_idx,
-                           dt, dTable.data_ptr(), ws.data_ptr(), nbytes, raw)
-    if st:
-        raise SgaError(st, "embed_bwd")
-    return dTable
+    return _ext().embed_bwd(ids, dOut, num_rows, scale, padding_idx, dTable, stream)
 
 
 def embed_device_error(device=None, stream=None) -> int:

@@ -1,21 +1,27 @@
-"""Build libsga.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libsga.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_dense.so, the Python entry of the dense operators, with the host compiler.
 
-Translation units compile in parallel; the shared library is linked next to
-this file.  No CMake, no torch extension machinery: the library has a plain C
-ABI and the Python binding loads it with ctypes.
+Translation units compile in parallel; the shared libraries are linked next to
+this file.  No CMake, no torch extension machinery: libsga.so has a plain C
+ABI, which the Python binding loads with ctypes; _dense.so calls the same ABI
+and is built against torch's headers, so that checking and allocating tensors
+takes no interpreter time.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsga.so")
+DENSE = os.path.join(HERE, "_dense.so")
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -56,14 +62,53 @@ def _compile(src: str, extra, verbose: bool) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_dense(verbose: bool) -> str:
+    src = os.path.join(CSRC, "dense_binding.cpp")
+    obj = os.path.join(BUILD, "dense_binding.o")
+    hdr = os.path.join(ROOT, "include", "sga.h")
+    if os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(src), os.path.getmtime(hdr)):
+        return obj
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-fvisibility=hidden", "-w",
+           *(f for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda,
+                         sysconfig.get_paths()["include"]) for f in ("-isystem", d)),
+           "-c", src, "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_dense(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    if os.path.exists(DENSE) and os.path.getmtime(DENSE) >= max(os.path.getmtime(obj), os.path.getmtime(LIB)):
+        return
+    tmp = DENSE + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", HERE, "-lsga", "-L", lib, "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, DENSE)
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, jobs: int | None = None) -> str:
-    """Compile every csrc/*.cu and link libsga.so; returns the library path."""
+    """Compile every csrc source, link libsga.so and _dense.so; returns libsga.so's path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
-    with cf.ThreadPoolExecutor(jobs) as ex:
+    with cf.ThreadPoolExecutor(jobs + 1) as ex:
+        dense = ex.submit(_compile_dense, verbose)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
+        dense_obj = dense.result()
     if (not os.path.exists(LIB)
             or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs)):
         tmp = LIB + f".tmp{os.getpid()}"
@@ -72,6 +117,7 @@ def build(verbose: bool = False, ptxas_info: bool = False, jobs: int | None = No
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _link_dense(dense_obj)
     return LIB
 
 

@@ -84,7 +84,7 @@ def test_a_layer_and_its_gradients():
         (ref * G).sum().backward()
     finally:
         torch.backends.cuda.matmul.allow_tf32 = tf32
-    pairs = [("out", out, ref)] + [(n, p[n].grad, p64[n].grad) for n in p]
+    pairs = [("out", out.detach(), ref.detach())] + [(n, p[n].grad, p64[n].grad) for n in p]
     for name, a, b in pairs:
         assert float((a.double() - b).norm()) <= 1e-3 * float(b.norm()), name
     assert seq_plan.device_error() == 0 and plan.device_error() == 0 and sga.embed_device_error() == 0
