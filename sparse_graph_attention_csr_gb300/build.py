@@ -92,7 +92,7 @@ def _link_dense(obj: str) -> None:
         return
     tmp = DENSE + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", HERE, "-lsga", "-L", lib, "-lc10",
-           "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+           "-lc10_cuda", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

@@ -6,8 +6,7 @@
 // Checked and allocated in Python they take 14 to 20 on the host, most of it
 // interpreter time; here they take about half.
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -126,7 +125,7 @@ class Place {
 };
 
 Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, at::Device device) {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+    return at::detail::empty_cuda(shape, dtype, device, std::nullopt);   // (at::empty without the dispatcher)
 }
 
 // ---- attention over packed sequences -----------------------------------------------
@@ -241,7 +240,7 @@ py::tuple layer_norm_fwd_(const Tensor &X, const Maybe &weight, const Maybe &bia
         throw py::value_error("eps must be finite and not negative, got " + std::to_string(eps));
     const at::Device dev = X.device();
     const Place on(dev, stream);
-    Tensor o = out ? *out : at::empty_like(X), m = mean ? *mean : fresh(n.lead, at::kFloat, dev),
+    Tensor o = out ? *out : fresh(X.sizes(), X.scalar_type(), dev), m = mean ? *mean : fresh(n.lead, at::kFloat, dev),
            r = rstd ? *rstd : fresh(n.lead, at::kFloat, dev);
     if (out || mean || rstd) {
         need(o, "out", dev, X.scalar_type(), X.sizes());
@@ -268,12 +267,12 @@ py::tuple layer_norm_bwd_(const Tensor &X, const Maybe &weight, const Tensor &me
     if (!weight && (dweight || dbias)) throw py::value_error("dweight and dbias need a weight");
     if (!bias && dbias) throw py::value_error("dbias given with bias=False");
     const Place on(dev, stream);
-    Tensor x = dX ? *dX : at::empty_like(X), ws;
+    Tensor x = dX ? *dX : fresh(X.sizes(), X.scalar_type(), dev), ws;
     Maybe w = dweight, b = dbias;
     size_t bytes = 0;
     if (weight) {
-        if (!w) w = at::empty_like(*weight);
-        if (bias && !b) b = at::empty_like(*weight);
+        if (!w) w = fresh({n.C}, weight->scalar_type(), dev);
+        if (bias && !b) b = fresh({n.C}, weight->scalar_type(), dev);
         bytes = sga_norm_bwd_workspace_bytes(n.N, n.C);
         ws = fresh({(int64_t)bytes}, at::kByte, dev);
     }
