@@ -4,10 +4,10 @@
 // The tensor cores have no fp32 product, and the tolerance of the fp32 layers
 // (1e-5) rules out tf32, so these kernels are bound by the FMA pipes (two
 // products of the forward, three and four of the backward's two passes).
-// Blocks of 256 threads (16 x 16) take a 64-row tile of one side and walk the
-// 64-row tiles of the other through shared memory, the next tiles copied while
-// one is in use; each thread holds a 4 x 4 piece of the scores and a 4 x D/16
-// piece of the result.  Tiles are row-major with rows of D + 4 floats: both
+// Blocks of 256 threads (16 x 16) take 16 RA rows of one side (RA = 4: a 64-row
+// tile; RA = 2: half of one) and walk the 64-row tiles of the other through
+// shared memory, the next tiles copied while one is in use; each thread holds an
+// RA x 4 piece of the scores and an RA x D/16 piece of the result.  Tiles are row-major with rows of D + 4 floats: both
 // products read them 16 bytes at a time along a row without bank conflicts, so
 // no tile is stored transposed.  Two blocks an SM where registers and shared
 // memory allow (forward, 2048 rows, 8 heads of 64, full: 366 -> 285 us, 30
@@ -35,14 +35,15 @@ constexpr int kPP = kT + 4;    // pitch of a score tile
 
 template <int D> constexpr int kPitch = D + 4;
 template <int D> constexpr int kTileFloats = kT * (D + 4);
-constexpr int kScoreFloats = kT * kPP;
+template <int D, int RA> constexpr int kOwnFloats = 16 * RA * (D + 4);   // an owner tile: 16 RA rows
+template <int RA> constexpr int kScoreFloats = 16 * RA * kPP;
 
-// rows [r0, r0 + 64) of head h of a [T][heads][D] tensor, asynchronously (rows
+// rows [r0, r0 + ROWS) of head h of a [T][heads][D] tensor, asynchronously (rows
 // past `rows` as zeros)
-template <int D>
+template <int D, int ROWS = kT>
 __device__ __forceinline__ void load_tile(float *dst, const void *src, int64_t r0, int64_t rows, int heads, int h) {
     constexpr int C4 = D / 4;
-    for (int i = threadIdx.x; i < kT * C4; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * C4; i += kThreads) {
         const int r = i / C4, c = i % C4;
         const bool in = r0 + r < rows;
         tc::cp16(tc::smem_u32(dst + r * kPitch<D> + 4 * c),
@@ -51,22 +52,22 @@ __device__ __forceinline__ void load_tile(float *dst, const void *src, int64_t r
 }
 
 // s[a][c] = row (ty + 16 a) of A . row (tx + 16 c) of B
-template <int D>
-__device__ __forceinline__ void dot_tiles(float (&s)[4][4], const float *A, const float *B, int ty, int tx) {
-    float2 acc[4][4];
+template <int D, int RA>
+__device__ __forceinline__ void dot_tiles(float (&s)[RA][4], const float *A, const float *B, int ty, int tx) {
+    float2 acc[RA][4];
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < RA; ++a)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[a][c] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-        float4 x[4], y[4];
+        float4 x[RA], y[4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) x[a] = *reinterpret_cast<const float4 *>(A + (ty + 16 * a) * kPitch<D> + d);
+        for (int a = 0; a < RA; ++a) x[a] = *reinterpret_cast<const float4 *>(A + (ty + 16 * a) * kPitch<D> + d);
 #pragma unroll
         for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4 *>(B + (tx + 16 * c) * kPitch<D> + d);
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int a = 0; a < RA; ++a)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 acc[a][c] = ffma2(make_float2(x[a].x, x[a].y), make_float2(y[c].x, y[c].y), acc[a][c]);
@@ -74,7 +75,7 @@ __device__ __forceinline__ void dot_tiles(float (&s)[4][4], const float *A, cons
             }
     }
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < RA; ++a)
 #pragma unroll
         for (int c = 0; c < 4; ++c) s[a][c] = acc[a][c].x + acc[a][c].y;
 }
@@ -104,32 +105,32 @@ template <int D> __device__ __forceinline__ void load_cols(float (&v)[kCols<D>],
 }
 
 // acc[a][x] += sum_j P[ty + 16 a][j] B[j][col x] over the 64 rows of B
-template <int D>
-__device__ __forceinline__ void add_product(float (&acc)[4][kCols<D>], const float *P, const float *B, int ty, int tx) {
+template <int D, int RA>
+__device__ __forceinline__ void add_product(float (&acc)[RA][kCols<D>], const float *P, const float *B, int ty, int tx) {
     constexpr int NC = kCols<D>;
 #pragma unroll 2
     for (int j = 0; j < kT; j += 4) {
-        float4 p[4];
+        float4 p[RA];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) p[a] = *reinterpret_cast<const float4 *>(P + (ty + 16 * a) * kPP + j);
+        for (int a = 0; a < RA; ++a) p[a] = *reinterpret_cast<const float4 *>(P + (ty + 16 * a) * kPP + j);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             float v[NC];
             load_cols<D>(v, B + (j + u) * kPitch<D>, tx);
 #pragma unroll
-            for (int a = 0; a < 4; ++a) axpy2<NC>(acc[a], u == 0 ? p[a].x : u == 1 ? p[a].y : u == 2 ? p[a].z : p[a].w, v);
+            for (int a = 0; a < RA; ++a) axpy2<NC>(acc[a], u == 0 ? p[a].x : u == 1 ? p[a].y : u == 2 ? p[a].z : p[a].w, v);
         }
     }
 }
 
 // Stores the rows, scaled, and returns whether any element of this thread's row
 // a was not finite, as bit a.
-template <int D>
-__device__ __forceinline__ uint32_t store_rows(float *dst, const float (&acc)[4][kCols<D>], const float (&f)[4], int64_t r0,
+template <int D, int RA>
+__device__ __forceinline__ uint32_t store_rows(float *dst, const float (&acc)[RA][kCols<D>], const float (&f)[RA], int64_t r0,
                                                int64_t rows, int heads, int h, int ty, int tx) {
     uint32_t bad = 0;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int a = 0; a < RA; ++a) {
         const int64_t row = r0 + ty + 16 * a;
         if (row >= rows) continue;
         float *o = dst + (row * heads + h) * D;
@@ -145,11 +146,11 @@ __device__ __forceinline__ uint32_t store_rows(float *dst, const float (&acc)[4]
 
 // Calls redo(a, half) for every row (ty + 16 a of the warp's half) of which a
 // thread found an element that is not finite; the warp together, after its stores.
-template <typename F> __device__ __forceinline__ void each_bad_row(uint32_t bad, F redo) {
+template <int RA, typename F> __device__ __forceinline__ void each_bad_row(uint32_t bad, F redo) {
     if (!__any_sync(SGA_FULL_MASK, bad != 0)) return;
     __syncwarp();
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
+    for (int a = 0; a < RA; ++a) {
         const uint32_t who = __ballot_sync(SGA_FULL_MASK, (bad >> a) & 1u);
         for (int half = 0; half < 2; ++half)
             if ((who >> (16 * half)) & 0xffffu) redo(a, half);
@@ -167,11 +168,12 @@ __device__ __forceinline__ float half_sum(float v) {
     return v;
 }
 
-// What each of a thread's four rows sees: queries of a key row, or keys of a
+// What each of a thread's rows sees: queries of a key row, or keys of a
 // query row.  Rows past the last see nothing.
-__device__ __forceinline__ void intervals(const SeqArgs &a, bool keys, int64_t r0, int ty, int64_t (&lo)[4], int64_t (&hi)[4]) {
+template <int RA>
+__device__ __forceinline__ void intervals(const SeqArgs &a, bool keys, int64_t r0, int ty, int64_t (&lo)[RA], int64_t (&hi)[RA]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RA; ++i) {
         const int64_t row = r0 + ty + 16 * i;
         lo[i] = hi[i] = 0;
         if (row < a.rows) {
@@ -181,34 +183,50 @@ __device__ __forceinline__ void intervals(const SeqArgs &a, bool keys, int64_t r
         }
     }
 }
-__device__ __forceinline__ void in_tile(const int64_t (&lo)[4], const int64_t (&hi)[4], int64_t t0, int (&l)[4], int (&h)[4]) {
+template <int RA>
+__device__ __forceinline__ void in_tile(const int64_t (&lo)[RA], const int64_t (&hi)[RA], int64_t t0, int (&l)[RA], int (&h)[RA]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RA; ++i) {
         l[i] = (int)max((int64_t)0, min((int64_t)kT, lo[i] - t0));
         h[i] = (int)max((int64_t)0, min((int64_t)kT, hi[i] - t0));
     }
 }
 
+// Unit u of a pass: 16 RA rows (from `row` of a tile) of one head.
+template <int RA> struct Unit {
+    uint32_t tile;
+    int head, row;
+    __device__ __forceinline__ Unit(uint32_t u, int heads) {
+        constexpr uint32_t S = 4 / RA;
+        tile = u / (S * heads);
+        head = (int)(u / S % heads);
+        row = (int)(u % S) * 16 * RA;
+    }
+};
+// Blocks that an SM should hold.
+template <int RA, bool TWO> constexpr int kBlocks = RA == 2 || TWO ? 2 : 1;
+
 // ---- forward ------------------------------------------------------------------
 
-template <int D> __global__ void __launch_bounds__(kThreads, D < 128 ? 2 : 1) seq_fwd_f32_kernel(const SeqArgs a) {
+template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA, (D < 128)>) seq_fwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *sK = sQ + kTileFloats<D>, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>;
+    float *sQ = sm, *sK = sQ + kOwnFloats<D, RA>, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const SeqTile t = a.qtiles[blockIdx.x / a.H];
-    const int h = blockIdx.x % a.H, hk = h / (a.H / a.Hkv);
-    const int64_t q0 = (int64_t)t.tile * kT;
+    const Unit<RA> u(blockIdx.x, a.H);
+    const SeqTile t = a.qtiles[u.tile];
+    const int h = u.head, hk = h / (a.H / a.Hkv);
+    const int64_t q0 = (int64_t)t.tile * kT + u.row;
     const float scale2 = a.scale * kLog2e;
-    load_tile<D>(sQ, a.Q, q0, a.rows, a.H, h);
+    load_tile<D, 16 * RA>(sQ, a.Q, q0, a.rows, a.H, h);
     load_tile<D>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
     tc::cp_commit();
     load_tile<D>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
     tc::cp_commit();
-    int64_t lo[4], hi[4];
+    int64_t lo[RA], hi[RA];
     intervals(a, false, q0, ty, lo, hi);
-    float m[4], l[4], acc[4][kCols<D>];
+    float m[RA], l[RA], acc[RA][kCols<D>];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RA; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -217,17 +235,17 @@ template <int D> __global__ void __launch_bounds__(kThreads, D < 128 ? 2 : 1) se
     for (int kt = t.t0; kt < t.t1; ++kt) {
         const int64_t k0 = (int64_t)kt * kT;
         const bool full = kt >= t.f0 && kt < t.f1;
-        int kl[4], kh[4];
+        int kl[RA], kh[RA];
         in_tile(lo, hi, k0, kl, kh);
         tc::cp_wait<1>();   // this K (V may be on its way)
         __syncthreads();
-        float s[4][4];
-        dot_tiles<D>(s, sQ, sK, ty, tx);
+        float s[RA][4];
+        dot_tiles<D, RA>(s, sQ, sK, ty, tx);
         __syncthreads();
         if (kt + 1 < t.t1) load_tile<D>(sK, a.K, k0 + kT, a.rows, a.Hkv, hk);   // beside the softmax and P V
         tc::cp_commit();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RA; ++i) {
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -251,20 +269,20 @@ template <int D> __global__ void __launch_bounds__(kThreads, D < 128 ? 2 : 1) se
         }
         tc::cp_wait<1>();   // this V
         __syncthreads();
-        add_product<D>(acc, sP, sV, ty, tx);
+        add_product<D, RA>(acc, sP, sV, ty, tx);
         __syncthreads();
         if (kt + 1 < t.t1) load_tile<D>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);   // beside the next scores
         tc::cp_commit();
     }
-    float inv[4];
+    float inv[RA];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RA; ++i) {
         inv[i] = 1.f / l[i];
         const int64_t row = q0 + ty + 16 * i;
         if (tx == 0 && row < a.rows) a.lse_w[row * a.H + h] = (m[i] + log2f(l[i])) * kLn2;
     }
-    const uint32_t bad = store_rows<D>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
-    each_bad_row(bad, [&](int i, int half) {
+    const uint32_t bad = store_rows<D, RA>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+    each_bad_row<RA>(bad, [&](int i, int half) {
         seq::out_row_alone<float, D>(a, q0 + (ty & ~1) + half + 16 * i, h, hk, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
                                      __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half));
     });
@@ -272,24 +290,25 @@ template <int D> __global__ void __launch_bounds__(kThreads, D < 128 ? 2 : 1) se
 
 // ---- backward -------------------------------------------------------------------
 
-template <int D> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float *sm, uint32_t unit) {
-    float *sQ = sm, *sG = sQ + kTileFloats<D>, *sV = sG + kTileFloats<D>, *sP = sV + kTileFloats<D>,
-          *sK = sP + kScoreFloats;   // two K tiles
+template <int D, int RA> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float *sm, uint32_t unit) {
+    float *sQ = sm, *sG = sQ + kOwnFloats<D, RA>, *sV = sG + kOwnFloats<D, RA>, *sP = sV + kTileFloats<D>,
+          *sK = sP + kScoreFloats<RA>;   // two K tiles
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const SeqTile t = a.qtiles[unit / a.H];
-    const int h = unit % a.H, hk = h / (a.H / a.Hkv);
-    const int64_t q0 = (int64_t)t.tile * kT;
+    const Unit<RA> u(unit, a.H);
+    const SeqTile t = a.qtiles[u.tile];
+    const int h = u.head, hk = h / (a.H / a.Hkv);
+    const int64_t q0 = (int64_t)t.tile * kT + u.row;
     const float scale2 = a.scale * kLog2e;
-    load_tile<D>(sQ, a.Q, q0, a.rows, a.H, h);
-    load_tile<D>(sG, a.dOut, q0, a.rows, a.H, h);
+    load_tile<D, 16 * RA>(sQ, a.Q, q0, a.rows, a.H, h);
+    load_tile<D, 16 * RA>(sG, a.dOut, q0, a.rows, a.H, h);
     load_tile<D>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
     load_tile<D>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
     tc::cp_commit();
-    int64_t lo[4], hi[4];
+    int64_t lo[RA], hi[RA];
     intervals(a, false, q0, ty, lo, hi);
-    float ls[4], dl[4], acc[4][kCols<D>];
+    float ls[RA], dl[RA], acc[RA][kCols<D>];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RA; ++i) {
         const int64_t r = (int64_t)h * a.rows_pad + q0 + ty + 16 * i;
         ls[i] = a.ws_nlse[r];
         dl[i] = a.ws_ndelta[r];
@@ -300,19 +319,19 @@ template <int D> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float
         const int64_t k0 = (int64_t)kt * kT;
         const bool full = kt >= t.f0 && kt < t.f1;
         float *sKi = sK + (kt - t.t0) % 2 * kTileFloats<D>, *sKn = sK + (kt - t.t0 + 1) % 2 * kTileFloats<D>;
-        int kl[4], kh[4];
+        int kl[RA], kh[RA];
         in_tile(lo, hi, k0, kl, kh);
         tc::cp_wait<0>();
         __syncthreads();   // this K and V; the last dS K is done with the other K and with dS
         if (kt + 1 < t.t1) load_tile<D>(sKn, a.K, k0 + kT, a.rows, a.Hkv, hk);
-        float s[4][4], g[4][4];
-        dot_tiles<D>(g, sG, sV, ty, tx);
+        float s[RA][4], g[RA][4];
+        dot_tiles<D, RA>(g, sG, sV, ty, tx);
         __syncthreads();
         if (kt + 1 < t.t1) load_tile<D>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);
         tc::cp_commit();
-        dot_tiles<D>(s, sQ, sKi, ty, tx);
+        dot_tiles<D, RA>(s, sQ, sKi, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RA; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int j = tx + 16 * c;
@@ -320,23 +339,26 @@ template <int D> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float
                 sP[(ty + 16 * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, ls[i])) * (g[i][c] + dl[i]) : 0.f;
             }
         __syncthreads();
-        add_product<D>(acc, sP, sKi, ty, tx);
+        add_product<D, RA>(acc, sP, sKi, ty, tx);
     }
-    const float f[4] = {a.scale, a.scale, a.scale, a.scale};
-    const uint32_t bad = store_rows<D>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
-    each_bad_row(bad, [&](int i, int half) {
+    float f[RA];
+#pragma unroll
+    for (int i = 0; i < RA; ++i) f[i] = a.scale;
+    const uint32_t bad = store_rows<D, RA>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
+    each_bad_row<RA>(bad, [&](int i, int half) {
         seq::query_row_alone<float, D>(a, q0 + (ty & ~1) + half + 16 * i, h, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
                                        __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
     });
 }
 
-template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, float *sm, uint32_t unit) {
-    float *sK = sm, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>,
-          *sS = sP + kScoreFloats;   // two pairs of Q and dOut tiles
+template <int D, int RA> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, float *sm, uint32_t unit) {
+    float *sK = sm, *sV = sK + kOwnFloats<D, RA>, *sP = sV + kOwnFloats<D, RA>,
+          *sS = sP + kScoreFloats<RA>;   // two pairs of Q and dOut tiles
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const SeqTile t = a.ktiles[unit / a.Hkv];
-    const int hk = unit % a.Hkv, grp = a.H / a.Hkv;
-    const int64_t k0 = (int64_t)t.tile * kT;
+    const Unit<RA> u(unit, a.Hkv);
+    const SeqTile t = a.ktiles[u.tile];
+    const int hk = u.head, grp = a.H / a.Hkv;
+    const int64_t k0 = (int64_t)t.tile * kT + u.row;
     const float scale2 = a.scale * kLog2e;
     const int nt = t.t1 - t.t0, n = nt * grp;   // steps: (head of the group, query tile)
     auto fetch = [&](int i) {
@@ -345,15 +367,15 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, flo
         load_tile<D>(dst, a.Q, q0, a.rows, a.H, hk * grp + i / nt);
         load_tile<D>(dst + kTileFloats<D>, a.dOut, q0, a.rows, a.H, hk * grp + i / nt);
     };
-    load_tile<D>(sK, a.K, k0, a.rows, a.Hkv, hk);
-    load_tile<D>(sV, a.V, k0, a.rows, a.Hkv, hk);
+    load_tile<D, 16 * RA>(sK, a.K, k0, a.rows, a.Hkv, hk);
+    load_tile<D, 16 * RA>(sV, a.V, k0, a.rows, a.Hkv, hk);
     fetch(0);
     tc::cp_commit();
-    int64_t lo[4], hi[4];
+    int64_t lo[RA], hi[RA];
     intervals(a, true, k0, ty, lo, hi);
-    float dk[4][kCols<D>], dv[4][kCols<D>];
+    float dk[RA][kCols<D>], dv[RA][kCols<D>];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RA; ++i)
 #pragma unroll
         for (int x = 0; x < kCols<D>; ++x) dk[i][x] = dv[i][x] = 0.f;
     for (int step = 0; step < n; ++step) {
@@ -361,7 +383,7 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, flo
         const int qt = t.t0 + step % nt;
         const int64_t q0 = (int64_t)qt * kT;
         const bool full = qt >= t.f0 && qt < t.f1;
-        int ql[4], qh[4];
+        int ql[RA], qh[RA];
         in_tile(lo, hi, q0, ql, qh);
         float ls[4], dl[4];
 #pragma unroll
@@ -374,11 +396,11 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, flo
         __syncthreads();   // these tiles; the last dS^T Q is done with the other ones and with dS
         if (step + 1 < n) fetch(step + 1);
         tc::cp_commit();
-        float s[4][4], g[4][4];
-        dot_tiles<D>(s, sK, sQ, ty, tx);
-        dot_tiles<D>(g, sV, sG, ty, tx);
+        float s[RA][4], g[RA][4];
+        dot_tiles<D, RA>(s, sK, sQ, ty, tx);
+        dot_tiles<D, RA>(g, sV, sG, ty, tx);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RA; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int j = tx + 16 * c;
@@ -388,20 +410,25 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, flo
                 g[i][c] = on ? p * (g[i][c] + dl[c]) : 0.f;
             }
         __syncthreads();
-        add_product<D>(dv, sP, sG, ty, tx);
+        add_product<D, RA>(dv, sP, sG, ty, tx);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RA; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sP[(ty + 16 * i) * kPP + tx + 16 * c] = g[i][c];   // dS^T over P^T
         __syncthreads();
-        add_product<D>(dk, sP, sQ, ty, tx);
+        add_product<D, RA>(dk, sP, sQ, ty, tx);
     }
-    const float one[4] = {1.f, 1.f, 1.f, 1.f}, f[4] = {a.scale, a.scale, a.scale, a.scale};
-    const uint32_t bad_v = store_rows<D>(static_cast<float *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
-    const uint32_t bad_k = store_rows<D>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
+    float one[RA], f[RA];
+#pragma unroll
+    for (int i = 0; i < RA; ++i) {
+        one[i] = 1.f;
+        f[i] = a.scale;
+    }
+    const uint32_t bad_v = store_rows<D, RA>(static_cast<float *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
+    const uint32_t bad_k = store_rows<D, RA>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
     for (int x = 0; x < 2; ++x)
-        each_bad_row(x ? bad_k : bad_v, [&](int i, int half) {
+        each_bad_row<RA>(x ? bad_k : bad_v, [&](int i, int half) {
             seq::key_row_alone<float, D>(a, x == 1, k0 + (ty & ~1) + half + 16 * i, hk,
                                          __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
                                          __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
@@ -409,11 +436,11 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, flo
 }
 
 // Both passes in one launch, the dK/dV units (the longer ones) first.
-template <int D> __global__ void __launch_bounds__(kThreads, D == 32 ? 2 : 1) seq_bwd_f32_kernel(const SeqArgs a) {
+template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA, (D == 32)>) seq_bwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
-    const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv;
-    if (blockIdx.x < kv) dkdv_pass<D>(a, sm, blockIdx.x);
-    else dq_pass<D>(a, sm, blockIdx.x - kv);
+    const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv * (4 / RA);
+    if (blockIdx.x < kv) dkdv_pass<D, RA>(a, sm, blockIdx.x);
+    else dq_pass<D, RA>(a, sm, blockIdx.x - kv);
 }
 
 // Row terms: D / EL lanes of 16 bytes a (row, head), four of them in flight.
@@ -452,23 +479,25 @@ template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_term
     }
 }
 
-template <int D> cudaError_t launch_fwd(const SeqArgs &a, cudaStream_t s) {
-    constexpr size_t smem = sizeof(float) * (3 * kTileFloats<D> + kScoreFloats);
-    if (cudaError_t e = allow_smem<seq_fwd_f32_kernel<D>>(smem); e != cudaSuccess) return e;
+template <int D, int RA> cudaError_t launch_fwd(const SeqArgs &a, cudaStream_t s) {
+    constexpr size_t smem = sizeof(float) * (kOwnFloats<D, RA> + 2 * kTileFloats<D> + kScoreFloats<RA>);
+    if (cudaError_t e = allow_smem<seq_fwd_f32_kernel<D, RA>>(smem); e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_FWD, s, false);
-    seq_fwd_f32_kernel<D><<<(unsigned)((int64_t)a.n_tiles * a.H), kThreads, smem, s>>>(a);
+    seq_fwd_f32_kernel<D, RA><<<(unsigned)((int64_t)a.n_tiles * a.H * (4 / RA)), kThreads, smem, s>>>(a);
     note_launch(SGA_KERN_SEQ_FWD, s, true);
     return cudaGetLastError();
 }
 
-template <int D> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
-    constexpr size_t smem = sizeof(float) * (6 * kTileFloats<D> + kScoreFloats);   // (dK/dV; dQ takes a tile less)
+template <int D, int RA> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
+    constexpr size_t kv = sizeof(float) * (2 * kOwnFloats<D, RA> + 4 * kTileFloats<D> + kScoreFloats<RA>);
+    constexpr size_t q = sizeof(float) * (2 * kOwnFloats<D, RA> + 3 * kTileFloats<D> + kScoreFloats<RA>);
+    constexpr size_t smem = kv > q ? kv : q;
     static_assert(smem <= 227 * 1024, "shared memory");
-    cudaError_t e = allow_smem<seq_bwd_f32_kernel<D>>(smem);
+    cudaError_t e = allow_smem<seq_bwd_f32_kernel<D, RA>>(smem);
     if (e == cudaSuccess) e = seq_row_terms<float>(a, D, s);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD, s, false);
-    seq_bwd_f32_kernel<D><<<(unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H)), kThreads, smem, s>>>(a);
+    seq_bwd_f32_kernel<D, RA><<<(unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H) * (4 / RA)), kThreads, smem, s>>>(a);
     note_launch(SGA_KERN_SEQ_BWD, s, true);
     return cudaGetLastError();
 }
@@ -489,11 +518,20 @@ template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStr
 template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t);
 template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
 
+// Owner tiles of 32 rows where 64 would leave SMs without a block; they read
+// twice as much shared memory a product.  32 : 64 rows, forward, D = 64: 512
+// rows, 4 heads (32 units of 64) 36 : 49 us, 1024 rows, 8 heads (128) 105 : 95;
+// backward: 512 rows, 4 heads (64 units) D = 32 40 : 52, D = 64 58 : 74, D = 128
+// 99 : 121; 1024 rows, 4 heads (128), D = 32 95 : 95; 8 heads (256), D = 64 320 : 244.
 cudaError_t seq_fwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
-    return D == 32 ? launch_fwd<32>(a, s) : D == 64 ? launch_fwd<64>(a, s) : launch_fwd<128>(a, s);
+    if (2 * (int64_t)a.n_tiles * a.H <= a.num_sms)
+        return D == 32 ? launch_fwd<32, 2>(a, s) : D == 64 ? launch_fwd<64, 2>(a, s) : launch_fwd<128, 2>(a, s);
+    return D == 32 ? launch_fwd<32, 4>(a, s) : D == 64 ? launch_fwd<64, 4>(a, s) : launch_fwd<128, 4>(a, s);
 }
 cudaError_t seq_bwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
-    return D == 32 ? launch_bwd<32>(a, s) : D == 64 ? launch_bwd<64>(a, s) : launch_bwd<128>(a, s);
+    if ((int64_t)a.n_tiles * (a.H + a.Hkv) <= a.num_sms)
+        return D == 32 ? launch_bwd<32, 2>(a, s) : D == 64 ? launch_bwd<64, 2>(a, s) : launch_bwd<128, 2>(a, s);
+    return D == 32 ? launch_bwd<32, 4>(a, s) : D == 64 ? launch_bwd<64, 4>(a, s) : launch_bwd<128, 4>(a, s);
 }
 
 }  // namespace sga
