@@ -944,6 +944,8 @@ class Embedding(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, ids, table, scale=1.0, padding_idx=None):
+        if padding_idx is not None and not 0 <= padding_idx < table.shape[0]:
+            raise ValueError(f"padding_idx must be in [0, {table.shape[0]}), got {padding_idx}")
         ids = ids.contiguous()
         out = embed_fwd(ids, table.contiguous(), scale)
         ctx.rows, ctx.scale, ctx.padding_idx = table.shape[0], scale, padding_idx

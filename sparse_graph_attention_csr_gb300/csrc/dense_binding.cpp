@@ -7,6 +7,7 @@
 // interpreter time; here they take about half.
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
@@ -99,7 +100,10 @@ void distinct(std::initializer_list<Named> outs, std::initializer_list<Named> in
 
 // A call on tensors of `device`, on `stream` (a torch.cuda.Stream) or the
 // device's current stream: device and stream are current while this lives, so
-// that what is allocated belongs to the stream that writes it.
+// that what is allocated belongs to the stream that writes it.  With a stream
+// given, the allocator is told that the inputs are used on it and the results
+// on the caller's stream: memory that either frees early is not handed out
+// while the other still uses it.
 class Place {
   public:
     Place(at::Device device, const py::object &stream) {
@@ -113,14 +117,28 @@ class Place {
             static_cast<c10::DeviceType>(stream.attr("device_type").cast<int>()));
         if (s.device_index() != device.index())
             throw py::value_error("stream is on cuda:" + std::to_string(s.device_index()) + ", the tensors on " + device.str());
+        caller_ = c10::cuda::getCurrentCUDAStream(device.index());
         on_.emplace(s);
         raw_ = s.stream();
     }
     void *raw() const { return raw_; }
+    void used(std::initializer_list<Named> ins, std::initializer_list<Named> outs) const {
+        if (!caller_ || *caller_ == on_->current_stream()) return;
+        auto note = [](const Named &n, c10::cuda::CUDAStream s) {
+            if (n.t && n.t->numel() > 0)
+                c10::cuda::CUDACachingAllocator::recordStream(n.t->storage().data_ptr(), s);
+        };
+        for (const Named &n : ins) note(n, on_->current_stream());
+        for (const Named &n : outs) {
+            note(n, on_->current_stream());   // (one given by the caller)
+            note(n, *caller_);
+        }
+    }
 
   private:
     std::optional<c10::cuda::CUDAGuard> dev_;
     std::optional<c10::cuda::CUDAStreamGuard> on_;
+    std::optional<c10::cuda::CUDAStream> caller_;
     void *raw_ = nullptr;
 };
 
@@ -177,6 +195,7 @@ py::tuple seq_attn_fwd_(const SeqPlan &p, const Tensor &Q, const Tensor &K, cons
     Tensor l = seq_result(p, lse, "lse", {T, p.H}, at::kFloat, -std::numeric_limits<double>::infinity());
     if (out || lse) distinct({named("out", o), named("lse", l)}, {named("Q", Q), named("K", K), named("V", V)});
     check(seq_attn_fwd(p.handle, ptr(Q), ptr(K), ptr(V), T, f, ptr(o), static_cast<float *>(ptr(l)), on.raw()), "seq_attn_fwd");
+    on.used({named("Q", Q), named("K", K), named("V", V)}, {named("out", o), named("lse", l)});
     return py::make_tuple(std::move(o), std::move(l));
 }
 
@@ -199,6 +218,8 @@ py::tuple seq_attn_bwd_(const SeqPlan &p, const Tensor &Q, const Tensor &K, cons
     check(seq_attn_bwd(p.handle, ptr(Q), ptr(K), ptr(V), ptr(out), static_cast<const float *>(ptr(lse)), ptr(dOut), T, f,
                        ptr(q), ptr(k), ptr(v), ptr(ws), (size_t)p.ws_bytes, on.raw()),
           "seq_attn_bwd");
+    on.used({named("Q", Q), named("K", K), named("V", V), named("out", out), named("lse", lse), named("dOut", dOut)},
+            {named("dQ", q), named("dK", k), named("dV", v)});
     return py::make_tuple(std::move(q), std::move(k), std::move(v));
 }
 
@@ -254,6 +275,7 @@ py::tuple layer_norm_fwd_(const Tensor &X, const Maybe &weight, const Maybe &bia
     check(layer_norm_fwd(ptr(X), ptr(weight), ptr(bias), n.N, n.C, (float)eps, n.dt, n.wdt, ptr(o),
                          static_cast<float *>(ptr(m)), static_cast<float *>(ptr(r)), on.raw()),
           "layer_norm_fwd");
+    on.used({named("X", X), named("weight", weight), named("bias", bias)}, {named("out", o), named("mean", m), named("rstd", r)});
     return py::make_tuple(std::move(o), std::move(m), std::move(r));
 }
 
@@ -287,6 +309,8 @@ py::tuple layer_norm_bwd_(const Tensor &X, const Maybe &weight, const Tensor &me
                          ptr(dOut), n.N, n.C, n.dt, n.wdt, ptr(x), ptr(w), ptr(b), weight ? ptr(ws) : nullptr, bytes,
                          on.raw()),
           "layer_norm_bwd");
+    on.used({named("X", X), named("weight", weight), named("mean", mean), named("rstd", rstd), named("dOut", dOut)},
+            {named("dX", x), named("dweight", w), named("dbias", b)});
     return py::make_tuple(std::move(x), w ? py::cast(*w) : py::none(), b ? py::cast(*b) : py::none());
 }
 
@@ -325,6 +349,7 @@ Tensor embed_fwd_(const Tensor &ids, const Tensor &table, double scale, const Ma
         distinct({named("out", o)}, {named("ids", ids), named("table", table)});
     }
     check(embed_fwd(ptr(ids), b, ptr(table), ids.numel(), V, C, f, dt, ptr(o), on.raw()), "embed_fwd");
+    on.used({named("ids", ids), named("table", table)}, {named("out", o)});
     return o;
 }
 
@@ -350,6 +375,7 @@ Tensor embed_bwd_(const Tensor &ids, const Tensor &dOut, int64_t V, double scale
     const Tensor ws = fresh({(int64_t)bytes}, at::kByte, dev);
     check(embed_bwd(ptr(ids), b, ptr(dOut), N, V, C, f, padding_idx.value_or(-1), dt, ptr(t), ptr(ws), bytes, on.raw()),
           "embed_bwd");
+    on.used({named("ids", ids), named("dOut", dOut)}, {named("dTable", t)});
     return t;
 }
 

@@ -639,7 +639,8 @@ sga_status layer_norm_fwd(const void *X, const void *weight, const void *bias, i
 
 size_t sga_norm_bwd_workspace_bytes(int64_t N, int64_t C) {
     if (N <= 0 || C <= 0) return 0;
-    return (size_t)std::min<int64_t>(bwd_blocks(device_sms()), N) * 2 * (size_t)C * sizeof(float);
+    const int64_t most = C > 4096 ? (N + 15) / 16 : N;   // (wide rows: slabs of at least 16)
+    return (size_t)std::min<int64_t>(bwd_blocks(device_sms()), most) * 2 * (size_t)C * sizeof(float);
 }
 
 sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, const float *rstd, const void *dOut,

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
                         *reinterpret_cast<uint4 *>(out + cb + 8 * q) = pack<__nv_bfloat16>(x + 8 * q);
             }
             if (in) a.lse_w[row * a.H + h] = (m + log2f(l)) * kLn2;
-            uint32_t again = __ballot_sync(SGA_FULL_MASK, bad && in);
+            uint32_t again = __ballot_sync(SGA_FULL_MASK, bad && in && l == l);
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;

@@ -4,7 +4,9 @@
 // The tiled passes multiply the weights of masked pairs, which are zero, with
 // whatever the masked rows hold; an infinity or NaN there would turn the product
 // into NaN.  A pass therefore computes every row whose result is not finite
-// again here.  Nothing is spent on this while the inputs are finite.
+// again here.  Nothing is spent on this while the inputs are finite, nor where
+// the row itself makes every weight NaN (a batch that has gone NaN throughout):
+// its result is NaN with or without the masked pairs.
 #pragma once
 
 #include "seq.h"
@@ -35,6 +37,12 @@ template <typename T, int D> struct RowFrag {
 #pragma unroll
         for (int i = 0; i < W; ++i) x[i] = fmaf(w, o.x[i], x[i]);
     }
+    __device__ __forceinline__ bool has_nan() const {   // (of the whole row)
+        bool b = false;
+#pragma unroll
+        for (int i = 0; i < W; ++i) b |= x[i] != x[i];
+        return __any_sync(SGA_FULL_MASK, b);
+    }
     // store the columns [c0, c0 + n)
     __device__ __forceinline__ void store(void *base, int64_t off, float f, int c0, int n) const {
 #pragma unroll
@@ -45,7 +53,8 @@ template <typename T, int D> struct RowFrag {
     }
 };
 
-// out of one query row over the keys [lo, hi).
+// out of one query row over the keys [lo, hi); the caller leaves out rows whose
+// sum of weights is NaN.
 template <typename T, int D>
 __device__ __forceinline__ void out_row_alone(const SeqArgs &a, int64_t row, int h, int hk, int64_t lo, int64_t hi) {
     RowFrag<T, D> q, k, v, acc;
@@ -74,6 +83,7 @@ __device__ __forceinline__ void key_row_alone(const SeqArgs &a, bool DK, int64_t
     const int64_t at = (row * a.Hkv + hk) * D;
     k.load(a.K, at);
     v.load(a.V, at);
+    if (k.has_nan() || (DK && v.has_nan())) return;   // every score (for dK: or dP) of the row is NaN
     acc.zero();
     const int grp = a.H / a.Hkv;
     for (int h = hk * grp; h < (hk + 1) * grp; ++h)
@@ -96,6 +106,7 @@ __device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, i
     const int hk = h / (a.H / a.Hkv);
     q.load(a.Q, at);
     g.load(a.dOut, at);
+    if (q.has_nan() || g.has_nan()) return;   // every score or dP of the row is NaN
     acc.zero();
     for (int64_t j = lo; j < hi; ++j) {
         k.load(a.K, (j * a.Hkv + hk) * D);

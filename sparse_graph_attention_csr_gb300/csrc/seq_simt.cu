@@ -281,7 +281,10 @@ template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA,
         const int64_t row = q0 + ty + 16 * i;
         if (tx == 0 && row < a.rows) a.lse_w[row * a.H + h] = (m[i] + log2f(l[i])) * kLn2;
     }
-    const uint32_t bad = store_rows<D, RA>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+    uint32_t bad = store_rows<D, RA>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+#pragma unroll
+    for (int i = 0; i < RA; ++i)
+        if (l[i] != l[i]) bad &= ~(1u << i);   // NaN whatever the masked rows hold
     each_bad_row<RA>(bad, [&](int i, int half) {
         seq::out_row_alone<float, D>(a, q0 + (ty & ~1) + half + 16 * i, h, hk, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
                                      __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half));

@@ -172,5 +172,7 @@ def test_refusals():
     for p in (-1, 5):
         with pytest.raises(ValueError):
             sga.embed_bwd(ids, torch.randn(10, 8, device="cuda"), 5, padding_idx=p)
+        with pytest.raises(ValueError):
+            sga.Embedding.apply(ids, table, 1.0, p)   # in the forward, not first in the backward
     with pytest.raises(ValueError):
         sga.embed_bwd(ids, torch.randn(10, 8, device="cuda"), -1)

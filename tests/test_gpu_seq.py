@@ -214,6 +214,49 @@ def test_streams_graphs_and_overlap():
     assert plan.device_error() == 0
 
 
+def test_inputs_freed_while_another_stream_uses_them():
+    """The inputs of a call on a given stream are dropped, and their memory is
+    asked for again, before that stream has begun: the allocator has to hold it."""
+    sp, Q, K, V, dO = make([1500, 700], 4, 4, 64, "bf16")
+    plan = sga.SeqPlan(sp, 4, 64)
+    out, lse = sga.seq_attn_fwd(plan, Q, K, V)
+    ref = sga.seq_attn_bwd(plan, Q, K, V, out, lse, dO)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gate = torch.randn(6000, 6000, device="cuda")
+    x = [t.clone() for t in (Q, K, V, dO)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(8):
+            gate = gate @ gate * 1e-4   # keeps the stream busy for some milliseconds
+    o, l = sga.seq_attn_fwd(plan, *x[:3], stream=s)
+    g = sga.seq_attn_bwd(plan, *x[:3], o, l, x[3], stream=s)
+    shapes = [t.shape for t in x]
+    del x
+    junk = [torch.full(sh, float("nan"), device="cuda", dtype=torch.bfloat16) for sh in shapes for _ in range(2)]
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and all(torch.equal(a, b) for a, b in zip(g, ref))
+    del junk
+
+
+def test_a_batch_that_is_nan_throughout():
+    """Results are NaN, and no row is computed again for it (4096 rows would
+    take seconds)."""
+    for dt in ("bf16", "f32"):
+        sp, Q, K, V, dO = make([4096], 2, 2, 64, dt)
+        for t in (Q, K, V, dO):
+            t.fill_(float("nan"))
+        plan = sga.SeqPlan(sp, 2, 64, DT[dt])
+        t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        t0.record()
+        out, lse = sga.seq_attn_fwd(plan, Q, K, V)
+        g = sga.seq_attn_bwd(plan, Q, K, V, out, lse, dO)
+        t1.record()
+        torch.cuda.synchronize()
+        assert all(torch.isnan(t).all() for t in (out, *g))
+        assert t0.elapsed_time(t1) < 200
+
+
 def test_refusals():
     sp = ptr_of([10, 20])
     for bad in ([1, 5], [0, 5, 4], [0, -1]):
