@@ -453,15 +453,18 @@ constexpr int kTerms = 4;
 template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
     constexpr int EL = Elt<T>::EL, L = D / EL, G = 256 / L;   // G items of a block at a time
     const int sub = threadIdx.x % L;
-    const int64_t n = a.rows_pad * a.H, g0 = (int64_t)blockIdx.x * (G * kTerms) + threadIdx.x / L;
+    const int64_t live = a.rows * a.H, n = a.rows_pad * a.H, g0 = (int64_t)blockIdx.x * (G * kTerms) + threadIdx.x / L;
     uint4 x[kTerms], y[kTerms];
+    float lse[kTerms];
 #pragma unroll
     for (int k = 0; k < kTerms; ++k) {
         const int64_t g = g0 + k * G;
         x[k] = y[k] = make_uint4(0, 0, 0, 0);
-        if (g < a.rows * a.H) {   // (an item's elements follow the one's before)
+        lse[k] = INFINITY;
+        if (g < live) {   // (an item's elements follow the one's before)
             x[k] = ldg16(static_cast<const T *>(a.out) + g * D + sub * EL);
             y[k] = ldg16(static_cast<const T *>(a.dOut) + g * D + sub * EL);
+            if (sub == 0) lse[k] = __ldg(a.lse + g) * kLog2e;
         }
     }
 #pragma unroll
@@ -474,10 +477,11 @@ template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_term
         for (int i = 0; i < EL; ++i) d = fmaf(u[i], v[i], d);
         d = group_sum<L>(d);
         if (sub == 0 && g < n) {
-            const int64_t row = g / a.H, at = (g % a.H) * a.rows_pad + row;
-            const bool in = row < a.rows;
-            a.ws_nlse[at] = in ? -(a.lse[g] * kLog2e) : -INFINITY;
-            a.ws_ndelta[at] = in ? -d : 0.f;
+            // (a 64-bit division takes longer than the rest of an item)
+            const int64_t row = n <= UINT32_MAX ? (int64_t)((uint32_t)g / (uint32_t)a.H) : g / a.H;
+            const int64_t at = (g - row * a.H) * a.rows_pad + row;
+            a.ws_nlse[at] = -lse[k];
+            a.ws_ndelta[at] = g < live ? -d : 0.f;
         }
     }
 }
