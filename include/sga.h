@@ -375,7 +375,7 @@ sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, 
  * reproducible.  Its workspace is 256-byte aligned. */
 sga_status embed_fwd(const void *ids, int id_bytes, const void *table, int64_t N, int64_t V, int64_t C, float scale,
                      sga_dtype dt, void *out, void *stream);
-size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t C);
+size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t V, int64_t C);
 sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N, int64_t V, int64_t C, float scale,
                      int64_t padding_idx, sga_dtype dt, void *dTable, void *workspace, size_t workspace_bytes,
                      void *stream);
@@ -506,8 +506,8 @@ typedef enum {
     SGA_KERN_GAT_FWD = 23, SGA_KERN_GAT_BWD_DST = 24, SGA_KERN_GAT_BWD_SRC = 25,
     SGA_KERN_SEQ_FWD = 26, SGA_KERN_SEQ_BWD_ROWS = 27, SGA_KERN_SEQ_BWD = 28,
     SGA_KERN_NORM_FWD = 29, SGA_KERN_NORM_BWD = 30, SGA_KERN_NORM_REDUCE = 31,
-    SGA_KERN_EMBED_FWD = 32, SGA_KERN_EMBED_BWD = 33,
-    SGA_KERN_COUNT = 34
+    SGA_KERN_EMBED_FWD = 32, SGA_KERN_EMBED_BWD = 33, SGA_KERN_EMBED_ADD = 34,
+    SGA_KERN_COUNT = 35
 } sga_kernel_id;
 /* (Planned GATv2 passes merge their split rows inside the edge kernels --
  * the last chunk of a row to finish merges it -- so SGA_KERN_GATV2_FWD_MERGE

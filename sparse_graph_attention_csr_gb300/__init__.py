@@ -38,7 +38,7 @@ KERNELS = {
     "bsr_bwd_dkdv": 18, "agg_fwd": 19, "agg_fwd_merge": 20, "agg_bwd": 21, "agg_bwd_merge": 22,
     "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25, "seq_fwd": 26, "seq_bwd_rows": 27,
     "seq_bwd": 28, "norm_fwd": 29, "norm_bwd": 30, "norm_reduce": 31, "embed_fwd": 32,
-    "embed_bwd": 33,
+    "embed_bwd": 33, "embed_add": 34,
 }
 
 SGA_LAYER_ATTENTION, SGA_LAYER_MINMAX, SGA_LAYER_GAT = 0, 1, 2
@@ -136,7 +136,7 @@ _SIGNATURES = {
     "layer_norm_bwd": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp,
                         ctypes.c_size_t, _vp], _int),
     "embed_fwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _int, _vp, _vp], _int),
-    "sga_embed_bwd_workspace_bytes": ([_i64, _i64], ctypes.c_size_t),
+    "sga_embed_bwd_workspace_bytes": ([_i64, _i64, _i64], ctypes.c_size_t),
     "embed_bwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _i64, _int, _vp, _vp, ctypes.c_size_t,
                    _vp], _int),
     "sga_embed_read_device_error": ([_vp, ctypes.POINTER(ctypes.c_int32)], _int),

@@ -371,7 +371,7 @@ Tensor embed_bwd_(const Tensor &ids, const Tensor &dOut, int64_t V, double scale
         need(t, "dTable", dev, dOut.scalar_type(), {V, C});
         distinct({named("dTable", t)}, {named("ids", ids), named("dOut", dOut)});
     }
-    const size_t bytes = sga_embed_bwd_workspace_bytes(N, C);
+    const size_t bytes = sga_embed_bwd_workspace_bytes(N, V, C);
     const Tensor ws = fresh({(int64_t)bytes}, at::kByte, dev);
     check(embed_bwd(ptr(ids), b, ptr(dOut), N, V, C, f, padding_idx.value_or(-1), dt, ptr(t), ptr(ws), bytes, on.raw()),
           "embed_bwd");

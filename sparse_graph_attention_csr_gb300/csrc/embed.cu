@@ -11,6 +11,7 @@
 // block adds the row's partials in chunk order.  No float atomics: the sums'
 // order is fixed and results are bitwise reproducible.
 #include <algorithm>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -114,7 +115,7 @@ struct GradArgs {
     int32_t *hist;              // [digit][block] counts
     float *part;                // [chunks][2][C]: the row that runs on from the chunk before, the row that runs on
     int64_t N, V, chunks, padding;
-    int wide, L, C, bits, passes, gshift;
+    int wide, L, C, bits, passes, gshift, few;
     float scale;
 };
 
@@ -481,6 +482,112 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
     else join_rows<T, 1>(a, reinterpret_cast<float *>(cnt), who);
 }
 
+// Few rows (atom or edge types) and few tokens: no sort.  A block takes
+// consecutive tokens; each of its warps owns every 32nd row and adds the row's
+// tokens in order, found by a vote over the block's ids, so nothing is shared.
+// Then a warp adds the blocks' sums.  30011 tokens x 100 fp32 into 119 rows:
+// 18 us a call, 28 sorted.
+constexpr int kFewRows = 256, kFewTokens = 512;   // rows; tokens of a block
+
+template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const GradArgs a, int64_t per) {
+    constexpr int EL = kEl<T, VEC>, M = VEC ? 8 : 4, U = VEC ? 1 : 4;   // M tokens in flight, of U groups each
+    __shared__ int32_t id[kFewTokens];
+    __shared__ uint16_t list[kSortWarps][kFewTokens];   // a warp's tokens, by row and in order: token | row / 32 << 9
+    static_assert(kFewTokens <= 512 && kFewRows <= 32 * 128, "list entries");
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, V = (int)a.V, n = a.C / EL;
+    const int64_t t0 = min(a.N, blockIdx.x * per);
+    const int cnt = (int)min(per, a.N - t0);
+    for (int i = threadIdx.x; i < kFewTokens; i += kSortThreads) id[i] = i < cnt ? key_of(a, t0 + i) : V;
+    __syncthreads();
+    const T *dOut = static_cast<const T *>(a.dOut) + t0 * a.C;
+    float *part = a.part + ((int64_t)blockIdx.x * V + wp) * a.C;   // the warp's first row; the next is 32 rows on
+    int total = 0;
+    for (int q = 0; wp + 32 * q < V; ++q) {
+        const int before = total;
+        for (int b = 0; b < cnt; b += 32) {
+            const bool on = id[b + lane] == wp + 32 * q;
+            const uint32_t who = __ballot_sync(SGA_FULL_MASK, on);
+            if (on) list[wp][total + __popc(who & ((1u << lane) - 1u))] = (uint16_t)((b + lane) | q << 9);
+            total += __popc(who);
+        }
+        if (total == before)   // a row without a token here
+            for (int c = lane; c < a.C; c += 32) part[(int64_t)32 * q * a.C + c] = 0.f;
+    }
+    __syncwarp();
+    for (int g0 = lane; g0 - lane < n; g0 += 32 * U) {
+        float acc[U][EL];
+        int cur = -1;
+        auto flush = [&] {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < EL; ++i) {
+                    if (cur >= 0 && g0 + 32 * u < n) part[(int64_t)32 * cur * a.C + (g0 + 32 * u) * EL + i] = acc[u][i];
+                    acc[u][i] = 0.f;
+                }
+        };
+        flush();
+        for (int k = 0; k < total; k += M) {
+            uint4 raw[M][U];
+            int row[M];
+#pragma unroll
+            for (int z = 0; z < M; ++z) {
+                const int e = k + z < total ? list[wp][k + z] : -1;
+                row[z] = e >> 9;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    raw[z][u] = make_uint4(0, 0, 0, 0);
+                    if (e < 0 || g0 + 32 * u >= n) continue;
+                    const T *p = dOut + (int64_t)(e & 511) * a.C + (int64_t)(g0 + 32 * u) * EL;
+                    if constexpr (VEC) raw[z][u] = ldg16_stream(p);
+                    else raw[z][u].x = __float_as_uint(to_f32<T>(__ldg(p)));
+                }
+            }
+#pragma unroll
+            for (int z = 0; z < M; ++z) {
+                if (row[z] < 0) break;
+                if (row[z] != cur) {
+                    flush();
+                    cur = row[z];
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[EL];
+                    if constexpr (VEC) unpack<T>(raw[z][u], x);
+                    else x[0] = __uint_as_float(raw[z][u].x);
+#pragma unroll
+                    for (int i = 0; i < EL; ++i) acc[u][i] += x[i];
+                }
+            }
+        }
+        flush();
+    }
+}
+
+// The blocks' sums of every row: a warp per W columns of a row, its lanes take
+// every 32nd block's.
+template <typename T, int W> __global__ void __launch_bounds__(256) embed_add_few_kernel(const GradArgs a, int B) {
+    const int lane = threadIdx.x & 31;
+    const int64_t stride = a.V * a.C, it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (it >= stride / W) return;
+    Cols<W> s;
+    s.zero();
+    for (int b0 = 0; b0 < B; b0 += 160) {
+        Cols<W> x[5];
+#pragma unroll
+        for (int z = 0; z < 5; ++z) {
+            x[z].zero();
+            const int b = b0 + 32 * z + lane;
+            if (b < B) x[z].load(a.part + b * stride + it * W);
+        }
+#pragma unroll
+        for (int z = 0; z < 5; ++z) s.add(x[z]);
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) s.x[i] = group_sum<32>(s.x[i]);
+    if (lane == 0) s.store(static_cast<T *>(a.dTable) + it * W, a.scale);
+}
+
 // Blocks of the gradient's launch: one an SM, fewer where that leaves them under 256 tokens.
 int grad_blocks(int64_t N, int sms) { return (int)std::min<int64_t>(sms, std::max<int64_t>(1, (N + 255) / 256)); }
 
@@ -488,6 +595,14 @@ int grad_blocks(int64_t N, int sms) { return (int)std::min<int64_t>(sms, std::ma
 int chunk_len(int64_t N, int sms) {
     const int64_t per = (N + (int64_t)sms * kSortWarps - 1) / ((int64_t)sms * kSortWarps);
     return (int)std::max<int64_t>(16, (per + 3) / 4 * 4);
+}
+
+// Tokens of a block where the gradient goes without the sort (0: it is sorted):
+// a block an SM, but as many tokens as rows, so that the blocks' sums are no
+// more than the tokens, and at least 128.
+int few_tokens(int64_t N, int64_t V, int sms) {
+    const int64_t per = std::max<int64_t>(std::max<int64_t>(128, V), (N + sms - 1) / sms);
+    return V > 0 && V <= kFewRows && V <= N && per <= kFewTokens ? (int)per : 0;
 }
 
 int bits_of(int64_t v) {
@@ -499,7 +614,7 @@ int bits_of(int64_t v) {
 struct Layout {
     size_t key[2], tok[2], hist, part, bytes;
 };
-Layout layout(int64_t N, int64_t C, int sms) {
+Layout layout(int64_t N, int64_t V, int64_t C, int sms) {
     Layout l{};
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -507,6 +622,11 @@ Layout layout(int64_t N, int64_t C, int sms) {
         off += round256(bytes);
         return at;
     };
+    if (const int per = few_tokens(N, V, sms)) {
+        l.part = take((size_t)((N + per - 1) / per) * V * C * 4);
+        l.bytes = off;
+        return l;
+    }
     for (int i = 0; i < 2; ++i) {
         l.key[i] = take((size_t)N * 4 + 16);
         l.tok[i] = take((size_t)N * 4 + 16);
@@ -522,6 +642,19 @@ template <typename T, bool VEC> cudaError_t grad_t(GradArgs a, int blocks, cudaS
     const int n = a.C / kEl<T, VEC>;
     a.gshift = 0;
     while (a.gshift < 5 && (1 << a.gshift) < n) ++a.gshift;
+    if (a.few) {
+        blocks = (int)((a.N + a.few - 1) / a.few);
+        note_launch(SGA_KERN_EMBED_BWD, s, false);
+        embed_grad_few_kernel<T, VEC><<<(unsigned)blocks, kSortThreads, 0, s>>>(a, a.few);
+        note_launch(SGA_KERN_EMBED_BWD, s, true);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+        const int64_t warps = a.V * a.C / (a.C % 4 == 0 ? 4 : 1);
+        note_launch(SGA_KERN_EMBED_ADD, s, false);
+        if (a.C % 4 == 0) embed_add_few_kernel<T, 4><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(a, blocks);
+        else embed_add_few_kernel<T, 1><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(a, blocks);
+        note_launch(SGA_KERN_EMBED_ADD, s, true);
+        return cudaGetLastError();
+    }
     void *args[] = {&a};
     note_launch(SGA_KERN_EMBED_BWD, s, false);
     const cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(embed_grad_kernel<T, VEC>), dim3(blocks),
@@ -577,8 +710,8 @@ sga_status embed_fwd(const void *ids, int id_bytes, const void *table, int64_t N
                          : fwd_t<__nv_bfloat16, false>(ids, wide, table, N, V, (int)C, scale, out, s));
 }
 
-size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t C) {
-    return N <= 0 || C <= 0 || N >= INT32_MAX ? 0 : layout(N, C, device_sms()).bytes;
+size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t V, int64_t C) {
+    return N <= 0 || V < 0 || C <= 0 || N >= INT32_MAX ? 0 : layout(N, V, C, device_sms()).bytes;
 }
 
 sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N, int64_t V, int64_t C, float scale,
@@ -592,7 +725,7 @@ sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (N == 0) return status_of(V > 0 ? cudaMemsetAsync(dTable, 0, (size_t)V * C * e, s) : cudaSuccess);
     const int sms = device_sms();
-    const Layout l = layout(N, C, sms);
+    const Layout l = layout(N, V, C, sms);
     if (!workspace || !aligned(workspace, 256)) return SGA_EINVAL;
     if (workspace_bytes < l.bytes) return SGA_EWORKSPACE;
     char *ws = static_cast<char *>(workspace);
@@ -613,6 +746,7 @@ sga_status embed_bwd(const void *ids, int id_bytes, const void *dOut, int64_t N,
     a.L = chunk_len(N, sms);
     a.chunks = (N + a.L - 1) / a.L;
     a.padding = padding_idx;
+    a.few = few_tokens(N, V, sms);
     a.scale = scale;
     const int bits = bits_of(V);
     a.passes = (bits + 7) / 8;

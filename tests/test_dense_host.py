@@ -74,5 +74,5 @@ def test_embedding_arguments():
     bwd = lambda d=P, t=P, ws=P, n=1 << 40: lib.embed_bwd(P, 4, d, 4, 5, 8, 1.0, -1, 0, t, ws, n, None)
     assert bwd(d=None) == sga.SGA_EINVAL and bwd(t=None) == sga.SGA_EINVAL and bwd(ws=None) == sga.SGA_EINVAL
     assert bwd(n=0) == sga.SGA_EWORKSPACE
-    assert lib.sga_embed_bwd_workspace_bytes(0, 8) == 0
+    assert lib.sga_embed_bwd_workspace_bytes(0, 5, 8) == 0
     assert lib.sga_embed_read_device_error(None, None) == sga.SGA_EINVAL
