@@ -189,6 +189,30 @@ inline int device_sms() {
 
 void note_launch(sga_kernel_id which, cudaStream_t s, bool after);
 
+// Two kernels of one call, the second of which needs the first's results: the
+// second is launched while the first still runs (its blocks take their places as
+// the first's leave room) and waits for its end and its writes before it reads
+// them.  The first calls first_of_two() (it may, early), the second
+// second_of_two() before it touches memory that the first writes.
+__device__ __forceinline__ void first_of_two() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void second_of_two() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_second(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A &...args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    (void)cudaLaunchKernelEx(&cfg, kernel, args...);
+    return cudaGetLastError();   // as after <<<>>>: read and cleared
+}
+
 // Let Kernel launch with `smem` bytes of dynamic shared memory: raises the
 // kernel's limit whenever a launch needs more than any before it (kernels whose
 // size depends on the call's shape would otherwise keep the first call's limit

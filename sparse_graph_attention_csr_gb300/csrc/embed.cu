@@ -494,6 +494,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
     __shared__ int32_t id[kFewTokens];
     __shared__ uint16_t list[kSortWarps][kFewTokens];   // a warp's tokens, by row and in order: token | row / 32 << 9
     static_assert(kFewTokens <= 512 && kFewRows <= 32 * 128, "list entries");
+    first_of_two();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, V = (int)a.V, n = a.C / EL;
     const int64_t t0 = min(a.N, blockIdx.x * per);
     const int cnt = (int)min(per, a.N - t0);
@@ -567,6 +568,7 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
 // The blocks' sums of every row: a warp per W columns of a row, its lanes take
 // every 32nd block's.
 template <typename T, int W> __global__ void __launch_bounds__(256) embed_add_few_kernel(const GradArgs a, int B) {
+    second_of_two();
     const int lane = threadIdx.x & 31;
     const int64_t stride = a.V * a.C, it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (it >= stride / W) return;
@@ -650,10 +652,10 @@ template <typename T, bool VEC> cudaError_t grad_t(GradArgs a, int blocks, cudaS
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
         const int64_t warps = a.V * a.C / (a.C % 4 == 0 ? 4 : 1);
         note_launch(SGA_KERN_EMBED_ADD, s, false);
-        if (a.C % 4 == 0) embed_add_few_kernel<T, 4><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(a, blocks);
-        else embed_add_few_kernel<T, 1><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(a, blocks);
+        const cudaError_t e = launch_second(a.C % 4 == 0 ? embed_add_few_kernel<T, 4> : embed_add_few_kernel<T, 1>,
+                                            dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, a, blocks);
         note_launch(SGA_KERN_EMBED_ADD, s, true);
-        return cudaGetLastError();
+        return e;
     }
     void *args[] = {&a};
     note_launch(SGA_KERN_EMBED_BWD, s, false);

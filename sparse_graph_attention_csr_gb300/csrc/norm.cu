@@ -211,6 +211,7 @@ template <typename TX, typename TW, int EL, int TPR, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
     __shared__ float red[2][32];
     extern __shared__ float acc_sm[];   // [2][C] sums of the block's groups
+    first_of_two();
     constexpr int GPB = THREADS / TPR;
     const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int nvec = a.C / EL;
@@ -294,6 +295,7 @@ constexpr int kRingThreads = 128, kRingStages = 6;
 template <typename TX, typename TW, int TPR, int NV>
 __global__ void __launch_bounds__(kRingThreads, 4) norm_bwd_ring_kernel(const NormArgs a) {
     constexpr int EL = Elt<TX>::EL, GPB = kRingThreads / TPR;
+    first_of_two();
     extern __shared__ __align__(16) unsigned char ring_sm[];   // [stage][vector][x, dy][thread] 16 bytes; then [2][C] sums
     const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int nvec = a.C / EL;
@@ -431,6 +433,7 @@ template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_
 
 // Column sums of wide rows: a thread per column over the rows of a slab.
 template <typename TX> __global__ void __launch_bounds__(256) norm_cols_wide_kernel(const NormArgs a, int64_t slab) {
+    first_of_two();
     const int c = blockIdx.x * 256 + threadIdx.x;
     const int64_t r0 = (int64_t)blockIdx.y * slab, r1 = min(a.N, r0 + slab);
     if (c >= a.C) return;
@@ -451,6 +454,7 @@ template <typename TX> __global__ void __launch_bounds__(256) norm_cols_wide_ker
 template <typename TW> __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ part, int blocks,
                                                                                   int C, TW *dw, TW *db) {
     __shared__ float sm[32][33];
+    second_of_two();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane, n = 2 * (int64_t)C;   // column of [dw | db]
     float s = 0.f;
@@ -585,9 +589,10 @@ template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bo
     }
     if (e != cudaSuccess || !a.part) return e;
     note_launch(SGA_KERN_NORM_REDUCE, s, false);
-    norm_reduce_kernel<TW><<<(unsigned)((2 * (int64_t)a.C + 31) / 32), 1024, 0, s>>>(a.part, blocks, a.C, dw, db);
+    e = launch_second(norm_reduce_kernel<TW>, dim3((unsigned)((2 * (int64_t)a.C + 31) / 32)), dim3(1024), 0, s,
+                      static_cast<const float *>(a.part), blocks, a.C, dw, db);
     note_launch(SGA_KERN_NORM_REDUCE, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 sga_status check_norm(int64_t N, int64_t C, sga_dtype dt, sga_dtype wdt) {

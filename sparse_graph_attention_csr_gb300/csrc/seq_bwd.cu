@@ -202,6 +202,7 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    second_of_two();   // the row terms
     const uint32_t tS = tmem_base + C::TS, tP = tmem_base + C::TP, tK = tmem_base + C::TK, tV = tmem_base + C::TV;
 
     if (warp < 4) {
@@ -419,6 +420,7 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    second_of_two();   // the row terms
     const uint32_t tS = tmem_base + C::TS, tP = tmem_base + C::TP, tQ = tmem_base + C::TQ, tA = tmem_base + C::TA,
                    tG = tmem_base + C::TG;
 
@@ -633,9 +635,9 @@ template <int D> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
     if (e == cudaSuccess) e = seq_row_terms<__nv_bfloat16>(a, D, s);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD, s, false);
-    seq_bwd_kernel<D><<<(unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H)), kThreads, smem, s>>>(prm);
+    e = launch_second(seq_bwd_kernel<D>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H))), dim3(kThreads), smem, s, prm);
     note_launch(SGA_KERN_SEQ_BWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

@@ -441,6 +441,7 @@ template <int D, int RA> __device__ __forceinline__ void dkdv_pass(const SeqArgs
 // Both passes in one launch, the dK/dV units (the longer ones) first.
 template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA, (D == 32)>) seq_bwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
+    second_of_two();
     const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv * (4 / RA);
     if (blockIdx.x < kv) dkdv_pass<D, RA>(a, sm, blockIdx.x);
     else dq_pass<D, RA>(a, sm, blockIdx.x - kv);
@@ -451,6 +452,7 @@ template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA,
 // that their weights are zero, and Delta = 0.
 constexpr int kTerms = 4;
 template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
+    first_of_two();
     constexpr int EL = Elt<T>::EL, L = D / EL, G = 256 / L;   // G items of a block at a time
     const int sub = threadIdx.x % L;
     const int64_t live = a.rows * a.H, n = a.rows_pad * a.H, g0 = (int64_t)blockIdx.x * (G * kTerms) + threadIdx.x / L;
@@ -504,9 +506,10 @@ template <int D, int RA> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s
     if (e == cudaSuccess) e = seq_row_terms<float>(a, D, s);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD, s, false);
-    seq_bwd_f32_kernel<D, RA><<<(unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H) * (4 / RA)), kThreads, smem, s>>>(a);
+    e = launch_second(seq_bwd_f32_kernel<D, RA>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H) * (4 / RA))),
+                      dim3(kThreads), smem, s, a);
     note_launch(SGA_KERN_SEQ_BWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T, int D> cudaError_t launch_terms(const SeqArgs &a, cudaStream_t s) {
