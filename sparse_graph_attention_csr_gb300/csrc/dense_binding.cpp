@@ -167,9 +167,9 @@ int64_t seq_inputs(const SeqPlan &p, const Tensor &Q, const Tensor &K, const Ten
 
 float seq_scale(const SeqPlan &p, std::optional<double> scale) {
     if (!scale) return (float)(1.0 / std::sqrt((double)p.D));
-    const float f = (float)*scale;
-    if (!(*scale > 0.0) || !(*scale < std::numeric_limits<double>::infinity()))
-        throw py::value_error("scale must be positive and finite, got " + std::to_string(*scale));
+    const float f = (float)*scale;   // (a double may overflow, or round to zero)
+    if (!(f > 0.f) || !std::isfinite(f))
+        throw py::value_error("scale must be a positive and finite float32, got " + std::to_string(*scale));
     return f;
 }
 
@@ -324,8 +324,9 @@ int id_bytes(const Tensor &ids) {
     return (int)ids.element_size();
 }
 float embed_scale(double scale) {
-    if (!std::isfinite(scale)) throw py::value_error("scale must be finite, got " + std::to_string(scale));
-    return (float)scale;
+    const float f = (float)scale;   // (a double may overflow)
+    if (!std::isfinite(f)) throw py::value_error("scale must be a finite float32, got " + std::to_string(scale));
+    return f;
 }
 at::DimVector with_width(const Tensor &ids, int64_t C) {
     at::DimVector s(ids.sizes());

@@ -659,10 +659,10 @@ template <typename T, bool VEC> cudaError_t grad_t(GradArgs a, int blocks, cudaS
     }
     void *args[] = {&a};
     note_launch(SGA_KERN_EMBED_BWD, s, false);
-    const cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(embed_grad_kernel<T, VEC>), dim3(blocks),
-                                                      dim3(kSortThreads), args, 0, s);
+    (void)cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(embed_grad_kernel<T, VEC>), dim3(blocks),
+                                      dim3(kSortThreads), args, 0, s);
     note_launch(SGA_KERN_EMBED_BWD, s, true);
-    return e;
+    return cudaGetLastError();
 }
 
 sga_status check_embed(int64_t N, int64_t V, int64_t C, sga_dtype dt, int id_bytes) {

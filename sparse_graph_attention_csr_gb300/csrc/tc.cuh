@@ -100,16 +100,6 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t tmem_d, uint64_t adesc, uin
         ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A's rows are TMEM lanes, two bf16 of K to a
-// 32-bit column (a 16-deep k-step spans eight columns).
-__device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
 // Arrive on the mbarrier once all previously issued MMAs of this thread finish.
 __device__ __forceinline__ void mma_commit(uint64_t *mbar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
@@ -207,7 +197,9 @@ template <int N> __device__ __forceinline__ void reg_inc() {
 // same) lane issues.  Operands that are the same in every lane stay in uniform
 // registers; in a branch that a single lane takes, the compiler moves each of
 // them there again for every product (measured on the attention forward: about
-// 120 cycles a product, twice what the tensor core takes for it).
+// 120 cycles a product, twice what the tensor core takes for it).  _ts: D[tmem]
+// (+)= A[tmem] * B[smem], A's rows in the TMEM lanes, two bf16 of K to a 32-bit
+// column (a 16-deep k-step spans eight columns).
 
 __device__ __forceinline__ void mma_bf16_ss_w(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                               uint32_t accumulate) {

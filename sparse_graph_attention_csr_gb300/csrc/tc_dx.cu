@@ -310,10 +310,6 @@ __global__ void __launch_bounds__(kDwThreads, 1) tc_dw_kernel(const __grid_const
 
 }  // namespace
 
-namespace {
-
-}  // namespace
-
 // The driver's tensor-map encoder, looked up once through the runtime.
 cudaError_t tmap_encoder(PFN_cuTensorMapEncodeTiled_v12000 &out) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;

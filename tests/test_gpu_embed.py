@@ -176,3 +176,12 @@ def test_refusals():
             sga.Embedding.apply(ids, table, 1.0, p)   # in the forward, not first in the backward
     with pytest.raises(ValueError):
         sga.embed_bwd(ids, torch.randn(10, 8, device="cuda"), -1)
+
+
+@pytest.mark.parametrize("scale", [1e39, -1e39])
+def test_scale_past_float32(scale):
+    ids, table = zipf(10, 5, torch.int64), torch.randn(5, 8, device="cuda")
+    with pytest.raises(ValueError, match="scale"):
+        sga.embed_fwd(ids, table, scale)
+    with pytest.raises(ValueError, match="scale"):
+        sga.embed_bwd(ids, torch.randn(10, 8, device="cuda"), 5, scale)

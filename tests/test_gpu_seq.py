@@ -287,3 +287,11 @@ def test_refusals():
     off = torch.empty(30 * 2 * 64 + 1, device="cuda").bfloat16()[1:].view(30, 2, 64)
     with pytest.raises(sga.SgaError):
         sga.seq_attn_fwd(plan, off, K, K)
+
+
+@pytest.mark.parametrize("scale", [1e39, 1e-60])
+def test_scale_past_float32(scale):
+    plan = sga.SeqPlan(ptr_of([10, 20]), 2, 64)
+    Q = torch.randn(30, 2, 64, device="cuda").bfloat16()
+    with pytest.raises(ValueError, match="scale"):
+        sga.seq_attn_fwd(plan, Q, Q, Q, scale)
