@@ -4,14 +4,15 @@
 // The tensor cores have no fp32 product, and the tolerance of the fp32 layers
 // (1e-5) rules out tf32, so these kernels are bound by the FMA pipes (two
 // products of the forward, three and four of the backward's two passes).
-// Blocks of 256 threads (16 x 16) take 16 RA rows of one side (RA = 4: a 64-row
-// tile; RA = 2: half of one) and walk the 64-row tiles of the other through
-// shared memory, the next tiles copied while one is in use; each thread holds an
-// RA x 4 piece of the scores and an RA x D/16 piece of the result.  Tiles are row-major with rows of D + 4 floats: both
-// products read them 16 bytes at a time along a row without bank conflicts, so
-// no tile is stored transposed.  Two blocks an SM where registers and shared
-// memory allow (forward, 2048 rows, 8 heads of 64, full: 366 -> 285 us, 30
-// TFLOP/s; backward with D = 32 593 -> 496 us; with D = 64 it spills and loses).
+// Blocks of TY x 16 threads take TY RA rows of one side (a 64-row tile or a part
+// of one) and walk the 64-row tiles of the other through shared memory, the next
+// tiles copied while one is in use; each thread holds an RA x 4 piece of the
+// scores and an RA x D/16 piece of the result.  Tiles are row-major with rows of
+// D + 4 floats: both products read them 16 bytes at a time along a row without
+// bank conflicts, so no tile is stored transposed.  RA = 4 reads half as much
+// shared memory a product as RA = 2, and 128 threads leave a thread the
+// registers to read ahead: 2048 rows, 8 heads of 64, full, forward 275 us (31
+// TFLOP/s), backward 798 (938 with 256 threads).
 //   forward: S = Q K^T, online softmax (running maximum and sum per row),
 //     O = O alpha + P V;
 //   dQ pass (a tile of queries): S, dP = dOut V^T, dS = P (dP - Delta),
@@ -22,7 +23,7 @@
 // is owned by one block: no atomics, bitwise reproducible.
 // A row whose result is not finite is computed again over its own interval alone
 // (seq_rows.cuh).  Leaving masked pairs out of every sum instead, with a test a
-// pair, took 78 instead of 66 us on five sequences of 1 to 512 rows, D = 32.
+// pair, took a fifth longer on five sequences of 1 to 512 rows, D = 32.
 #include "seq_rows.cuh"
 #include "tc.cuh"
 
@@ -30,20 +31,19 @@ namespace sga {
 namespace {
 
 constexpr int kT = 64;         // rows of a tile
-constexpr int kThreads = 256;
 constexpr int kPP = kT + 4;    // pitch of a score tile
 
 template <int D> constexpr int kPitch = D + 4;
 template <int D> constexpr int kTileFloats = kT * (D + 4);
-template <int D, int RA> constexpr int kOwnFloats = 16 * RA * (D + 4);   // an owner tile: 16 RA rows
-template <int RA> constexpr int kScoreFloats = 16 * RA * kPP;
+template <int D, int RA, int TY> constexpr int kOwnFloats = TY * RA * (D + 4);   // an owner tile: TY RA rows
+template <int RA, int TY> constexpr int kScoreFloats = TY * RA * kPP;
 
 // rows [r0, r0 + ROWS) of head h of a [T][heads][D] tensor, asynchronously (rows
 // past `rows` as zeros)
-template <int D, int ROWS = kT>
+template <int D, int TY, int ROWS = kT>
 __device__ __forceinline__ void load_tile(float *dst, const void *src, int64_t r0, int64_t rows, int heads, int h) {
     constexpr int C4 = D / 4;
-    for (int i = threadIdx.x; i < ROWS * C4; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * C4; i += 16 * TY) {
         const int r = i / C4, c = i % C4;
         const bool in = r0 + r < rows;
         tc::cp16(tc::smem_u32(dst + r * kPitch<D> + 4 * c),
@@ -52,18 +52,18 @@ __device__ __forceinline__ void load_tile(float *dst, const void *src, int64_t r
 }
 
 // s[a][c] = row (ty + 16 a) of A . row (tx + 16 c) of B
-template <int D, int RA>
+template <int D, int RA, int TY>
 __device__ __forceinline__ void dot_tiles(float (&s)[RA][4], const float *A, const float *B, int ty, int tx) {
     float2 acc[RA][4];
 #pragma unroll
     for (int a = 0; a < RA; ++a)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[a][c] = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int d = 0; d < D; d += 4) {
         float4 x[RA], y[4];
 #pragma unroll
-        for (int a = 0; a < RA; ++a) x[a] = *reinterpret_cast<const float4 *>(A + (ty + 16 * a) * kPitch<D> + d);
+        for (int a = 0; a < RA; ++a) x[a] = *reinterpret_cast<const float4 *>(A + (ty + TY * a) * kPitch<D> + d);
 #pragma unroll
         for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4 *>(B + (tx + 16 * c) * kPitch<D> + d);
 #pragma unroll
@@ -105,14 +105,14 @@ template <int D> __device__ __forceinline__ void load_cols(float (&v)[kCols<D>],
 }
 
 // acc[a][x] += sum_j P[ty + 16 a][j] B[j][col x] over the 64 rows of B
-template <int D, int RA>
+template <int D, int RA, int TY>
 __device__ __forceinline__ void add_product(float (&acc)[RA][kCols<D>], const float *P, const float *B, int ty, int tx) {
     constexpr int NC = kCols<D>;
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < kT; j += 4) {
         float4 p[RA];
 #pragma unroll
-        for (int a = 0; a < RA; ++a) p[a] = *reinterpret_cast<const float4 *>(P + (ty + 16 * a) * kPP + j);
+        for (int a = 0; a < RA; ++a) p[a] = *reinterpret_cast<const float4 *>(P + (ty + TY * a) * kPP + j);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             float v[NC];
@@ -125,13 +125,13 @@ __device__ __forceinline__ void add_product(float (&acc)[RA][kCols<D>], const fl
 
 // Stores the rows, scaled, and returns whether any element of this thread's row
 // a was not finite, as bit a.
-template <int D, int RA>
+template <int D, int RA, int TY>
 __device__ __forceinline__ uint32_t store_rows(float *dst, const float (&acc)[RA][kCols<D>], const float (&f)[RA], int64_t r0,
                                                int64_t rows, int heads, int h, int ty, int tx) {
     uint32_t bad = 0;
 #pragma unroll
     for (int a = 0; a < RA; ++a) {
-        const int64_t row = r0 + ty + 16 * a;
+        const int64_t row = r0 + ty + TY * a;
         if (row >= rows) continue;
         float *o = dst + (row * heads + h) * D;
 #pragma unroll
@@ -144,9 +144,9 @@ __device__ __forceinline__ uint32_t store_rows(float *dst, const float (&acc)[RA
     return bad;
 }
 
-// Calls redo(a, half) for every row (ty + 16 a of the warp's half) of which a
+// Calls redo(a, half) for every row (ty + TY a of the warp's half) of which a
 // thread found an element that is not finite; the warp together, after its stores.
-template <int RA, typename F> __device__ __forceinline__ void each_bad_row(uint32_t bad, F redo) {
+template <int RA, int TY, typename F> __device__ __forceinline__ void each_bad_row(uint32_t bad, F redo) {
     if (!__any_sync(SGA_FULL_MASK, bad != 0)) return;
     __syncwarp();
 #pragma unroll
@@ -170,11 +170,11 @@ __device__ __forceinline__ float half_sum(float v) {
 
 // What each of a thread's rows sees: queries of a key row, or keys of a
 // query row.  Rows past the last see nothing.
-template <int RA>
+template <int RA, int TY>
 __device__ __forceinline__ void intervals(const SeqArgs &a, bool keys, int64_t r0, int ty, int64_t (&lo)[RA], int64_t (&hi)[RA]) {
 #pragma unroll
     for (int i = 0; i < RA; ++i) {
-        const int64_t row = r0 + ty + 16 * i;
+        const int64_t row = r0 + ty + TY * i;
         lo[i] = hi[i] = 0;
         if (row < a.rows) {
             const int2 se = __ldg(a.range + row);
@@ -192,38 +192,43 @@ __device__ __forceinline__ void in_tile(const int64_t (&lo)[RA], const int64_t (
     }
 }
 
-// Unit u of a pass: 16 RA rows (from `row` of a tile) of one head.
-template <int RA> struct Unit {
+// Unit u of a pass: TY RA rows (from `row` of a tile) of one head.
+template <int RA, int TY> struct Unit {
     uint32_t tile;
     int head, row;
     __device__ __forceinline__ Unit(uint32_t u, int heads) {
-        constexpr uint32_t S = 4 / RA;
+        constexpr uint32_t S = kT / (TY * RA);
         tile = u / (S * heads);
         head = (int)(u / S % heads);
-        row = (int)(u % S) * 16 * RA;
+        row = (int)(u % S) * TY * RA;
     }
 };
-// Blocks that an SM should hold.
-template <int RA, bool TWO> constexpr int kBlocks = RA == 2 || TWO ? 2 : 1;
+// The unit of a block: longest first, one an SM; where all of them fit two an
+// SM, the shortest beside the longest (1024 rows, 8 heads of 64, causal: 68 ->
+// 62 us).
+__device__ __forceinline__ uint32_t unit_of_block(const SeqArgs &a) {
+    const uint32_t b = blockIdx.x, n = gridDim.x, m = (uint32_t)a.num_sms;
+    return b >= m && n <= 2 * m ? n - 1 - (b - m) : b;
+}
 
 // ---- forward ------------------------------------------------------------------
 
-template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA, (D < 128)>) seq_fwd_f32_kernel(const SeqArgs a) {
+template <int D, int RA, int TY, int MB> __global__ void __launch_bounds__(16 * TY, MB) seq_fwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
-    float *sQ = sm, *sK = sQ + kOwnFloats<D, RA>, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>;
+    float *sQ = sm, *sK = sQ + kOwnFloats<D, RA, TY>, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const Unit<RA> u(blockIdx.x, a.H);
+    const Unit<RA, TY> u(unit_of_block(a), a.H);
     const SeqTile t = a.qtiles[u.tile];
     const int h = u.head, hk = h / (a.H / a.Hkv);
     const int64_t q0 = (int64_t)t.tile * kT + u.row;
     const float scale2 = a.scale * kLog2e;
-    load_tile<D, 16 * RA>(sQ, a.Q, q0, a.rows, a.H, h);
-    load_tile<D>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    load_tile<D, TY, TY * RA>(sQ, a.Q, q0, a.rows, a.H, h);
+    load_tile<D, TY>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
     tc::cp_commit();
-    load_tile<D>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    load_tile<D, TY>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
     tc::cp_commit();
     int64_t lo[RA], hi[RA];
-    intervals(a, false, q0, ty, lo, hi);
+    intervals<RA, TY>(a, false, q0, ty, lo, hi);
     float m[RA], l[RA], acc[RA][kCols<D>];
 #pragma unroll
     for (int i = 0; i < RA; ++i) {
@@ -240,9 +245,9 @@ template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA,
         tc::cp_wait<1>();   // this K (V may be on its way)
         __syncthreads();
         float s[RA][4];
-        dot_tiles<D, RA>(s, sQ, sK, ty, tx);
+        dot_tiles<D, RA, TY>(s, sQ, sK, ty, tx);
         __syncthreads();
-        if (kt + 1 < t.t1) load_tile<D>(sK, a.K, k0 + kT, a.rows, a.Hkv, hk);   // beside the softmax and P V
+        if (kt + 1 < t.t1) load_tile<D, TY>(sK, a.K, k0 + kT, a.rows, a.Hkv, hk);   // beside the softmax and P V
         tc::cp_commit();
 #pragma unroll
         for (int i = 0; i < RA; ++i) {
@@ -259,7 +264,7 @@ template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA,
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float p = exp2_diff(s[i][c], mn);
-                sP[(ty + 16 * i) * kPP + tx + 16 * c] = p;
+                sP[(ty + TY * i) * kPP + tx + 16 * c] = p;
                 sum += p;
             }
             l[i] = l[i] * al + half_sum(sum);
@@ -269,50 +274,50 @@ template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA,
         }
         tc::cp_wait<1>();   // this V
         __syncthreads();
-        add_product<D, RA>(acc, sP, sV, ty, tx);
+        add_product<D, RA, TY>(acc, sP, sV, ty, tx);
         __syncthreads();
-        if (kt + 1 < t.t1) load_tile<D>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);   // beside the next scores
+        if (kt + 1 < t.t1) load_tile<D, TY>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);   // beside the next scores
         tc::cp_commit();
     }
     float inv[RA];
 #pragma unroll
     for (int i = 0; i < RA; ++i) {
         inv[i] = 1.f / l[i];
-        const int64_t row = q0 + ty + 16 * i;
+        const int64_t row = q0 + ty + TY * i;
         if (tx == 0 && row < a.rows) a.lse_w[row * a.H + h] = (m[i] + log2f(l[i])) * kLn2;
     }
-    uint32_t bad = store_rows<D, RA>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
+    uint32_t bad = store_rows<D, RA, TY>(static_cast<float *>(a.out_w), acc, inv, q0, a.rows, a.H, h, ty, tx);
 #pragma unroll
     for (int i = 0; i < RA; ++i)
         if (l[i] != l[i]) bad &= ~(1u << i);   // NaN whatever the masked rows hold
-    each_bad_row<RA>(bad, [&](int i, int half) {
-        seq::out_row_alone<float, D>(a, q0 + (ty & ~1) + half + 16 * i, h, hk, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
+    each_bad_row<RA, TY>(bad, [&](int i, int half) {
+        seq::out_row_alone<float, D>(a, q0 + (ty & ~1) + half + TY * i, h, hk, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
                                      __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half));
     });
 }
 
 // ---- backward -------------------------------------------------------------------
 
-template <int D, int RA> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float *sm, uint32_t unit) {
-    float *sQ = sm, *sG = sQ + kOwnFloats<D, RA>, *sV = sG + kOwnFloats<D, RA>, *sP = sV + kTileFloats<D>,
-          *sK = sP + kScoreFloats<RA>;   // two K tiles
+template <int D, int RA, int TY> __device__ __forceinline__ void dq_pass(const SeqArgs &a, float *sm, uint32_t unit) {
+    float *sQ = sm, *sG = sQ + kOwnFloats<D, RA, TY>, *sV = sG + kOwnFloats<D, RA, TY>, *sP = sV + kTileFloats<D>,
+          *sK = sP + kScoreFloats<RA, TY>;   // two K tiles
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const Unit<RA> u(unit, a.H);
+    const Unit<RA, TY> u(unit, a.H);
     const SeqTile t = a.qtiles[u.tile];
     const int h = u.head, hk = h / (a.H / a.Hkv);
     const int64_t q0 = (int64_t)t.tile * kT + u.row;
     const float scale2 = a.scale * kLog2e;
-    load_tile<D, 16 * RA>(sQ, a.Q, q0, a.rows, a.H, h);
-    load_tile<D, 16 * RA>(sG, a.dOut, q0, a.rows, a.H, h);
-    load_tile<D>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
-    load_tile<D>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    load_tile<D, TY, TY * RA>(sQ, a.Q, q0, a.rows, a.H, h);
+    load_tile<D, TY, TY * RA>(sG, a.dOut, q0, a.rows, a.H, h);
+    load_tile<D, TY>(sK, a.K, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
+    load_tile<D, TY>(sV, a.V, (int64_t)t.t0 * kT, a.rows, a.Hkv, hk);
     tc::cp_commit();
     int64_t lo[RA], hi[RA];
-    intervals(a, false, q0, ty, lo, hi);
+    intervals<RA, TY>(a, false, q0, ty, lo, hi);
     float ls[RA], dl[RA], acc[RA][kCols<D>];
 #pragma unroll
     for (int i = 0; i < RA; ++i) {
-        const int64_t r = (int64_t)h * a.rows_pad + q0 + ty + 16 * i;
+        const int64_t r = (int64_t)h * a.rows_pad + q0 + ty + TY * i;
         ls[i] = a.ws_nlse[r];
         dl[i] = a.ws_ndelta[r];
 #pragma unroll
@@ -326,39 +331,39 @@ template <int D, int RA> __device__ __forceinline__ void dq_pass(const SeqArgs &
         in_tile(lo, hi, k0, kl, kh);
         tc::cp_wait<0>();
         __syncthreads();   // this K and V; the last dS K is done with the other K and with dS
-        if (kt + 1 < t.t1) load_tile<D>(sKn, a.K, k0 + kT, a.rows, a.Hkv, hk);
+        if (kt + 1 < t.t1) load_tile<D, TY>(sKn, a.K, k0 + kT, a.rows, a.Hkv, hk);
         float s[RA][4], g[RA][4];
-        dot_tiles<D, RA>(g, sG, sV, ty, tx);
+        dot_tiles<D, RA, TY>(g, sG, sV, ty, tx);
         __syncthreads();
-        if (kt + 1 < t.t1) load_tile<D>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);
+        if (kt + 1 < t.t1) load_tile<D, TY>(sV, a.V, k0 + kT, a.rows, a.Hkv, hk);
         tc::cp_commit();
-        dot_tiles<D, RA>(s, sQ, sKi, ty, tx);
+        dot_tiles<D, RA, TY>(s, sQ, sKi, ty, tx);
 #pragma unroll
         for (int i = 0; i < RA; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int j = tx + 16 * c;
                 const bool on = full || (j >= kl[i] && j < kh[i]);
-                sP[(ty + 16 * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, ls[i])) * (g[i][c] + dl[i]) : 0.f;
+                sP[(ty + TY * i) * kPP + j] = on ? fast_exp2(fmaf(s[i][c], scale2, ls[i])) * (g[i][c] + dl[i]) : 0.f;
             }
         __syncthreads();
-        add_product<D, RA>(acc, sP, sKi, ty, tx);
+        add_product<D, RA, TY>(acc, sP, sKi, ty, tx);
     }
     float f[RA];
 #pragma unroll
     for (int i = 0; i < RA; ++i) f[i] = a.scale;
-    const uint32_t bad = store_rows<D, RA>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
-    each_bad_row<RA>(bad, [&](int i, int half) {
-        seq::query_row_alone<float, D>(a, q0 + (ty & ~1) + half + 16 * i, h, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
+    const uint32_t bad = store_rows<D, RA, TY>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
+    each_bad_row<RA, TY>(bad, [&](int i, int half) {
+        seq::query_row_alone<float, D>(a, q0 + (ty & ~1) + half + TY * i, h, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
                                        __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
     });
 }
 
-template <int D, int RA> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, float *sm, uint32_t unit) {
-    float *sK = sm, *sV = sK + kOwnFloats<D, RA>, *sP = sV + kOwnFloats<D, RA>,
-          *sS = sP + kScoreFloats<RA>;   // two pairs of Q and dOut tiles
+template <int D, int RA, int TY> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, float *sm, uint32_t unit) {
+    float *sK = sm, *sV = sK + kOwnFloats<D, RA, TY>, *sP = sV + kOwnFloats<D, RA, TY>,
+          *sS = sP + kScoreFloats<RA, TY>;   // two pairs of Q and dOut tiles
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    const Unit<RA> u(unit, a.Hkv);
+    const Unit<RA, TY> u(unit, a.Hkv);
     const SeqTile t = a.ktiles[u.tile];
     const int hk = u.head, grp = a.H / a.Hkv;
     const int64_t k0 = (int64_t)t.tile * kT + u.row;
@@ -367,15 +372,15 @@ template <int D, int RA> __device__ __forceinline__ void dkdv_pass(const SeqArgs
     auto fetch = [&](int i) {
         float *dst = sS + i % 2 * 2 * kTileFloats<D>;
         const int64_t q0 = (int64_t)(t.t0 + i % nt) * kT;
-        load_tile<D>(dst, a.Q, q0, a.rows, a.H, hk * grp + i / nt);
-        load_tile<D>(dst + kTileFloats<D>, a.dOut, q0, a.rows, a.H, hk * grp + i / nt);
+        load_tile<D, TY>(dst, a.Q, q0, a.rows, a.H, hk * grp + i / nt);
+        load_tile<D, TY>(dst + kTileFloats<D>, a.dOut, q0, a.rows, a.H, hk * grp + i / nt);
     };
-    load_tile<D, 16 * RA>(sK, a.K, k0, a.rows, a.Hkv, hk);
-    load_tile<D, 16 * RA>(sV, a.V, k0, a.rows, a.Hkv, hk);
+    load_tile<D, TY, TY * RA>(sK, a.K, k0, a.rows, a.Hkv, hk);
+    load_tile<D, TY, TY * RA>(sV, a.V, k0, a.rows, a.Hkv, hk);
     fetch(0);
     tc::cp_commit();
     int64_t lo[RA], hi[RA];
-    intervals(a, true, k0, ty, lo, hi);
+    intervals<RA, TY>(a, true, k0, ty, lo, hi);
     float dk[RA][kCols<D>], dv[RA][kCols<D>];
 #pragma unroll
     for (int i = 0; i < RA; ++i)
@@ -400,8 +405,8 @@ template <int D, int RA> __device__ __forceinline__ void dkdv_pass(const SeqArgs
         if (step + 1 < n) fetch(step + 1);
         tc::cp_commit();
         float s[RA][4], g[RA][4];
-        dot_tiles<D, RA>(s, sK, sQ, ty, tx);
-        dot_tiles<D, RA>(g, sV, sG, ty, tx);
+        dot_tiles<D, RA, TY>(s, sK, sQ, ty, tx);
+        dot_tiles<D, RA, TY>(g, sV, sG, ty, tx);
 #pragma unroll
         for (int i = 0; i < RA; ++i)
 #pragma unroll
@@ -409,18 +414,18 @@ template <int D, int RA> __device__ __forceinline__ void dkdv_pass(const SeqArgs
                 const int j = tx + 16 * c;
                 const bool on = full || (j >= ql[i] && j < qh[i]);
                 const float p = on ? fast_exp2(fmaf(s[i][c], scale2, ls[c])) : 0.f;
-                sP[(ty + 16 * i) * kPP + j] = p;
+                sP[(ty + TY * i) * kPP + j] = p;
                 g[i][c] = on ? p * (g[i][c] + dl[c]) : 0.f;
             }
         __syncthreads();
-        add_product<D, RA>(dv, sP, sG, ty, tx);
+        add_product<D, RA, TY>(dv, sP, sG, ty, tx);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < RA; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sP[(ty + 16 * i) * kPP + tx + 16 * c] = g[i][c];   // dS^T over P^T
+            for (int c = 0; c < 4; ++c) sP[(ty + TY * i) * kPP + tx + 16 * c] = g[i][c];   // dS^T over P^T
         __syncthreads();
-        add_product<D, RA>(dk, sP, sQ, ty, tx);
+        add_product<D, RA, TY>(dk, sP, sQ, ty, tx);
     }
     float one[RA], f[RA];
 #pragma unroll
@@ -428,23 +433,23 @@ template <int D, int RA> __device__ __forceinline__ void dkdv_pass(const SeqArgs
         one[i] = 1.f;
         f[i] = a.scale;
     }
-    const uint32_t bad_v = store_rows<D, RA>(static_cast<float *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
-    const uint32_t bad_k = store_rows<D, RA>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
+    const uint32_t bad_v = store_rows<D, RA, TY>(static_cast<float *>(a.dV), dv, one, k0, a.rows, a.Hkv, hk, ty, tx);
+    const uint32_t bad_k = store_rows<D, RA, TY>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
     for (int x = 0; x < 2; ++x)
-        each_bad_row<RA>(x ? bad_k : bad_v, [&](int i, int half) {
-            seq::key_row_alone<float, D>(a, x == 1, k0 + (ty & ~1) + half + 16 * i, hk,
+        each_bad_row<RA, TY>(x ? bad_k : bad_v, [&](int i, int half) {
+            seq::key_row_alone<float, D>(a, x == 1, k0 + (ty & ~1) + half + TY * i, hk,
                                          __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
                                          __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
         });
 }
 
 // Both passes in one launch, the dK/dV units (the longer ones) first.
-template <int D, int RA> __global__ void __launch_bounds__(kThreads, kBlocks<RA, (D == 32)>) seq_bwd_f32_kernel(const SeqArgs a) {
+template <int D, int RA, int TY, int MB> __global__ void __launch_bounds__(16 * TY, MB) seq_bwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
     second_of_two();
-    const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv * (4 / RA);
-    if (blockIdx.x < kv) dkdv_pass<D, RA>(a, sm, blockIdx.x);
-    else dq_pass<D, RA>(a, sm, blockIdx.x - kv);
+    const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv * (kT / (TY * RA));
+    if (blockIdx.x < kv) dkdv_pass<D, RA, TY>(a, sm, blockIdx.x);
+    else dq_pass<D, RA, TY>(a, sm, blockIdx.x - kv);
 }
 
 // Row terms: D / EL lanes of 16 bytes a (row, head), four of them in flight.
@@ -488,26 +493,26 @@ template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_term
     }
 }
 
-template <int D, int RA> cudaError_t launch_fwd(const SeqArgs &a, cudaStream_t s) {
-    constexpr size_t smem = sizeof(float) * (kOwnFloats<D, RA> + 2 * kTileFloats<D> + kScoreFloats<RA>);
-    if (cudaError_t e = allow_smem<seq_fwd_f32_kernel<D, RA>>(smem); e != cudaSuccess) return e;
+template <int D, int RA, int TY, int MB> cudaError_t launch_fwd(const SeqArgs &a, cudaStream_t s) {
+    constexpr size_t smem = sizeof(float) * (kOwnFloats<D, RA, TY> + 2 * kTileFloats<D> + kScoreFloats<RA, TY>);
+    if (cudaError_t e = allow_smem<seq_fwd_f32_kernel<D, RA, TY, MB>>(smem); e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_FWD, s, false);
-    seq_fwd_f32_kernel<D, RA><<<(unsigned)((int64_t)a.n_tiles * a.H * (4 / RA)), kThreads, smem, s>>>(a);
+    seq_fwd_f32_kernel<D, RA, TY, MB><<<(unsigned)((int64_t)a.n_tiles * a.H * (kT / (TY * RA))), 16 * TY, smem, s>>>(a);
     note_launch(SGA_KERN_SEQ_FWD, s, true);
     return cudaGetLastError();
 }
 
-template <int D, int RA> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
-    constexpr size_t kv = sizeof(float) * (2 * kOwnFloats<D, RA> + 4 * kTileFloats<D> + kScoreFloats<RA>);
-    constexpr size_t q = sizeof(float) * (2 * kOwnFloats<D, RA> + 3 * kTileFloats<D> + kScoreFloats<RA>);
+template <int D, int RA, int TY, int MB> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
+    constexpr size_t kv = sizeof(float) * (2 * kOwnFloats<D, RA, TY> + 4 * kTileFloats<D> + kScoreFloats<RA, TY>);
+    constexpr size_t q = sizeof(float) * (2 * kOwnFloats<D, RA, TY> + 3 * kTileFloats<D> + kScoreFloats<RA, TY>);
     constexpr size_t smem = kv > q ? kv : q;
     static_assert(smem <= 227 * 1024, "shared memory");
-    cudaError_t e = allow_smem<seq_bwd_f32_kernel<D, RA>>(smem);
+    cudaError_t e = allow_smem<seq_bwd_f32_kernel<D, RA, TY, MB>>(smem);
     if (e == cudaSuccess) e = seq_row_terms<float>(a, D, s);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD, s, false);
-    e = launch_second(seq_bwd_f32_kernel<D, RA>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H) * (4 / RA))),
-                      dim3(kThreads), smem, s, a);
+    e = launch_second(seq_bwd_f32_kernel<D, RA, TY, MB>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H) * (kT / (TY * RA)))),
+                      dim3(16 * TY), smem, s, a);
     note_launch(SGA_KERN_SEQ_BWD, s, true);
     return e;
 }
@@ -528,20 +533,34 @@ template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStr
 template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t);
 template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
 
-// Owner tiles of 32 rows where 64 would leave SMs without a block; they read
-// twice as much shared memory a product.  32 : 64 rows, forward, D = 64: 512
-// rows, 4 heads (32 units of 64) 36 : 49 us, 1024 rows, 8 heads (128) 105 : 95;
-// backward: 512 rows, 4 heads (64 units) D = 32 40 : 52, D = 64 58 : 74, D = 128
-// 99 : 121; 1024 rows, 4 heads (128), D = 32 95 : 95; 8 heads (256), D = 64 320 : 244.
+// Owner tiles of 32 rows (4 x 8); of 16 (2 x 8) where 32 would leave SMs without
+// a block: 512 rows, 4 heads (64 units of 32), forward D = 32, 64, 128: 16 rows
+// 18.7, 24.8, 37.1 us, 32 rows 24.8, 33.0, 47.4; 1024 rows, 8 heads (256),
+// D = 64: 117 : 84.  Backward, 256 rows, 4 heads (64): 16.6, 22.8, 33.2 :
+// 18.9, 27.1, 41.3.  In the forward four blocks an SM fit in 128 registers a
+// thread with a few spills, against three: 2048 rows, 8 heads (512 units), D =
+// 32 174 : 213 us, D = 64 275 : 309; fewer units do not need them (256, D = 64,
+// causal 64 : 62).  In the backward D = 32 is faster with two blocks an SM while
+// they are enough (1024 rows, 4 heads 81 : 102 us, 8 heads 140 : 124), and D = 128,
+// whose tiles leave room for one block an SM, with 64 rows and 256 threads from
+// there on (1024 rows, 8 heads 400 : 484 us; 512 rows, 8 heads, causal 117 : 74).
 cudaError_t seq_fwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
-    if (2 * (int64_t)a.n_tiles * a.H <= a.num_sms)
-        return D == 32 ? launch_fwd<32, 2>(a, s) : D == 64 ? launch_fwd<64, 2>(a, s) : launch_fwd<128, 2>(a, s);
-    return D == 32 ? launch_fwd<32, 4>(a, s) : D == 64 ? launch_fwd<64, 4>(a, s) : launch_fwd<128, 4>(a, s);
+    const int64_t units = 2 * (int64_t)a.n_tiles * a.H;
+    if ((D == 128 ? 2 : 1) * units <= a.num_sms)
+        return D == 32 ? launch_fwd<32, 2, 8, 3>(a, s) : D == 64 ? launch_fwd<64, 2, 8, 3>(a, s) : launch_fwd<128, 2, 8, 2>(a, s);
+    const bool many = units > 3 * (int64_t)a.num_sms;
+    if (D == 32) return many ? launch_fwd<32, 4, 8, 4>(a, s) : launch_fwd<32, 4, 8, 3>(a, s);
+    if (D == 64) return many ? launch_fwd<64, 4, 8, 4>(a, s) : launch_fwd<64, 4, 8, 3>(a, s);
+    return launch_fwd<128, 4, 8, 2>(a, s);
 }
 cudaError_t seq_bwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
-    if ((int64_t)a.n_tiles * (a.H + a.Hkv) <= a.num_sms)
-        return D == 32 ? launch_bwd<32, 2>(a, s) : D == 64 ? launch_bwd<64, 2>(a, s) : launch_bwd<128, 2>(a, s);
-    return D == 32 ? launch_bwd<32, 4>(a, s) : D == 64 ? launch_bwd<64, 4>(a, s) : launch_bwd<128, 4>(a, s);
+    const int64_t units = 2 * (int64_t)a.n_tiles * (a.H + a.Hkv);
+    if ((D == 128 ? 2 : 1) * units <= a.num_sms)
+        return D == 32 ? launch_bwd<32, 2, 8, 3>(a, s) : D == 64 ? launch_bwd<64, 2, 8, 2>(a, s) : launch_bwd<128, 2, 8, 1>(a, s);
+    const bool many = units > 2 * (int64_t)a.num_sms;
+    if (D == 32) return many ? launch_bwd<32, 4, 8, 3>(a, s) : launch_bwd<32, 4, 8, 2>(a, s);
+    if (D == 64) return launch_bwd<64, 4, 8, 2>(a, s);
+    return many ? launch_bwd<128, 4, 16, 1>(a, s) : launch_bwd<128, 4, 8, 1>(a, s);
 }
 
 }  // namespace sga
