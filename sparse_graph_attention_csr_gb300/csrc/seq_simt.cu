@@ -12,7 +12,7 @@
 // bank conflicts, so no tile is stored transposed.  RA = 4 reads half as much
 // shared memory a product as RA = 2, and 128 threads leave a thread the
 // registers to read ahead: 2048 rows, 8 heads of 64, full, forward 275 us (31
-// TFLOP/s), backward 798 (938 with 256 threads).
+// TFLOP/s), backward 791 (938 with 256 threads).
 //   forward: S = Q K^T, online softmax (running maximum and sum per row),
 //     O = O alpha + P V;
 //   dQ pass (a tile of queries): S, dP = dOut V^T, dS = P (dP - Delta),
@@ -37,6 +37,7 @@ template <int D> constexpr int kPitch = D + 4;
 template <int D> constexpr int kTileFloats = kT * (D + 4);
 template <int D, int RA, int TY> constexpr int kOwnFloats = TY * RA * (D + 4);   // an owner tile: TY RA rows
 template <int RA, int TY> constexpr int kScoreFloats = TY * RA * kPP;
+template <int TY> constexpr bool kTwoScores = TY == 8;   // score tiles of the dK/dV pass
 
 // rows [r0, r0 + ROWS) of head h of a [T][heads][D] tensor, asynchronously (rows
 // past `rows` as zeros)
@@ -361,7 +362,8 @@ template <int D, int RA, int TY> __device__ __forceinline__ void dq_pass(const S
 
 template <int D, int RA, int TY> __device__ __forceinline__ void dkdv_pass(const SeqArgs &a, float *sm, uint32_t unit) {
     float *sK = sm, *sV = sK + kOwnFloats<D, RA, TY>, *sP = sV + kOwnFloats<D, RA, TY>,
-          *sS = sP + kScoreFloats<RA, TY>;   // two pairs of Q and dOut tiles
+          *sD = sP + (kTwoScores<TY> ? kScoreFloats<RA, TY> : 0),   // dS^T: over P^T where there is no room for both
+          *sS = sD + kScoreFloats<RA, TY>;                          // two pairs of Q and dOut tiles
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const Unit<RA, TY> u(unit, a.Hkv);
     const SeqTile t = a.ktiles[u.tile];
@@ -416,16 +418,19 @@ template <int D, int RA, int TY> __device__ __forceinline__ void dkdv_pass(const
                 const float p = on ? fast_exp2(fmaf(s[i][c], scale2, ls[c])) : 0.f;
                 sP[(ty + TY * i) * kPP + j] = p;
                 g[i][c] = on ? p * (g[i][c] + dl[c]) : 0.f;
+                if (kTwoScores<TY>) sD[(ty + TY * i) * kPP + j] = g[i][c];
             }
         __syncthreads();
         add_product<D, RA, TY>(dv, sP, sG, ty, tx);
-        __syncthreads();
+        if (!kTwoScores<TY>) {
+            __syncthreads();
 #pragma unroll
-        for (int i = 0; i < RA; ++i)
+            for (int i = 0; i < RA; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sP[(ty + TY * i) * kPP + tx + 16 * c] = g[i][c];   // dS^T over P^T
-        __syncthreads();
-        add_product<D, RA, TY>(dk, sP, sQ, ty, tx);
+                for (int c = 0; c < 4; ++c) sD[(ty + TY * i) * kPP + tx + 16 * c] = g[i][c];
+            __syncthreads();
+        }
+        add_product<D, RA, TY>(dk, sD, sQ, ty, tx);
     }
     float one[RA], f[RA];
 #pragma unroll
@@ -503,7 +508,7 @@ template <int D, int RA, int TY, int MB> cudaError_t launch_fwd(const SeqArgs &a
 }
 
 template <int D, int RA, int TY, int MB> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
-    constexpr size_t kv = sizeof(float) * (2 * kOwnFloats<D, RA, TY> + 4 * kTileFloats<D> + kScoreFloats<RA, TY>);
+    constexpr size_t kv = sizeof(float) * (2 * kOwnFloats<D, RA, TY> + 4 * kTileFloats<D> + (kTwoScores<TY> ? 2 : 1) * kScoreFloats<RA, TY>);
     constexpr size_t q = sizeof(float) * (2 * kOwnFloats<D, RA, TY> + 3 * kTileFloats<D> + kScoreFloats<RA, TY>);
     constexpr size_t smem = kv > q ? kv : q;
     static_assert(smem <= 227 * 1024, "shared memory");
