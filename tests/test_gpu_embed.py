@@ -185,3 +185,18 @@ def test_scale_past_float32(scale):
         sga.embed_fwd(ids, table, scale)
     with pytest.raises(ValueError, match="scale"):
         sga.embed_bwd(ids, torch.randn(10, 8, device="cuda"), 5, scale)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [8, 31, 100, 400])
+def test_few_rows_off_a_16_byte_boundary(C, dt):
+    """Few rows and tokens: a gradient that begins off 16 bytes gives what an aligned one does."""
+    N, V = 1003, 119
+    ids = zipf(N, V, torch.int64, C)
+    flat = torch.randn(N * C + 1, device="cuda").to(DT[dt])
+    off = flat[1:].view(N, C)
+    assert off.data_ptr() % 16
+    dT = sga.embed_bwd(ids, off, V, 0.5)
+    assert torch.equal(dT, sga.embed_bwd(ids, off.clone(), V, 0.5))
+    v, b = embed_bwd_reference(ids, off, V, 0.5, None)
+    within(dT, (v, b + 2 ** -24 * v.abs()), "dTable")
