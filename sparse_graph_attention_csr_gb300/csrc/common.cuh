@@ -189,16 +189,24 @@ inline int device_sms() {
 
 void note_launch(sga_kernel_id which, cudaStream_t s, bool after);
 
-// Two kernels of one call, the second of which needs the first's results: the
-// second is launched while the first still runs (its blocks take their places as
-// the first's leave room) and waits for its end and its writes before it reads
-// them.  The first calls first_of_two() (it may, early), the second
-// second_of_two() before it touches memory that the first writes.
-__device__ __forceinline__ void first_of_two() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void second_of_two() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A kernel launched by launch_early may start while the stream's previous kernel
+// still runs, if that one lets it: its blocks take their places as the previous
+// one's leave room, and wait for that one's end and writes before they touch
+// memory.  Every kernel launched this way calls wait_previous() in every block,
+// before any access to memory that another kernel writes or reads and before any
+// return (so that its own end implies the end of all before it).
+// No block may hold tensor memory while it waits: a block of the kernel that it
+// waits for may still have to allocate its own.  let_next_start() may be called at
+// any time.  Kernels whose next one fills the GPU with equal shares a block
+// (norm_reduce before a norm's backward, the attention backward, the fp32
+// attention forward) do not call it: blocks that start early, where there is
+// room, leave the SMs unevenly filled (169343 x 512 layer norm backward 90 -> 117
+// us).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>
-cudaError_t launch_second(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A &...args) {
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

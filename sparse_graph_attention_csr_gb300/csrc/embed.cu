@@ -61,6 +61,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(const void *__restrict__ ids, bool wide, const T *__restrict__ table,
                                                         int64_t N, int64_t V, int C, float scale, int sh, T *out) {
     constexpr int EL = kEl<T, VEC>, U = 4;
+    let_next_start();
+    wait_previous();
     const int n = C / EL, lanes = 1 << sh, sub = threadIdx.x & (lanes - 1);
     const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> sh;
     for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> sh; t < N; t += step) {
@@ -501,7 +503,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
     __shared__ uint16_t list[kSortWarps][kFewTokens];   // a warp's tokens, by row and in order: token | row / 32 << 9
     extern __shared__ __align__(16) unsigned char stage[];
     static_assert(kFewTokens <= 512 && kFewRows <= 32 * 128, "list entries");
-    first_of_two();
+    let_next_start();
+    wait_previous();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, V = (int)a.V, n = a.C / EL;
     const int64_t t0 = min(a.N, blockIdx.x * per);
     const int cnt = (int)min(per, a.N - t0);
@@ -589,7 +592,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
 // The blocks' sums of every row: a warp per W columns of a row, its lanes take
 // every 32nd block's.
 template <typename T, int W> __global__ void __launch_bounds__(256) embed_add_few_kernel(const GradArgs a, int B) {
-    second_of_two();
+    let_next_start();
+    wait_previous();
     const int lane = threadIdx.x & 31;
     const int64_t stride = a.V * a.C, it = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (it >= stride / W) return;
@@ -668,18 +672,20 @@ template <typename T, bool VEC> cudaError_t grad_t(GradArgs a, int blocks, cudaS
     if (a.few) {
         blocks = (int)((a.N + a.few - 1) / a.few);
         note_launch(SGA_KERN_EMBED_BWD, s, false);
-        const size_t bytes = (size_t)a.few * a.C * sizeof(T);
+        const int64_t per = a.few;
+        const size_t bytes = (size_t)per * a.C * sizeof(T);
+        cudaError_t le;
         if (bytes <= kStage && aligned(a.dOut, 16)) {
             if (cudaError_t e = allow_smem<embed_grad_few_kernel<T, VEC, true>>(kStage); e != cudaSuccess) return e;
-            embed_grad_few_kernel<T, VEC, true><<<(unsigned)blocks, kSortThreads, bytes, s>>>(a, a.few);
+            le = launch_early(embed_grad_few_kernel<T, VEC, true>, dim3((unsigned)blocks), dim3(kSortThreads), bytes, s, a, per);
         } else {
-            embed_grad_few_kernel<T, VEC, false><<<(unsigned)blocks, kSortThreads, 0, s>>>(a, a.few);
+            le = launch_early(embed_grad_few_kernel<T, VEC, false>, dim3((unsigned)blocks), dim3(kSortThreads), 0, s, a, per);
         }
         note_launch(SGA_KERN_EMBED_BWD, s, true);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+        if (le != cudaSuccess) return le;
         const int64_t warps = a.V * a.C / (a.C % 4 == 0 ? 4 : 1);
         note_launch(SGA_KERN_EMBED_ADD, s, false);
-        const cudaError_t e = launch_second(a.C % 4 == 0 ? embed_add_few_kernel<T, 4> : embed_add_few_kernel<T, 1>,
+        const cudaError_t e = launch_early(a.C % 4 == 0 ? embed_add_few_kernel<T, 4> : embed_add_few_kernel<T, 1>,
                                             dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, a, blocks);
         note_launch(SGA_KERN_EMBED_ADD, s, true);
         return e;
@@ -709,10 +715,10 @@ cudaError_t fwd_t(const void *ids, bool wide, const void *table, int64_t N, int6
     const int64_t blocks = ((N << sh) + 255) / 256;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)device_sms() * 32);
     note_launch(SGA_KERN_EMBED_FWD, s, false);
-    embed_fwd_kernel<T, VEC><<<grid, 256, 0, s>>>(ids, wide, static_cast<const T *>(table), N, V, C, scale, sh,
-                                                  static_cast<T *>(out));
+    const cudaError_t e = launch_early(embed_fwd_kernel<T, VEC>, dim3(grid), dim3(256), 0, s, ids, wide,
+                                       static_cast<const T *>(table), N, V, C, scale, sh, static_cast<T *>(out));
     note_launch(SGA_KERN_EMBED_FWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

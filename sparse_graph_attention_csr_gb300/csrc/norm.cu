@@ -114,6 +114,8 @@ template <int TPR, int K> __device__ __forceinline__ void row_sum(float (&v)[K],
 template <typename TX, typename TW, int EL, int TPR, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
     __shared__ float red[1][32];
+    let_next_start();
+    wait_previous();
     constexpr int GPB = THREADS / TPR;
     const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int nvec = a.C / EL;
@@ -211,7 +213,8 @@ template <typename TX, typename TW, int EL, int TPR, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
     __shared__ float red[2][32];
     extern __shared__ float acc_sm[];   // [2][C] sums of the block's groups
-    first_of_two();
+    let_next_start();
+    wait_previous();
     constexpr int GPB = THREADS / TPR;
     const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int nvec = a.C / EL;
@@ -295,7 +298,8 @@ constexpr int kRingThreads = 128, kRingStages = 6;
 template <typename TX, typename TW, int TPR, int NV>
 __global__ void __launch_bounds__(kRingThreads, 4) norm_bwd_ring_kernel(const NormArgs a) {
     constexpr int EL = Elt<TX>::EL, GPB = kRingThreads / TPR;
-    first_of_two();
+    let_next_start();
+    wait_previous();
     extern __shared__ __align__(16) unsigned char ring_sm[];   // [stage][vector][x, dy][thread] 16 bytes; then [2][C] sums
     const int sub = threadIdx.x % TPR, grp = threadIdx.x / TPR;
     const int nvec = a.C / EL;
@@ -382,6 +386,8 @@ __global__ void __launch_bounds__(kRingThreads, 4) norm_bwd_ring_kernel(const No
 // Rows too wide for registers: a block per row, x read again (from L2) in each step.
 template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_fwd_wide_kernel(const NormArgs a) {
     __shared__ float red[1][32];
+    let_next_start();
+    wait_previous();
     const TX *X = static_cast<const TX *>(a.X);
     const TW *w = static_cast<const TW *>(a.w), *b = static_cast<const TW *>(a.b);
     const float inv = 1.f / (float)a.C;
@@ -411,6 +417,8 @@ template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_
 
 template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_bwd_wide_kernel(const NormArgs a) {
     __shared__ float red[2][32];
+    let_next_start();
+    wait_previous();
     const TW *w = static_cast<const TW *>(a.w);
     const float inv = 1.f / (float)a.C;
     for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
@@ -433,7 +441,8 @@ template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_
 
 // Column sums of wide rows: a thread per column over the rows of a slab.
 template <typename TX> __global__ void __launch_bounds__(256) norm_cols_wide_kernel(const NormArgs a, int64_t slab) {
-    first_of_two();
+    let_next_start();
+    wait_previous();
     const int c = blockIdx.x * 256 + threadIdx.x;
     const int64_t r0 = (int64_t)blockIdx.y * slab, r1 = min(a.N, r0 + slab);
     if (c >= a.C) return;
@@ -454,7 +463,7 @@ template <typename TX> __global__ void __launch_bounds__(256) norm_cols_wide_ker
 template <typename TW> __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ part, int blocks,
                                                                                   int C, TW *dw, TW *db) {
     __shared__ float sm[32][33];
-    second_of_two();
+    wait_previous();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane, n = 2 * (int64_t)C;   // column of [dw | db]
     float s = 0.f;
@@ -486,9 +495,9 @@ cudaError_t launch_fwd(const NormArgs &a, cudaStream_t s) {
     const int64_t need = (a.N + GPB - 1) / GPB;
     const unsigned grid = (unsigned)std::min<int64_t>(need, (int64_t)device_sms() * 32);
     note_launch(SGA_KERN_NORM_FWD, s, false);
-    norm_fwd_kernel<TX, TW, EL, TPR, NV, TH><<<grid, TH, 0, s>>>(a);
+    const cudaError_t e = launch_early(norm_fwd_kernel<TX, TW, EL, TPR, NV, TH>, dim3(grid), dim3(TH), 0, s, a);
     note_launch(SGA_KERN_NORM_FWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename TX, typename TW, int EL, int TPR, int NV>
@@ -511,9 +520,9 @@ cudaError_t launch_bwd(const NormArgs &a, int &blocks, cudaStream_t s) {
     }
     blocks = (int)std::min<int64_t>((a.N + GPB - 1) / GPB, (int64_t)device_sms() * fit);
     note_launch(SGA_KERN_NORM_BWD, s, false);
-    norm_bwd_kernel<TX, TW, EL, TPR, NV, TH><<<(unsigned)blocks, TH, smem, s>>>(a);
+    const cudaError_t e = launch_early(norm_bwd_kernel<TX, TW, EL, TPR, NV, TH>, dim3((unsigned)blocks), dim3(TH), smem, s, a);
     note_launch(SGA_KERN_NORM_BWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename TX, typename TW, int TPR, int NV> cudaError_t launch_bwd_ring(const NormArgs &a, int &blocks, cudaStream_t s) {
@@ -523,9 +532,9 @@ template <typename TX, typename TW, int TPR, int NV> cudaError_t launch_bwd_ring
     const size_t smem = std::max(ring, sums);
     if (cudaError_t e = allow_smem<norm_bwd_ring_kernel<TX, TW, TPR, NV>>(smem); e != cudaSuccess) return e;
     note_launch(SGA_KERN_NORM_BWD, s, false);
-    norm_bwd_ring_kernel<TX, TW, TPR, NV><<<(unsigned)blocks, kRingThreads, smem, s>>>(a);
+    const cudaError_t e = launch_early(norm_bwd_ring_kernel<TX, TW, TPR, NV>, dim3((unsigned)blocks), dim3(kRingThreads), smem, s, a);
     note_launch(SGA_KERN_NORM_BWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 // Threads of a row by its number of 16-byte vectors (or of elements, where the
@@ -552,9 +561,9 @@ template <typename TX, typename TW> cudaError_t norm_fwd_t(const NormArgs &a, bo
     }
     const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)device_sms() * 8);
     note_launch(SGA_KERN_NORM_FWD, s, false);
-    norm_fwd_wide_kernel<TX, TW><<<grid, 256, 0, s>>>(a);
+    const cudaError_t e = launch_early(norm_fwd_wide_kernel<TX, TW>, dim3(grid), dim3(256), 0, s, a);
     note_launch(SGA_KERN_NORM_FWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bool vec, bool pairs, TW *dw, TW *db, cudaStream_t s) {
@@ -576,20 +585,19 @@ template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bo
     else {
         const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)device_sms() * 8);
         note_launch(SGA_KERN_NORM_BWD, s, false);
-        norm_bwd_wide_kernel<TX, TW><<<grid, 256, 0, s>>>(a);
+        e = launch_early(norm_bwd_wide_kernel<TX, TW>, dim3(grid), dim3(256), 0, s, a);
         note_launch(SGA_KERN_NORM_BWD, s, true);
-        if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
+        if (e != cudaSuccess || !a.part) return e;
         const int64_t want = std::min<int64_t>(bwd_blocks(device_sms()), (a.N + 15) / 16);
         const int64_t slab = (a.N + want - 1) / want;
         blocks = (int)((a.N + slab - 1) / slab);
         note_launch(SGA_KERN_NORM_BWD, s, false);
-        norm_cols_wide_kernel<TX><<<dim3((unsigned)((a.C + 255) / 256), (unsigned)blocks), 256, 0, s>>>(a, slab);
+        e = launch_early(norm_cols_wide_kernel<TX>, dim3((unsigned)((a.C + 255) / 256), (unsigned)blocks), dim3(256), 0, s, a, slab);
         note_launch(SGA_KERN_NORM_BWD, s, true);
-        e = cudaGetLastError();
     }
     if (e != cudaSuccess || !a.part) return e;
     note_launch(SGA_KERN_NORM_REDUCE, s, false);
-    e = launch_second(norm_reduce_kernel<TW>, dim3((unsigned)((2 * (int64_t)a.C + 31) / 32)), dim3(1024), 0, s,
+    e = launch_early(norm_reduce_kernel<TW>, dim3((unsigned)((2 * (int64_t)a.C + 31) / 32)), dim3(1024), 0, s,
                       static_cast<const float *>(a.part), blocks, a.C, dw, db);
     note_launch(SGA_KERN_NORM_REDUCE, s, true);
     return e;

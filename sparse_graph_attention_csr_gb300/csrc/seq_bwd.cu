@@ -187,7 +187,6 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
     const int hk = unit % a.Hkv, grp = a.H / a.Hkv;
     const int nt = t.t1 - t.t0, n = nt * grp;   // steps: (head of the group, query tile)
 
-    if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
     if (tid == 32) {
         tc::mbar_init(&kv_full, 1);
         rq.init();
@@ -199,10 +198,11 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
         tc::mbar_init(&ds_full, kSoft);
         tc::mbar_init(&acc_full, 1);
     }
+    wait_previous();
+    if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    second_of_two();   // the row terms
     const uint32_t tS = tmem_base + C::TS, tP = tmem_base + C::TP, tK = tmem_base + C::TK, tV = tmem_base + C::TV;
 
     if (warp < 4) {
@@ -406,7 +406,6 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
     const int h = unit % a.H, hk = h / (a.H / a.Hkv);
     const int n = t.t1 - t.t0;
 
-    if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
     if (tid == 32) {
         tc::mbar_init(&q_full, kSoft);
         tc::mbar_init(&s_free, kSoft);
@@ -417,10 +416,11 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
         tc::mbar_init(&ds_full, kSoft);
         tc::mbar_init(&acc_full, 1);
     }
+    wait_previous();
+    if (warp == 0) tc::tmem_alloc(&tmem_base, 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    second_of_two();   // the row terms
     const uint32_t tS = tmem_base + C::TS, tP = tmem_base + C::TP, tQ = tmem_base + C::TQ, tA = tmem_base + C::TA,
                    tG = tmem_base + C::TG;
 
@@ -615,6 +615,7 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
 template <int D> __global__ void __launch_bounds__(kThreads, 1) seq_bwd_kernel(const __grid_constant__ BwdParams prm) {
     extern __shared__ __align__(1024) unsigned char smem[];
     if (tc::smem_u32(smem) & 1023) {
+        wait_previous();
         if (threadIdx.x == 0) atomicOr(prm.a.d_err, tc::kErrMmaTimeout);
         return;
     }
@@ -635,7 +636,7 @@ template <int D> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
     if (e == cudaSuccess) e = seq_row_terms<__nv_bfloat16>(a, D, s);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD, s, false);
-    e = launch_second(seq_bwd_kernel<D>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H))), dim3(kThreads), smem, s, prm);
+    e = launch_early(seq_bwd_kernel<D>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H))), dim3(kThreads), smem, s, prm);
     note_launch(SGA_KERN_SEQ_BWD, s, true);
     return e;
 }

@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
     const int hk = head[0] / (a.H / a.Hkv);
     const int t0 = min(st[0].t0, st[NS - 1].t0), t1 = max(st[0].t1, st[NS - 1].t1), n = t1 - t0;
 
-    if (warp == 0) tc::tmem_alloc(&tmem_base, C::TCOLS);
     if (tid == 32) {
         tc::mbar_init(&q_full, 1);
         for (int i = 0; i < C::NST; ++i) {
@@ -111,6 +110,9 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
         }
         tc::mbar_init(&mma_done, 1);
     }
+    let_next_start();
+    wait_previous();
+    if (warp == 0) tc::tmem_alloc(&tmem_base, C::TCOLS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -340,9 +342,9 @@ template <int D, int NS> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
                           : prm.pair_heads ? (int64_t)a.n_tiles * (a.H / 2)
                                            : (int64_t)((a.n_tiles + 1) / 2) * a.H;
     note_launch(SGA_KERN_SEQ_FWD, s, false);
-    seq_fwd_kernel<D, NS><<<(unsigned)units, C::THREADS, C::BYTES + 1024, s>>>(prm);
+    e = launch_early(seq_fwd_kernel<D, NS>, dim3((unsigned)units), dim3(C::THREADS), C::BYTES + 1024, s, prm);
     note_launch(SGA_KERN_SEQ_FWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

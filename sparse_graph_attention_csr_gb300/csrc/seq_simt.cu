@@ -216,6 +216,7 @@ __device__ __forceinline__ uint32_t unit_of_block(const SeqArgs &a) {
 
 template <int D, int RA, int TY, int MB> __global__ void __launch_bounds__(16 * TY, MB) seq_fwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
+    wait_previous();
     float *sQ = sm, *sK = sQ + kOwnFloats<D, RA, TY>, *sV = sK + kTileFloats<D>, *sP = sV + kTileFloats<D>;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     const Unit<RA, TY> u(unit_of_block(a), a.H);
@@ -451,7 +452,7 @@ template <int D, int RA, int TY> __device__ __forceinline__ void dkdv_pass(const
 // Both passes in one launch, the dK/dV units (the longer ones) first.
 template <int D, int RA, int TY, int MB> __global__ void __launch_bounds__(16 * TY, MB) seq_bwd_f32_kernel(const SeqArgs a) {
     extern __shared__ __align__(16) float sm[];
-    second_of_two();
+    wait_previous();
     const uint32_t kv = (uint32_t)a.n_tiles * a.Hkv * (kT / (TY * RA));
     if (blockIdx.x < kv) dkdv_pass<D, RA, TY>(a, sm, blockIdx.x);
     else dq_pass<D, RA, TY>(a, sm, blockIdx.x - kv);
@@ -462,7 +463,8 @@ template <int D, int RA, int TY, int MB> __global__ void __launch_bounds__(16 * 
 // that their weights are zero, and Delta = 0.
 constexpr int kTerms = 4;
 template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
-    first_of_two();
+    let_next_start();
+    wait_previous();
     constexpr int EL = Elt<T>::EL, L = D / EL, G = 256 / L;   // G items of a block at a time
     const int sub = threadIdx.x % L;
     const int64_t live = a.rows * a.H, n = a.rows_pad * a.H, g0 = (int64_t)blockIdx.x * (G * kTerms) + threadIdx.x / L;
@@ -502,9 +504,9 @@ template <int D, int RA, int TY, int MB> cudaError_t launch_fwd(const SeqArgs &a
     constexpr size_t smem = sizeof(float) * (kOwnFloats<D, RA, TY> + 2 * kTileFloats<D> + kScoreFloats<RA, TY>);
     if (cudaError_t e = allow_smem<seq_fwd_f32_kernel<D, RA, TY, MB>>(smem); e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_FWD, s, false);
-    seq_fwd_f32_kernel<D, RA, TY, MB><<<(unsigned)((int64_t)a.n_tiles * a.H * (kT / (TY * RA))), 16 * TY, smem, s>>>(a);
+    const cudaError_t e = launch_early(seq_fwd_f32_kernel<D, RA, TY, MB>, dim3((unsigned)((int64_t)a.n_tiles * a.H * (kT / (TY * RA)))), dim3(16 * TY), smem, s, a);
     note_launch(SGA_KERN_SEQ_FWD, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 template <int D, int RA, int TY, int MB> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
@@ -516,7 +518,7 @@ template <int D, int RA, int TY, int MB> cudaError_t launch_bwd(const SeqArgs &a
     if (e == cudaSuccess) e = seq_row_terms<float>(a, D, s);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD, s, false);
-    e = launch_second(seq_bwd_f32_kernel<D, RA, TY, MB>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H) * (kT / (TY * RA)))),
+    e = launch_early(seq_bwd_f32_kernel<D, RA, TY, MB>, dim3((unsigned)((int64_t)a.n_tiles * (a.Hkv + a.H) * (kT / (TY * RA)))),
                       dim3(16 * TY), smem, s, a);
     note_launch(SGA_KERN_SEQ_BWD, s, true);
     return e;
@@ -525,9 +527,9 @@ template <int D, int RA, int TY, int MB> cudaError_t launch_bwd(const SeqArgs &a
 template <typename T, int D> cudaError_t launch_terms(const SeqArgs &a, cudaStream_t s) {
     constexpr int per = kTerms * 256 / (D / Elt<T>::EL);   // items of a block
     note_launch(SGA_KERN_SEQ_BWD_ROWS, s, false);
-    seq_row_terms_kernel<T, D><<<(unsigned)((a.rows_pad * a.H + per - 1) / per), 256, 0, s>>>(a);
+    const cudaError_t e = launch_early(seq_row_terms_kernel<T, D>, dim3((unsigned)((a.rows_pad * a.H + per - 1) / per)), dim3(256), 0, s, a);
     note_launch(SGA_KERN_SEQ_BWD_ROWS, s, true);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
