@@ -105,3 +105,71 @@ def test_a_captured_layer():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, model(p, ids, seq_plan, plan))
+
+
+@pytest.mark.parametrize("dtype,heads,kv,width", [(torch.bfloat16, 4, 2, 64), (torch.bfloat16, 2, 2, 128),
+                                                  (torch.bfloat16, 4, 1, 32), (torch.float32, 4, 2, 32)])
+def test_calls_in_a_row_equal_calls_apart(dtype, heads, kv, width):
+    """Kernels start while the one before them ends: a chain of calls, each on the
+    results of earlier ones and into buffers that earlier ones read, gives bit
+    for bit what the same calls give one by one, and captured."""
+    lens, c, rows = [300, 1, 70, 129, 700], heads * width, 90
+    T = sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dtype)
+    ptr = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device="cuda")
+    seqs = sga.SeqPlan(ptr, heads, width, dtype, kv_heads=kv, causal=True)
+    few, many = (torch.randint(0, n, (T,), generator=gen, device="cuda") for n in (rows, 70000))
+    tables, w, b, dO = (r(rows, c), r(70000, c)), r(c), r(c), r(T, heads, width)
+    indptr = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    edge = sga.Plan(indptr, indptr[:-1].flip(0).contiguous(), heads, width, dtype)
+    x, y, dx, o, dq, e = (torch.empty(T, c, device="cuda", dtype=dtype) for _ in range(6))
+    k, v, dk, dv = (torch.empty(T, kv, width, device="cuda", dtype=dtype) for _ in range(4))
+    mean, rstd, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty(T, heads, device="cuda")
+    dw, db, dts = torch.empty_like(w), torch.empty_like(b), [torch.empty_like(t) for t in tables]
+    h = lambda t: t.view(T, heads, width)
+    steps = []
+    for i, ids in enumerate((few, many)):
+        steps += [
+            lambda i=i, ids=ids: sga.embed_fwd(ids, tables[i], out=x),
+            lambda: sga.layer_norm_fwd(x, w, b, out=y, mean=mean, rstd=rstd),
+            lambda: k.copy_(h(y)[:, :kv]), lambda: v.copy_(h(x)[:, -kv:]),
+            lambda: sga.seq_attn_fwd(seqs, h(y), k, v, out=h(o), lse=lse),
+            lambda: sga.seq_attn_bwd(seqs, h(y), k, v, h(o), lse, dO, dQ=h(dq), dK=dk, dV=dv),
+            lambda: sga.seq_attn_fwd(seqs, h(dq), dk, dv, out=h(e)),
+            lambda: sga.seq_attn_fwd(seqs, h(o), dk, v, out=h(dx)),
+            lambda: sga.layer_norm_bwd(x, w, mean, rstd, dq, dX=dx, dweight=dw, dbias=db),
+            lambda: sga.layer_norm_fwd(dx, dw, db, out=dq),
+            lambda i=i, ids=ids: sga.embed_bwd(ids, dx, len(tables[i]), dTable=dts[i]),
+            lambda i=i: sga.embed_fwd(few, dts[i], out=x),
+            lambda: e.add_(sga.gt_attn_fwd(edge, h(x), h(dq), h(y))[0].view(T, c)),
+            lambda: sga.layer_norm_fwd(e, w, b, out=e),
+        ]
+    results = [x, y, dx, o, dq, e, k, v, dk, dv, mean, rstd, lse, dw, db, *dts]
+
+    def run(apart):
+        for step in steps:
+            step()
+            if apart:
+                torch.cuda.synchronize()
+
+    run(True)
+    want = [t.clone() for t in results]
+    assert all(torch.isfinite(t.float()).all() for t in want)
+    for _ in range(5):
+        for t in results:
+            t.fill_(1)
+        run(False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, u) for t, u in zip(results, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(False)
+        run(False)
+    for _ in range(3):
+        for t in results:
+            t.fill_(1)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, u) for t, u in zip(results, want))
+    assert seqs.device_error() == 0 and edge.device_error() == 0 and sga.embed_device_error() == 0
