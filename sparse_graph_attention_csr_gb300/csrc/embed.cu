@@ -486,21 +486,22 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
 }
 
 // Few rows (atom or edge types) and few tokens: no sort.  A block takes
-// consecutive tokens; each of its warps owns every 32nd row and adds the row's
-// tokens in order, found by a vote over the block's ids, so nothing is shared.
-// Then a warp adds the blocks' sums.  STAGED: the block's part of dOut, which is
-// contiguous, is copied to shared memory while the ids are listed, so that a warp
-// with a frequent row does not wait for memory batch after batch.  30011 tokens x
-// 100 into 119 rows, id i with a weight of 1 / i: fp32 16.5 us a call (19.0 from
-// memory, 28 sorted), bf16 16.4 (24.9).
+// consecutive tokens; each of its warps owns every 32nd row, finds the rows'
+// tokens by votes over the block's ids and adds them in order, so that nothing is
+// shared.  Then a warp adds the blocks' sums.  STAGED: the block's part of dOut,
+// which is contiguous, is copied to shared memory while the ids are listed, so
+// that a warp with a frequent row does not wait for memory batch after batch.
+// 30011 tokens x 100 into 119 rows, id i with a weight of 1 / i: fp32 14.4 us a
+// call (2.5 more from memory, 28 sorted), bf16 13.6 (8.5 more from memory).
 constexpr int kFewRows = 256, kFewTokens = 512;   // rows; tokens of a block
-constexpr size_t kStage = 190 * 1024;             // shared memory beside the lists
+constexpr size_t kStage = 220 * 1024;             // shared memory beside the lists
 
 template <typename T, bool VEC, bool STAGED>
 __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const GradArgs a, int64_t per) {
     constexpr int EL = kEl<T, VEC>, M = VEC ? 8 : 4, U = VEC ? 1 : 4;   // M tokens in flight, of U groups each
     __shared__ int32_t id[kFewTokens];
-    __shared__ uint16_t list[kSortWarps][kFewTokens];   // a warp's tokens, by row and in order: token | row / 32 << 9
+    __shared__ uint16_t found[kFewTokens], sorted[kFewTokens];   // the warps' tokens in order, and by row: token | row / 32 << 9
+    __shared__ int32_t count[kSortWarps];
     extern __shared__ __align__(16) unsigned char stage[];
     static_assert(kFewTokens <= 512 && kFewRows <= 32 * 128, "list entries");
     let_next_start();
@@ -520,16 +521,30 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
     for (int i = threadIdx.x; i < kFewTokens; i += kSortThreads) id[i] = i < cnt ? key_of(a, t0 + i) : V;
     __syncthreads();
     float *part = a.part + ((int64_t)blockIdx.x * V + wp) * a.C;   // the warp's first row; the next is 32 rows on
+    const uint32_t below = (1u << lane) - 1u;
+    auto mine = [&](int b) { return (id[b + lane] & 31) == wp && id[b + lane] < V; };
     int total = 0;
-    for (int q = 0; wp + 32 * q < V; ++q) {
-        const int before = total;
-        for (int b = 0; b < cnt; b += 32) {
-            const bool on = id[b + lane] == wp + 32 * q;
-            const uint32_t who = __ballot_sync(SGA_FULL_MASK, on);
-            if (on) list[wp][total + __popc(who & ((1u << lane) - 1u))] = (uint16_t)((b + lane) | q << 9);
-            total += __popc(who);
+    for (int b = 0; b < cnt; b += 32) total += __popc(__ballot_sync(SGA_FULL_MASK, mine(b)));
+    if (lane == 0) count[wp] = total;
+    __syncthreads();
+    const int base = __reduce_add_sync(SGA_FULL_MASK, lane < wp ? count[lane] : 0);
+    uint16_t *f = found + base, *list = sorted + base;
+    for (int b = 0, at = 0; b < cnt; b += 32) {
+        const bool on = mine(b);
+        const uint32_t who = __ballot_sync(SGA_FULL_MASK, on);
+        if (on) f[at + __popc(who & below)] = (uint16_t)((b + lane) | (id[b + lane] >> 5) << 9);
+        at += __popc(who);
+    }
+    __syncwarp();
+    for (int q = 0, at = 0; wp + 32 * q < V; ++q) {
+        const int before = at;
+        for (int b = 0; b < total; b += 32) {
+            const int e = b + lane < total ? f[b + lane] : -1;
+            const uint32_t who = __ballot_sync(SGA_FULL_MASK, e >> 9 == q);
+            if (e >> 9 == q) list[at + __popc(who & below)] = (uint16_t)e;
+            at += __popc(who);
         }
-        if (total == before)   // a row without a token here
+        if (at == before)   // a row without a token here
             for (int c = lane; c < a.C; c += 32) part[(int64_t)32 * q * a.C + c] = 0.f;
     }
     if constexpr (STAGED) {
@@ -557,7 +572,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
             int row[M];
 #pragma unroll
             for (int z = 0; z < M; ++z) {
-                const int e = k + z < total ? list[wp][k + z] : -1;
+                const int e = k + z < total ? list[k + z] : -1;
                 row[z] = e >> 9;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {

@@ -11,8 +11,8 @@
 // D + 4 floats: both products read them 16 bytes at a time along a row without
 // bank conflicts, so no tile is stored transposed.  RA = 4 reads half as much
 // shared memory a product as RA = 2, and 128 threads leave a thread the
-// registers to read ahead: 2048 rows, 8 heads of 64, full, forward 275 us (31
-// TFLOP/s), backward 791 (938 with 256 threads).
+// registers to read ahead: 2048 rows, 8 heads of 64, full, forward 272 us (32
+// TFLOP/s), backward 789 (938 with 256 threads).
 //   forward: S = Q K^T, online softmax (running maximum and sum per row),
 //     O = O alpha + P V;
 //   dQ pass (a tile of queries): S, dP = dOut V^T, dS = P (dP - Delta),
@@ -541,16 +541,17 @@ template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t);
 template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
 
 // Owner tiles of 32 rows (4 x 8); of 16 (2 x 8) where 32 would leave SMs without
-// a block: 512 rows, 4 heads (64 units of 32), forward D = 32, 64, 128: 16 rows
-// 18.7, 24.8, 37.1 us, 32 rows 24.8, 33.0, 47.4; 1024 rows, 8 heads (256),
-// D = 64: 117 : 84.  Backward, 256 rows, 4 heads (64): 16.6, 22.8, 33.2 :
-// 18.9, 27.1, 41.3.  In the forward four blocks an SM fit in 128 registers a
-// thread with a few spills, against three: 2048 rows, 8 heads (512 units), D =
-// 32 174 : 213 us, D = 64 275 : 309; fewer units do not need them (256, D = 64,
-// causal 64 : 62).  In the backward D = 32 is faster with two blocks an SM while
-// they are enough (1024 rows, 4 heads 81 : 102 us, 8 heads 140 : 124), and D = 128,
-// whose tiles leave room for one block an SM, with 64 rows and 256 threads from
-// there on (1024 rows, 8 heads 400 : 484 us; 512 rows, 8 heads, causal 117 : 74).
+// a block (us a call, launches apart): 512 rows, 4 heads (64 units of 32),
+// forward D = 32, 64, 128: 16 rows 18.7, 24.8, 37.1, 32 rows 24.8, 33.0, 47.4;
+// 1024 rows, 8 heads (256), D = 64: 117 : 84.  Backward, 256 rows, 4 heads (64):
+// 16.6, 22.8, 33.2 : 18.9, 27.1, 41.3.  In the forward four blocks an SM fit in
+// 128 registers a thread with a few spills, against three: 2048 rows, 8 heads
+// (512 units), D = 32 174 : 213, D = 64 275 : 309; fewer units do not need them
+// (256, D = 64, causal 64 : 62).  In the backward D = 32 is faster with two blocks
+// an SM while they are enough (1024 rows, 4 heads 81 : 102, 8 heads 140 : 124), and
+// D = 128, whose tiles leave room for one block an SM, with 64 rows and 256
+// threads from there on (1024 rows, 8 heads 400 : 484; 512 rows, 8 heads, causal
+// 117 : 74).
 cudaError_t seq_fwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
     const int64_t units = 2 * (int64_t)a.n_tiles * a.H;
     if ((D == 128 ? 2 : 1) * units <= a.num_sms)

@@ -173,3 +173,63 @@ def test_calls_in_a_row_equal_calls_apart(dtype, heads, kv, width):
         torch.cuda.synchronize()
         assert all(torch.equal(t, u) for t, u in zip(results, want))
     assert seqs.device_error() == 0 and edge.device_error() == 0 and sga.embed_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_forked_streams(dtype):
+    """Calls on two streams that fork and join, eager and in one captured graph:
+    a call waits for what its stream waits for, not for the kernel before it only."""
+    T, c, rows = 1200, 128, 50
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dtype)
+    seqs = sga.SeqPlan(torch.tensor([0, 500, 501, T], dtype=torch.int32, device="cuda"), 2, 64, dtype, causal=False)
+    ids, table, w, b = torch.randint(0, rows, (T,), generator=gen, device="cuda"), r(rows, c), r(c), r(c)
+    x, y, z, o, dt = (torch.empty(n, c, device="cuda", dtype=dtype) for n in (T, T, T, T, rows))
+    h = lambda t: t.view(T, 2, 64)
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        sga.embed_fwd(ids, table, out=x)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            sga.layer_norm_fwd(x, w, b, out=y)           # beside the attention on the main stream
+        sga.seq_attn_fwd(seqs, h(x), h(x), h(x), out=h(z))
+        main.wait_stream(side)
+        sga.seq_attn_fwd(seqs, h(y), h(z), h(x), out=h(o))   # of both
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            sga.embed_bwd(ids, o, rows, dTable=dt)
+            sga.layer_norm_fwd(o, w, b, out=y)
+        main.wait_stream(side)
+        sga.layer_norm_fwd(y, w, b, out=x)
+
+    results = (x, y, z, o, dt)
+    run()
+    torch.cuda.synchronize()
+    sga.embed_fwd(ids, table, out=x)
+    torch.cuda.synchronize()
+    ref = [sga.layer_norm_fwd(x, w, b)[0], sga.seq_attn_fwd(seqs, h(x), h(x), h(x))[0]]
+    torch.cuda.synchronize()
+    ref.append(sga.seq_attn_fwd(seqs, h(ref[0]), ref[1], h(x))[0].view(T, c))
+    torch.cuda.synchronize()
+    y2 = sga.layer_norm_fwd(ref[2], w, b)[0]
+    torch.cuda.synchronize()
+    want = (sga.layer_norm_fwd(y2, w, b)[0], y2, ref[1].view(T, c), ref[2], sga.embed_bwd(ids, ref[2], rows))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for t in results:
+            t.fill_(1)
+        run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, u) for t, u in zip(results, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(5):
+        for t in results:
+            t.fill_(1)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, u) for t, u in zip(results, want))
+    assert seqs.device_error() == 0 and sga.embed_device_error() == 0
