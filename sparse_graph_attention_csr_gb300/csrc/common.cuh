@@ -197,7 +197,8 @@ void note_launch(sga_kernel_id which, cudaStream_t s, bool after);
 // return (so that its own end implies the end of all before it).
 // No block may hold tensor memory while it waits: a block of the kernel that it
 // waits for may still have to allocate its own.  let_next_start() may be called at
-// any time.  Kernels whose next one fills the GPU with equal shares a block
+// any time, by a kernel with tensor memory once every block has its own (the next
+// kernel may be a library's, which takes its own before it waits).  Kernels whose next one fills the GPU with equal shares a block
 // (norm_reduce before a norm's backward, the attention backward, the fp32
 // attention forward) do not call it: blocks that start early, where there is
 // room, leave the SMs unevenly filled (169343 x 512 layer norm backward 90 -> 117

@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
         }
         tc::mbar_init(&mma_done, 1);
     }
-    let_next_start();
     wait_previous();
     if (warp == 0) tc::tmem_alloc(&tmem_base, C::TCOLS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    let_next_start();
     const uint32_t tS = tmem_base + C::TS, tO = tmem_base + C::TO;
 
     if (warp < 4) {
