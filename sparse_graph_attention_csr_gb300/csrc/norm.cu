@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
 // same sums, but each thread copies its vectors of the next STAGES - 1 rows into
 // its own slots of shared memory (cp.async; nothing is shared, so there is no
 // barrier).  The loads in flight are then not bound by registers: 169343 x 512
-// bf16 takes 97 us with a row ahead in registers (128 threads, 16 warps an SM).
+// bf16 takes 87 us, with a row ahead in registers 97 (128 threads, 16 warps an SM).
 constexpr int kRingThreads = 128, kRingStages = 6;
 
 template <typename TX, typename TW, int TPR, int NV>
@@ -539,7 +539,7 @@ template <typename TX, typename TW, int TPR, int NV> cudaError_t launch_bwd_ring
 
 // Threads of a row by its number of 16-byte vectors (or of elements, where the
 // width or an address is no multiple of 16 bytes).  Two vectors a thread where
-// a warp can hold the row: of 1048576 x 256 bf16, 172 us (6.2 TB/s) with two,
+// a warp can hold the row: of 1048576 x 256 bf16, 170 us (6.3 TB/s) with two,
 // 189 with four, 193 with one; blocks of 128 threads, 32 an SM (16 to 64 the
 // same, 8 15% slower).
 template <typename TX, typename TW> cudaError_t norm_fwd_t(const NormArgs &a, bool vec, bool pairs, cudaStream_t s) {
