@@ -22,7 +22,9 @@
 // Roles as in the forward: one lane loads by TMA, one issues the products,
 // eight warps (two per TMEM lane quarter, each with half of a tile's columns)
 // turn scores into weights.  P and dS are rounded to bf16 once (half a step,
-// 2^-8 relative), which is of the size of the rounding of the gradients.
+// 2^-8 relative), which is of the size of the rounding of the gradients; in dQ,
+// whose terms cancel where the keys share an offset, the sum of the roundings is
+// taken out again (at the dQ pass).
 //
 // As in the forward, a row whose result is not finite is computed again over
 // its own interval alone, so that nothing of a pair that is masked reaches it.
@@ -71,7 +73,8 @@ template <int D> struct QCfg : BwdCfg<D> {
     using B = BwdCfg<D>;
     static constexpr int NK = 4, NV = 3;                          // K, V tiles in flight
     static constexpr uint32_t ST0 = 0, V0 = ST0 + NK * B::TB;
-    static constexpr uint32_t BAR0 = V0 + NV * B::TB, BYTES = BAR0 + 256;   // barriers
+    static constexpr uint32_t RES0 = V0 + NV * B::TB;             // sums of a row's rounding errors, by part
+    static constexpr uint32_t BAR0 = RES0 + kParts * 512, BYTES = BAR0 + 256;   // barriers
     static constexpr uint32_t TS = 0, TP = 128, TQ = 256, TA = 384, TG = 448;   // S, dP, dQ; Q and dOut as A operands
 };
 constexpr uint32_t kMaxSmem = 227 * 1024;
@@ -139,27 +142,33 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t *v) {
 #pragma unroll
     for (int c = 0; c < N; c += 32) tc::tmem_wait_ld(v + c);
 }
-// The weights as bf16 pairs over the first half of their scores' columns.
-__device__ __forceinline__ void store_weights(uint32_t taddr, const float *p) {
-    constexpr int N = kCols;
-    static_assert(N == 64, "one store of 32 columns");
-    uint32_t pk[N / 2];
+// The weights as bf16 pairs, over the first half of their scores' columns.
+__device__ __forceinline__ void round_weights(const float *p, uint32_t *pk) {
 #pragma unroll
-    for (int c = 0; c < N; c += 2) pk[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
+    for (int c = 0; c < kCols; c += 2) pk[c >> 1] = pack_bf16x2(p[c], p[c + 1]);
+}
+__device__ __forceinline__ void store_weights(uint32_t taddr, const uint32_t *pk) {
+    static_assert(kCols == 64, "one store of 32 columns");
     tc::tmem_st32_async(taddr, pk);
     tc::tmem_wait_st();
 }
+__device__ __forceinline__ void store_weights(uint32_t taddr, const float *p) {
+    uint32_t pk[kCols / 2];
+    round_weights(p, pk);
+    store_weights(taddr, pk);
+}
 
-// 32 columns of a row from TMEM, scaled, to bf16 at dst (if `in`); the lanes
-// whose row was not finite.
-__device__ __forceinline__ uint32_t store_from_tmem(uint32_t taddr, __nv_bfloat16 *dst, float f, bool in) {
+// 32 columns of a row from TMEM, less `sub` (if any), scaled, to bf16 at dst (if
+// `in`); the lanes whose row was not finite.
+__device__ __forceinline__ uint32_t store_from_tmem(uint32_t taddr, __nv_bfloat16 *dst, float f, bool in,
+                                                    const float *sub = nullptr) {
     bool bad = false;
     uint32_t o[32];
     tc::tmem_ld32(taddr, o);   // warp-collective: every lane takes part
     float x[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        x[i] = __uint_as_float(o[i]) * f;
+        x[i] = (sub ? __uint_as_float(o[i]) - sub[i] : __uint_as_float(o[i])) * f;
         bad |= !(fabsf(x[i]) < INFINITY);
     }
     if (in)
@@ -389,6 +398,48 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
 }
 
 // ---- dQ ----------------------------------------------------------------------------
+//
+// A row's dS sum to zero, so an offset that all keys share leaves no trace in
+// dQ = sum_j dS_j k_j; but of dS rounded to bf16, dS_j + e_j, it leaves offset x
+// sum_j e_j, which grows with the offset while dQ does not.  The weight warps
+// know every e_j, so in a column with an offset dQ is formed as sum_j (dS_j +
+// e_j) k_j - (sum_j e_j) c, c being the mean of four of the row's own keys: an error
+// of sum_j e_j (k_j - c), in which the offset is gone.  Nothing is assumed of dS
+// itself.  (A second product, of the e_j, would be the eighth of the two
+// passes; what is left of dQ's error is then the forward's, whose rounded out
+// enters Delta.)  512 keys of 64 +- 1, bf16, D = 64, queries of 1 / 64: dQ's
+// error against the formula with that out is 0.0025 of its norm, and was 0.104
+// with single roundings.  It costs 2% at 8192 rows, 8/4 heads of 128 (causal 303
+// -> 310 us), 5% at 8 heads of 64 (235 -> 251) and 1.7 us on 128 graphs of 9 to 38
+// rows, 4 heads of 64 (16.6 -> 18.3).  In dK = sum_i dS_i q_i the terms of a key's queries do not cancel:
+// its roundings are of the size of dK's own.
+
+// c at the columns [c0, c0 + 32) as bf16 pairs, zero in a column where the four
+// are farther apart than |c| / 2 (no offset to speak of).  c lies between them:
+// they are representable, and each rounding on the way to it is monotone.  Of
+// eight keys and more rows of similar lengths take the same four, so that their
+// loads are one.
+__device__ __forceinline__ void mean_key(const SeqArgs &a, int D, int64_t lo, int64_t hi, int hk, int c0, uint32_t (&c)[16]) {
+    const int64_t n = max(hi - lo, (int64_t)1), m = n < 8 ? n : (int64_t)1 << (31 - __clz((int)n));   // (n < 2^31)
+    uint4 raw[4][4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.K) + ((lo + (m * (2 * s + 1) >> 3)) * a.Hkv + hk) * D + c0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) raw[s][q] = ldg16(k + 8 * q);
+    }
+    const __nv_bfloat162 fourth = __float2bfloat162_rn(0.25f), half = __float2bfloat162_rn(0.5f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        __nv_bfloat162 x[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[s] = reinterpret_cast<const __nv_bfloat162 *>(raw[s])[i];
+        const __nv_bfloat162 mean = __hadd2(__hfma2(x[1], fourth, __hmul2(x[0], fourth)), __hfma2(x[3], fourth, __hmul2(x[2], fourth))),
+                             apart = __hsub2(__hmax2(__hmax2(x[0], x[1]), __hmax2(x[2], x[3])),
+                                             __hmin2(__hmin2(x[0], x[1]), __hmin2(x[2], x[3])));
+        c[i] = reinterpret_cast<const uint32_t &>(mean) & __hle2_mask(apart, __hmul2(__habs2(mean), half));
+    }
+}
 
 template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, unsigned char *smem, uint32_t unit) {
     using C = QCfg<D>;
@@ -534,6 +585,20 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
             if (lane == 0) tc::mbar_arrive(&q_full);
         }
         const uint32_t ts = tS + part * N + tl, tp = tP + part * N + tl;
+        constexpr int SL = D <= 32 * kParts ? 1 : D / (32 * kParts);   // slices of 32 columns that a part stores
+        uint32_t mean[SL][16];
+#pragma unroll
+        for (int k = 0; k < SL; ++k)   // (while the first tiles arrive)
+            if ((k * kParts + part) * 32 < D) mean_key(a, D, lo, hi, hk, (k * kParts + part) * 32, mean[k]);
+        float2 res = make_float2(0.f, 0.f);   // the part's sum of e_j
+        float p[N];                           // a tile's dS, and rounded
+        uint32_t pk[N / 2];
+#pragma unroll
+        for (int c = 0; c < N; ++c) p[c] = __uint_as_float(pk[c >> 1] = 0u);
+        auto add_errors = [&](int c) {   // of the columns c, c + 1
+            const float2 r = make_float2(__uint_as_float(pk[c >> 1] << 16), __uint_as_float(pk[c >> 1] & 0xffff0000u));
+            res = fadd2(res, ffma2(make_float2(p[c], p[c + 1]), make_float2(-1.f, -1.f), r));
+        };
         bool ok = true;
         for (int i = 0; i < n; ++i) {
             const int kt = t.t0 + i;
@@ -547,9 +612,11 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&s_free);
-            float p[N];
+            // the errors of the tile before are added between the exponentials, which
+            // leave issue slots (after the dS have been handed over: 8% slower)
 #pragma unroll
             for (int c = 0; c < N; c += 2) {
+                add_errors(c);
                 const float2 x = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2, l2);
                 p[c] = fast_exp2(x.x);
                 p[c + 1] = fast_exp2(x.y);
@@ -576,17 +643,36 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
                     if (!((bits >> (c & 31)) & 1u)) p[c] = 0.f;
                 }
             }
-            store_weights(tp, p);
+            round_weights(p, pk);
+            store_weights(tp, pk);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ds_full);
         }
+#pragma unroll
+        for (int c = 0; c < N; c += 2) add_errors(c);
+        // the parts' sums, added in order (every weight warp comes here, after a timeout too)
+        float *sums = reinterpret_cast<float *>(smem + C::RES0);
+        sums[part * 128 + quarter * 32 + lane] = res.x + res.y;
+        asm volatile("bar.sync 1, %0;" ::"n"(128 * kParts) : "memory");
+        float err = sums[quarter * 32 + lane];
+#pragma unroll
+        for (int k = 1; k < kParts; ++k) err += sums[k * 128 + quarter * 32 + lane];
         if (ok && !tc::warp_wait(&acc_full, 0, tc::kWaitLimit)) ok = false;
         if (ok) {
             tc::fence_after_sync();
-            for (int c0 = part * 32; c0 < D; c0 += 32 * kParts) {
+#pragma unroll
+            for (int k = 0; k < SL; ++k) {
+                const int c0 = (k * kParts + part) * 32;
+                if (c0 >= D) break;
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dQ) + ((in ? row : 0) * a.H + h) * D + c0;
-                uint32_t again = store_from_tmem(tQ + c0 + tl, dst, a.scale, in);
+                float sub[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sub[2 * i] = err * __uint_as_float(mean[k][i] << 16);
+                    sub[2 * i + 1] = err * __uint_as_float(mean[k][i] & 0xffff0000u);
+                }
+                uint32_t again = store_from_tmem(tQ + c0 + tl, dst, a.scale, in, sub);
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;
