@@ -336,7 +336,8 @@ size_t sga_seq_bwd_workspace_bytes(const sga_seq_plan *plan);
 /* As sga_read_device_error, for a sequence plan. */
 sga_status sga_seq_read_device_error(const sga_seq_plan *plan, void *stream, int32_t *code);
 
-/* scale: positive and finite.  The current device must be the plan's. */
+/* scale: positive, and scale log2(e) finite in float32 (scores are held in
+ * units of log2).  The current device must be the plan's. */
 sga_status seq_attn_fwd(const sga_seq_plan *plan, const void *Q, const void *K, const void *V, int64_t T, float scale,
                         void *out, float *lse, void *stream);
 

@@ -168,8 +168,8 @@ int64_t seq_inputs(const SeqPlan &p, const Tensor &Q, const Tensor &K, const Ten
 float seq_scale(const SeqPlan &p, std::optional<double> scale) {
     if (!scale) return (float)(1.0 / std::sqrt((double)p.D));
     const float f = (float)*scale;   // (a double may overflow, or round to zero)
-    if (!(f > 0.f) || !std::isfinite(f))
-        throw py::value_error("scale must be a positive and finite float32, got " + std::to_string(*scale));
+    if (!(f > 0.f) || !std::isfinite(f * 1.4426950408889634f))   // (scores are held in units of log2)
+        throw py::value_error("scale must be positive, and scale log2(e) a finite float32, got " + std::to_string(*scale));
     return f;
 }
 

@@ -137,7 +137,7 @@ cudaError_t seq_build(sga_seq_plan *p, const std::vector<int32_t> &ptr, const in
 sga_status check_seq(const sga_seq_plan *p, int64_t T, float scale, std::initializer_list<const void *> ps) {
     if (!p) return SGA_EINVAL;
     if (T < p->rows) return SGA_EINVAL;
-    if (!(scale > 0.f) || !(scale < INFINITY)) return SGA_EINVAL;
+    if (!(scale > 0.f) || !(scale * kLog2e < INFINITY)) return SGA_EINVAL;   // (scores are held in units of log2)
     if (p->rows == 0) return SGA_OK;
     for (const void *q : ps)
         if (!q || !aligned(q, 16)) return SGA_EINVAL;
