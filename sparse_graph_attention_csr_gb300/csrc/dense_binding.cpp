@@ -15,6 +15,7 @@
 #include <cmath>
 #include <limits>
 #include <optional>
+#include <sstream>
 #include <string>
 
 #include "../../include/sga.h"
@@ -257,8 +258,12 @@ Norm norm_inputs(const Tensor &X, const Maybe &weight, const Maybe &bias) {
 py::tuple layer_norm_fwd_(const Tensor &X, const Maybe &weight, const Maybe &bias, double eps, const Maybe &out,
                           const Maybe &mean, const Maybe &rstd, const py::object &stream) {
     const Norm n = norm_inputs(X, weight, bias);
-    if (!(eps >= 0.0) || !(eps < std::numeric_limits<double>::infinity()))
-        throw py::value_error("eps must be finite and not negative, got " + std::to_string(eps));
+    const float feps = (float)eps;   // (a double may overflow, or round to zero)
+    if (!(eps >= 0.0) || !std::isfinite(feps) || (feps == 0.f && eps != 0.0)) {
+        std::ostringstream got;
+        got << eps;
+        throw py::value_error("eps must be zero or a positive and finite float32, got " + got.str());
+    }
     const at::Device dev = X.device();
     const Place on(dev, stream);
     Tensor o = out ? *out : fresh(X.sizes(), X.scalar_type(), dev), m = mean ? *mean : fresh(n.lead, at::kFloat, dev),
@@ -272,7 +277,7 @@ py::tuple layer_norm_fwd_(const Tensor &X, const Maybe &weight, const Maybe &bia
         distinct({named("out", o), named("mean", m), named("rstd", r)},
                  {named("X", x), named("weight", weight), named("bias", bias)});
     }
-    check(layer_norm_fwd(ptr(X), ptr(weight), ptr(bias), n.N, n.C, (float)eps, n.dt, n.wdt, ptr(o),
+    check(layer_norm_fwd(ptr(X), ptr(weight), ptr(bias), n.N, n.C, feps, n.dt, n.wdt, ptr(o),
                          static_cast<float *>(ptr(m)), static_cast<float *>(ptr(r)), on.raw()),
           "layer_norm_fwd");
     on.used({named("X", X), named("weight", weight), named("bias", bias)}, {named("out", o), named("mean", m), named("rstd", r)});
