@@ -26,8 +26,8 @@
 // whose terms cancel where the keys share an offset, the sum of the roundings is
 // taken out again (at the dQ pass).
 //
-// As in the forward, a row whose result is not finite is computed again over
-// its own interval alone, so that nothing of a pair that is masked reaches it.
+// As in the forward, what is not finite in a row for a row that is masked for it
+// is computed again over its own interval alone.
 // Measured: 8192 rows, 8/4 heads of 128, causal 302 us, full 561 us: 1.22
 // PFLOP/s of the five products that a backward pass needs, 1.71 of the seven
 // computed, the rate of the library's product under the power limit (1.70).
@@ -372,18 +372,26 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
         if (ok && !tc::warp_wait(&acc_full, 0, tc::kWaitLimit)) ok = false;
         if (ok) {
             tc::fence_after_sync();
+            uint32_t again[2] = {0, 0};   // rows of dV, dK
             for (int c = part; c < D / 16; c += kParts) {   // 32 columns each: dV's, then dK's
                 const bool dk = c >= D / 32;
                 const int c0 = (dk ? c - D / 32 : c) * 32;
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(dk ? a.dK : a.dV) + ((in ? row : 0) * a.Hkv + hk) * D + c0;
-                uint32_t again = store_from_tmem((dk ? tK : tV) + c0 + tl, dst, dk ? a.scale : 1.f, in);
-                while (again) {
-                    const int src = __ffs(again) - 1;
-                    again &= again - 1;
-                    seq::key_row_alone<__nv_bfloat16, D>(a, dk, __shfl_sync(SGA_FULL_MASK, row, src), hk, __shfl_sync(SGA_FULL_MASK, lo, src),
-                                     __shfl_sync(SGA_FULL_MASK, hi, src), c0, 32);
-                }
+                const uint32_t bad = store_from_tmem((dk ? tK : tV) + c0 + tl, dst, dk ? a.scale : 1.f, in);
+                if (dk) again[1] |= bad;
+                else again[0] |= bad;
             }
+            __syncwarp();   // (the rows are read back)
+#pragma unroll
+            for (int dk = 0; dk < 2; ++dk)
+                while (again[dk]) {
+                    const int src = __ffs(again[dk]) - 1;
+                    again[dk] &= again[dk] - 1;
+                    const seq::Span sp{__shfl_sync(SGA_FULL_MASK, lo, src), __shfl_sync(SGA_FULL_MASK, hi, src), (int64_t)t.t0 * 128,
+                                       min(a.rows, (int64_t)t.t1 * 128)};
+                    seq::key_row_alone<__nv_bfloat16, D>(a, dk != 0, __shfl_sync(SGA_FULL_MASK, row, src), hk, sp,
+                                                         seq::slice_columns<D>(dk * (D / 32), part, kParts));
+                }
         } else if (lane == 0) {
             atomicOr(a.d_err, tc::kErrMmaTimeout);
         }
@@ -661,6 +669,7 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
         if (ok && !tc::warp_wait(&acc_full, 0, tc::kWaitLimit)) ok = false;
         if (ok) {
             tc::fence_after_sync();
+            uint32_t again = 0;
 #pragma unroll
             for (int k = 0; k < SL; ++k) {
                 const int c0 = (k * kParts + part) * 32;
@@ -672,13 +681,15 @@ template <int D> __device__ __forceinline__ void dq_pass(const BwdParams &prm, u
                     sub[2 * i] = err * __uint_as_float(mean[k][i] << 16);
                     sub[2 * i + 1] = err * __uint_as_float(mean[k][i] & 0xffff0000u);
                 }
-                uint32_t again = store_from_tmem(tQ + c0 + tl, dst, a.scale, in, sub);
-                while (again) {
-                    const int src = __ffs(again) - 1;
-                    again &= again - 1;
-                    seq::query_row_alone<__nv_bfloat16, D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, __shfl_sync(SGA_FULL_MASK, lo, src),
-                                       __shfl_sync(SGA_FULL_MASK, hi, src), c0, 32);
-                }
+                again |= store_from_tmem(tQ + c0 + tl, dst, a.scale, in, sub);
+            }
+            __syncwarp();   // (the rows are read back)
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                const seq::Span sp{__shfl_sync(SGA_FULL_MASK, lo, src), __shfl_sync(SGA_FULL_MASK, hi, src), (int64_t)t.t0 * 128,
+                                   min(a.rows, (int64_t)t.t1 * 128)};
+                seq::query_row_alone<__nv_bfloat16, D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, sp, seq::slice_columns<D>(0, part, kParts));
             }
         } else if (lane == 0) {
             atomicOr(a.d_err, tc::kErrMmaTimeout);

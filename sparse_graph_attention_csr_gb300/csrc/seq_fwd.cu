@@ -20,9 +20,9 @@
 // of the size of the rounding of the output itself.
 //
 // A zero weight times an infinity or NaN is NaN, so a tile that is masked in
-// part could carry one from a value row that the query does not see.  A row
-// whose result is not finite is therefore computed again by its warp over its
-// own interval alone (nothing is spent on this otherwise).
+// part could carry one from a value row that the query does not see.  What is not
+// finite in a row for such a value row is computed again by its warp over its own
+// interval alone (seq_rows.cuh; nothing is spent on this otherwise).
 //
 // Measured: 16384 rows, 8/2 heads of 128, causal 357 us (1.54 PFLOP/s; the
 // library's product of 8192^3 reaches 1.90 in a burst and 1.70 under the power
@@ -307,11 +307,13 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             }
             if (in) a.lse_w[row * a.H + h] = (m + log2f(l)) * kLn2;
             uint32_t again = __ballot_sync(SGA_FULL_MASK, bad && in && l == l);
+            __syncwarp();   // (the rows are read back)
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
-                seq::out_row_alone<__nv_bfloat16, D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, hk, __shfl_sync(SGA_FULL_MASK, lo, src),
-                             __shfl_sync(SGA_FULL_MASK, hi, src));
+                const seq::Span sp{__shfl_sync(SGA_FULL_MASK, lo, src), __shfl_sync(SGA_FULL_MASK, hi, src), (int64_t)t.t0 * 128,
+                                   min(a.rows, (int64_t)t.t1 * 128)};
+                seq::out_row_alone<__nv_bfloat16, D>(a, __shfl_sync(SGA_FULL_MASK, row, src), h, hk, sp);
             }
             tc::fence_before_sync();
         } else if (!ok && lane == 0) {

@@ -21,8 +21,8 @@
 //     K Q^T, dP^T = V dOut^T, dV += P^T dOut, dK += dS^T Q.
 // The scores are computed twice in the backward pass so that every output row
 // is owned by one block: no atomics, bitwise reproducible.
-// A row whose result is not finite is computed again over its own interval alone
-// (seq_rows.cuh).  Leaving masked pairs out of every sum instead, with a test a
+// What is not finite in a row for a row that is masked for it is computed again
+// over its own interval alone (seq_rows.cuh).  Leaving masked pairs out of every sum instead, with a test a
 // pair, took a fifth longer on five sequences of 1 to 512 rows, D = 32.
 #include "seq_rows.cuh"
 #include "tc.cuh"
@@ -193,6 +193,12 @@ __device__ __forceinline__ void in_tile(const int64_t (&lo)[RA], const int64_t (
     }
 }
 
+// What the rows of this half of the warp came from (seq_rows.cuh).
+__device__ __forceinline__ seq::Span span_of(const SeqArgs &a, const SeqTile &t, int64_t lo, int64_t hi, int half) {
+    return seq::Span{__shfl_sync(SGA_FULL_MASK, lo, 16 * half), __shfl_sync(SGA_FULL_MASK, hi, 16 * half), (int64_t)t.t0 * kT,
+                     min(a.rows, (int64_t)t.t1 * kT)};
+}
+
 // Unit u of a pass: TY RA rows (from `row` of a tile) of one head.
 template <int RA, int TY> struct Unit {
     uint32_t tile;
@@ -293,8 +299,7 @@ template <int D, int RA, int TY, int MB> __global__ void __launch_bounds__(16 * 
     for (int i = 0; i < RA; ++i)
         if (l[i] != l[i]) bad &= ~(1u << i);   // NaN whatever the masked rows hold
     each_bad_row<RA, TY>(bad, [&](int i, int half) {
-        seq::out_row_alone<float, D>(a, q0 + (ty & ~1) + half + TY * i, h, hk, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
-                                     __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half));
+        seq::out_row_alone<float, D>(a, q0 + (ty & ~1) + half + TY * i, h, hk, span_of(a, t, lo[i], hi[i], half));
     });
 }
 
@@ -356,8 +361,7 @@ template <int D, int RA, int TY> __device__ __forceinline__ void dq_pass(const S
     for (int i = 0; i < RA; ++i) f[i] = a.scale;
     const uint32_t bad = store_rows<D, RA, TY>(static_cast<float *>(a.dQ), acc, f, q0, a.rows, a.H, h, ty, tx);
     each_bad_row<RA, TY>(bad, [&](int i, int half) {
-        seq::query_row_alone<float, D>(a, q0 + (ty & ~1) + half + TY * i, h, __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
-                                       __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
+        seq::query_row_alone<float, D>(a, q0 + (ty & ~1) + half + TY * i, h, span_of(a, t, lo[i], hi[i], half), ~0u);
     });
 }
 
@@ -443,9 +447,7 @@ template <int D, int RA, int TY> __device__ __forceinline__ void dkdv_pass(const
     const uint32_t bad_k = store_rows<D, RA, TY>(static_cast<float *>(a.dK), dk, f, k0, a.rows, a.Hkv, hk, ty, tx);
     for (int x = 0; x < 2; ++x)
         each_bad_row<RA, TY>(x ? bad_k : bad_v, [&](int i, int half) {
-            seq::key_row_alone<float, D>(a, x == 1, k0 + (ty & ~1) + half + TY * i, hk,
-                                         __shfl_sync(SGA_FULL_MASK, lo[i], 16 * half),
-                                         __shfl_sync(SGA_FULL_MASK, hi[i], 16 * half), 0, D);
+            seq::key_row_alone<float, D>(a, x == 1, k0 + (ty & ~1) + half + TY * i, hk, span_of(a, t, lo[i], hi[i], half), ~0u);
         });
 }
 
