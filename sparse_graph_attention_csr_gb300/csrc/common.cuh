@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "../../include/sga.h"
+#include "device_state.h"
 
 #define SGA_FULL_MASK 0xffffffffu
 
@@ -175,18 +176,6 @@ constexpr int kErrIndexRange = 1;   // a gathered node id was outside [0, N)
 
 // ---- host-side launch bookkeeping (defined in api.cu) -----------------------
 namespace sga {
-// SMs of the current device (looked up once per device).
-inline int device_sms() {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<int> known[kMaxDevices];
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < kMaxDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
-    if (dev >= 0 && dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 void note_launch(sga_kernel_id which, cudaStream_t s, bool after);
 
 // A kernel launched by launch_early may start while the stream's previous kernel
@@ -220,20 +209,5 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
     cfg.numAttrs = 1;
     (void)cudaLaunchKernelEx(&cfg, kernel, args...);
     return cudaGetLastError();   // as after <<<>>>: read and cleared
-}
-
-// Let Kernel launch with `smem` bytes of dynamic shared memory: raises the
-// kernel's limit whenever a launch needs more than any before it (kernels whose
-// size depends on the call's shape would otherwise keep the first call's limit
-// and refuse a larger launch).
-template <auto Kernel> cudaError_t allow_smem(size_t smem) {
-    static std::atomic<size_t> allowed{48 * 1024};
-    if (smem <= allowed.load(std::memory_order_relaxed)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    size_t cur = allowed.load(std::memory_order_relaxed);
-    while (smem > cur && !allowed.compare_exchange_weak(cur, smem, std::memory_order_relaxed)) {
-    }
-    return cudaSuccess;
 }
 }

@@ -508,16 +508,15 @@ cudaError_t launch_bwd(const NormArgs &a, int &blocks, cudaStream_t s) {
     if (cudaError_t e = allow_smem<norm_bwd_kernel<TX, TW, EL, TPR, NV, TH>>(smem); e != cudaSuccess) return e;
     // as many blocks as are resident at once: a few more would run alone (4099 x
     // 301 fp32: 8.4 us with three an SM, 12.6 with four, of which three fit)
-    static std::atomic<int> per_sm{0};
-    int fit = per_sm.load(std::memory_order_relaxed);
-    if (fit == 0) {
-        if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &fit, norm_bwd_kernel<TX, TW, EL, TPR, NV, TH>, TH, sizeof(float) * 2 * 4096);
-            e != cudaSuccess)
-            return e;
-        fit = std::max(1, std::min(fit, kNormBlocksPerSm));
-        per_sm.store(fit, std::memory_order_relaxed);
-    }
+    static std::atomic<int> per_sm[kMaxDevices];
+    cudaError_t asked = cudaSuccess;
+    const int fit = per_device(per_sm, [&] {
+        int n = 0;
+        asked = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_bwd_kernel<TX, TW, EL, TPR, NV, TH>, TH,
+                                                              sizeof(float) * 2 * 4096);
+        return asked == cudaSuccess ? std::max(1, std::min(n, kNormBlocksPerSm)) : 0;
+    });
+    if (asked != cudaSuccess) return asked;
     blocks = (int)std::min<int64_t>((a.N + GPB - 1) / GPB, (int64_t)device_sms() * fit);
     note_launch(SGA_KERN_NORM_BWD, s, false);
     const cudaError_t e = launch_early(norm_bwd_kernel<TX, TW, EL, TPR, NV, TH>, dim3((unsigned)blocks), dim3(TH), smem, s, a);
