@@ -1,6 +1,6 @@
 // What the host remembers of a device: its SMs, and the shared memory that each
 // kernel may use there.  Both belong to one device of the process: another one is
-// asked, or told, for itself.
+// asked, or told, for itself.  And how plans give back device memory.
 #pragma once
 
 #include <cuda_runtime_api.h>
@@ -56,6 +56,17 @@ template <auto Kernel> cudaError_t allow_smem(size_t smem) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess && dev >= 0) allowed[dev].store(smem, std::memory_order_relaxed);
     return e;
+}
+
+// Frees a plan's memory.  A plan may be dropped at any time, also while some stream
+// of the process is being captured (a collector may run then), and cudaFree would
+// end that capture unless the thread says that it does not take part in it.
+inline void free_device(void *p) {
+    if (!p) return;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool set = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;   // (the mode before comes back in it)
+    cudaFree(p);
+    if (set) cudaThreadExchangeStreamCaptureMode(&mode);
 }
 
 }  // namespace sga

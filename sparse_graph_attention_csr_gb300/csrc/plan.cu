@@ -510,7 +510,7 @@ sga_status plan_build(sga_plan *p, cudaStream_t s) {
 }
 
 void plan_free(sga_plan *p) {
-    for (void *x : p->owned) cudaFree(x);
+    for (void *x : p->owned) free_device(x);
     p->owned.clear();
 }
 

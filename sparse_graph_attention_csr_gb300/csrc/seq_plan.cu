@@ -94,11 +94,11 @@ std::vector<SeqTile> pair_list(std::vector<SeqTile> all) {
 }
 
 void seq_free(sga_seq_plan *p) {
-    cudaFree(p->d_qpairs);
-    cudaFree(p->d_range);
-    cudaFree(p->d_qtiles);
-    cudaFree(p->d_ktiles);
-    cudaFree(p->d_err);
+    free_device(p->d_qpairs);
+    free_device(p->d_range);
+    free_device(p->d_qtiles);
+    free_device(p->d_ktiles);
+    free_device(p->d_err);
 }
 
 template <typename P> cudaError_t dev_alloc(sga_seq_plan *p, P **out, size_t count) {

@@ -1,4 +1,6 @@
 """Calls of packed-sequence attention at the edges of what its documentation allows."""
+import threading
+
 import pytest
 import torch
 
@@ -30,3 +32,25 @@ def test_largest_scale(dt):
     bound = (2 ** -8 if dt == "bf16" else 0) * K.double().abs().mean(0) + 32 * 2 ** -24 * K.double().abs().mean(0)
     last = (2 ** -8 if dt == "bf16" else 2 ** -24) * (mean.abs() + bound)
     assert ((out.double() - mean).abs() <= bound + last).all()
+
+
+@pytest.mark.parametrize("where", ["here", "another thread"])
+def test_plans_dropped_during_a_capture(where):
+    """Plans that the capture does not use, freed while it runs: it goes on."""
+    ptr = ptr_of([20, 300])
+    plans = [sga.SeqPlan(ptr, 3, 64), sga.SeqPlan(ptr, 2, 32, torch.float32), sga.Plan(ptr_of([1] * 320), ptr_of([1] * 319), 2, 32)]
+    kept, Q = sga.SeqPlan(ptr, 2, 64), torch.randn(320, 2, 64, device="cuda").bfloat16()
+    want = sga.seq_attn_fwd(kept, Q, Q, Q)[0]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        if where == "here":
+            plans.clear()
+        else:
+            t = threading.Thread(target=plans.clear)
+            t.start()
+            t.join()
+        out = sga.seq_attn_fwd(kept, Q, Q, Q)[0]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and kept.device_error() == 0
