@@ -14,8 +14,12 @@
 // reproducible.  Statistics and sums are fp32.
 #include <algorithm>
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "tc.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace sga {
 
@@ -383,59 +387,159 @@ __global__ void __launch_bounds__(kRingThreads, 4) norm_bwd_ring_kernel(const No
     block_sums<EL, TPR, NV, kRingThreads>(a, acc_sm, dw, db);
 }
 
-// Rows too wide for registers: a block per row, x read again (from L2) in each step.
-template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_fwd_wide_kernel(const NormArgs a) {
-    __shared__ float red[1][32];
+// Rows too wide for registers: CL blocks of TH threads a row (more than one: a
+// cluster), x read again (from L2) in each step, EL elements a load and U loads of
+// a thread in flight.  256 threads to 16384 columns, 1024 to 65536, then clusters
+// of eight: a row that is one block's work is read at what one SM can.  1 row of
+// 2^20 fp32: 32 us forward, 39 backward (one block of 256 threads, a load at a
+// time: 896 and 1430).
+template <int CL> struct RowCluster {
+    float (*slots)[2][8];   // [which sum][value][rank], in every block's shared memory
+    __device__ __forceinline__ static int rank() { return CL > 1 ? (int)cg::this_cluster().block_rank() : 0; }
+    // every block of the row runs, so that its shared memory may be written
+    __device__ __forceinline__ static void start() {
+        if constexpr (CL > 1) cg::this_cluster().sync();
+    }
+    // Adds the blocks' sums, in the order of their ranks.  `which` alternates: a slot
+    // is written again only after the barrier of the sum in between, to which a
+    // block comes after it has read the slot.
+    template <int K> __device__ __forceinline__ void add(float (&v)[K], int which) const {
+        if constexpr (CL > 1) {
+            cg::cluster_group row = cg::this_cluster();
+            if (threadIdx.x < CL)
+#pragma unroll
+                for (int k = 0; k < K; ++k) *row.map_shared_rank(&slots[which][k][rank()], threadIdx.x) = v[k];
+            row.sync();
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                v[k] = 0.f;
+#pragma unroll
+                for (int i = 0; i < CL; ++i) v[k] += slots[which][k][i];
+            }
+        }
+    }
+};
+
+template <typename TX, typename TW, int EL, int TH, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(TH) norm_fwd_wide_kernel(const NormArgs a) {
+    constexpr int U = EL == 8 ? 2 : EL == 4 ? 4 : 8, STEP = TH * EL;
+    __shared__ float red[1][32], slots[2][2][8];
     let_next_start();
     wait_previous();
     const TX *X = static_cast<const TX *>(a.X);
     const TW *w = static_cast<const TW *>(a.w), *b = static_cast<const TW *>(a.b);
     const float inv = 1.f / (float)a.C;
-    for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+    const RowCluster<CL> row_blocks{slots};
+    const int share = (a.C / EL + CL - 1) / CL * EL, first = row_blocks.rank() * share, last = min(a.C, first + share);   // the block's columns
+    row_blocks.start();
+    for (int64_t row = blockIdx.x / CL; row < a.N; row += gridDim.x / CL) {
         const TX *x = X + row * a.C;
         TX *y = static_cast<TX *>(a.Y) + row * a.C;
+        auto each = [&](auto f) {   // f(elements, column) over the thread's columns
+            for (int c0 = first + threadIdx.x * EL; c0 < last; c0 += U * STEP) {
+                Raw<TX, EL> r[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * STEP < last) r[u].load(x + c0 + u * STEP);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * STEP < last) f(r[u], c0 + u * STEP);
+            }
+        };
         float s[1] = {0.f};
-        for (int c = threadIdx.x; c < a.C; c += 256) s[0] += to_f32<TX>(x[c]);
-        row_sum<256, 1>(s, red);
+        each([&](const Raw<TX, EL> &r, int) {
+#pragma unroll
+            for (int i = 0; i < EL; ++i) s[0] += r.at(i);
+        });
+        row_sum<TH, 1>(s, red);
+        row_blocks.add(s, 0);
         const float mean = s[0] * inv;
         s[0] = 0.f;
-        for (int c = threadIdx.x; c < a.C; c += 256) {
-            const float d = to_f32<TX>(x[c]) - mean;
-            s[0] = fmaf(d, d, s[0]);
-        }
-        row_sum<256, 1>(s, red);
+        each([&](const Raw<TX, EL> &r, int) {
+#pragma unroll
+            for (int i = 0; i < EL; ++i) {
+                const float d = r.at(i) - mean;
+                s[0] = fmaf(d, d, s[0]);
+            }
+        });
+        row_sum<TH, 1>(s, red);
+        row_blocks.add(s, 1);
         const float rstd = rsqrtf(s[0] * inv + a.eps);
-        for (int c = threadIdx.x; c < a.C; c += 256)
-            y[c] = from_f32<TX>(fmaf((to_f32<TX>(x[c]) - mean) * rstd, w ? to_f32<TW>(w[c]) : 1.f,
-                                     b ? to_f32<TW>(b[c]) : 0.f));
-        if (threadIdx.x == 0) {
+        each([&](const Raw<TX, EL> &r, int c) {
+            Raw<TW, EL> wr, br;
+            br.zero();
+            if (w) wr.load(w + c);
+            if (b) br.load(b + c);
+            float o[EL];
+#pragma unroll
+            for (int i = 0; i < EL; ++i) o[i] = fmaf((r.at(i) - mean) * rstd, w ? wr.at(i) : 1.f, br.at(i));
+            store_el<TX, EL>(y + c, o);
+        });
+        if (threadIdx.x == 0 && first == 0) {
             a.mean[row] = mean;
             a.rstd[row] = rstd;
         }
     }
 }
 
-template <typename TX, typename TW> __global__ void __launch_bounds__(256) norm_bwd_wide_kernel(const NormArgs a) {
-    __shared__ float red[2][32];
+template <typename TX, typename TW, int EL, int TH, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(TH) norm_bwd_wide_kernel(const NormArgs a) {
+    constexpr int U = EL == 8 ? 1 : EL == 4 ? 2 : 4, STEP = TH * EL;
+    __shared__ float red[2][32], slots[2][2][8];
     let_next_start();
     wait_previous();
     const TW *w = static_cast<const TW *>(a.w);
     const float inv = 1.f / (float)a.C;
-    for (int64_t row = blockIdx.x; row < a.N; row += gridDim.x) {
+    const RowCluster<CL> row_blocks{slots};
+    const int share = (a.C / EL + CL - 1) / CL * EL, first = row_blocks.rank() * share, last = min(a.C, first + share);   // the block's columns
+    row_blocks.start();
+    int which = 0;
+    for (int64_t row = blockIdx.x / CL; row < a.N; row += gridDim.x / CL) {
         const TX *x = static_cast<const TX *>(a.X) + row * a.C, *dy = static_cast<const TX *>(a.dY) + row * a.C;
         TX *dx = static_cast<TX *>(a.dX) + row * a.C;
         const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+        auto each = [&](auto f) {   // f(xhat, g, column) over the thread's columns
+            for (int c0 = first + threadIdx.x * EL; c0 < last; c0 += U * STEP) {
+                Raw<TX, EL> xr[U], gr[U];
+                Raw<TW, EL> wr[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * STEP < last) {
+                        xr[u].load(x + c0 + u * STEP);
+                        gr[u].load(dy + c0 + u * STEP);
+                        if (w) wr[u].load(w + c0 + u * STEP);
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * STEP < last) {
+                        float h[EL], g[EL];
+#pragma unroll
+                        for (int i = 0; i < EL; ++i) {
+                            h[i] = (xr[u].at(i) - mean) * rstd;
+                            g[i] = gr[u].at(i) * (w ? wr[u].at(i) : 1.f);
+                        }
+                        f(h, g, c0 + u * STEP);
+                    }
+            }
+        };
         float s[2] = {0.f, 0.f};
-        for (int c = threadIdx.x; c < a.C; c += 256) {
-            const float g = to_f32<TX>(dy[c]) * (w ? to_f32<TW>(w[c]) : 1.f);
-            s[0] += g;
-            s[1] = fmaf(g, (to_f32<TX>(x[c]) - mean) * rstd, s[1]);
-        }
-        row_sum<256, 2>(s, red);
-        for (int c = threadIdx.x; c < a.C; c += 256) {
-            const float g = to_f32<TX>(dy[c]) * (w ? to_f32<TW>(w[c]) : 1.f);
-            dx[c] = from_f32<TX>(rstd * (g - s[0] * inv - (to_f32<TX>(x[c]) - mean) * rstd * (s[1] * inv)));
-        }
+        each([&](const float (&h)[EL], const float (&g)[EL], int) {
+#pragma unroll
+            for (int i = 0; i < EL; ++i) {
+                s[0] += g[i];
+                s[1] = fmaf(g[i], h[i], s[1]);
+            }
+        });
+        row_sum<TH, 2>(s, red);
+        row_blocks.add(s, which);
+        which ^= 1;
+        const float c1 = s[0] * inv, c2 = s[1] * inv;
+        each([&](const float (&h)[EL], const float (&g)[EL], int c) {
+            float o[EL];
+#pragma unroll
+            for (int i = 0; i < EL; ++i) o[i] = rstd * (g[i] - c1 - h[i] * c2);
+            store_el<TX, EL>(dx + c, o);
+        });
     }
 }
 
@@ -482,6 +586,18 @@ template <typename TW> __global__ void __launch_bounds__(1024) norm_reduce_kerne
         if (c < C) dw[c] = from_f32<TW>(s);
         else if (db) db[c - C] = from_f32<TW>(s);
     }
+}
+
+// The same from few blocks: a thread per column.
+template <typename TW> __global__ void __launch_bounds__(256) norm_reduce_few_kernel(const float *__restrict__ part, int blocks,
+                                                                                     int C, TW *dw, TW *db) {
+    wait_previous();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = 2 * (int64_t)C;
+    if (i >= n) return;
+    float s = 0.f;
+    for (int b = 0; b < blocks; ++b) s += part[b * n + i];
+    if (i < C) dw[i] = from_f32<TW>(s);
+    else if (db) db[i - C] = from_f32<TW>(s);
 }
 
 // Blocks of the backward pass, each with a row of sums: four an SM.
@@ -536,6 +652,14 @@ template <typename TX, typename TW, int TPR, int NV> cudaError_t launch_bwd_ring
     return e;
 }
 
+// The wide kernels by width: 256 threads a row, 1024, eight blocks of 1024.
+cudaError_t launch_wide(const NormArgs &a, cudaStream_t s, void (*narrow)(NormArgs), void (*wide)(NormArgs), void (*cluster)(NormArgs)) {
+    const int64_t sms = device_sms();
+    if (a.C <= 16384) return launch_early(narrow, dim3((unsigned)std::min(a.N, sms * 8)), dim3(256), 0, s, a);
+    if (a.C <= 65536) return launch_early(wide, dim3((unsigned)std::min(a.N, sms * 2)), dim3(1024), 0, s, a);
+    return launch_early(cluster, dim3((unsigned)std::min(a.N, sms / 4) * 8), dim3(1024), 0, s, a);
+}
+
 // Threads of a row by its number of 16-byte vectors (or of elements, where the
 // width or an address is no multiple of 16 bytes).  Two vectors a thread where
 // a warp can hold the row: of 1048576 x 256 bf16, 170 us (6.3 TB/s) with two,
@@ -558,9 +682,11 @@ template <typename TX, typename TW> cudaError_t norm_fwd_t(const NormArgs &a, bo
         if (a.C <= 512) return launch_fwd<TX, TW, 1, 32, 16>(a, s);
         if (a.C <= 4096) return launch_fwd<TX, TW, 1, 256, 16>(a, s);
     }
-    const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)device_sms() * 8);
     note_launch(SGA_KERN_NORM_FWD, s, false);
-    const cudaError_t e = launch_early(norm_fwd_wide_kernel<TX, TW>, dim3(grid), dim3(256), 0, s, a);
+    const cudaError_t e = launch_wide(
+        a, s, vec ? norm_fwd_wide_kernel<TX, TW, EL, 256, 1> : norm_fwd_wide_kernel<TX, TW, 1, 256, 1>,
+        vec ? norm_fwd_wide_kernel<TX, TW, EL, 1024, 1> : norm_fwd_wide_kernel<TX, TW, 1, 1024, 1>,
+        vec ? norm_fwd_wide_kernel<TX, TW, EL, 1024, 8> : norm_fwd_wide_kernel<TX, TW, 1, 1024, 8>);
     note_launch(SGA_KERN_NORM_FWD, s, true);
     return e;
 }
@@ -582,9 +708,10 @@ template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bo
     else if (a.C <= 512) e = launch_bwd<TX, TW, 1, 32, 16>(a, blocks, s);
     else if (a.C <= 4096) e = launch_bwd<TX, TW, 1, 256, 16>(a, blocks, s);
     else {
-        const unsigned grid = (unsigned)std::min<int64_t>(a.N, (int64_t)device_sms() * 8);
         note_launch(SGA_KERN_NORM_BWD, s, false);
-        e = launch_early(norm_bwd_wide_kernel<TX, TW>, dim3(grid), dim3(256), 0, s, a);
+        e = launch_wide(a, s, vec ? norm_bwd_wide_kernel<TX, TW, EL, 256, 1> : norm_bwd_wide_kernel<TX, TW, 1, 256, 1>,
+                        vec ? norm_bwd_wide_kernel<TX, TW, EL, 1024, 1> : norm_bwd_wide_kernel<TX, TW, 1, 1024, 1>,
+                        vec ? norm_bwd_wide_kernel<TX, TW, EL, 1024, 8> : norm_bwd_wide_kernel<TX, TW, 1, 1024, 8>);
         note_launch(SGA_KERN_NORM_BWD, s, true);
         if (e != cudaSuccess || !a.part) return e;
         const int64_t want = std::min<int64_t>(bwd_blocks(device_sms()), (a.N + 15) / 16);
@@ -596,8 +723,14 @@ template <typename TX, typename TW> cudaError_t norm_bwd_t(const NormArgs &a, bo
     }
     if (e != cudaSuccess || !a.part) return e;
     note_launch(SGA_KERN_NORM_REDUCE, s, false);
-    e = launch_early(norm_reduce_kernel<TW>, dim3((unsigned)((2 * (int64_t)a.C + 31) / 32)), dim3(1024), 0, s,
-                      static_cast<const float *>(a.part), blocks, a.C, dw, db);
+    const int64_t sums = 2 * (int64_t)a.C;
+    // (wide rows have few blocks of sums and many columns)
+    if (a.C > 4096 && blocks <= 32)
+        e = launch_early(norm_reduce_few_kernel<TW>, dim3((unsigned)((sums + 255) / 256)), dim3(256), 0, s,
+                         static_cast<const float *>(a.part), blocks, a.C, dw, db);
+    else
+        e = launch_early(norm_reduce_kernel<TW>, dim3((unsigned)((sums + 31) / 32)), dim3(1024), 0, s,
+                         static_cast<const float *>(a.part), blocks, a.C, dw, db);
     note_launch(SGA_KERN_NORM_REDUCE, s, true);
     return e;
 }
