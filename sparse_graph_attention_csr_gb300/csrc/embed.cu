@@ -56,7 +56,8 @@ template <typename T, bool VEC> __device__ __forceinline__ void store_g(T *p, co
 // ---- forward ------------------------------------------------------------------
 
 // A warp takes 32 >> sh tokens at a time (1 << sh lanes each); U groups of a
-// lane's row are loaded before any is stored.
+// lane's row are loaded before any is stored.  Where there are few tokens, their
+// columns are spread over gridDim.y blocks (1 of 2^20 bf16: 5.5 us, 297 by one warp).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(const void *__restrict__ ids, bool wide, const T *__restrict__ table,
                                                         int64_t N, int64_t V, int C, float scale, int sh, T *out) {
@@ -68,10 +69,10 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void *__restrict__
     for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> sh; t < N; t += step) {
         const int64_t id = id_at(ids, t, wide);
         const bool ok = id >= 0 && id < V;
-        if (!ok && sub == 0) atomicOr(&g_embed_err, kErrIndexRange);
+        if (!ok && sub == 0 && blockIdx.y == 0) atomicOr(&g_embed_err, kErrIndexRange);
         const T *src = table + (ok ? id : 0) * C;
         T *dst = out + t * C;
-        for (int c0 = sub; c0 < n; c0 += U * lanes) {
+        for (int c0 = sub + (int)blockIdx.y * U * lanes; c0 < n; c0 += U * lanes * (int)gridDim.y) {
             float x[U][EL];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void *__restrict__
 constexpr int kSortThreads = 1024, kSortWarps = 32;
 constexpr int kDigits = 256;
 constexpr int kLongRow = 8;
+constexpr int kJoinCols = 4096;   // columns that a warp joins (wider rows: several warps)
 
 struct GradArgs {
     const void *ids, *dOut;
@@ -406,13 +408,15 @@ template <int W, int M> __device__ __forceinline__ Cols<W> columns_of(const Grad
 }
 
 // sm: kSortWarps * 32 * W floats.
-template <typename T, int W> __device__ __forceinline__ void join_rows(const GradArgs &a, float *sm, int64_t (*who)[3]) {
+template <typename T, int W> __device__ __forceinline__ void join_rows(const GradArgs &a, float *sm, int64_t (*who)[4]) {
     const int32_t *key = a.key[a.passes & 1];
     T *dTable = static_cast<T *>(a.dTable);
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    // a block's chunks are apart: the hot rows, which begin close together, go to different blocks
-    for (int64_t base = 0; base < a.chunks; base += (int64_t)gridDim.x * kSortWarps) {
-        const int64_t c0 = base + (int64_t)wp * gridDim.x + blockIdx.x;
+    const int64_t slabs = (a.C + kJoinCols - 1) / kJoinCols, items = a.chunks * slabs;   // (chunk, columns)
+    // a block's items are apart: the hot rows, which begin close together, go to different blocks
+    for (int64_t base = 0; base < items; base += (int64_t)gridDim.x * kSortWarps) {
+        const int64_t it = base + (int64_t)wp * gridDim.x + blockIdx.x, c0 = it / slabs;   // (past the last chunk: nothing runs on)
+        const int k0 = (int)(it % slabs) * kJoinCols, k1 = min(a.C, k0 + kJoinCols);
         int32_t cur = 0;
         int64_t cl = 0;
         const bool on = runs_on(a, key, c0, cur, cl);
@@ -421,10 +425,11 @@ template <typename T, int W> __device__ __forceinline__ void join_rows(const Gra
             who[wp][0] = lng ? cl : -1;
             who[wp][1] = c0;
             who[wp][2] = cur;
+            who[wp][3] = k0;
         }
         const bool any = __syncthreads_or(lng);
         if (on && !lng)
-            for (int col = lane * W; col < a.C; col += 32 * W) {
+            for (int col = k0 + lane * W; col < k1; col += 32 * W) {
                 Cols<W> s;
                 s.load(a.part + (c0 * 2 + 1) * a.C + col);
                 s.add(columns_of<W, kLongRow / 2>(a, c0 + 1, cl + 1, col));
@@ -438,11 +443,12 @@ template <typename T, int W> __device__ __forceinline__ void join_rows(const Gra
             const int64_t l = who[w][0];
             if (l < 0) continue;   // (the same for the whole block)
             const int64_t f = who[w][1], id = who[w][2], per = (l - f + shares - 1) / shares;
-            for (int cb = 0; cb < a.C; cb += 32 * W * cols) {
+            const int last = min(a.C, (int)who[w][3] + kJoinCols);
+            for (int cb = (int)who[w][3]; cb < last; cb += 32 * W * cols) {
                 const int col = cb + (slab * 32 + lane) * W;
                 Cols<W> s;
                 s.zero();
-                if (col < a.C && share < shares) {
+                if (col < last && share < shares) {
                     s = columns_of<W, 8>(a, min(l + 1, f + 1 + share * per), min(l + 1, f + 1 + (share + 1) * per), col);
                     if (share == 0) {
                         Cols<W> v;
@@ -453,7 +459,7 @@ template <typename T, int W> __device__ __forceinline__ void join_rows(const Gra
 #pragma unroll
                 for (int i = 0; i < W; ++i) sm[(wp * 32 + lane) * W + i] = s.x[i];
                 __syncthreads();
-                if (share == 0 && col < a.C) {
+                if (share == 0 && col < last) {
                     for (int q = 1; q < shares; ++q)
 #pragma unroll
                         for (int i = 0; i < W; ++i) s.x[i] += sm[((q * cols + slab) * 32 + lane) * W + i];
@@ -469,7 +475,7 @@ template <typename T, int W> __device__ __forceinline__ void join_rows(const Gra
 template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_kernel(const GradArgs a) {
     __shared__ int32_t cnt[kSortWarps][kDigits];
     __shared__ int32_t scan[kSortWarps + 2 * kDigits];
-    __shared__ int64_t who[kSortWarps][3];
+    __shared__ int64_t who[kSortWarps][4];
     const int64_t t0 = (int64_t)blockIdx.x * kSortThreads + threadIdx.x, nt = (int64_t)gridDim.x * kSortThreads;
     if constexpr (VEC) {
         for (int64_t i = t0; i < a.V * a.C / Elt<T>::EL; i += nt)
@@ -488,7 +494,10 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
 // Few rows (atom or edge types) and few tokens: no sort.  A block takes
 // consecutive tokens; each of its warps owns every 32nd row, finds the rows'
 // tokens by votes over the block's ids and adds them in order, so that nothing is
-// shared.  Then a warp adds the blocks' sums.  STAGED: the block's part of dOut,
+// shared.  Of 16 rows and fewer, 32 / R warps share the rows that are alike modulo R
+// and take a part of the columns each; blocks that are fewer than the SMs share
+// their columns with gridDim.y others (1000 x 4096 bf16 into 1 row: 18.5 us, 197 by
+// one warp a block).  Then the blocks' sums are added.  STAGED: the block's part of dOut,
 // which is contiguous, is copied to shared memory while the ids are listed, so
 // that a warp with a frequent row does not wait for memory batch after batch.
 // 30011 tokens x 100 into 119 rows, id i with a weight of 1 / i: fp32 14.4 us a
@@ -496,7 +505,8 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
 constexpr int kFewRows = 256, kFewTokens = 512;   // rows; tokens of a block
 constexpr size_t kStage = 220 * 1024;             // shared memory beside the lists
 
-template <typename T, bool VEC, bool STAGED>
+// SHARED: 16 rows and fewer.
+template <typename T, bool VEC, bool STAGED, bool SHARED>
 __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const GradArgs a, int64_t per) {
     constexpr int EL = kEl<T, VEC>, M = VEC ? 8 : 4, U = VEC ? 1 : 4;   // M tokens in flight, of U groups each
     __shared__ int32_t id[kFewTokens];
@@ -507,6 +517,14 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
     let_next_start();
     wait_previous();
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, V = (int)a.V, n = a.C / EL;
+    // the warp's rows (own, own + R, ..) and columns (groups [n0, n1), every parts-th 32 U of them)
+    const int rsh = !SHARED ? 5 : V > 1 ? 32 - __clz(V - 1) : 0, R = 1 << rsh, own = wp & (R - 1), part_of = wp >> rsh, parts = kSortWarps >> rsh;
+    int n0 = 0, n1 = n;
+    if constexpr (!STAGED) {
+        const int rounds = (n + 32 * U - 1) / (32 * U), share = (rounds + (int)gridDim.y - 1) / (int)gridDim.y * 32 * U;
+        n0 = (int)blockIdx.y * share;
+        n1 = min(n, n0 + share);
+    }
     const int64_t t0 = min(a.N, blockIdx.x * per);
     const int cnt = (int)min(per, a.N - t0);
     const T *dOut = static_cast<const T *>(a.dOut) + t0 * a.C;
@@ -520,41 +538,41 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
     }
     for (int i = threadIdx.x; i < kFewTokens; i += kSortThreads) id[i] = i < cnt ? key_of(a, t0 + i) : V;
     __syncthreads();
-    float *part = a.part + ((int64_t)blockIdx.x * V + wp) * a.C;   // the warp's first row; the next is 32 rows on
+    float *part = a.part + ((int64_t)blockIdx.x * V + own) * a.C;   // the warp's first row; the next is R rows on
     const uint32_t below = (1u << lane) - 1u;
-    auto mine = [&](int b) { return (id[b + lane] & 31) == wp && id[b + lane] < V; };
+    auto mine = [&](int b) { return (id[b + lane] & (R - 1)) == own && id[b + lane] < V; };
     int total = 0;
     for (int b = 0; b < cnt; b += 32) total += __popc(__ballot_sync(SGA_FULL_MASK, mine(b)));
     if (lane == 0) count[wp] = total;
     __syncthreads();
-    const int base = __reduce_add_sync(SGA_FULL_MASK, lane < wp ? count[lane] : 0);
+    const int base = __reduce_add_sync(SGA_FULL_MASK, lane < own ? count[lane] : 0);
     uint16_t *f = found + base, *list = sorted + base;
-    for (int b = 0, at = 0; b < cnt; b += 32) {
-        const bool on = mine(b);
-        const uint32_t who = __ballot_sync(SGA_FULL_MASK, on);
-        if (on) f[at + __popc(who & below)] = (uint16_t)((b + lane) | (id[b + lane] >> 5) << 9);
-        at += __popc(who);
-    }
-    __syncwarp();
-    for (int q = 0, at = 0; wp + 32 * q < V; ++q) {
-        const int before = at;
-        for (int b = 0; b < total; b += 32) {
-            const int e = b + lane < total ? f[b + lane] : -1;
-            const uint32_t who = __ballot_sync(SGA_FULL_MASK, e >> 9 == q);
-            if (e >> 9 == q) list[at + __popc(who & below)] = (uint16_t)e;
+    if (part_of == 0) {   // (the parts read what the first one lists)
+        for (int b = 0, at = 0; b < cnt; b += 32) {
+            const bool on = mine(b);
+            const uint32_t who = __ballot_sync(SGA_FULL_MASK, on);
+            if (on) f[at + __popc(who & below)] = (uint16_t)((b + lane) | (id[b + lane] >> rsh) << 9);
             at += __popc(who);
         }
-        if (at == before)   // a row without a token here
-            for (int c = lane; c < a.C; c += 32) part[(int64_t)32 * q * a.C + c] = 0.f;
+        __syncwarp();
+        for (int q = 0, at = 0; own + R * q < V; ++q) {
+            const int before = at;
+            for (int b = 0; b < total; b += 32) {
+                const int e = b + lane < total ? f[b + lane] : -1;
+                const uint32_t who = __ballot_sync(SGA_FULL_MASK, e >> 9 == q);
+                if (e >> 9 == q) list[at + __popc(who & below)] = (uint16_t)e;
+                at += __popc(who);
+            }
+            if (at == before)   // a row without a token here
+                for (int c = n0 * EL + lane; c < n1 * EL; c += 32) part[(int64_t)R * q * a.C + c] = 0.f;
+        }
     }
     if constexpr (STAGED) {
         tc::cp_wait<0>();
-        __syncthreads();
         dOut = reinterpret_cast<const T *>(stage);
-    } else {
-        __syncwarp();
     }
-    for (int g0 = lane; g0 - lane < n; g0 += 32 * U) {
+    __syncthreads();
+    for (int g0 = n0 + part_of * 32 * U + lane; g0 - lane < n1; g0 += 32 * U * parts) {
         float acc[U][EL];
         int cur = -1;
         auto flush = [&] {
@@ -562,7 +580,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < EL; ++i) {
-                    if (cur >= 0 && g0 + 32 * u < n) part[(int64_t)32 * cur * a.C + (g0 + 32 * u) * EL + i] = acc[u][i];
+                    if (cur >= 0 && g0 + 32 * u < n1) part[(int64_t)R * cur * a.C + (g0 + 32 * u) * EL + i] = acc[u][i];
                     acc[u][i] = 0.f;
                 }
         };
@@ -577,7 +595,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_grad_few_kernel(const G
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     raw[z][u] = make_uint4(0, 0, 0, 0);
-                    if (e < 0 || g0 + 32 * u >= n) continue;
+                    if (e < 0 || g0 + 32 * u >= n1) continue;
                     const T *p = dOut + (int64_t)(e & 511) * a.C + (int64_t)(g0 + 32 * u) * EL;
                     if constexpr (VEC) raw[z][u] = STAGED ? *reinterpret_cast<const uint4 *>(p) : ldg16_stream(p);
                     else raw[z][u].x = __float_as_uint(to_f32<T>(STAGED ? *p : __ldg(p)));
@@ -628,6 +646,27 @@ template <typename T, int W> __global__ void __launch_bounds__(256) embed_add_fe
 #pragma unroll
     for (int i = 0; i < W; ++i) s.x[i] = group_sum<32>(s.x[i]);
     if (lane == 0) s.store(static_cast<T *>(a.dTable) + it * W, a.scale);
+}
+
+// The same of few blocks: a thread per W columns, whatever their number.
+template <typename T, int W> __global__ void __launch_bounds__(256) embed_add_fewer_kernel(const GradArgs a, int B) {
+    let_next_start();
+    wait_previous();
+    const int64_t stride = a.V * a.C, it = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (it >= stride / W) return;
+    Cols<W> s;
+    s.zero();
+    for (int b0 = 0; b0 < B; b0 += 4) {
+        Cols<W> x[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            x[z].zero();
+            if (b0 + z < B) x[z].load(a.part + (b0 + z) * stride + it * W);
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z) s.add(x[z]);
+    }
+    s.store(static_cast<T *>(a.dTable) + it * W, a.scale);
 }
 
 // Blocks of the gradient's launch: one an SM, fewer where that leaves them under
@@ -694,18 +733,30 @@ template <typename T, bool VEC> cudaError_t grad_t(GradArgs a, int blocks, cudaS
         const int64_t per = a.few;
         const size_t bytes = (size_t)per * a.C * sizeof(T);
         cudaError_t le;
+        constexpr int kShared = 16;
         if (bytes <= kStage && aligned(a.dOut, 16)) {
-            if (cudaError_t e = allow_smem<embed_grad_few_kernel<T, VEC, true>>(kStage); e != cudaSuccess) return e;
-            le = launch_early(embed_grad_few_kernel<T, VEC, true>, dim3((unsigned)blocks), dim3(kSortThreads), bytes, s, a, per);
+            auto launch = [&]<bool SHARED>() {
+                if (cudaError_t e = allow_smem<embed_grad_few_kernel<T, VEC, true, SHARED>>(kStage); e != cudaSuccess) return e;
+                return launch_early(embed_grad_few_kernel<T, VEC, true, SHARED>, dim3((unsigned)blocks), dim3(kSortThreads), bytes, s, a, per);
+            };
+            le = a.V <= kShared ? launch.template operator()<true>() : launch.template operator()<false>();
         } else {
-            le = launch_early(embed_grad_few_kernel<T, VEC, false>, dim3((unsigned)blocks), dim3(kSortThreads), 0, s, a, per);
+            const int64_t rounds = (n + (VEC ? 31 : 127)) / (VEC ? 32 : 128);
+            const dim3 grid((unsigned)blocks, (unsigned)std::max<int64_t>(1, std::min<int64_t>(rounds, device_sms() / blocks)));
+            le = launch_early(a.V <= kShared ? embed_grad_few_kernel<T, VEC, false, true> : embed_grad_few_kernel<T, VEC, false, false>, grid,
+                              dim3(kSortThreads), 0, s, a, per);
         }
         note_launch(SGA_KERN_EMBED_BWD, s, true);
         if (le != cudaSuccess) return le;
-        const int64_t warps = a.V * a.C / (a.C % 4 == 0 ? 4 : 1);
+        const int64_t items = a.V * a.C / (a.C % 4 == 0 ? 4 : 1);
         note_launch(SGA_KERN_EMBED_ADD, s, false);
-        const cudaError_t e = launch_early(a.C % 4 == 0 ? embed_add_few_kernel<T, 4> : embed_add_few_kernel<T, 1>,
-                                            dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, a, blocks);
+        cudaError_t e;
+        if (blocks <= 16)
+            e = launch_early(a.C % 4 == 0 ? embed_add_fewer_kernel<T, 4> : embed_add_fewer_kernel<T, 1>,
+                             dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s, a, blocks);
+        else
+            e = launch_early(a.C % 4 == 0 ? embed_add_few_kernel<T, 4> : embed_add_few_kernel<T, 1>, dim3((unsigned)((items + 7) / 8)),
+                             dim3(256), 0, s, a, blocks);
         note_launch(SGA_KERN_EMBED_ADD, s, true);
         return e;
     }
@@ -733,8 +784,10 @@ cudaError_t fwd_t(const void *ids, bool wide, const void *table, int64_t N, int6
     while (sh < 5 && (4 << sh) < n) ++sh;   // four groups a lane
     const int64_t blocks = ((N << sh) + 255) / 256;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)device_sms() * 32);
+    const int64_t rounds = (n + (4 << sh) - 1) / (4 << sh);   // of a lane over its row
+    const unsigned slabs = (unsigned)std::max<int64_t>(1, std::min<int64_t>(rounds, device_sms() * 4 / (int64_t)grid));
     note_launch(SGA_KERN_EMBED_FWD, s, false);
-    const cudaError_t e = launch_early(embed_fwd_kernel<T, VEC>, dim3(grid), dim3(256), 0, s, ids, wide,
+    const cudaError_t e = launch_early(embed_fwd_kernel<T, VEC>, dim3(grid, slabs), dim3(256), 0, s, ids, wide,
                                        static_cast<const T *>(table), N, V, C, scale, sh, static_cast<T *>(out));
     note_launch(SGA_KERN_EMBED_FWD, s, true);
     return e;
