@@ -321,8 +321,10 @@ sga_status sga_permute_rows(const void *src, int64_t N, int64_t row_bytes, const
 typedef struct sga_seq_plan sga_seq_plan;
 
 /* seq_ptr: [B+1] int32, device; seq_ptr[0] = 0, non-decreasing (SGA_EINVAL
- * otherwise).  Read during this call only, which synchronises `stream` and
- * allocates the plan's device memory on the current device. */
+ * otherwise).  Read during this call only, which synchronises `stream` (so that
+ * it may not be captured) and allocates the plan's device memory on the current
+ * device: about 0.15 ms, and 0.07 ms to destroy it, which waits for the device.
+ * A plan may be destroyed while other work is captured. */
 sga_status sga_seq_plan_create(const int32_t *seq_ptr, int64_t B, int H, int Hkv, int D, sga_dtype dt, int causal,
                                void *stream, sga_seq_plan **out);
 void sga_seq_plan_destroy(sga_seq_plan *plan);
@@ -372,8 +374,8 @@ sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, 
  * reads as a row of zeros, adds to no gradient and sets a bit in the device's
  * error word.  The backward writes all of dTable [V, C] = scale times the sum
  * of dOut over each row's tokens (zero for a row without one, and for
- * padding_idx >= 0), summed by tokens sorted by id in a fixed order: bitwise
- * reproducible.  Its workspace is 256-byte aligned. */
+ * padding_idx >= 0), summed in fp32 in an order that the sizes and ids fix:
+ * bitwise reproducible.  Its workspace is 256-byte aligned. */
 sga_status embed_fwd(const void *ids, int id_bytes, const void *table, int64_t N, int64_t V, int64_t C, float scale,
                      sga_dtype dt, void *out, void *stream);
 size_t sga_embed_bwd_workspace_bytes(int64_t N, int64_t V, int64_t C);

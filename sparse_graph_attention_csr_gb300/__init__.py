@@ -675,7 +675,9 @@ class SeqPlan:
     ``H`` query heads of ``D`` elements (32, 64 or 128) share ``kv_heads`` key
     and value heads (default H); ``causal``: row i sees rows j <= i of its
     sequence, otherwise all of them.  Calls on one plan may overlap (other
-    streams, captured graphs); the plan must outlive them.
+    streams, captured graphs); the plan must outlive them.  Making a plan
+    synchronises the stream (about 0.15 ms, dropping it 0.07): make one a batch,
+    not one a layer, and outside a capture.
     """
 
     def __init__(self, seq_ptr: torch.Tensor, H: int, D: int, dtype=torch.bfloat16,

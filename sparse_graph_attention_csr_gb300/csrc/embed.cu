@@ -1,4 +1,5 @@
-// Embedding lookup with scaling, and its gradient by sorted tokens.
+// Embedding lookup with scaling, and its gradient by sorted tokens, or without a
+// sort into few rows.
 //   forward:  out_t = scale table[id_t]
 //   backward: dTable_v = scale sum over the tokens t with id_t = v of dOut_t
 //
@@ -491,17 +492,20 @@ template <typename T, bool VEC> __global__ void __launch_bounds__(kSortThreads, 
     else join_rows<T, 1>(a, reinterpret_cast<float *>(cnt), who);
 }
 
-// Few rows (atom or edge types) and few tokens: no sort.  A block takes
-// consecutive tokens; each of its warps owns every 32nd row, finds the rows'
-// tokens by votes over the block's ids and adds them in order, so that nothing is
-// shared.  Of 16 rows and fewer, 32 / R warps share the rows that are alike modulo R
-// and take a part of the columns each; blocks that are fewer than the SMs share
-// their columns with gridDim.y others (1000 x 4096 bf16 into 1 row: 18.5 us, 197 by
-// one warp a block).  Then the blocks' sums are added.  STAGED: the block's part of dOut,
-// which is contiguous, is copied to shared memory while the ids are listed, so
-// that a warp with a frequent row does not wait for memory batch after batch.
-// 30011 tokens x 100 into 119 rows, id i with a weight of 1 / i: fp32 14.4 us a
-// call (2.5 more from memory, 28 sorted), bf16 13.6 (8.5 more from memory).
+// Few rows (atom or edge types) and few tokens: no sort.  A block takes consecutive
+// tokens; each of its warps owns every 32nd row, finds the rows' tokens by votes
+// over the block's ids and adds them in order, so that nothing is shared.  Of 16
+// rows and fewer, 32 / R warps share the rows that are alike modulo R and take a
+// part of the columns each; blocks that are fewer than the SMs share their columns
+// with gridDim.y others (1000 x 4096 bf16 into 1 row: 18.5 us, 197 by one warp a
+// block).  Then the blocks' sums are added.  STAGED: the block's part of dOut, which
+// is contiguous, is copied to shared memory while the ids are listed, so that a warp
+// with a frequent row does not wait for memory batch after batch. 30011 tokens x 100
+// into 119 rows, id i with a weight of 1 / i: fp32 14.4 us a call (2.5 more from
+// memory, 28 sorted), bf16 13.6 (8.5 more from memory).  At the ends of its range it
+// is still the faster one: 70000 x 100 into 256 rows 21 us (257 rows, sorted: fp32
+// 42, bf16 46), 76000 x 100 into 119 rows fp32 25, bf16 20 (80000, sorted: 36, 40);
+// past them a block's lists would have to be walked again.
 constexpr int kFewRows = 256, kFewTokens = 512;   // rows; tokens of a block
 constexpr size_t kStage = 220 * 1024;             // shared memory beside the lists
 

@@ -28,9 +28,9 @@
 //
 // As in the forward, what is not finite in a row for a row that is masked for it
 // is computed again over its own interval alone.
-// Measured: 8192 rows, 8/4 heads of 128, causal 302 us, full 561 us: 1.22
-// PFLOP/s of the five products that a backward pass needs, 1.71 of the seven
-// computed, the rate of the library's product under the power limit (1.70).
+// Measured: 8192 rows, 8/4 heads of 128, causal 310 us, full 580 us: 1.18
+// PFLOP/s of the five products that a backward pass needs, 1.66 of the seven
+// computed (the library's product under the power limit: 1.70).
 // What is left to gain is the two repeated products, against an fp32 dQ in
 // memory that several CTAs add to.
 //
@@ -407,20 +407,20 @@ template <int D> __device__ __forceinline__ void dkdv_pass(const BwdParams &prm,
 
 // ---- dQ ----------------------------------------------------------------------------
 //
-// A row's dS sum to zero, so an offset that all keys share leaves no trace in
-// dQ = sum_j dS_j k_j; but of dS rounded to bf16, dS_j + e_j, it leaves offset x
-// sum_j e_j, which grows with the offset while dQ does not.  The weight warps
-// know every e_j, so in a column with an offset dQ is formed as sum_j (dS_j +
-// e_j) k_j - (sum_j e_j) c, c being the mean of four of the row's own keys: an error
-// of sum_j e_j (k_j - c), in which the offset is gone.  Nothing is assumed of dS
-// itself.  (A second product, of the e_j, would be the eighth of the two
-// passes; what is left of dQ's error is then the forward's, whose rounded out
-// enters Delta.)  512 keys of 64 +- 1, bf16, D = 64, queries of 1 / 64: dQ's
-// error against the formula with that out is 0.0025 of its norm, and was 0.104
-// with single roundings.  It costs 2% at 8192 rows, 8/4 heads of 128 (causal 303
-// -> 310 us), 5% at 8 heads of 64 (235 -> 251) and 1.7 us on 128 graphs of 9 to 38
-// rows, 4 heads of 64 (16.6 -> 18.3).  In dK = sum_i dS_i q_i the terms of a key's queries do not cancel:
-// its roundings are of the size of dK's own.
+// A row's dS sum to zero, so an offset that all keys share leaves no trace in dQ =
+// sum_j dS_j k_j; but of dS rounded to bf16, dS_j + e_j, it leaves offset x sum_j
+// e_j, which grows with the offset while dQ does not.  The weight warps know every
+// e_j, so in a column with an offset dQ is formed as sum_j (dS_j + e_j) k_j - (sum_j
+// e_j) c, c being the mean of four of the row's own keys: an error of sum_j e_j (k_j
+// - c), in which the offset is gone.  Nothing is assumed of dS itself.  (A second
+// product, of the e_j, would be the eighth of the two passes; what is left of dQ's
+// error is then the forward's, whose rounded out enters Delta.)  512 keys of 64 +-
+// 1, bf16, D = 64, queries of 1 / 64: dQ's error against the formula with that out
+// is 0.0025 of its norm, and was 0.104 with single roundings.  It costs 2% at 8192
+// rows, 8/4 heads of 128 (causal 303 -> 310 us), 5% at 8 heads of 64 (235 -> 251)
+// and 1.7 us on 128 graphs of 9 to 38 rows, 4 heads of 64 (16.6 -> 18.3).  In dK =
+// sum_i dS_i q_i the terms of a key's queries do not cancel: its roundings are of
+// the size of dK's own.
 
 // c at the columns [c0, c0 + 32) as bf16 pairs, zero in a column where the four
 // are farther apart than |c| / 2 (no offset to speak of).  c lies between them:

@@ -2,8 +2,10 @@
 // the backward pass for both dtypes.
 //
 // The tensor cores have no fp32 product, and the tolerance of the fp32 layers
-// (1e-5) rules out tf32, so these kernels are bound by the FMA pipes (two
-// products of the forward, three and four of the backward's two passes).
+// (1e-5) rules out a single tf32 one; operands split into two or three tf32 parts,
+// with three products or more for one, have not been tried.  So these kernels are
+// bound by the FMA pipes (two products of the forward, three and four of the
+// backward's two passes).
 // Blocks of TY x 16 threads take TY RA rows of one side (a 64-row tile or a part
 // of one) and walk the 64-row tiles of the other through shared memory, the next
 // tiles copied while one is in use; each thread holds an RA x 4 piece of the
@@ -52,7 +54,7 @@ __device__ __forceinline__ void load_tile(float *dst, const void *src, int64_t r
     }
 }
 
-// s[a][c] = row (ty + 16 a) of A . row (tx + 16 c) of B
+// s[a][c] = row (ty + TY a) of A . row (tx + 16 c) of B
 template <int D, int RA, int TY>
 __device__ __forceinline__ void dot_tiles(float (&s)[RA][4], const float *A, const float *B, int ty, int tx) {
     float2 acc[RA][4];
@@ -105,7 +107,7 @@ template <int D> __device__ __forceinline__ void load_cols(float (&v)[kCols<D>],
     }
 }
 
-// acc[a][x] += sum_j P[ty + 16 a][j] B[j][col x] over the 64 rows of B
+// acc[a][x] += sum_j P[ty + TY a][j] B[j][col x] over the 64 rows of B
 template <int D, int RA, int TY>
 __device__ __forceinline__ void add_product(float (&acc)[RA][kCols<D>], const float *P, const float *B, int ty, int tx) {
     constexpr int NC = kCols<D>;
