@@ -367,6 +367,47 @@ sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, 
                           int64_t N, int64_t C, sga_dtype dt, sga_dtype wdt, void *dX, void *dweight, void *dbias,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- norm and rotary positions of query and key heads -------------------------
+ *
+ * Every head x [D] of Q [T, H, D] and K [T, Hkv, D] is normed, y = x r w with
+ * r = 1 / sqrt(sum x^2 / D + eps) and w = wq or wk [D] (in wdt: float32, or
+ * dt; NULL for ones), and its first `rot` elements are turned in pairs by the
+ * row's positions: pair i by the angle pos[t, axis_i] f_i, from the first
+ * element of the pair towards the second.  A pair is elements (i, i + rot / 2),
+ * or with interleaved = 1 (2 i, 2 i + 1).  pos [T, axes], int32 or int64
+ * (pos_bytes 4 or 8), of either sign; angles are exact to 2^-54 turns a position
+ * and rounded to float32 once.  rq [T, H], rk [T, Hkv] (float32) are r, kept for
+ * the backward pass; with both NULL nothing is normed and the weights are NULL.
+ * D in {32, 64, 128}, (H + Hkv) D <= 32768.  A row's heads lie one behind the
+ * other, rows ldq and ldk elements apart (multiples of 16 bytes: slices of one
+ * projection's result); Qo, Ko, dQo, dKo, dQ, dK are dense.  Qo may be Q where
+ * that is dense, Ko likewise, and dQ may be dQo, dK dKo.  Tensors are 16-byte
+ * aligned, weights by their element. */
+#define SGA_MAX_AXES 4
+typedef struct {
+    int32_t D, rot, axes, interleaved;
+    uint64_t turn[64];   /* of each pair: turns a position, in units of 2^-64 */
+    uint8_t axis[64];    /* and the column of pos that it takes */
+} sga_rotary;
+
+/* freqs [rot / 2]: radians a position.  sections [axes]: how many pairs, in
+ * order, take each column of pos (their sum is rot / 2); NULL with axes = 1.
+ * rot: a multiple of 16, at most D; 0 turns nothing.  1 <= axes <= SGA_MAX_AXES.
+ * Host memory only. */
+sga_status sga_rotary_init(sga_rotary *out, int D, int rot, const double *freqs, const int32_t *sections, int axes,
+                           int interleaved);
+sga_status qk_norm_rope_fwd(const sga_rotary *rot, const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *pos,
+                            int pos_bytes, const void *wq, const void *wk, int64_t T, int H, int Hkv, float eps,
+                            sga_dtype dt, sga_dtype wdt, void *Qo, void *Ko, float *rq, float *rk, void *stream);
+/* Workspace of the backward pass (16-byte aligned), needed for dwq and dwk only:
+ * both are given, in wdt, or both NULL.  Sums are taken in a fixed order:
+ * bitwise reproducible. */
+size_t sga_qk_norm_rope_bwd_workspace_bytes(int64_t T, int D);
+sga_status qk_norm_rope_bwd(const sga_rotary *rot, const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *pos,
+                            int pos_bytes, const void *wq, const void *wk, const float *rq, const float *rk, const void *dQo,
+                            const void *dKo, int64_t T, int H, int Hkv, sga_dtype dt, sga_dtype wdt, void *dQ, void *dK,
+                            void *dwq, void *dwk, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- embedding --------------------------------------------------------------
  *
  * out[t] = scale table[ids[t]] for ids [N] (int32 or int64: id_bytes 4 or 8)
@@ -510,7 +551,8 @@ typedef enum {
     SGA_KERN_SEQ_FWD = 26, SGA_KERN_SEQ_BWD_ROWS = 27, SGA_KERN_SEQ_BWD = 28,
     SGA_KERN_NORM_FWD = 29, SGA_KERN_NORM_BWD = 30, SGA_KERN_NORM_REDUCE = 31,
     SGA_KERN_EMBED_FWD = 32, SGA_KERN_EMBED_BWD = 33, SGA_KERN_EMBED_ADD = 34,
-    SGA_KERN_COUNT = 35
+    SGA_KERN_QK_ROPE_FWD = 35, SGA_KERN_QK_ROPE_BWD = 36, SGA_KERN_QK_ROPE_REDUCE = 37,
+    SGA_KERN_COUNT = 38
 } sga_kernel_id;
 /* (Planned GATv2 passes merge their split rows inside the edge kernels --
  * the last chunk of a row to finish merges it -- so SGA_KERN_GATV2_FWD_MERGE

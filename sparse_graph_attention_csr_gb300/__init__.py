@@ -37,7 +37,7 @@ KERNELS = {
     "bsr_bwd_dkdv": 18, "agg_fwd": 19, "agg_fwd_merge": 20, "agg_bwd": 21, "agg_bwd_merge": 22,
     "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25, "seq_fwd": 26, "seq_bwd_rows": 27,
     "seq_bwd": 28, "norm_fwd": 29, "norm_bwd": 30, "norm_reduce": 31, "embed_fwd": 32,
-    "embed_bwd": 33, "embed_add": 34,
+    "embed_bwd": 33, "embed_add": 34, "qk_rope_fwd": 35, "qk_rope_bwd": 36, "qk_rope_reduce": 37,
 }
 
 SGA_LAYER_ATTENTION, SGA_LAYER_MINMAX, SGA_LAYER_GAT = 0, 1, 2
@@ -134,6 +134,12 @@ _SIGNATURES = {
     "sga_norm_bwd_workspace_bytes": ([_i64, _i64], ctypes.c_size_t),
     "layer_norm_bwd": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp,
                         ctypes.c_size_t, _vp], _int),
+    "sga_rotary_init": ([_vp, _int, _int, _vp, _vp, _int, _int], _int),
+    "qk_norm_rope_fwd": ([_vp, _vp, _i64, _vp, _i64, _vp, _int, _vp, _vp, _i64, _int, _int, _f32, _int,
+                          _int, _vp, _vp, _vp, _vp, _vp], _int),
+    "sga_qk_norm_rope_bwd_workspace_bytes": ([_i64, _int], ctypes.c_size_t),
+    "qk_norm_rope_bwd": ([_vp, _vp, _i64, _vp, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int,
+                          _int, _int, _int, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _int),
     "embed_fwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _int, _vp, _vp], _int),
     "sga_embed_bwd_workspace_bytes": ([_i64, _i64, _i64], ctypes.c_size_t),
     "embed_bwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _i64, _int, _vp, _vp, ctypes.c_size_t,
@@ -760,6 +766,63 @@ def layer_norm_bwd(X, weight, mean, rstd, dOut, bias: bool = True, dX=None, dwei
     return _ext().layer_norm_bwd(X, weight, mean, rstd, dOut, bias, dX, dweight, dbias, stream)
 
 
+# ------------------------- norm and rotary positions of query and key heads
+
+class Rotary:
+    """The frequencies of rotary positions: pair i of a head's first ``dims``
+    elements (default all ``D``; a multiple of 16) turns by pos * freqs[i].
+
+    ``freqs``: dims / 2 numbers, radians a position; default
+    base ** (-2 i / dims).  ``sections``: with positions of several axes
+    [T, axes] (time, height and width, say), how many pairs, in order, take each
+    axis; their sum is dims / 2.  A pair is elements (i, i + dims / 2), or with
+    ``interleaved`` (2 i, 2 i + 1).  Host memory only: make one a model.
+    """
+
+    def __init__(self, D: int, dims: int | None = None, base: float = 10000.0, sections=None,
+                 interleaved: bool = False, freqs=None):
+        self.D, self.dims = int(D), int(D) if dims is None else int(dims)
+        if self.D not in (32, 64, 128):
+            raise ValueError(f"D must be 32, 64 or 128, got {self.D}")
+        if self.dims < 0 or self.dims > self.D or self.dims % 16:
+            raise ValueError(f"dims must be a multiple of 16 from 0 to {self.D}, got {self.dims}")
+        if freqs is None:
+            if not 0.0 < base < float("inf"):
+                raise ValueError(f"base must be positive and finite, got {base}")
+            freqs = [float(base) ** (-2.0 * i / self.dims) for i in range(self.dims // 2)]
+        self.freqs = [float(f) for f in freqs]
+        if len(self.freqs) != self.dims // 2 or not all(abs(f) < float("inf") for f in self.freqs):
+            raise ValueError(f"freqs must be {self.dims // 2} finite numbers")
+        self.sections = None if sections is None else [int(n) for n in sections]
+        if self.sections is not None and (not 1 <= len(self.sections) <= 4 or min(self.sections) < 0
+                                          or sum(self.sections) != self.dims // 2):
+            raise ValueError(f"sections must be one to four counts that add up to dims / 2 = {self.dims // 2}, "
+                             f"got {self.sections}")
+        self.axes = 1 if self.sections is None else len(self.sections)
+        self.interleaved = bool(interleaved)
+        self._c = _ext().Rotary(self.D, self.dims, self.freqs, self.sections or [], self.interleaved)
+
+
+def qk_norm_rope_fwd(rot: Rotary, Q, K, pos, wq=None, wk=None, eps: float | None = 1e-6, out_q=None,
+                     out_k=None, rq=None, rk=None, stream=None):
+    """Norm of every head of Q [T, H, D] and K [T, kv_heads, D] and its rotary
+    position: (Q', K', rq [T, H], rk [T, kv_heads]) with r = 1 / sqrt(mean
+    square + eps) float32.  wq, wk: [D], float32 or Q's dtype, or None; ``eps``
+    None: no norm, rotation alone (rq and rk are None).  pos: [T] or [T, axes],
+    int32 or int64.  Q and K may be slices of one projection's result (rows any
+    multiple of 16 bytes apart); ``out_q`` may be Q itself, ``out_k`` K, where
+    they are contiguous."""
+    return _ext().qk_norm_rope_fwd(rot._c, Q, K, pos, wq, wk, eps, out_q, out_k, rq, rk, stream)
+
+
+def qk_norm_rope_bwd(rot: Rotary, Q, K, pos, wq, wk, rq, rk, dQo, dKo, dQ=None, dK=None, dwq=None,
+                     dwk=None, stream=None):
+    """(dQ, dK, dwq, dwk) from the forward's rq and rk (None: rotation alone);
+    dwq and dwk in the weights' dtype, None without them.  ``dQ`` may be dQo
+    itself, ``dK`` dKo."""
+    return _ext().qk_norm_rope_bwd(rot._c, Q, K, pos, wq, wk, rq, rk, dQo, dKo, dQ, dK, dwq, dwk, stream)
+
+
 # ------------------------------------------------------------------- embedding
 
 def embed_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
@@ -959,3 +1022,36 @@ class Embedding(torch.autograd.Function):
         (ids,) = ctx.saved_tensors
         dTable = embed_bwd(ids, dOut.contiguous(), ctx.rows, ctx.scale, ctx.padding_idx)
         return None, dTable, None, None
+
+
+def _rows16(t):
+    """t [T, heads, D], or a copy of it where its heads are not dense within a row
+    or its rows not on 16-byte boundaries."""
+    if t.dim() != 3 or t.is_contiguous():
+        return t
+    ok = t.stride(2) == 1 and t.stride(1) == t.shape[2] and t.stride(0) >= t.shape[1] * t.shape[2] \
+        and t.stride(0) * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+class QKNormRope(torch.autograd.Function):
+    """Norm and rotary positions of query and key heads as an autograd function:
+    ``q, k = QKNormRope.apply(Q, K, pos, wq, wk, rot, eps)``; wq and wk [D] in
+    float32 or Q's dtype, or both None; ``eps`` None: rotation alone."""
+
+    @staticmethod
+    def forward(ctx, Q, K, pos, wq=None, wk=None, rot=None, eps=1e-6):
+        Q, K, pos = _rows16(Q), _rows16(K), pos.contiguous()
+        wq = None if wq is None else wq.contiguous()
+        wk = None if wk is None else wk.contiguous()
+        q, k, rq, rk = qk_norm_rope_fwd(rot, Q, K, pos, wq, wk, eps)
+        ctx.rot = rot
+        ctx.save_for_backward(Q, K, pos, wq, wk, rq, rk)
+        return q, k
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dQo, dKo):
+        Q, K, pos, wq, wk, rq, rk = ctx.saved_tensors
+        dQ, dK, dwq, dwk = qk_norm_rope_bwd(ctx.rot, Q, K, pos, wq, wk, rq, rk, dQo.contiguous(), dKo.contiguous())
+        return dQ, dK, None, dwq, dwk, None, None

@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <pybind11/stl.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <cmath>
@@ -17,6 +18,7 @@
 #include <optional>
 #include <sstream>
 #include <string>
+#include <vector>
 
 #include "../../include/sga.h"
 
@@ -319,6 +321,148 @@ py::tuple layer_norm_bwd_(const Tensor &X, const Maybe &weight, const Tensor &me
     return py::make_tuple(std::move(x), w ? py::cast(*w) : py::none(), b ? py::cast(*b) : py::none());
 }
 
+// ---- norm and rotary positions of query and key heads ---------------------------------------
+
+sga_rotary rotary_(int D, int rot, const std::vector<double> &freqs, const std::vector<int32_t> &sections, bool interleaved) {
+    sga_rotary r;
+    if ((int64_t)freqs.size() * 2 != rot)
+        throw py::value_error("freqs must hold dims / 2 = " + std::to_string(rot / 2) + " numbers, got " + std::to_string(freqs.size()));
+    check(sga_rotary_init(&r, D, rot, freqs.data(), sections.empty() ? nullptr : sections.data(),
+                          sections.empty() ? 1 : (int)sections.size(), interleaved ? 1 : 0),
+          "sga_rotary_init");
+    return r;
+}
+
+// Q or K: [T, heads, D], dense within a row; the elements from a row to the next.
+int64_t rope_rows(const sga_rotary &r, const Tensor &t, const char *name, at::Device device, at::ScalarType dtype, int64_t T) {
+    need_cuda(t, name);
+    if (t.device() != device)
+        throw py::value_error(std::string(name) + " is on " + t.device().str() + ", expected " + device.str());
+    if (t.scalar_type() != dtype)
+        throw py::type_error(std::string(name) + " must be " + text(dtype) + ", got " + text(t.scalar_type()));
+    if (t.dim() != 3 || t.size(0) != T || t.size(1) < 1 || t.size(2) != r.D)
+        throw py::value_error(std::string(name) + " must be [T, heads, " + std::to_string(r.D) + "] with T = " + std::to_string(T) +
+                              ", got " + text(t.sizes()));
+    const int64_t row = t.size(1) * r.D, el = 16 / (int64_t)t.element_size();
+    if (T == 0) return row;
+    if (t.stride(2) != 1 || (t.size(1) > 1 && t.stride(1) != r.D) || (T > 1 && (t.stride(0) < row || t.stride(0) % el)) ||
+        reinterpret_cast<uintptr_t>(t.data_ptr()) % 16)
+        throw py::value_error(std::string(name) + "'s heads must be dense within a row, and its rows begin on 16-byte boundaries");
+    return T > 1 ? t.stride(0) : row;
+}
+
+struct Rope {
+    int64_t T, H, Hkv, ldq, ldk;
+    sga_dtype dt, wdt;
+    at::ScalarType type, wtype;
+    int pos_bytes;
+    at::Device device;
+};
+
+Rope rope_inputs(const sga_rotary &r, const Tensor &Q, const Tensor &K, const Tensor &pos, const Maybe &wq, const Maybe &wk, bool norm) {
+    need_cuda(Q, "Q");
+    Rope x{0, 0, 0, 0, 0, code(Q), code(Q), Q.scalar_type(), Q.scalar_type(), 0, Q.device()};
+    x.T = Q.dim() == 3 ? Q.size(0) : 0;
+    x.ldq = rope_rows(r, Q, "Q", x.device, x.type, x.T);
+    x.ldk = rope_rows(r, K, "K", x.device, x.type, x.T);
+    x.H = Q.size(1);
+    x.Hkv = K.size(1);
+    need_cuda(pos, "pos");
+    if (pos.scalar_type() != at::kInt && pos.scalar_type() != at::kLong)
+        throw py::type_error(std::string("pos must be torch.int32 or torch.int64, got ") + text(pos.scalar_type()));
+    if (r.axes == 1 && pos.dim() == 1) need(pos, "pos", x.device, pos.scalar_type(), {x.T});
+    else need(pos, "pos", x.device, pos.scalar_type(), {x.T, r.axes});
+    x.pos_bytes = (int)pos.element_size();
+    if (wq.has_value() != wk.has_value()) throw py::value_error("give both weights, or none");
+    if (wq) {
+        if (!norm) throw py::value_error("weights need a norm (eps is None)");
+        const at::ScalarType w = wq->scalar_type();
+        if (w != at::kFloat && w != x.type)
+            throw py::type_error(std::string("weights must be ") + text(x.type) + " or torch.float32, got " + text(w));
+        need(*wq, "wq", x.device, w, {r.D});
+        need(*wk, "wk", x.device, w, {r.D});
+        x.wtype = w;
+        x.wdt = w == at::kFloat ? SGA_F32 : SGA_BF16;
+    }
+    return x;
+}
+
+py::tuple qk_norm_rope_fwd_(const sga_rotary &r, const Tensor &Q, const Tensor &K, const Tensor &pos, const Maybe &wq, const Maybe &wk,
+                            std::optional<double> eps, const Maybe &out_q, const Maybe &out_k, const Maybe &rq, const Maybe &rk,
+                            const py::object &stream) {
+    const Rope x = rope_inputs(r, Q, K, pos, wq, wk, eps.has_value());
+    const float feps = eps ? (float)*eps : 0.f;   // (a double may overflow, or round to zero)
+    if (eps && (!(*eps >= 0.0) || !std::isfinite(feps) || (feps == 0.f && *eps != 0.0))) {
+        std::ostringstream got;
+        got << *eps;
+        throw py::value_error("eps must be zero or a positive and finite float32, or None, got " + got.str());
+    }
+    if (!eps && (rq || rk)) throw py::value_error("rq and rk need a norm (eps is None)");
+    const Place on(x.device, stream);
+    Tensor q = out_q ? *out_q : fresh({x.T, x.H, r.D}, x.type, x.device), k = out_k ? *out_k : fresh({x.T, x.Hkv, r.D}, x.type, x.device);
+    Maybe sq = rq, sk = rk;
+    if (eps && !sq) sq = fresh({x.T, x.H}, at::kFloat, x.device);
+    if (eps && !sk) sk = fresh({x.T, x.Hkv}, at::kFloat, x.device);
+    if (out_q || out_k || rq || rk) {
+        need(q, "out_q", x.device, x.type, {x.T, x.H, r.D});
+        need(k, "out_k", x.device, x.type, {x.T, x.Hkv, r.D});
+        if (sq) need(*sq, "rq", x.device, at::kFloat, {x.T, x.H});
+        if (sk) need(*sk, "rk", x.device, at::kFloat, {x.T, x.Hkv});
+        // in place: a head is read before it is written
+        const Maybe qi = ptr(q) == ptr(Q) && Q.is_contiguous() ? Maybe() : Maybe(Q), ki = ptr(k) == ptr(K) && K.is_contiguous() ? Maybe() : Maybe(K);
+        distinct({named("out_q", q), named("out_k", k), named("rq", sq), named("rk", sk)},
+                 {named("Q", qi), named("K", ki), named("pos", pos), named("wq", wq), named("wk", wk)});
+    }
+    check(qk_norm_rope_fwd(&r, ptr(Q), x.ldq, ptr(K), x.ldk, ptr(pos), x.pos_bytes, ptr(wq), ptr(wk), x.T, (int)x.H, (int)x.Hkv, feps,
+                           x.dt, x.wdt, ptr(q), ptr(k), static_cast<float *>(ptr(sq)), static_cast<float *>(ptr(sk)), on.raw()),
+          "qk_norm_rope_fwd");
+    on.used({named("Q", Q), named("K", K), named("pos", pos), named("wq", wq), named("wk", wk)},
+            {named("out_q", q), named("out_k", k), named("rq", sq), named("rk", sk)});
+    return py::make_tuple(std::move(q), std::move(k), sq ? py::cast(*sq) : py::none(), sk ? py::cast(*sk) : py::none());
+}
+
+py::tuple qk_norm_rope_bwd_(const sga_rotary &r, const Tensor &Q, const Tensor &K, const Tensor &pos, const Maybe &wq, const Maybe &wk,
+                            const Maybe &rq, const Maybe &rk, const Tensor &dQo, const Tensor &dKo, const Maybe &dQ, const Maybe &dK,
+                            const Maybe &dwq, const Maybe &dwk, const py::object &stream) {
+    if (rq.has_value() != rk.has_value()) throw py::value_error("give both rq and rk, or none (rotation alone)");
+    const Rope x = rope_inputs(r, Q, K, pos, wq, wk, rq.has_value());
+    if (rq) {
+        need(*rq, "rq", x.device, at::kFloat, {x.T, x.H});
+        need(*rk, "rk", x.device, at::kFloat, {x.T, x.Hkv});
+    }
+    need(dQo, "dQo", x.device, x.type, {x.T, x.H, r.D});
+    need(dKo, "dKo", x.device, x.type, {x.T, x.Hkv, r.D});
+    if (!wq && (dwq || dwk)) throw py::value_error("dwq and dwk need weights");
+    const Place on(x.device, stream);
+    Tensor q = dQ ? *dQ : fresh({x.T, x.H, r.D}, x.type, x.device), k = dK ? *dK : fresh({x.T, x.Hkv, r.D}, x.type, x.device), ws;
+    Maybe gq = dwq, gk = dwk;
+    size_t bytes = 0;
+    if (wq) {
+        if (!gq) gq = fresh({r.D}, x.wtype, x.device);
+        if (!gk) gk = fresh({r.D}, x.wtype, x.device);
+        bytes = sga_qk_norm_rope_bwd_workspace_bytes(x.T, r.D);
+        ws = fresh({(int64_t)bytes}, at::kByte, x.device);
+    }
+    if (dQ || dK || dwq || dwk) {
+        need(q, "dQ", x.device, x.type, {x.T, x.H, r.D});
+        need(k, "dK", x.device, x.type, {x.T, x.Hkv, r.D});
+        if (gq) need(*gq, "dwq", x.device, x.wtype, {r.D});
+        if (gk) need(*gk, "dwk", x.device, x.wtype, {r.D});
+        const Maybe qi = ptr(q) == ptr(dQo) ? Maybe() : Maybe(dQo), ki = ptr(k) == ptr(dKo) ? Maybe() : Maybe(dKo);
+        distinct({named("dQ", q), named("dK", k), named("dwq", gq), named("dwk", gk)},
+                 {named("Q", Q), named("K", K), named("pos", pos), named("wq", wq), named("wk", wk), named("rq", rq), named("rk", rk),
+                  named("dQo", qi), named("dKo", ki)});
+    }
+    check(qk_norm_rope_bwd(&r, ptr(Q), x.ldq, ptr(K), x.ldk, ptr(pos), x.pos_bytes, ptr(wq), ptr(wk), static_cast<const float *>(ptr(rq)),
+                           static_cast<const float *>(ptr(rk)), ptr(dQo), ptr(dKo), x.T, (int)x.H, (int)x.Hkv, x.dt, x.wdt, ptr(q), ptr(k),
+                           ptr(gq), ptr(gk), wq ? ptr(ws) : nullptr, bytes, on.raw()),
+          "qk_norm_rope_bwd");
+    on.used({named("Q", Q), named("K", K), named("pos", pos), named("wq", wq), named("wk", wk), named("rq", rq), named("rk", rk),
+             named("dQo", dQo), named("dKo", dKo)},
+            {named("dQ", q), named("dK", k), named("dwq", gq), named("dwk", gk)});
+    return py::make_tuple(std::move(q), std::move(k), gq ? py::cast(*gq) : py::none(), gk ? py::cast(*gk) : py::none());
+}
+
 // ---- embedding -------------------------------------------------------------------------
 
 int id_bytes(const Tensor &ids) {
@@ -399,6 +543,9 @@ PYBIND11_MODULE(_dense, m) {
     m.def("seq_attn_bwd", &seq_attn_bwd_);
     m.def("layer_norm_fwd", &layer_norm_fwd_);
     m.def("layer_norm_bwd", &layer_norm_bwd_);
+    py::class_<sga_rotary>(m, "Rotary").def(py::init(&rotary_));
+    m.def("qk_norm_rope_fwd", &qk_norm_rope_fwd_);
+    m.def("qk_norm_rope_bwd", &qk_norm_rope_bwd_);
     m.def("embed_fwd", &embed_fwd_);
     m.def("embed_bwd", &embed_bwd_);
 }

@@ -1,0 +1,148 @@
+"""64-bit references of the transformer-layer operators (norm and rotary positions of heads, windowed attention, the
+gated feed-forward product), each with an elementwise bound on the error of a kernel that computes in fp32 and rounds
+where the dtype says.
+
+Units of rounding: U = 2^-24 for an fp32 operation, `last` for the result's own rounding (2^-8 in bf16).  A sum of n
+terms in any order is off by at most (n + 4) U times the sum of their magnitudes."""
+import math
+
+import torch
+
+from dense_ref import ROUND, U, within  # noqa: F401
+
+LOW = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8}
+
+
+def angles(rot, pos):
+    """[T, 1, pairs] angles in 64 bits, and the bound on the kernel's: its stored frequency (two roundings in 64 bits, 2^-64
+    turns), half turns in fp32 (U pi) and sincospi (2 ulp of at most 1)."""
+    f = torch.tensor(rot.freqs, dtype=torch.float64, device=pos.device)
+    which = torch.tensor([a for a, n in enumerate(rot.sections or [rot.dims // 2]) for _ in range(n)], device=pos.device, dtype=torch.long)
+    p = pos.double().reshape(pos.shape[0], -1)[:, which]
+    ang = (p * f)[:, None]
+    return ang, (p.abs() * (f.abs() * 2.0 ** -51 + 2.0 ** -61))[:, None] + (math.pi + 4) * U
+
+
+def turned(rot, x, xb, pos, back=False):
+    """x [T, h, D] turned, and its bound from x's."""
+    ang, ab = angles(rot, pos)
+    c, s = torch.cos(ang), torch.sin(-ang if back else ang)
+    R, h = rot.dims, rot.dims // 2
+    a, b = (slice(0, R, 2), slice(1, R, 2)) if rot.interleaved else (slice(0, h), slice(h, R))
+    y, yb = x.clone(), xb.clone()
+    u, v = x[..., a], x[..., b]
+    mag = u.abs() + v.abs()
+    err = (ab + 3 * U) * (mag + xb[..., a] + xb[..., b])
+    y[..., a], y[..., b] = u * c - v * s, u * s + v * c
+    yb[..., a] = c.abs() * xb[..., a] + s.abs() * xb[..., b] + err
+    yb[..., b] = s.abs() * xb[..., a] + c.abs() * xb[..., b] + err
+    return y, yb
+
+
+def rope_reference(rot, x, pos, w, eps):
+    """{out, r: (value, bound)} of one side (queries or keys)."""
+    D, last = x.shape[-1], ROUND[x.dtype]
+    v = x.double()
+    if eps is None:
+        y, yb = v, torch.zeros_like(v)
+        r = None
+    else:
+        ww = torch.ones(D, dtype=torch.float64, device=x.device) if w is None else w.double()
+        r = ((v * v).mean(-1) + eps) ** -0.5
+        rel = (D / 2 + 6) * U
+        y = v * r[..., None] * ww
+        yb = (rel + 3 * U) * y.abs()
+    out, ob = turned(rot, y, yb, pos)
+    ob = ob + last * (out.abs() + ob) + 1e-30
+    return {"out": (out, ob), "r": None if r is None else (r, rel * r + 1e-30)}
+
+
+def rope_bwd_reference(rot, x, pos, w, r, dout):
+    """{dx, dw: (value, bound)} of one side, at the given r."""
+    D, last = x.shape[-1], ROUND[x.dtype]
+    d = dout.double()
+    dn, dnb = turned(rot, d, torch.zeros_like(d), pos, back=True)
+    if r is None:
+        return {"dx": (dn, dnb + last * (dn.abs() + dnb) + 1e-30), "dw": None}
+    rr = r.double()[..., None]
+    xh = x.double() * rr
+    ww = torch.ones(D, dtype=torch.float64, device=x.device) if w is None else w.double()
+    g = dn * ww
+    gb = dnb * ww.abs() + 2 * U * g.abs()
+    s = (g * xh).mean(-1, keepdim=True)
+    sb = (gb * xh.abs()).mean(-1, keepdim=True) + (D + 8) * U * (g * xh).abs().mean(-1, keepdim=True)
+    dx = rr * (g - xh * s)
+    dxb = rr * (gb + xh.abs() * sb + 5 * U * (g.abs() + (xh * s).abs()))
+    dxb = dxb + last * (dx.abs() + dxb) + 1e-30
+    res = {"dx": (dx, dxb), "dw": None}
+    if w is not None:
+        n = x.shape[0] * x.shape[1]
+        dw = (dn * xh).sum((0, 1))
+        dwb = (dnb * xh.abs()).sum((0, 1)) + (n + 8) * U * (dn * xh).abs().sum((0, 1))
+        res["dw"] = (dw, dwb + ROUND[w.dtype] * (dw.abs() + dwb) + 1e-30)
+    return res
+
+
+def visible(n, causal, window, sinks, device="cuda"):
+    """[n, n]: row i sees key j."""
+    i = torch.arange(n, device=device)
+    apart = i[:, None] - i[None]
+    vis = (apart.abs() < (window or n)) | (i[None] < sinks)
+    return vis & (apart >= 0) if causal else vis
+
+
+def window_reference(seq_ptr, Q, K, V, scale, causal, window, sinks, dOut=None, out_used=None):
+    """{name: (value, bound)} of out, lse and, with dOut, dQ, dK, dV: each sequence and head by itself.  The gradients'
+    bound takes the forward's rounded out (out_used), from which the kernels form Delta."""
+    dt, R = Q.dtype, LOW[Q.dtype]
+    last = ROUND[dt]
+    T, H, D = Q.shape
+    g = H // K.shape[1]
+    q, k, v = (t.double() for t in (Q, K, V))
+    z = torch.zeros_like
+    out, out_b, lse, lse_b = z(q), z(q), z(q[..., 0]), z(q[..., 0])
+    res = {"out": (out, out_b), "lse": (lse, lse_b)}
+    if dOut is not None:
+        do, ou = dOut.double(), out_used.double()
+        dQ, dQb, dK, dKb, dV, dVb = z(q), z(q), z(k), z(k), z(v), z(v)
+        res |= {"dQ": (dQ, dQb), "dK": (dK, dKb), "dV": (dV, dVb)}
+    ptr = [int(x) for x in seq_ptr]
+    for b, e in zip(ptr[:-1], ptr[1:]):
+        n = e - b
+        if n == 0:
+            continue
+        vis = visible(n, causal, window, sinks, Q.device)
+        for h in range(H):
+            qi, ki, vi = q[b:e, h], k[b:e, h // g], v[b:e, h // g]
+            s = torch.where(vis, scale * (qi @ ki.T), -torch.inf)
+            ls = torch.logsumexp(s, 1)
+            p = torch.exp(s - ls[:, None])
+            ds = (D + 4) * U * scale * (qi.abs() @ ki.abs().T) + 8 * U * (1 + ls.abs()[:, None])
+            ds = torch.where(vis, ds, 0.0)
+            top = ds.amax(1)
+            o = p @ vi
+            out[b:e, h], lse[b:e, h] = o, ls
+            lse_b[b:e, h] = top + (n + 8) * U * (1 + ls.abs())
+            rel = R + 2 * top + 2 * (n + 8) * U
+            out_b[b:e, h] = rel[:, None] * (p @ vi.abs()) + last * o.abs() + 1e-30
+            if dOut is None:
+                continue
+            doi, oi = do[b:e, h], ou[b:e, h]
+            dp = doi @ vi.T
+            delta = (doi * o).sum(1)
+            d_delta = (doi.abs() * (oi - o).abs()).sum(1) + (D + 4) * U * (doi.abs() * oi.abs()).sum(1)
+            pe = p * (ds + lse_b[b:e, h][:, None] + 8 * U * (1 + ls.abs()[:, None]))
+            dsv = p * (dp - delta[:, None])
+            dse = (R + 4 * U) * dsv.abs() + pe * (dp - delta[:, None]).abs() + \
+                p * ((D + 4) * U * (doi.abs() @ vi.abs().T) + d_delta[:, None])
+            sums = (n * g + 8) * U
+            dQ[b:e, h] = scale * (dsv @ ki)
+            dQb[b:e, h] = scale * (dse @ ki.abs() + sums * (dsv.abs() @ ki.abs()))
+            dK[b:e, h // g] += scale * (dsv.T @ qi)
+            dKb[b:e, h // g] += scale * (dse.T @ qi.abs() + sums * (dsv.abs().T @ qi.abs()))
+            dV[b:e, h // g] += p.T @ doi
+            dVb[b:e, h // g] += (R * p + pe + sums * p).T @ doi.abs()
+    if dOut is not None:
+        for x, xb in ((dQ, dQb), (dK, dKb), (dV, dVb)):
+            xb += last * (x.abs() + xb) + 1e-30
+    return res
