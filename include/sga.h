@@ -327,6 +327,13 @@ typedef struct sga_seq_plan sga_seq_plan;
  * A plan may be destroyed while other work is captured. */
 sga_status sga_seq_plan_create(const int32_t *seq_ptr, int64_t B, int H, int Hkv, int D, sga_dtype dt, int causal,
                                void *stream, sga_seq_plan **out);
+
+/* The same with a sliding window: of the keys above, row i sees those with
+ * |i - j| < window, and the first `sinks` rows of its sequence (under causal those
+ * of them with j <= i).  window = 0: no window (sinks = 0 then).  1 <= window, 0 <=
+ * sinks otherwise; what a row does not see still does not reach it. */
+sga_status sga_seq_plan_create_windowed(const int32_t *seq_ptr, int64_t B, int H, int Hkv, int D, sga_dtype dt, int causal,
+                                        int64_t window, int64_t sinks, void *stream, sga_seq_plan **out);
 void sga_seq_plan_destroy(sga_seq_plan *plan);
 
 /* seq_ptr[B]: the rows that sequences cover. */
@@ -552,7 +559,8 @@ typedef enum {
     SGA_KERN_NORM_FWD = 29, SGA_KERN_NORM_BWD = 30, SGA_KERN_NORM_REDUCE = 31,
     SGA_KERN_EMBED_FWD = 32, SGA_KERN_EMBED_BWD = 33, SGA_KERN_EMBED_ADD = 34,
     SGA_KERN_QK_ROPE_FWD = 35, SGA_KERN_QK_ROPE_BWD = 36, SGA_KERN_QK_ROPE_REDUCE = 37,
-    SGA_KERN_COUNT = 38
+    SGA_KERN_SEQ_JOIN = 38,
+    SGA_KERN_COUNT = 39
 } sga_kernel_id;
 /* (Planned GATv2 passes merge their split rows inside the edge kernels --
  * the last chunk of a row to finish merges it -- so SGA_KERN_GATV2_FWD_MERGE

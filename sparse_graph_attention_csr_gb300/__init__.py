@@ -38,6 +38,7 @@ KERNELS = {
     "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25, "seq_fwd": 26, "seq_bwd_rows": 27,
     "seq_bwd": 28, "norm_fwd": 29, "norm_bwd": 30, "norm_reduce": 31, "embed_fwd": 32,
     "embed_bwd": 33, "embed_add": 34, "qk_rope_fwd": 35, "qk_rope_bwd": 36, "qk_rope_reduce": 37,
+    "seq_join": 38,
 }
 
 SGA_LAYER_ATTENTION, SGA_LAYER_MINMAX, SGA_LAYER_GAT = 0, 1, 2
@@ -123,6 +124,8 @@ _SIGNATURES = {
     "sga_relabel_csr": ([_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp], _int),
     "sga_permute_rows": ([_vp, _i64, _i64, _vp, _int, _vp, _vp], _int),
     "sga_seq_plan_create": ([_vp, _i64, _int, _int, _int, _int, _int, _vp, ctypes.POINTER(_vp)], _int),
+    "sga_seq_plan_create_windowed": ([_vp, _i64, _int, _int, _int, _int, _int, _i64, _i64, _vp,
+                                      ctypes.POINTER(_vp)], _int),
     "sga_seq_plan_destroy": ([_vp], None),
     "sga_seq_plan_rows": ([_vp], _i64),
     "sga_seq_bwd_workspace_bytes": ([_vp], ctypes.c_size_t),
@@ -680,16 +683,23 @@ class SeqPlan:
 
     ``H`` query heads of ``D`` elements (32, 64 or 128) share ``kv_heads`` key
     and value heads (default H); ``causal``: row i sees rows j <= i of its
-    sequence, otherwise all of them.  Calls on one plan may overlap (other
+    sequence, otherwise all of them.  With a ``window`` it sees of these the rows
+    with |i - j| < window, and the sequence's first ``sinks`` rows (under causal
+    those of them with j <= i).  Calls on one plan may overlap (other
     streams, captured graphs); the plan must outlive them.  Making a plan
     synchronises the stream (about 0.15 ms, dropping it 0.07): make one a batch,
     not one a layer, and outside a capture.
     """
 
     def __init__(self, seq_ptr: torch.Tensor, H: int, D: int, dtype=torch.bfloat16,
-                 kv_heads: int | None = None, causal: bool = True, stream=None):
+                 kv_heads: int | None = None, causal: bool = True, stream=None,
+                 window: int | None = None, sinks: int = 0):
         if dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"the layers compute in torch.float32 or torch.bfloat16, not {dtype}")
+        if window is not None and not 1 <= int(window) < 2 ** 63:
+            raise ValueError(f"window must be at least 1, or None, got {window}")
+        if not 0 <= int(sinks) < 2 ** 63 or (sinks and window is None):
+            raise ValueError(f"sinks must not be negative, and need a window, got {sinks}")
         _need(seq_ptr, "seq_ptr", torch.int32)
         if seq_ptr.dim() != 1 or seq_ptr.numel() < 1:
             raise ValueError("seq_ptr must be 1-D with B + 1 entries")
@@ -697,14 +707,15 @@ class SeqPlan:
         self.H, self.D = int(H), int(D)
         self.kv_heads = self.H if kv_heads is None else int(kv_heads)
         self.causal, self.dtype, self.device = bool(causal), dtype, seq_ptr.device
+        self.window, self.sinks = None if window is None else int(window), int(sinks)
         self._h = None
         handle = ctypes.c_void_p()
         ctx, raw = _place(self.device, stream)
         with ctx:
-            _check(_lib().sga_seq_plan_create(
+            _check(_lib().sga_seq_plan_create_windowed(
                 _ptr(seq_ptr), self.B, self.H, self.kv_heads, self.D,
-                SGA_F32 if dtype == torch.float32 else SGA_BF16, 1 if causal else 0, raw,
-                ctypes.byref(handle)), "sga_seq_plan_create")
+                SGA_F32 if dtype == torch.float32 else SGA_BF16, 1 if causal else 0, self.window or 0,
+                self.sinks, raw, ctypes.byref(handle)), "sga_seq_plan_create")
         self._h = handle
         self.rows = int(_lib().sga_seq_plan_rows(handle))
         self._c = _ext().SeqPlan(handle.value, self.device.index, dtype == torch.float32, self.rows,

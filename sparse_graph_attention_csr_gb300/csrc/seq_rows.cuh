@@ -24,11 +24,77 @@ namespace seq {
 
 constexpr int kStep = 8;
 
-// What a row's result came from: the interval [lo, hi) that it sees, within the
-// rows [w0, w1) of the tiles that were walked for it.
-struct Span {
-    int64_t lo, hi, w0, w1;
+// What a row sees, or what sees it: the interval [lo, hi), and before it the
+// sinks [slo, shi) of a windowed plan's query where they do not touch it.
+template <bool WIN> struct View {
+    int64_t lo = 0, hi = 0;
 };
+template <> struct View<true> {
+    int64_t lo = 0, hi = 0, slo = 0, shi = 0;
+};
+template <bool WIN> __device__ __forceinline__ View<WIN> query_view(const SeqArgs &a, int64_t row) {
+    View<WIN> v;
+    const int2 se = __ldg(a.range + row);
+    v.lo = se.x;
+    v.hi = a.causal ? row + 1 : se.y;
+    if constexpr (WIN) {
+        const int64_t lo = max((int64_t)se.x, row - a.window + 1), hi = min(v.hi, row + a.window), s = min((int64_t)se.x + a.sinks, v.hi);
+        if (s >= lo) {
+            v.hi = max(hi, s);
+        } else {
+            v.lo = lo;
+            v.hi = hi;
+            v.slo = se.x;
+            v.shi = s;
+        }
+    }
+    return v;
+}
+template <bool WIN> __device__ __forceinline__ View<WIN> key_view(const SeqArgs &a, int64_t row) {
+    View<WIN> v;
+    const int2 se = __ldg(a.range + row);
+    v.lo = a.causal ? row : (int64_t)se.x;
+    v.hi = se.y;
+    if constexpr (WIN)
+        if (row - se.x >= a.sinks) {
+            v.lo = max(v.lo, row - a.window + 1);
+            v.hi = min(v.hi, row + a.window);
+        }
+    return v;
+}
+
+// What a row's result came from: its view, within the rows [w0, w1) of the tiles
+// that were walked for it (and [v0, v1) of its sinks' tiles).
+template <bool WIN> struct Span : View<WIN> {
+    int64_t w0 = 0, w1 = 0, v0 = 0, v1 = 0;
+};
+// The span of lane src's row, whose view is `v` there, over the tiles of `t`.
+template <bool WIN> __device__ __forceinline__ Span<WIN> span_of_lane(const SeqArgs &a, const View<WIN> &v, int src, const SeqTile &t, int tile_rows) {
+    Span<WIN> sp;
+    sp.lo = __shfl_sync(SGA_FULL_MASK, v.lo, src);
+    sp.hi = __shfl_sync(SGA_FULL_MASK, v.hi, src);
+    sp.w0 = (int64_t)t.t0 * tile_rows;
+    sp.w1 = min(a.rows, (int64_t)t.t1 * tile_rows);
+    if constexpr (WIN) {
+        sp.slo = __shfl_sync(SGA_FULL_MASK, v.slo, src);
+        sp.shi = __shfl_sync(SGA_FULL_MASK, v.shi, src);
+        sp.v0 = (int64_t)t.g0 * tile_rows;
+        sp.v1 = min(a.rows, (int64_t)t.g1 * tile_rows);
+    }
+    return sp;
+}
+
+// Part 0: the sinks; part 1: the interval.
+template <bool WIN> __device__ __forceinline__ int64_t first_of(const Span<WIN> &sp, int part) {
+    if constexpr (WIN)
+        if (part == 0) return sp.slo;
+    return sp.lo;
+}
+template <bool WIN> __device__ __forceinline__ int64_t end_of(const Span<WIN> &sp, int part) {
+    if constexpr (WIN)
+        if (part == 0) return sp.shi;
+    return sp.hi;
+}
 
 // A head's row, D / 32 consecutive elements a lane.
 template <typename T, int D> struct RowFrag {
@@ -89,11 +155,20 @@ template <int D> __device__ __forceinline__ uint32_t slice_columns(int first, in
 
 // Whether a row of head h of `base` that the span's tiles hold, but its interval
 // does not, is not finite in one of the columns `want`.
-template <typename T, int D>
-__device__ __forceinline__ bool masked_row_spoils(const void *base, int heads, int h, const Span &sp, uint32_t want) {
-    for (int side = 0; side < 2; ++side) {
-        const int64_t e = side ? sp.w1 : sp.lo;
-        for (int64_t j = side ? sp.hi : sp.w0; j < e; j += kStep) {
+template <typename T, int D, bool WIN>
+__device__ __forceinline__ bool masked_row_spoils(const void *base, int heads, int h, const Span<WIN> &sp, uint32_t want) {
+    // before and behind the interval; of a windowed plan, what the two walks hold
+    // before the sinks, between them and the interval, and behind it
+    for (int side = 0; side < (WIN ? 6 : 2); ++side) {
+        int64_t b = side ? sp.hi : sp.w0, e = side ? sp.w1 : sp.lo;
+        if constexpr (WIN) {
+            const int64_t x0 = side < 3 ? sp.v0 : sp.w0, x1 = side < 3 ? sp.v1 : sp.w1;
+            const bool two = sp.slo < sp.shi;
+            const int64_t s0 = two ? sp.slo : sp.lo, s1 = two ? sp.shi : sp.lo;
+            b = side % 3 == 0 ? x0 : side % 3 == 1 ? max(x0, s1) : max(x0, sp.hi);
+            e = side % 3 == 0 ? min(x1, s0) : side % 3 == 1 ? min(x1, sp.lo) : x1;
+        }
+        for (int64_t j = b; j < e; j += kStep) {
             uint32_t bad = 0;
 #pragma unroll
             for (int u = 0; u < kStep; ++u) {
@@ -109,22 +184,24 @@ __device__ __forceinline__ bool masked_row_spoils(const void *base, int heads, i
 
 // The columns of out of one query row that are not finite; the caller leaves out
 // rows whose sum of weights is NaN.
-template <typename T, int D> __device__ __forceinline__ void out_row_alone(const SeqArgs &a, int64_t row, int h, int hk, const Span &sp) {
+template <typename T, int D, bool WIN>
+__device__ __forceinline__ void out_row_alone(const SeqArgs &a, int64_t row, int h, int hk, const Span<WIN> &sp) {
     RowFrag<T, D> q, acc;
     const int64_t at = (row * a.H + h) * D;
     acc.load(a.out_w, at);
     const uint32_t want = acc.not_finite();
-    if (!masked_row_spoils<T, D>(a.V, a.Hkv, hk, sp, want)) return;
+    if (!masked_row_spoils<T, D, WIN>(a.V, a.Hkv, hk, sp, want)) return;
     q.load(a.Q, at);
     acc.zero();
     float m = -INFINITY, l = 0.f;
-    for (int64_t j = sp.lo; j < sp.hi && !acc.all_nan(want); j += kStep) {
+    for (int part = WIN ? 0 : 1; part < 2; ++part)   // (the sinks, the interval)
+      for (int64_t j = first_of(sp, part), e = end_of(sp, part); j < e && !acc.all_nan(want); j += kStep) {
         RowFrag<T, D> v[kStep];
         float s[kStep], mn = m;
 #pragma unroll
         for (int u = 0; u < kStep; ++u) {
             RowFrag<T, D> k;
-            const int64_t r = (min(j + u, sp.hi - 1) * a.Hkv + hk) * D;
+            const int64_t r = (min(j + u, e - 1) * a.Hkv + hk) * D;
             k.load(a.K, r);
             v[u].load(a.V, r);
             s[u] = q.dot(k) * (a.scale * kLog2e);
@@ -137,7 +214,7 @@ template <typename T, int D> __device__ __forceinline__ void out_row_alone(const
         for (int i = 0; i < RowFrag<T, D>::W; ++i) acc.x[i] *= al;
 #pragma unroll
         for (int u = 0; u < kStep; ++u)
-            if (j + u < sp.hi) {
+            if (j + u < e) {
                 const float p = exp2_diff(s[u], m);
                 l += p;
                 acc.add(p, v[u]);
@@ -147,8 +224,8 @@ template <typename T, int D> __device__ __forceinline__ void out_row_alone(const
 }
 
 // The columns `mine` of dK (DK) or dV of one key row that are not finite.
-template <typename T, int D>
-__device__ __forceinline__ void key_row_alone(const SeqArgs &a, bool DK, int64_t row, int hk, const Span &sp, uint32_t mine) {
+template <typename T, int D, bool WIN>
+__device__ __forceinline__ void key_row_alone(const SeqArgs &a, bool DK, int64_t row, int hk, const Span<WIN> &sp, uint32_t mine) {
     RowFrag<T, D> k, v, acc;
     const int64_t at = (row * a.Hkv + hk) * D;
     k.load(a.K, at);
@@ -159,7 +236,7 @@ __device__ __forceinline__ void key_row_alone(const SeqArgs &a, bool DK, int64_t
     const uint32_t want = acc.not_finite() & mine;
     const int h0 = hk * (a.H / a.Hkv), h1 = h0 + a.H / a.Hkv;
     bool spoilt = false;
-    for (int h = h0; h < h1 && !spoilt; ++h) spoilt = masked_row_spoils<T, D>(DK ? a.Q : a.dOut, a.H, h, sp, want);
+    for (int h = h0; h < h1 && !spoilt; ++h) spoilt = masked_row_spoils<T, D, WIN>(DK ? a.Q : a.dOut, a.H, h, sp, want);
     if (!spoilt) return;
     acc.zero();
     for (int h = h0; h < h1; ++h)
@@ -182,8 +259,8 @@ __device__ __forceinline__ void key_row_alone(const SeqArgs &a, bool DK, int64_t
 }
 
 // The columns `mine` of dQ of one query row that are not finite.
-template <typename T, int D>
-__device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, int h, const Span &sp, uint32_t mine) {
+template <typename T, int D, bool WIN>
+__device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, int h, const Span<WIN> &sp, uint32_t mine) {
     RowFrag<T, D> q, g, acc;
     const int64_t at = (row * a.H + h) * D, t = (int64_t)h * a.rows_pad + row;
     const int hk = h / (a.H / a.Hkv);
@@ -191,24 +268,25 @@ __device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, i
     if (nlse != nlse || nd != nd) return;   // every dS of the row is NaN
     acc.load(a.dQ, at);
     const uint32_t want = acc.not_finite() & mine;
-    if (!masked_row_spoils<T, D>(a.K, a.Hkv, hk, sp, want)) return;
+    if (!masked_row_spoils<T, D, WIN>(a.K, a.Hkv, hk, sp, want)) return;
     q.load(a.Q, at);
     g.load(a.dOut, at);
     acc.zero();
-    for (int64_t j = sp.lo; j < sp.hi && !acc.all_nan(want); j += kStep) {
+    for (int part = WIN ? 0 : 1; part < 2; ++part)   // (the sinks, the interval)
+      for (int64_t j = first_of(sp, part), e = end_of(sp, part); j < e && !acc.all_nan(want); j += kStep) {
         RowFrag<T, D> k[kStep];
         float w[kStep];
 #pragma unroll
         for (int u = 0; u < kStep; ++u) {
             RowFrag<T, D> v;
-            const int64_t r = (min(j + u, sp.hi - 1) * a.Hkv + hk) * D;
+            const int64_t r = (min(j + u, e - 1) * a.Hkv + hk) * D;
             k[u].load(a.K, r);
             v.load(a.V, r);
             w[u] = fast_exp2(fmaf(q.dot(k[u]), a.scale * kLog2e, nlse)) * (g.dot(v) + nd);
         }
 #pragma unroll
         for (int u = 0; u < kStep; ++u)
-            if (j + u < sp.hi) acc.add(w[u], k[u]);
+            if (j + u < e) acc.add(w[u], k[u]);
     }
     acc.store(a.dQ, at, a.scale, want);
 }

@@ -3,7 +3,7 @@
 
 #include <cuda.h>
 
-#include "seq.h"
+#include "seq_rows.cuh"
 #include "tc.cuh"
 
 namespace sga {
@@ -30,9 +30,48 @@ __device__ __forceinline__ uint32_t column_bits(int lo, int hi, int w) {
     return upto_b & ~upto_a;
 }
 
+// The tiles that a query tile (or two of one unit) walks, in order: of windowed
+// plans the sinks' (of both tiles) and then the window's, which are disjoint.
+template <bool WIN> struct Walk {
+    int t0, n;
+    __device__ __forceinline__ Walk(const SeqTile &x, const SeqTile &y) : t0(min(x.t0, y.t0)), n(max(x.t1, y.t1) - t0) {}
+    __device__ __forceinline__ int tile(int i) const { return t0 + i; }
+};
+template <> struct Walk<true> {
+    int g0, ng, h0, nh, t0, n;
+    __device__ __forceinline__ Walk(const SeqTile &x, const SeqTile &y) {
+        t0 = min(x.t0, y.t0);
+        // (the second tile's sinks begin no earlier than the first's)
+        const int g1 = min(x.g1, t0), h1 = min(y.g1, t0);
+        g0 = x.g0;
+        ng = max(0, g1 - g0);
+        h0 = ng > 0 ? max(y.g0, g1) : y.g0;
+        nh = max(0, h1 - h0);
+        n = ng + nh + max(x.t1, y.t1) - t0;
+    }
+    __device__ __forceinline__ int tile(int i) const { return i < ng ? g0 + i : i < ng + nh ? h0 + i - ng : t0 + i - ng - nh; }
+};
+// Whether the tile's own walk holds tile kt of the other side.
+template <bool WIN> __device__ __forceinline__ bool walks(const SeqTile &t, int kt) {
+    return (kt >= t.t0 && kt < t.t1) || (WIN && kt >= t.g0 && kt < t.g1);
+}
+// A tile's own walk.
+template <bool WIN> __device__ __forceinline__ int own_count(const SeqTile &t) { return (WIN ? t.g1 - t.g0 : 0) + t.t1 - t.t0; }
+template <bool WIN> __device__ __forceinline__ int own_tile(const SeqTile &t, int i) {
+    if (WIN && i < t.g1 - t.g0) return t.g0 + i;
+    return t.t0 + i - (WIN ? t.g1 - t.g0 : 0);
+}
+
 // a row's interval relative to the tile that starts at row t0
 __device__ __forceinline__ int rel(int64_t x, int64_t t0) {
     return (int)max((int64_t)0, min((int64_t)128, x - t0));
+}
+
+// The columns of word w of the tile at row t0 that a row sees.
+template <bool WIN> __device__ __forceinline__ uint32_t view_bits(const View<WIN> &v, int64_t t0, int w) {
+    uint32_t bits = column_bits(rel(v.lo, t0), rel(v.hi, t0), w);
+    if constexpr (WIN) bits |= column_bits(rel(v.slo, t0), rel(v.shi, t0), w);
+    return bits;
 }
 
 }  // namespace seq

@@ -1,0 +1,65 @@
+// Row terms of the attention backward, for both dtypes: -lse log2(e) and -Delta.
+#include "seq.h"
+
+namespace sga {
+namespace {
+
+// Row terms: D / EL lanes of 16 bytes a (row, head), four of them in flight.
+// Rows behind the last sequence (to the end of its tile) get -lse = -inf, so
+// that their weights are zero, and Delta = 0.
+constexpr int kTerms = 4;
+template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
+    let_next_start();
+    wait_previous();
+    constexpr int EL = Elt<T>::EL, L = D / EL, G = 256 / L;   // G items of a block at a time
+    const int sub = threadIdx.x % L;
+    const int64_t live = a.rows * a.H, n = a.rows_pad * a.H, g0 = (int64_t)blockIdx.x * (G * kTerms) + threadIdx.x / L;
+    uint4 x[kTerms], y[kTerms];
+    float lse[kTerms];
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) {
+        const int64_t g = g0 + k * G;
+        x[k] = y[k] = make_uint4(0, 0, 0, 0);
+        lse[k] = INFINITY;
+        if (g < live) {   // (an item's elements follow the one's before)
+            x[k] = ldg16(static_cast<const T *>(a.out) + g * D + sub * EL);
+            y[k] = ldg16(static_cast<const T *>(a.dOut) + g * D + sub * EL);
+            if (sub == 0) lse[k] = __ldg(a.lse + g) * kLog2e;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) {
+        const int64_t g = g0 + k * G;
+        float u[EL], v[EL], d = 0.f;
+        unpack<T>(x[k], u);
+        unpack<T>(y[k], v);
+#pragma unroll
+        for (int i = 0; i < EL; ++i) d = fmaf(u[i], v[i], d);
+        d = group_sum<L>(d);
+        if (sub == 0 && g < n) {
+            // (a 64-bit division takes longer than the rest of an item)
+            const int64_t row = n <= UINT32_MAX ? (int64_t)((uint32_t)g / (uint32_t)a.H) : g / a.H;
+            const int64_t at = (g - row * a.H) * a.rows_pad + row;
+            a.ws_nlse[at] = -lse[k];
+            a.ws_ndelta[at] = g < live ? -d : 0.f;
+        }
+    }
+}
+
+template <typename T, int D> cudaError_t launch_terms(const SeqArgs &a, cudaStream_t s) {
+    constexpr int per = kTerms * 256 / (D / Elt<T>::EL);   // items of a block
+    note_launch(SGA_KERN_SEQ_BWD_ROWS, s, false);
+    const cudaError_t e = launch_early(seq_row_terms_kernel<T, D>, dim3((unsigned)((a.rows_pad * a.H + per - 1) / per)), dim3(256), 0, s, a);
+    note_launch(SGA_KERN_SEQ_BWD_ROWS, s, true);
+    return e;
+}
+
+}  // namespace
+
+template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s) {
+    return D == 32 ? launch_terms<T, 32>(a, s) : D == 64 ? launch_terms<T, 64>(a, s) : launch_terms<T, 128>(a, s);
+}
+template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t);
+template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
+
+}  // namespace sga

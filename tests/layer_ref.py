@@ -91,6 +91,25 @@ def visible(n, causal, window, sinks, device="cuda"):
     return vis & (apart >= 0) if causal else vis
 
 
+def shared_offset(k, n, causal, window, sinks):
+    """[n, D]: the four of a query row's keys whose mean the bf16 dQ pass takes for an offset that all its keys share, in
+    the columns where they are no farther apart than half of it (a little more, for the mean's own rounding); zero in the
+    others."""
+    i = torch.arange(n, device=k.device)
+    end = i + 1 if causal else torch.full_like(i, n)
+    w = window or n
+    lo, hi, s = (i - w + 1).clamp(min=0), torch.minimum(end, i + w), end.clamp(max=sinks)
+    apart = s < lo                      # the sinks lie before the window, else the two are one interval
+    lo, hi = torch.where(apart, lo, 0), torch.where(apart, hi, torch.maximum(hi, s))
+    m = hi - lo
+    m = torch.where(m < 8, m, 2 ** torch.floor(torch.log2(m.double())).long())
+    at = torch.stack([lo + (m * (2 * x + 1) >> 3) for x in range(4)])
+    at[3] = torch.where(apart & (s > 0), s >> 1, at[3])
+    four = k[at]
+    c = four.mean(0)
+    return torch.where(four.amax(0) - four.amin(0) <= 0.52 * c.abs(), c, 0.0)
+
+
 def window_reference(seq_ptr, Q, K, V, scale, causal, window, sinks, dOut=None, out_used=None):
     """{name: (value, bound)} of out, lse and, with dOut, dQ, dK, dV: each sequence and head by itself.  The gradients'
     bound takes the forward's rounded out (out_used), from which the kernels form Delta."""
@@ -138,6 +157,12 @@ def window_reference(seq_ptr, Q, K, V, scale, causal, window, sinks, dOut=None, 
             sums = (n * g + 8) * U
             dQ[b:e, h] = scale * (dsv @ ki)
             dQb[b:e, h] = scale * (dse @ ki.abs() + sums * (dsv.abs() @ ki.abs()))
+            if R:
+                # dQ is formed as sum_j (dS_j + e_j) k_j - (sum_j e_j) c with |e_j| <= R |dS_j|: off by sum_j e_j (k_j - c),
+                # not sum_j e_j k_j; c is a mean in bf16 (three roundings of at most 2^-8)
+                c = shared_offset(ki, n, causal, window, sinks)
+                far = (dsv.abs()[:, :, None] * ((ki[None] - c[:, None]).abs() - ki.abs()[None]).clamp(min=0)).sum(1)
+                dQb[b:e, h] += scale * R * (far + 2.0 ** -6 * c.abs() * dsv.abs().sum(1)[:, None])
             dK[b:e, h // g] += scale * (dsv.T @ qi)
             dKb[b:e, h // g] += scale * (dse.T @ qi.abs() + sums * (dsv.abs().T @ qi.abs()))
             dV[b:e, h // g] += p.T @ doi

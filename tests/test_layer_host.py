@@ -66,3 +66,14 @@ def test_host_tensors_are_refused():
         sga.qk_norm_rope_fwd(rot, x, x, torch.arange(2))
     with pytest.raises(ValueError, match="CUDA tensor"):
         sga.qk_norm_rope_bwd(rot, x, x, torch.arange(2), None, None, None, None, x, x)
+
+
+def test_windowed_plan_arguments():
+    lib, out = sga.load_library(), ctypes.c_void_p()
+    new = lambda window, sinks, causal=1, D=64, ptr=P: lib.sga_seq_plan_create_windowed(ptr, 4, 2, 2, D, 1, causal, window, sinks, None, ctypes.byref(out))
+    assert new(-1, 0) == new(0, 1) == new(4, -1) == new(4, 1, causal=2) == new(4, 1, ptr=None) == sga.SGA_EINVAL
+    assert new(4, 1, D=48) == sga.SGA_EUNSUPPORTED
+    sp = torch.tensor([0, 4], dtype=torch.int32)
+    for window, sinks in ((0, 0), (-3, 0), (None, 2), (4, -1)):
+        with pytest.raises(ValueError, match="window|sinks"):
+            sga.SeqPlan(sp, 1, 32, window=window, sinks=sinks)
