@@ -415,6 +415,39 @@ sga_status qk_norm_rope_bwd(const sga_rotary *rot, const void *Q, int64_t ldq, c
                             const void *dKo, int64_t T, int H, int Hkv, sga_dtype dt, sga_dtype wdt, void *dQ, void *dK,
                             void *dwq, void *dwk, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- gated feed-forward product ------------------------------------------------
+ *
+ * Both projections of a gated feed-forward block, the activation and the product:
+ *   G = X Wg,  U = X Wu,  out = act(G) U
+ * for X [T, F] and Wg, Wu [F, M] of dt (products summed in fp32, in fp32 tensors to
+ * fp32's accuracy); act: silu, gelu (g times the normal distribution function) or
+ * relu.  G and U [T, M], rounded to dt, are kept for the backward pass, or both NULL.
+ * out is formed from the sums before they are rounded; the backward takes dG and dU
+ * from G and U as they are, and in bf16 rounds them once:
+ *   dG = dOut U act'(G),  dU = dOut act(G),
+ *   dX = dG Wg^T + dU Wu^T,  dWg = X^T dG,  dWu = X^T dU.
+ * dX may be NULL, dWg and dWu together too (not computed).  Tensors are dense and
+ * 16-byte aligned; rows of a multiple of 16 bytes are read as they lie, others are
+ * copied to the workspace first (fp32 always).  1 <= F, M <= 2^20, any T.  Sums are
+ * taken in an order that the sizes fix: bitwise reproducible.  In fp32 an infinity
+ * or NaN in X or a weight makes the results that it enters not finite (which of the
+ * two, is not defined).  Workspaces are 256-byte aligned. */
+#define SGA_ACT_SILU 0
+#define SGA_ACT_GELU 1
+#define SGA_ACT_RELU 2
+size_t sga_gated_ff_fwd_workspace_bytes(int64_t T, int64_t F, int64_t M, sga_dtype dt);
+sga_status gated_ff_fwd(const void *X, const void *Wg, const void *Wu, int64_t T, int64_t F, int64_t M, int act, sga_dtype dt,
+                        void *out, void *G, void *U, void *workspace, size_t workspace_bytes, void *stream);
+size_t sga_gated_ff_bwd_workspace_bytes(int64_t T, int64_t F, int64_t M, sga_dtype dt);
+sga_status gated_ff_bwd(const void *X, const void *Wg, const void *Wu, const void *G, const void *U, const void *dOut, int64_t T,
+                        int64_t F, int64_t M, int act, sga_dtype dt, void *dX, void *dWg, void *dWu, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Read and clear the current device's error word of these calls (a wait of the
+ * tensor-core products that gave up).  Synchronises `stream`; SGA_EDEVICE_CHECK if it
+ * was non-zero. */
+sga_status sga_gated_ff_read_device_error(void *stream, int32_t *code);
+
 /* ---- embedding --------------------------------------------------------------
  *
  * out[t] = scale table[ids[t]] for ids [N] (int32 or int64: id_bytes 4 or 8)
@@ -560,7 +593,9 @@ typedef enum {
     SGA_KERN_EMBED_FWD = 32, SGA_KERN_EMBED_BWD = 33, SGA_KERN_EMBED_ADD = 34,
     SGA_KERN_QK_ROPE_FWD = 35, SGA_KERN_QK_ROPE_BWD = 36, SGA_KERN_QK_ROPE_REDUCE = 37,
     SGA_KERN_SEQ_JOIN = 38,
-    SGA_KERN_COUNT = 39
+    SGA_KERN_FF_LAY = 39, SGA_KERN_FF_FWD = 40, SGA_KERN_FF_SLOPES = 41, SGA_KERN_FF_DX = 42, SGA_KERN_FF_DW = 43,
+    SGA_KERN_FF_JOIN = 44,
+    SGA_KERN_COUNT = 45
 } sga_kernel_id;
 /* (Planned GATv2 passes merge their split rows inside the edge kernels --
  * the last chunk of a row to finish merges it -- so SGA_KERN_GATV2_FWD_MERGE

@@ -38,7 +38,7 @@ KERNELS = {
     "gat_fwd": 23, "gat_bwd_dst": 24, "gat_bwd_src": 25, "seq_fwd": 26, "seq_bwd_rows": 27,
     "seq_bwd": 28, "norm_fwd": 29, "norm_bwd": 30, "norm_reduce": 31, "embed_fwd": 32,
     "embed_bwd": 33, "embed_add": 34, "qk_rope_fwd": 35, "qk_rope_bwd": 36, "qk_rope_reduce": 37,
-    "seq_join": 38,
+    "seq_join": 38, "ff_lay": 39, "ff_fwd": 40, "ff_slopes": 41, "ff_dx": 42, "ff_dw": 43, "ff_join": 44,
 }
 
 SGA_LAYER_ATTENTION, SGA_LAYER_MINMAX, SGA_LAYER_GAT = 0, 1, 2
@@ -143,6 +143,13 @@ _SIGNATURES = {
     "sga_qk_norm_rope_bwd_workspace_bytes": ([_i64, _int], ctypes.c_size_t),
     "qk_norm_rope_bwd": ([_vp, _vp, _i64, _vp, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int,
                           _int, _int, _int, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], _int),
+    "sga_gated_ff_fwd_workspace_bytes": ([_i64, _i64, _i64, _int], ctypes.c_size_t),
+    "gated_ff_fwd": ([_vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                      _vp], _int),
+    "sga_gated_ff_bwd_workspace_bytes": ([_i64, _i64, _i64, _int], ctypes.c_size_t),
+    "gated_ff_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp,
+                      ctypes.c_size_t, _vp], _int),
+    "sga_gated_ff_read_device_error": ([_vp, ctypes.POINTER(ctypes.c_int32)], _int),
     "embed_fwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _int, _vp, _vp], _int),
     "sga_embed_bwd_workspace_bytes": ([_i64, _i64, _i64], ctypes.c_size_t),
     "embed_bwd": ([_vp, _int, _vp, _i64, _i64, _i64, _f32, _i64, _int, _vp, _vp, ctypes.c_size_t,
@@ -675,6 +682,20 @@ def _place(device, stream):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
+def _device_word(read: str, device, stream) -> int:
+    """Read and clear an error word that a device has one of."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    code = ctypes.c_int32()
+    ctx, raw = _place(device, stream)
+    with ctx:
+        st = getattr(_lib(), read)(raw, ctypes.byref(code))
+    if st not in (SGA_OK, SGA_EDEVICE_CHECK):
+        _check(st, read)
+    return int(code.value)
+
+
 class SeqPlan:
     """A plan for attention over packed sequences: sequence b is rows
     seq_ptr[b] .. seq_ptr[b + 1] of the node tensors ([B + 1] int32, from 0,
@@ -834,6 +855,29 @@ def qk_norm_rope_bwd(rot: Rotary, Q, K, pos, wq, wk, rq, rk, dQo, dKo, dQ=None, 
     return _ext().qk_norm_rope_bwd(rot._c, Q, K, pos, wq, wk, rq, rk, dQo, dKo, dQ, dK, dwq, dwk, stream)
 
 
+# --------------------------------------------------- gated feed-forward product
+
+def gated_ff_fwd(X, Wg, Wu, act: str = "silu", save: bool = True, out=None, G=None, U=None, stream=None):
+    """Both projections of a gated feed-forward block, the activation and the
+    product: (out, G, U) with G = X Wg, U = X Wu and out = act(G) U [..., M] of
+    X [..., F] and Wg, Wu [F, M]; ``act``: "silu", "gelu" or "relu".  G and U are
+    kept for the backward pass; with ``save=False`` they are not written (None)."""
+    return _ext().gated_ff_fwd(X, Wg, Wu, act, save, out, G, U, stream)
+
+
+def gated_ff_bwd(X, Wg, Wu, G, U, dOut, act: str = "silu", input: bool = True, weights: bool = True,
+                 dX=None, dWg=None, dWu=None, stream=None):
+    """(dX, dWg, dWu) from the forward's G and U.  ``input=False``: no dX,
+    ``weights=False``: no dWg and dWu (None in their place)."""
+    return _ext().gated_ff_bwd(X, Wg, Wu, G, U, dOut, act, input, weights, dX, dWg, dWu, stream)
+
+
+def gated_ff_device_error(device=None, stream=None) -> int:
+    """Read and clear the feed-forward calls' error word on ``device`` (default:
+    the current one); 0 = no wait of their products gave up."""
+    return _device_word("sga_gated_ff_read_device_error", device, stream)
+
+
 # ------------------------------------------------------------------- embedding
 
 def embed_fwd(ids, table, scale: float = 1.0, out=None, stream=None):
@@ -855,16 +899,7 @@ def embed_bwd(ids, dOut, num_rows: int, scale: float = 1.0, padding_idx: int | N
 def embed_device_error(device=None, stream=None) -> int:
     """Read and clear the embedding calls' error word on ``device`` (default:
     the current one); 0 = every id was inside its table."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    code = ctypes.c_int32()
-    ctx, raw = _place(device, stream)
-    with ctx:
-        st = _lib().sga_embed_read_device_error(raw, ctypes.byref(code))
-    if st not in (SGA_OK, SGA_EDEVICE_CHECK):
-        _check(st, "sga_embed_read_device_error")
-    return int(code.value)
+    return _device_word("sga_embed_read_device_error", device, stream)
 
 
 # -------------------------------------------------------------- autograd layers
@@ -1066,3 +1101,33 @@ class QKNormRope(torch.autograd.Function):
         Q, K, pos, wq, wk, rq, rk = ctx.saved_tensors
         dQ, dK, dwq, dwk = qk_norm_rope_bwd(ctx.rot, Q, K, pos, wq, wk, rq, rk, dQo.contiguous(), dKo.contiguous())
         return dQ, dK, None, dwq, dwk, None, None
+
+
+def _begin16(t):
+    """t, contiguous and beginning on a 16-byte boundary (a copy where it is not)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class GatedFF(torch.autograd.Function):
+    """The gated product of a feed-forward block as an autograd function:
+    ``h = GatedFF.apply(X, Wg, Wu, "silu")`` = act(X Wg) (X Wu); the block's
+    second projection is an ordinary product of h."""
+
+    @staticmethod
+    def forward(ctx, X, Wg, Wu, act="silu"):
+        X, Wg, Wu = _begin16(X), _begin16(Wg), _begin16(Wu)
+        save = any(ctx.needs_input_grad)
+        out, G, U = gated_ff_fwd(X, Wg, Wu, act, save=save)
+        ctx.act = act
+        if save:
+            ctx.save_for_backward(X, Wg, Wu, G, U)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dOut):
+        X, Wg, Wu, G, U = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dX, dWg, dWu = gated_ff_bwd(X, Wg, Wu, G, U, _begin16(dOut), ctx.act, need[0], need[1] or need[2])
+        return dX, dWg, dWu, None

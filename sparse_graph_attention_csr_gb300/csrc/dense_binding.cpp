@@ -463,6 +463,107 @@ py::tuple qk_norm_rope_bwd_(const sga_rotary &r, const Tensor &Q, const Tensor &
     return py::make_tuple(std::move(q), std::move(k), gq ? py::cast(*gq) : py::none(), gk ? py::cast(*gk) : py::none());
 }
 
+// ---- gated feed-forward product ---------------------------------------------------------------
+
+struct Ff {
+    int64_t T, F, M;
+    sga_dtype dt;
+    at::ScalarType type;
+    at::IntArrayRef lead;
+    at::Device device;
+    int act;
+    at::DimVector hidden;   // [..., M]
+};
+
+int ff_act(const std::string &act) {
+    if (act == "silu") return SGA_ACT_SILU;
+    if (act == "gelu") return SGA_ACT_GELU;
+    if (act == "relu") return SGA_ACT_RELU;
+    throw py::value_error("act must be silu, gelu or relu, got " + act);
+}
+
+void need16(const Tensor &t, const char *name) {
+    if (t.numel() > 0 && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16)
+        throw py::value_error(std::string(name) + " must begin on a 16-byte boundary");
+}
+
+Ff ff_inputs(const Tensor &X, const Tensor &Wg, const Tensor &Wu, const std::string &act) {
+    need_cuda(X, "X");
+    if (X.dim() < 1 || X.size(-1) < 1) throw py::value_error("X must be [..., F] with F >= 1, got " + text(X.sizes()));
+    need_cuda(Wg, "Wg");
+    if (Wg.dim() != 2 || Wg.size(1) < 1) throw py::value_error("Wg must be [F, M] with M >= 1, got " + text(Wg.sizes()));
+    Ff f{0, X.size(-1), Wg.size(1), code(X), X.scalar_type(), X.sizes().slice(0, X.dim() - 1), X.device(), ff_act(act), {}};
+    f.T = X.numel() / f.F;
+    need_contiguous(X, "X");
+    need(Wg, "Wg", f.device, f.type, {f.F, f.M});
+    need(Wu, "Wu", f.device, f.type, {f.F, f.M});
+    need16(X, "X");
+    need16(Wg, "Wg");
+    need16(Wu, "Wu");
+    f.hidden = at::DimVector(f.lead);
+    f.hidden.push_back(f.M);
+    return f;
+}
+
+Tensor ff_result(const Maybe &given, const char *name, const Ff &f, at::IntArrayRef shape) {
+    if (!given) return fresh(shape, f.type, f.device);
+    need(*given, name, f.device, f.type, shape);
+    need16(*given, name);
+    return *given;
+}
+
+py::tuple gated_ff_fwd_(const Tensor &X, const Tensor &Wg, const Tensor &Wu, const std::string &act, bool save, const Maybe &out,
+                        const Maybe &G, const Maybe &U, const py::object &stream) {
+    const Ff f = ff_inputs(X, Wg, Wu, act);
+    if (!save && (G || U)) throw py::value_error("G and U given with save=False");
+    const Place on(f.device, stream);
+    Tensor o = ff_result(out, "out", f, f.hidden);
+    Maybe g, u;
+    if (save) {
+        g = ff_result(G, "G", f, f.hidden);
+        u = ff_result(U, "U", f, f.hidden);
+    }
+    if (out || G || U)
+        distinct({named("out", o), named("G", g), named("U", u)}, {named("X", X), named("Wg", Wg), named("Wu", Wu)});
+    const size_t bytes = sga_gated_ff_fwd_workspace_bytes(f.T, f.F, f.M, f.dt);
+    Tensor ws;
+    if (bytes) ws = fresh({(int64_t)bytes}, at::kByte, f.device);
+    check(gated_ff_fwd(ptr(X), ptr(Wg), ptr(Wu), f.T, f.F, f.M, f.act, f.dt, ptr(o), ptr(g), ptr(u), bytes ? ptr(ws) : nullptr, bytes, on.raw()),
+          "gated_ff_fwd");
+    on.used({named("X", X), named("Wg", Wg), named("Wu", Wu)}, {named("out", o), named("G", g), named("U", u)});
+    return py::make_tuple(std::move(o), g ? py::cast(*g) : py::none(), u ? py::cast(*u) : py::none());
+}
+
+py::tuple gated_ff_bwd_(const Tensor &X, const Tensor &Wg, const Tensor &Wu, const Tensor &G, const Tensor &U, const Tensor &dOut,
+                        const std::string &act, bool input, bool weights, const Maybe &dX, const Maybe &dWg, const Maybe &dWu,
+                        const py::object &stream) {
+    const Ff f = ff_inputs(X, Wg, Wu, act);
+    for (const Named &n : {named("G", G), named("U", U), named("dOut", dOut)}) {
+        need(*n.t, n.name, f.device, f.type, f.hidden);
+        need16(*n.t, n.name);
+    }
+    if (!input && dX) throw py::value_error("dX given with input=False");
+    if (!weights && (dWg || dWu)) throw py::value_error("dWg or dWu given with weights=False");
+    const Place on(f.device, stream);
+    Maybe x, wg, wu;
+    if (input) x = ff_result(dX, "dX", f, X.sizes());
+    if (weights) {
+        wg = ff_result(dWg, "dWg", f, {f.F, f.M});
+        wu = ff_result(dWu, "dWu", f, {f.F, f.M});
+    }
+    if (dX || dWg || dWu)
+        distinct({named("dX", x), named("dWg", wg), named("dWu", wu)},
+                 {named("X", X), named("Wg", Wg), named("Wu", Wu), named("G", G), named("U", U), named("dOut", dOut)});
+    const size_t bytes = sga_gated_ff_bwd_workspace_bytes(f.T, f.F, f.M, f.dt);
+    const Tensor ws = fresh({(int64_t)bytes}, at::kByte, f.device);
+    check(gated_ff_bwd(ptr(X), ptr(Wg), ptr(Wu), ptr(G), ptr(U), ptr(dOut), f.T, f.F, f.M, f.act, f.dt, ptr(x), ptr(wg), ptr(wu), ptr(ws),
+                       bytes, on.raw()),
+          "gated_ff_bwd");
+    on.used({named("X", X), named("Wg", Wg), named("Wu", Wu), named("G", G), named("U", U), named("dOut", dOut)},
+            {named("dX", x), named("dWg", wg), named("dWu", wu)});
+    return py::make_tuple(x ? py::cast(*x) : py::none(), wg ? py::cast(*wg) : py::none(), wu ? py::cast(*wu) : py::none());
+}
+
 // ---- embedding -------------------------------------------------------------------------
 
 int id_bytes(const Tensor &ids) {
@@ -546,6 +647,8 @@ PYBIND11_MODULE(_dense, m) {
     py::class_<sga_rotary>(m, "Rotary").def(py::init(&rotary_));
     m.def("qk_norm_rope_fwd", &qk_norm_rope_fwd_);
     m.def("qk_norm_rope_bwd", &qk_norm_rope_bwd_);
+    m.def("gated_ff_fwd", &gated_ff_fwd_);
+    m.def("gated_ff_bwd", &gated_ff_bwd_);
     m.def("embed_fwd", &embed_fwd_);
     m.def("embed_bwd", &embed_bwd_);
 }

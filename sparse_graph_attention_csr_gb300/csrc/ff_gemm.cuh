@@ -1,0 +1,540 @@
+// Products of the gated feed-forward block on the tcgen05 tensor cores, by CTA
+// pairs (tc_pair.cuh): tiles of 256 x 256 (forward: 256 rows x 128 gate and the
+// same 128 up columns, so that one thread has both halves of a result).
+//
+// Persistent pairs; in each CTA
+//   warp 0, one lane: TMA loads of its half of a k-block's operands (128 rows of A,
+//     128 columns of B, 64 deep) into a ring, arriving at the first CTA's barriers;
+//   warp 1 (first CTA): the products, into one of two accumulators of 256 columns;
+//   warps 4 .. 11: move finished accumulators to registers and add them there
+//     (every `depth` k-blocks), and store a tile's result, through shared memory
+//     and TMA where its rows allow it.
+// Operands lie in memory as the tensors do: X and dG of the dX product along their
+// depth (K-major), weights of the forward and both operands of the dW product
+// across it (MN-major).
+//
+// fp32: an operand is the sum of three bf16 parts (8 + 8 + 8 bits); of the nine
+// products of parts the six that reach 2^-24 of the result are taken, smallest
+// first.  The tensor core's accumulator drops what falls below its last bit, which
+// adds up over a long depth, so each k-block of 64 is added to fp32 registers by
+// itself: 4 products of the leading parts round nothing worth mentioning.
+//
+// Tiles are dealt to the pairs by whole rounds; the last, incomplete round would
+// leave pairs idle, so its tiles' depth is cut into equal shares, which leave fp32
+// sums that a second kernel adds in order (where that is quicker): no atomics, bitwise
+// reproducible.
+//
+// Every wait is bounded; a timeout sets the error word and ends the role.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "ff.h"
+#include "tc_dx.cuh"
+#include "tc_pair.cuh"
+
+namespace sga {
+
+cudaError_t bf16_tensor_map(CUtensorMap *m, const __nv_bfloat16 *base, int64_t rows, int64_t cols, int64_t row_elems,
+                            uint32_t box_cols, uint32_t box_rows);   // (tc_dx.cu)
+
+namespace {
+
+// Bit kErrMmaTimeout: a wait gave up since the last read, per device.
+__device__ int32_t g_ff_err;
+
+constexpr int kFfThreads = 384;
+// Registers a thread at launch and after the split: an epilogue thread holds 128
+// sums.  The shares add up to the launch's total.
+constexpr int kFfLaunch = 168, kFfCtrl = 56, kFfEpi = 224;
+static_assert(kFfCtrl + 2 * kFfEpi <= 3 * kFfLaunch, "register split");
+
+template <FfMode MODE, bool F32> struct FfCfg {
+    static constexpr int PARTS = F32 ? 3 : 1;
+    static constexpr uint32_t TB = 128 * 128;                // a CTA's share of an operand's k-block, 128 x 64 bf16
+    static constexpr uint32_t STAGE = 2 * PARTS * TB;
+    static constexpr int NST = F32 ? 2 : 6;
+    static constexpr uint32_t OUT0 = NST * STAGE;            // staging of results: 32 rows x 64 bf16 a warp
+    static constexpr uint32_t BYTES = OUT0 + 8 * 4096;
+    static constexpr bool A_MN = MODE == FfMode::DW, B_MN = MODE != FfMode::DX;
+    static constexpr int BN = MODE == FfMode::FWD ? 128 : 256;   // columns of a result that a tile covers
+};
+constexpr int kTileFloats = 256 * 256;
+
+struct FfParams {
+    CUtensorMap ta[2][3], tb[2][3];   // [segment (DX) or operand][part]
+    CUtensorMap to[3];                // results: FWD out, G, U; DX dX; DW dWg, dWu
+    void *out[3];
+    float *partial;
+    int64_t rows, cols;               // of a result
+    int tiles_m, tiles_n;             // tiles
+    int kb, kb_seg;                   // k-blocks of a tile; of a segment
+    int depth;                        // k-blocks between two moves to registers
+    int pairs, whole;                 // pairs of the grid; tiles dealt whole
+    int act, tma_out;
+};
+
+// Tile t's row and column of tiles: eight rows of tiles at a time, column by column,
+// so that what the pairs load at one time is near square.
+__host__ __device__ __forceinline__ void ff_tile(int t, int tiles_m, int tiles_n, int &m, int &n) {
+    const int per = 8 * tiles_n, g = t / per, rest = t - g * per, rows = tiles_m - 8 * g < 8 ? tiles_m - 8 * g : 8;
+    n = rest / rows;
+    m = 8 * g + rest - n * rows;
+}
+
+// A pair's units: whole tiles pair, pair + pairs, ... of the first `whole`, then its
+// share of the others' k-blocks, laid end to end; a share is no longer than a tile is
+// deep, so it lies in one tile or two.
+struct FfUnit {
+    int tile, k0, k1, slot;   // k-blocks [k0, k1); slot of the partial sums, or -1 for a whole tile
+};
+struct FfUnits {
+    int pair, pairs, kb, full, tile, k0, k1, next;   // the share: [k0, k1) of `tile`, [0, next) of the one behind it
+    __host__ __device__ FfUnits(int tiles, int whole, int depth, int n_pairs, int which) : pair(which), pairs(n_pairs), kb(depth) {
+        full = pair < whole ? (whole - 1 - pair) / pairs + 1 : 0;
+        const int64_t all = (int64_t)(tiles - whole) * kb, b = all * pair / pairs, e = all * (pair + 1) / pairs;
+        const int t = (int)(b / kb);
+        tile = whole + t;
+        k0 = (int)(b - (int64_t)t * kb);
+        k1 = (int)(e - b) < kb - k0 ? k0 + (int)(e - b) : kb;
+        next = (int)(e - b) - (k1 - k0);
+    }
+    // the i-th; false past the last
+    __host__ __device__ __forceinline__ bool get(int i, FfUnit &u) const {
+        if (i < full) {
+            u = {pair + i * pairs, 0, kb, -1};
+            return true;
+        }
+        if (i == full && k0 < k1) {
+            u = {tile, k0, k1, 2 * pair};
+            return true;
+        }
+        if (i == full + 1 && next > 0) {
+            u = {tile + 1, 0, next, 2 * pair + 1};
+            return true;
+        }
+        return false;
+    }
+};
+
+template <FfMode MODE, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_gemm_kernel(const __grid_constant__ FfParams p) {
+    using C = FfCfg<MODE, F32>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full[C::NST], empty[C::NST], tfull[2], tempty[2];
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
+    const uint32_t sbase = tc::smem_u32(smem), rank = tc::cluster_rank();
+    const FfUnits units(p.tiles_m * p.tiles_n, p.whole, p.kb, p.pairs, blockIdx.x >> 1);
+
+    if (tid == 32) {
+        for (int i = 0; i < C::NST; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&tfull[i], 1);
+            tc::mbar_init(&tempty[i], 16);   // the epilogue warps of both CTAs
+        }
+    }
+    wait_previous();
+    tc::cluster_sync();   // both CTAs run, their barriers initialised
+    if (warp == 0) tc::tmem_alloc_pair(&tmem_base, 512);
+    tc::fence_before_sync();
+    tc::cluster_sync();
+    tc::fence_after_sync();
+    let_next_start();
+
+    if (warp < 4) {
+        tc::reg_dec<kFfCtrl>();
+        if (warp == 0 && lane == 0) {   // ----------------------------------- TMA producer
+            bool ok = true;
+            int it = 0;
+            FfUnit u;
+            for (int i = 0; ok && units.get(i, u); ++i) {
+                int tm, tn;
+                ff_tile(u.tile, p.tiles_m, p.tiles_n, tm, tn);
+                for (int kb = u.k0; kb < u.k1; ++kb, ++it) {
+                    const int s = it % C::NST, r = it / C::NST;
+                    if (r >= 1 && !tc::mbar_wait_cluster(&empty[s], (r - 1) & 1, tc::kWaitLimit)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) tc::mbar_expect_tx(&full[s], 2 * C::STAGE);
+                    const uint32_t bar = tc::map_rank(&full[s], 0), at = sbase + s * C::STAGE;
+                    const int seg = MODE == FfMode::DX && kb >= p.kb_seg, k = (kb - (seg ? p.kb_seg : 0)) * 64;
+                    const int m0 = tm * 256 + rank * 128;
+                    int b, n0;   // which B, and the first of this CTA's columns
+                    if (MODE == FfMode::FWD) {
+                        b = rank;
+                        n0 = tn * 128;
+                    } else if (MODE == FfMode::DX) {
+                        b = seg;
+                        n0 = tn * 256 + rank * 128;
+                    } else {
+                        b = 2 * tn >= p.tiles_n;
+                        n0 = (tn - (b ? p.tiles_n / 2 : 0)) * 256 + rank * 128;
+                    }
+#pragma unroll
+                    for (int q = 0; q < C::PARTS; ++q) {
+                        const uint32_t pa = at + q * C::TB, pb = at + (C::PARTS + q) * C::TB;
+                        const CUtensorMap *ma = &p.ta[MODE == FfMode::DX ? seg : 0][q], *mb = &p.tb[b][q];
+                        if (C::A_MN) {
+                            tc::tma_load_2d_pair(pa, ma, m0, k, bar);
+                            tc::tma_load_2d_pair(pa + 8192, ma, m0 + 64, k, bar);
+                        } else {
+                            tc::tma_load_2d_pair(pa, ma, k, m0, bar);
+                        }
+                        if (C::B_MN) {
+                            tc::tma_load_2d_pair(pb, mb, n0, k, bar);
+                            tc::tma_load_2d_pair(pb + 8192, mb, n0 + 64, k, bar);
+                        } else {
+                            tc::tma_load_2d_pair(pb, mb, k, n0, bar);
+                        }
+                    }
+                }
+            }
+            // (what the products' completion arrives at, here and in the other CTA, stays until it has)
+            for (int i = it - 1; ok && i >= 0 && i >= it - C::NST; --i)
+                ok = tc::mbar_wait_cluster(&empty[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
+            if (!ok) atomicOr(&g_ff_err, tc::kErrMmaTimeout);
+            // loads of both CTAs that no product consumed (only after a timeout) land before the pair ends
+            if (rank == 0)
+                for (int i = it - 1; i >= 0 && i >= it - C::NST; --i) tc::mbar_wait_cluster(&full[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
+        } else if (warp == 1 && rank == 0) {   // ---------------------------- MMA issuer (the warp in step)
+            constexpr uint32_t idesc = tc::idesc_bf16(256, 256) | (C::A_MN ? tc::kMajorMnA : 0u) | (C::B_MN ? tc::kMajorMnB : 0u);
+            // parts of A and B by product, the smallest products first
+            constexpr int NP = F32 ? 6 : 1, PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+            bool ok = true;
+            int it = 0, chunk = 0;
+            FfUnit u;
+            for (int i = 0; ok && units.get(i, u); ++i)
+                for (int c0 = u.k0; ok && c0 < u.k1; c0 += p.depth, ++chunk) {
+                    const int buf = chunk & 1, use = chunk >> 1, c1 = min(u.k1, c0 + p.depth);
+                    if (use >= 1 && !tc::warp_wait_cluster(&tempty[buf], (use - 1) & 1, tc::kWaitLimit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t d = tmem_base + buf * 256;
+                    for (int kb = c0; kb < c1; ++kb, ++it) {
+                        const int s = it % C::NST;
+                        if (!tc::warp_wait_cluster(&full[s], (it / C::NST) & 1, tc::kWaitLimit)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t at = sbase + s * C::STAGE;
+#pragma unroll
+                        for (int q = 0; q < NP; ++q) {
+                            const uint32_t a = at + (F32 ? PA[q] : 0) * C::TB, b = at + (C::PARTS + (F32 ? PB[q] : 0)) * C::TB;
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma_bf16_pair_w(d, C::A_MN ? tc::desc_sw128_mn(a + kk * 2048, 8192) : tc::desc_sw128(a + kk * 32),
+                                                    C::B_MN ? tc::desc_sw128_mn(b + kk * 2048, 8192) : tc::desc_sw128(b + kk * 32), idesc,
+                                                    kb > c0 || q > 0 || kk > 0);
+                        }
+                        tc::mma_commit_pair_w(&empty[s]);
+                    }
+                    tc::mma_commit_pair_w(&tfull[buf]);
+                }
+            if (!ok && lane == 0) atomicOr(&g_ff_err, tc::kErrMmaTimeout);
+            // (every product issued is complete before TMEM is released: the epilogue of both CTAs waits for tfull;
+            // after a timeout the last commit is waited for here)
+            if (!ok)
+                for (int b = 0; b < 2; ++b) tc::warp_wait_cluster(&tfull[b], ((chunk + (b ^ (chunk & 1))) >> 1) & 1, 1u << 16);
+        }
+        __syncwarp();
+    } else {   // ---------------------------------------------------- sums and results
+        tc::reg_inc<kFfEpi>();
+        const int quarter = warp & 3, half = (warp - 4) >> 2;   // TMEM lanes 32 quarter ..; which half of the columns
+        const uint32_t tl = (uint32_t)(quarter * 32) << 16, stage = sbase + C::OUT0 + (warp - 4) * 4096;
+        bool ok = true, stored = false;
+        int chunk = 0;
+        FfUnit u;
+        // column of a tile at which the thread's j-th block of 32 lies (forward: gate, gate, up, up)
+        auto column = [&](int j) { return MODE == FfMode::FWD ? (j >> 1) * 128 + half * 64 + (j & 1) * 32 : half * 128 + j * 32; };
+        for (int i = 0; ok && units.get(i, u); ++i) {
+            float acc[128];
+#pragma unroll
+            for (int k = 0; k < 128; ++k) acc[k] = 0.f;
+            for (int c0 = u.k0; c0 < u.k1; c0 += p.depth, ++chunk) {
+                const int buf = chunk & 1;
+                if (!tc::warp_wait_cluster(&tfull[buf], (chunk >> 1) & 1, tc::kWaitLimit)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t v[16];
+                    tc::tmem_ld16(tmem_base + buf * 256 + column(j >> 1) + (j & 1) * 16 + tl, v);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) acc[16 * j + k] += __uint_as_float(v[k]);
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::arrive_at(tc::map_rank(&tempty[buf], 0));
+            }
+            if (!ok) break;
+            int tm, tn;
+            ff_tile(u.tile, p.tiles_m, p.tiles_n, tm, tn);
+            const int r = rank * 128 + quarter * 32;   // the warp's first row of the tile
+            if (u.slot >= 0) {   // a share: its sums
+                float *dst = p.partial + (int64_t)u.slot * kTileFloats + (r + lane) * 256;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        *reinterpret_cast<float4 *>(dst + column(j) + k) =
+                            make_float4(acc[32 * j + k], acc[32 * j + k + 1], acc[32 * j + k + 2], acc[32 * j + k + 3]);
+                continue;
+            }
+            const int64_t row0 = (int64_t)tm * 256 + r;
+            const int which = MODE == FfMode::DW && 2 * tn >= p.tiles_n;   // dWu
+            const int64_t col0 = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN;
+            if constexpr (!F32) {
+                // 64 columns of one result at a time, staged in the swizzle of its tensor map
+                constexpr int PIECES = MODE == FfMode::FWD ? 3 : 2;
+#pragma unroll
+                for (int x = 0; x < PIECES; ++x) {
+                    if (MODE == FfMode::FWD && x > 0 && !p.out[x]) break;
+                    const int64_t col = col0 + (MODE == FfMode::FWD ? half * 64 : half * 128 + x * 64);
+                    const int o = MODE == FfMode::FWD ? x : which;
+                    if (stored) tc::bulk_wait_read();   // (the lane that stored; others have nothing to wait for)
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        float y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int e = 8 * c + k;
+                            if (MODE != FfMode::FWD) y[k] = acc[64 * x + e];
+                            else if (x == 0) y[k] = ff_act<true>(acc[e], p.act) * acc[64 + e];
+                            else y[k] = acc[64 * (x - 1) + e];
+                        }
+                        const uint4 v = pack<__nv_bfloat16>(y);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(v.x),
+                                     "r"(v.y), "r"(v.z), "r"(v.w)
+                                     : "memory");
+                    }
+                    if (p.tma_out) {
+                        tc::fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0 && col < p.cols && row0 < p.rows) {
+                            tc::tma_store_2d(&p.to[o], (int)col, (int)row0, stage);
+                            tc::bulk_commit();
+                            stored = true;
+                        }
+                    } else {   // rows off 16 bytes: two elements a lane, a row at a time
+                        __syncwarp();
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out[o]);
+                        for (int q = 0; q < 32 && row0 + q < p.rows; ++q) {
+                            uint32_t v;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(stage + q * 128 + (((lane >> 2) ^ (q & 7)) << 4) + (lane & 3) * 4));
+                            unsigned short *d = reinterpret_cast<unsigned short *>(dst + (row0 + q) * p.cols + col + 2 * lane);
+                            if (col + 2 * lane < p.cols) d[0] = (unsigned short)v;
+                            if (col + 2 * lane + 1 < p.cols) d[1] = (unsigned short)(v >> 16);
+                        }
+                    }
+                }
+            } else {
+                const int64_t row = row0 + lane;
+                if (row < p.rows) {
+                    constexpr int PIECES = MODE == FfMode::FWD ? 3 : 1;
+#pragma unroll
+                    for (int x = 0; x < PIECES; ++x) {
+                        if (MODE == FfMode::FWD && x > 0 && !p.out[x]) break;
+                        float *dst = static_cast<float *>(p.out[MODE == FfMode::FWD ? x : which]) + row * p.cols;
+#pragma unroll
+                        for (int c = 0; c < (MODE == FfMode::FWD ? 64 : 128); c += 4) {
+                            const int64_t col = col0 + (MODE == FfMode::FWD ? half * 64 : half * 128) + c;
+                            float y[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (MODE != FfMode::FWD) y[k] = acc[c + k];
+                                else if (x == 0) y[k] = ff_act<false>(acc[c + k], p.act) * acc[64 + c + k];
+                                else y[k] = acc[64 * (x - 1) + c + k];
+                            }
+                            if (p.tma_out && col + 3 < p.cols) {   // (rows on 16 bytes)
+                                *reinterpret_cast<float4 *>(dst + col) = make_float4(y[0], y[1], y[2], y[3]);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (col + k < p.cols) dst[col + k] = y[k];
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        if (stored) tc::bulk_wait_all();
+        if (!ok && lane == 0) atomicOr(&g_ff_err, tc::kErrMmaTimeout);
+        tc::fence_before_sync();
+    }
+    __syncwarp();
+    tc::cluster_sync();   // nothing arrives at this CTA's barriers, or reads its operands, any more
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc_pair(tmem_base, 512);
+}
+
+// The shares of the tiles of the last round added in order, and their results; a
+// thread four columns of a row (forward: of the gate and of the up half).
+template <FfMode MODE, bool F32> __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ FfParams p) {
+    using C = FfCfg<MODE, F32>;
+    constexpr int Q = C::BN / 4;   // threads of a row
+    wait_previous();
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(id % Q) * 4, r = (int)(id / Q % 256), t = (int)(id / Q / 256);
+    const int tiles = p.tiles_m * p.tiles_n;
+    if (t >= tiles - p.whole) return;
+    // the pairs whose shares hold k-blocks of the tile
+    const int64_t all = (int64_t)(tiles - p.whole) * p.kb, b = (int64_t)t * p.kb, e = b + p.kb;
+    float y[2][4] = {};
+    for (int pair = (int)(b * p.pairs / all); pair < p.pairs; ++pair) {
+        const int64_t pb = all * pair / p.pairs, pe = all * (pair + 1) / p.pairs;
+        if (pb >= e) break;
+        if (pe <= b || pb == pe) continue;
+        // the share's own units are counted from its first tile
+        const int slot = 2 * pair + (t - (int)(pb / p.kb));
+        const float *src = p.partial + (int64_t)slot * kTileFloats + r * 256 + c;
+#pragma unroll
+        for (int h = 0; h < (MODE == FfMode::FWD ? 2 : 1); ++h) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + 128 * h);
+            y[h][0] += v.x;
+            y[h][1] += v.y;
+            y[h][2] += v.z;
+            y[h][3] += v.w;
+        }
+    }
+    int tm, tn;
+    ff_tile(p.whole + t, p.tiles_m, p.tiles_n, tm, tn);
+    const int which = MODE == FfMode::DW && 2 * tn >= p.tiles_n;
+    const int64_t row = (int64_t)tm * 256 + r, col = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN + c;
+    if (row >= p.rows) return;
+    using T = std::conditional_t<F32, float, __nv_bfloat16>;
+    auto store = [&](void *base, const float *x) {
+        T *dst = static_cast<T *>(base) + row * p.cols + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (col + k < p.cols) dst[k] = from_f32<T>(x[k]);
+    };
+    if (MODE == FfMode::FWD) {
+        float o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = ff_act<!F32>(y[0][k], p.act) * y[1][k];
+        store(p.out[0], o);
+        if (p.out[1]) store(p.out[1], y[0]);
+        if (p.out[2]) store(p.out[2], y[1]);
+    } else {
+        store(p.out[which], y[0]);
+    }
+}
+
+struct FfPlan {
+    int64_t tiles_m, tiles_n, kb, kb_seg, tiles;
+    int pairs, whole;
+    bool split;
+};
+template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32) {
+    FfPlan q{};
+    auto div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    if (MODE == FfMode::FWD) {
+        q.tiles_m = div(T, 256);
+        q.tiles_n = div(M, 128);
+        q.kb = q.kb_seg = div(F, 64);
+    } else if (MODE == FfMode::DX) {
+        q.tiles_m = div(T, 256);
+        q.tiles_n = div(F, 256);
+        q.kb_seg = div(M, 64);
+        q.kb = 2 * q.kb_seg;
+    } else {
+        q.tiles_m = div(F, 256);
+        q.tiles_n = 2 * div(M, 256);
+        q.kb = q.kb_seg = div(T, 64);
+    }
+    q.tiles = q.tiles_m * q.tiles_n;
+    const int most = std::max(1, device_sms() / 2);
+    q.pairs = (int)std::min<int64_t>(most, q.tiles);
+    q.whole = (int)std::min<int64_t>(q.tiles, INT32_MAX);
+    const int64_t rest = q.tiles % most;
+    // sharing the last round takes its k-blocks from kb to about rest kb / pairs, at
+    // the cost of writing and reading the sums and a second launch, some 20 k-blocks
+    // (a k-block in fp32, six products of parts, counts as four)
+    const int64_t cost = f32 ? 5 : 20;
+    if (rest && q.kb - (rest * q.kb + most - 1) / most > cost) {
+        q.split = true;
+        q.pairs = most;
+        q.whole = (int)(q.tiles - rest);
+    }
+    return q;
+}
+
+}  // namespace
+
+template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, cudaStream_t s) {
+    using C = FfCfg<MODE, F32>;
+    static_assert(C::BYTES + 1024 + 256 <= 227 * 1024, "shared memory");
+    const FfPlan q = ff_plan<MODE>(a.T, a.F, a.M, F32);
+    FfParams p{};
+    cudaError_t e = cudaSuccess;
+    auto operand = [&](CUtensorMap (&maps)[3], const FfMatrix &m, bool mn) {
+        for (int i = 0; i < C::PARTS && e == cudaSuccess; ++i)
+            e = bf16_tensor_map(&maps[i], m.p + i * m.part_elems(), m.rows, m.cols, m.ld, 64, mn ? 64 : 128);
+    };
+    if (MODE == FfMode::FWD) {
+        operand(p.ta[0], a.x, false);
+        operand(p.tb[0], a.wg, true);
+        operand(p.tb[1], a.wu, true);
+        p.rows = a.T;
+        p.cols = a.M;
+        p.out[0] = a.out;
+        p.out[1] = a.g;
+        p.out[2] = a.u;
+    } else if (MODE == FfMode::DX) {
+        operand(p.ta[0], a.dg, false);
+        operand(p.ta[1], a.du, false);
+        operand(p.tb[0], a.wg, false);
+        operand(p.tb[1], a.wu, false);
+        p.rows = a.T;
+        p.cols = a.F;
+        p.out[0] = a.out;
+    } else {
+        operand(p.ta[0], a.x, true);
+        operand(p.tb[0], a.dg, true);
+        operand(p.tb[1], a.du, true);
+        p.rows = a.F;
+        p.cols = a.M;
+        p.out[0] = a.g;
+        p.out[1] = a.u;
+    }
+    p.tma_out = p.cols * (F32 ? 4 : 2) % 16 == 0;
+    if (!F32 && p.tma_out)
+        for (int i = 0; i < 3 && e == cudaSuccess; ++i)
+            if (p.out[i]) e = bf16_tensor_map(&p.to[i], static_cast<const __nv_bfloat16 *>(p.out[i]), p.rows, p.cols, p.cols, 64, 32);
+    if (e == cudaSuccess) e = allow_smem<ff_gemm_kernel<MODE, F32>>(C::BYTES + 1024);
+    if (e != cudaSuccess) return e;
+    p.partial = a.partial;
+    p.tiles_m = (int)q.tiles_m;
+    p.tiles_n = (int)q.tiles_n;
+    p.kb = (int)q.kb;
+    p.kb_seg = (int)q.kb_seg;
+    p.depth = F32 ? 1 : 256;   // bf16: sums of 16384 products drop at most 2^-14 of their size on the way
+    p.pairs = q.pairs;
+    p.whole = q.whole;
+    p.act = a.act;
+    const sga_kernel_id id = MODE == FfMode::FWD ? SGA_KERN_FF_FWD : MODE == FfMode::DX ? SGA_KERN_FF_DX : SGA_KERN_FF_DW;
+    note_launch(id, s, false);
+    e = launch_early(ff_gemm_kernel<MODE, F32>, dim3(2 * (unsigned)q.pairs), dim3(kFfThreads), C::BYTES + 1024, s, p);
+    note_launch(id, s, true);
+    if (e != cudaSuccess || !q.split) return e;
+    const int64_t threads = (q.tiles - q.whole) * 256 * (C::BN / 4);
+    note_launch(SGA_KERN_FF_JOIN, s, false);
+    e = launch_early(ff_join_kernel<MODE, F32>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+    note_launch(SGA_KERN_FF_JOIN, s, true);
+    return e;
+}
+
+}  // namespace sga

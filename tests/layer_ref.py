@@ -171,3 +171,60 @@ def window_reference(seq_ptr, Q, K, V, scale, causal, window, sinks, dOut=None, 
         for x, xb in ((dQ, dQb), (dK, dKb), (dV, dVb)):
             xb += last * (x.abs() + xb) + 1e-30
     return res
+
+
+def _act(g, act):
+    """act(g), its derivative, the size of the derivative's terms, and the kernels' relative error of an evaluation (fp32
+    exponential or erfc: a few units, and as many more as their argument is large)."""
+    if act == "silu":
+        s = torch.sigmoid(g)
+        return g * s, s * (1 + g * (1 - s)), s + (g * s * (1 - s)).abs(), (16 + 4 * g.abs()) * U
+    if act == "gelu":
+        p, f = 0.5 * torch.special.erfc(-g * math.sqrt(0.5)), g * torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+        return g * p, p + f, p + f.abs(), (16 + 4 * g.abs() + 2 * g * g) * U
+    on = (g > 0).double()
+    return torch.relu(g), on, on, torch.zeros_like(g)
+
+
+def _product(a, ab, b, bb, dt, n):
+    """a b and its bound from the operands'.  A sum of n products on the tensor cores: every addition drops at most 2 U of
+    what has been summed (bf16: in runs of 16384; fp32: in runs of 64, of products of parts that leave out 2 U), and the
+    runs' fp32 sums."""
+    run = 64 if dt == torch.float32 else 16384
+    k = 2 * (min(n, run) + 8) + n / run + 4
+    mag = a.abs() @ b.abs()
+    return a @ b, k * U * mag + ab @ b.abs() + a.abs() @ bb + ab @ bb
+
+
+def ff_reference(X, Wg, Wu, act):
+    """{out, G, U: (value, bound)}."""
+    dt, last = X.dtype, ROUND[X.dtype]
+    x, wg, wu = X.double().reshape(-1, X.shape[-1]), Wg.double(), Wu.double()
+    z = torch.zeros_like
+    g, gb = _product(x, z(x), wg, z(wg), dt, x.shape[1])
+    u, ub = _product(x, z(x), wu, z(wu), dt, x.shape[1])
+    a, _, _, rel = _act(g, act)
+    ab = 1.2 * gb + rel * a.abs() + 1e-37     # (|act'| < 1.13; 1e-37: results below the normal range)
+    out = a * u
+    ob = ab * (u.abs() + ub) + a.abs() * ub + 2 * U * out.abs()
+    fin = lambda v, b: (v.reshape(*X.shape[:-1], -1), (b + last * (v.abs() + b) + 1e-37).reshape(*X.shape[:-1], -1))
+    return {"out": fin(out, ob), "G": fin(g, gb), "U": fin(u, ub)}
+
+
+def ff_bwd_reference(X, Wg, Wu, G, Up, dOut, act):
+    """{dX, dWg, dWu: (value, bound)} at the given G and U."""
+    dt, last, R = X.dtype, ROUND[X.dtype], LOW[X.dtype]
+    flat = lambda t: t.double().reshape(-1, t.shape[-1])
+    x, wg, wu, g, u, do = flat(X), Wg.double(), Wu.double(), flat(G), flat(Up), flat(dOut)
+    z = torch.zeros_like
+    a, slope, terms, rel = _act(g, act)
+    dg, du = do * u * slope, do * a
+    dgb = (do * u).abs() * (rel + 4 * U) * terms + (3 * U + R) * dg.abs() + 1e-37
+    dub = do.abs() * rel * a.abs() + (3 * U + R) * du.abs() + 1e-37
+    M = wg.shape[1]
+    dx, dxb = _product(torch.cat([dg, du], 1), torch.cat([dgb, dub], 1), torch.cat([wg, wu], 1).T, z(torch.cat([wg, wu], 1).T), dt, 2 * M)
+    n = x.shape[0]
+    dwg, dwgb = _product(x.T, z(x.T), dg, dgb, dt, n)
+    dwu, dwub = _product(x.T, z(x.T), du, dub, dt, n)
+    fin = lambda v, b, s: (v.reshape(s), (b + last * (v.abs() + b) + 1e-37).reshape(s))
+    return {"dX": fin(dx, dxb, X.shape), "dWg": fin(dwg, dwgb, Wg.shape), "dWu": fin(dwu, dwub, Wu.shape)}

@@ -77,3 +77,26 @@ def test_windowed_plan_arguments():
     for window, sinks in ((0, 0), (-3, 0), (None, 2), (4, -1)):
         with pytest.raises(ValueError, match="window|sinks"):
             sga.SeqPlan(sp, 1, 32, window=window, sinks=sinks)
+
+
+def test_gated_ff_arguments():
+    lib = sga.load_library()
+    fwd = lambda X=P, T=4, F=16, M=24, act=0, dt=1, o=P, G=P, U=P, ws=P, n=1 << 40: \
+        lib.gated_ff_fwd(X, P, P, T, F, M, act, dt, o, G, U, ws, n, None)
+    assert fwd(T=0) == sga.SGA_OK
+    for bad in (dict(X=None), dict(X=ODD), dict(T=-1), dict(F=0), dict(M=0), dict(act=3), dict(act=-1), dict(o=None), dict(o=ODD), dict(G=None),
+                dict(U=None), dict(G=ODD), dict(F=15, ws=None), dict(F=15, ws=ODD)):
+        assert fwd(**bad) == sga.SGA_EINVAL, bad
+    for bad in (dict(dt=2), dict(T=1 << 31), dict(F=(1 << 20) + 1), dict(M=(1 << 20) + 1), dict(T=(1 << 31) - 2000, M=1 << 20)):
+        assert fwd(**bad) == sga.SGA_EUNSUPPORTED, bad
+    assert fwd(F=15, n=0) == fwd(dt=0, n=0) == sga.SGA_EWORKSPACE
+    bwd = lambda G=P, dt=1, dX=P, dWg=P, dWu=P, ws=P, n=1 << 40, act=0: lib.gated_ff_bwd(P, P, P, G, P, P, 4, 16, 24, act, dt, dX, dWg, dWu, ws, n, None)
+    for bad in (dict(G=None), dict(G=ODD), dict(dX=ODD), dict(dWg=None), dict(dWu=None), dict(dWu=ODD), dict(ws=None), dict(ws=ODD), dict(act=9)):
+        assert bwd(**bad) == sga.SGA_EINVAL, bad
+    assert bwd(n=0) == sga.SGA_EWORKSPACE
+    assert bwd(dX=None, dWg=None, dWu=None) == sga.SGA_OK
+    assert lib.sga_gated_ff_fwd_workspace_bytes(0, 16, 24, 1) == lib.sga_gated_ff_bwd_workspace_bytes(4, 0, 24, 1) == 0
+    assert lib.sga_gated_ff_bwd_workspace_bytes(4, 16, 24, 0) >= 4 * 24 * 2 * 6
+    assert lib.sga_gated_ff_read_device_error(None, None) == sga.SGA_EINVAL
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        sga.gated_ff_fwd(torch.zeros(2, 16), torch.zeros(16, 8), torch.zeros(16, 8))
