@@ -176,7 +176,8 @@ def _own(st):
     if op == "win_fwd":
         return sga.seq_attn_fwd(st["plan"], st["Q"], st["K"], st["V"])
     if op == "win_bwd":
-        return sga.seq_attn_bwd(st["plan"], st["Q"], st["K"], st["V"], st["out"], st["lse"], st["dOut"])
+        # (the plain form's out and lse of a single block of rows are views)
+        return sga.seq_attn_bwd(st["plan"], st["Q"], st["K"], st["V"], st["out"].contiguous(), st["lse"].contiguous(), st["dOut"])
     if op == "ff_fwd":
         return sga.gated_ff_fwd(st["X"], st["Wg"], st["Wu"], act=st["act"])
     return sga.gated_ff_bwd(st["X"], st["Wg"], st["Wu"], st["G"], st["U"], st["dOut"], act=st["act"])
