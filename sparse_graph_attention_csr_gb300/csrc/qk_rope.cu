@@ -7,10 +7,14 @@
 //     dx = r (g - xhat sum(g xhat) / D),  dw = sum over rows and heads of dn xhat
 //
 // Bound by DRAM: the forward reads and writes Q and K once, the backward reads
-// them and their gradients and writes one gradient.  A head is held by D / (2 EL)
-// lanes, each with two 16-byte chunks that hold both elements of its pairs, so a
-// rotation needs no exchange.  A block takes a few rows: the cosines and sines of
-// their pairs are formed once, in shared memory, and serve all heads of a row.
+// them and their gradients and writes one gradient.  A row belongs to a group of D /
+// (2 EL) lanes, which take its heads one after the other: a lane holds two 16-byte
+// chunks of a head with both elements of its pairs, so a rotation needs no exchange,
+// and the cosines and sines of its pairs, formed once a row, and its columns'
+// weights stay in registers.  (With a block's rows and heads dealt to its groups,
+// turns and weights through shared memory, instructions bound it: 69636 rows of
+// 16/4 heads of 128 bf16 216 us forward, 255 backward.)  Where rows are few their
+// heads are dealt to several groups.
 //
 // Angles: a frequency is kept as turns a position in units of 2^-64, so that
 // position x frequency, a product of integers that wraps, is the exact fraction of
@@ -22,6 +26,7 @@
 // bitwise reproducible.  Statistics and sums are fp32.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -39,7 +44,7 @@ sga_status status_of(cudaError_t e) {
     return SGA_ECUDA;
 }
 
-constexpr int kThreads = 256, kMaxRows = 32;   // of a block
+constexpr int kThreads = 128;   // of a block
 
 struct RopeArgs {
     sga_rotary rot;
@@ -49,216 +54,226 @@ struct RopeArgs {
     const float *rq_in, *rk_in;
     float *part;             // [blocks][2][D] sums of dwq, dwk, or null
     int64_t T, ldq, ldk;     // rows; elements from a row of Q, K to the next
-    int H, Hkv, rows;        // heads; rows a block takes at a time
+    int H, Hkv;
+    int per, parts, qparts;  // heads a group takes at a time (0: all of a row's); shares of a row, those of its queries
     float eps;
     int wide;                // 64-bit positions
 };
 
 template <typename T> __device__ __forceinline__ uint4 load16(const T *p) { return *reinterpret_cast<const uint4 *>(p); }
 
-// Where a lane's two chunks of EL elements lie in a head, and which pair its
-// e-th element (of EL) belongs to.
-//   halves: pair i is elements (i, i + rot / 2); a lane's chunks are that far
-//     apart, so its e-th pair is (x0[e], x1[e]); chunks past the rotated ones
-//     follow by twos.
-//   interleaved: pair i is elements (2 i, 2 i + 1); the chunks are half a head
-//     apart, pairs e < EL / 2 in the first.
-template <int D, int EL> struct Lane {
-    int c0, c1, pair;    // chunks; halves: the first pair, or -1 (nothing rotated)
-    __device__ __forceinline__ Lane(const sga_rotary &r, int lane) {
-        constexpr int G = D / (2 * EL);
-        const int half = r.rot / (2 * EL);   // (halves: lanes with a rotated chunk)
-        if (r.interleaved) {
-            c0 = lane;
-            c1 = lane + G;
-            pair = lane * EL / 2;
-        } else if (lane < half) {
-            c0 = lane;
-            c1 = lane + half;
-            pair = lane * EL;
-        } else {
-            c0 = 2 * lane;   // (2 half + 2 (lane - half))
-            c1 = c0 + 1;
-            pair = -1;
+// A lane's 2 EL elements of a head as the first (a) and second (b) elements of its
+// EL pairs.
+//   halves: pair i is elements (i, i + rot / 2); the lane's chunks are that far apart,
+//     a one, b the other; chunks past the rotated ones follow by twos.
+//   interleaved: pair i is elements (2 i, 2 i + 1); the chunks are half a head apart,
+//     a their even elements, b their odd ones.
+template <typename T, int D, bool INTER> struct Lane {
+    static constexpr int EL = Elt<T>::EL, G = D / (2 * EL);
+    int c0, c1;   // chunks (offsets in elements)
+    int lane, rot;
+    __device__ __forceinline__ Lane(const sga_rotary &r, int l) : lane(l), rot(r.rot) {
+        const int half = r.rot / (2 * EL);
+        c0 = EL * (INTER || lane < half ? lane : 2 * lane);   // (2 half + 2 (lane - half))
+        c1 = INTER ? c0 + EL * G : lane < half ? c0 + EL * half : c0 + EL;
+    }
+    // the pair that the lane's e-th is (of those that turn), or past rot / 2
+    __device__ __forceinline__ int pair(int e) const {
+        if (INTER) return e < EL / 2 ? lane * (EL / 2) + e : (lane + G) * (EL / 2) + e - EL / 2;
+        return lane * EL + e;
+    }
+    __device__ __forceinline__ static void split(const uint4 &x, const uint4 &y, float *a, float *b) {
+        float t[2 * EL];
+        unpack<T>(x, t);
+        unpack<T>(y, t + EL);
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            a[e] = t[INTER ? 2 * e : e];
+            b[e] = t[INTER ? 2 * e + 1 : EL + e];
+        }
+    }
+    __device__ __forceinline__ void load(const T *head, uint4 *raw) const {
+        raw[0] = load16(head + c0);
+        raw[1] = load16(head + c1);
+    }
+    __device__ __forceinline__ void store(T *head, const float *a, const float *b) const {
+        float t[2 * EL];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            t[INTER ? 2 * e : e] = a[e];
+            t[INTER ? 2 * e + 1 : EL + e] = b[e];
+        }
+        *reinterpret_cast<uint4 *>(head + c0) = pack<T>(t);
+        *reinterpret_cast<uint4 *>(head + c1) = pack<T>(t + EL);
+    }
+    // where element i of (a, b) lies in a head
+    __device__ __forceinline__ int column(bool second, int e) const {
+        const int i = INTER ? 2 * e + second : e;
+        return (INTER ? i < EL : !second) ? c0 + i : c1 + (INTER ? i - EL : i);
+    }
+    // the weights of the lane's columns, ones without
+    template <typename TW> __device__ __forceinline__ void weights(const TW *w, float *a, float *b) const {
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            a[e] = w ? to_f32<TW>(w[column(false, e)]) : 1.f;
+            b[e] = w ? to_f32<TW>(w[column(true, e)]) : 1.f;
+        }
+    }
+    // cosines and sines of the row's angles; pairs that do not turn: 1 and 0
+    __device__ __forceinline__ void turns(const RopeArgs &a, int64_t row, float *c, float *s) const {
+        const sga_rotary &r = a.rot;
+        int64_t p = 0;
+        int axis = -1;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+            const int i = pair(e);
+            c[e] = 1.f;
+            s[e] = 0.f;
+            if (2 * i >= rot) continue;
+            if (r.axis[i] != axis) {
+                axis = r.axis[i];
+                const int64_t at = row * r.axes + axis;
+                p = a.wide ? (int64_t)__ldg(static_cast<const long long *>(a.pos) + at) : (int64_t)__ldg(static_cast<const int *>(a.pos) + at);
+            }
+            // half turns in [-1, 1): the top 32 bits, rounded
+            const uint64_t turn = (uint64_t)p * r.turn[i];
+            sincospif((float)(int32_t)(uint32_t)((turn + 0x80000000ull) >> 32) * 0x1p-31f, s + e, c + e);
+        }
+    }
+    // (a, b) turned (BACK: by the negative angles).  What does not turn stays bit for
+    // bit (0 times an infinity would not).
+    template <bool BACK> __device__ __forceinline__ void turn(float *a, float *b, const float *c, const float *s) const {
+#pragma unroll
+        for (int e = 0; e < EL; e += 2) {
+            const float2 u = make_float2(a[e], a[e + 1]), v = make_float2(b[e], b[e + 1]), cc = make_float2(c[e], c[e + 1]),
+                         ss = make_float2(s[e], s[e + 1]), ns = make_float2(-s[e], -s[e + 1]);
+            const float2 x = ffma2(v, BACK ? ss : ns, fmul2(u, cc)), y = ffma2(u, BACK ? ns : ss, fmul2(v, cc));
+            if (2 * pair(e) < rot) {
+                a[e] = x.x;
+                b[e] = y.x;
+            }
+            if (2 * pair(e + 1) < rot) {
+                a[e + 1] = x.y;
+                b[e + 1] = y.y;
+            }
         }
     }
 };
 
-// cos, sin of the angles of a block's rows: [row][e / 2][lane] as float4 (two
-// pairs).  Pairs past the rotated ones turn by nothing.
-template <int D, int EL>
-__device__ __forceinline__ void fill_turns(const RopeArgs &a, float4 *cs, int64_t t0, int rows) {
-    constexpr int G = D / (2 * EL), P = D / 2;
-    const sga_rotary &r = a.rot;
-    for (int i = threadIdx.x; i < rows * P; i += kThreads) {
-        const int row = i / P, e = i % P / G, lane = i % G;
-        int pair;
-        if (r.interleaved) pair = e < EL / 2 ? lane * (EL / 2) + e : (lane + G) * (EL / 2) + e - EL / 2;
-        else pair = lane * EL + e;
-        float s = 0.f, c = 1.f;
-        if (2 * pair < r.rot) {
-            const int64_t at = (t0 + row) * r.axes + r.axis[pair];
-            const int64_t p = a.wide ? __ldg(static_cast<const long long *>(a.pos) + at)
-                                     : (int64_t)__ldg(static_cast<const int *>(a.pos) + at);
-            const uint64_t turn = (uint64_t)p * r.turn[pair];
-            // half turns in [-1, 1): the top 32 bits, rounded
-            const float x = (float)(int32_t)(uint32_t)((turn + 0x80000000ull) >> 32) * 0x1p-31f;
-            sincospif(x, &s, &c);
-        }
-        reinterpret_cast<float2 *>(cs + (row * (EL / 2) + e / 2) * G + lane)[e & 1] = make_float2(c, s);
-    }
-}
-
-// Turns the lane's pairs (back: by the negative angles).
-template <int EL, int G, bool BACK>
-__device__ __forceinline__ void turn_pairs(const RopeArgs &a, float *x0, float *x1, const float4 *cs, int pair) {
-    if (!a.rot.interleaved && pair < 0) return;   // (x0 and x1 belong to no pair)
+template <int EL> __device__ __forceinline__ void mul(float *x, const float *y) {
 #pragma unroll
     for (int e = 0; e < EL; e += 2) {
-        const float4 t = cs[(e / 2) * G];
-        float *u, *v;
-        if (!a.rot.interleaved) {
-            const float u0 = x0[e], v0 = x1[e], u1 = x0[e + 1], v1 = x1[e + 1];
-            const float s0 = BACK ? -t.y : t.y, s1 = BACK ? -t.w : t.w;
-            x0[e] = u0 * t.x - v0 * s0;
-            x1[e] = u0 * s0 + v0 * t.x;
-            x0[e + 1] = u1 * t.z - v1 * s1;
-            x1[e + 1] = u1 * s1 + v1 * t.z;
-        } else {   // pairs e, e + 1: elements 2 e .. 2 e + 3 of the lane's 2 EL
-            u = 2 * e < EL ? x0 + 2 * e : x1 + 2 * e - EL;
-            v = u + 1;
-            const int p = e < EL / 2 ? pair + e : pair + e + (G - 1) * (EL / 2);
-            const float s0 = BACK ? -t.y : t.y, s1 = BACK ? -t.w : t.w;
-            const float u0 = u[0], v0 = v[0], u1 = u[2], v1 = v[2];
-            if (2 * p < a.rot.rot) {
-                u[0] = u0 * t.x - v0 * s0;
-                v[0] = u0 * s0 + v0 * t.x;
-            }
-            if (2 * (p + 1) < a.rot.rot) {
-                u[2] = u1 * t.z - v1 * s1;
-                v[2] = u1 * s1 + v1 * t.z;
-            }
-        }
+        const float2 t = fmul2(make_float2(x[e], x[e + 1]), make_float2(y[e], y[e + 1]));
+        x[e] = t.x;
+        x[e + 1] = t.y;
     }
 }
-
-// The weights as fp32: [2][D], ones where there are none.
-template <typename TW, int D> __device__ __forceinline__ void fill_weights(const RopeArgs &a, float *w) {
-    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-        const TW *src = static_cast<const TW *>(i < D ? a.wq : a.wk);
-        w[i] = src ? to_f32<TW>(src[i % D]) : 1.f;
-    }
-}
-
-template <int EL> __device__ __forceinline__ void load_f32(const float *p, float *x) {
+template <int EL> __device__ __forceinline__ void mul(float *x, float y) {
 #pragma unroll
-    for (int i = 0; i < EL; i += 4) {
-        const float4 q = *reinterpret_cast<const float4 *>(p + i);
-        x[i] = q.x;
-        x[i + 1] = q.y;
-        x[i + 2] = q.z;
-        x[i + 3] = q.w;
+    for (int e = 0; e < EL; e += 2) {
+        const float2 t = fmul2(make_float2(x[e], x[e + 1]), make_float2(y, y));
+        x[e] = t.x;
+        x[e + 1] = t.y;
     }
 }
 
-// Item `it` of a block: a head (queries' first, then keys') of one of its rows.
-struct Item {
-    int row, head;
-    bool key;
-    __device__ __forceinline__ Item(const RopeArgs &a, int it) {
-        const int heads = a.H + a.Hkv;
-        row = it / heads;
-        head = it - row * heads;
-        key = head >= a.H;
-        if (key) head -= a.H;
+// A group's share of a row: all of its heads, or `per` of its queries' or keys'.
+struct Share {
+    int64_t row;
+    bool in;
+    int part;
+    __device__ __forceinline__ Share(const RopeArgs &a, int64_t u) {
+        row = a.per ? u / a.parts : u;
+        part = a.per ? (int)(u - row * a.parts) : 0;
+        in = row < a.T;
     }
 };
-
-template <typename T, typename TW, int D> __global__ void __launch_bounds__(kThreads) qk_rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int EL = Elt<T>::EL, G = D / (2 * EL), GROUPS = kThreads / G, U = 2;
-    extern __shared__ float4 cs[];   // [rows][EL / 2][G]
-    __shared__ __align__(16) float w[2 * D];
-    let_next_start();
-    wait_previous();
-    fill_weights<TW, D>(a, w);
-    const int lane = threadIdx.x % G, grp = threadIdx.x / G;
-    const Lane<D, EL> at(a.rot, lane);
-    const bool norm = a.rq != nullptr;
-    for (int64_t t0 = (int64_t)blockIdx.x * a.rows; t0 < a.T; t0 += (int64_t)gridDim.x * a.rows) {
-        const int rows = (int)min((int64_t)a.rows, a.T - t0), items = rows * (a.H + a.Hkv);
-        uint4 x[U][2];
-        auto fetch = [&](int it0) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int it = it0 + u * GROUPS;
-                x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-                if (it < items) {
-                    const Item m(a, it);
-                    const T *src = static_cast<const T *>(m.key ? a.K : a.Q) + (t0 + m.row) * (m.key ? a.ldk : a.ldq) + m.head * D;
-                    x[u][0] = load16(src + at.c0 * EL);
-                    x[u][1] = load16(src + at.c1 * EL);
-                }
-            }
-        };
-        fetch(grp);
-        __syncthreads();   // the rows before are done with cs
-        fill_turns<D, EL>(a, cs, t0, rows);
-        __syncthreads();
-        // every group of a warp runs the same number of rounds: the sums are warp-wide calls
-        for (int i0 = 0; i0 < items; i0 += U * GROUPS) {
-            float y[U][2 * EL];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                unpack<T>(x[u][0], y[u]);
-                unpack<T>(x[u][1], y[u] + EL);
-            }
-            fetch(i0 + U * GROUPS + grp);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int it = i0 + u * GROUPS + grp;
-                const Item m(a, it);
-                if (norm) {
-                    float s = 0.f, wr[2 * EL];
-#pragma unroll
-                    for (int i = 0; i < 2 * EL; ++i) s = fmaf(y[u][i], y[u][i], s);
-                    const float r = rsqrtf(group_sum<G>(s) * (1.f / D) + a.eps);
-                    load_f32<EL>(w + m.key * D + at.c0 * EL, wr);
-                    load_f32<EL>(w + m.key * D + at.c1 * EL, wr + EL);
-#pragma unroll
-                    for (int i = 0; i < 2 * EL; ++i) y[u][i] *= r * wr[i];
-                    if (lane == 0 && it < items) {
-                        if (m.key) a.rk[(t0 + m.row) * a.Hkv + m.head] = r;
-                        else a.rq[(t0 + m.row) * a.H + m.head] = r;
-                    }
-                }
-                if (it < items) {
-                    turn_pairs<EL, G, false>(a, y[u], y[u] + EL, cs + m.row * (EL / 2) * G + lane, at.pair);
-                    T *dst = static_cast<T *>(m.key ? a.Ko : a.Qo) + ((t0 + m.row) * (m.key ? a.Hkv : a.H) + m.head) * D;
-                    *reinterpret_cast<uint4 *>(dst + at.c0 * EL) = pack<T>(y[u]);
-                    *reinterpret_cast<uint4 *>(dst + at.c1 * EL) = pack<T>(y[u] + EL);
-                }
-            }
-        }
+// Calls phase(keys, first head, end, steps): the steps are the same in all groups of
+// a warp, whose sums are warp-wide calls.
+template <typename F> __device__ __forceinline__ void each_phase(const RopeArgs &a, const Share &s, F phase) {
+    if (a.per == 0) {
+        phase(false, 0, s.in ? a.H : 0, a.H);
+        phase(true, 0, s.in ? a.Hkv : 0, a.Hkv);
+    } else {
+        const bool key = s.part >= a.qparts;
+        const int h0 = (key ? s.part - a.qparts : s.part) * a.per;
+        phase(key, h0, s.in ? min(key ? a.Hkv : a.H, h0 + a.per) : h0, a.per);
     }
 }
 
-// A block's sums of one weight's gradient: its groups added in order.
-template <int D, int EL, int G>
-__device__ __forceinline__ void block_sums(float *sm, const float *acc, const Lane<D, EL> &at, float *out) {
-    const int grp = threadIdx.x / G;
-    // the groups of a warp first (lanes G apart), then the warps
-    float s[2 * EL];
+template <typename T, typename TW, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads) qk_rope_fwd_kernel(const __grid_constant__ RopeArgs a) {
+    using L = Lane<T, D, INTER>;
+    constexpr int EL = L::EL, G = L::G, U = 4;
+    let_next_start();
+    wait_previous();
+    const L at(a.rot, threadIdx.x % G);
+    const bool norm = a.rq != nullptr;
+    const int64_t units = a.T * a.parts, step = (int64_t)gridDim.x * (kThreads / G);
+    // (whole warps: a group past the last row takes part in the sums)
+    for (int64_t u0 = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / 32 * (32 / G); u0 < units; u0 += step) {
+        const Share sh(a, u0 + threadIdx.x % 32 / G);
+        float c[EL], s[EL];
+        bool turned = false;
+        each_phase(a, sh, [&](bool key, int h0, int h1, int steps) {
+            const T *src = static_cast<const T *>(key ? a.K : a.Q) + (sh.in ? sh.row : 0) * (key ? a.ldk : a.ldq) + h0 * D;
+            T *dst = static_cast<T *>(key ? a.Ko : a.Qo) + ((sh.in ? sh.row : 0) * (key ? a.Hkv : a.H) + h0) * D;
+            float *r = norm ? (key ? a.rk : a.rq) + (sh.in ? sh.row : 0) * (key ? a.Hkv : a.H) + h0 : nullptr;
+            const int n = h1 - h0;
+            uint4 x[U][2];
+            auto fetch = [&](int u, int i) {
+                x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+                if (i < n) at.load(src + i * D, x[u]);
+            };
+#pragma unroll
+            for (int u = 0; u < U; ++u) fetch(u, u);
+            float wa[EL], wb[EL];
+            at.template weights<TW>(static_cast<const TW *>(key ? a.wk : a.wq), wa, wb);
+            if (!turned && sh.in) at.turns(a, sh.row, c, s);   // (while the first heads arrive)
+            turned = true;
+            for (int i0 = 0; i0 < steps; i0 += U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u;
+                    float ya[EL], yb[EL];
+                    L::split(x[u][0], x[u][1], ya, yb);
+                    fetch(u, i + U);
+                    if (norm) {
+                        float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < EL; e += 2) {
+                            const float2 va = make_float2(ya[e], ya[e + 1]), vb = make_float2(yb[e], yb[e + 1]);
+                            q = ffma2(vb, vb, ffma2(va, va, q));
+                        }
+                        const float inv = rsqrtf(group_sum<G>(q.x + q.y) * (1.f / D) + a.eps);
+                        mul<EL>(ya, inv);
+                        mul<EL>(yb, inv);
+                        mul<EL>(ya, wa);
+                        mul<EL>(yb, wb);
+                        if (at.lane == 0 && i < n) r[i] = inv;
+                    }
+                    if (i < n) {
+                        at.template turn<false>(ya, yb, c, s);
+                        at.store(dst + i * D, ya, yb);
+                    }
+                }
+            }
+        });
+    }
+}
+
+// A block's sums of one weight's gradient: the groups of a warp first (lanes G
+// apart), then the warps in order.
+template <typename L, int D> __device__ __forceinline__ void block_sums(float *sm, const float *sa, const float *sb, const L &at, float *out) {
+    constexpr int EL = L::EL, G = L::G;
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2 * EL; ++i) {
-        s[i] = acc[i];
+        float t = i < EL ? sa[i % EL] : sb[i % EL];
 #pragma unroll
-        for (int o = 16; o >= G; o >>= 1) s[i] += __shfl_xor_sync(SGA_FULL_MASK, s[i], o);
+        for (int o = 16; o >= G; o >>= 1) t += __shfl_xor_sync(SGA_FULL_MASK, t, o);
+        if (threadIdx.x % 32 < G) sm[threadIdx.x / 32 * D + at.column(i >= EL, i % EL)] = t;
     }
-    constexpr int PER = 32 / G;   // groups of a warp
-    __syncthreads();
-    if (grp % PER == 0)
-#pragma unroll
-        for (int i = 0; i < 2 * EL; ++i) sm[(threadIdx.x / 32) * D + (i < EL ? at.c0 * EL + i : at.c1 * EL + i - EL)] = s[i];
     __syncthreads();
     for (int i = threadIdx.x; i < D; i += kThreads) {
         float t = 0.f;
@@ -268,88 +283,105 @@ __device__ __forceinline__ void block_sums(float *sm, const float *acc, const La
     }
 }
 
-template <typename T, typename TW, int D> __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-    constexpr int EL = Elt<T>::EL, G = D / (2 * EL), GROUPS = kThreads / G;
-    extern __shared__ float4 cs[];   // [rows][EL / 2][G]
-    __shared__ __align__(16) float w[2 * D];
+template <typename T, typename TW, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+    using L = Lane<T, D, INTER>;
+    constexpr int EL = L::EL, G = L::G, U = 2;
     __shared__ float sums[kThreads / 32 * D];
     let_next_start();
     wait_previous();
-    fill_weights<TW, D>(a, w);
-    const int lane = threadIdx.x % G, grp = threadIdx.x / G;
-    const Lane<D, EL> at(a.rot, lane);
+    const L at(a.rot, threadIdx.x % G);
     const bool norm = a.rq_in != nullptr;
-    float aq[2 * EL], ak[2 * EL];   // this thread's sums of dwq, dwk
+    float qa[EL], qb[EL], ka[EL], kb[EL];   // this thread's sums of dwq, dwk
 #pragma unroll
-    for (int i = 0; i < 2 * EL; ++i) aq[i] = ak[i] = 0.f;
-    for (int64_t t0 = (int64_t)blockIdx.x * a.rows; t0 < a.T; t0 += (int64_t)gridDim.x * a.rows) {
-        const int rows = (int)min((int64_t)a.rows, a.T - t0), items = rows * (a.H + a.Hkv);
-        uint4 x[2], g[2];
-        float r_next = 0.f;
-        auto fetch = [&](int it) {
-            x[0] = x[1] = g[0] = g[1] = make_uint4(0, 0, 0, 0);
-            r_next = 0.f;
-            if (it < items) {
-                const Item m(a, it);
-                const T *src = static_cast<const T *>(m.key ? a.dKo : a.dQo) + ((t0 + m.row) * (m.key ? a.Hkv : a.H) + m.head) * D;
-                g[0] = load16(src + at.c0 * EL);
-                g[1] = load16(src + at.c1 * EL);
-                if (norm) {
-                    src = static_cast<const T *>(m.key ? a.K : a.Q) + (t0 + m.row) * (m.key ? a.ldk : a.ldq) + m.head * D;
-                    x[0] = load16(src + at.c0 * EL);
-                    x[1] = load16(src + at.c1 * EL);
-                    r_next = m.key ? a.rk_in[(t0 + m.row) * a.Hkv + m.head] : a.rq_in[(t0 + m.row) * a.H + m.head];
+    for (int e = 0; e < EL; ++e) qa[e] = qb[e] = ka[e] = kb[e] = 0.f;
+    const int64_t units = a.T * a.parts, step = (int64_t)gridDim.x * (kThreads / G);
+    for (int64_t u0 = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / 32 * (32 / G); u0 < units; u0 += step) {
+        const Share sh(a, u0 + threadIdx.x % 32 / G);
+        float c[EL], s[EL];
+        bool turned = false;
+        each_phase(a, sh, [&](bool key, int h0, int h1, int steps) {
+            const int64_t row = sh.in ? sh.row : 0, first = row * (key ? a.Hkv : a.H) + h0;
+            const T *src = static_cast<const T *>(key ? a.K : a.Q) + row * (key ? a.ldk : a.ldq) + h0 * D;
+            const T *grad = static_cast<const T *>(key ? a.dKo : a.dQo) + first * D;
+            const float *r = norm ? (key ? a.rk_in : a.rq_in) + first : nullptr;
+            T *dst = static_cast<T *>(key ? a.Ko : a.Qo) + first * D;
+            const int n = h1 - h0;
+            uint4 x[U][2], g[U][2];
+            float inv[U];
+            auto fetch = [&](int u, int i) {
+                x[u][0] = x[u][1] = g[u][0] = g[u][1] = make_uint4(0, 0, 0, 0);
+                inv[u] = 0.f;
+                if (i < n) {
+                    at.load(grad + i * D, g[u]);
+                    if (norm) {
+                        at.load(src + i * D, x[u]);
+                        inv[u] = r[i];
+                    }
+                }
+            };
+#pragma unroll
+            for (int u = 0; u < U; ++u) fetch(u, u);
+            float wa[EL], wb[EL];
+            at.template weights<TW>(static_cast<const TW *>(key ? a.wk : a.wq), wa, wb);
+            if (!turned && sh.in) at.turns(a, sh.row, c, s);
+            turned = true;
+            for (int i0 = 0; i0 < steps; i0 += U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u;
+                    float da[EL], db[EL];
+                    L::split(g[u][0], g[u][1], da, db);
+                    const uint4 x0 = x[u][0], x1 = x[u][1];
+                    const float rr = inv[u];
+                    fetch(u, i + U);
+                    if (i < n) at.template turn<true>(da, db, c, s);
+                    if (norm) {
+                        float xa[EL], xb[EL];
+                        L::split(x0, x1, xa, xb);
+                        mul<EL>(xa, rr);
+                        mul<EL>(xb, rr);
+                        auto add = [&](float *sa, float *sb) {
+#pragma unroll
+                            for (int e = 0; e < EL; e += 2) {
+                                const float2 y = ffma2(make_float2(da[e], da[e + 1]), make_float2(xa[e], xa[e + 1]), make_float2(sa[e], sa[e + 1]));
+                                const float2 z = ffma2(make_float2(db[e], db[e + 1]), make_float2(xb[e], xb[e + 1]), make_float2(sb[e], sb[e + 1]));
+                                sa[e] = y.x;
+                                sa[e + 1] = y.y;
+                                sb[e] = z.x;
+                                sb[e + 1] = z.y;
+                            }
+                        };
+                        if (key) add(ka, kb);
+                        else add(qa, qb);
+                        mul<EL>(da, wa);
+                        mul<EL>(db, wb);
+                        float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < EL; e += 2)
+                            q = ffma2(make_float2(db[e], db[e + 1]), make_float2(xb[e], xb[e + 1]),
+                                      ffma2(make_float2(da[e], da[e + 1]), make_float2(xa[e], xa[e + 1]), q));
+                        const float m = -group_sum<G>(q.x + q.y) * (1.f / D);
+                        const float2 mm = make_float2(m, m), ri = make_float2(rr, rr);
+#pragma unroll
+                        for (int e = 0; e < EL; e += 2) {
+                            const float2 y = fmul2(ri, ffma2(mm, make_float2(xa[e], xa[e + 1]), make_float2(da[e], da[e + 1])));
+                            const float2 z = fmul2(ri, ffma2(mm, make_float2(xb[e], xb[e + 1]), make_float2(db[e], db[e + 1])));
+                            da[e] = y.x;
+                            da[e + 1] = y.y;
+                            db[e] = z.x;
+                            db[e + 1] = z.y;
+                        }
+                    }
+                    if (i < n) at.store(dst + i * D, da, db);
                 }
             }
-        };
-        fetch(grp);
-        __syncthreads();
-        fill_turns<D, EL>(a, cs, t0, rows);
-        __syncthreads();
-        for (int i0 = 0; i0 < items; i0 += GROUPS) {
-            const int it = i0 + grp;
-            float xh[2 * EL], dn[2 * EL];
-            const float r = r_next;
-            unpack<T>(g[0], dn);
-            unpack<T>(g[1], dn + EL);
-            unpack<T>(x[0], xh);
-            unpack<T>(x[1], xh + EL);
-            fetch(it + GROUPS);
-            const Item m(a, it);
-            if (it < items) turn_pairs<EL, G, true>(a, dn, dn + EL, cs + m.row * (EL / 2) * G + lane, at.pair);
-            if (norm) {
-                float wr[2 * EL], s = 0.f;
-                load_f32<EL>(w + m.key * D + at.c0 * EL, wr);
-                load_f32<EL>(w + m.key * D + at.c1 * EL, wr + EL);
-#pragma unroll
-                for (int i = 0; i < 2 * EL; ++i) xh[i] *= r;
-                if (m.key) {
-#pragma unroll
-                    for (int i = 0; i < 2 * EL; ++i) ak[i] = fmaf(dn[i], xh[i], ak[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2 * EL; ++i) aq[i] = fmaf(dn[i], xh[i], aq[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 2 * EL; ++i) {
-                    dn[i] *= wr[i];
-                    s = fmaf(dn[i], xh[i], s);
-                }
-                s = group_sum<G>(s) * (1.f / D);
-#pragma unroll
-                for (int i = 0; i < 2 * EL; ++i) dn[i] = r * (dn[i] - xh[i] * s);
-            }
-            if (it < items) {
-                T *dst = static_cast<T *>(m.key ? a.Ko : a.Qo) + ((t0 + m.row) * (m.key ? a.Hkv : a.H) + m.head) * D;
-                *reinterpret_cast<uint4 *>(dst + at.c0 * EL) = pack<T>(dn);
-                *reinterpret_cast<uint4 *>(dst + at.c1 * EL) = pack<T>(dn + EL);
-            }
-        }
+        });
     }
     if (!a.part) return;
     float *out = a.part + (int64_t)blockIdx.x * 2 * D;
-    block_sums<D, EL, G>(sums, aq, at, out);
-    block_sums<D, EL, G>(sums, ak, at, out + D);
+    block_sums<L, D>(sums, qa, qb, at, out);
+    block_sums<L, D>(sums, ka, kb, at, out + D);
 }
 
 // dwq, dwk from the blocks' sums: 32 columns a block; its 32 warps take every
@@ -374,41 +406,46 @@ __global__ void __launch_bounds__(1024) qk_rope_reduce_kernel(const float *__res
     if (lane == 0) (c < D ? dwq : dwk)[c < D ? c : c - D] = from_f32<TW>(s);
 }
 
-constexpr int kBwdBlocksPerSm = 4;   // most of the backward pass, each with a row of sums
+constexpr int kBwdBlocksPerSm = 8;   // most of the backward pass, each with a row of sums
 
-// Rows a block takes at a time: enough heads for four rounds of its groups, but
-// no fewer blocks than SMs where there are rows for them.
-int rows_of(int64_t T, int heads, int groups) {
-    const int64_t want = (4 * groups + heads - 1) / heads, spread = std::max<int64_t>(1, T / device_sms());
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, spread), kMaxRows));
+// Deals a row's heads to several groups where one group a row would leave SMs
+// without work, four heads at least each (or all of a row's).
+void deal_heads(RopeArgs &a, int groups) {
+    const int64_t want = (int64_t)device_sms() * groups * 2;
+    a.per = 0;
+    a.parts = 1;
+    if (a.T >= want || a.H + a.Hkv <= 4) return;
+    const int64_t share = std::min<int64_t>((want + a.T - 1) / a.T, (a.H + a.Hkv + 3) / 4);   // shares of a row
+    a.per = (int)((a.H + a.Hkv + share - 1) / share);
+    a.qparts = (a.H + a.per - 1) / a.per;
+    a.parts = a.qparts + (a.Hkv + a.per - 1) / a.per;
 }
 
-template <typename T, typename TW, int D> cudaError_t launch_fwd(RopeArgs &a, cudaStream_t s) {
-    a.rows = rows_of(a.T, a.H + a.Hkv, kThreads / (D / (2 * Elt<T>::EL)));
-    const int64_t blocks = std::min<int64_t>((a.T + a.rows - 1) / a.rows, (int64_t)device_sms() * 64);
+template <typename T, typename TW, int D, bool INTER> cudaError_t launch_fwd(RopeArgs &a, cudaStream_t s) {
+    constexpr int groups = kThreads / Lane<T, D, INTER>::G;
+    deal_heads(a, groups);
+    const int64_t blocks = std::min<int64_t>((a.T * a.parts + groups - 1) / groups, (int64_t)device_sms() * 64);
     note_launch(SGA_KERN_QK_ROPE_FWD, s, false);
-    const cudaError_t e = launch_early(qk_rope_fwd_kernel<T, TW, D>, dim3((unsigned)blocks), dim3(kThreads),
-                                       (size_t)a.rows * D / 2 * sizeof(float2), s, a);
+    const cudaError_t e = launch_early(qk_rope_fwd_kernel<T, TW, D, INTER>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
     note_launch(SGA_KERN_QK_ROPE_FWD, s, true);
     return e;
 }
 
-template <typename T, typename TW, int D> cudaError_t launch_bwd(RopeArgs &a, void *dwq, void *dwk, cudaStream_t s) {
-    a.rows = rows_of(a.T, a.H + a.Hkv, kThreads / (D / (2 * Elt<T>::EL)));
+template <typename T, typename TW, int D, bool INTER> cudaError_t launch_bwd(RopeArgs &a, void *dwq, void *dwk, cudaStream_t s) {
+    constexpr int groups = kThreads / Lane<T, D, INTER>::G;
+    deal_heads(a, groups);
     // as many blocks as are resident at once
     static std::atomic<int> per_sm[kMaxDevices];
     cudaError_t asked = cudaSuccess;
     const int fit = per_device(per_sm, [&] {
         int n = 0;
-        asked = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, qk_rope_bwd_kernel<T, TW, D>, kThreads,
-                                                              kMaxRows * D / 2 * sizeof(float2));
+        asked = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, qk_rope_bwd_kernel<T, TW, D, INTER>, kThreads, 0);
         return asked == cudaSuccess ? std::max(1, std::min(n, kBwdBlocksPerSm)) : 0;
     });
     if (asked != cudaSuccess) return asked;
-    const int blocks = (int)std::min<int64_t>((a.T + a.rows - 1) / a.rows, (int64_t)device_sms() * fit);
+    const int blocks = (int)std::min<int64_t>((a.T * a.parts + groups - 1) / groups, (int64_t)device_sms() * fit);
     note_launch(SGA_KERN_QK_ROPE_BWD, s, false);
-    cudaError_t e = launch_early(qk_rope_bwd_kernel<T, TW, D>, dim3((unsigned)blocks), dim3(kThreads),
-                                 (size_t)a.rows * D / 2 * sizeof(float2), s, a);
+    cudaError_t e = launch_early(qk_rope_bwd_kernel<T, TW, D, INTER>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a);
     note_launch(SGA_KERN_QK_ROPE_BWD, s, true);
     if (e != cudaSuccess || !a.part) return e;
     note_launch(SGA_KERN_QK_ROPE_REDUCE, s, false);
@@ -418,10 +455,11 @@ template <typename T, typename TW, int D> cudaError_t launch_bwd(RopeArgs &a, vo
     return e;
 }
 
-template <typename F> cudaError_t by_type(int D, sga_dtype dt, sga_dtype wdt, F f) {
+template <typename F> cudaError_t by_type(const sga_rotary &r, sga_dtype dt, sga_dtype wdt, F f) {
+    auto pairing = [&](auto t, auto w, auto d) { return r.interleaved ? f(t, w, d, std::true_type()) : f(t, w, d, std::false_type()); };
     auto width = [&](auto t, auto w) {
-        return D == 32 ? f(t, w, std::integral_constant<int, 32>())
-               : D == 64 ? f(t, w, std::integral_constant<int, 64>()) : f(t, w, std::integral_constant<int, 128>());
+        return r.D == 32 ? pairing(t, w, std::integral_constant<int, 32>())
+               : r.D == 64 ? pairing(t, w, std::integral_constant<int, 64>()) : pairing(t, w, std::integral_constant<int, 128>());
     };
     if (dt == SGA_F32) return width(float(), float());
     if (wdt == SGA_F32) return width(__nv_bfloat16(), float());
@@ -511,12 +549,14 @@ sga_status qk_norm_rope_fwd(const sga_rotary *rot, const void *Q, int64_t ldq, c
     a.eps = eps;
     a.wide = pos_bytes == 8;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return status_of(by_type(rot->D, dt, wdt, [&](auto t, auto w, auto d) { return launch_fwd<decltype(t), decltype(w), decltype(d)::value>(a, s); }));
+    return status_of(by_type(*rot, dt, wdt, [&](auto t, auto w, auto d, auto i) {
+        return launch_fwd<decltype(t), decltype(w), decltype(d)::value, decltype(i)::value>(a, s);
+    }));
 }
 
 size_t sga_qk_norm_rope_bwd_workspace_bytes(int64_t T, int D) {
     if (T <= 0 || D <= 0) return 0;
-    return (size_t)std::min<int64_t>((int64_t)device_sms() * kBwdBlocksPerSm, T) * 2 * (size_t)D * sizeof(float);
+    return (size_t)device_sms() * kBwdBlocksPerSm * 2 * (size_t)D * sizeof(float);
 }
 
 sga_status qk_norm_rope_bwd(const sga_rotary *rot, const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *pos,
@@ -563,7 +603,9 @@ sga_status qk_norm_rope_bwd(const sga_rotary *rot, const void *Q, int64_t ldq, c
     a.H = H;
     a.Hkv = Hkv;
     a.wide = pos_bytes == 8;
-    return status_of(by_type(rot->D, dt, wdt, [&](auto t, auto w, auto d) { return launch_bwd<decltype(t), decltype(w), decltype(d)::value>(a, dwq, dwk, s); }));
+    return status_of(by_type(*rot, dt, wdt, [&](auto t, auto w, auto d, auto i) {
+        return launch_bwd<decltype(t), decltype(w), decltype(d)::value, decltype(i)::value>(a, dwq, dwk, s);
+    }));
 }
 
 }  // extern "C"
