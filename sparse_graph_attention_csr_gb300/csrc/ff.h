@@ -34,13 +34,30 @@ struct FfProduct {
 
 // ---- activations: 0 silu, 1 gelu (by the normal distribution function), 2 relu -------
 
-// Phi(x), the normal distribution function: erfc's own accuracy in its tail.
-__device__ __forceinline__ float ff_phi(float x) { return 0.5f * erfcf(-0.70710678118654752f * x); }
+// Phi(x) = erfc(-x / sqrt(2)) / 2, the normal distribution function, to a few units
+// of its own size in the tail too.  FAST: by the Chebyshev fit to erfc of "Numerical
+// Recipes" (Press et al., erfcc), whose relative error is below 1.2e-7 everywhere; erfcf
+// takes three times as long (2708 x 256 x 680 forward 17.0 us, with relu 12.6).
+template <bool FAST> __device__ __forceinline__ float ff_phi(float x) {
+    if (!FAST) return 0.5f * erfcf(-0.70710678118654752f * x);
+    const float z = 0.70710678118654752f * fabsf(x), t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
+    float y = fmaf(t, 0.17087277f, -0.82215223f);
+    y = fmaf(t, y, 1.48851587f);
+    y = fmaf(t, y, -1.13520398f);
+    y = fmaf(t, y, 0.27886807f);
+    y = fmaf(t, y, -0.18628806f);
+    y = fmaf(t, y, 0.09678418f);
+    y = fmaf(t, y, 0.37409196f);
+    y = fmaf(t, y, 1.00002368f);
+    y = fmaf(t, y, -1.26551223f);
+    const float q = 0.5f * t * fast_exp2(kLog2e * fmaf(-z, z, y));
+    return x < 0.f ? q : 1.f - q;
+}
 
 // act(g); FAST: results that are rounded to bf16
 template <bool FAST> __device__ __forceinline__ float ff_act(float g, int act) {
     if (act == SGA_ACT_SILU) return FAST ? __fdividef(g, 1.f + fast_exp2(-kLog2e * g)) : g / (1.f + expf(-g));
-    if (act == SGA_ACT_GELU) return g * ff_phi(g);
+    if (act == SGA_ACT_GELU) return g * ff_phi<FAST>(g);
     return g != g ? g : fmaxf(g, 0.f);
 }
 // act(g) and its derivative (relu: 0 at 0)
@@ -50,7 +67,7 @@ template <bool FAST> __device__ __forceinline__ void ff_act_slope(float g, int a
         a = g * s;
         slope = fmaf(a, 1.f - s, s);
     } else if (act == SGA_ACT_GELU) {
-        const float p = ff_phi(g);
+        const float p = ff_phi<FAST>(g);
         a = g * p;
         slope = fmaf(g * 0.39894228040143268f, FAST ? fast_exp2(-0.5f * kLog2e * g * g) : expf(-0.5f * g * g), p);
     } else {

@@ -118,6 +118,38 @@ struct FfUnits {
     }
 };
 
+// 32 x 32 floats of a warp (a row a lane) to rows of `ld` floats from dst, of which
+// `rows` and `cols` are there, through the warp's staging: whole rows at a time (a row
+// a lane, as they lie in the registers, would be 32 places a store).  vec: rows begin on
+// 16 bytes, and cols is a multiple of 4.
+__device__ __forceinline__ void ff_store_block(uint32_t stage, const float *x, float *dst, int64_t ld, int rows, int cols, bool vec) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();   // (what was staged before has been read)
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((c ^ (lane & 7)) << 4)), "f"(x[4 * c]),
+                     "f"(x[4 * c + 1]), "f"(x[4 * c + 2]), "f"(x[4 * c + 3])
+                     : "memory");
+    __syncwarp();
+    if (vec) {
+        const int c = lane & 7;
+#pragma unroll
+        for (int q = 0; q < 32; q += 4) {
+            const int r = q + (lane >> 3);
+            float y[4];
+            tc::lds128(stage + r * 128 + ((c ^ (r & 7)) << 4), y);
+            if (r < rows && 4 * c < cols) *reinterpret_cast<float4 *>(dst + r * ld + 4 * c) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+    } else {
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            float y;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(stage + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4));
+            if (r < rows && lane < cols) dst[r * ld + lane] = y;
+        }
+    }
+}
+
 template <FfMode MODE, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_gemm_kernel(const __grid_constant__ FfParams p) {
     using C = FfCfg<MODE, F32>;
@@ -282,17 +314,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
             int tm, tn;
             ff_tile(u.tile, p.tiles_m, p.tiles_n, tm, tn);
             const int r = rank * 128 + quarter * 32;   // the warp's first row of the tile
+            const int64_t row0 = (int64_t)tm * 256 + r;
+            const int rows = (int)max((int64_t)0, min((int64_t)32, p.rows - row0));
             if (u.slot >= 0) {   // a share: its sums
-                float *dst = p.partial + (int64_t)u.slot * kTileFloats + (r + lane) * 256;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        *reinterpret_cast<float4 *>(dst + column(j) + k) =
-                            make_float4(acc[32 * j + k], acc[32 * j + k + 1], acc[32 * j + k + 2], acc[32 * j + k + 3]);
+                    if (rows > 0) {
+                        if (stored) tc::bulk_wait_read();   // (a result's store may still read the staging)
+                        ff_store_block(stage, acc + 32 * j, p.partial + (int64_t)u.slot * kTileFloats + r * 256 + column(j), 256, rows, 32, true);
+                    }
                 continue;
             }
-            const int64_t row0 = (int64_t)tm * 256 + r;
             const int which = MODE == FfMode::DW && 2 * tn >= p.tiles_n;   // dWu
             const int64_t col0 = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN;
             if constexpr (!F32) {
@@ -341,30 +373,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                     }
                 }
             } else {
-                const int64_t row = row0 + lane;
-                if (row < p.rows) {
-                    constexpr int PIECES = MODE == FfMode::FWD ? 3 : 1;
+                constexpr int PIECES = MODE == FfMode::FWD ? 3 : 1, BLOCKS = MODE == FfMode::FWD ? 2 : 4;
 #pragma unroll
-                    for (int x = 0; x < PIECES; ++x) {
-                        if (MODE == FfMode::FWD && x > 0 && !p.out[x]) break;
-                        float *dst = static_cast<float *>(p.out[MODE == FfMode::FWD ? x : which]) + row * p.cols;
+                for (int x = 0; x < PIECES; ++x) {
+                    if (rows <= 0 || (MODE == FfMode::FWD && x > 0 && !p.out[x])) break;
+                    float *dst = static_cast<float *>(p.out[MODE == FfMode::FWD ? x : which]) + row0 * p.cols;
 #pragma unroll
-                        for (int c = 0; c < (MODE == FfMode::FWD ? 64 : 128); c += 4) {
-                            const int64_t col = col0 + (MODE == FfMode::FWD ? half * 64 : half * 128) + c;
-                            float y[4];
+                    for (int j = 0; j < BLOCKS; ++j) {
+                        const int64_t col = col0 + half * (32 * BLOCKS) + 32 * j;
+                        const int cols = (int)max((int64_t)0, min((int64_t)32, p.cols - col));
+                        if (MODE != FfMode::FWD) {
+                            ff_store_block(stage, acc + 32 * j, dst + col, p.cols, rows, cols, p.tma_out);
+                        } else if (x > 0) {
+                            ff_store_block(stage, acc + 64 * (x - 1) + 32 * j, dst + col, p.cols, rows, cols, p.tma_out);
+                        } else {
+                            float y[32];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (MODE != FfMode::FWD) y[k] = acc[c + k];
-                                else if (x == 0) y[k] = ff_act<false>(acc[c + k], p.act) * acc[64 + c + k];
-                                else y[k] = acc[64 * (x - 1) + c + k];
-                            }
-                            if (p.tma_out && col + 3 < p.cols) {   // (rows on 16 bytes)
-                                *reinterpret_cast<float4 *>(dst + col) = make_float4(y[0], y[1], y[2], y[3]);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (col + k < p.cols) dst[col + k] = y[k];
-                            }
+                            for (int k = 0; k < 32; ++k) y[k] = ff_act<false>(acc[32 * j + k], p.act) * acc[64 + 32 * j + k];
+                            ff_store_block(stage, y, dst + col, p.cols, rows, cols, p.tma_out);
                         }
                     }
                 }
@@ -390,6 +416,10 @@ template <FfMode MODE, bool F32> __global__ void __launch_bounds__(256) ff_join_
     const int c = (int)(id % Q) * 4, r = (int)(id / Q % 256), t = (int)(id / Q / 256);
     const int tiles = p.tiles_m * p.tiles_n;
     if (t >= tiles - p.whole) return;
+    int tm, tn;
+    ff_tile(p.whole + t, p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t row = (int64_t)tm * 256 + r;
+    if (row >= p.rows) return;   // (whose sums were not stored)
     // the pairs whose shares hold k-blocks of the tile
     const int64_t all = (int64_t)(tiles - p.whole) * p.kb, b = (int64_t)t * p.kb, e = b + p.kb;
     float y[2][4] = {};
@@ -409,11 +439,8 @@ template <FfMode MODE, bool F32> __global__ void __launch_bounds__(256) ff_join_
             y[h][3] += v.w;
         }
     }
-    int tm, tn;
-    ff_tile(p.whole + t, p.tiles_m, p.tiles_n, tm, tn);
     const int which = MODE == FfMode::DW && 2 * tn >= p.tiles_n;
-    const int64_t row = (int64_t)tm * 256 + r, col = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN + c;
-    if (row >= p.rows) return;
+    const int64_t col = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN + c;
     using T = std::conditional_t<F32, float, __nv_bfloat16>;
     auto store = [&](void *base, const float *x) {
         T *dst = static_cast<T *>(base) + row * p.cols + col;

@@ -283,8 +283,14 @@ template <typename L, int D> __device__ __forceinline__ void block_sums(float *s
     }
 }
 
+// Blocks an SM of the backward pass, each with a row of sums.
+constexpr int kBwdBlocksPerSm = 3;
+
+// The queries of all rows, then the keys: one weight's sums at a time in registers,
+// which pays for forming the turns again (LB blocks an SM, where the registers of one
+// pair of sums more would leave room for fewer).
 template <typename T, typename TW, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) qk_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
     using L = Lane<T, D, INTER>;
     constexpr int EL = L::EL, G = L::G, U = 2;
     __shared__ float sums[kThreads / 32 * D];
@@ -292,21 +298,24 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_cons
     wait_previous();
     const L at(a.rot, threadIdx.x % G);
     const bool norm = a.rq_in != nullptr;
-    float qa[EL], qb[EL], ka[EL], kb[EL];   // this thread's sums of dwq, dwk
+    const int64_t step = (int64_t)gridDim.x * (kThreads / G);
+    for (int key = 0; key < 2; ++key) {
+        const int heads = key ? a.Hkv : a.H, steps = a.per ? a.per : heads, parts = a.per ? (heads + a.per - 1) / a.per : 1;
+        const int64_t units = a.T * parts;
+        float wa[EL], wb[EL], sa[EL], sb[EL];
+        at.template weights<TW>(static_cast<const TW *>(key ? a.wk : a.wq), wa, wb);
 #pragma unroll
-    for (int e = 0; e < EL; ++e) qa[e] = qb[e] = ka[e] = kb[e] = 0.f;
-    const int64_t units = a.T * a.parts, step = (int64_t)gridDim.x * (kThreads / G);
-    for (int64_t u0 = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / 32 * (32 / G); u0 < units; u0 += step) {
-        const Share sh(a, u0 + threadIdx.x % 32 / G);
-        float c[EL], s[EL];
-        bool turned = false;
-        each_phase(a, sh, [&](bool key, int h0, int h1, int steps) {
-            const int64_t row = sh.in ? sh.row : 0, first = row * (key ? a.Hkv : a.H) + h0;
+        for (int e = 0; e < EL; ++e) sa[e] = sb[e] = 0.f;   // this thread's sums of the weight's gradient
+        for (int64_t u0 = (int64_t)blockIdx.x * (kThreads / G) + threadIdx.x / 32 * (32 / G); u0 < units; u0 += step) {
+            const int64_t unit = u0 + threadIdx.x % 32 / G;
+            const bool in = unit < units;
+            const int64_t row = !in ? 0 : a.per ? unit / parts : unit;
+            const int h0 = in && a.per ? (int)(unit - row * parts) * a.per : 0, n = in ? min(heads - h0, steps) : 0;
+            const int64_t first = row * heads + h0;
             const T *src = static_cast<const T *>(key ? a.K : a.Q) + row * (key ? a.ldk : a.ldq) + h0 * D;
             const T *grad = static_cast<const T *>(key ? a.dKo : a.dQo) + first * D;
             const float *r = norm ? (key ? a.rk_in : a.rq_in) + first : nullptr;
             T *dst = static_cast<T *>(key ? a.Ko : a.Qo) + first * D;
-            const int n = h1 - h0;
             uint4 x[U][2], g[U][2];
             float inv[U];
             auto fetch = [&](int u, int i) {
@@ -322,10 +331,8 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_cons
             };
 #pragma unroll
             for (int u = 0; u < U; ++u) fetch(u, u);
-            float wa[EL], wb[EL];
-            at.template weights<TW>(static_cast<const TW *>(key ? a.wk : a.wq), wa, wb);
-            if (!turned && sh.in) at.turns(a, sh.row, c, s);
-            turned = true;
+            float c[EL], s[EL];
+            at.turns(a, row, c, s);   // (while the first heads arrive)
             for (int i0 = 0; i0 < steps; i0 += U) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
@@ -341,19 +348,15 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_cons
                         L::split(x0, x1, xa, xb);
                         mul<EL>(xa, rr);
                         mul<EL>(xb, rr);
-                        auto add = [&](float *sa, float *sb) {
 #pragma unroll
-                            for (int e = 0; e < EL; e += 2) {
-                                const float2 y = ffma2(make_float2(da[e], da[e + 1]), make_float2(xa[e], xa[e + 1]), make_float2(sa[e], sa[e + 1]));
-                                const float2 z = ffma2(make_float2(db[e], db[e + 1]), make_float2(xb[e], xb[e + 1]), make_float2(sb[e], sb[e + 1]));
-                                sa[e] = y.x;
-                                sa[e + 1] = y.y;
-                                sb[e] = z.x;
-                                sb[e + 1] = z.y;
-                            }
-                        };
-                        if (key) add(ka, kb);
-                        else add(qa, qb);
+                        for (int e = 0; e < EL; e += 2) {
+                            const float2 y = ffma2(make_float2(da[e], da[e + 1]), make_float2(xa[e], xa[e + 1]), make_float2(sa[e], sa[e + 1]));
+                            const float2 z = ffma2(make_float2(db[e], db[e + 1]), make_float2(xb[e], xb[e + 1]), make_float2(sb[e], sb[e + 1]));
+                            sa[e] = y.x;
+                            sa[e + 1] = y.y;
+                            sb[e] = z.x;
+                            sb[e + 1] = z.y;
+                        }
                         mul<EL>(da, wa);
                         mul<EL>(db, wb);
                         float2 q = make_float2(0.f, 0.f);
@@ -376,12 +379,9 @@ __global__ void __launch_bounds__(kThreads) qk_rope_bwd_kernel(const __grid_cons
                     if (i < n) at.store(dst + i * D, da, db);
                 }
             }
-        });
+        }
+        if (a.part) block_sums<L, D>(sums, sa, sb, at, a.part + (int64_t)blockIdx.x * 2 * D + key * D);
     }
-    if (!a.part) return;
-    float *out = a.part + (int64_t)blockIdx.x * 2 * D;
-    block_sums<L, D>(sums, qa, qb, at, out);
-    block_sums<L, D>(sums, ka, kb, at, out + D);
 }
 
 // dwq, dwk from the blocks' sums: 32 columns a block; its 32 warps take every
@@ -405,8 +405,6 @@ __global__ void __launch_bounds__(1024) qk_rope_reduce_kernel(const float *__res
     const int c = blockIdx.x * 32 + wp;
     if (lane == 0) (c < D ? dwq : dwk)[c < D ? c : c - D] = from_f32<TW>(s);
 }
-
-constexpr int kBwdBlocksPerSm = 8;   // most of the backward pass, each with a row of sums
 
 // Deals a row's heads to several groups where one group a row would leave SMs
 // without work, four heads at least each (or all of a row's).

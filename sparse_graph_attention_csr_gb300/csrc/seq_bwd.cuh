@@ -324,21 +324,33 @@ template <int D, bool WIN> __device__ __forceinline__ void dkdv_pass(const BwdPa
             tc::fence_after_sync();
             uint32_t v[N];
             load_scores(ts, v);
-#pragma unroll
-            for (int c = 0; c < N; c += 2) {
-                const float2 x = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2,
-                                       make_float2(r[c], r[c + 1]));
-                p[c] = fast_exp2(x.x);
-                p[c + 1] = fast_exp2(x.y);
-            }
             const bool masked = qt < t.f0 || qt >= t.f1;
             uint32_t bits[N / 32];
+            auto weights = [&](int c0, int c1) {
+#pragma unroll
+                for (int c = c0; c < c1; c += 2) {
+                    const float2 x = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2,
+                                           make_float2(r[c], r[c + 1]));
+                    p[c] = fast_exp2(x.x);
+                    p[c + 1] = fast_exp2(x.y);
+                }
+            };
+            // zero where the pair is masked
+            auto mask = [&](int w) {
+                if (WIN && __all_sync(SGA_FULL_MASK, bits[w] == ~0u)) return;
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (!((bits[w] >> c) & 1u)) p[32 * w + c] = 0.f;
+            };
+            if (!WIN || !masked) weights(0, N);
             if (masked) {
                 const int cl = seq::rel(view.lo, (int64_t)qt * 128), ch = seq::rel(view.hi, (int64_t)qt * 128);
 #pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    if (c % 32 == 0) bits[c / 32] = seq::column_bits(cl, ch, (part * N + c) / 32);
-                    if (!((bits[c / 32] >> (c & 31)) & 1u)) p[c] = 0.f;
+                for (int w = 0; w < N / 32; ++w) {
+                    bits[w] = seq::column_bits(cl, ch, part * (N / 32) + w);
+                    // (a word that no row of the warp sees needs no exponentials, as in the forward)
+                    if (WIN && !__all_sync(SGA_FULL_MASK, bits[w] == 0)) weights(32 * w, 32 * w + 32);
+                    mask(w);
                 }
             }
             store_weights(ts, p);
@@ -364,8 +376,7 @@ template <int D, bool WIN> __device__ __forceinline__ void dkdv_pass(const BwdPa
             }
             if (masked)   // (zero weights times an infinity)
 #pragma unroll
-                for (int c = 0; c < N; ++c)
-                    if (!((bits[c / 32] >> (c & 31)) & 1u)) p[c] = 0.f;
+                for (int w = 0; w < N / 32; ++w) mask(w);
             store_weights(tp, p);
             tc::fence_before_sync();
             __syncwarp();
@@ -659,11 +670,13 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
                 p[c + 1] = x.y;
             }
             if (kt < t.f0 || kt >= t.f1) {
-                uint32_t bits = 0;
 #pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    if (c % 32 == 0) bits = seq::view_bits<WIN>(view, (int64_t)kt * 128, (part * N + c) / 32);
-                    if (!((bits >> (c & 31)) & 1u)) p[c] = 0.f;
+                for (int w = 0; w < N / 32; ++w) {
+                    const uint32_t bits = seq::view_bits<WIN>(view, (int64_t)kt * 128, part * (N / 32) + w);
+                    if (WIN && __all_sync(SGA_FULL_MASK, bits == ~0u)) continue;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!((bits >> c) & 1u)) p[32 * w + c] = 0.f;
                 }
             }
             round_weights(p, pk);

@@ -238,18 +238,31 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(ts + 32 * c, v + 32 * c);
 #pragma unroll
             for (int c = 0; c < 4; ++c) tc::tmem_wait_ld(v + 32 * c);
+            // A window cuts most masked tiles between words of 32 columns: words that all
+            // of the warp's rows see need no mask, and those that none of them sees
+            // neither exponentials.
+            uint32_t dead = 0;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (kt < t.f0 || kt >= t.f1) {
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const uint32_t bits = seq::view_bits<WIN>(view, (int64_t)kt * 128, w);
+                    if (WIN && __all_sync(SGA_FULL_MASK, bits == 0)) {
+                        dead |= 1u << w;
+                        continue;
+                    }
+                    if (!WIN || !__all_sync(SGA_FULL_MASK, bits == ~0u))
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((bits >> c) & 1u)) v[32 * w + c] = 0xff800000u;   // -inf
+                        for (int c = 0; c < 32; ++c)
+                            if (!((bits >> c) & 1u)) v[32 * w + c] = 0xff800000u;   // -inf
+                    if (WIN)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[32 * w + c]));
                 }
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (!WIN || (kt >= t.f0 && kt < t.f1))
 #pragma unroll
-            for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
+                for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(v[c]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
             const bool grow = top > m + kLazyLog2;   // (also from m = -inf)
             const bool move = grow && l > 0.f;
@@ -269,13 +282,26 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             const float sub = m == -INFINITY ? 0.f : m;   // nothing seen yet: every weight is zero
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 k2 = make_float2(scale2, scale2), s2 = make_float2(-sub, -sub);
+            auto weights = [&](int c0, int c1) {
 #pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-                float2 x = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2, s2);
-                x.x = fast_exp2(x.x);
-                x.y = fast_exp2(x.y);
-                sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], x);
-                v[c >> 1] = pack_bf16x2(x.x, x.y);
+                for (int c = c0; c < c1; c += 2) {
+                    float2 x = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), k2, s2);
+                    x.x = fast_exp2(x.x);
+                    x.y = fast_exp2(x.y);
+                    sum[(c >> 1) & 1] = fadd2(sum[(c >> 1) & 1], x);
+                    v[c >> 1] = pack_bf16x2(x.x, x.y);
+                }
+            };
+            if (!WIN || dead == 0) {
+                weights(0, 128);
+            } else {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    if (!((dead >> w) & 1u)) weights(32 * w, 32 * w + 32);
+                    else
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) v[16 * w + c] = 0u;
+                }
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tc::tmem_st32_async(ts, v);
