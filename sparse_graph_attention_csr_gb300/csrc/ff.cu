@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(256) ff_slopes_kernel(const T *G, const T *U, 
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             float a, slope;
-            ff_act_slope<sizeof(T) == 2>(g[k], act, a, slope);
+            ff_act_slope(g[k], act, a, slope);
             g[k] = d[k] * u[k] * slope;
             u[k] = d[k] * a;
         }

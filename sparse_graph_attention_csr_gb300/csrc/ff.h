@@ -35,11 +35,10 @@ struct FfProduct {
 // ---- activations: 0 silu, 1 gelu (by the normal distribution function), 2 relu -------
 
 // Phi(x) = erfc(-x / sqrt(2)) / 2, the normal distribution function, to a few units
-// of its own size in the tail too.  FAST: by the Chebyshev fit to erfc of "Numerical
-// Recipes" (Press et al., erfcc), whose relative error is below 1.2e-7 everywhere; erfcf
-// takes three times as long (2708 x 256 x 680 forward 17.0 us, with relu 12.6).
-template <bool FAST> __device__ __forceinline__ float ff_phi(float x) {
-    if (!FAST) return 0.5f * erfcf(-0.70710678118654752f * x);
+// of its own size in the tail too: by the Chebyshev fit to erfc of "Numerical Recipes"
+// (Press et al., erfcc), whose relative error is below 1.2e-7 everywhere.  erfcf, whose
+// chain is longer, took 20 us of the 67 of 4099 x 301 x 803 in fp32.
+__device__ __forceinline__ float ff_phi(float x) {
     const float z = 0.70710678118654752f * fabsf(x), t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
     float y = fmaf(t, 0.17087277f, -0.82215223f);
     y = fmaf(t, y, 1.48851587f);
@@ -54,22 +53,23 @@ template <bool FAST> __device__ __forceinline__ float ff_phi(float x) {
     return x < 0.f ? q : 1.f - q;
 }
 
-// act(g); FAST: results that are rounded to bf16
-template <bool FAST> __device__ __forceinline__ float ff_act(float g, int act) {
-    if (act == SGA_ACT_SILU) return FAST ? __fdividef(g, 1.f + fast_exp2(-kLog2e * g)) : g / (1.f + expf(-g));
-    if (act == SGA_ACT_GELU) return g * ff_phi<FAST>(g);
+// act(g).  Exponentials and quotients by the MUFU instructions: off by a few units of
+// fp32, and half a unit more for each unit of |g|.
+__device__ __forceinline__ float ff_act(float g, int act) {
+    if (act == SGA_ACT_SILU) return __fdividef(g, 1.f + fast_exp2(-kLog2e * g));
+    if (act == SGA_ACT_GELU) return g * ff_phi(g);
     return g != g ? g : fmaxf(g, 0.f);
 }
 // act(g) and its derivative (relu: 0 at 0)
-template <bool FAST> __device__ __forceinline__ void ff_act_slope(float g, int act, float &a, float &slope) {
+__device__ __forceinline__ void ff_act_slope(float g, int act, float &a, float &slope) {
     if (act == SGA_ACT_SILU) {
-        const float e = FAST ? fast_exp2(-kLog2e * g) : expf(-g), s = FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+        const float s = __fdividef(1.f, 1.f + fast_exp2(-kLog2e * g));
         a = g * s;
         slope = fmaf(a, 1.f - s, s);
     } else if (act == SGA_ACT_GELU) {
-        const float p = ff_phi<FAST>(g);
+        const float p = ff_phi(g);
         a = g * p;
-        slope = fmaf(g * 0.39894228040143268f, FAST ? fast_exp2(-0.5f * kLog2e * g * g) : expf(-0.5f * g * g), p);
+        slope = fmaf(g * 0.39894228040143268f, fast_exp2(-0.5f * kLog2e * g * g), p);
     } else {
         a = g != g ? g : fmaxf(g, 0.f);
         slope = g > 0.f ? 1.f : 0.f;

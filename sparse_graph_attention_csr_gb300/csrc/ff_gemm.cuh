@@ -344,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                         for (int k = 0; k < 8; ++k) {
                             const int e = 8 * c + k;
                             if (MODE != FfMode::FWD) y[k] = acc[64 * x + e];
-                            else if (x == 0) y[k] = ff_act<true>(acc[e], p.act) * acc[64 + e];
+                            else if (x == 0) y[k] = ff_act(acc[e], p.act) * acc[64 + e];
                             else y[k] = acc[64 * (x - 1) + e];
                         }
                         const uint4 v = pack<__nv_bfloat16>(y);
@@ -389,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                         } else {
                             float y[32];
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) y[k] = ff_act<false>(acc[32 * j + k], p.act) * acc[64 + 32 * j + k];
+                            for (int k = 0; k < 32; ++k) y[k] = ff_act(acc[32 * j + k], p.act) * acc[64 + 32 * j + k];
                             ff_store_block(stage, y, dst + col, p.cols, rows, cols, p.tma_out);
                         }
                     }
@@ -451,7 +451,7 @@ template <FfMode MODE, bool F32> __global__ void __launch_bounds__(256) ff_join_
     if (MODE == FfMode::FWD) {
         float o[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = ff_act<!F32>(y[0][k], p.act) * y[1][k];
+        for (int k = 0; k < 4; ++k) o[k] = ff_act(y[0][k], p.act) * y[1][k];
         store(p.out[0], o);
         if (p.out[1]) store(p.out[1], y[0]);
         if (p.out[2]) store(p.out[2], y[1]);

@@ -82,6 +82,9 @@ template <int D> struct QCfg : BwdCfg<D> {
     static constexpr uint32_t RES0 = V0 + NV * B::TB;             // sums of a row's rounding errors, by part
     static constexpr uint32_t BAR0 = RES0 + kParts * 512, BYTES = BAR0 + 256;   // barriers
     static constexpr uint32_t TS = 0, TP = 128, TQ = 256, TA = 384, TG = 448;   // S, dP, dQ; Q and dOut as A operands
+    // Q and dOut arrive in the rings' last places (read by their threads from memory, a
+    // row a thread, every load would touch 32 lines)
+    static constexpr uint32_t Q0 = ST0 + (NK - 1) * B::TB, G0 = V0 + (NV - 1) * B::TB;
 };
 constexpr uint32_t kMaxSmem = 227 * 1024;
 static_assert(KvCfg<128>::BYTES <= kMaxSmem && QCfg<128>::BYTES <= kMaxSmem, "shared memory");
@@ -111,7 +114,7 @@ template <int N, uint32_t TB> struct Ring {
 };
 
 struct BwdParams {
-    CUtensorMap tq, tk, tv, tg;
+    CUtensorMap tq, tk, tv, tg, to_q, to_k, to_v;
     SeqArgs a;
 };
 
@@ -164,9 +167,11 @@ __device__ __forceinline__ void store_weights(uint32_t taddr, const float *p) {
     store_weights(taddr, pk);
 }
 
-// 32 columns of a row from TMEM, less `sub` (if any), scaled, to bf16 at dst (if
-// `in`); the lanes whose row was not finite.
-__device__ __forceinline__ uint32_t store_from_tmem(uint32_t taddr, __nv_bfloat16 *dst, float f, bool in,
+// 32 columns (from c0) of a row from TMEM, less `sub` (if any), scaled, to bf16 at dst
+// (if `in`), or TMA: into the row's place in a tile of results; the lanes whose row was
+// not finite.
+template <bool TMA>
+__device__ __forceinline__ uint32_t store_from_tmem(uint32_t taddr, __nv_bfloat16 *dst, uint32_t tile, int r, int c0, float f, bool in,
                                                     const float *sub = nullptr) {
     bool bad = false;
     uint32_t o[32];
@@ -177,9 +182,12 @@ __device__ __forceinline__ uint32_t store_from_tmem(uint32_t taddr, __nv_bfloat1
         x[i] = (sub ? __uint_as_float(o[i]) - sub[i] : __uint_as_float(o[i])) * f;
         bad |= !(fabsf(x[i]) < INFINITY);
     }
-    if (in)
+    if constexpr (TMA) {
+        seq::stage_columns(tile, r, c0, x);
+    } else if (in) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(dst + 8 * q) = pack<__nv_bfloat16>(x + 8 * q);
+    }
     return __ballot_sync(SGA_FULL_MASK, bad && in);
 }
 
@@ -383,6 +391,8 @@ template <int D, bool WIN> __device__ __forceinline__ void dkdv_pass(const BwdPa
             if (lane == 0) tc::mbar_arrive(&ds_full);
         }
         if (ok && !tc::warp_wait(&acc_full, 0, tc::kWaitLimit)) ok = false;
+        // the two parts of a row's results go on together, or neither does (after a timeout)
+        if (seq::kTmaResult<D>) ok = !seq::pair_any(2 + quarter, !ok);
         if (WIN && ok && t.part) {   // this part's sums, as they are
             tc::fence_after_sync();
             float *dst = a.ws_part + (((int64_t)(t.part - 1) * a.Hkv + hk) * 256 + quarter * 32 + lane) * D;
@@ -397,14 +407,29 @@ template <int D, bool WIN> __device__ __forceinline__ void dkdv_pass(const BwdPa
             }
         } else if (ok) {
             tc::fence_after_sync();
+            constexpr bool kTma = seq::kTmaResult<D>;
             uint32_t again[2] = {0, 0};   // rows of dV, dK
             for (int c = part; c < D / 16; c += kParts) {   // 32 columns each: dV's, then dK's
                 const bool dk = c >= D / 32;
                 const int c0 = (dk ? c - D / 32 : c) * 32;
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(dk ? a.dK : a.dV) + ((in ? row : 0) * a.Hkv + hk) * D + c0;
-                const uint32_t bad = store_from_tmem((dk ? tK : tV) + c0 + tl, dst, dk ? a.scale : 1.f, in);
+                // (every product that reads K or V is done)
+                const uint32_t bad = store_from_tmem<kTma>((dk ? tK : tV) + c0 + tl, dst, sbase + C::R0 + (dk ? 0 : C::TB),
+                                                           quarter * 32 + lane, c0, dk ? a.scale : 1.f, in);
                 if (dk) again[1] |= bad;
                 else again[0] |= bad;
+            }
+            if constexpr (kTma) {   // the two parts share the atoms of their rows
+                tc::fence_proxy_async();
+                const bool redo = seq::pair_any(2 + quarter, (again[0] | again[1]) != 0);
+                if (lane == 0 && part < C::DA) {
+                    seq::store_atom(&prm.to_v, sbase + C::R0 + C::TB, part, quarter * 32, hk, (int64_t)t.tile * 128 + quarter * 32, a.rows);
+                    seq::store_atom(&prm.to_k, sbase + C::R0, part, quarter * 32, hk, (int64_t)t.tile * 128 + quarter * 32, a.rows);
+                    tc::bulk_commit();
+                    if (redo) tc::bulk_wait_all();
+                    else tc::bulk_wait_read();
+                }
+                if (redo) seq::pair_any(2 + quarter, false);
             }
             __syncwarp();   // (the rows are read back)
 #pragma unroll
@@ -452,11 +477,22 @@ template <int D, bool WIN> __device__ __forceinline__ void dkdv_pass(const BwdPa
 // are farther apart than |c| / 2 (no offset to speak of).  c lies between them:
 // they are representable, and each rounding on the way to it is monotone.  Of
 // eight keys and more rows of similar lengths take the same four, so that their
-// loads are one.  Where the row sees sinks apart from its window, the fourth is one
-// of them (their middle): an offset is one that they share too.
+// loads are one.  Of a windowed plan the rows of a warp that belong to one sequence take
+// theirs from what all of them see, where that is anything (each its own: 8 us of the 40
+// of a unit at a window of 1024); and where a row sees sinks apart from its window, the
+// fourth is one of them (their middle): an offset is one that they share too.
 template <bool WIN>
 __device__ __forceinline__ void mean_key(const SeqArgs &a, int D, const seq::View<WIN> &view, int hk, int c0, uint32_t (&c)[16]) {
-    const int64_t lo = view.lo, n = max(view.hi - lo, (int64_t)1), m = n < 8 ? n : (int64_t)1 << (31 - __clz((int)n));   // (n < 2^31)
+    int64_t lo = view.lo, hi = view.hi;
+    if constexpr (WIN) {
+        const uint32_t peers = __match_any_sync(SGA_FULL_MASK, view.begin);
+        const int64_t l = __shfl_sync(SGA_FULL_MASK, view.lo, 31 - __clz(peers)), h = __shfl_sync(SGA_FULL_MASK, view.hi, __ffs(peers) - 1);
+        if (l < h) {
+            lo = l;
+            hi = h;
+        }
+    }
+    const int64_t n = max(hi - lo, (int64_t)1), m = n < 8 ? n : (int64_t)1 << (31 - __clz((int)n));   // (n < 2^31)
     uint4 raw[4][4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -486,8 +522,8 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::BAR0);
     uint64_t &q_full = bar[0], &s_full = bar[1], &s_free = bar[2], &dp_full = bar[3], &ds_full = bar[4], &acc_full = bar[5];
     uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(bar + 6);
-    uint64_t *ring_full = bar + 7, *ring_empty = ring_full + C::NK + C::NV;
-    static_assert((7 + 2 * (C::NK + C::NV)) * 8 <= 256, "barriers");
+    uint64_t &rows_full = bar[7], *ring_full = bar + 8, *ring_empty = ring_full + C::NK + C::NV;
+    static_assert((8 + 2 * (C::NK + C::NV)) * 8 <= 256, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem);
     const Ring<C::NK, C::TB> rk{ring_full, ring_empty, sbase + C::ST0};
@@ -497,6 +533,7 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
     const int n = seq::own_count<WIN>(t);
 
     if (tid == 32) {
+        tc::mbar_init(&rows_full, 1);
         tc::mbar_init(&q_full, kSoft);
         tc::mbar_init(&s_free, kSoft);
         rk.init();
@@ -519,8 +556,12 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
         if (warp == 0 && lane == 0) {   // ----------------------------------- TMA producer
             bool ok = true;
             int i = 0, v = 0;   // tiles of K and V issued
+            tc::mbar_expect_tx(&rows_full, 2 * C::TB);
+            seq::load_tile<C::DA>(sbase + C::Q0, &prm.tq, h, t.tile * 128, &rows_full);
+            seq::load_tile<C::DA>(sbase + C::G0, &prm.tg, h, t.tile * 128, &rows_full);
             for (; i < n; ++i) {
-                if (!rk.wait_room(i)) {
+                // (the last places are free once Q and dOut are in TMEM)
+                if ((i == (C::NK < C::NV ? C::NK : C::NV) - 1 && !tc::mbar_wait(&q_full, 0, tc::kWaitLimit)) || !rk.wait_room(i)) {
                     ok = false;
                     break;
                 }
@@ -537,6 +578,7 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
             }
             if (!ok) atomicOr(a.d_err, tc::kErrMmaTimeout);
             // loads that no product consumed (only after a timeout) land before the CTA ends
+            tc::mbar_wait(&rows_full, 0, tc::kWaitLimit);
             rk.drain(i);
             rv.drain(v);
         } else if (warp == 1) {   // ----------------------------------------- MMA issuer (the warp in step)
@@ -593,23 +635,24 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
         const float nlse = a.ws_nlse[(int64_t)h * a.rows_pad + row], nd = a.ws_ndelta[(int64_t)h * a.rows_pad + row];
         const float2 k2 = make_float2(scale2, scale2), l2 = make_float2(nlse, nlse), d2 = make_float2(nd, nd);
         constexpr int N = kCols;
+        bool ok = tc::warp_wait(&rows_full, 0, tc::kWaitLimit);
         // the row's share of Q and dOut into TMEM (rows past the last, and the
-        // columns past a head of 32, as zeros)
+        // columns past a head of 32, are zeros)
         {
             constexpr int CW = C::DP / 2 / kParts;   // columns (bf16 pairs) of a part
+            const int r = quarter * 32 + lane;
             for (int x = 0; x < 2; ++x) {
-                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(x ? a.dOut : a.Q) + ((in ? row : 0) * a.H + h) * D;
+                const uint32_t src = sbase + (x ? C::G0 : C::Q0) + r * 128;
 #pragma unroll
                 for (int c = 0; c < CW; c += 8) {
                     const int e = 2 * (part * CW + c);    // first element
                     uint32_t u[8];
 #pragma unroll
                     for (int k = 0; k < 8; k += 4) {
-                        const uint4 q = in && e + 2 * k < D ? ldg16(src + e + 2 * k) : make_uint4(0, 0, 0, 0);
-                        u[k] = q.x;
-                        u[k + 1] = q.y;
-                        u[k + 2] = q.z;
-                        u[k + 3] = q.w;
+                        float q[4];
+                        tc::lds128(src + (e >> 6) * 16384 + ((((e & 63) / 8 + k / 4) ^ (r & 7)) << 4), q);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) u[k + z] = __float_as_uint(q[z]);
                     }
                     tc::tmem_st8_async((x ? tG : tA) + part * CW + c + tl, u);
                 }
@@ -634,8 +677,7 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
             const float2 r = make_float2(__uint_as_float(pk[c >> 1] << 16), __uint_as_float(pk[c >> 1] & 0xffff0000u));
             res = fadd2(res, ffma2(make_float2(p[c], p[c + 1]), make_float2(-1.f, -1.f), r));
         };
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n && ok; ++i) {
             const int kt = seq::own_tile<WIN>(t, i);
             if (!tc::warp_wait(&s_full, i & 1, tc::kWaitLimit)) {
                 ok = false;
@@ -695,8 +737,11 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
 #pragma unroll
         for (int k = 1; k < kParts; ++k) err += sums[k * 128 + quarter * 32 + lane];
         if (ok && !tc::warp_wait(&acc_full, 0, tc::kWaitLimit)) ok = false;
+        // the two parts of a row's results go on together, or neither does (after a timeout)
+        if (seq::kTmaResult<D>) ok = !seq::pair_any(2 + quarter, !ok);
         if (ok) {
             tc::fence_after_sync();
+            constexpr bool kTma = seq::kTmaResult<D>;
             uint32_t again = 0;
 #pragma unroll
             for (int k = 0; k < SL; ++k) {
@@ -709,7 +754,19 @@ template <int D, bool WIN> __device__ __forceinline__ void dq_pass(const BwdPara
                     sub[2 * i] = err * __uint_as_float(mean[k][i] << 16);
                     sub[2 * i + 1] = err * __uint_as_float(mean[k][i] & 0xffff0000u);
                 }
-                again |= store_from_tmem(tQ + c0 + tl, dst, a.scale, in, sub);
+                // (every product that reads a tile is done)
+                again |= store_from_tmem<kTma>(tQ + c0 + tl, dst, sbase + C::ST0, quarter * 32 + lane, c0, a.scale, in, sub);
+            }
+            if constexpr (kTma) {   // the two parts share the atoms of their rows
+                tc::fence_proxy_async();
+                const bool redo = seq::pair_any(2 + quarter, again != 0);
+                if (lane == 0 && part < C::DA) {
+                    seq::store_atom(&prm.to_q, sbase + C::ST0, part, quarter * 32, h, (int64_t)t.tile * 128 + quarter * 32, a.rows);
+                    tc::bulk_commit();
+                    if (redo) tc::bulk_wait_all();
+                    else tc::bulk_wait_read();
+                }
+                if (redo) seq::pair_any(2 + quarter, false);
             }
             __syncwarp();   // (the rows are read back)
             while (again) {
@@ -755,6 +812,11 @@ template <int D, bool WIN> cudaError_t launch(const SeqArgs &a, cudaStream_t s) 
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tg, a.dOut, a.rows, a.H, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tk, a.K, a.rows, a.Hkv, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tv, a.V, a.rows, a.Hkv, D);
+    if (seq::kTmaResult<D>) {
+        if (e == cudaSuccess) e = seq_tensor_map(&prm.to_q, a.dQ, a.rows, a.H, D, 32);
+        if (e == cudaSuccess) e = seq_tensor_map(&prm.to_k, a.dK, a.rows, a.Hkv, D, 32);
+        if (e == cudaSuccess) e = seq_tensor_map(&prm.to_v, a.dV, a.rows, a.Hkv, D, 32);
+    }
     constexpr size_t smem = KvCfg<D>::BYTES > QCfg<D>::BYTES ? KvCfg<D>::BYTES : QCfg<D>::BYTES;
     if (e == cudaSuccess) e = allow_smem<seq_bwd_kernel<D, WIN>>(smem);
     if (e == cudaSuccess) e = seq_row_terms<__nv_bfloat16>(a, D, s);

@@ -66,7 +66,7 @@ template <int D, int NS> struct FwdCfg {
 };
 
 struct FwdParams {
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     SeqArgs a;
     int pair_heads;   // NS = 2: the two tiles are two heads of one row tile
 };
@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             const float inv = 1.f / l;
             bool bad = false;
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out_w) + ((in ? row : 0) * a.H + h) * D;
+            const uint32_t stage = sbase + C::Q0 + s * C::TB;   // (every product that reads Q is done)
 #pragma unroll
             for (int cb = 0; cb < D; cb += 32) {
                 uint32_t o[32];
@@ -328,13 +329,28 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
                     x[i] = __uint_as_float(o[i]) * inv;
                     bad |= !(fabsf(x[i]) < INFINITY);
                 }
-                if (in)
+                if constexpr (seq::kTmaResult<D>) {
+                    seq::stage_columns(stage, quarter * 32 + lane, cb, x);
+                } else if (in) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         *reinterpret_cast<uint4 *>(out + cb + 8 * q) = pack<__nv_bfloat16>(x + 8 * q);
+                }
             }
             if (in) a.lse_w[row * a.H + h] = (m + log2f(l)) * kLn2;
             uint32_t again = __ballot_sync(SGA_FULL_MASK, bad && in && l == l);
+            if constexpr (seq::kTmaResult<D>) {
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll
+                    for (int at = 0; at < C::DA; ++at)
+                        seq::store_atom(&prm.to, stage, at, quarter * 32, h, (int64_t)t.tile * 128 + quarter * 32, a.rows);
+                    tc::bulk_commit();
+                    if (again) tc::bulk_wait_all();
+                    else tc::bulk_wait_read();
+                }
+            }
             __syncwarp();   // (the rows are read back)
             while (again) {
                 const int src = __ffs(again) - 1;
@@ -365,6 +381,7 @@ template <int D, int NS, bool WIN> cudaError_t launch(const SeqArgs &a, cudaStre
     cudaError_t e = seq_tensor_map(&prm.tq, a.Q, a.rows, a.H, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tk, a.K, a.rows, a.Hkv, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tv, a.V, a.rows, a.Hkv, D);
+    if (e == cudaSuccess && seq::kTmaResult<D>) e = seq_tensor_map(&prm.to, a.out_w, a.rows, a.H, D, 32);
     if (e == cudaSuccess) e = allow_smem<seq_fwd_kernel<D, NS, WIN>>(C::BYTES + 1024);
     if (e != cudaSuccess) return e;
     const int64_t units = NS == 1 ? (int64_t)a.n_tiles * a.H

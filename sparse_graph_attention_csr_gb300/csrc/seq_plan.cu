@@ -142,18 +142,23 @@ std::vector<SeqTile> key_tiles(const Mask &m) {
     return all;
 }
 
-// Cuts the walks of key tiles that are more than twice as long as a window's (the
-// sinks' of long sequences, which one block would walk alone while the others are
-// long done), into parts of about a window's length, at least 16 tiles.
-std::vector<SeqJoin> cut_walks(const Mask &m, std::vector<SeqTile> &keys, int &n_parts) {
+// Cuts the walks of key tiles that are twice as long as a window's or more (the sinks'
+// of long sequences, which one block would walk alone while the others are long done)
+// into parts of about a window's length, or of an eighth of an SM's share of all walks,
+// where that is more: fewer parts are fewer sums to join.  3428 rows of four sequences,
+// 4/2 heads of 32, fp32, window 129, a sink: backward 128 us with parts of 16 tiles at
+// least, 72 without the sink.
+std::vector<SeqJoin> cut_walks(const Mask &m, std::vector<SeqTile> &keys, int64_t sm_heads, int &n_parts) {
     std::vector<SeqJoin> joins;
     n_parts = 0;
     if (!m.window) return joins;
-    const int64_t span = (m.window + m.TR - 1) / m.TR * (m.causal ? 1 : 2) + 1, most = std::max<int64_t>(span, 16);
+    int64_t all = 0;
+    for (const SeqTile &t : keys) all += t.t1 - t.t0;
+    const int64_t span = (m.window + m.TR - 1) / m.TR * (m.causal ? 1 : 2) + 1, most = std::max(span, all / (8 * std::max<int64_t>(1, sm_heads)));
     std::vector<SeqTile> out;
     for (const SeqTile &t : keys) {
         const int64_t n = t.t1 - t.t0;
-        if (n <= 2 * most) {
+        if (n < 2 * most) {
             out.push_back(t);
             continue;
         }
@@ -219,7 +224,7 @@ cudaError_t seq_build(sga_seq_plan *p, const std::vector<int32_t> &ptr, const in
     const Mask mask{ptr, p->rows, p->tile_rows, p->causal != 0, p->window, p->sinks};
     const std::vector<SeqTile> q = query_tiles(mask);
     std::vector<SeqTile> k = key_tiles(mask);
-    const std::vector<SeqJoin> joins = cut_walks(mask, k, p->n_parts);
+    const std::vector<SeqJoin> joins = cut_walks(mask, k, p->num_sms / p->Hkv, p->n_parts);
     const bool pairs = p->dt == SGA_BF16 && p->H / p->Hkv % 2 != 0;
     const std::vector<SeqTile> qp = pairs ? pair_list(q) : std::vector<SeqTile>();
     p->n_tiles = (int)q.size();

@@ -31,6 +31,7 @@ template <bool WIN> struct View {
 };
 template <> struct View<true> {
     int64_t lo = 0, hi = 0, slo = 0, shi = 0;
+    int32_t begin = -1;   // of the row's sequence
 };
 template <bool WIN> __device__ __forceinline__ View<WIN> query_view(const SeqArgs &a, int64_t row) {
     View<WIN> v;
@@ -38,6 +39,7 @@ template <bool WIN> __device__ __forceinline__ View<WIN> query_view(const SeqArg
     v.lo = se.x;
     v.hi = a.causal ? row + 1 : se.y;
     if constexpr (WIN) {
+        v.begin = se.x;
         const int64_t lo = max((int64_t)se.x, row - a.window + 1), hi = min(v.hi, row + a.window), s = min((int64_t)se.x + a.sinks, v.hi);
         if (s >= lo) {
             v.hi = max(hi, s);

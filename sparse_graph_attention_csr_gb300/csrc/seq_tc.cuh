@@ -12,7 +12,8 @@ namespace sga {
 // head x 128 rows in the 128-byte swizzle (one column atom of a K-major tile).
 // Rows past the last sequence, and elements past D (D = 32: the box is wider
 // than a head), read as zero.
-cudaError_t seq_tensor_map(CUtensorMap *m, const void *base, int64_t rows, int heads, int D);
+// box_rows: 128, or 32 for a result that each warp stores its share of.
+cudaError_t seq_tensor_map(CUtensorMap *m, const void *base, int64_t rows, int heads, int D, int box_rows = 128);
 
 namespace seq {
 
@@ -21,6 +22,37 @@ template <int DA>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int head, int row, uint64_t *mbar) {
 #pragma unroll
     for (int at = 0; at < DA; ++at) tc::tma_load_3d(dst + at * 16384, map, at * 64, head, row, mbar);
+}
+
+// Results leave through shared memory and TMA where a head fills whole boxes of 64
+// columns: stored by the threads that hold a row each, every 16-byte store of a warp
+// would touch 32 lines.
+template <int D> constexpr bool kTmaResult = D >= 64;
+// 32 columns from c0 of a row of a tile, scaled, into the tile's place (K-major,
+// 128-byte swizzle, as loaded).
+__device__ __forceinline__ void stage_columns(uint32_t tile, int row, int c0, const float *x) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 v = pack<__nv_bfloat16>(x + 8 * q);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(tile + (c0 >> 6) * 16384 + row * 128 +
+                                                                      ((((c0 & 63) / 8 + q) ^ (row & 7)) << 4)),
+                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+    }
+}
+// One lane: 32 rows (from tile row r, packed row `row`) of the tile's column atom to
+// head `head` of the result.
+__device__ __forceinline__ void store_atom(const CUtensorMap *map, uint32_t tile, int atom, int r, int head, int64_t row, int64_t rows) {
+    if (row < rows) tc::tma_store_3d(map, atom * 64, head, (int)row, tile + atom * 16384 + r * 128);
+}
+// Barrier `id` over 64 threads, with whether any of them passed `flag`.
+__device__ __forceinline__ bool pair_any(int id, bool flag) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)flag), "r"(id) : "memory");
+    return r != 0;
 }
 
 // Bit c of the result's word w: column 32 w + c of a tile lies in [lo, hi).

@@ -91,7 +91,7 @@ def visible(n, causal, window, sinks, device="cuda"):
     return vis & (apart >= 0) if causal else vis
 
 
-def shared_offset(k, n, causal, window, sinks):
+def shared_offset(k, n, begin, causal, window, sinks, windowed):
     """[n, D]: the four of a query row's keys whose mean the bf16 dQ pass takes for an offset that all its keys share, in
     the columns where they are no farther apart than half of it (a little more, for the mean's own rounding); zero in the
     others."""
@@ -101,6 +101,11 @@ def shared_offset(k, n, causal, window, sinks):
     lo, hi, s = (i - w + 1).clamp(min=0), torch.minimum(end, i + w), end.clamp(max=sinks)
     apart = s < lo                      # the sinks lie before the window, else the two are one interval
     lo, hi = torch.where(apart, lo, 0), torch.where(apart, hi, torch.maximum(hi, s))
+    # the rows of 32 packed rows that are of one sequence take theirs from what all of them see, if that is anything
+    if windowed:
+        g = torch.div(begin + i, 32, rounding_mode="floor") * 32 - begin
+        l, h = lo[(g + 31).clamp(max=n - 1)], hi[g.clamp(min=0)]
+        lo, hi = torch.where(l < h, l, lo), torch.where(l < h, h, hi)
     m = hi - lo
     m = torch.where(m < 8, m, 2 ** torch.floor(torch.log2(m.double())).long())
     at = torch.stack([lo + (m * (2 * x + 1) >> 3) for x in range(4)])
@@ -126,6 +131,8 @@ def window_reference(seq_ptr, Q, K, V, scale, causal, window, sinks, dOut=None, 
         dQ, dQb, dK, dKb, dV, dVb = z(q), z(q), z(k), z(k), z(v), z(v)
         res |= {"dQ": (dQ, dQb), "dK": (dK, dKb), "dV": (dV, dVb)}
     ptr = [int(x) for x in seq_ptr]
+    # (a window that holds every sequence is none)
+    windowed = bool(window) and max(window, sinks) < max(e - b for b, e in zip(ptr[:-1], ptr[1:]))
     for b, e in zip(ptr[:-1], ptr[1:]):
         n = e - b
         if n == 0:
@@ -160,7 +167,7 @@ def window_reference(seq_ptr, Q, K, V, scale, causal, window, sinks, dOut=None, 
             if R:
                 # dQ is formed as sum_j (dS_j + e_j) k_j - (sum_j e_j) c with |e_j| <= R |dS_j|: off by sum_j e_j (k_j - c),
                 # not sum_j e_j k_j; c is a mean in bf16 (three roundings of at most 2^-8)
-                c = shared_offset(ki, n, causal, window, sinks)
+                c = shared_offset(ki, n, b, causal, window, sinks, windowed)
                 far = (dsv.abs()[:, :, None] * ((ki[None] - c[:, None]).abs() - ki.abs()[None]).clamp(min=0)).sum(1)
                 dQb[b:e, h] += scale * R * (far + 2.0 ** -6 * c.abs() * dsv.abs().sum(1)[:, None])
             dK[b:e, h // g] += scale * (dsv.T @ qi)
