@@ -171,6 +171,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
             tc::mbar_init(&tempty[i], 16);   // the epilogue warps of both CTAs
         }
     }
+    if (warp == 2 && lane == 0) {   // (while the previous kernel ends)
+        for (int i = 0; i < 2; ++i)
+            for (int q = 0; q < C::PARTS; ++q) {
+                if (i == 0 || MODE == FfMode::DX) tc::prefetch_map(&p.ta[i][q]);
+                tc::prefetch_map(&p.tb[i][q]);
+            }
+    }
     wait_previous();
     tc::cluster_sync();   // both CTAs run, their barriers initialised
     if (warp == 0) tc::tmem_alloc_pair(&tmem_base, 512);
@@ -396,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                 }
             }
         }
-        if (stored) tc::bulk_wait_all();
+        if (stored) tc::bulk_wait_read();   // (shared memory stays until then; the kernel's end waits for the rest)
         if (!ok && lane == 0) atomicOr(&g_ff_err, tc::kErrMmaTimeout);
         tc::fence_before_sync();
     }
