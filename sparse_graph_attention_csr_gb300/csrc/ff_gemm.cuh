@@ -413,32 +413,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
     if (warp == 0) tc::tmem_dealloc_pair(tmem_base, 512);
 }
 
-// The shares of the tiles of the last round added in order, and their results; a
-// thread four columns of a row (forward: of the gate and of the up half).
-template <FfMode MODE, bool F32> __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ FfParams p) {
+// Which shares make up each tile of the last round, in the order of their k-blocks:
+// slot[first[t]] .. slot[first[t + 1] - 1] of tile whole + t.
+constexpr int kFfMaxPairs = 128;
+struct FfShares {
+    uint16_t first[kFfMaxPairs + 1], slot[2 * kFfMaxPairs];
+};
+
+// The shares of the tiles of the last round (blockIdx.y) added in order, and their
+// results; a thread four columns of a row (forward: of the gate and of the up half).
+template <FfMode MODE, bool F32>
+__global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ FfParams p, const __grid_constant__ FfShares shares) {
     using C = FfCfg<MODE, F32>;
-    constexpr int Q = C::BN / 4;   // threads of a row
+    constexpr int Q = C::BN / 4, HALVES = MODE == FfMode::FWD ? 2 : 1;   // threads of a row
     wait_previous();
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int c = (int)(id % Q) * 4, r = (int)(id / Q % 256), t = (int)(id / Q / 256);
-    const int tiles = p.tiles_m * p.tiles_n;
-    if (t >= tiles - p.whole) return;
+    const int id = blockIdx.x * 256 + threadIdx.x, c = id % Q * 4, r = id / Q;
     int tm, tn;
-    ff_tile(p.whole + t, p.tiles_m, p.tiles_n, tm, tn);
+    ff_tile(p.whole + blockIdx.y, p.tiles_m, p.tiles_n, tm, tn);
     const int64_t row = (int64_t)tm * 256 + r;
     if (row >= p.rows) return;   // (whose sums were not stored)
-    // the pairs whose shares hold k-blocks of the tile
-    const int64_t all = (int64_t)(tiles - p.whole) * p.kb, b = (int64_t)t * p.kb, e = b + p.kb;
     float y[2][4] = {};
-    for (int pair = (int)(b * p.pairs / all); pair < p.pairs; ++pair) {
-        const int64_t pb = all * pair / p.pairs, pe = all * (pair + 1) / p.pairs;
-        if (pb >= e) break;
-        if (pe <= b || pb == pe) continue;
-        // the share's own units are counted from its first tile
-        const int slot = 2 * pair + (t - (int)(pb / p.kb));
-        const float *src = p.partial + (int64_t)slot * kTileFloats + r * 256 + c;
+    const int end = shares.first[blockIdx.y + 1];
+#pragma unroll 4
+    for (int k = shares.first[blockIdx.y]; k < end; ++k) {
+        const float *src = p.partial + (int64_t)shares.slot[k] * kTileFloats + r * 256 + c;
 #pragma unroll
-        for (int h = 0; h < (MODE == FfMode::FWD ? 2 : 1); ++h) {
+        for (int h = 0; h < HALVES; ++h) {
             const float4 v = *reinterpret_cast<const float4 *>(src + 128 * h);
             y[h][0] += v.x;
             y[h][1] += v.y;
@@ -451,6 +451,12 @@ template <FfMode MODE, bool F32> __global__ void __launch_bounds__(256) ff_join_
     using T = std::conditional_t<F32, float, __nv_bfloat16>;
     auto store = [&](void *base, const float *x) {
         T *dst = static_cast<T *>(base) + row * p.cols + col;
+        if (p.tma_out) {   // (rows on 16 bytes)
+            if (col >= p.cols) return;
+            if constexpr (F32) *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+            else *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (col + k < p.cols) dst[k] = from_f32<T>(x[k]);
@@ -490,7 +496,7 @@ template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32)
         q.kb = q.kb_seg = div(T, 64);
     }
     q.tiles = q.tiles_m * q.tiles_n;
-    const int most = std::max(1, device_sms() / 2);
+    const int most = std::max(1, std::min(device_sms() / 2, kFfMaxPairs));
     q.pairs = (int)std::min<int64_t>(most, q.tiles);
     q.whole = (int)std::min<int64_t>(q.tiles, INT32_MAX);
     const int64_t rest = q.tiles % most;
@@ -564,9 +570,20 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, cuda
     e = launch_early(ff_gemm_kernel<MODE, F32>, dim3(2 * (unsigned)q.pairs), dim3(kFfThreads), C::BYTES + 1024, s, p);
     note_launch(id, s, true);
     if (e != cudaSuccess || !q.split) return e;
-    const int64_t threads = (q.tiles - q.whole) * 256 * (C::BN / 4);
+    const int rest = (int)(q.tiles - q.whole);   // (less than the pairs)
+    FfShares shares{};
+    int n = 0, begun = 0;   // shares, tiles that have one
+    for (int pair = 0; pair < q.pairs; ++pair) {   // (end to end: the tiles and their k-blocks in order)
+        const FfUnits units((int)q.tiles, q.whole, (int)q.kb, q.pairs, pair);
+        FfUnit u;
+        for (int i = units.full; units.get(i, u); ++i) {
+            if (u.tile - q.whole == begun) shares.first[begun++] = (uint16_t)n;
+            shares.slot[n++] = (uint16_t)u.slot;
+        }
+    }
+    shares.first[rest] = (uint16_t)n;
     note_launch(SGA_KERN_FF_JOIN, s, false);
-    e = launch_early(ff_join_kernel<MODE, F32>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, p);
+    e = launch_early(ff_join_kernel<MODE, F32>, dim3(C::BN / 4, (unsigned)rest), dim3(256), 0, s, p, shares);   // (256 rows of BN / 4 threads)
     note_launch(SGA_KERN_FF_JOIN, s, true);
     return e;
 }

@@ -402,8 +402,10 @@ template <bool WIN> cudaError_t seq_fwd_bf16(const SeqArgs &a, int D, cudaStream
     // Measured, one : two tiles a CTA, D = 128, causal: 2048 rows, 8/2 heads
     // (128 tiles) 31 : 35 us; 4096 (256) 54.5 : 55.7; 8192 (512) 117 : 103.
     // D = 64: causal 4096 rows, 8 heads 43 : 48, 8192 80 : 84; full 4096 rows,
-    // 16 heads 92 : 88.
-    const bool one = (int64_t)a.n_tiles * a.H <= 2 * (int64_t)a.num_sms || (D <= 64 && a.causal);
+    // 16 heads 92 : 88.  With a window units are short and alike: D = 64, 24576 rows,
+    // 8 heads, full, window 100, 58 : 72; causal, window 1024, 86 : 94 (8/2 heads 84 :
+    // 81); D = 128, 34270 rows, 8/2 heads, causal, window 1000, 172 : 162.
+    const bool one = (int64_t)a.n_tiles * a.H <= 2 * (int64_t)a.num_sms || (D <= 64 && (a.causal || WIN));
     if (D == 32) return one ? launch<32, 1, WIN>(a, s) : launch<32, 2, WIN>(a, s);
     if (D == 64) return one ? launch<64, 1, WIN>(a, s) : launch<64, 2, WIN>(a, s);
     return one ? launch<128, 1, WIN>(a, s) : launch<128, 2, WIN>(a, s);
