@@ -87,12 +87,19 @@ struct Named {
 Named named(const char *n, const Tensor &t) { return {n, &t}; }
 Named named(const char *n, const Maybe &t) { return {n, t ? &*t : nullptr}; }
 
+// The bytes from a tensor's first element to its last (strides are not negative).
+int64_t span_bytes(const Tensor &t) {
+    int64_t last = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    return (last + 1) * (int64_t)t.element_size();
+}
+
 // Outputs must not share memory with inputs or one another.
 void distinct(std::initializer_list<Named> outs, std::initializer_list<Named> ins) {
     auto clash = [](const Named &a, const Named &b) {
         if (!a.t || !b.t || a.t->numel() == 0 || b.t->numel() == 0) return;
         const char *p = static_cast<const char *>(a.t->data_ptr()), *q = static_cast<const char *>(b.t->data_ptr());
-        if (p < q + b.t->nbytes() && q < p + a.t->nbytes())
+        if (p < q + span_bytes(*b.t) && q < p + span_bytes(*a.t))
             throw py::value_error(std::string(a.name) + " shares memory with " + b.name);
     };
     for (auto o = outs.begin(); o != outs.end(); ++o) {

@@ -196,31 +196,32 @@ __device__ __forceinline__ void out_row_alone(const SeqArgs &a, int64_t row, int
     q.load(a.Q, at);
     acc.zero();
     float m = -INFINITY, l = 0.f;
-    for (int part = WIN ? 0 : 1; part < 2; ++part)   // (the sinks, the interval)
-      for (int64_t j = first_of(sp, part), e = end_of(sp, part); j < e && !acc.all_nan(want); j += kStep) {
-        RowFrag<T, D> v[kStep];
-        float s[kStep], mn = m;
+    for (int part = WIN ? 0 : 1; part < 2; ++part) {   // (the sinks, the interval)
+        for (int64_t j = first_of(sp, part), e = end_of(sp, part); j < e && !acc.all_nan(want); j += kStep) {
+            RowFrag<T, D> v[kStep];
+            float s[kStep], mn = m;
 #pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            RowFrag<T, D> k;
-            const int64_t r = (min(j + u, e - 1) * a.Hkv + hk) * D;
-            k.load(a.K, r);
-            v[u].load(a.V, r);
-            s[u] = q.dot(k) * (a.scale * kLog2e);
-            mn = fmaxf(mn, s[u]);   // (the last row again behind the interval)
-        }
-        const float al = exp2_diff(m, mn);
-        m = mn;
-        l *= al;
-#pragma unroll
-        for (int i = 0; i < RowFrag<T, D>::W; ++i) acc.x[i] *= al;
-#pragma unroll
-        for (int u = 0; u < kStep; ++u)
-            if (j + u < e) {
-                const float p = exp2_diff(s[u], m);
-                l += p;
-                acc.add(p, v[u]);
+            for (int u = 0; u < kStep; ++u) {
+                RowFrag<T, D> k;
+                const int64_t r = (min(j + u, e - 1) * a.Hkv + hk) * D;
+                k.load(a.K, r);
+                v[u].load(a.V, r);
+                s[u] = q.dot(k) * (a.scale * kLog2e);
+                mn = fmaxf(mn, s[u]);   // (the last row again behind the interval)
             }
+            const float al = exp2_diff(m, mn);
+            m = mn;
+            l *= al;
+#pragma unroll
+            for (int i = 0; i < RowFrag<T, D>::W; ++i) acc.x[i] *= al;
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+                if (j + u < e) {
+                    const float p = exp2_diff(s[u], m);
+                    l += p;
+                    acc.add(p, v[u]);
+                }
+        }
     }
     acc.store(a.out_w, at, 1.f / l, want);
 }
@@ -274,21 +275,22 @@ __device__ __forceinline__ void query_row_alone(const SeqArgs &a, int64_t row, i
     q.load(a.Q, at);
     g.load(a.dOut, at);
     acc.zero();
-    for (int part = WIN ? 0 : 1; part < 2; ++part)   // (the sinks, the interval)
-      for (int64_t j = first_of(sp, part), e = end_of(sp, part); j < e && !acc.all_nan(want); j += kStep) {
-        RowFrag<T, D> k[kStep];
-        float w[kStep];
+    for (int part = WIN ? 0 : 1; part < 2; ++part) {   // (the sinks, the interval)
+        for (int64_t j = first_of(sp, part), e = end_of(sp, part); j < e && !acc.all_nan(want); j += kStep) {
+            RowFrag<T, D> k[kStep];
+            float w[kStep];
 #pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            RowFrag<T, D> v;
-            const int64_t r = (min(j + u, e - 1) * a.Hkv + hk) * D;
-            k[u].load(a.K, r);
-            v.load(a.V, r);
-            w[u] = fast_exp2(fmaf(q.dot(k[u]), a.scale * kLog2e, nlse)) * (g.dot(v) + nd);
+            for (int u = 0; u < kStep; ++u) {
+                RowFrag<T, D> v;
+                const int64_t r = (min(j + u, e - 1) * a.Hkv + hk) * D;
+                k[u].load(a.K, r);
+                v.load(a.V, r);
+                w[u] = fast_exp2(fmaf(q.dot(k[u]), a.scale * kLog2e, nlse)) * (g.dot(v) + nd);
+            }
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+                if (j + u < e) acc.add(w[u], k[u]);
         }
-#pragma unroll
-        for (int u = 0; u < kStep; ++u)
-            if (j + u < e) acc.add(w[u], k[u]);
     }
     acc.store(a.dQ, at, a.scale, want);
 }

@@ -260,6 +260,9 @@ def test_refusals():
         f(sga.Rotary(32), Q, K, pos)
     with pytest.raises(ValueError, match="shares memory"):
         f(rot, Q, K, pos, out_q=Q, out_k=Q[:, :1].reshape(-1)[:0].new_empty(0).set_(Q.untyped_storage(), 0, (8, 1, 64)))
+    buf = torch.randn(8, 6, 64, device="cuda")   # results among the rows of the slices that they are formed from
+    with pytest.raises(ValueError, match="out_q shares memory with Q"):
+        f(rot, buf[:, :2], buf[:, 2:3], pos, out_q=buf.view(-1)[-8 * 2 * 64:].view(8, 2, 64))
     _, _, rq, rk = f(rot, Q, K, pos, wq, wk)
     b = sga.qk_norm_rope_bwd
     with pytest.raises(ValueError, match="both rq and rk"):
