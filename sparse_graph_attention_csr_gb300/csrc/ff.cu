@@ -96,13 +96,15 @@ __global__ void __launch_bounds__(256) ff_slopes_kernel(const T *G, const T *U, 
         load8<T, VEC>(G + at, c, dg.cols, g);
         load8<T, VEC>(U + at, c, dg.cols, u);
         load8<T, VEC>(dOut + at, c, dg.cols, d);
+        ff_with_slope(act, [&](auto f) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            float a, slope;
-            ff_act_slope(g[k], act, a, slope);
-            g[k] = d[k] * u[k] * slope;
-            u[k] = d[k] * a;
-        }
+            for (int k = 0; k < 8; ++k) {
+                float a, slope;
+                f(g[k], a, slope);
+                g[k] = d[k] * u[k] * slope;
+                u[k] = d[k] * a;
+            }
+        });
         store_parts<sizeof(T) == 4>(const_cast<__nv_bfloat16 *>(dg.p) + row * dg.ld + c, dg.part_elems(), g);
         store_parts<sizeof(T) == 4>(const_cast<__nv_bfloat16 *>(du.p) + row * du.ld + c, du.part_elems(), u);
     }

@@ -55,24 +55,33 @@ __device__ __forceinline__ float ff_phi(float x) {
 
 // act(g).  Exponentials and quotients by the MUFU instructions: off by a few units of
 // fp32, and half a unit more for each unit of |g|.
-__device__ __forceinline__ float ff_act(float g, int act) {
-    if (act == SGA_ACT_SILU) return __fdividef(g, 1.f + fast_exp2(-kLog2e * g));
-    if (act == SGA_ACT_GELU) return g * ff_phi(g);
-    return g != g ? g : fmaxf(g, 0.f);
+__device__ __forceinline__ float ff_silu(float g) { return __fdividef(g, 1.f + fast_exp2(-kLog2e * g)); }
+__device__ __forceinline__ float ff_relu(float g) { return g != g ? g : fmaxf(g, 0.f); }
+// Calls f with the activation.
+template <typename F> __device__ __forceinline__ void ff_with_act(int act, F f) {
+    if (act == SGA_ACT_SILU) f([](float g) { return ff_silu(g); });
+    else if (act == SGA_ACT_GELU) f([](float g) { return g * ff_phi(g); });
+    else f([](float g) { return ff_relu(g); });
 }
-// act(g) and its derivative (relu: 0 at 0)
-__device__ __forceinline__ void ff_act_slope(float g, int act, float &a, float &slope) {
+// Calls f with a function of g, a, slope: the activation and its derivative (relu: 0 at 0).
+template <typename F> __device__ __forceinline__ void ff_with_slope(int act, F f) {
     if (act == SGA_ACT_SILU) {
-        const float s = __fdividef(1.f, 1.f + fast_exp2(-kLog2e * g));
-        a = g * s;
-        slope = fmaf(a, 1.f - s, s);
+        f([](float g, float &a, float &slope) {
+            const float s = __fdividef(1.f, 1.f + fast_exp2(-kLog2e * g));
+            a = g * s;
+            slope = fmaf(a, 1.f - s, s);
+        });
     } else if (act == SGA_ACT_GELU) {
-        const float p = ff_phi(g);
-        a = g * p;
-        slope = fmaf(g * 0.39894228040143268f, fast_exp2(-0.5f * kLog2e * g * g), p);
+        f([](float g, float &a, float &slope) {
+            const float p = ff_phi(g);
+            a = g * p;
+            slope = fmaf(g * 0.39894228040143268f, fast_exp2(-0.5f * kLog2e * g * g), p);
+        });
     } else {
-        a = g != g ? g : fmaxf(g, 0.f);
-        slope = g > 0.f ? 1.f : 0.f;
+        f([](float g, float &a, float &slope) {
+            a = ff_relu(g);
+            slope = g > 0.f ? 1.f : 0.f;
+        });
     }
 }
 

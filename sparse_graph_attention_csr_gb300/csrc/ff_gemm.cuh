@@ -16,8 +16,9 @@
 // fp32: an operand is the sum of three bf16 parts (8 + 8 + 8 bits); of the nine
 // products of parts the six that reach 2^-24 of the result are taken, smallest
 // first.  The tensor core's accumulator drops what falls below its last bit, which
-// adds up over a long depth, so each k-block of 64 is added to fp32 registers by
-// itself: 4 products of the leading parts round nothing worth mentioning.
+// adds up over a long depth, so sums of four k-blocks (256 deep) are added to fp32
+// registers: 16 additions of the leading parts' products drop at most 2^-19 of a sum,
+// and about 2^-22 of its terms' size.
 //
 // Tiles are dealt to the pairs by whole rounds; the last, incomplete round would
 // leave pairs idle, so its tiles' depth is cut into equal shares, which leave fp32
@@ -155,7 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
     using C = FfCfg<MODE, F32>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[C::NST], empty[C::NST], tfull[2], tempty[2];
+    __shared__ uint64_t full[C::NST], empty[C::NST][C::PARTS], tfull[2], tempty[2];
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem), rank = tc::cluster_rank();
@@ -164,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
     if (tid == 32) {
         for (int i = 0; i < C::NST; ++i) {
             tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
+            for (int q = 0; q < C::PARTS; ++q) tc::mbar_init(&empty[i][q], 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&tfull[i], 1);
@@ -197,7 +198,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                 ff_tile(u.tile, p.tiles_m, p.tiles_n, tm, tn);
                 for (int kb = u.k0; kb < u.k1; ++kb, ++it) {
                     const int s = it % C::NST, r = it / C::NST;
-                    if (r >= 1 && !tc::mbar_wait_cluster(&empty[s], (r - 1) & 1, tc::kWaitLimit)) {
+                    // (the parts' places get free one after the other, the smallest's first)
+                    if (r >= 1 && !tc::mbar_wait_cluster(&empty[s][C::PARTS - 1], (r - 1) & 1, tc::kWaitLimit)) {
                         ok = false;
                         break;
                     }
@@ -217,7 +219,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                         n0 = (tn - (b ? p.tiles_n / 2 : 0)) * 256 + rank * 128;
                     }
 #pragma unroll
-                    for (int q = 0; q < C::PARTS; ++q) {
+                    for (int q = C::PARTS - 1; q >= 0; --q) {
+                        if (q < C::PARTS - 1 && r >= 1) ok = ok && tc::mbar_wait_cluster(&empty[s][q], (r - 1) & 1, tc::kWaitLimit);
                         const uint32_t pa = at + q * C::TB, pb = at + (C::PARTS + q) * C::TB;
                         const CUtensorMap *ma = &p.ta[MODE == FfMode::DX ? seg : 0][q], *mb = &p.tb[b][q];
                         if (C::A_MN) {
@@ -233,11 +236,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                             tc::tma_load_2d_pair(pb, mb, k, n0, bar);
                         }
                     }
+                    if (!ok) {   // (all of the stage is on its way, so that it can be waited for)
+                        ++it;
+                        break;
+                    }
                 }
             }
             // (what the products' completion arrives at, here and in the other CTA, stays until it has)
             for (int i = it - 1; ok && i >= 0 && i >= it - C::NST; --i)
-                ok = tc::mbar_wait_cluster(&empty[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
+                for (int q = 0; q < C::PARTS; ++q) ok = ok && tc::mbar_wait_cluster(&empty[i % C::NST][q], (i / C::NST) & 1, tc::kWaitLimit);
             if (!ok) atomicOr(&g_ff_err, tc::kErrMmaTimeout);
             // loads of both CTAs that no product consumed (only after a timeout) land before the pair ends
             if (rank == 0)
@@ -274,8 +281,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                                 tc::mma_bf16_pair_w(d, C::A_MN ? tc::desc_sw128_mn(a + kk * 2048, 8192) : tc::desc_sw128(a + kk * 32),
                                                     C::B_MN ? tc::desc_sw128_mn(b + kk * 2048, 8192) : tc::desc_sw128(b + kk * 32), idesc,
                                                     kb > c0 || q > 0 || kk > 0);
+                            // a part's place is free after the last product that takes it
+                            if (F32 && q == 1) tc::mma_commit_pair_w(&empty[s][2]);
+                            if (F32 && q == 4) tc::mma_commit_pair_w(&empty[s][1]);
                         }
-                        tc::mma_commit_pair_w(&empty[s]);
+                        tc::mma_commit_pair_w(&empty[s][0]);
                     }
                     tc::mma_commit_pair_w(&tfull[buf]);
                 }
@@ -334,27 +344,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
             }
             const int which = MODE == FfMode::DW && 2 * tn >= p.tiles_n;   // dWu
             const int64_t col0 = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN;
-            if constexpr (!F32) {
-                // 64 columns of one result at a time, staged in the swizzle of its tensor map
-                constexpr int PIECES = MODE == FfMode::FWD ? 3 : 2;
+            // 64 columns x[0 .. 63] of result o, from column col
+            auto store = [&](int o, const float *x, int64_t col) {
+                if constexpr (F32) {
 #pragma unroll
-                for (int x = 0; x < PIECES; ++x) {
-                    if (MODE == FfMode::FWD && x > 0 && !p.out[x]) break;
-                    const int64_t col = col0 + (MODE == FfMode::FWD ? half * 64 : half * 128 + x * 64);
-                    const int o = MODE == FfMode::FWD ? x : which;
+                    for (int j = 0; j < 64; j += 32)
+                        if (rows > 0 && col + j < p.cols)
+                            ff_store_block(stage, x + j, static_cast<float *>(p.out[o]) + row0 * p.cols + col + j, p.cols, rows,
+                                           (int)min((int64_t)32, p.cols - col - j), p.tma_out);
+                } else {   // staged in the swizzle of its tensor map
                     if (stored) tc::bulk_wait_read();   // (the lane that stored; others have nothing to wait for)
                     __syncwarp();
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        float y[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int e = 8 * c + k;
-                            if (MODE != FfMode::FWD) y[k] = acc[64 * x + e];
-                            else if (x == 0) y[k] = ff_act(acc[e], p.act) * acc[64 + e];
-                            else y[k] = acc[64 * (x - 1) + e];
-                        }
-                        const uint4 v = pack<__nv_bfloat16>(y);
+                        const uint4 v = pack<__nv_bfloat16>(x + 8 * c);
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(v.x),
                                      "r"(v.y), "r"(v.z), "r"(v.w)
                                      : "memory");
@@ -362,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                     if (p.tma_out) {
                         tc::fence_proxy_async();
                         __syncwarp();
-                        if (lane == 0 && col < p.cols && row0 < p.rows) {
+                        if (lane == 0 && col < p.cols && rows > 0) {
                             tc::tma_store_2d(&p.to[o], (int)col, (int)row0, stage);
                             tc::bulk_commit();
                             stored = true;
@@ -370,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                     } else {   // rows off 16 bytes: two elements a lane, a row at a time
                         __syncwarp();
                         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out[o]);
-                        for (int q = 0; q < 32 && row0 + q < p.rows; ++q) {
+                        for (int q = 0; q < rows; ++q) {
                             uint32_t v;
                             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(stage + q * 128 + (((lane >> 2) ^ (q & 7)) << 4) + (lane & 3) * 4));
                             unsigned short *d = reinterpret_cast<unsigned short *>(dst + (row0 + q) * p.cols + col + 2 * lane);
@@ -379,28 +382,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                         }
                     }
                 }
-            } else {
-                constexpr int PIECES = MODE == FfMode::FWD ? 3 : 1, BLOCKS = MODE == FfMode::FWD ? 2 : 4;
-#pragma unroll
-                for (int x = 0; x < PIECES; ++x) {
-                    if (rows <= 0 || (MODE == FfMode::FWD && x > 0 && !p.out[x])) break;
-                    float *dst = static_cast<float *>(p.out[MODE == FfMode::FWD ? x : which]) + row0 * p.cols;
-#pragma unroll
-                    for (int j = 0; j < BLOCKS; ++j) {
-                        const int64_t col = col0 + half * (32 * BLOCKS) + 32 * j;
-                        const int cols = (int)max((int64_t)0, min((int64_t)32, p.cols - col));
-                        if (MODE != FfMode::FWD) {
-                            ff_store_block(stage, acc + 32 * j, dst + col, p.cols, rows, cols, p.tma_out);
-                        } else if (x > 0) {
-                            ff_store_block(stage, acc + 64 * (x - 1) + 32 * j, dst + col, p.cols, rows, cols, p.tma_out);
-                        } else {
-                            float y[32];
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) y[k] = ff_act(acc[32 * j + k], p.act) * acc[64 + 32 * j + k];
-                            ff_store_block(stage, y, dst + col, p.cols, rows, cols, p.tma_out);
-                        }
-                    }
+            };
+            if constexpr (MODE == FfMode::FWD) {
+                const int64_t col = col0 + half * 64;
+                if (p.out[1]) {
+                    store(1, acc, col);
+                    store(2, acc + 64, col);
                 }
+                // (one activation's code after the other: chosen per element, it did not
+                // fit the instruction caches)
+                ff_with_act(p.act, [&](auto f) {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) acc[e] = f(acc[e]) * acc[64 + e];
+                });
+                store(0, acc, col);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) store(which, acc + 64 * x, col0 + half * 128 + 64 * x);
             }
         }
         if (stored) tc::bulk_wait_read();   // (shared memory stays until then; the kernel's end waits for the rest)
@@ -463,11 +461,15 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ Ff
     };
     if (MODE == FfMode::FWD) {
         float o[4];
+        ff_with_act(p.act, [&](auto f) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = ff_act(y[0][k], p.act) * y[1][k];
+            for (int k = 0; k < 4; ++k) o[k] = f(y[0][k]) * y[1][k];
+        });
         store(p.out[0], o);
-        if (p.out[1]) store(p.out[1], y[0]);
-        if (p.out[2]) store(p.out[2], y[1]);
+        if (p.out[1]) {
+            store(p.out[1], y[0]);
+            store(p.out[2], y[1]);
+        }
     } else {
         store(p.out[which], y[0]);
     }
@@ -561,7 +563,10 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, cuda
     p.tiles_n = (int)q.tiles_n;
     p.kb = (int)q.kb;
     p.kb_seg = (int)q.kb_seg;
-    p.depth = F32 ? 1 : 256;   // bf16: sums of 16384 products drop at most 2^-14 of their size on the way
+    // bf16: sums of 16384 products drop at most 2^-14 of their size on the way.  fp32,
+    // 8192 x 1024 x 4096: 1 k-block 544 us (reading the sums takes a third of the
+    // tensor cores' time), 2 473, 4 450, 8 440.
+    p.depth = F32 ? 4 : 256;
     p.pairs = q.pairs;
     p.whole = q.whole;
     p.act = a.act;

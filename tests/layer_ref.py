@@ -195,9 +195,9 @@ def _act(g, act):
 
 def _product(a, ab, b, bb, dt, n):
     """a b and its bound from the operands'.  A sum of n products on the tensor cores: every addition drops at most 2 U of
-    what has been summed (bf16: in runs of 16384; fp32: in runs of 64, of products of parts that leave out 2 U), and the
+    what has been summed (bf16: in runs of 16384; fp32: in runs of 256, of products of parts that leave out 2 U), and the
     runs' fp32 sums."""
-    run = 64 if dt == torch.float32 else 16384
+    run = 256 if dt == torch.float32 else 16384
     k = 2 * (min(n, run) + 8) + n / run + 4
     mag = a.abs() @ b.abs()
     return a @ b, k * U * mag + ab @ b.abs() + a.abs() @ bb + ab @ bb
