@@ -1070,14 +1070,18 @@ class Embedding(torch.autograd.Function):
         return None, dTable, None, None
 
 
+def _begin16(t):
+    """t, contiguous and beginning on a 16-byte boundary (a copy where it is not)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _rows16(t):
     """t [T, heads, D], or a copy of it where its heads are not dense within a row
     or its rows not on 16-byte boundaries."""
-    if t.dim() != 3 or t.is_contiguous():
-        return t
-    ok = t.stride(2) == 1 and t.stride(1) == t.shape[2] and t.stride(0) >= t.shape[1] * t.shape[2] \
-        and t.stride(0) * t.element_size() % 16 == 0 and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    dense = t.dim() == 3 and t.stride(2) == 1 and t.stride(1) == t.shape[2] \
+        and t.stride(0) >= t.shape[1] * t.shape[2] and t.stride(0) * t.element_size() % 16 == 0
+    return t if dense and t.data_ptr() % 16 == 0 else _begin16(t)
 
 
 class QKNormRope(torch.autograd.Function):
@@ -1099,14 +1103,8 @@ class QKNormRope(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dQo, dKo):
         Q, K, pos, wq, wk, rq, rk = ctx.saved_tensors
-        dQ, dK, dwq, dwk = qk_norm_rope_bwd(ctx.rot, Q, K, pos, wq, wk, rq, rk, dQo.contiguous(), dKo.contiguous())
+        dQ, dK, dwq, dwk = qk_norm_rope_bwd(ctx.rot, Q, K, pos, wq, wk, rq, rk, _begin16(dQo), _begin16(dKo))
         return dQ, dK, None, dwq, dwk, None, None
-
-
-def _begin16(t):
-    """t, contiguous and beginning on a 16-byte boundary (a copy where it is not)."""
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 class GatedFF(torch.autograd.Function):

@@ -283,17 +283,19 @@ template <typename L, int D> __device__ __forceinline__ void block_sums(float *s
     }
 }
 
-// Blocks an SM of the backward pass, each with a row of sums: as registers allow
-// (69636 rows of 16/4 heads of 128 bf16 202 us with four, 192 with three; 30011 rows of
-// 4/4 heads of 64 fp32 42 with four, 46 with three).
-template <typename T> constexpr int kBwdBlocksPerSm = sizeof(T) == 2 ? 3 : 4;
+// Blocks an SM of the backward pass, each with a row of sums, and heads in flight: as
+// registers allow (69636 rows of 16/4 heads of 128 bf16 192 us with three blocks and
+// two heads, 202 with four blocks, or one head; 30011 rows of 4/4 heads of 64 fp32 38
+// with three blocks and four heads, 39 with four blocks, 42 and 46 with four and three
+// of two).
+constexpr int kBwdBlocksPerSm = 3;
 
 // The queries of all rows, then the keys: one weight's sums at a time in registers,
 // which pays for forming the turns again (another pair would leave room for fewer blocks).
 template <typename T, typename TW, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm<T>) qk_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) qk_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
     using L = Lane<T, D, INTER>;
-    constexpr int EL = L::EL, G = L::G, U = 2;
+    constexpr int EL = L::EL, G = L::G, U = sizeof(T) == 4 ? 4 : 2;
     __shared__ float sums[kThreads / 32 * D];
     let_next_start();
     wait_previous();
@@ -439,7 +441,7 @@ template <typename T, typename TW, int D, bool INTER> cudaError_t launch_bwd(Rop
     const int fit = per_device(per_sm, [&] {
         int n = 0;
         asked = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, qk_rope_bwd_kernel<T, TW, D, INTER>, kThreads, 0);
-        return asked == cudaSuccess ? std::max(1, std::min(n, kBwdBlocksPerSm<T>)) : 0;
+        return asked == cudaSuccess ? std::max(1, std::min(n, kBwdBlocksPerSm)) : 0;
     });
     if (asked != cudaSuccess) return asked;
     const int blocks = (int)std::min<int64_t>((a.T * a.parts + groups - 1) / groups, (int64_t)device_sms() * fit);
@@ -555,7 +557,7 @@ sga_status qk_norm_rope_fwd(const sga_rotary *rot, const void *Q, int64_t ldq, c
 
 size_t sga_qk_norm_rope_bwd_workspace_bytes(int64_t T, int D) {
     if (T <= 0 || D <= 0) return 0;
-    return (size_t)device_sms() * kBwdBlocksPerSm<float> * 2 * (size_t)D * sizeof(float);
+    return (size_t)device_sms() * kBwdBlocksPerSm * 2 * (size_t)D * sizeof(float);
 }
 
 sga_status qk_norm_rope_bwd(const sga_rotary *rot, const void *Q, int64_t ldq, const void *K, int64_t ldk, const void *pos,

@@ -198,6 +198,15 @@ def test_autograd_and_streams():
     y = torch.randn(50, 64, 4, device="cuda").transpose(1, 2)
     q2, k2 = sga.QKNormRope.apply(y, y, pos, None, None, rot, None)
     assert torch.equal(q2, sga.qk_norm_rope_fwd(rot, y.contiguous(), y.contiguous(), pos, eps=None)[0]) and torch.equal(q2, k2)
+    # tensors, and gradients, that do not begin on 16 bytes too
+    z = torch.randn(2 * 50 * 4 * 64 + 1, device="cuda")
+    a, g = z[1:1 + 50 * 256].view(50, 4, 64), z[1 + 50 * 256:].view(50, 4, 64)
+    a.requires_grad_()
+    q3, k3 = sga.QKNormRope.apply(a, a.detach(), pos, None, None, rot, 1e-6)
+    (ga,) = torch.autograd.grad(q3, a, g)
+    d = a.detach().clone()
+    r3 = sga.qk_norm_rope_fwd(rot, d, d, pos)
+    assert torch.equal(q3, r3[0]) and torch.equal(ga, sga.qk_norm_rope_bwd(rot, d, d, pos, None, None, r3[2], r3[3], g.clone(), torch.zeros_like(d))[0])
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     r2 = sga.qk_norm_rope_fwd(rot, xd[:, :4], xd[:, 4:6], pos, wq.detach(), wk.detach(), stream=s)
