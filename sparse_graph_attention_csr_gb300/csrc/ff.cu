@@ -49,6 +49,8 @@ template <bool F32> __device__ __forceinline__ void store_parts(__nv_bfloat16 *d
 }
 
 // Elements c .. c + 7 of a row of `cols` (zeros past its end).  VEC: whole 16 bytes.
+// (The 16 bytes around elements that begin elsewhere, moved down in registers, took
+// longer than one load an element: dG and dU of 4099 x 803 fp32 22 against 17 us.)
 template <typename T, bool VEC> __device__ __forceinline__ void load8(const T *row, int64_t c, int64_t cols, float *x) {
     if constexpr (VEC) {
         constexpr int EL = Elt<T>::EL;
@@ -245,7 +247,9 @@ sga_status gated_ff_fwd(const void *X, const void *Wg, const void *Wu, int64_t T
     p.u = U;
     p.partial = reinterpret_cast<float *>(w.base + w.used);
     cudaError_t e = lay_out(lay, w.f32, s);
-    if (e == cudaSuccess) e = w.f32 ? ff_product<FfMode::FWD, true>(p, s) : ff_product<FfMode::FWD, false>(p, s);
+    FfShares shares{}, none{};
+    if (e == cudaSuccess) e = w.f32 ? ff_product<FfMode::FWD, true>(p, shares, s) : ff_product<FfMode::FWD, false>(p, shares, s);
+    if (e == cudaSuccess) e = w.f32 ? ff_join<true, true>(shares, none, s) : ff_join<true, false>(shares, none, s);
     return status_of(e);
 }
 
@@ -257,7 +261,8 @@ size_t sga_gated_ff_bwd_workspace_bytes(int64_t T, int64_t F, int64_t M, sga_dty
     w.take(nullptr, F, M, nullptr);
     w.operand(T, M);
     w.operand(T, M);
-    w.bytes(std::max(partial_bytes<FfMode::DX>(T, F, M, w.f32), partial_bytes<FfMode::DW>(T, F, M, w.f32)));
+    w.bytes(partial_bytes<FfMode::DX>(T, F, M, w.f32));
+    w.bytes(partial_bytes<FfMode::DW>(T, F, M, w.f32));
     return w.used;
 }
 
@@ -294,18 +299,21 @@ sga_status gated_ff_bwd(const void *X, const void *Wg, const void *Wu, const voi
     p.F = F;
     p.M = M;
     p.act = act;
-    p.partial = reinterpret_cast<float *>(w.base + w.used);
     cudaError_t e = lay_out(lay, w.f32, s);
     if (e == cudaSuccess) e = w.f32 ? slopes<float>(G, U, dOut, act, p.dg, p.du, s) : slopes<__nv_bfloat16>(G, U, dOut, act, p.dg, p.du, s);
+    FfShares of_x{}, of_w{};
     if (dX && e == cudaSuccess) {
         p.out = dX;
-        e = w.f32 ? ff_product<FfMode::DX, true>(p, s) : ff_product<FfMode::DX, false>(p, s);
+        p.partial = reinterpret_cast<float *>(w.base + w.bytes(partial_bytes<FfMode::DX>(T, F, M, w.f32)));
+        e = w.f32 ? ff_product<FfMode::DX, true>(p, of_x, s) : ff_product<FfMode::DX, false>(p, of_x, s);
     }
     if (dWg && e == cudaSuccess) {
         p.g = dWg;
         p.u = dWu;
-        e = w.f32 ? ff_product<FfMode::DW, true>(p, s) : ff_product<FfMode::DW, false>(p, s);
+        p.partial = reinterpret_cast<float *>(w.base + w.bytes(partial_bytes<FfMode::DW>(T, F, M, w.f32)));
+        e = w.f32 ? ff_product<FfMode::DW, true>(p, of_w, s) : ff_product<FfMode::DW, false>(p, of_w, s);
     }
+    if (e == cudaSuccess) e = w.f32 ? ff_join<false, true>(of_x, of_w, s) : ff_join<false, false>(of_x, of_w, s);
     return status_of(e);
 }
 

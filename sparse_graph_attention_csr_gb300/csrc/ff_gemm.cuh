@@ -411,30 +411,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
     if (warp == 0) tc::tmem_dealloc_pair(tmem_base, 512);
 }
 
-// Which shares make up each tile of the last round, in the order of their k-blocks:
-// slot[first[t]] .. slot[first[t + 1] - 1] of tile whole + t.
+// A product's tiles of the last round, whose shares are to be joined: which ones make
+// up each, in the order of their k-blocks (slot[first[t]] .. slot[first[t + 1] - 1] of
+// tile whole + t).
 constexpr int kFfMaxPairs = 128;
 struct FfShares {
+    const float *partial;
+    void *out[3];
+    int64_t rows, cols;
+    int tiles_m, tiles_n, whole, tiles;   // tiles: of the last round
+    int act, wide;                        // wide: rows on 16 bytes
     uint16_t first[kFfMaxPairs + 1], slot[2 * kFfMaxPairs];
 };
 
-// The shares of the tiles of the last round (blockIdx.y) added in order, and their
-// results; a thread four columns of a row (forward: of the gate and of the up half).
-template <FfMode MODE, bool F32>
-__global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ FfParams p, const __grid_constant__ FfShares shares) {
-    using C = FfCfg<MODE, F32>;
-    constexpr int Q = C::BN / 4, HALVES = MODE == FfMode::FWD ? 2 : 1;   // threads of a row
+// The shares of a tile (blockIdx.y) added in order, and its results; a thread four
+// columns of a row (forward: of the gate and of the up half).  The backward's two
+// products are joined together (the first's tiles before the second's).
+template <bool FWD, bool F32>
+__global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ FfShares a, const __grid_constant__ FfShares b) {
+    constexpr int Q = (FWD ? 128 : 256) / 4, HALVES = FWD ? 2 : 1;   // threads of a row
     wait_previous();
+    const bool second = !FWD && (int)blockIdx.y >= a.tiles;   // dWg, dWu
+    const FfShares &p = second ? b : a;
+    const int t = (int)blockIdx.y - (second ? a.tiles : 0);
     const int id = blockIdx.x * 256 + threadIdx.x, c = id % Q * 4, r = id / Q;
     int tm, tn;
-    ff_tile(p.whole + blockIdx.y, p.tiles_m, p.tiles_n, tm, tn);
+    ff_tile(p.whole + t, p.tiles_m, p.tiles_n, tm, tn);
     const int64_t row = (int64_t)tm * 256 + r;
     if (row >= p.rows) return;   // (whose sums were not stored)
     float y[2][4] = {};
-    const int end = shares.first[blockIdx.y + 1];
+    const int end = p.first[t + 1];
 #pragma unroll 4
-    for (int k = shares.first[blockIdx.y]; k < end; ++k) {
-        const float *src = p.partial + (int64_t)shares.slot[k] * kTileFloats + r * 256 + c;
+    for (int k = p.first[t]; k < end; ++k) {
+        const float *src = p.partial + (int64_t)p.slot[k] * kTileFloats + r * 256 + c;
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
             const float4 v = *reinterpret_cast<const float4 *>(src + 128 * h);
@@ -444,12 +453,12 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ Ff
             y[h][3] += v.w;
         }
     }
-    const int which = MODE == FfMode::DW && 2 * tn >= p.tiles_n;
-    const int64_t col = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN + c;
+    const int which = second && 2 * tn >= p.tiles_n;
+    const int64_t col = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * (4 * Q) + c;
     using T = std::conditional_t<F32, float, __nv_bfloat16>;
     auto store = [&](void *base, const float *x) {
         T *dst = static_cast<T *>(base) + row * p.cols + col;
-        if (p.tma_out) {   // (rows on 16 bytes)
+        if (p.wide) {
             if (col >= p.cols) return;
             if constexpr (F32) *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
             else *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
@@ -459,7 +468,7 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ Ff
         for (int k = 0; k < 4; ++k)
             if (col + k < p.cols) dst[k] = from_f32<T>(x[k]);
     };
-    if (MODE == FfMode::FWD) {
+    if (FWD) {
         float o[4];
         ff_with_act(p.act, [&](auto f) {
 #pragma unroll
@@ -502,10 +511,13 @@ template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32)
     q.pairs = (int)std::min<int64_t>(most, q.tiles);
     q.whole = (int)std::min<int64_t>(q.tiles, INT32_MAX);
     const int64_t rest = q.tiles % most;
-    // sharing the last round takes its k-blocks from kb to about rest kb / pairs, at
-    // the cost of writing and reading the sums and a second launch, some 20 k-blocks
-    // (a k-block in fp32, six products of parts, counts as four)
-    const int64_t cost = f32 ? 5 : 20;
+    // Sharing the last round takes its k-blocks from kb to about rest kb / pairs, at the
+    // cost of writing and reading the sums and a launch more: some 40 k-blocks, 20 where
+    // a tile has few rows (in fp32, six products of parts a k-block, 8): 2708 x 256 x
+    // 680 bf16 dWg, dWu (6 tiles of 43) shared 27.7 us, whole 24.7; 4099 x 301 x 803 dX
+    // (34 of 26) 34 : 29; 16 x 4096 x 4096 forward (32 of 64) 22.2 : 25.5; 16384 x 1024 x
+    // 2816 backward (28 of 88 and 12 of 256) 295 : 354.
+    const int64_t cost = f32 ? 8 : (MODE == FfMode::DW ? F : T) <= 128 ? 20 : 40;
     if (rest && q.kb - (rest * q.kb + most - 1) / most > cost) {
         q.split = true;
         q.pairs = most;
@@ -516,7 +528,8 @@ template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32)
 
 }  // namespace
 
-template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, cudaStream_t s) {
+// Launches the product; what is left to join is noted in `shares`.
+template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, FfShares &shares, cudaStream_t s) {
     using C = FfCfg<MODE, F32>;
     static_assert(C::BYTES + 1024 + 256 <= 227 * 1024, "shared memory");
     const FfPlan q = ff_plan<MODE>(a.T, a.F, a.M, F32);
@@ -575,8 +588,16 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, cuda
     e = launch_early(ff_gemm_kernel<MODE, F32>, dim3(2 * (unsigned)q.pairs), dim3(kFfThreads), C::BYTES + 1024, s, p);
     note_launch(id, s, true);
     if (e != cudaSuccess || !q.split) return e;
-    const int rest = (int)(q.tiles - q.whole);   // (less than the pairs)
-    FfShares shares{};
+    shares.partial = p.partial;
+    for (int i = 0; i < 3; ++i) shares.out[i] = p.out[i];
+    shares.rows = p.rows;
+    shares.cols = p.cols;
+    shares.tiles_m = p.tiles_m;
+    shares.tiles_n = p.tiles_n;
+    shares.whole = p.whole;
+    shares.tiles = (int)(q.tiles - q.whole);   // (less than the pairs)
+    shares.act = p.act;
+    shares.wide = p.tma_out;
     int n = 0, begun = 0;   // shares, tiles that have one
     for (int pair = 0; pair < q.pairs; ++pair) {   // (end to end: the tiles and their k-blocks in order)
         const FfUnits units((int)q.tiles, q.whole, (int)q.kb, q.pairs, pair);
@@ -586,9 +607,15 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, cuda
             shares.slot[n++] = (uint16_t)u.slot;
         }
     }
-    shares.first[rest] = (uint16_t)n;
+    shares.first[shares.tiles] = (uint16_t)n;
+    return e;
+}
+
+// Joins what one product (forward), or two, left.
+template <bool FWD, bool F32> cudaError_t ff_join(const FfShares &a, const FfShares &b, cudaStream_t s) {
+    if (a.tiles + b.tiles == 0) return cudaSuccess;
     note_launch(SGA_KERN_FF_JOIN, s, false);
-    e = launch_early(ff_join_kernel<MODE, F32>, dim3(C::BN / 4, (unsigned)rest), dim3(256), 0, s, p, shares);   // (256 rows of BN / 4 threads)
+    const cudaError_t e = launch_early(ff_join_kernel<FWD, F32>, dim3(FWD ? 32 : 64, (unsigned)(a.tiles + b.tiles)), dim3(256), 0, s, a, b);
     note_launch(SGA_KERN_FF_JOIN, s, true);
     return e;
 }
