@@ -1,6 +1,7 @@
 // Products of the gated feed-forward block on the tcgen05 tensor cores, by CTA
 // pairs (tc_pair.cuh): tiles of 256 x 256 (forward: 256 rows x 128 gate and the
-// same 128 up columns, so that one thread has both halves of a result).
+// same 128 up columns, so that one thread has both halves of a result; dX: narrower
+// ones where that covers its columns with less beside them).
 //
 // Persistent pairs; in each CTA
 //   warp 0, one lane: TMA loads of its half of a k-block's operands (128 rows of A,
@@ -59,7 +60,7 @@ template <FfMode MODE, bool F32> struct FfCfg {
     static constexpr uint32_t OUT0 = NST * STAGE;            // staging of results: 32 rows x 64 bf16 a warp
     static constexpr uint32_t BYTES = OUT0 + 8 * 4096;
     static constexpr bool A_MN = MODE == FfMode::DW, B_MN = MODE != FfMode::DX;
-    static constexpr int BN = MODE == FfMode::FWD ? 128 : 256;   // columns of a result that a tile covers
+    static constexpr int BN = MODE == FfMode::FWD ? 128 : 256;   // columns of a result that a tile covers (DX: at most)
 };
 constexpr int kTileFloats = 256 * 256;
 
@@ -70,6 +71,7 @@ struct FfParams {
     float *partial;
     int64_t rows, cols;               // of a result
     int tiles_m, tiles_n;             // tiles
+    int width;                        // columns of a result that a tile covers
     int kb, kb_seg;                   // k-blocks of a tile; of a segment
     int depth;                        // k-blocks between two moves to registers
     int pairs, whole;                 // pairs of the grid; tiles dealt whole
@@ -161,6 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
     const int tid = threadIdx.x, lane = tid & 31, warp = tc::warp_index();
     const uint32_t sbase = tc::smem_u32(smem), rank = tc::cluster_rank();
     const FfUnits units(p.tiles_m * p.tiles_n, p.whole, p.kb, p.pairs, blockIdx.x >> 1);
+    const int width = MODE == FfMode::DX ? p.width : C::BN;
 
     if (tid == 32) {
         for (int i = 0; i < C::NST; ++i) {
@@ -203,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                         ok = false;
                         break;
                     }
-                    if (rank == 0) tc::mbar_expect_tx(&full[s], 2 * C::STAGE);
+                    if (rank == 0) tc::mbar_expect_tx(&full[s], MODE == FfMode::DX ? C::PARTS * (2 * C::TB + width * 128) : 2 * C::STAGE);
                     const uint32_t bar = tc::map_rank(&full[s], 0), at = sbase + s * C::STAGE;
                     const int seg = MODE == FfMode::DX && kb >= p.kb_seg, k = (kb - (seg ? p.kb_seg : 0)) * 64;
                     const int m0 = tm * 256 + rank * 128;
@@ -213,7 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                         n0 = tn * 128;
                     } else if (MODE == FfMode::DX) {
                         b = seg;
-                        n0 = tn * 256 + rank * 128;
+                        n0 = tn * width + rank * (width / 2);
                     } else {
                         b = 2 * tn >= p.tiles_n;
                         n0 = (tn - (b ? p.tiles_n / 2 : 0)) * 256 + rank * 128;
@@ -250,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
             if (rank == 0)
                 for (int i = it - 1; i >= 0 && i >= it - C::NST; --i) tc::mbar_wait_cluster(&full[i % C::NST], (i / C::NST) & 1, tc::kWaitLimit);
         } else if (warp == 1 && rank == 0) {   // ---------------------------- MMA issuer (the warp in step)
-            constexpr uint32_t idesc = tc::idesc_bf16(256, 256) | (C::A_MN ? tc::kMajorMnA : 0u) | (C::B_MN ? tc::kMajorMnB : 0u);
+            const uint32_t idesc = tc::idesc_bf16(256, MODE == FfMode::DX ? width : 256) | (C::A_MN ? tc::kMajorMnA : 0u) | (C::B_MN ? tc::kMajorMnB : 0u);
             // parts of A and B by product, the smallest products first
             constexpr int NP = F32 ? 6 : 1, PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
             bool ok = true;
@@ -318,6 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                 tc::fence_after_sync();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
+                    if (MODE == FfMode::DX && column(j >> 1) >= width) continue;
                     uint32_t v[16];
                     tc::tmem_ld16(tmem_base + buf * 256 + column(j >> 1) + (j & 1) * 16 + tl, v);
 #pragma unroll
@@ -336,22 +340,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
             if (u.slot >= 0) {   // a share: its sums
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (rows > 0) {
+                    if (rows > 0 && (MODE != FfMode::DX || column(j) < width)) {
                         if (stored) tc::bulk_wait_read();   // (a result's store may still read the staging)
                         ff_store_block(stage, acc + 32 * j, p.partial + (int64_t)u.slot * kTileFloats + r * 256 + column(j), 256, rows, 32, true);
                     }
                 continue;
             }
             const int which = MODE == FfMode::DW && 2 * tn >= p.tiles_n;   // dWu
-            const int64_t col0 = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * C::BN;
+            const int64_t col0 = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * width, end = min(p.cols, col0 + width);
             // 64 columns x[0 .. 63] of result o, from column col
             auto store = [&](int o, const float *x, int64_t col) {
                 if constexpr (F32) {
 #pragma unroll
                     for (int j = 0; j < 64; j += 32)
-                        if (rows > 0 && col + j < p.cols)
+                        if (rows > 0 && col + j < end)
                             ff_store_block(stage, x + j, static_cast<float *>(p.out[o]) + row0 * p.cols + col + j, p.cols, rows,
-                                           (int)min((int64_t)32, p.cols - col - j), p.tma_out);
+                                           (int)min((int64_t)32, end - col - j), p.tma_out);
                 } else {   // staged in the swizzle of its tensor map
                     if (stored) tc::bulk_wait_read();   // (the lane that stored; others have nothing to wait for)
                     __syncwarp();
@@ -365,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                     if (p.tma_out) {
                         tc::fence_proxy_async();
                         __syncwarp();
-                        if (lane == 0 && col < p.cols && rows > 0) {
+                        if (lane == 0 && col < end && rows > 0) {
                             tc::tma_store_2d(&p.to[o], (int)col, (int)row0, stage);
                             tc::bulk_commit();
                             stored = true;
@@ -377,8 +381,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfThreads, 1) ff_ge
                             uint32_t v;
                             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(stage + q * 128 + (((lane >> 2) ^ (q & 7)) << 4) + (lane & 3) * 4));
                             unsigned short *d = reinterpret_cast<unsigned short *>(dst + (row0 + q) * p.cols + col + 2 * lane);
-                            if (col + 2 * lane < p.cols) d[0] = (unsigned short)v;
-                            if (col + 2 * lane + 1 < p.cols) d[1] = (unsigned short)(v >> 16);
+                            if (col + 2 * lane < end) d[0] = (unsigned short)v;
+                            if (col + 2 * lane + 1 < end) d[1] = (unsigned short)(v >> 16);
                         }
                     }
                 }
@@ -419,7 +423,7 @@ struct FfShares {
     const float *partial;
     void *out[3];
     int64_t rows, cols;
-    int tiles_m, tiles_n, whole, tiles;   // tiles: of the last round
+    int tiles_m, tiles_n, width, whole, tiles;   // tiles: of the last round
     int act, wide;                        // wide: rows on 16 bytes
     uint16_t first[kFfMaxPairs + 1], slot[2 * kFfMaxPairs];
 };
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ Ff
     int tm, tn;
     ff_tile(p.whole + t, p.tiles_m, p.tiles_n, tm, tn);
     const int64_t row = (int64_t)tm * 256 + r;
-    if (row >= p.rows) return;   // (whose sums were not stored)
+    if (row >= p.rows || (!FWD && c >= p.width)) return;   // (whose sums were not stored)
     float y[2][4] = {};
     const int end = p.first[t + 1];
 #pragma unroll 4
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ Ff
         }
     }
     const int which = second && 2 * tn >= p.tiles_n;
-    const int64_t col = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * (4 * Q) + c;
+    const int64_t col = (int64_t)(tn - (which ? p.tiles_n / 2 : 0)) * (FWD ? 4 * Q : p.width) + c;
     using T = std::conditional_t<F32, float, __nv_bfloat16>;
     auto store = [&](void *base, const float *x) {
         T *dst = static_cast<T *>(base) + row * p.cols + col;
@@ -486,11 +490,12 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ Ff
 
 struct FfPlan {
     int64_t tiles_m, tiles_n, kb, kb_seg, tiles;
-    int pairs, whole;
+    int width, pairs, whole;
     bool split;
 };
 template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32) {
     FfPlan q{};
+    q.width = FfCfg<MODE, false>::BN;
     auto div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     if (MODE == FfMode::FWD) {
         q.tiles_m = div(T, 256);
@@ -499,6 +504,13 @@ template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32)
     } else if (MODE == FfMode::DX) {
         q.tiles_m = div(T, 256);
         q.tiles_n = div(F, 256);
+        // Tiles no wider than the columns' even shares, in whole blocks of what the
+        // epilogue stores at a time.  (B lies along the depth here; across it, its
+        // columns come in 64s a CTA.)  Backward, 256 wide and so: 4099 x 301 x 803 fp32
+        // (two of 160) 97 : 87 us, 20000 x 32 x 128 fp32 (32) 64 : 56, 20000 x 520 x
+        // 1300 bf16 (three of 192) 215 : 209.
+        const int64_t block = f32 ? 32 : 64;
+        q.width = (int)(div(div(F, q.tiles_n), block) * block);
         q.kb_seg = div(M, 64);
         q.kb = 2 * q.kb_seg;
     } else {
@@ -535,9 +547,9 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, FfSh
     const FfPlan q = ff_plan<MODE>(a.T, a.F, a.M, F32);
     FfParams p{};
     cudaError_t e = cudaSuccess;
-    auto operand = [&](CUtensorMap (&maps)[3], const FfMatrix &m, bool mn) {
+    auto operand = [&](CUtensorMap (&maps)[3], const FfMatrix &m, bool mn, uint32_t box = 128) {
         for (int i = 0; i < C::PARTS && e == cudaSuccess; ++i)
-            e = bf16_tensor_map(&maps[i], m.p + i * m.part_elems(), m.rows, m.cols, m.ld, 64, mn ? 64 : 128);
+            e = bf16_tensor_map(&maps[i], m.p + i * m.part_elems(), m.rows, m.cols, m.ld, 64, mn ? 64 : box);
     };
     if (MODE == FfMode::FWD) {
         operand(p.ta[0], a.x, false);
@@ -551,8 +563,8 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, FfSh
     } else if (MODE == FfMode::DX) {
         operand(p.ta[0], a.dg, false);
         operand(p.ta[1], a.du, false);
-        operand(p.tb[0], a.wg, false);
-        operand(p.tb[1], a.wu, false);
+        operand(p.tb[0], a.wg, false, q.width / 2);
+        operand(p.tb[1], a.wu, false, q.width / 2);
         p.rows = a.T;
         p.cols = a.F;
         p.out[0] = a.out;
@@ -574,6 +586,7 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, FfSh
     p.partial = a.partial;
     p.tiles_m = (int)q.tiles_m;
     p.tiles_n = (int)q.tiles_n;
+    p.width = q.width;
     p.kb = (int)q.kb;
     p.kb_seg = (int)q.kb_seg;
     // bf16: sums of 16384 products drop at most 2^-14 of their size on the way.  fp32,
@@ -594,6 +607,7 @@ template <FfMode MODE, bool F32> cudaError_t ff_product(const FfProduct &a, FfSh
     shares.cols = p.cols;
     shares.tiles_m = p.tiles_m;
     shares.tiles_n = p.tiles_n;
+    shares.width = p.width;
     shares.whole = p.whole;
     shares.tiles = (int)(q.tiles - q.whole);   // (less than the pairs)
     shares.act = p.act;

@@ -42,6 +42,14 @@ def test_sizes(T, F, M, dt):
     check(T, F, M, dt)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("F", [5, 32, 40, 65, 96, 129, 160, 192, 200, 257, 301, 320, 384, 392, 513, 577, 1025])
+def test_widths_of_tiles(F, dt):
+    """dX's tiles are as wide as its columns' even shares: from one block to 256 columns."""
+    check(300, F, 72, dt, "relu")
+    check(1100, F, 800, dt)
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_activations(dt, act):
