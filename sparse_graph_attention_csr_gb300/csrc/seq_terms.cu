@@ -4,12 +4,16 @@
 namespace sga {
 namespace {
 
-// Row terms: D / EL lanes of 16 bytes a (row, head), four of them in flight.
+// Row terms: D / EL lanes of 16 bytes a (row, head), two of them in flight: what is in
+// flight on an SM comes from its blocks (25176 rows, 8 heads of 128, bf16: one 25.1 us,
+// two 25.4, four 28.6, eight 43; 60000 rows, 4 of 64: 17.0, 17.6, 20.2, 32).  The next
+// kernel's blocks take the places that are free when they may start, so they may once
+// the loads are out: started before, they lay uneven over the SMs (2900 rows, 4/2 heads
+// of 32, window 129, fp32: backward 72 us, now 59).
 // Rows behind the last sequence (to the end of its tile) get -lse = -inf, so
 // that their weights are zero, and Delta = 0.
-constexpr int kTerms = 4;
+constexpr int kTerms = 2;
 template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
-    let_next_start();
     wait_previous();
     constexpr int EL = Elt<T>::EL, L = D / EL, G = 256 / L;   // G items of a block at a time
     const int sub = threadIdx.x % L;
@@ -27,6 +31,7 @@ template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_term
             if (sub == 0) lse[k] = __ldg(a.lse + g) * kLog2e;
         }
     }
+    let_next_start();
 #pragma unroll
     for (int k = 0; k < kTerms; ++k) {
         const int64_t g = g0 + k * G;
