@@ -516,7 +516,8 @@ template <int D, int RA, int TY, int MB, bool WIN> cudaError_t launch_bwd(const 
 // 128 registers a thread with a few spills, against three: 2048 rows, 8 heads
 // (512 units), D = 32 174 : 213, D = 64 275 : 309; fewer units do not need them
 // (256, D = 64, causal 64 : 62).  In the backward D = 32 is faster with two blocks
-// an SM while they are enough (1024 rows, 4 heads 81 : 102, 8 heads 140 : 124), and
+// an SM while they are enough (1024 rows, 4 heads 81 : 102, 8 heads 140 : 124), or take
+// no more rounds than three (2000 rows, 4 heads 265 : 292, causal 136 : 153), and
 // D = 128, whose tiles leave room for one block an SM, with 64 rows and 256
 // threads from there on (1024 rows, 8 heads 400 : 484; 512 rows, 8 heads, causal
 // 117 : 74).
@@ -534,7 +535,10 @@ template <bool WIN> cudaError_t seq_bwd_f32(const SeqArgs &a, int D, cudaStream_
     if ((D == 128 ? 2 : 1) * units <= a.num_sms)
         return D == 32 ? launch_bwd<32, 2, 8, 3, WIN>(a, s) : D == 64 ? launch_bwd<64, 2, 8, 2, WIN>(a, s) : launch_bwd<128, 2, 8, 1, WIN>(a, s);
     const bool many = units > 2 * (int64_t)a.num_sms;
-    if (D == 32) return many ? launch_bwd<32, 4, 8, 3, WIN>(a, s) : launch_bwd<32, 4, 8, 2, WIN>(a, s);
+    // (two rounds of two blocks an SM, where three would take two rounds as well; with a
+    // window, whose blocks differ more, three: 2900 rows, 552 units, 59 : 64)
+    const bool two_rounds = !WIN && units > 3 * (int64_t)a.num_sms && units <= 4 * (int64_t)a.num_sms;
+    if (D == 32) return many && !two_rounds ? launch_bwd<32, 4, 8, 3, WIN>(a, s) : launch_bwd<32, 4, 8, 2, WIN>(a, s);
     if (D == 64) return launch_bwd<64, 4, 8, 2, WIN>(a, s);
     return many ? launch_bwd<128, 4, 16, 1, WIN>(a, s) : launch_bwd<128, 4, 8, 1, WIN>(a, s);
 }
