@@ -233,15 +233,18 @@ def _qk_bwd(st):
 
 def _near(st):
     """The rows in blocks: the rows of each [n, BLOCK], the keys of each [n, m] (those that the window of one of its rows
-    may reach, and the first rows of its first row's sequence), and which pairs are visible [n, BLOCK, m]."""
+    may reach, and the first rows of its first row's sequence; both ways as many behind its last row as there are first
+    rows, since those of a sequence that begins there, or shortly before, may lie behind its windows), and which pairs are
+    visible [n, BLOCK, m]."""
     ptr = st["seq_ptr"].long()
+    dev = ptr.device
     T, w = st["Q"].shape[0], st["reach"]
     n = (T + BLOCK - 1) // BLOCK
-    first = torch.arange(n, device="cuda")[:, None] * BLOCK
-    row = first + torch.arange(BLOCK, device="cuda")
-    near = first + torch.arange(1 - w, BLOCK + (0 if st["causal"] else w - 1), device="cuda")
+    first = torch.arange(n, device=dev)[:, None] * BLOCK
+    row = first + torch.arange(BLOCK, device=dev)
+    near = first + torch.arange(1 - w, BLOCK + (0 if st["causal"] else max(w, min(st["sinks"], T)) - 1), device=dev)
     begin = ptr[torch.searchsorted(ptr, first, right=True) - 1]
-    head = begin + torch.arange(st["sinks"], device="cuda")
+    head = begin + torch.arange(st["sinks"], device=dev)
     key = torch.cat([near, torch.where(head < near[:, :1], head, -torch.ones_like(head))], 1)
     there = (row < T)[..., None] & ((key >= 0) & (key < T))[:, None]
     row, key = row.clamp(0, T - 1), key.clamp(0, T - 1)
@@ -268,7 +271,7 @@ def _packed(y, T):
 def _added(y, key, T):
     """[n, kv head, 1, m, D] summed over the keys' rows -> [T, kv head, D]."""
     n, k, _, m, d = y.shape
-    return torch.zeros(T, k, d, device="cuda").index_add_(0, key.flatten(), y[:, :, 0].permute(0, 2, 1, 3).reshape(n * m, k, d))
+    return torch.zeros(T, k, d, device=y.device).index_add_(0, key.flatten(), y[:, :, 0].permute(0, 2, 1, 3).reshape(n * m, k, d))
 
 
 def _win_fwd(st):
