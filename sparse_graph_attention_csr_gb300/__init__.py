@@ -1110,12 +1110,18 @@ class QKNormRope(torch.autograd.Function):
 class GatedFF(torch.autograd.Function):
     """The gated product of a feed-forward block as an autograd function:
     ``h = GatedFF.apply(X, Wg, Wu, "silu")`` = act(X Wg) (X Wu); the block's
-    second projection is an ordinary product of h."""
+    second projection is an ordinary product of h.  The projections are kept only
+    where a gradient may be asked for."""
+
+    @classmethod
+    def apply(cls, X, Wg, Wu, act="silu"):
+        # (in forward gradients are always off, and needs_input_grad goes by the tensors alone:
+        # parameters need one under no_grad too)
+        return super().apply(X, Wg, Wu, act, torch.is_grad_enabled() and any(t.requires_grad for t in (X, Wg, Wu)))
 
     @staticmethod
-    def forward(ctx, X, Wg, Wu, act="silu"):
+    def forward(ctx, X, Wg, Wu, act, save):
         X, Wg, Wu = _begin16(X), _begin16(Wg), _begin16(Wu)
-        save = any(ctx.needs_input_grad)
         out, G, U = gated_ff_fwd(X, Wg, Wu, act, save=save)
         ctx.act = act
         if save:
@@ -1128,4 +1134,4 @@ class GatedFF(torch.autograd.Function):
         X, Wg, Wu, G, U = ctx.saved_tensors
         need = ctx.needs_input_grad
         dX, dWg, dWu = gated_ff_bwd(X, Wg, Wu, G, U, _begin16(dOut), ctx.act, need[0], need[1] or need[2])
-        return dX, dWg, dWu, None
+        return dX, dWg, dWu, None, None
