@@ -82,8 +82,9 @@ struct SeqArgs {
 // rows of a head's slice of the backward's row terms: whole tiles, 512-byte aligned
 inline int64_t seq_rows_pad(int64_t rows) { return (rows + 127) / 128 * 128; }
 
-// -lse * log2(e) and -Delta of every row, head-major (seq_terms.cu)
-template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s);
+// -lse * log2(e) and -Delta of every row, head-major (seq_terms.cu); uneven: the next
+// kernel's first blocks may lie unevenly over the SMs (fp32, D < 128)
+template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s, bool uneven = false);
 // the parts of cut walks added up (seq_join.cu)
 template <typename T> cudaError_t seq_join(const SeqArgs &a, int D, cudaStream_t s);
 // WIN: a plan with a window (a.window > 0)

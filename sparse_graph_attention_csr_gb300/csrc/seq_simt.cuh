@@ -490,13 +490,13 @@ template <int D, int RA, int TY, int MB, bool WIN> cudaError_t launch_fwd(const 
     return e;
 }
 
-template <int D, int RA, int TY, int MB, bool WIN> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s) {
+template <int D, int RA, int TY, int MB, bool WIN> cudaError_t launch_bwd(const SeqArgs &a, cudaStream_t s, bool uneven = false) {
     constexpr size_t kv = sizeof(float) * (2 * kOwnFloats<D, RA, TY> + 4 * kTileFloats<D> + (kTwoScores<TY> ? 2 : 1) * kScoreFloats<RA, TY>);
     constexpr size_t q = sizeof(float) * (2 * kOwnFloats<D, RA, TY> + 3 * kTileFloats<D> + kScoreFloats<RA, TY>);
     constexpr size_t smem = kv > q ? kv : q;
     static_assert(smem <= 227 * 1024, "shared memory");
     cudaError_t e = allow_smem<seq_bwd_f32_kernel<D, RA, TY, MB, WIN>>(smem);
-    if (e == cudaSuccess) e = seq_row_terms<float>(a, D, s);
+    if (e == cudaSuccess) e = seq_row_terms<float>(a, D, s, uneven);
     if (e != cudaSuccess) return e;
     note_launch(SGA_KERN_SEQ_BWD, s, false);
     e = launch_early(seq_bwd_f32_kernel<D, RA, TY, MB, WIN>, dim3((unsigned)(((int64_t)a.n_ktiles * a.Hkv + (int64_t)a.n_tiles * a.H) * (kT / (TY * RA)))),
@@ -515,12 +515,10 @@ template <int D, int RA, int TY, int MB, bool WIN> cudaError_t launch_bwd(const 
 // 16.6, 22.8, 33.2 : 18.9, 27.1, 41.3.  In the forward four blocks an SM fit in
 // 128 registers a thread with a few spills, against three: 2048 rows, 8 heads
 // (512 units), D = 32 174 : 213, D = 64 275 : 309; fewer units do not need them
-// (256, D = 64, causal 64 : 62).  In the backward D = 32 is faster with two blocks
-// an SM while they are enough (1024 rows, 4 heads 81 : 102, 8 heads 140 : 124), or take
-// no more rounds than three (2000 rows, 4 heads 265 : 292, causal 136 : 153), and
-// D = 128, whose tiles leave room for one block an SM, with 64 rows and 256
-// threads from there on (1024 rows, 8 heads 400 : 484; 512 rows, 8 heads, causal
-// 117 : 74).
+// (256, D = 64, causal 64 : 62).  In the backward D = 128, whose tiles leave
+// room for one block an SM, takes 64 rows and 256 threads where there are more than two
+// units an SM (1024 rows, 8 heads 400 : 484; 512 rows, 8 heads, causal 117 : 74), and
+// D = 32 two blocks an SM or three (at seq_bwd_f32).
 template <bool WIN> cudaError_t seq_fwd_f32(const SeqArgs &a, int D, cudaStream_t s) {
     const int64_t units = 2 * (int64_t)a.n_tiles * a.H;
     if ((D == 128 ? 2 : 1) * units <= a.num_sms)
@@ -534,12 +532,34 @@ template <bool WIN> cudaError_t seq_bwd_f32(const SeqArgs &a, int D, cudaStream_
     const int64_t units = 2 * (int64_t)a.n_tiles * (a.H + a.Hkv);
     if ((D == 128 ? 2 : 1) * units <= a.num_sms)
         return D == 32 ? launch_bwd<32, 2, 8, 3, WIN>(a, s) : D == 64 ? launch_bwd<64, 2, 8, 2, WIN>(a, s) : launch_bwd<128, 2, 8, 1, WIN>(a, s);
-    const bool many = units > 2 * (int64_t)a.num_sms;
-    // (two rounds of two blocks an SM, where three would take two rounds as well; with a
-    // window, whose blocks differ more, three: 2900 rows, 552 units, 59 : 64)
-    const bool two_rounds = !WIN && units > 3 * (int64_t)a.num_sms && units <= 4 * (int64_t)a.num_sms;
-    if (D == 32) return many && !two_rounds ? launch_bwd<32, 4, 8, 3, WIN>(a, s) : launch_bwd<32, 4, 8, 2, WIN>(a, s);
-    if (D == 64) return launch_bwd<64, 4, 8, 2, WIN>(a, s);
+    const int64_t sms = a.num_sms;
+    const bool many = units > 2 * sms;
+    // One to a few rounds of blocks: how long they take depends on where the first ones
+    // lie (410 cases without a window, one sequence or several, of 1 to 10 units an SM,
+    // against laying them unevenly always: 8% less on average, 6% more at worst; evenly
+    // always: 1% and 25% more).  us, unevenly : evenly.
+    //   D = 64, a key head a query head, causal, 1.5 to 2.2 units an SM: 1100 rows, 4
+    //     heads (1.9) 112 : 125; 800 rows, 4 heads (1.4) 90 : 82, 8 heads (2.7) 96 : 85.
+    //     Full, 2 to 2.8: 700 rows, 8 heads (2.3) 114 : 141; 1100, 4 heads (1.9) 144 : 127.
+    //     Grouped heads: 1500 rows, 8/4 heads, causal (3.8) 371 : 304.
+    //   D = 32, full, three blocks an SM, a key head a query head, 3 to 3.5: 2000 rows, 4
+    //     heads (3.4) 228 : 283; 2600 (4.3) 403 : 397.  Two query heads a key head, from
+    //     4.5 on: 2000 rows, 8/4 heads (5.1) 431 : 476; 1700 rows (4.3) 357 : 321; four:
+    //     2200 rows, 8/2 heads (4.6) 899 : 698.  Causal: 1500 rows, 8/4 heads (3.8) 199 : 186.
+    bool uneven = false;
+    if constexpr (!WIN) {
+        const bool own = a.H == a.Hkv;
+        if (D == 64 && own) uneven = a.causal ? 2 * units > 3 * sms && 5 * units <= 11 * sms : many && 5 * units <= 14 * sms;
+        if (D == 32 && !a.causal) uneven = own ? units > 3 * sms && 2 * units <= 7 * sms : a.H == 2 * a.Hkv && 2 * units > 9 * sms;
+    }
+    // D = 32, two blocks an SM : three.  Two while all fit so (1000 rows, 4 heads (1.7) 70 :
+    // 72), and where both take two rounds (full, 2200 rows, 4 heads (3.7) 288 : 357; causal
+    // the late ones are short: 1500 rows, 4 heads (2.5) 93 : 110); full and 2.6, 1600 rows,
+    // 167 : 150; more than 4, 2900 rows, 541 : 495, causal 243 : 235.  With a window, whose
+    // blocks differ more, three: 2900 rows, 552 units, 64 : 59.
+    const bool two = !many || (!WIN && !uneven && units <= 4 * sms && (a.causal || units > 3 * sms));
+    if (D == 32) return two ? launch_bwd<32, 4, 8, 2, WIN>(a, s, uneven) : launch_bwd<32, 4, 8, 3, WIN>(a, s, uneven);
+    if (D == 64) return launch_bwd<64, 4, 8, 2, WIN>(a, s, uneven);
     return many ? launch_bwd<128, 4, 16, 1, WIN>(a, s) : launch_bwd<128, 4, 8, 1, WIN>(a, s);
 }
 

@@ -10,10 +10,11 @@ namespace {
 // kernel's blocks take the places that are free when they may start, so they may once
 // the loads are out: started before, they lay uneven over the SMs (2900 rows, 4/2 heads
 // of 32, window 129, fp32: backward 72 us, now 59).
+// With four in flight half as many blocks end later, and the next kernel's lie uneven
+// again; the fp32 passes ask for that where their rounds come out better so.
 // Rows behind the last sequence (to the end of its tile) get -lse = -inf, so
 // that their weights are zero, and Delta = 0.
-constexpr int kTerms = 2;
-template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
+template <typename T, int D, int kTerms> __global__ void __launch_bounds__(256) seq_row_terms_kernel(const SeqArgs a) {
     wait_previous();
     constexpr int EL = Elt<T>::EL, L = D / EL, G = 256 / L;   // G items of a block at a time
     const int sub = threadIdx.x % L;
@@ -51,20 +52,22 @@ template <typename T, int D> __global__ void __launch_bounds__(256) seq_row_term
     }
 }
 
-template <typename T, int D> cudaError_t launch_terms(const SeqArgs &a, cudaStream_t s) {
+template <typename T, int D, int kTerms = 2> cudaError_t launch_terms(const SeqArgs &a, cudaStream_t s) {
     constexpr int per = kTerms * 256 / (D / Elt<T>::EL);   // items of a block
     note_launch(SGA_KERN_SEQ_BWD_ROWS, s, false);
-    const cudaError_t e = launch_early(seq_row_terms_kernel<T, D>, dim3((unsigned)((a.rows_pad * a.H + per - 1) / per)), dim3(256), 0, s, a);
+    const cudaError_t e = launch_early(seq_row_terms_kernel<T, D, kTerms>, dim3((unsigned)((a.rows_pad * a.H + per - 1) / per)), dim3(256), 0, s, a);
     note_launch(SGA_KERN_SEQ_BWD_ROWS, s, true);
     return e;
 }
 
 }  // namespace
 
-template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s) {
+template <typename T> cudaError_t seq_row_terms(const SeqArgs &a, int D, cudaStream_t s, bool uneven) {
+    if constexpr (sizeof(T) == 4)
+        if (uneven && D < 128) return D == 32 ? launch_terms<T, 32, 4>(a, s) : launch_terms<T, 64, 4>(a, s);
     return D == 32 ? launch_terms<T, 32>(a, s) : D == 64 ? launch_terms<T, 64>(a, s) : launch_terms<T, 128>(a, s);
 }
-template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t);
-template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t);
+template cudaError_t seq_row_terms<float>(const SeqArgs &, int, cudaStream_t, bool);
+template cudaError_t seq_row_terms<__nv_bfloat16>(const SeqArgs &, int, cudaStream_t, bool);
 
 }  // namespace sga
