@@ -37,7 +37,8 @@
 //
 // Every wait is bounded; a timeout sets the plan's error word and ends the role.
 //
-// WIN: plans with a window (their own translation unit, seq_fwd_win.cu).
+// WIN: plans with a window (their own translation unit, seq_fwd_win.cu).  TMA: results
+// leave through shared memory and TMA.
 #pragma once
 
 #include <algorithm>
@@ -71,7 +72,7 @@ struct FwdParams {
     int pair_heads;   // NS = 2: the two tiles are two heads of one row tile
 };
 
-template <int D, int NS, bool WIN>
+template <int D, int NS, bool WIN, bool TMA>
 __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
     seq_fwd_kernel(const __grid_constant__ FwdParams prm) {
     using C = FwdCfg<D, NS>;
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
                     x[i] = __uint_as_float(o[i]) * inv;
                     bad |= !(fabsf(x[i]) < INFINITY);
                 }
-                if constexpr (seq::kTmaResult<D>) {
+                if constexpr (TMA) {
                     seq::stage_columns(stage, quarter * 32 + lane, cb, x);
                 } else if (in) {
 #pragma unroll
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
             }
             if (in) a.lse_w[row * a.H + h] = (m + log2f(l)) * kLn2;
             uint32_t again = __ballot_sync(SGA_FULL_MASK, bad && in && l == l);
-            if constexpr (seq::kTmaResult<D>) {
+            if constexpr (TMA) {
                 tc::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NS>::THREADS, NS == 2 ? 1 : 2)
     }
 }
 
-template <int D, int NS, bool WIN> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
+template <int D, int NS, bool WIN, bool TMA = seq::kTmaResult<D>> cudaError_t launch(const SeqArgs &a, cudaStream_t s) {
     using C = FwdCfg<D, NS>;
     static_assert(C::BYTES + 1024 <= (NS == 2 ? 226 : 113) * 1024, "shared memory");
     FwdParams prm{};
@@ -381,14 +382,14 @@ template <int D, int NS, bool WIN> cudaError_t launch(const SeqArgs &a, cudaStre
     cudaError_t e = seq_tensor_map(&prm.tq, a.Q, a.rows, a.H, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tk, a.K, a.rows, a.Hkv, D);
     if (e == cudaSuccess) e = seq_tensor_map(&prm.tv, a.V, a.rows, a.Hkv, D);
-    if (e == cudaSuccess && seq::kTmaResult<D>) e = seq_tensor_map(&prm.to, a.out_w, a.rows, a.H, D, 32);
-    if (e == cudaSuccess) e = allow_smem<seq_fwd_kernel<D, NS, WIN>>(C::BYTES + 1024);
+    if (e == cudaSuccess && TMA) e = seq_tensor_map(&prm.to, a.out_w, a.rows, a.H, D, 32);
+    if (e == cudaSuccess) e = allow_smem<seq_fwd_kernel<D, NS, WIN, TMA>>(C::BYTES + 1024);
     if (e != cudaSuccess) return e;
     const int64_t units = NS == 1 ? (int64_t)a.n_tiles * a.H
                           : prm.pair_heads ? (int64_t)a.n_tiles * (a.H / 2)
                                            : (int64_t)((a.n_tiles + 1) / 2) * a.H;
     note_launch(SGA_KERN_SEQ_FWD, s, false);
-    e = launch_early(seq_fwd_kernel<D, NS, WIN>, dim3((unsigned)units), dim3(C::THREADS), C::BYTES + 1024, s, prm);
+    e = launch_early(seq_fwd_kernel<D, NS, WIN, TMA>, dim3((unsigned)units), dim3(C::THREADS), C::BYTES + 1024, s, prm);
     note_launch(SGA_KERN_SEQ_FWD, s, true);
     return e;
 }
@@ -407,6 +408,11 @@ template <bool WIN> cudaError_t seq_fwd_bf16(const SeqArgs &a, int D, cudaStream
     // 81); D = 128, 34270 rows, 8/2 heads, causal, window 1000, 172 : 162.
     const bool one = (int64_t)a.n_tiles * a.H <= 2 * (int64_t)a.num_sms || (D <= 64 && (a.causal || WIN));
     if (D == 32) return one ? launch<32, 1, WIN>(a, s) : launch<32, 2, WIN>(a, s);
+    // A unit an SM at most: a thread's own stores are out sooner, and no other unit waits
+    // for the SM.  Stored by TMA : so, D = 64, causal: 76 rows, 4 heads 3.85 : 3.70 us;
+    // 300 rows, 4 heads 5.58 : 5.40; 128 graphs of 9 to 38 rows, 8/2 heads (200 units) 7.03
+    // : 7.43; 80 sequences of 300 rows, 1 head (188) 8.2 : 8.6.
+    if (D == 64 && one && (int64_t)a.n_tiles * a.H <= a.num_sms) return launch<64, 1, WIN, false>(a, s);
     if (D == 64) return one ? launch<64, 1, WIN>(a, s) : launch<64, 2, WIN>(a, s);
     return one ? launch<128, 1, WIN>(a, s) : launch<128, 2, WIN>(a, s);
 }
