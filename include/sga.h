@@ -382,8 +382,8 @@ sga_status layer_norm_bwd(const void *X, const void *weight, const float *mean, 
  * row's positions: pair i by the angle pos[t, axis_i] f_i, from the first
  * element of the pair towards the second.  A pair is elements (i, i + rot / 2),
  * or with interleaved = 1 (2 i, 2 i + 1).  pos [T, axes], int32 or int64
- * (pos_bytes 4 or 8), of either sign; angles are exact to 2^-54 turns a position
- * and rounded to float32 once.  rq [T, H], rk [T, Hkv] (float32) are r, kept for
+ * (pos_bytes 4 or 8), of either sign; a frequency is held to 2^-52 of itself and
+ * 2^-54 turns a position, and the angle, exact from there, rounded to float32 once.  rq [T, H], rk [T, Hkv] (float32) are r, kept for
  * the backward pass; with both NULL nothing is normed and the weights are NULL.
  * D in {32, 64, 128}, (H + Hkv) D <= 32768.  A row's heads lie one behind the
  * other, rows ldq and ldk elements apart (multiples of 16 bytes: slices of one
@@ -428,10 +428,13 @@ sga_status qk_norm_rope_bwd(const sga_rotary *rot, const void *Q, int64_t ldq, c
  *   dX = dG Wg^T + dU Wu^T,  dWg = X^T dG,  dWu = X^T dU.
  * dX may be NULL, dWg and dWu together too (not computed).  Tensors are dense and
  * 16-byte aligned; rows of a multiple of 16 bytes are read as they lie, others are
- * copied to the workspace first (fp32 always).  1 <= F, M <= 2^20, any T.  Sums are
- * taken in an order that the sizes fix: bitwise reproducible.  In fp32 an infinity
- * or NaN in X or a weight makes the results that it enters not finite (which of the
- * two, is not defined).  Workspaces are 256-byte aligned. */
+ * copied to the workspace first (fp32 always, in parts of 6 bytes an element).  The
+ * backward's workspace also holds dG and dU, together 4 bytes an element of [T, M] in
+ * bf16 and 12 in fp32 (65536 x 8192: 6.4 GB), and workspaces up to 80 MB of partial
+ * sums.  1 <= F, M <= 2^20, any T.  Sums are taken in an order that the sizes fix:
+ * bitwise reproducible.  In fp32 an infinity or NaN in X or a weight makes the results
+ * that it enters not finite (which of the two, is not defined).  Workspaces are
+ * 256-byte aligned. */
 #define SGA_ACT_SILU 0
 #define SGA_ACT_GELU 1
 #define SGA_ACT_RELU 2

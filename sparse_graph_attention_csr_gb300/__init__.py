@@ -868,7 +868,8 @@ def gated_ff_fwd(X, Wg, Wu, act: str = "silu", save: bool = True, out=None, G=No
 def gated_ff_bwd(X, Wg, Wu, G, U, dOut, act: str = "silu", input: bool = True, weights: bool = True,
                  dX=None, dWg=None, dWu=None, stream=None):
     """(dX, dWg, dWu) from the forward's G and U.  ``input=False``: no dX,
-    ``weights=False``: no dWg and dWu (None in their place)."""
+    ``weights=False``: no dWg and dWu (None in their place).  During the call dG
+    and dU take 4 bytes a hidden element in bfloat16, 12 in float32."""
     return _ext().gated_ff_bwd(X, Wg, Wu, G, U, dOut, act, input, weights, dX, dWg, dWu, stream)
 
 

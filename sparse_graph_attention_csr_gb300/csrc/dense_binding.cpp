@@ -1,5 +1,6 @@
 // Python entry of the dense operators (attention over packed sequences, layer
-// norm, embedding): argument checks, result and workspace allocation on the
+// norm, embedding, norm and rotary positions of heads, the gated feed-forward
+// product): argument checks, result and workspace allocation on the
 // stream that writes them, and the call of the C ABI (include/sga.h).
 //
 // The smallest calls of these operators take a few microseconds on the GPU.

@@ -34,10 +34,12 @@ struct FfProduct {
 
 // ---- activations: 0 silu, 1 gelu (by the normal distribution function), 2 relu -------
 
-// Phi(x) = erfc(-x / sqrt(2)) / 2, the normal distribution function, to a few units
-// of its own size in the tail too: by the Chebyshev fit to erfc of "Numerical Recipes"
-// (Press et al., erfcc), whose relative error is below 1.2e-7 everywhere.  erfcf, whose
-// chain is longer, took 20 us of the 67 of 4099 x 301 x 803 in fp32.
+// Phi(x) = erfc(-x / sqrt(2)) / 2, the normal distribution function, by the Chebyshev
+// fit to erfc of "Numerical Recipes" (Press et al., erfcc), whose relative error is below
+// 1.2e-7 (2 units of 2^-24) everywhere.  In fp32 the exponent's rounding adds to that in
+// the tail: off by 8 + 2 x^2 such units of Phi for x < 0 (emulated: 34 down to x = -4, 122
+// to -8), by 6 for x > 0.  erfcf, whose chain is longer, took 20 us more of a forward of
+// 4099 x 301 x 803 in fp32.
 __device__ __forceinline__ float ff_phi(float x) {
     const float z = 0.70710678118654752f * fabsf(x), t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
     float y = fmaf(t, 0.17087277f, -0.82215223f);
@@ -54,7 +56,7 @@ __device__ __forceinline__ float ff_phi(float x) {
 }
 
 // act(g).  Exponentials and quotients by the MUFU instructions: off by a few units of
-// fp32, and half a unit more for each unit of |g|.
+// 2^-24, and by 1.2 more for each unit of |g| (the exponent's rounding).
 __device__ __forceinline__ float ff_silu(float g) { return __fdividef(g, 1.f + fast_exp2(-kLog2e * g)); }
 __device__ __forceinline__ float ff_relu(float g) { return g != g ? g : fmaxf(g, 0.f); }
 // Calls f with the activation.

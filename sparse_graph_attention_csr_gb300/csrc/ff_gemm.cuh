@@ -510,8 +510,8 @@ template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32)
         // Tiles no wider than the columns' even shares, in whole blocks of what the
         // epilogue stores at a time.  (B lies along the depth here; across it, its
         // columns come in 64s a CTA.)  Backward, 256 wide and so: 4099 x 301 x 803 fp32
-        // (two of 160) 97 : 87 us, 20000 x 32 x 128 fp32 (32) 64 : 56, 20000 x 520 x
-        // 1300 bf16 (three of 192) 215 : 209.
+        // (two of 160) 101 : 94 us, 20000 x 32 x 128 fp32 (32) 63 : 57, 20000 x 520 x
+        // 1300 bf16 (three of 192) 213 : 207.
         const int64_t block = f32 ? 32 : 64;
         q.width = (int)(div(div(F, q.tiles_n), block) * block);
         q.kb_seg = div(M, 64);
@@ -528,10 +528,10 @@ template <FfMode MODE> FfPlan ff_plan(int64_t T, int64_t F, int64_t M, bool f32)
     const int64_t rest = q.tiles % most;
     // Sharing the last round takes its k-blocks from kb to about rest kb / pairs, at the
     // cost of writing and reading the sums and a launch more: some 40 k-blocks, 20 where
-    // a tile has few rows (in fp32, six products of parts a k-block, 8): 2708 x 256 x
-    // 680 bf16 dWg, dWu (6 tiles of 43) shared 27.7 us, whole 24.7; 4099 x 301 x 803 dX
-    // (34 of 26) 34 : 29; 16 x 4096 x 4096 forward (32 of 64) 22.2 : 25.5; 16384 x 1024 x
-    // 2816 backward (28 of 88 and 12 of 256) 295 : 354.
+    // a tile has few rows (in fp32, six products of parts a k-block, 8).  Shared : whole,
+    // us: 2708 x 256 x 680 bf16 dWg, dWu (6 tiles of 43) 27.7 : 24.7; 4099 x 301 x 803 fp32
+    // backward, whose dX has 34 of 26, 94 : 110; 16 x 4096 x 4096 bf16 forward (32 of 64)
+    // 22.2 : 25.5; 16384 x 1024 x 2816 bf16 backward (28 of 88 and 12 of 256) 295 : 354.
     const int64_t cost = f32 ? 8 : (MODE == FfMode::DW ? F : T) <= 128 ? 20 : 40;
     if (rest && q.kb - (rest * q.kb + most - 1) / most > cost) {
         q.split = true;

@@ -403,9 +403,13 @@ template <bool WIN> cudaError_t seq_fwd_bf16(const SeqArgs &a, int D, cudaStream
     // Measured, one : two tiles a CTA, D = 128, causal: 2048 rows, 8/2 heads
     // (128 tiles) 31 : 35 us; 4096 (256) 54.5 : 55.7; 8192 (512) 117 : 103.
     // D = 64: causal 4096 rows, 8 heads 43 : 48, 8192 80 : 84; full 4096 rows,
-    // 16 heads 92 : 88.  With a window units are short and alike: D = 64, 24576 rows,
-    // 8 heads, full, window 100, 58 : 72; causal, window 1024, 86 : 94 (8/2 heads 84 :
-    // 81); D = 128, 34270 rows, 8/2 heads, causal, window 1000, 172 : 162.
+    // 16 heads 92 : 88.  With a window units are short and alike, and D = 64 takes one
+    // tile whatever the window: 24576 rows, 8 heads, full, window 100, 49 : 62; causal,
+    // window 1024, 93 : 100.  Where two heads share their keys two tiles are as quick from
+    // a window of about 1000 on, by how the rounds come out: 8/2 heads, causal, window 128,
+    // 36 : 41; 1024, 90 : 86 (of 16384 rows 65.5 : 67.5); 2000, 137 : 129 (94 : 97); 4000,
+    // 227 : 225.  D = 128, 34270 rows, 8/2 heads, causal, window 1000, 172 : 162; but 24576
+    // rows of 8 heads, window 128, 53 : 62.
     const bool one = (int64_t)a.n_tiles * a.H <= 2 * (int64_t)a.num_sms || (D <= 64 && (a.causal || WIN));
     if (D == 32) return one ? launch<32, 1, WIN>(a, s) : launch<32, 2, WIN>(a, s);
     // A unit an SM at most: a thread's own stores are out sooner, and no other unit waits
