@@ -535,9 +535,10 @@ template <bool WIN> cudaError_t seq_bwd_f32(const SeqArgs &a, int D, cudaStream_
     const int64_t sms = a.num_sms;
     const bool many = units > 2 * sms;
     // One to a few rounds of blocks: how long they take depends on where the first ones
-    // lie (410 cases without a window, one sequence or several, of 1 to 10 units an SM,
-    // against laying them unevenly always: 8% less on average, 6% more at worst; evenly
-    // always: 1% and 25% more).  us, unevenly : evenly.
+    // lie.  410 cases without a window, one sequence or several, of 1 to 10 units an SM,
+    // take by this rule 8% less on average than with blocks that lie unevenly always, and
+    // 6% more at worst; with blocks that lie evenly always 7% less and 25% more.  us,
+    // unevenly : evenly.
     //   D = 64, a key head a query head, causal, 1.5 to 2.2 units an SM: 1100 rows, 4
     //     heads (1.9) 112 : 125; 800 rows, 4 heads (1.4) 90 : 82, 8 heads (2.7) 96 : 85.
     //     Full, 2 to 2.8: 700 rows, 8 heads (2.3) 114 : 141; 1100, 4 heads (1.9) 144 : 127.
